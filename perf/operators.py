@@ -5,7 +5,7 @@ Kinds of case (sizes: the decode-layer and expert shapes of qmm_synth.workloads,
 ``linear``        y = x W^T with W stored as e4m3 codes and one scale per 128 x 128 block; the tokens are
                   quantized in the call, one scale per token and 128 values along K.  Serving.
 ``linear_train``  the same product in training: weights (fp32 masters), tokens and output gradients are
-                  quantized in the step, which gives y, dx = dy W and dW = dy^T x.
+                  quantized in the step, which gives y, dx = dy W and dW = dy^T x, all of the tokens' type.
 ``experts``       the product with an expert's matrix picked for every (token, slot).
 ``experts_train`` expert products, their weighted sum per token, and the gradients of all of it.
 ``route``         a router: softmax over the experts, the S largest, their weights, tokens per expert and the
@@ -113,14 +113,14 @@ def work(case):
     if kind == "linear":
         return {"bytes": float(N * K * b + codes + N * M * b), "flops": 2.0 * N * M * K}
     if kind == "linear_train":
-        return {"bytes": float(2 * N * K * b + 2 * N * M * b + 2 * 4 * M * K), "flops": 6.0 * N * M * K}
+        return {"bytes": float(2 * N * K * b + 2 * N * M * b + (4 + b) * M * K), "flops": 6.0 * N * M * K}
     S, E = case["S"], case["E"]
     pairs = N * S * (1.0 - case["empty"])
     if kind == "experts":
         rows = pairs if case["per_slot"] else N
         used = E * (1.0 - (1.0 - S / E) ** N)
         return {"bytes": float(rows * K * b + used * codes + N * S * M * b), "flops": 2.0 * pairs * M * K}
-    return {"bytes": float(2 * N * K * b + 2 * N * M * b + 2 * 4 * E * M * K + (4 + 2 * b) * N * S),
+    return {"bytes": float(2 * N * K * b + 2 * N * M * b + (4 + b) * E * M * K + (4 + 2 * b) * N * S),
             "flops": 6.0 * pairs * M * K}
 
 
@@ -262,7 +262,7 @@ def _plain_linear_train(s):
     y = _spread(*_quantize(x)) @ wd.t()
     dx = _spread(*_quantize(dy))[:, :M] @ wd[:, :K]
     dw = _spread(*_quantize(dy.t())) @ _spread(*_quantize(x.t())).t()
-    return {"y": y.to(x.dtype), "dx": dx.to(x.dtype), "dw": dw}
+    return {"y": y.to(x.dtype), "dx": dx.to(x.dtype), "dw": dw.to(x.dtype)}
 
 
 def _dispatch(ids, E, capacity):
@@ -315,7 +315,7 @@ def _plain_experts_train(s):
     dx = dx.float().sum(1).to(x.dtype)
     gt = _spread(*_quantize(_to_experts(dpairs.float(), at, E, C).transpose(1, 2)))
     xt = _spread(*_quantize(_to_experts(_pair_rows(x, N, S).float(), at, E, C).transpose(1, 2)))
-    dw = torch.bmm(gt, xt.transpose(1, 2).contiguous())
+    dw = torch.bmm(gt, xt.transpose(1, 2).contiguous()).to(x.dtype)
     return {"out": out, "dx": dx, "dw": dw, "dweights": dweights}
 
 
@@ -362,7 +362,7 @@ def _own_linear_train(s):
     m.update(s["w"], transposed=mt)
     xq, xt = q.f8_quantize_pair(x)
     gq, gt = q.f8_quantize_pair(dy)
-    return {"y": m.gemm(xq, out_dtype=x.dtype), "dx": mt.gemm(gq, out_dtype=x.dtype), "dw": q.f8_wgrad(gt, xt)}
+    return {"y": m.gemm(xq, out_dtype=x.dtype), "dx": mt.gemm(gq, out_dtype=x.dtype), "dw": q.f8_wgrad(gt, xt, dtype=x.dtype)}
 
 
 def _own_experts(s):
@@ -378,7 +378,7 @@ def _own_experts_train(s):
     out = q.route_combine(y, weights)
     dpairs, dweights = q.route_combine_backward(y, weights, dout)
     dx = q.route_combine(mt.gemm_id(q.f8_quantize(dpairs), plan, out_dtype=x.dtype))
-    dw = q.f8_wgrad(q.f8_quantize_t(dpairs, plan), q.f8_quantize_t(x, plan), plan)
+    dw = q.f8_wgrad(q.f8_quantize_t(dpairs, plan), q.f8_quantize_t(x, plan), plan, dtype=x.dtype)
     return {"out": out, "dx": dx, "dw": dw, "dweights": dweights}
 
 
