@@ -12,12 +12,18 @@ check tensor metadata, allocate outputs with torch and marshal pointers.
     y = qm_stack.gemm_id(x, ids) # expert-indexed matrix-vector
     y = qm_stack.gemm_id_tiled(x, ids)  # expert-indexed, matrix cores, any N
     w = qm.dequantize()          # exact fp32 weights (or fp16 staging values)
+
+8-bit float weights and tokens with a scale per block of 128 are in ``f8`` (F8Matrix), the
+expert router that makes the expert-indexed calls' ids in ``routing``.
 """
 
 import ctypes
 
 import torch
 
+from .f8 import F8Matrix, F8Tokens, f8_quantize, f8_quantize_pair, f8_quantize_t, f8_wgrad  # noqa: F401
+from .routing import (  # noqa: F401
+    RoutePlan, Routing, balance_loss, route, route_backward, route_combine, route_combine_backward, route_plan)
 from ._lib import DTYPES, LIB_PATH, NOALLOC_SCRATCH_BYTES, QMM_OK, STATUS, TILES, TYPES, QmmError, check, lib  # noqa: F401
 
 __all__ = [
@@ -26,6 +32,9 @@ __all__ = [
     "qmm_gemm_noalloc",
     "qmm_gemm_id", "qmm_gemm_id_tiled", "qmm_dequantize", "qmm_quantize", "quantize",
     "qmm_tile_for_tokens", "qmm_row_bytes", "qmm_block_weights", "qmm_block_bytes",
+    "F8Matrix", "F8Tokens", "f8_quantize", "f8_quantize_pair", "f8_quantize_t", "f8_wgrad",
+    "Routing", "RoutePlan", "route", "route_plan", "balance_loss", "route_backward", "route_combine",
+    "route_combine_backward",
 ]
 
 _XT = {torch.float32: DTYPES["f32"], torch.float16: DTYPES["f16"]}

@@ -16,7 +16,7 @@ STATUS = {
 }
 TYPES = {"q4_0": 0, "q8_0": 1, "q4_k": 2, "q6_k": 3, "a4g64": 4,
          "q4_1": 5, "q5_0": 6, "q5_1": 7, "q2_k": 8, "q3_k": 9, "q5_k": 10}
-DTYPES = {"f32": 0, "f16": 1}
+DTYPES = {"f32": 0, "f16": 1, "bf16": 2}  # bf16: the qmm_f8_* and qmm_route* calls only
 TILES = {"auto": 0, 32: 32, 64: 64}
 NOALLOC_SCRATCH_BYTES = 64 << 20  # QMM_NOALLOC_SCRATCH_BYTES of include/qmm.h
 
@@ -33,6 +33,7 @@ def _load():
             f"{LIB_PATH} is not built; run `python block_quantized_weight_matmul_amd/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i64, i32, c_int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
+    size, f32 = ctypes.c_size_t, ctypes.c_float
     sigs = {
         "qmm_create": (c_int, [ctypes.POINTER(vp), c_int, vp, i64, i64, i64]),
         "qmm_destroy": (c_int, [vp]),
@@ -46,6 +47,32 @@ def _load():
         "qmm_gemm_id_tiled": (c_int, [vp, vp, c_int, i64, i64, c_int, vp, vp, c_int, vp]),
         "qmm_dequantize": (c_int, [vp, i64, vp, c_int, vp]),
         "qmm_quantize": (c_int, [c_int, vp, i64, i64, vp, vp]),
+        "qmm_f8_padded": (i64, [i64]),
+        "qmm_f8_create": (c_int, [ctypes.POINTER(vp), vp, vp, i64, i64, i64]),
+        "qmm_f8_destroy": (c_int, [vp]),
+        "qmm_f8_quantize": (c_int, [vp, c_int, i64, i64, i64, vp, vp, vp, vp, vp]),
+        "qmm_f8_quantize_weight": (c_int, [vp, c_int, i64, i64, i64, vp, vp, vp, vp, vp]),
+        "qmm_f8_transpose": (c_int, [vp, vp, vp, vp]),
+        "qmm_f8_dequantize": (c_int, [vp, i64, vp, c_int, vp]),
+        "qmm_f8_linear_workspace_bytes": (size, [vp, i64]),
+        "qmm_f8_linear": (c_int, [vp, vp, c_int, i64, i64, vp, c_int, vp, size, vp]),
+        "qmm_f8_gemm_workspace_bytes": (size, [vp, i64]),
+        "qmm_f8_gemm": (c_int, [vp, vp, vp, i64, vp, c_int, vp, size, vp]),
+        "qmm_route_plan_bytes": (size, [i64, i64]),
+        "qmm_route_plan": (c_int, [vp, i64, i64, i64, vp, size, vp]),
+        "qmm_f8_linear_id_workspace_bytes": (size, [vp, i64, i64, c_int]),
+        "qmm_f8_linear_id": (c_int, [vp, vp, c_int, i64, i64, c_int, vp, vp, c_int, vp, size, vp]),
+        "qmm_f8_gemm_id": (c_int, [vp, vp, vp, i64, i64, c_int, vp, vp, c_int, vp]),
+        "qmm_f8_routed_tokens": (i64, [i64, i64]),
+        "qmm_f8_quantize_routed": (c_int, [vp, c_int, i64, i64, i64, c_int, i64, i64, vp, vp, vp, vp]),
+        "qmm_f8_wgrad": (c_int, [vp, vp, vp, vp, i64, i64, i64, vp, c_int, vp]),
+        "qmm_f8_wgrad_id": (c_int, [vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, c_int, vp]),
+        "qmm_route_workspace_bytes": (size, [i64, i64]),
+        "qmm_route": (c_int, [vp, c_int, i64, i64, i64, vp, c_int, f32, vp, vp, vp, vp, vp, vp, size, vp]),
+        "qmm_balance_loss": (c_int, [vp, vp, i64, i64, f32, vp, vp]),
+        "qmm_route_backward": (c_int, [vp, c_int, i64, i64, i64, vp, c_int, f32, vp, vp, vp, vp, vp, vp]),
+        "qmm_route_combine": (c_int, [vp, c_int, vp, c_int, i64, i64, i64, vp, vp]),
+        "qmm_route_combine_backward": (c_int, [vp, c_int, vp, c_int, i64, i64, i64, vp, vp, vp, vp]),
         "qmm_tile_for_tokens": (c_int, [i64]),
         "qmm_row_bytes": (ctypes.c_size_t, [c_int, i64]),
         "qmm_block_weights": (c_int, [c_int]),

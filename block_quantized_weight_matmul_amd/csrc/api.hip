@@ -9,6 +9,7 @@
 #include <new>
 
 #include "qmm.h"
+#include "api_common.hpp"
 #include "decode.hpp"
 #include "internal.hpp"
 
@@ -18,8 +19,10 @@ struct qmm_matrix {
 };
 
 namespace {
-
 thread_local char g_err[512] = "";
+}
+
+namespace qmm {
 
 qmm_status fail(qmm_status s, const char* fmt, ...) {
   va_list ap;
@@ -34,6 +37,19 @@ qmm_status ok() {
   return QMM_OK;
 }
 
+qmm_status hip_fail(hipError_t e, const char* what) {
+  return fail(QMM_E_HIP, "%s: %s (%s)", what, hipGetErrorName(e), hipGetErrorString(e));
+}
+
+}  // namespace qmm
+
+using qmm::aligned;
+using qmm::fail;
+using qmm::hip_fail;
+using qmm::ok;
+
+namespace {
+
 constexpr int kBW[qmm::kNumFormats] = {32, 32, 256, 256, 64, 32, 32, 32, 256, 256, 256};
 constexpr int kBB[qmm::kNumFormats] = {18, 34, 144, 210, 36, 20, 22, 24, 84, 110, 176};
 
@@ -41,11 +57,6 @@ bool valid_type(int t) { return t >= 0 && t < qmm::kNumFormats; }
 // the types qmm_quantize encodes (the others have no quantizer here)
 bool quantizable_type(int t) { return t >= 0 && t <= QMM_A4G64; }
 bool valid_dtype(int t) { return t == QMM_F32 || t == QMM_F16; }
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-qmm_status hip_fail(hipError_t e, const char* what) {
-  return fail(QMM_E_HIP, "%s: %s (%s)", what, hipGetErrorName(e), hipGetErrorString(e));
-}
 
 // The current device must be the handle's device.
 qmm_status check_device(const qmm_matrix* h) {

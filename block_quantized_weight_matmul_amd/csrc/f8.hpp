@@ -1,0 +1,191 @@
+// f8.hpp -- e4m3 values with a scale for each block of 128: device helpers of the quantizers and products, and
+// the launch interface between the C ABI (f8_api.hip) and the kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace qmm {
+
+// Element types of the calls' 16- and 32-bit tensors (the values of qmm_dtype).
+enum { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2 };
+
+constexpr int kF8Block = 128;             // values per scale along K; rows per scale of a weight block
+constexpr float kF8Max = 448.0f;          // largest e4m3 value
+constexpr float kF8MinScale = 0x1p-80f;   // smallest scale: keeps remainders of the quotient exact
+constexpr int64_t kF8MaxRows = int64_t(1) << 24;  // rows of a call's tokens, weights and outputs
+constexpr int64_t kF8MaxK = int64_t(1) << 22;     // padded K of a call: a tile's rows stay in 32-bit offsets
+constexpr int64_t kRouteMaxExperts = 1024;
+constexpr int64_t kRouteMaxPairs = int64_t(1) << 22;
+
+inline __host__ __device__ int64_t f8_pad(int64_t n) { return (n + kF8Block - 1) / kF8Block * kF8Block; }
+
+struct F8Desc {
+  const uint8_t* codes;  // [n_experts][M][Kp], Kp = f8_pad(K)
+  const float* scales;   // [n_experts][f8_pad(M) / 128][Kp / 128]
+  int64_t n_experts, M, K, Kp;
+  int cus;
+};
+
+// Routing plan: int32 arrays in one device buffer (route.hip builds it, the expert products read it).  Pairs are
+// sorted by bucket, ascending inside one: buckets 0 .. E-1 the experts, E the empty slots (id -1), E+1 ids that
+// name no expert.  map[t] lists, per token tile of kPlanTiles[t] pairs, (bucket, first position, end position).
+constexpr int kPlanTileKinds = 4;
+constexpr int kPlanTiles[kPlanTileKinds] = {16, 32, 64, 128};
+struct PlanDesc {
+  int64_t pairs, E;
+  int64_t counts, offsets, tile128, order, map[kPlanTileKinds], scratch, total;  // int32 offsets in the buffer
+  int64_t cap[kPlanTileKinds];                                                    // entries of each map
+};
+PlanDesc plan_desc(int64_t pairs, int64_t E);
+hipError_t launch_route_plan(const int32_t* ids, int64_t pairs, int64_t E, int32_t* plan, hipStream_t s);
+
+// Quantizers.  codes_r / scales_r: groups of 128 along K ([N][Kp], [Kp / 128][N]); codes_c / scales_c: groups of
+// 128 along the rows ([K][Np], [Np / 128][K]); either may be null.  plan: rows are the plan's pairs, each expert's
+// padded to 128 on their own (Np = 128 * cap[3]); pair p reads row p / slots.
+struct F8QuantArgs {
+  const void* x;
+  int64_t ldx, N, K;
+  uint8_t* codes_r;
+  float* scales_r;
+  uint8_t* codes_c;
+  float* scales_c;
+  const int32_t* plan;  // null: dense
+  PlanDesc pd;
+  int slots;  // rows of x a pair shares: pair / slots
+};
+hipError_t launch_f8_quantize(const F8QuantArgs& a, int dt, hipStream_t s);
+// Weights: one scale per 128 x 128 block; codes_t / scales_t (may be null): the transposed matrix' codes.
+hipError_t launch_f8_quantize_weight(const void* w, int dt, int64_t E, int64_t M, int64_t K, uint8_t* codes,
+                                     float* scales, uint8_t* codes_t, float* scales_t, hipStream_t s);
+hipError_t launch_f8_transpose(const F8Desc& m, uint8_t* codes_t, float* scales_t, hipStream_t s);
+hipError_t launch_f8_dequantize(const F8Desc& m, int64_t expert, void* out, int dt, hipStream_t s);
+
+// Products.  Dense: y[N][M] = x W^T of quantized tokens (codes_r / scales_r layout).
+size_t f8_gemm_workspace_bytes(const F8Desc& m, int64_t N);
+hipError_t launch_f8_gemm(const F8Desc& m, const uint8_t* xc, const float* xs, int64_t N, void* y, int yt, void* ws,
+                          hipStream_t s);
+// Fused quantization for few tokens: whether a raw call of N tokens takes one launch, and that launch.
+bool f8_linear_fused(const F8Desc& m, int64_t N);
+hipError_t launch_f8_linear(const F8Desc& m, const void* x, int xt, int64_t ldx, int64_t N, void* y, int yt,
+                            hipStream_t s);
+// Expert-indexed: rows of x are tokens (slots = S) or pairs (slots = 1); y [pairs][M].
+hipError_t launch_f8_gemm_id(const F8Desc& m, const uint8_t* xc, const float* xs, int64_t pairs, int slots,
+                             const int32_t* plan, void* y, int yt, hipStream_t s);
+bool f8_linear_id_fused(const F8Desc& m, int64_t pairs);
+hipError_t launch_f8_linear_id(const F8Desc& m, const void* x, int xt, int64_t pairs, int slots, const int32_t* ids,
+                               void* y, int yt, hipStream_t s);
+// Weight gradients: dw[M][K] = g^T x over N tokens, both quantized along the tokens (codes_c layout); with a plan
+// dw[E][M][K], each expert over its own pairs.
+struct F8WgradArgs {
+  const uint8_t* gc;
+  const float* gs;
+  const uint8_t* xc;
+  const float* xs;
+  int64_t M, K, Np;
+  void* dw;
+  int dt;
+  const int32_t* plan;
+  PlanDesc pd;
+};
+hipError_t launch_f8_wgrad(const F8WgradArgs& a, hipStream_t s);
+
+// Router.
+struct RouteArgs {
+  const void* logits;
+  int lt;
+  int64_t N;
+  int E, S, normalise;
+  float coef;
+  const uint8_t* valid;  // null: every row
+  int32_t* ids;
+  float* weights;
+  int32_t* counts;  // [E + 1]: tokens per expert, then rows with an expert
+  float* psum;      // [E]
+  float* loss;      // null: none
+  void* ws;
+};
+size_t route_workspace_bytes(int64_t N, int64_t E);
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+hipError_t launch_balance_loss(const int32_t* counts, const float* psum, int E, int S, float coef, float* loss,
+                               hipStream_t s);
+struct RouteBackwardArgs {
+  const void* logits;
+  int lt;
+  int64_t N;
+  int E, S, normalise;
+  float coef;
+  const uint8_t* valid;
+  const int32_t* ids;
+  const float* dweights;  // null: none
+  const int32_t* counts;
+  const float* dloss;     // null: none
+  void* dlogits;
+};
+hipError_t launch_route_backward(const RouteBackwardArgs& a, hipStream_t s);
+// out[t] = sum_s w[t][s] y[t][s] (w null: plain sum)
+hipError_t launch_route_combine(const void* y, int yt, const void* w, int wt, int64_t N, int S, int64_t M, void* out,
+                                hipStream_t s);
+hipError_t launch_route_combine_backward(const void* y, int yt, const void* w, int wt, int64_t N, int S, int64_t M,
+                                         const void* dout, void* dy, void* dw, hipStream_t s);
+
+#ifdef __HIPCC__
+// ---- device helpers ----------------------------------------------------------------------------
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <int DT> struct Elem;
+template <> struct Elem<DT_F32> { typedef float T; };
+template <> struct Elem<DT_F16> { typedef _Float16 T; };
+template <> struct Elem<DT_BF16> { typedef __bf16 T; };
+
+// 8 consecutive elements as fp32; p is 16-byte aligned
+template <int DT>
+__device__ __forceinline__ void load8(const typename Elem<DT>::T* p, float* v) {
+  if constexpr (DT == DT_F32) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    typedef typename Elem<DT>::T T8 __attribute__((ext_vector_type(8)));
+    const T8 a = *reinterpret_cast<const T8*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(a[i]);
+  }
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// Scale of a block whose largest |x| has these bits: max(a / 448, 2^-80), NaN if the block holds an Inf or a NaN.
+__device__ __forceinline__ float f8_scale(uint32_t amax_bits) {
+  if (amax_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+  return fmaxf(__uint_as_float(amax_bits) / kF8Max, kF8MinScale);
+}
+
+// x / s ready for the hardware's one rounding to e4m3.  q is x / s to within half a step of fp32 (one correction of
+// x * (1 / s) by the exact remainder); an inexact q takes the odd one of the two fp32 neighbours of the quotient,
+// which an e4m3 rounding (4 of 24 bits) cannot tell from the quotient itself.  Rounding q directly would round
+// twice and miss the definition wherever q lands on the middle of two e4m3 values.
+__device__ __forceinline__ float f8_quotient(float x, float s, float rs) {
+  float q = x * rs;
+  q = fmaf(fmaf(-q, s, x), rs, q);
+  const float r = fmaf(-q, s, x);
+  const uint32_t b = __float_as_uint(q);
+  const uint32_t below = (__float_as_uint(r) ^ b) >> 31;  // 1: the quotient is nearer to zero than q
+  const uint32_t odd = r == 0.0f ? b : (b - below) | 1u;
+  return __uint_as_float((odd & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u));  // the correction loses a -0
+}
+
+// four codes in one word, lowest byte first
+__device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
+}
+
+template <int DT>
+__device__ __forceinline__ typename Elem<DT>::T to_elem(float v) { return static_cast<typename Elem<DT>::T>(v); }
+#endif
+
+}  // namespace qmm

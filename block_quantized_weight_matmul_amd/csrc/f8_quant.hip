@@ -1,0 +1,345 @@
+// f8_quant.hip -- quantizers to e4m3 with a scale per block of 128, the transposition of quantized weights, and
+// their decoding.
+//
+// A block's scale is s = max(fp32(max |x| / 448), 2^-80); a code is the e4m3 value nearest to the real quotient
+// x / s (ties to even).  All four forms read their input once and are bound by memory: 2 or 4 bytes in and 1 out
+// per value (the division, made exact by its remainder, is ~10 fp32 operations).
+#include <climits>
+
+#include "f8.hpp"
+
+namespace qmm {
+
+namespace {
+
+// largest of v over the 16 lanes of a DPP row
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x128, 0xF, 0xF, false)));  // row_ror:8
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x124, 0xF, 0xF, false)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x122, 0xF, 0xF, false)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x121, 0xF, 0xF, false)));
+  return v;
+}
+
+// 8 elements of a row from column c; columns from K on are zero.  VEC: every row and c are 16-byte aligned.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load_row8(const typename Elem<DT>::T* row, int64_t c, int64_t K, float* v) {
+  if (VEC && c + 8 <= K) {
+    load8<DT>(row + c, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = c + i < K ? static_cast<float>(row[c + i]) : 0.0f;
+}
+
+__device__ __forceinline__ uint2 codes8(const float* v, float s, float rs) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = f8_quotient(v[i], s, rs);
+  return make_uint2(f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7]));
+}
+
+// Groups along K only: 16 lanes hold one token's group, 8 values each; a workgroup takes 16 tokens of one group, so
+// that their scales (group-major) are one 64-byte store.
+template <int DT, bool VEC>
+__global__ __launch_bounds__(256) void k_f8_quant_rows(F8QuantArgs a) {
+  const int lane = threadIdx.x & 15;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  if (t >= a.N) return;
+  const int64_t g = blockIdx.y;
+  const int64_t c = g * kF8Block + lane * 8;
+  float v[8];
+  load_row8<DT, VEC>(static_cast<const typename Elem<DT>::T*>(a.x) + t * a.ldx, c, a.K, v);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+  const float s = f8_scale(max16(m));
+  *reinterpret_cast<uint2*>(a.codes_r + t * f8_pad(a.K) + c) = codes8(v, s, 1.0f / s);
+  if (lane == 0) a.scales_r[g * a.N + t] = s;
+}
+
+// Transposed write of a 128 x 128 tile of codes: thread (team, lane) gives, for each of its 8 columns, the 8 codes
+// of its 8 rows.  8-byte pieces are exchanged through LDS with the piece index xored by the column's lane, so that
+// both the writes (16 lanes, 16 columns) and the reads (one column, 16 pieces) use every bank once.
+__device__ __forceinline__ void lds_put(uint2* tile, int team, int lane, int j, uint2 v) {
+  tile[(lane * 8 + j) * 16 + (team ^ lane)] = v;
+}
+__device__ __forceinline__ uint2 lds_get(const uint2* tile, int col, int piece) {
+  return tile[col * 16 + (piece ^ (col >> 3))];
+}
+
+// A 128 x 128 tile in registers, 8 x 8 values a thread (rows team * 8 .., columns lane * 8 ..).
+// ROWS: one scale per row of the tile; COLS: one per column, codes transposed; neither: one for the tile, codes as
+// they stand and (codes_c given) transposed.
+template <int DT, bool VEC, bool ROWS, bool COLS>
+__global__ __launch_bounds__(256) void k_f8_quant_tile(F8QuantArgs a, int64_t w_rows_pad) {
+  typedef typename Elem<DT>::T T;
+  __shared__ uint2 tile[128 * 16];
+  __shared__ uint32_t cmax[16][128];
+  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
+  const int64_t Kp = f8_pad(a.K);
+  const unsigned tiles_k = static_cast<unsigned>(Kp / kF8Block);
+  const int64_t g = blockIdx.x % tiles_k;  // tile along K
+  const int64_t j = blockIdx.x / tiles_k;  // tile along the rows
+  const T* x = static_cast<const T*>(a.x);
+  const int64_t N = a.N;
+  const int64_t e = blockIdx.y;  // expert of a weight
+  if (!ROWS && !COLS) x += e * a.N * a.K;
+  const int64_t c = g * kF8Block + lane * 8;
+  float v[8][8];
+  if (a.plan) {
+    const int32_t* mp = a.plan + a.pd.map[3] + 3 * j;
+    const int bucket = mp[0], first = mp[1], end = mp[2];
+    if (bucket < 0 || bucket >= a.pd.E) return;  // no expert's pairs: no product reads this group
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const int at = first + team * 8 + p;
+      if (at < end) {
+        const int64_t r = a.plan[a.pd.order + at] / a.slots;
+        load_row8<DT, VEC>(x + r * a.ldx, c, a.K, v[p]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const int64_t r = j * kF8Block + team * 8 + p;
+      if (r < N) {
+        load_row8<DT, VEC>(x + r * a.ldx, c, a.K, v[p]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
+      }
+    }
+  }
+  if (ROWS) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[p][i]));
+      const float s = f8_scale(max16(m));
+      const int64_t r = j * kF8Block + team * 8 + p;
+      if (r < N) {
+        *reinterpret_cast<uint2*>(a.codes_r + r * Kp + c) = codes8(v[p], s, 1.0f / s);
+        if (lane == 0) a.scales_r[g * N + r] = s;
+      }
+    }
+  }
+  const int64_t tiles = a.plan ? a.pd.cap[3] : (N + kF8Block - 1) / kF8Block;
+  const int64_t Np = tiles * kF8Block;
+  if (COLS) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int p = 0; p < 8; ++p) m = max(m, abs_bits(v[p][i]));
+      cmax[team][lane * 8 + i] = m;
+    }
+    __syncthreads();
+    if (threadIdx.x < 128) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int t = 0; t < 16; ++t) m = max(m, cmax[t][threadIdx.x]);
+      const float s = f8_scale(m);
+      cmax[0][threadIdx.x] = __float_as_uint(s);
+      const int64_t k = g * kF8Block + threadIdx.x;
+      if (k < a.K) a.scales_c[j * a.K + k] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = __uint_as_float(cmax[0][lane * 8 + i]);
+      float col[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) col[p] = v[p][i];
+      lds_put(tile, team, lane, i, codes8(col, s, 1.0f / s));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const int col = p * 16 + team;
+      const int64_t k = g * kF8Block + col;
+      if (k < a.K) *reinterpret_cast<uint2*>(a.codes_c + k * Np + j * kF8Block + lane * 8) = lds_get(tile, col, lane);
+    }
+  }
+  if (!ROWS && !COLS) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[p][i]));
+    m = max16(m);
+    if (lane == 0) cmax[0][team] = m;
+    __syncthreads();
+    m = 0;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) m = max(m, cmax[0][t]);
+    const float s = f8_scale(m), rs = 1.0f / s;
+    const int64_t G = Kp / kF8Block, R = f8_pad(N) / kF8Block;
+    uint2 q[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      q[p] = codes8(v[p], s, rs);
+      const int64_t r = j * kF8Block + team * 8 + p;
+      if (r < N) *reinterpret_cast<uint2*>(a.codes_r + (e * N + r) * Kp + c) = q[p];
+    }
+    if (threadIdx.x == 0) a.scales_r[(e * R + j) * G + g] = s;
+    if (a.codes_c) {
+      if (threadIdx.x == 0) a.scales_c[(e * G + g) * R + j] = s;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t b[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) b[p] = ((i < 4 ? q[p].x : q[p].y) >> (8 * (i & 3))) & 0xFFu;
+        lds_put(tile, team, lane, i,
+                make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24));
+      }
+      __syncthreads();
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const int col = p * 16 + team;
+        const int64_t k = g * kF8Block + col;
+        if (k < a.K)
+          *reinterpret_cast<uint2*>(a.codes_c + (e * a.K + k) * w_rows_pad + j * kF8Block + lane * 8) =
+              lds_get(tile, col, lane);
+      }
+    }
+  }
+}
+
+// The codes of the transposed matrix: the same bytes, tile by tile.
+__global__ __launch_bounds__(256) void k_f8_transpose(const uint8_t* codes, const float* scales, int64_t M, int64_t K,
+                                                      uint8_t* codes_t, float* scales_t) {
+  __shared__ uint2 tile[128 * 16];
+  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
+  const int64_t Kp = f8_pad(K), Mp = f8_pad(M), G = Kp / kF8Block, R = Mp / kF8Block;
+  const int64_t g = blockIdx.x % static_cast<unsigned>(G), j = blockIdx.x / static_cast<unsigned>(G), e = blockIdx.y;
+  uint2 q[8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int64_t r = j * kF8Block + team * 8 + p;
+    q[p] = r < M ? *reinterpret_cast<const uint2*>(codes + (e * M + r) * Kp + g * kF8Block + lane * 8) : make_uint2(0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t b[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) b[p] = ((i < 4 ? q[p].x : q[p].y) >> (8 * (i & 3))) & 0xFFu;
+    lds_put(tile, team, lane, i,
+            make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24));
+  }
+  if (threadIdx.x == 0) scales_t[(e * G + g) * R + j] = scales[(e * R + j) * G + g];
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int col = p * 16 + team;
+    const int64_t k = g * kF8Block + col;
+    if (k < K)
+      *reinterpret_cast<uint2*>(codes_t + (e * K + k) * Mp + j * kF8Block + lane * 8) = lds_get(tile, col, lane);
+  }
+}
+
+// Decoded weights: code times scale, exact in fp32 up to its one rounding, rounded once more to a 16-bit output.
+template <int DT>
+__global__ __launch_bounds__(256) void k_f8_dequantize(const uint8_t* codes, const float* scales, int64_t M, int64_t K,
+                                                       typename Elem<DT>::T* out) {
+  const int64_t Kp = f8_pad(K);
+  const int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, r = blockIdx.y + int64_t(65535) * blockIdx.z;
+  if (k >= K || r >= M) return;
+  const float s = scales[r / kF8Block * (Kp / kF8Block) + k / kF8Block];
+  const float v = __builtin_amdgcn_cvt_f32_fp8(codes[r * Kp + k], 0);
+  out[r * K + k] = to_elem<DT>(v * s);
+}
+
+template <int DT>
+hipError_t quantize_dt(const F8QuantArgs& a, hipStream_t st) {
+  const int esz = DT == DT_F32 ? 4 : 2;
+  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ldx * esz % 16 == 0 || a.N <= 1);
+  const int64_t G = f8_pad(a.K) / kF8Block;
+  if (!a.codes_c) {
+    const dim3 grid(static_cast<unsigned>((a.N + 15) / 16), static_cast<unsigned>(G));
+    if (vec) k_f8_quant_rows<DT, true><<<grid, 256, 0, st>>>(a);
+    else k_f8_quant_rows<DT, false><<<grid, 256, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  const int64_t tiles = a.plan ? a.pd.cap[3] : (a.N + kF8Block - 1) / kF8Block;
+  if (tiles * G > INT_MAX) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(tiles * G));
+  if (a.codes_r) {
+    if (vec) k_f8_quant_tile<DT, true, true, true><<<grid, 256, 0, st>>>(a, 0);
+    else k_f8_quant_tile<DT, false, true, true><<<grid, 256, 0, st>>>(a, 0);
+  } else {
+    if (vec) k_f8_quant_tile<DT, true, false, true><<<grid, 256, 0, st>>>(a, 0);
+    else k_f8_quant_tile<DT, false, false, true><<<grid, 256, 0, st>>>(a, 0);
+  }
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t quantize_weight_dt(const F8QuantArgs& a, int64_t E, hipStream_t st) {
+  const int esz = DT == DT_F32 ? 4 : 2;
+  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.K * esz % 16 == 0;
+  const int64_t tiles = f8_pad(a.K) / kF8Block * (f8_pad(a.N) / kF8Block);
+  if (tiles > INT_MAX) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(E));
+  if (vec) k_f8_quant_tile<DT, true, false, false><<<grid, 256, 0, st>>>(a, f8_pad(a.N));
+  else k_f8_quant_tile<DT, false, false, false><<<grid, 256, 0, st>>>(a, f8_pad(a.N));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_f8_quantize(const F8QuantArgs& a, int dt, hipStream_t st) {
+  switch (dt) {
+    case DT_F32: return quantize_dt<DT_F32>(a, st);
+    case DT_F16: return quantize_dt<DT_F16>(a, st);
+    case DT_BF16: return quantize_dt<DT_BF16>(a, st);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_f8_quantize_weight(const void* w, int dt, int64_t E, int64_t M, int64_t K, uint8_t* codes,
+                                     float* scales, uint8_t* codes_t, float* scales_t, hipStream_t st) {
+  F8QuantArgs a{};
+  a.x = w;
+  a.ldx = K;
+  a.N = M;
+  a.K = K;
+  a.codes_r = codes;
+  a.scales_r = scales;
+  a.codes_c = codes_t;
+  a.scales_c = scales_t;
+  switch (dt) {
+    case DT_F32: return quantize_weight_dt<DT_F32>(a, E, st);
+    case DT_F16: return quantize_weight_dt<DT_F16>(a, E, st);
+    case DT_BF16: return quantize_weight_dt<DT_BF16>(a, E, st);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_f8_transpose(const F8Desc& m, uint8_t* codes_t, float* scales_t, hipStream_t st) {
+  const int64_t tiles = m.Kp / kF8Block * (f8_pad(m.M) / kF8Block);
+  if (tiles > INT_MAX) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(m.n_experts));
+  k_f8_transpose<<<grid, 256, 0, st>>>(m.codes, m.scales, m.M, m.K, codes_t, scales_t);
+  return hipGetLastError();
+}
+
+hipError_t launch_f8_dequantize(const F8Desc& m, int64_t expert, void* out, int dt, hipStream_t st) {
+  const uint8_t* c = m.codes + expert * m.M * m.Kp;
+  const float* s = m.scales + expert * (f8_pad(m.M) / kF8Block) * (m.Kp / kF8Block);
+  const unsigned gy = static_cast<unsigned>(m.M < 65535 ? m.M : 65535);
+  const dim3 grid(static_cast<unsigned>((m.K + 255) / 256), gy, static_cast<unsigned>((m.M + 65534) / 65535));
+  switch (dt) {
+    case DT_F32: k_f8_dequantize<DT_F32><<<grid, 256, 0, st>>>(c, s, m.M, m.K, static_cast<float*>(out)); break;
+    case DT_F16: k_f8_dequantize<DT_F16><<<grid, 256, 0, st>>>(c, s, m.M, m.K, static_cast<_Float16*>(out)); break;
+    case DT_BF16: k_f8_dequantize<DT_BF16><<<grid, 256, 0, st>>>(c, s, m.M, m.K, static_cast<__bf16*>(out)); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace qmm

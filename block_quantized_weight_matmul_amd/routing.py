@@ -1,0 +1,193 @@
+"""The expert router and the sum of its slots: the binding of include/qmm.h's qmm_route* calls.
+
+    r = route(logits, S, normalise=True, coef=0.01)      # ids, weights, counts, psum, loss
+    y = experts.linear_id(x, r.ids)                      # F8Matrix, or QMatrix.gemm_id
+    out = route_combine(y, r.weights)
+
+Backward, every gradient a call:
+
+    dy, dweights = route_combine_backward(y, r.weights, dout)
+    dlogits = route_backward(logits, r, dweights, dloss)
+
+A trainer that adds counts and psum over GPUs before the loss calls balance_loss on the sums and hands a Routing with
+the summed counts to route_backward.
+"""
+
+from typing import NamedTuple, Optional
+
+import torch
+
+from ._lib import check, lib
+from .f8 import _DT, _Device, _out, _place, _shape, _tensor
+
+
+class Routing(NamedTuple):
+    ids: torch.Tensor      # int32 [N, S], -1: no expert left
+    weights: torch.Tensor  # fp32 [N, S]
+    counts: torch.Tensor   # int32 [E + 1]: pairs per expert, then the rows that have an expert
+    psum: torch.Tensor     # fp32 [E]: sum of the probabilities over the rows
+    loss: torch.Tensor     # fp32, no dimension
+    normalise: bool
+    coef: float
+    valid: Optional[torch.Tensor]
+
+
+class RoutePlan:
+    """(token, slot) pairs of ids [N, S] sorted by expert; see route_plan."""
+
+    __slots__ = ("data", "N", "S", "n_experts")
+
+    def __init__(self, data, N, S, n_experts):
+        self.data, self.N, self.S, self.n_experts = data, N, S, n_experts
+
+    @property
+    def counts(self):
+        """Pairs per expert, int32 [E] (a view of the plan)."""
+        return self.data[:self.n_experts]
+
+    def per_slot(self, rows, name):
+        """1: a row per (token, slot) pair, 0: a row per token."""
+        if rows == self.N and self.S != 1:
+            return 0
+        if rows != self.N * self.S:
+            raise ValueError(f"{name} has {rows} rows; the plan's ids are {self.N} x {self.S}")
+        return 1
+
+    def per_slot_rows(self, x, name):
+        if x.dim() == 3:
+            _shape(x, name, (self.N, self.S, x.shape[2]))
+            return 1
+        return self.per_slot(x.shape[0], name)
+
+
+def route_plan(ids: torch.Tensor, n_experts: int) -> RoutePlan:
+    """Sort the pairs of ids [N, S] (int32; -1: an empty slot) by expert, once for every product that reads them."""
+    _tensor(ids, "ids", (torch.int32,), (2,))
+    N, S = ids.shape
+    E = int(n_experts)
+    if S < 1 or E < 1:
+        raise ValueError("ids needs a slot and the plan an expert")
+    device = _place(None, (ids, "ids"))
+    nb = lib.qmm_route_plan_bytes(N * S, E)
+    data = torch.empty(max(nb, 16) // 4, dtype=torch.int32, device=device)
+    with _Device(device) as stream:
+        check(lib.qmm_route_plan(ids.data_ptr(), N, S, E, data.data_ptr(), nb, stream))
+    return RoutePlan(data, N, S, E)
+
+
+def _logits(logits, valid):
+    _tensor(logits, "logits", tuple(_DT), (2,))
+    device = _place(None, (logits, "logits"))
+    if valid is not None:
+        _tensor(valid, "valid", (torch.uint8, torch.bool), (1,))
+        _shape(valid, "valid", (logits.shape[0],))
+        _place(device, (valid, "valid"))
+    return device
+
+
+def route(logits: torch.Tensor, S: int, normalise: bool = True, coef: float = 0.0,
+          valid: Optional[torch.Tensor] = None) -> Routing:
+    """Softmax over logits [N, E], the S largest experts of each row and the balance loss.  valid [N] (uint8 or bool):
+    0 marks padded rows."""
+    device = _logits(logits, valid)
+    N, E = logits.shape
+    S = int(S)
+    if not 1 <= S <= min(E, 64):
+        raise ValueError(f"S={S} outside [1, {min(E, 64)}]")
+    ids = torch.empty((N, S), dtype=torch.int32, device=device)
+    weights = torch.empty((N, S), dtype=torch.float32, device=device)
+    counts = torch.empty(E + 1, dtype=torch.int32, device=device)
+    nb = lib.qmm_route_workspace_bytes(N, E)
+    # sums over the rows, the loss and the workspace in one allocation
+    pad = (E + 1 + 3) // 4 * 4
+    buf = torch.empty(pad + nb // 4, dtype=torch.float32, device=device)
+    psum, loss = buf[:E], buf[E]
+    with _Device(device) as stream:
+        check(lib.qmm_route(logits.data_ptr(), _DT[logits.dtype], N, E, S, valid.data_ptr() if valid is not None else None,
+                            int(bool(normalise)), float(coef), ids.data_ptr(), weights.data_ptr(), counts.data_ptr(),
+                            psum.data_ptr(), loss.data_ptr(), buf.data_ptr() + 4 * pad, nb, stream))
+    return Routing(ids, weights, counts, psum, loss, bool(normalise), float(coef), valid)
+
+
+def balance_loss(counts: torch.Tensor, psum: torch.Tensor, S: int, coef: float) -> torch.Tensor:
+    """coef * sum_e f_e P_e from counts [E + 1] and psum [E] (added over micro-batches or GPUs)."""
+    _tensor(counts, "counts", (torch.int32,), (1,))
+    _tensor(psum, "psum", (torch.float32,), (1,))
+    E = psum.shape[0]
+    _shape(counts, "counts", (E + 1,))
+    device = _place(None, (counts, "counts"), (psum, "psum"))
+    loss = torch.empty((), dtype=torch.float32, device=device)
+    with _Device(device) as stream:
+        check(lib.qmm_balance_loss(counts.data_ptr(), psum.data_ptr(), E, int(S), float(coef), loss.data_ptr(), stream))
+    return loss
+
+
+def route_backward(logits: torch.Tensor, routing: Routing, dweights: Optional[torch.Tensor] = None,
+                   dloss: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dlogits [N, E] of logits' type from the gradients with respect to the weights ([N, S] fp32) and the loss (fp32, one
+    element on the device); either may be None."""
+    device = _logits(logits, routing.valid)
+    N, E = logits.shape
+    S = routing.ids.shape[1]
+    _shape(routing.ids, "ids", (N, S))
+    _shape(routing.counts, "counts", (E + 1,))
+    _place(device, (routing.ids, "ids"), (routing.counts, "counts"))
+    if dweights is not None:
+        _tensor(dweights, "dweights", (torch.float32,), (2,))
+        _shape(dweights, "dweights", (N, S))
+        _place(device, (dweights, "dweights"))
+    if dloss is not None:
+        _tensor(dloss, "dloss", (torch.float32,))
+        if dloss.numel() != 1:
+            raise ValueError("dloss must have one element")
+        _place(device, (dloss, "dloss"))
+    valid = routing.valid
+    dlogits = torch.empty_like(logits)
+    with _Device(device) as stream:
+        check(lib.qmm_route_backward(logits.data_ptr(), _DT[logits.dtype], N, E, S,
+                                     valid.data_ptr() if valid is not None else None, int(routing.normalise), routing.coef,
+                                     routing.ids.data_ptr(), dweights.data_ptr() if dweights is not None else None,
+                                     routing.counts.data_ptr(), dloss.data_ptr() if dloss is not None else None,
+                                     dlogits.data_ptr(), stream))
+    return dlogits
+
+
+def _slots(y, weights):
+    _tensor(y, "y", tuple(_DT), (3,))
+    device = _place(None, (y, "y"))
+    N, S, M = y.shape
+    if S < 1 or M < 1:
+        raise ValueError("y needs a slot and a column")
+    if weights is not None:
+        _tensor(weights, "weights", (torch.float32, y.dtype), (2,))
+        _shape(weights, "weights", (N, S))
+        _place(device, (weights, "weights"))
+    return device, N, S, M
+
+
+def route_combine(y: torch.Tensor, weights: Optional[torch.Tensor] = None, out: torch.Tensor = None) -> torch.Tensor:
+    """out [N, M] = sum over the slots of weights [N, S] (fp32 or y's type) times y [N, S, M]; without weights the plain
+    sum (the gradient of a row that a token's slots share)."""
+    device, N, S, M = _slots(y, weights)
+    o = _out(out, (N, M), y.dtype, device)
+    if o.dtype != y.dtype:
+        raise ValueError("out must have y's dtype")
+    with _Device(device) as stream:
+        check(lib.qmm_route_combine(y.data_ptr(), _DT[y.dtype], weights.data_ptr() if weights is not None else None,
+                                    _DT[weights.dtype] if weights is not None else 0, N, S, M, o.data_ptr(), stream))
+    return o
+
+
+def route_combine_backward(y: torch.Tensor, weights: torch.Tensor, dout: torch.Tensor):
+    """(dy [N, S, M] of y's type, dweights [N, S] of weights' type) from dout [N, M] of y's type."""
+    if weights is None:
+        raise ValueError("weights are needed; without them dy is dout for every slot")
+    device, N, S, M = _slots(y, weights)
+    _tensor(dout, "dout", (y.dtype,), (2,))
+    _shape(dout, "dout", (N, M))
+    _place(device, (dout, "dout"))
+    dy, dw = torch.empty_like(y), torch.empty_like(weights)
+    with _Device(device) as stream:
+        check(lib.qmm_route_combine_backward(y.data_ptr(), _DT[y.dtype], weights.data_ptr(), _DT[weights.dtype], N, S, M,
+                                             dout.data_ptr(), dy.data_ptr(), dw.data_ptr(), stream))
+    return dy, dw

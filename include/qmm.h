@@ -100,8 +100,9 @@ typedef enum {
   QMM_Q5_K = 10
 } qmm_type;
 
-/* Element type of activations (x) and of qmm_dequantize's output. */
-typedef enum { QMM_F32 = 0, QMM_F16 = 1 } qmm_dtype;
+/* Element type of activations (x) and of qmm_dequantize's output.  QMM_BF16 is taken by
+ * the qmm_f8_* and qmm_route* calls only. */
+typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_dtype;
 
 /* Token tile of the matrix-matrix path (candle pull request, sections "What
  * changes" and "Where the 64-token tile is used"): AUTO applies
@@ -345,6 +346,217 @@ qmm_status qmm_dequantize(const qmm_matrix *h, int64_t expert, void *out, qmm_dt
  */
 qmm_status qmm_quantize(qmm_type type, const float *w, int64_t M, int64_t K, void *blocks,
                         qmm_stream_t stream);
+
+/*
+ * e4m3 products with one scale per block of 128
+ * ---------------------------------------------
+ * Both operands are 8-bit floats (e4m3: 4 exponent bits, 3 mantissa bits, largest value
+ * 448, one NaN code, no infinity).  The values of a block share an fp32 scale:
+ *   tokens    one scale per token and 128 consecutive values along K;
+ *   weights   one scale per 128 rows x 128 values along K.
+ *     s    = max(fp32(max |v| / 448), 2^-80)     over the block's values v
+ *     code = the e4m3 value nearest to v / s     (ties to even, one rounding)
+ * and a code stands for code * s.  A block that holds an Inf or a NaN gets the scale NaN
+ * (its codes are unspecified): what is computed from it is NaN.
+ * Let Kp = qmm_f8_padded(K), the next multiple of 128, and G = Kp / 128.
+ *   codes of R rows     R * Kp bytes, row r at r * Kp; bytes K .. Kp-1 of a row are zero.
+ *   scales of N tokens  fp32 [G][N]: group-major, so that a group's tokens are adjacent.
+ *   scales of weights   fp32 [qmm_f8_padded(M) / 128][G] per expert.
+ * With K a multiple of 128 the codes are a plain row-major matrix.
+ *
+ *   y[t, r] = sum_g sx[g, t] sw[r / 128, g] sum_{k in g} xq[t, k] wq[r, k]
+ *
+ * Sums are fp32 and y is rounded once to its type.  For an fp32 y a group's 128 products are
+ * summed to 24 bits.  For a 16-bit y they run on the 8-bit matrix cores, which cut each of 8
+ * products at 2^-13 of the largest one's exponent: about 2e-5 of the result on ordinary
+ * data, far below the type's own rounding, and twice as fast.
+ * The path and with it the order of the sums depends on the shapes only: the same call
+ * gives the same bits.  Conventions are those at the top of this file; in addition every
+ * call with nothing to compute (N = 0) returns QMM_OK without looking at its pointers.
+ * Sizes: 0 <= N <= 2^24, 1 <= M <= 2^24, 1 <= K <= 2^22 - 128 unless said otherwise.
+ *
+ * Training: dx = dy W is the product of dy, quantized as tokens along M, with the
+ * transposed matrix' codes (a 128 x 128 block transposes onto a block: the same codes and
+ * scales, qmm_f8_transpose).  dW = dy^T x runs over the tokens: both operands are
+ * quantized in groups of 128 tokens (codes_t of qmm_f8_quantize) and qmm_f8_wgrad
+ * multiplies them.
+ */
+typedef struct qmm_f8_matrix qmm_f8_matrix;
+
+/* n rounded up to a multiple of 128; 0 for n <= 0. */
+int64_t qmm_f8_padded(int64_t n);
+
+/*
+ * qmm_f8_create / qmm_f8_destroy -- describe quantized weights (as qmm_create).
+ *   codes   DEVICE, 16-byte aligned, n_experts * M * Kp bytes.
+ *   scales  DEVICE fp32, 4-byte aligned, n_experts * (qmm_f8_padded(M) / 128) * G.
+ * Both are borrowed.  They may be rewritten in stream order (qmm_f8_quantize_weight).
+ *   n_experts 1 .. 8192.
+ */
+qmm_status qmm_f8_create(qmm_f8_matrix **out, const void *codes, const float *scales,
+                         int64_t n_experts, int64_t M, int64_t K);
+qmm_status qmm_f8_destroy(qmm_f8_matrix *h);
+
+/*
+ * qmm_f8_quantize -- quantize tokens, along K, along the tokens, or both in one pass.
+ *   x         DEVICE [N, K] of type xt, row t at element t * ldx (ldx >= K), aligned to its
+ *             elements (16-byte aligned rows are read faster).
+ *   codes     DEVICE, 16-byte aligned, [N][Kp]; scales fp32 [G][N].  NULL, both: not wanted.
+ *   codes_t   DEVICE, 16-byte aligned, [K][Np] with Np = qmm_f8_padded(N): the codes of the
+ *             transpose, one scale per channel and 128 tokens; scales_t fp32 [Np / 128][K].
+ *             NULL, both: not wanted.
+ */
+qmm_status qmm_f8_quantize(const void *x, qmm_dtype xt, int64_t ldx, int64_t N, int64_t K,
+                           void *codes, float *scales, void *codes_t, float *scales_t,
+                           qmm_stream_t stream);
+
+/*
+ * qmm_f8_quantize_weight -- quantize weights w [n_experts, M, K] (type wt, contiguous) in
+ * blocks of 128 x 128: codes and scales as qmm_f8_create takes them.  codes_t / scales_t
+ * (NULL, both: not wanted) receive the transposed matrices' (n_experts x K rows of
+ * qmm_f8_padded(M) bytes).
+ */
+qmm_status qmm_f8_quantize_weight(const void *w, qmm_dtype wt, int64_t n_experts, int64_t M,
+                                  int64_t K, void *codes, float *scales, void *codes_t,
+                                  float *scales_t, qmm_stream_t stream);
+
+/* qmm_f8_transpose -- codes and scales of the transposed matrices (as
+ * qmm_f8_quantize_weight's codes_t, scales_t) from a handle's. */
+qmm_status qmm_f8_transpose(const qmm_f8_matrix *h, void *codes_t, float *scales_t,
+                            qmm_stream_t stream);
+
+/* qmm_f8_dequantize -- one expert's weights code * s as [M, K] of type ot (as
+ * qmm_dequantize; 16-bit outputs are rounded once more). */
+qmm_status qmm_f8_dequantize(const qmm_f8_matrix *h, int64_t expert, void *out, qmm_dtype ot,
+                             qmm_stream_t stream);
+
+/*
+ * qmm_f8_linear -- quantize the tokens and multiply: y = x W^T for N tokens.
+ *   x     as qmm_f8_quantize.     y   DEVICE [N, M] of type yt, element-aligned.
+ *   ws    DEVICE, 16-byte aligned, ws_bytes >= qmm_f8_linear_workspace_bytes(h, N) (may be
+ *         NULL when that is 0: a few tokens are quantized inside the product's one launch).
+ *         Borrowed until the stream passes the call; concurrent calls need separate ones.
+ * qmm_f8_gemm -- the product alone, of tokens quantized before (several matrices that read
+ * the same tokens share one qmm_f8_quantize).
+ *   codes, scales  of N tokens.   ws  as above, qmm_f8_gemm_workspace_bytes(h, N).
+ */
+size_t qmm_f8_linear_workspace_bytes(const qmm_f8_matrix *h, int64_t N);
+qmm_status qmm_f8_linear(const qmm_f8_matrix *h, const void *x, qmm_dtype xt, int64_t ldx,
+                         int64_t N, void *y, qmm_dtype yt, void *ws, size_t ws_bytes,
+                         qmm_stream_t stream);
+size_t qmm_f8_gemm_workspace_bytes(const qmm_f8_matrix *h, int64_t N);
+qmm_status qmm_f8_gemm(const qmm_f8_matrix *h, const void *codes, const float *scales,
+                       int64_t N, void *y, qmm_dtype yt, void *ws, size_t ws_bytes,
+                       qmm_stream_t stream);
+
+/*
+ * qmm_route_plan -- sort N * S (token, slot) pairs by expert for the calls below.
+ *   ids   DEVICE int32 [N, S]: an expert 0 .. E-1; -1 is an empty slot (a dropped or padded
+ *         token).  Duplicates are pairs of their own.  S 1..64, E 1..1024, N * S <= 2^22.
+ *   plan  DEVICE, 16-byte aligned, qmm_route_plan_bytes(N * S, E) bytes.  Its first E + 2
+ *         int32 are the pairs of each expert, of the empty slots and of the ids that name no
+ *         expert; the rest is the library's.  The same ids give the same plan.
+ */
+size_t qmm_route_plan_bytes(int64_t pairs, int64_t E);
+qmm_status qmm_route_plan(const int32_t *ids, int64_t N, int64_t S, int64_t E, void *plan,
+                          size_t plan_bytes, qmm_stream_t stream);
+
+/*
+ * qmm_f8_linear_id / qmm_f8_gemm_id -- expert-indexed forms: y[t, s] = x_ts W_{ids[t, s]}^T,
+ * y [N, S, M].  x_per_slot as qmm_gemm_id; x [rows, K] contiguous with rows = N * S or N, the
+ * rows' codes below 4 GiB.  An empty slot's row is zeros, the row of an id that names no
+ * expert all NaN.
+ *   plan   qmm_route_plan of the ids with E = the handle's n_experts (<= 1024).
+ *   ws     qmm_f8_linear_id_workspace_bytes(h, N, S, x_per_slot) bytes, as qmm_f8_linear.
+ */
+size_t qmm_f8_linear_id_workspace_bytes(const qmm_f8_matrix *h, int64_t N, int64_t S,
+                                        int x_per_slot);
+qmm_status qmm_f8_linear_id(const qmm_f8_matrix *h, const void *x, qmm_dtype xt, int64_t N,
+                            int64_t S, int x_per_slot, const int32_t *ids, void *y,
+                            qmm_dtype yt, void *ws, size_t ws_bytes, qmm_stream_t stream);
+qmm_status qmm_f8_gemm_id(const qmm_f8_matrix *h, const void *codes, const float *scales,
+                          int64_t N, int64_t S, int x_per_slot, const void *plan, void *y,
+                          qmm_dtype yt, qmm_stream_t stream);
+
+/*
+ * qmm_f8_quantize_routed -- the transposed quantization (codes_t of qmm_f8_quantize) of the
+ * pairs' rows in the plan's order, each expert's pairs padded to groups of 128 on their own.
+ *   x   [rows, K] as qmm_f8_linear_id, row t at t * ldx.
+ *   Np  = qmm_f8_routed_tokens(N * S, E), an upper bound that depends on the sizes only;
+ *         codes_t [K][Np], scales_t fp32 [Np / 128][K].  Groups past the experts' own are not
+ *         written (and not read by qmm_f8_wgrad_id).
+ * qmm_f8_wgrad -- dw[M, K] = g^T x over N tokens, every element written.
+ *   g_codes, g_scales  codes_t / scales_t of g [N, M];  x_codes, x_scales those of x [N, K].
+ *   dw  DEVICE of type dt, element-aligned.  N = 0 writes zeros.  N <= 2^23.
+ * qmm_f8_wgrad_id -- dw[E, M, K], each expert over its own pairs (zeros where it has none);
+ *   both operands from qmm_f8_quantize_routed with the same plan.
+ */
+int64_t qmm_f8_routed_tokens(int64_t pairs, int64_t E);
+qmm_status qmm_f8_quantize_routed(const void *x, qmm_dtype xt, int64_t ldx, int64_t N,
+                                  int64_t S, int x_per_slot, int64_t K, int64_t E,
+                                  const void *plan, void *codes_t, float *scales_t,
+                                  qmm_stream_t stream);
+qmm_status qmm_f8_wgrad(const void *g_codes, const float *g_scales, const void *x_codes,
+                        const float *x_scales, int64_t N, int64_t M, int64_t K, void *dw,
+                        qmm_dtype dt, qmm_stream_t stream);
+qmm_status qmm_f8_wgrad_id(const void *g_codes, const float *g_scales, const void *x_codes,
+                           const float *x_scales, int64_t N, int64_t S, int64_t M, int64_t K,
+                           int64_t E, const void *plan, void *dw, qmm_dtype dt,
+                           qmm_stream_t stream);
+
+/*
+ * qmm_route -- the router in front of the expert-indexed paths.  Per token t, over the E
+ * logits l: p = softmax(l); the S experts of the largest logits, largest first, ties to the
+ * lower index; a logit of -inf (a masked expert) or NaN is never chosen.
+ *   logits   DEVICE [N, E] of type lt, contiguous.  E 1..1024, S 1..min(64, E).
+ *   valid    DEVICE uint8 [N] or NULL: 0 marks a padded row, as if all its logits were -inf.
+ *   normalise 0: weights are p of the chosen experts; 1: divided by their sum.
+ *   ids      int32 [N, S] for qmm_gemm_id / qmm_route_plan; -1 where no expert is left.
+ *   weights  fp32 [N, S]; 0 where the id is -1.
+ *   counts   int32 [E + 1]: pairs of each expert; counts[E] = T, the rows with an expert.
+ *   psum     fp32 [E]: sum over the rows of p.
+ *   loss     fp32 [1] or NULL: the balance loss coef * sum_e f_e P_e with
+ *            f_e = E counts[e] / (S T) and P_e = psum[e] / T; 0 when T = 0.
+ *   ws       DEVICE, 16-byte aligned, qmm_route_workspace_bytes(N, E).
+ * A row with a NaN among its logits, or +inf as its largest, has NaN weights and makes psum
+ * and loss NaN.  Sums over the tokens have a fixed order.  N = 0 writes zero counts, psum and
+ * loss.
+ *
+ * qmm_balance_loss -- the loss from counts and psum, for a caller that adds them over several
+ * micro-batches or GPUs first.
+ *
+ * qmm_route_backward -- dlogits [N, E] (type lt) of a scalar whose gradients are dweights
+ * [N, S] (fp32; NULL: none) with respect to the weights and dloss (fp32 [1] on the DEVICE;
+ * NULL: none) with respect to the loss.  f_e is a constant of the loss, from counts (the
+ * summed ones, if they were summed); ids are qmm_route's.  Padded rows get zeros.
+ */
+size_t qmm_route_workspace_bytes(int64_t N, int64_t E);
+qmm_status qmm_route(const void *logits, qmm_dtype lt, int64_t N, int64_t E, int64_t S,
+                     const uint8_t *valid, int normalise, float coef, int32_t *ids,
+                     float *weights, int32_t *counts, float *psum, float *loss, void *ws,
+                     size_t ws_bytes, qmm_stream_t stream);
+qmm_status qmm_balance_loss(const int32_t *counts, const float *psum, int64_t E, int64_t S,
+                            float coef, float *loss, qmm_stream_t stream);
+qmm_status qmm_route_backward(const void *logits, qmm_dtype lt, int64_t N, int64_t E, int64_t S,
+                              const uint8_t *valid, int normalise, float coef,
+                              const int32_t *ids, const float *dweights,
+                              const int32_t *counts, const float *dloss, void *dlogits,
+                              qmm_stream_t stream);
+
+/*
+ * qmm_route_combine -- out[t] = sum_s weights[t, s] y[t, s] over y [N, S, M], in fp32, slots in
+ * order, rounded once to y's type (out [N, M] has it too).  weights [N, S] fp32 or of y's type
+ * (wt); NULL: the plain sum, the gradient of a token row that its slots share.
+ * qmm_route_combine_backward -- dy[t, s] = weights[t, s] dout[t] (fp32 product, rounded to y's
+ * type) and dweights[t, s] = <y[t, s], dout[t]> (fp32 sum, rounded to wt).
+ * All contiguous and element-aligned.  S 1..64.
+ */
+qmm_status qmm_route_combine(const void *y, qmm_dtype yt, const void *weights, qmm_dtype wt,
+                             int64_t N, int64_t S, int64_t M, void *out, qmm_stream_t stream);
+qmm_status qmm_route_combine_backward(const void *y, qmm_dtype yt, const void *weights,
+                                      qmm_dtype wt, int64_t N, int64_t S, int64_t M,
+                                      const void *dout, void *dy, void *dweights,
+                                      qmm_stream_t stream);
 
 /* qmm_tile_for_tokens -- 64 when a 64-token tile pads no more tokens than a
  * 32-token tile, else 32 (candle pull request, section "Where the 64-token tile

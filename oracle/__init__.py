@@ -16,6 +16,8 @@ Contents
              in fp64, plus the tolerance scale ``S = |x| . |W|^T``.
 ``quantize`` reference quantizers fp32 -> blocks (``quantize_blocks``), the
              check for the library's GPU quantizer.
+``f8``       e4m3 codes with a scale per block of 128: quantizers and decoding.
+``route``    the expert router, balance loss and their gradients.
 ``tile``     the 32/64-token tile rule of the candle pull request
              "Metal: 64-token tile for the quantized matrix-matrix kernel",
              section "Where the 64-token tile is used".
@@ -36,3 +38,4 @@ from .formats import (  # noqa: F401
 from .matmul import matmul_ref, matmul_id_ref, tolerance_scale, tolerance_scale_id  # noqa: F401
 from .tile import tile_for_tokens, pad_tokens  # noqa: F401
 from .quantize import quantize_blocks  # noqa: F401
+from . import f8, route  # noqa: F401

@@ -1,0 +1,154 @@
+"""Refusals of the e4m3 and router calls, without a GPU: the binding's checks of metadata (host tensors that pass them
+are refused for their placement, before a C call) and the C ABI's checks before it looks for a device."""
+
+import ctypes
+
+import pytest
+import torch
+
+import block_quantized_weight_matmul_amd as q
+from block_quantized_weight_matmul_amd import _lib as L
+
+
+def expect(fn, text):
+    with pytest.raises(ValueError, match=text):
+        fn()
+
+
+def f32(*shape):
+    return torch.zeros(shape, dtype=torch.float32)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def matrix(M, K, E=1):
+    m = object.__new__(q.F8Matrix)
+    m.M, m.K, m.n_experts, m._h, m.device = M, K, E, None, torch.device("cpu")
+    return m
+
+
+def plan(N, S, E):
+    return q.RoutePlan(i32(64), N, S, E)
+
+
+def test_quantize_refusals():
+    expect(lambda: q.f8_quantize(torch.zeros((2, 3), dtype=torch.float64)), "x has dtype")
+    expect(lambda: q.f8_quantize(f32(4)), "dimensions")
+    expect(lambda: q.f8_quantize(f32(4, 0)), "no columns")
+    expect(lambda: q.f8_quantize(f32(4, 8)), "device tensor")
+    expect(lambda: q.f8_quantize([1.0]), "torch tensor")
+    expect(lambda: q.F8Matrix.quantize(f32(4, 8)), "device tensor")
+    expect(lambda: q.F8Matrix.quantize(f32(4)), "dimensions")
+    p = plan(4, 2, 3)
+    expect(lambda: q.f8_quantize_t(f32(5, 8), p), "5 rows")
+    expect(lambda: q.f8_quantize_t(f32(4, 3, 8), p), "x has shape")
+    expect(lambda: q.f8_quantize_t(f32(4, 8), p), "device tensor")
+
+
+def test_matrix_refusals():
+    codes, scales = torch.zeros((130, 256), dtype=torch.uint8), f32(2, 2)
+    expect(lambda: q.F8Matrix(codes.float(), scales, 130, 200), "codes has dtype")
+    expect(lambda: q.F8Matrix(codes, scales, 130, 100), "codes has shape")
+    expect(lambda: q.F8Matrix(codes, f32(1, 2), 130, 200), "scales has shape")
+    expect(lambda: q.F8Matrix(codes, scales.half(), 130, 200), "scales has dtype")
+    expect(lambda: q.F8Matrix(codes, scales, 130, 200, 2), "3 dimensions")
+    expect(lambda: q.F8Matrix(codes, scales, 0, 200), "positive")
+    expect(lambda: q.F8Matrix(codes, scales, 130, 200), "device tensor")
+
+
+def test_product_refusals():
+    m = matrix(48, 200)
+    expect(lambda: m.linear(f32(3, 201)), "matrix has K")
+    expect(lambda: m.linear(f32(200)), "dimensions")
+    expect(lambda: m.linear(torch.zeros((3, 200), dtype=torch.int8)), "x has dtype")
+    expect(lambda: m.linear(f32(3, 200)), "device tensor")
+    expect(lambda: m.gemm(f32(3, 200)), "f8_quantize")
+    st = matrix(48, 200, 4)
+    expect(lambda: st.linear(f32(3, 200)), "stacks 4")
+    expect(lambda: st.linear_id(f32(3, 200), i32(3, 2).long()), "ids has dtype")
+    expect(lambda: st.linear_id(f32(4, 200), i32(3, 2)), "x has shape")
+    expect(lambda: st.linear_id(f32(3, 3, 200), i32(3, 2)), "x has shape")
+    expect(lambda: st.linear_id(f32(3, 200), i32(3, 0)), "no slots")
+    expect(lambda: st.linear_id(f32(3, 200), i32(3, 2)), "device tensor")
+    t = object.__new__(q.F8Tokens)
+    t.codes, t.scales, t.rows, t.length, t.plan = torch.zeros((3, 256), dtype=torch.uint8), f32(2, 3), 3, 200, None
+    expect(lambda: st.gemm_id(t, plan(3, 2, 5)), "plan has 5 experts")
+    expect(lambda: st.gemm_id(t, plan(4, 2, 4)), "3 rows")
+    expect(lambda: matrix(48, 199).gemm(t), "tokens have K=200")
+    expect(lambda: m.update(f32(48, 201)), "w has shape")
+    expect(lambda: q.f8_wgrad(t, t, plan(3, 2, 5)), "quantized with the plan")
+
+
+def test_route_refusals():
+    expect(lambda: q.route(f32(4), 1), "dimensions")
+    expect(lambda: q.route(f32(4, 8), 2), "device tensor")
+    expect(lambda: q.route(f32(4, 8).long(), 2), "dtype")
+    expect(lambda: q.route_plan(i32(4, 2).long(), 8), "dtype")
+    expect(lambda: q.route_plan(i32(4, 2), 8), "device tensor")
+    expect(lambda: q.route_plan(i32(4, 0), 8), "a slot")
+    expect(lambda: q.balance_loss(i32(8), f32(8), 2, 0.1), "counts has shape")
+    expect(lambda: q.route_combine(f32(4, 8)), "dimensions")
+    expect(lambda: q.route_combine(f32(4, 2, 8), f32(4, 2)), "device tensor")
+    expect(lambda: q.route_combine_backward(f32(4, 2, 8), None, f32(4, 8)), "weights are needed")
+
+
+def test_c_argument_errors():
+    lib = L.lib
+    buf = ctypes.create_string_buffer(1 << 12)
+    p = (ctypes.addressof(buf) + 255) & ~255
+    h = ctypes.c_void_p()
+    assert lib.qmm_f8_padded(0) == 0 and lib.qmm_f8_padded(-5) == 0
+    assert [lib.qmm_f8_padded(n) for n in (1, 128, 129)] == [128, 128, 256]
+    assert lib.qmm_f8_create(None, p, p, 1, 4, 4) == -1
+    assert lib.qmm_f8_create(ctypes.byref(h), None, p, 1, 4, 4) == -1
+    assert lib.qmm_f8_create(ctypes.byref(h), p + 8, p, 1, 4, 4) == -4
+    assert lib.qmm_f8_create(ctypes.byref(h), p, p, 0, 4, 4) == -3
+    assert lib.qmm_f8_create(ctypes.byref(h), p, p, 1, 0, 4) == -3
+    assert lib.qmm_f8_create(ctypes.byref(h), p, p, 1, 4, 1 << 22) == -3
+    assert lib.qmm_f8_destroy(None) == 0
+    assert lib.qmm_f8_quantize(p, 3, 8, 2, 8, p, p, None, None, None) == -2
+    assert lib.qmm_f8_quantize(p, 0, 7, 2, 8, p, p, None, None, None) == -3      # rows overlap
+    assert lib.qmm_f8_quantize(p, 0, 8, 2, 0, p, p, None, None, None) == -3
+    assert lib.qmm_f8_quantize(p, 0, 8, -1, 8, p, p, None, None, None) == -3
+    assert lib.qmm_f8_quantize(p, 0, 8, 2, 8, p, None, None, None, None) == -1   # codes without scales
+    assert lib.qmm_f8_quantize(p, 0, 8, 2, 8, None, None, None, None, None) == -1
+    assert lib.qmm_f8_quantize(p + 2, 0, 8, 2, 8, p, p, None, None, None) == -4
+    assert lib.qmm_f8_quantize(p, 0, 8, 2, 8, p + 8, p, None, None, None) == -4
+    assert lib.qmm_f8_quantize(None, 0, 8, 0, 8, None, None, None, None, None) == 0  # nothing to do
+    assert lib.qmm_f8_quantize_weight(p, 0, 1, 4, 4, None, None, None, None, None) == -1
+    for fn, args in ((lib.qmm_f8_gemm, (None, p, p, 1, p, 0, None, 0, None)),
+                     (lib.qmm_f8_linear, (None, p, 0, 8, 1, p, 0, None, 0, None)),
+                     (lib.qmm_f8_gemm_id, (None, p, p, 1, 1, 1, p, p, 0, None)),
+                     (lib.qmm_f8_linear_id, (None, p, 0, 1, 1, 1, p, p, 0, None, 0, None)),
+                     (lib.qmm_f8_transpose, (None, p, p, None)), (lib.qmm_f8_dequantize, (None, 0, p, 0, None))):
+        assert fn(*args) == -1 and b"handle" in lib.qmm_last_error()
+    assert lib.qmm_f8_linear_workspace_bytes(None, 4) == 0
+    assert lib.qmm_route_plan_bytes(8, 1025) == 0 and lib.qmm_route_plan_bytes(-1, 4) == 0
+    need = lib.qmm_route_plan_bytes(8, 4)
+    assert need > 0
+    assert lib.qmm_route_plan(p, 4, 2, 4, p, need - 4, None) == -1
+    assert lib.qmm_route_plan(p, 4, 65, 4, p, 1 << 20, None) == -3
+    assert lib.qmm_route_plan(p, 4, 2, 1025, p, 1 << 20, None) == -3
+    assert lib.qmm_route_plan(p, 1 << 22, 2, 4, p, 1 << 40, None) == -3
+    assert lib.qmm_f8_wgrad(p, p, p, p, 1 << 24, 4, 4, p, 0, None) == -3
+    assert lib.qmm_f8_wgrad(p, p, p, p, 4, 4, 4, p, 5, None) == -2
+    assert lib.qmm_f8_wgrad(p, p, None, p, 4, 4, 4, p, 0, None) == -1
+    assert lib.qmm_f8_wgrad_id(p, p, p, p, 4, 1, 4, 4, 4, None, p, 0, None) == -1
+    assert lib.qmm_route(p, 0, 4, 8, 9, None, 1, 0.0, p, p, p, p, p, p, 1 << 20, None) == -3   # S > E
+    assert lib.qmm_route(p, 0, 4, 128, 65, None, 1, 0.0, p, p, p, p, p, p, 1 << 20, None) == -3
+    assert lib.qmm_route(p, 0, 4, 8, 2, None, 2, 0.0, p, p, p, p, p, p, 1 << 20, None) == -1
+    assert lib.qmm_route(p, 0, 4, 8, 2, None, 1, 0.0, p, p, p, p, p, p, 0, None) == -1         # workspace
+    assert lib.qmm_route(p, 0, 4, 8, 2, None, 1, 0.0, p, p, p, p, p, p + 4, 1 << 20, None) == -4
+    assert lib.qmm_route_combine(p, 2, p, 1, 4, 2, 8, p, None) == -2                            # weights' type
+    assert lib.qmm_route_combine(p, 0, None, 0, 4, 0, 8, p, None) == -3
+    assert lib.qmm_route_combine_backward(p, 0, None, 0, 4, 2, 8, p, p, p, None) == -1
+    # a call takes no bf16 that took none before
+    assert lib.qmm_gemv(None, p, 2, 1, p, None) == -1
+
+
+def test_row_layouts_need_no_device():
+    x = f32(4, 8)
+    from block_quantized_weight_matmul_amd import f8
+    expect(lambda: f8._rows(x, "x"), "device tensor")

@@ -1,0 +1,433 @@
+"""e4m3 operands with a scale per block of 128 on the device: quantizers bit for bit, products and gradients against
+the fp64 oracle within the bound its arithmetic allows (oracle.f8.product_bound, plus half a step of the output's type)."""
+
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_weight_matmul_amd as q
+from oracle import f8 as O
+from tests.gpu_helpers import to_host
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+HALF_STEP = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+SMALLEST = {torch.float32: 2.0 ** -149, torch.float16: 2.0 ** -24, torch.bfloat16: 2.0 ** -133}
+
+
+def host64(t):
+    return to_host(t.double())
+
+
+def dev(a, dtype=torch.float32):
+    return torch.from_numpy(np.ascontiguousarray(a)).to("cuda").to(dtype)
+
+
+def check(y, ref, bound, label=""):
+    """bound: an array, or a pair: for 32-bit outputs and for 16-bit ones (which the 8-bit matrix cores compute)."""
+    if isinstance(bound, tuple):
+        bound = bound[y.dtype != torch.float32]
+    got = host64(y)
+    assert got.shape == ref.shape, (got.shape, ref.shape)
+    tol = bound + (np.abs(ref) + bound) * HALF_STEP[y.dtype] + SMALLEST[y.dtype]
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), f"{label}: {bad.sum()} of {got.size}; worst {np.nanmax(np.abs(got - ref) / tol)} of the bound"
+
+
+def bounds(xv, wv):
+    return O.product_bound(xv, wv), O.product_bound(xv, wv, f8_cores=True)
+
+
+def same(codes, scales, want, label=""):
+    wc, ws = want
+    gc, gs = to_host(codes), to_host(scales)
+    assert gs.shape == ws.shape and gc.shape == wc.shape, label
+    assert np.array_equal(gs.view(np.uint32)[~np.isnan(ws)], ws.view(np.uint32)[~np.isnan(ws)]), f"{label}: scales"
+    assert np.array_equal(np.isnan(gs), np.isnan(ws)), f"{label}: NaN scales"
+    if np.isnan(ws).any():   # a block that holds an Inf or a NaN: its codes are not specified
+        keep = np.repeat(~np.isnan(ws.T), 128, 1)   # token scales: [groups, rows]
+        gc, wc = gc[keep], wc[keep]
+    assert np.array_equal(gc, wc), f"{label}: {(gc != wc).sum()} codes differ"
+
+
+def tricky(g, N, K):
+    """Normal values with ties (multiples of 1/64 of the largest), zeros, tiny and large rows."""
+    x = g.standard_normal((N, K))
+    x[::3] = np.round(x[::3] * 64) / 64
+    x[1::5] *= 2.0 ** -12
+    x[2::7] = 0.0
+    x[:, ::41] *= 16.0
+    return x
+
+
+SHAPES = [(1, 1), (1, 128), (3, 127), (5, 129), (16, 256), (33, 515), (129, 130), (300, 1111), (128, 2560)]
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("N,K", SHAPES)
+def test_quantize_bits(N, K, dtype):
+    g = np.random.default_rng([11, N, K])
+    x = dev(tricky(g, N, K), DTYPES[dtype])
+    xv = host64(x)
+    rows, cols = q.f8_quantize_pair(x)
+    same(rows.codes, rows.scales, O.quantize_rows(xv), "rows")
+    same(cols.codes, cols.scales, O.quantize_rows(xv.T), "columns")
+    only = q.f8_quantize(x)
+    assert torch.equal(only.codes, rows.codes) and torch.equal(only.scales, rows.scales)
+    only = q.f8_quantize_t(x)
+    assert torch.equal(only.codes, cols.codes) and torch.equal(only.scales, cols.scales)
+    want = O.rows_values(*O.quantize_rows(xv), K)
+    assert np.all(np.abs(host64(rows.values()) - want) <= np.abs(want) * 2.0 ** -24)
+
+
+def test_quantize_every_quotient():
+    """Ties and their fp32 neighbours: values m * s for every middle m of two codes, and the floats around them."""
+    v = O.e4m3_values()[:127]
+    mid = ((v[1:] + v[:-1]) / 2).astype(np.float32)
+    for amax in (448.0, 1.0, 3.0e-7, 1.7e30, 0.7315):
+        s = np.float32(O.scale(np.array([amax]))[0])
+        m = (mid.astype(np.float64) * s).astype(np.float32)
+        x = np.stack([m, np.nextafter(m, np.float32(np.inf)), np.nextafter(m, np.float32(0)), -m]).T
+        x = np.concatenate([np.full((126, 1), amax, np.float32), x], 1)
+        t = q.f8_quantize(dev(x))
+        same(t.codes, t.scales, O.quantize_rows(x), f"amax {amax}")
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_quantize_extremes(dtype):
+    big = {"f32": 3.0e38, "f16": 65504.0, "bf16": 3.0e38}[dtype]
+    x = np.zeros((6, 400))
+    x[0, 0], x[0, 1], x[0, 2] = big, -big / 2, big / 3
+    x[1, 200], x[1, 201] = 1e-30, -3e-31
+    x[2, 5] = np.inf
+    x[3, 130] = np.nan
+    x[4, 399] = -np.inf
+    x[5] = 2.0 ** -24
+    t = dev(x, DTYPES[dtype])
+    rows, cols = q.f8_quantize_pair(t)
+    same(rows.codes, rows.scales, O.quantize_rows(host64(t)))
+    same(cols.codes, cols.scales, O.quantize_rows(host64(t).T))
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_quantize_strided_rows(dtype):
+    g = np.random.default_rng(12)
+    wide = dev(tricky(g, 37, 700), DTYPES[dtype])
+    for lo, hi in ((0, 700), (8, 400), (1, 300), (699, 700)):
+        x = wide[:, lo:hi]
+        rows, cols = q.f8_quantize_pair(x)
+        same(rows.codes, rows.scales, O.quantize_rows(host64(x)), (lo, hi))
+        same(cols.codes, cols.scales, O.quantize_rows(host64(x).T), (lo, hi))
+    x = wide[::2]
+    assert torch.equal(q.f8_quantize(x).codes, q.f8_quantize(x.contiguous()).codes)
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("E,M,K", [(1, 1, 1), (1, 128, 128), (1, 130, 257), (3, 200, 515), (2, 127, 1024)])
+def test_weight_bits(E, M, K, dtype):
+    g = np.random.default_rng([13, E, M, K])
+    w = dev(g.standard_normal((E, M, K)) * 0.02, DTYPES[dtype])
+    m = q.F8Matrix.quantize(w)
+    wv = host64(w)
+    t = m.transposed()
+    u = q.F8Matrix(torch.full_like(t.codes, 99), torch.zeros_like(t.scales), K, M, E)
+    m.update(w, transposed=u)
+    for e in range(E):
+        same(m.codes[e], m.scales[e], O.quantize_weight(wv[e]), "weights")
+        want = O.quantize_weight(wv[e].T)
+        same(t.codes[e], t.scales[e], want, "transpose")
+        same(u.codes[e], u.scales[e], want, "transpose of update")
+        value = O.weight_values(*O.quantize_weight(wv[e]), K)
+        for dt in DTYPES.values():
+            check(m.dequantize(e, dt), value, np.abs(value) * 2.0 ** -24, "dequantize")
+
+
+def weights(g, M, K):
+    w = g.standard_normal((M, K)) * 0.02
+    codes, scales = O.quantize_weight(w)
+    return q.F8Matrix(dev_u8(codes), dev(scales), M, K), O.weight_values(codes, scales, K)
+
+
+def dev_u8(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to("cuda")
+
+
+TOKENS = [1, 2, 5, 8, 16, 17, 32, 33, 64, 100, 129, 256, 300]
+
+
+@pytest.mark.parametrize("N", TOKENS)
+@pytest.mark.parametrize("M,K", [(64, 128), (1000, 1111), (130, 515), (257, 2560), (1, 1), (4, 40)])
+def test_linear_and_gemm(N, M, K):
+    g = np.random.default_rng([14, N, M, K])
+    m, wv = weights(g, M, K)
+    for i, dt in enumerate(DTYPES.values()):
+        x = dev(g.standard_normal((N, K)), dt)
+        xv = O.rows_values(*O.quantize_rows(host64(x)), K)
+        ref, bound = xv @ wv.T, bounds(xv, wv)
+        y = torch.full((N, M), float("nan"), dtype=dt, device="cuda")
+        m.linear(x, out=y)
+        check(y, ref, bound, f"linear {dt}")
+        assert torch.equal(y, m.linear(x)), "two calls, two results"
+        out = list(DTYPES.values())[(i + 1) % 3]
+        check(m.gemm(q.f8_quantize(x), out_dtype=out), ref, bound, f"gemm to {out}")
+
+
+@pytest.mark.parametrize("N,M,K", [(1, 2560, 9728), (3, 1024, 8192), (16, 2560, 9728), (48, 512, 9728), (200, 512, 9728)])
+def test_linear_long_rows(N, M, K):
+    g = np.random.default_rng([15, N])
+    m, wv = weights(g, M, K)
+    x = dev(g.standard_normal((N, K)), torch.float16)
+    xv = O.rows_values(*O.quantize_rows(host64(x)), K)
+    check(m.linear(x, out_dtype=torch.float32), xv @ wv.T, bounds(xv, wv))
+
+
+def test_linear_strided_and_unaligned():
+    g = np.random.default_rng(16)
+    M, K = 96, 300
+    m, wv = weights(g, M, K)
+    wide = dev(g.standard_normal((40, 3 * K)), torch.bfloat16)
+    for n, lo in ((1, 5), (4, 8), (40, K), (40, 2 * K)):
+        x = wide[:n, lo:lo + K]
+        xv = O.rows_values(*O.quantize_rows(host64(x)), K)
+        y = torch.zeros(n * M + 1, dtype=torch.bfloat16, device="cuda")[1:].view(n, M)  # 2-byte aligned output
+        m.linear(x, out=y)
+        check(y, xv @ wv.T, bounds(xv, wv), (n, lo))
+
+
+def test_rows_behind_the_last_token_stay():
+    g = np.random.default_rng(17)
+    m, _ = weights(g, 100, 256)
+    for n in (1, 7, 20, 130):
+        y = torch.full((n + 3, 100), 7.0, device="cuda")
+        m.linear(dev(g.standard_normal((n, 256))), out=y[:n])
+        assert bool((y[n:] == 7.0).all()) and not bool((y[:n] == 7.0).any())
+
+
+def test_bad_token_poisons_its_row_only():
+    g = np.random.default_rng(18)
+    m, _ = weights(g, 70, 300)
+    for n in (3, 40, 200):
+        x = g.standard_normal((n, 300))
+        x[1, 17], x[2, 299] = np.nan, np.inf
+        y = to_host(m.linear(dev(x)))
+        assert np.isnan(y[1:3]).all() and np.isfinite(np.delete(y, (1, 2), 0)).all()
+
+
+def test_no_tokens():
+    g = np.random.default_rng(19)
+    m, _ = weights(g, 10, 20)
+    assert m.linear(torch.empty((0, 20), device="cuda")).shape == (0, 10)
+    t, tt = q.f8_quantize_pair(torch.empty((0, 20), device="cuda"))
+    assert m.gemm(t).shape == (0, 10)
+    dw = q.f8_wgrad(q.f8_quantize_t(torch.empty((0, 10), device="cuda")), tt, out=torch.full((10, 20), 5.0, device="cuda"))
+    assert bool((dw == 0).all())
+
+
+# ---- experts -----------------------------------------------------------------------------------
+
+def stack(g, E, M, K):
+    codes, scales, values = [], [], []
+    for _ in range(E):
+        c, s = O.quantize_weight(g.standard_normal((M, K)) * 0.02)
+        codes.append(c)
+        scales.append(s)
+        values.append(O.weight_values(c, s, K))
+    return q.F8Matrix(dev_u8(np.stack(codes)), dev(np.stack(scales)), M, K, E), values
+
+
+def id_reference(xv, ids, values, M):
+    N, S = ids.shape
+    ref, bound, coarse = (np.zeros((N, S, M)) for _ in range(3))
+    for e, w in enumerate(values):
+        t, s = np.nonzero(ids == e)
+        if len(t):
+            rows = xv[t, s] if xv.ndim == 3 else xv[t]
+            ref[t, s] = rows @ w.T
+            bound[t, s], coarse[t, s] = bounds(rows, w)
+    return ref, (bound, coarse)
+
+
+def quantized_values(x):
+    flat = host64(x).reshape(-1, x.shape[-1])
+    return O.rows_values(*O.quantize_rows(flat), x.shape[-1]).reshape(tuple(x.shape))
+
+
+ID_CASES = [  # N, S, E, M, K
+    (1, 1, 1, 16, 32), (1, 8, 128, 64, 512), (4, 8, 32, 300, 512), (5, 3, 4, 130, 200), (40, 2, 3, 70, 1111),
+    (16, 8, 8, 100, 256), (64, 4, 16, 129, 384), (300, 2, 5, 64, 130), (700, 1, 2, 20, 40), (2, 64, 100, 32, 128)]
+
+
+@pytest.mark.parametrize("per_slot", [False, True])
+@pytest.mark.parametrize("N,S,E,M,K", ID_CASES)
+def test_expert_products(N, S, E, M, K, per_slot):
+    g = np.random.default_rng([20, N, S, E])
+    m, values = stack(g, E, M, K)
+    ids = g.integers(0, E, (N, S)).astype(np.int32)   # duplicates among a token's slots too
+    if N > 1:
+        ids[g.random((N, S)) < 0.15] = -1
+        ids[N // 2, 0] = E           # names no expert
+        ids[N // 2 + 1:][:1] = -1    # a padded token
+    for dt in DTYPES.values():
+        x = dev(g.standard_normal((N, S, K) if per_slot else (N, K)), dt)
+        ref, bound = id_reference(quantized_values(x), ids, values, M)
+        plan = q.route_plan(dev_u8(ids), E)
+        want = np.array([(ids == e).sum() for e in range(E)])
+        assert np.array_equal(to_host(plan.counts), want)
+        rows = x.reshape(-1, K)
+        for y in (m.linear_id(x, dev_u8(ids)), m.gemm_id(q.f8_quantize(rows), plan, out_dtype=dt)):
+            none = ids >= E
+            assert bool(torch.isnan(y[torch.from_numpy(none).cuda()]).all())
+            y = torch.where(torch.from_numpy(none).cuda()[:, :, None], torch.zeros_like(y), y)
+            check(y, ref, bound, f"{dt}")
+
+
+def test_all_slots_empty_or_one_expert():
+    g = np.random.default_rng(21)
+    E, M, K = 4, 50, 130
+    m, values = stack(g, E, M, K)
+    for N in (2, 200):
+        x = dev(g.standard_normal((N, K)))
+        y = m.linear_id(x, torch.full((N, 2), -1, dtype=torch.int32, device="cuda"))
+        assert bool((y == 0).all())
+        ids = np.full((N, 2), 3, np.int32)
+        ref, bound = id_reference(quantized_values(x), ids, values, M)
+        check(m.linear_id(x, dev_u8(ids)), ref, bound)
+
+
+@pytest.mark.parametrize("pairs_per_token", [1, 3])
+def test_many_pairs(pairs_per_token):
+    """More pairs than one sweep of the plan's workgroups holds: every pair finds its own row."""
+    N, S, E, M, K = 110000, pairs_per_token, 5, 4, 8
+    g = np.random.default_rng(22)
+    m, values = stack(g, E, M, K)
+    ids = g.integers(-1, E, (N, S)).astype(np.int32)
+    x = dev(g.standard_normal((N, K)))
+    ref, bound = id_reference(quantized_values(x), ids, values, M)
+    check(m.linear_id(x, dev_u8(ids)), ref, bound)
+
+
+# ---- gradients ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("N,M,K", [(1, 1, 1), (5, 40, 30), (128, 128, 256), (333, 130, 257), (1000, 64, 300)])
+def test_gradients(N, M, K, dtype):
+    g = np.random.default_rng([23, N, M])
+    dt = DTYPES[dtype]
+    m, wv = weights(g, M, K)
+    x, dy = dev(g.standard_normal((N, K)), dt), dev(g.standard_normal((N, M)) * 0.01, dt)
+    xq, xt = q.f8_quantize_pair(x)
+    gq, gt = q.f8_quantize_pair(dy)
+    gv = O.rows_values(*O.quantize_rows(host64(dy)), M)
+    check(m.transposed().gemm(gq, out_dtype=dt), gv @ wv, bounds(gv, wv.T), "dx")
+    gtv, xtv = (O.rows_values(*O.quantize_rows(host64(t).T), N) for t in (dy, x))
+    for out in DTYPES.values():
+        check(q.f8_wgrad(gt, xt, dtype=out), gtv @ xtv.T, bounds(gtv, xtv), f"dw {out}")
+    # against the difference of the loss <dy, x W^T> along a direction: linear, so it is exact but for the quantization
+    # (half a step of e4m3 on each operand: 2^-4 relative, or 2^-10 of the block's largest / 448)
+    v = g.standard_normal((M, K))
+    dw = host64(q.f8_wgrad(gt, xt))
+    a, b = np.abs(host64(dy)), np.abs(host64(x))
+    da, db = a * 2.0 ** -4 + a.max() * 2.0 ** -18, b * 2.0 ** -4 + b.max() * 2.0 ** -18
+    slack = (da.T @ b + a.T @ db + da.T @ db) * (1 + 1e-3)
+    difference = (host64(dy) * (host64(x) @ v.T)).sum()
+    assert abs((dw * v).sum() - difference) <= (slack * np.abs(v)).sum()
+
+
+@pytest.mark.parametrize("per_slot", [False, True])
+@pytest.mark.parametrize("N,S,E,M,K", [(1, 1, 1, 5, 7), (40, 2, 4, 70, 130), (300, 3, 6, 33, 140), (2, 8, 64, 24, 40),
+                                       (600, 2, 2, 128, 128)])
+def test_expert_gradients(N, S, E, M, K, per_slot):
+    g = np.random.default_rng([24, N, E])
+    ids = g.integers(0, E, (N, S)).astype(np.int32)
+    if N > 1:
+        ids[g.random((N, S)) < 0.2] = -1
+        ids[ids == E - 1] = 0        # an expert without pairs
+        ids[1, 0] = E + 3            # names no expert: no part in any gradient
+    x = dev(g.standard_normal((N, S, K) if per_slot else (N, K)), torch.bfloat16)
+    dy = dev(g.standard_normal((N, S, M)), torch.bfloat16)
+    plan = q.route_plan(dev_u8(ids), E)
+    dw = torch.full((E, M, K), float("nan"), device="cuda", dtype=DTYPES["f32" if per_slot else "bf16"])
+    q.f8_wgrad(q.f8_quantize_t(dy, plan), q.f8_quantize_t(x, plan), plan, out=dw)
+    xv, gv = host64(x), host64(dy)
+    for e in range(E):
+        t, s = np.nonzero(ids == e)
+        if not len(t):
+            assert bool((dw[e] == 0).all())
+            continue
+        rows = xv[t, s] if per_slot else xv[t]
+        a = O.rows_values(*O.quantize_rows(gv[t, s].T), len(t))
+        b = O.rows_values(*O.quantize_rows(rows.T), len(t))
+        check(dw[e], a @ b.T, bounds(a, b), f"expert {e}")
+
+
+# ---- streams, graphs -----------------------------------------------------------------------------
+
+def test_side_stream_order():
+    g = np.random.default_rng(25)
+    m, wv = weights(g, 200, 640)
+    x = dev(g.standard_normal((5, 640)))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        y = m.linear(x * 2.0) * 0.5
+    side.synchronize()
+    xv = O.rows_values(*O.quantize_rows(host64(x) * 2), 640)
+    check(y, xv @ wv.T * 0.5, bounds(xv, wv)[0] * 0.5)
+
+
+def test_graph_replays():
+    g = np.random.default_rng(26)
+    M, K, E = 260, 515, 6
+    m, _ = weights(g, M, K)
+    ex, _ = stack(g, E, M, K)
+    w = dev(g.standard_normal((M, K)) * 0.02)
+    mt = m.transposed()
+    x1, x300 = dev(g.standard_normal((1, K))), dev(g.standard_normal((300, K)), torch.bfloat16)
+    dy = dev(g.standard_normal((300, M)) * 0.01, torch.bfloat16)
+    few, many = (dev_u8(g.integers(-1, E, (n, 2)).astype(np.int32)) for n in (3, 300))
+
+    def step():
+        m.update(w, transposed=mt)
+        xq, xt = q.f8_quantize_pair(x300)
+        gq, gt = q.f8_quantize_pair(dy)
+        plan = q.route_plan(many, E)
+        return [m.linear(x1), m.gemm(xq), mt.gemm(gq), q.f8_wgrad(gt, xt), ex.linear_id(x1.expand(3, K).contiguous(), few),
+                ex.linear_id(x300, many), ex.gemm_id(xq, plan)]
+
+    eager = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):   # two captures: workspaces of their own
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(step())
+        graphs.append(graph)
+    for rep in range(3):
+        for graph, out in zip(graphs, outs):
+            for o in out:
+                o.fill_(float("nan"))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(eager, out):
+                assert torch.equal(a, b), f"replay {rep}"
+        _ = (x300.float() * 2).sum().item()
+
+
+def test_new_weights_are_seen():
+    """update rewrites the borrowed codes in stream order: the next product uses them."""
+    g = np.random.default_rng(27)
+    w = [dev(g.standard_normal((64, 200))) for _ in range(2)]
+    m = q.F8Matrix.quantize(w[0])
+    x = dev(g.standard_normal((3, 200)))
+    first = m.linear(x).clone()
+    m.update(w[1])
+    second = m.linear(x)
+    assert not torch.equal(first, second)
+    assert torch.equal(second, q.F8Matrix.quantize(w[1]).linear(x))
