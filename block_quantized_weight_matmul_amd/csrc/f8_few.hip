@@ -1,0 +1,424 @@
+// f8_few.hip -- e4m3 products of few tokens, bound by reading the weights once.
+//
+// A workgroup owns 16 * RT weight rows and divides K among its waves (wave v takes groups v, v + KS, ..): a wave loads
+// its groups' codes straight into the registers of the matrix instruction (16 rows x 128 bytes, whole cache lines),
+// keeps its partial outputs, and the workgroup adds the waves' partials in wave order through LDS.  Nothing but the
+// partials and, for raw tokens, the tokens' codes passes through LDS.  Two batches of kBatch groups are in flight per
+// wave, so a row of 128 * 16 * 2 * kBatch values is requested before the first product.
+#include <algorithm>
+#include <climits>
+
+#include "f8.hpp"
+#include "f8_mma.hpp"
+
+namespace qmm {
+
+namespace {
+
+constexpr int kMaxWaves = 8;
+constexpr int kBatch = 4;
+constexpr int kFusedLds = 48 << 10;  // token codes a workgroup quantizes for itself
+
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x128, 0xF, 0xF, false)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x124, 0xF, 0xF, false)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x122, 0xF, 0xF, false)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x121, 0xF, 0xF, false)));
+  return v;
+}
+
+// Quantize `rows` tokens into LDS: codes [g][row][128], 16-byte pieces xored with the row's low bits, scales [g][row].
+// A team of 16 lanes takes one (row, group).  row_of(i): pointer to row i.
+template <int XT, class RowOf>
+__device__ __forceinline__ void quantize_to_lds(RowOf row_of, int rows, int64_t K, int G, bool vec, uint8_t* codes,
+                                                float* scales, int threads) {
+  typedef typename Elem<XT>::T T;
+  const int lane = threadIdx.x & 15;
+  for (int w = threadIdx.x >> 4; w < rows * G; w += threads >> 4) {
+    const int g = w / rows, t = w - g * rows;
+    const T* row = row_of(t);
+    const int64_t c = static_cast<int64_t>(g) * kF8Block + lane * 8;
+    float v[8];
+    if (vec && c + 8 <= K) {
+      load8<XT>(row + c, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c + i < K ? static_cast<float>(row[c + i]) : 0.0f;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+    const float s = f8_scale(max16(m)), rs = 1.0f / s;
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = f8_quotient(v[i], s, rs);
+    *reinterpret_cast<uint2*>(codes + static_cast<size_t>(w) * 128 + (((lane >> 1) ^ (t & 7)) * 16) + (lane & 1) * 8) =
+        make_uint2(f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7]));
+    if (lane == 0) scales[w] = s;
+  }
+}
+
+struct FewArgs {
+  const uint8_t* w;
+  const float* ws;
+  const void* x;      // raw tokens (RAW) or codes [N][Kp]
+  const float* xs;    // [G][N] (not RAW)
+  void* y;
+  int64_t M, K, Kp, ldx;
+  int N, G, waves, vec_x, vec_y;
+};
+
+template <int RT>
+struct Batch {
+  i32x4 lo[kBatch][RT], hi[kBatch][RT];
+};
+
+// RAW: element type of raw tokens, -1 for quantized ones
+template <int RT, int NT, int RAW, int OT>
+__global__ __launch_bounds__(64 * kMaxWaves) void k_f8_few(FewArgs a) {
+  extern __shared__ __align__(16) uint8_t sh[];
+  constexpr bool kExact = OT == DT_F32;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, q = lane >> 4;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * (16 * RT);
+  const uint8_t* wrow[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) wrow[i] = a.w + std::min<int64_t>(r0 + i * 16 + row, a.M - 1) * a.Kp + q * 32;
+  const float* wsc = a.ws + r0 / 128 * a.G;  // 16 * RT divides 128: the rows share their scales
+  const int KS = a.waves, last = a.G - 1;
+
+  Batch<RT> b0, b1;
+  auto load = [&](Batch<RT>& b, int i0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t g = std::min(i0 + u * KS, last);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        b.lo[u][i] = *reinterpret_cast<const i32x4*>(wrow[i] + g * 128);
+        b.hi[u][i] = *reinterpret_cast<const i32x4*>(wrow[i] + g * 128 + 16);
+      }
+    }
+  };
+  load(b0, wave);
+  load(b1, wave + kBatch * KS);
+
+  uint8_t* codes = sh;
+  float* scales = reinterpret_cast<float*>(sh + static_cast<size_t>(a.N) * a.Kp);
+  if constexpr (RAW >= 0) {
+    typedef typename Elem<RAW < 0 ? 0 : RAW>::T T;
+    const T* x = static_cast<const T*>(a.x);
+    const int64_t ldx = a.ldx;
+    quantize_to_lds<RAW < 0 ? 0 : RAW>([=](int t) { return x + t * ldx; }, a.N, a.K, a.G, a.vec_x, codes, scales,
+                                       KS * 64);
+    __syncthreads();
+  }
+
+  f32x4 acc[RT][NT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](const Batch<RT>& b, int i0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      // a group past the last is the last one again, its part multiplied by zero (what is NaN there is NaN anyway)
+      const int gu = i0 + u * KS, g = std::min(gu, last);
+      const float sw = gu <= last ? wsc[g] : 0.0f;
+      Frag<kExact> A[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) A[i].set(b.lo[u][i], b.hi[u][i]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int t = std::min(j * 16 + row, a.N - 1);
+        i32x4 lo, hi;
+        float s;
+        if constexpr (RAW >= 0) {
+          const uint8_t* p = codes + (static_cast<size_t>(g) * a.N + t) * 128;
+          lo = *reinterpret_cast<const i32x4*>(p + 16 * ((2 * q) ^ (t & 7)));
+          hi = *reinterpret_cast<const i32x4*>(p + 16 * ((2 * q + 1) ^ (t & 7)));
+          s = scales[g * a.N + t] * sw;
+        } else {
+          const uint8_t* p = static_cast<const uint8_t*>(a.x) + t * a.Kp + static_cast<int64_t>(g) * 128 + q * 32;
+          lo = *reinterpret_cast<const i32x4*>(p);
+          hi = *reinterpret_cast<const i32x4*>(p + 16);
+          s = a.xs[static_cast<int64_t>(g) * a.N + t] * sw;
+        }
+        Frag<kExact> B;
+        B.set(lo, hi);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const f32x4 p = group_sum(A[i], B);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], s, acc[i][j][e]);
+        }
+      }
+    }
+  };
+  for (int i0 = wave; i0 <= last; i0 += 2 * kBatch * KS) {
+    multiply(b0, i0);
+    if (i0 + 2 * kBatch * KS <= last) load(b0, i0 + 2 * kBatch * KS);
+    if (i0 + kBatch * KS <= last) multiply(b1, i0 + kBatch * KS);
+    if (i0 + 3 * kBatch * KS <= last) load(b1, i0 + 3 * kBatch * KS);
+  }
+
+  __syncthreads();
+  f32x4* part = reinterpret_cast<f32x4*>(sh);  // [wave][RT][NT][lane]
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[((wave * RT + i) * NT + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  typedef typename Elem<OT>::T T;
+  for (int p = wave; p < RT * NT; p += KS) {
+    f32x4 v = part[p * 64 + lane];
+    for (int k = 1; k < KS; ++k) v += part[(k * RT * NT + p) * 64 + lane];
+    const int i = p / NT, t = (p - i * NT) * 16 + row;
+    const int64_t r = r0 + i * 16 + q * 4, left = a.M - r;
+    if (t < a.N && left > 0)
+      store4<OT>(static_cast<T*>(a.y) + static_cast<int64_t>(t) * a.M + r, v, left < 4 ? static_cast<int>(left) : 4, a.vec_y);
+  }
+}
+
+// ---- experts -------------------------------------------------------------------------------------
+
+constexpr int kIdThreads = 256;
+constexpr int kIdPairs = 256;     // pairs of a fused call: one a thread
+constexpr int kIdRows = 64;       // rows of a workgroup, 16 a wave
+
+struct FewIdArgs {
+  const uint8_t* w;
+  const float* ws;
+  const void* x;
+  const int32_t* ids;
+  void* y;
+  int64_t M, K, Kp;
+  int E, pairs, slots, G, vec_x, vec_y;
+};
+
+// grid (row slices, distinct experts at most): workgroup (s, j) finds the j-th distinct expert among the ids (in order of
+// first appearance) and its pairs, quantizes their tokens 16 at a time and multiplies its rows by them.  Slice s of j = 0
+// also fills the rows of empty slots and of ids that name no expert.
+template <int XT, int OT>
+__global__ __launch_bounds__(kIdThreads) void k_f8_few_id(FewIdArgs a) {
+  extern __shared__ __align__(16) uint8_t sh[];
+  __shared__ int32_t first[kRouteMaxExperts];
+  __shared__ int32_t mine[kIdPairs];
+  __shared__ int32_t before[4], expert;
+  typedef typename Elem<XT>::T T;
+  typedef typename Elem<OT>::T O;
+  constexpr bool kExact = OT == DT_F32;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, row = lane & 15, q = lane >> 4;
+  const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kIdRows;
+  O* y = static_cast<O*>(a.y);
+
+  const int id = tid < a.pairs ? a.ids[tid] : -1;
+  const bool real = tid < a.pairs && id >= 0 && id < a.E;
+  for (int e = tid; e < a.E; e += kIdThreads) first[e] = kIdPairs;
+  if (tid == 0) expert = -1;
+  __syncthreads();
+  if (real) atomicMin(&first[id], tid);
+  __syncthreads();
+  const bool lead = real && first[id] == tid;
+  const uint64_t leads = __ballot(lead);
+  if (lane == 0) before[wave] = __popcll(leads);
+  __syncthreads();
+  int rank = __popcll(leads & ((1ull << lane) - 1));
+  for (int k = 0; k < wave; ++k) rank += before[k];
+  if (lead && rank == static_cast<int>(blockIdx.y)) expert = id;
+  __syncthreads();
+  if (blockIdx.y == 0) {
+    const int rows = static_cast<int>(std::min<int64_t>(kIdRows, a.M - s0));
+    for (int p = wave; p < a.pairs; p += kIdThreads / 64) {
+      const int other = a.ids[p];
+      if (other >= 0 && other < a.E) continue;
+      const float v = other == -1 ? 0.0f : __uint_as_float(0x7FC00000u);
+      if (lane < rows) y[static_cast<int64_t>(p) * a.M + s0 + lane] = to_elem<OT>(v);
+    }
+  }
+  const int e = expert;
+  if (e < 0) return;  // fewer distinct experts than workgroups
+  const bool own = real && id == e;
+  const uint64_t owns = __ballot(own);
+  if (lane == 0) before[wave] = __popcll(owns);
+  __syncthreads();
+  int at = __popcll(owns & ((1ull << lane) - 1)), all = 0;
+  for (int k = 0; k < 4; ++k) {
+    if (k < wave) at += before[k];
+    all += before[k];
+  }
+  if (own) mine[at] = tid;
+
+  const int64_t r0 = s0 + wave * 16;
+  const uint8_t* wrow = a.w + (static_cast<int64_t>(e) * a.M + std::min<int64_t>(r0 + row, a.M - 1)) * a.Kp + q * 32;
+  const float* wsc = a.ws + (static_cast<int64_t>(e) * ((a.M + 127) / 128) + std::min<int64_t>(r0, a.M - 1) / 128) * a.G;
+  const int last = a.G - 1;
+  i32x4 lo[kBatch], hi[kBatch];
+  auto load = [&](int g0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t g = std::min(g0 + u, last);
+      lo[u] = *reinterpret_cast<const i32x4*>(wrow + g * 128);
+      hi[u] = *reinterpret_cast<const i32x4*>(wrow + g * 128 + 16);
+    }
+  };
+  load(0);
+  __syncthreads();
+
+  float* scales = reinterpret_cast<float*>(sh + 16 * a.Kp);
+  for (int p0 = 0; p0 < all; p0 += 16) {
+    const int n = std::min(16, all - p0);
+    if (p0) {
+      load(0);
+      __syncthreads();  // the codes of the pass before are read
+    }
+    const T* x = static_cast<const T*>(a.x);
+    quantize_to_lds<XT>([&](int t) { return x + static_cast<int64_t>(mine[p0 + t] / a.slots) * a.K; }, n, a.K, a.G, a.vec_x,
+                        sh, scales, kIdThreads);
+    __syncthreads();
+    const int t = std::min(row, n - 1);
+    f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int g0 = 0; g0 <= last; g0 += kBatch) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int g = std::min(g0 + u, last);
+        const float sw = g0 + u <= last ? wsc[g] : 0.0f;
+        const uint8_t* p = sh + (g * n + t) * 128;
+        Frag<kExact> A, B;
+        A.set(lo[u], hi[u]);
+        B.set(*reinterpret_cast<const i32x4*>(p + 16 * ((2 * q) ^ (t & 7))),
+              *reinterpret_cast<const i32x4*>(p + 16 * ((2 * q + 1) ^ (t & 7))));
+        const f32x4 v = group_sum(A, B);
+        const float s = scales[g * n + t] * sw;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(v[i], s, acc[i]);
+      }
+      if (g0 + kBatch <= last) load(g0 + kBatch);
+    }
+    const int64_t r = r0 + q * 4, left = a.M - r;
+    if (row < n && left > 0)
+      store4<OT>(y + static_cast<int64_t>(mine[p0 + row]) * a.M + r, acc, left < 4 ? static_cast<int>(left) : 4, a.vec_y);
+  }
+}
+
+int few_waves(int G) { return std::max(1, std::min(kMaxWaves, (G + 1) / 2)); }
+
+template <int RT, int NT, int RAW, int OT>
+hipError_t few_run(const FewArgs& a, hipStream_t st) {
+  const int64_t blocks = (a.M + 16 * RT - 1) / (16 * RT);
+  const size_t codes = RAW >= 0 ? static_cast<size_t>(a.N) * (a.Kp + a.G * 4) : 0;
+  const size_t lds = std::max(codes, static_cast<size_t>(a.waves) * RT * NT * 1024);
+  k_f8_few<RT, NT, RAW, OT><<<static_cast<unsigned>(blocks), 64 * a.waves, lds, st>>>(a);
+  return hipGetLastError();
+}
+
+template <int RAW, int OT>
+hipError_t few_tokens(const FewArgs& a, hipStream_t st) {
+  if (RAW >= 0 || a.N <= 16) return few_run<1, 1, RAW, OT>(a, st);
+  if constexpr (RAW < 0) {
+    if (a.N <= 32) return few_run<1, 2, RAW, OT>(a, st);
+    return few_run<1, 4, RAW, OT>(a, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <int RAW>
+hipError_t few_out(const FewArgs& a, int yt, hipStream_t st) {
+  switch (yt) {
+    case DT_F32: return few_tokens<RAW, DT_F32>(a, st);
+    case DT_F16: return few_tokens<RAW, DT_F16>(a, st);
+    case DT_BF16: return few_tokens<RAW, DT_BF16>(a, st);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+FewArgs few_args(const F8Desc& m, int64_t N, void* y, int yt) {
+  FewArgs a{};
+  a.w = m.codes;
+  a.ws = m.scales;
+  a.y = y;
+  a.M = m.M;
+  a.K = m.K;
+  a.Kp = m.Kp;
+  a.N = static_cast<int>(N);
+  a.G = static_cast<int>(m.Kp / kF8Block);
+  a.waves = few_waves(a.G);
+  a.vec_y = store_vec(y, m.M, yt);
+  return a;
+}
+
+bool rows_vec(const void* x, int xt, int64_t ldx, int64_t N) {
+  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && (N <= 1 || ldx * (xt == DT_F32 ? 4 : 2) % 16 == 0);
+}
+
+template <int XT>
+hipError_t few_id_out(const FewIdArgs& a, int yt, dim3 grid, size_t lds, hipStream_t st) {
+  switch (yt) {
+    case DT_F32: k_f8_few_id<XT, DT_F32><<<grid, kIdThreads, lds, st>>>(a); break;
+    case DT_F16: k_f8_few_id<XT, DT_F16><<<grid, kIdThreads, lds, st>>>(a); break;
+    case DT_BF16: k_f8_few_id<XT, DT_BF16><<<grid, kIdThreads, lds, st>>>(a); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool f8_few_tokens(const F8Desc&, int64_t N) { return N <= 64; }
+
+hipError_t launch_f8_few(const F8Desc& m, const uint8_t* xc, const float* xs, int64_t N, void* y, int yt, hipStream_t st) {
+  FewArgs a = few_args(m, N, y, yt);
+  a.x = xc;
+  a.xs = xs;
+  return few_out<-1>(a, yt, st);
+}
+
+bool f8_linear_fused(const F8Desc& m, int64_t N) {
+  return N <= 16 && N * (m.Kp + m.Kp / kF8Block * 4) <= 16384;
+}
+
+hipError_t launch_f8_linear(const F8Desc& m, const void* x, int xt, int64_t ldx, int64_t N, void* y, int yt,
+                            hipStream_t st) {
+  FewArgs a = few_args(m, N, y, yt);
+  a.x = x;
+  a.ldx = ldx;
+  a.vec_x = rows_vec(x, xt, ldx, N);
+  switch (xt) {
+    case DT_F32: return few_out<DT_F32>(a, yt, st);
+    case DT_F16: return few_out<DT_F16>(a, yt, st);
+    case DT_BF16: return few_out<DT_BF16>(a, yt, st);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+bool f8_linear_id_fused(const F8Desc& m, int64_t pairs, int) {
+  return pairs <= kIdPairs && 16 * (m.Kp + m.Kp / kF8Block * 4) <= kFusedLds;
+}
+
+hipError_t launch_f8_linear_id(const F8Desc& m, const void* x, int xt, int64_t pairs, int slots, const int32_t* ids, void* y,
+                               int yt, hipStream_t st) {
+  FewIdArgs a{};
+  a.w = m.codes;
+  a.ws = m.scales;
+  a.x = x;
+  a.ids = ids;
+  a.y = y;
+  a.M = m.M;
+  a.K = m.K;
+  a.Kp = m.Kp;
+  a.E = static_cast<int>(m.n_experts);
+  a.pairs = static_cast<int>(pairs);
+  a.slots = slots;
+  a.G = static_cast<int>(m.Kp / kF8Block);
+  a.vec_x = rows_vec(x, xt, m.K, pairs / slots);
+  a.vec_y = store_vec(y, m.M, yt);
+  const int64_t slices = (m.M + kIdRows - 1) / kIdRows;
+  const dim3 grid(static_cast<unsigned>(slices), static_cast<unsigned>(std::min<int64_t>(pairs, m.n_experts)));
+  const size_t lds = 16 * static_cast<size_t>(m.Kp + a.G * 4);
+  switch (xt) {
+    case DT_F32: return few_id_out<DT_F32>(a, yt, grid, lds, st);
+    case DT_F16: return few_id_out<DT_F16>(a, yt, grid, lds, st);
+    case DT_BF16: return few_id_out<DT_BF16>(a, yt, grid, lds, st);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace qmm

@@ -137,7 +137,11 @@ def _empty_tokens(rows, pitch, device):
 
 
 def _quantize(x, along_k, along_n):
-    _tensor(x, "x", tuple(_DT), (2,))
+    _tensor(x, "x", tuple(_DT), (2, 3))
+    if x.dim() == 3:
+        if not x.is_contiguous():
+            raise ValueError("x of three dimensions must be contiguous")
+        x = x.view(-1, x.shape[2])
     N, K = x.shape
     if K == 0:
         raise ValueError("x has no columns")
@@ -151,7 +155,8 @@ def _quantize(x, along_k, along_n):
 
 
 def f8_quantize(x: torch.Tensor) -> F8Tokens:
-    """x [N, K] (fp32, fp16 or bf16; rows may be strided) quantized as tokens: one scale per 128 values along K."""
+    """x [N, K] (fp32, fp16 or bf16; rows may be strided) or [N, S, K] quantized as tokens: one scale per 128 values
+    along K."""
     return _quantize(x, True, False)[0]
 
 
