@@ -90,6 +90,7 @@ struct F8WgradArgs {
   int dt;
   const int32_t* plan;
   PlanDesc pd;
+  int cus;
 };
 hipError_t launch_f8_wgrad(const F8WgradArgs& a, hipStream_t s);
 
@@ -138,6 +139,7 @@ hipError_t launch_route_combine_backward(const void* y, int yt, const void* w, i
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 template <int DT> struct Elem;
 template <> struct Elem<DT_F32> { typedef float T; };

@@ -380,6 +380,7 @@ static qmm_status wgrad(const void* gc, const float* gs, const void* xc, const f
   a.Np = Np;
   a.dw = dw;
   a.dt = dt;
+  a.cus = 256;  // of gfx950; only the choice of a tile depends on it
   if (pd) {
     a.plan = static_cast<const int32_t*>(plan);
     a.pd = *pd;

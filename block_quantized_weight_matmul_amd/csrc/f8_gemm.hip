@@ -3,6 +3,7 @@
 // Tiled kernel for many tokens; the arithmetic and the choice of matrix cores are f8_mma.hpp's, few tokens f8_few.hip's.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 
 #include "f8.hpp"
 #include "f8_mma.hpp"
@@ -13,6 +14,9 @@ namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, voff, soff, 0, 0);
+}
 // 16 bytes a lane straight into LDS: lane i's at dst + 16 i (dst: the wave's base)
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t voff, uint32_t soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, voff, soff, 0, 0);
@@ -32,7 +36,7 @@ struct GemmArgs {
   PlanDesc pd;
   int map;            // index of the token tile's map in the plan
   int slots;          // MODE_ID: pairs that share a token row
-  int vec;            // outputs of 4 consecutive rows may be stored at once
+  int vec;            // 16 bytes of consecutive outputs may be stored at once
 };
 
 // One workgroup: TM rows x TN tokens, its waves in a WM x WN grid; K in stages of one group, two stages in LDS.
@@ -40,19 +44,36 @@ struct GemmArgs {
 // lanes of a read phase (8 rows, one piece) use every bank once.
 template <int TM, int TN, int WM, int WN, int MODE, int OT>
 __global__ __launch_bounds__(64 * WM * WN) void k_f8_gemm(GemmArgs a) {
-  constexpr int NT = 64 * WM * WN, RT = TM / WM / 16, CT = TN / WN / 16;
+  constexpr int NT = 64 * WM * WN, RT = TM / WM / 32, CT = TN / WN / 32;
   constexpr int AI = TM * 8 / NT, BI = TN * 8 / NT;  // 16-byte pieces a thread stages
   static_assert(AI * NT == TM * 8 && BI * NT == TN * 8, "tile");
   constexpr bool kRowScale = MODE == MODE_WGRAD;
-  constexpr int kStage = (TM + TN) * 128 + TN * 4 + (kRowScale ? TM * 4 : 0);
+  constexpr int W = WM * WN;
+  constexpr int TS = TN < 64 ? 64 : TN;                // room of the token scales: whole loads of 64
+  constexpr int kScales = TS + (kRowScale ? TM : 64);  // then the rows' or the row blocks'
+  constexpr int kUnitsPer = (kScales / 64 + W - 1) / W;  // loads of 64 scales a wave; those past the last repeat it
+  constexpr int kStage = (TM + TN) * 128 + kUnitsPer * W * 256;
   __shared__ __align__(128) uint8_t lds[2][kStage];
   typedef typename Elem<OT>::T T;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WM, wn = wave / WM;
   int64_t bid = blockIdx.x;
-  const int tm = static_cast<int>(bid % a.tiles_m);
-  bid /= a.tiles_m;
+  int tm;
+  if constexpr (MODE == MODE_DENSE) {
+    // Workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles, kGroup row tiles by all token tiles after
+    // another, so that the tiles it works on share their operands in its L2.
+    constexpr int kXcds = 8, kGroup = 1024 / TM;
+    const int64_t n = gridDim.x, per = n / kXcds, more = n % kXcds, x = bid % kXcds;
+    bid = x * per + std::min(x, more) + bid / kXcds;
+    const int64_t in = static_cast<int64_t>(kGroup) * a.tiles_n, gm = bid / in * kGroup;
+    const int64_t wide = std::min<int64_t>(kGroup, a.tiles_m - gm), off = bid % in;
+    tm = static_cast<int>(gm + off % wide);
+    bid = off / wide;
+  } else {
+    tm = static_cast<int>(bid % a.tiles_m);
+    bid /= a.tiles_m;
+  }
   const int64_t r0 = static_cast<int64_t>(tm) * TM;
   int64_t M = a.M, N = a.N;
   const uint8_t* w = a.w;
@@ -90,42 +111,43 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_gemm(GemmArgs a) {
     t0 = bid * TN;
   }
 
-  // what this thread stages: offsets from the tile's first row
+  // What this thread stages: 16-byte pieces, offsets from the tile's first row (rows past the end repeat the last), and
+  // scales, 64 to a wave's load.
   const int64_t last_m = M - 1 - r0;
   const __amdgpu_buffer_rsrc_t rw = rsrc(w + r0 * a.pitch, static_cast<uint32_t>(std::min<int64_t>(TM, M - r0) * a.pitch));
-  __amdgpu_buffer_rsrc_t rx, rxs;
-  uint32_t aoff[AI], boff[BI];
+  const __amdgpu_buffer_rsrc_t rx =
+      MODE == MODE_ID ? rsrc(a.x, static_cast<uint32_t>(N * a.pitch))
+                      : rsrc(a.x + t0 * a.pitch, static_cast<uint32_t>(std::min<int64_t>(TN, N - t0) * a.pitch));
+  auto token = [&](int i) -> int64_t {  // tile row i: its row of x, from t0
+    if constexpr (MODE == MODE_ID) return a.plan[a.pd.order + first + (i < count ? i : count - 1)] / a.slots;
+    else return i < N - 1 - t0 ? i : N - 1 - t0;
+  };
+  uint32_t aoff[AI], boff[BI], soff[kUnitsPer];
 #pragma unroll
   for (int i = 0; i < AI; ++i) {
     const int p = i * NT + tid, row = p >> 3;
-    aoff[i] = static_cast<uint32_t>((row < last_m ? row : last_m) * a.pitch) + 16 * ((p ^ row) & 7);
-  }
-  if constexpr (MODE == MODE_ID) {
-    rx = rsrc(a.x, static_cast<uint32_t>(N * a.pitch));
-    rxs = rsrc(a.xs, static_cast<uint32_t>(N * a.G * 4));
-  } else {
-    rx = rsrc(a.x + t0 * a.pitch, static_cast<uint32_t>(std::min<int64_t>(TN, N - t0) * a.pitch));
-    rxs = rx;
+    aoff[i] = static_cast<uint32_t>((row < last_m ? row : last_m) * a.pitch) + 16 * ((p ^ (row >> 1)) & 7);
   }
 #pragma unroll
   for (int i = 0; i < BI; ++i) {
     const int p = i * NT + tid, row = p >> 3;
-    int64_t src;
-    if constexpr (MODE == MODE_ID) src = a.plan[a.pd.order + first + (row < count ? row : count - 1)] / a.slots;
-    else src = row < N - 1 - t0 ? row : N - 1 - t0;
-    boff[i] = static_cast<uint32_t>(src * a.pitch) + 16 * ((p ^ row) & 7);
+    boff[i] = static_cast<uint32_t>(token(row) * a.pitch) + 16 * ((p ^ (row >> 1)) & 7);
   }
-  // scales: thread i < TN the token's, the next TM (WGRAD) the row's
-  int64_t soff = 0;
-  const bool sx_thread = tid < TN;
-  if constexpr (MODE == MODE_ID) {
-    if (sx_thread) soff = a.plan[a.pd.order + first + (tid < count ? tid : count - 1)] / a.slots;
-  } else {
-    if (sx_thread) soff = t0 + tid < N ? t0 + tid : N - 1;
+  const float* sbase[kUnitsPer];
+  int64_t sstep[kUnitsPer];
+  uint32_t sbytes[kUnitsPer];
+#pragma unroll
+  for (int k = 0; k < kUnitsPer; ++k) {
+    const int u = k * W + wave, i = std::min(u * 64 + lane, kScales - 1);
+    const bool tokens = u * 64 < TS;  // the same for a whole wave
+    if (i < TS) soff[k] = 4 * static_cast<uint32_t>(t0 + token(std::min(i, TN - 1)));
+    else if (kRowScale) soff[k] = 4 * static_cast<uint32_t>(r0 + (i - TS < last_m ? i - TS : last_m));
+    else soff[k] = 4 * static_cast<uint32_t>(std::min<int64_t>(i - TS, (M - 1) / 128 - r0 / 128) * a.G);
+    sbase[k] = tokens ? a.xs : kRowScale ? wsc : wsc + r0 / 128 * a.G;
+    sstep[k] = tokens ? N : kRowScale ? M : 1;
+    // the last row block's scales end at its G-th: a base advanced by g leaves G - g of them
+    sbytes[k] = tokens || kRowScale ? 0u : static_cast<uint32_t>(((M + 127) / 128 - r0 / 128) * a.G * 4);
   }
-  const float* srow_x = a.xs + soff;
-  const float* srow_w = kRowScale && tid < TM ? wsc + (r0 + tid < M ? r0 + tid : M - 1) : nullptr;
-  (void)rxs;
 
   auto stage = [&](int buf, int g) {
     uint8_t* d = lds[buf];
@@ -134,96 +156,120 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_gemm(GemmArgs a) {
     for (int i = 0; i < AI; ++i) load_lds16(rw, d + (i * NT + wave * 64) * 16, aoff[i], ks);
 #pragma unroll
     for (int i = 0; i < BI; ++i) load_lds16(rx, d + TM * 128 + (i * NT + wave * 64) * 16, boff[i], ks);
-  };
-  float nsx = 0.0f, nsw = 0.0f;
-  auto fetch_scales = [&](int g) {
-    if (sx_thread) nsx = srow_x[static_cast<int64_t>(g) * N];
-    if (kRowScale && tid < TM) nsw = srow_w[static_cast<int64_t>(g) * M];
-  };
-  auto put_scales = [&](int buf) {
-    float* s = reinterpret_cast<float*>(lds[buf] + (TM + TN) * 128);
-    if (sx_thread) s[tid] = nsx;
-    if (kRowScale && tid < TM) s[TN + tid] = nsw;
+#pragma unroll
+    for (int k = 0; k < kUnitsPer; ++k)
+      load_lds4(rsrc(sbase[k] + g * sstep[k], sbytes[k] ? sbytes[k] - 4 * g : static_cast<uint32_t>(sstep[k]) * 4),
+                d + (TM + TN) * 128 + (k * W + wave) * 256, soff[k], 0);
   };
 
-  f32x4 acc[RT][CT];
+  f32x16 acc[RT][CT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int j = 0; j < CT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < CT; ++j) acc[i][j] = f32x16{};
 
-  // a wave's rows lie in one 128-row block of the weights (TM / WM divides 128)
+  // a wave's rows lie in one 128-row block of the weights
   static_assert(128 % (TM / WM) == 0, "a wave's rows share their scales");
-  const float* wblock = wsc + (kRowScale ? 0 : ((r0 + wm * (TM / WM)) / 128) * static_cast<int64_t>(a.G));
-  const bool wave_rows = r0 + wm * (TM / WM) < M;
-
-  if (g0 < g1) {
-    stage(0, g0);
-    fetch_scales(g0);
-    put_scales(0);
+  const int row = lane & 31, half = lane >> 5;
+  uint32_t piece[2][2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    piece[m][0] = row * 128 + 16 * ((4 * m + 2 * half) ^ (row >> 1 & 7));
+    piece[m][1] = row * 128 + 16 * ((4 * m + 2 * half + 1) ^ (row >> 1 & 7));
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  for (int g = g0; g < g1; ++g) {
-    const int buf = (g - g0) & 1;
-    if (g + 1 < g1) {
-      stage(buf ^ 1, g + 1);
-      fetch_scales(g + 1);
-    }
-    const uint8_t* A = lds[buf] + wm * (TM / WM) * 128;
-    const uint8_t* B = lds[buf] + TM * 128 + wn * (TN / WN) * 128;
-    const float* S = reinterpret_cast<const float*>(lds[buf] + (TM + TN) * 128);
-    const int row = lane & 15, q = lane >> 4;
-    const int c0 = 16 * ((2 * q) ^ (row & 7)), c1 = 16 * ((2 * q + 1) ^ (row & 7));
-    float wscale = 1.0f;
-    if (!kRowScale && wave_rows) wscale = wblock[g];
-    Frag<OT == DT_F32> b[CT];
-    float s[CT];
+  typedef Frag32<OT == DT_F32> F;
+  auto read_frag = [&](F& f, const uint8_t* p) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+      f.set(m, *reinterpret_cast<const i32x4*>(p + piece[m][0]), *reinterpret_cast<const i32x4*>(p + piece[m][1]));
+  };
+  const uint8_t* Abase = lds[0] + wm * (TM / WM) * 128;
+  const uint8_t* Bbase = lds[0] + (TM + wn * (TN / WN)) * 128;
+  const float* Sbase = reinterpret_cast<const float*>(lds[0] + (TM + TN) * 128);
+  F b[CT];
+  float sc[CT];
+  auto read_b = [&](int buf) {
+    const float* S = Sbase + buf * (kStage / 4);
+    const float wscale = kRowScale ? 1.0f : S[TS + wm * (TM / WM) / 128];
 #pragma unroll
     for (int j = 0; j < CT; ++j) {
-      const i32x4 lo = *reinterpret_cast<const i32x4*>(B + (j * 16 + row) * 128 + c0);
-      const i32x4 hi = *reinterpret_cast<const i32x4*>(B + (j * 16 + row) * 128 + c1);
-      b[j].set(lo, hi);
-      s[j] = S[wn * (TN / WN) + j * 16 + row] * wscale;
+      read_frag(b[j], Bbase + buf * kStage + j * 4096);
+      sc[j] = S[wn * (TN / WN) + j * 32 + row] * wscale;
     }
+  };
+  auto read_rs = [&](f32x4* rs, int buf, int i) {
+    if (kRowScale) {
+      const float* S = Sbase + buf * (kStage / 4) + TS + wm * (TM / WM) + i * 32 + half * 4;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rs[k] = *reinterpret_cast<const f32x4*>(S + 8 * k);
+    }
+  };
+  auto add = [&](f32x16& to, const f32x16& p, float s, const f32x4* rs) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) to[e] = fmaf(p[e], kRowScale ? s * rs[e / 4][e % 4] : s, to[e]);
+  };
+
+  if (g0 < g1) stage(0, g0);
+  for (int g = g0; g < g1; ++g) {
+    const int buf = (g - g0) & 1;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the stage's loads, issued a whole stage ago
+    __syncthreads();
+    if (g + 1 < g1) stage(buf ^ 1, g + 1);
+    read_b(buf);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const i32x4 lo = *reinterpret_cast<const i32x4*>(A + (i * 16 + row) * 128 + c0);
-      const i32x4 hi = *reinterpret_cast<const i32x4*>(A + (i * 16 + row) * 128 + c1);
-      Frag<OT == DT_F32> av;
-      av.set(lo, hi);
-      f32x4 rs{1.0f, 1.0f, 1.0f, 1.0f};
-      if (kRowScale) rs = *reinterpret_cast<const f32x4*>(S + TN + wm * (TM / WM) + i * 16 + q * 4);
+      F av;
+      f32x4 rs[4];
+      read_frag(av, Abase + buf * kStage + i * 4096);
+      read_rs(rs, buf, i);
 #pragma unroll
-      for (int j = 0; j < CT; ++j) {
-        const f32x4 p = group_sum(av, b[j]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[i][j][e] = fmaf(p[e], kRowScale ? s[j] * rs[e] : s[j], acc[i][j][e]);
-      }
+      for (int j = 0; j < CT; ++j) add(acc[i][j], group_sum(av, b[j]), sc[j], rs);
     }
-    if (g + 1 < g1) put_scales(buf ^ 1);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
   }
 
+  // Outputs leave through LDS, 32 tokens of the wave's rows at a time: a lane holds 4 rows of one token, and stores
+  // straight from there would be 16 bytes a token (10 us of the 60 at 4096 x 4096 outputs).
+  constexpr int kRows = RT * 32, kPitch = kRows * static_cast<int>(sizeof(T)) + 16, kVec = 16 / static_cast<int>(sizeof(T));
+  static_assert(W * 32 * kPitch <= 2 * kStage, "the waves' regions fit the stages");
+  __syncthreads();
+  uint8_t* mine = lds[0] + wave * (32 * kPitch);
+  const int64_t rw0 = r0 + wm * kRows;
+  const int rows = static_cast<int>(std::min<int64_t>(kRows, M - rw0));  // may be negative
 #pragma unroll
   for (int j = 0; j < CT; ++j) {
-    const int t = wn * (TN / WN) + j * 16 + (lane & 15);
-    int64_t yrow;
-    if constexpr (MODE == MODE_ID) {
-      if (t >= count) continue;
-      yrow = a.plan[a.pd.order + first + t];
-    } else {
-      yrow = t0 + t;
-      if (yrow >= N) continue;
-    }
+    const int tj = wn * (TN / WN) + j * 32;
+    int tokens = MODE == MODE_ID ? count - tj : static_cast<int>(std::min<int64_t>(32, N - t0 - tj));
+    tokens = std::min(tokens, 32);
+    auto out = [&](int t) -> T* {
+      if constexpr (MODE == MODE_ID) return y + static_cast<int64_t>(a.plan[a.pd.order + first + tj + t]) * M + rw0;
+      else return y + (t0 + tj + t) * M + rw0;
+    };
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int64_t r = r0 + wm * (TM / WM) + i * 16 + (lane >> 4) * 4;
-      const int64_t left = M - r;
-      if (left > 0) store4<OT>(y + yrow * M + r, acc[i][j], left < 4 ? static_cast<int>(left) : 4, a.vec);
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        typedef T T4 __attribute__((ext_vector_type(4)));
+        T4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = to_elem<OT>(acc[i][j][4 * k + e]);
+        *reinterpret_cast<T4*>(mine + row * kPitch + (i * 32 + k * 8 + half * 4) * sizeof(T)) = o;
+      }
+    __builtin_amdgcn_wave_barrier();
+    if (a.vec) {  // M is a multiple of kVec and rows are 16-byte aligned
+      constexpr int kLanes = kRows / kVec;  // lanes that store one token's rows
+#pragma unroll
+      for (int n = 0; n < 32 * kLanes / 64; ++n) {
+        const int t = n * (64 / kLanes) + lane / kLanes, c = lane % kLanes * kVec;
+        if (t < tokens && c < rows)
+          *reinterpret_cast<uint4*>(out(t) + c) = *reinterpret_cast<const uint4*>(mine + t * kPitch + c * sizeof(T));
+      }
+    } else {
+      for (int n = lane; n < 32 * kRows; n += 64) {
+        const int t = n / kRows, c = n % kRows;
+        if (t < tokens && c < rows) out(t)[c] = *reinterpret_cast<const T*>(mine + t * kPitch + c * sizeof(T));
+      }
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -238,6 +284,92 @@ hipError_t run_tile(const GemmArgs& a, int ot, int64_t blocks, hipStream_t st) {
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
+}
+
+int store_vec16(const void* y, int64_t M, int ot) {
+  return reinterpret_cast<uintptr_t>(y) % 16 == 0 && M % (ot == DT_F32 ? 4 : 8) == 0;
+}
+
+// The tiles, the workgroups of each that a CU holds at once, and what one stage (128 values of K) of 1 .. per_cu of
+// them costs there, in us: 4096 x 4096 x 2560, 8192^3 and 512 x 4096 x 2560 with a 16-bit output.  A call takes the
+// tile with the least estimated time; against measurements of nine shapes the estimate is within 8%, and it is the
+// last round of a launch, its CUs part-filled, that decides (dx of 4096 x 2560, 32 stages: 256 x 256 tiles 60 us, 128 x
+// 128 67, 64 x 64 74; 512 x 4096: 33, 20, 14).
+struct TileKind {
+  int tm, tn, per_cu;
+  float round;   // prologue and epilogue of a round
+  float us[4];
+};
+enum { TILE_256 = 0, TILE_128 = 1, TILE_128_64 = 2, TILE_64 = 3, TILE_128_32 = 4 };
+constexpr TileKind kTiles[] = {
+    {256, 256, 1, 5.0f, {1.95f}},
+    {128, 128, 2, 2.0f, {0.85f, 1.21f}},
+    {128, 64, 3, 1.5f, {0.50f, 0.75f, 1.02f}},
+    {64, 64, 4, 1.0f, {0.33f, 0.48f, 0.75f, 0.99f}},
+    {128, 32, 4, 1.0f, {0.35f, 0.50f, 0.65f, 0.80f}},
+};
+
+// tiles: workgroups of a launch, of `stages` stages each
+float tile_cost(const TileKind& k, double tiles, double stages, int cus) {
+  const double per = std::ceil(tiles / cus);
+  const double full = std::floor(per / k.per_cu);
+  const int rest = static_cast<int>(per - full * k.per_cu);
+  return static_cast<float>(full * (k.us[k.per_cu - 1] * stages + k.round) + (rest > 0 ? k.us[rest - 1] * stages + k.round : 0.0));
+}
+
+int best_tile(const int* kinds, int n, const double* tiles, double stages, int cus) {
+  int best = 0;
+  for (int i = 1; i < n; ++i)
+    if (tile_cost(kTiles[kinds[i]], tiles[i], stages, cus) < tile_cost(kTiles[kinds[best]], tiles[best], stages, cus)) best = i;
+  return kinds[best];
+}
+
+// dense products: M rows, N tokens, `many` matrices
+template <int MODE>
+hipError_t run_dense(GemmArgs& a, int ot, int64_t many, double stages, int cus, hipStream_t st) {
+  // an fp32 output's operands are twice as wide in registers: no 256 x 256 tile
+  const int kinds[] = {TILE_128, TILE_128_64, TILE_64, TILE_256};
+  const int n = ot == DT_F32 ? 3 : 4;
+  double tiles[4];
+  for (int i = 0; i < n; ++i) {
+    const TileKind& k = kTiles[kinds[i]];
+    tiles[i] = static_cast<double>((a.M + k.tm - 1) / k.tm) * static_cast<double>((a.N + k.tn - 1) / k.tn) * static_cast<double>(many);
+  }
+  const int kind = best_tile(kinds, n, tiles, stages, cus);
+  const TileKind& k = kTiles[kind];
+  a.tiles_m = static_cast<int>((a.M + k.tm - 1) / k.tm);
+  a.tiles_n = static_cast<int>((a.N + k.tn - 1) / k.tn);
+  const int64_t blocks = static_cast<int64_t>(a.tiles_m) * a.tiles_n * many;
+  switch (kind) {
+    case TILE_256: return run_tile<256, 256, 2, 4, MODE>(a, ot, blocks, st);
+    case TILE_128: return run_tile<128, 128, 2, 2, MODE>(a, ot, blocks, st);
+    case TILE_128_64: return run_tile<128, 64, 2, 2, MODE>(a, ot, blocks, st);
+    default: return run_tile<64, 64, 2, 2, MODE>(a, ot, blocks, st);
+  }
+}
+
+// expert products: the pairs of each expert in tiles of their own
+hipError_t run_experts(GemmArgs& a, int ot, int cus, hipStream_t st) {
+  const int kinds[] = {TILE_128, TILE_128_64, TILE_64, TILE_128_32};
+  double tiles[4];
+  const double experts = static_cast<double>(std::min(a.pd.E, a.pd.pairs));
+  for (int i = 0; i < 4; ++i) {
+    const TileKind& k = kTiles[kinds[i]];
+    // about half a tile of each expert is padding
+    tiles[i] = static_cast<double>((a.M + k.tm - 1) / k.tm) * (static_cast<double>(a.pd.pairs) / k.tn + experts * 0.5);
+  }
+  const int kind = best_tile(kinds, 4, tiles, a.G, cus);
+  const TileKind& k = kTiles[kind];
+  a.tiles_m = static_cast<int>((a.M + k.tm - 1) / k.tm);
+  a.map = 0;
+  while (kPlanTiles[a.map] != k.tn) ++a.map;
+  const int64_t blocks = static_cast<int64_t>(a.tiles_m) * a.pd.cap[a.map];
+  switch (kind) {
+    case TILE_128: return run_tile<128, 128, 2, 2, MODE_ID>(a, ot, blocks, st);
+    case TILE_128_64: return run_tile<128, 64, 2, 2, MODE_ID>(a, ot, blocks, st);
+    case TILE_64: return run_tile<64, 64, 2, 2, MODE_ID>(a, ot, blocks, st);
+    default: return run_tile<128, 32, 4, 1, MODE_ID>(a, ot, blocks, st);
+  }
 }
 
 }  // namespace
@@ -257,10 +389,8 @@ hipError_t launch_f8_gemm(const F8Desc& m, const uint8_t* xc, const float* xs, i
   a.N = N;
   a.pitch = m.Kp;
   a.G = static_cast<int>(m.Kp / kF8Block);
-  a.vec = store_vec(y, m.M, yt);
-  a.tiles_m = static_cast<int>((m.M + 127) / 128);
-  a.tiles_n = static_cast<int>((N + 127) / 128);
-  return run_tile<128, 128, 2, 2, MODE_DENSE>(a, yt, static_cast<int64_t>(a.tiles_m) * a.tiles_n, st);
+  a.vec = store_vec16(y, m.M, yt);
+  return run_dense<MODE_DENSE>(a, yt, 1, a.G, m.cus, st);
 }
 
 hipError_t launch_f8_gemm_id(const F8Desc& m, const uint8_t* xc, const float* xs, int64_t pairs, int slots,
@@ -275,13 +405,11 @@ hipError_t launch_f8_gemm_id(const F8Desc& m, const uint8_t* xc, const float* xs
   a.N = pairs / slots;
   a.pitch = m.Kp;
   a.G = static_cast<int>(m.Kp / kF8Block);
-  a.vec = store_vec(y, m.M, yt);
+  a.vec = store_vec16(y, m.M, yt);
   a.plan = plan;
   a.pd = plan_desc(pairs, m.n_experts);
   a.slots = slots;
-  a.tiles_m = static_cast<int>((m.M + 127) / 128);
-  a.map = 3;
-  return run_tile<128, 128, 2, 2, MODE_ID>(a, yt, static_cast<int64_t>(a.tiles_m) * a.pd.cap[3], st);
+  return run_experts(a, yt, m.cus, st);
 }
 
 hipError_t launch_f8_wgrad(const F8WgradArgs& w, hipStream_t st) {
@@ -295,13 +423,11 @@ hipError_t launch_f8_wgrad(const F8WgradArgs& w, hipStream_t st) {
   a.N = w.M;
   a.pitch = w.Np;
   a.G = static_cast<int>(w.Np / kF8Block);
-  a.vec = store_vec(w.dw, w.K, w.dt);
+  a.vec = store_vec16(w.dw, w.K, w.dt);
   a.plan = w.plan;
   a.pd = w.pd;
-  a.tiles_m = static_cast<int>((w.K + 127) / 128);
-  a.tiles_n = static_cast<int>((w.M + 127) / 128);
   const int64_t E = w.plan ? w.pd.E : 1;
-  return run_tile<128, 128, 2, 2, MODE_WGRAD>(a, w.dt, static_cast<int64_t>(a.tiles_m) * a.tiles_n * E, st);
+  return run_dense<MODE_WGRAD>(a, w.dt, E, std::max(1.0, static_cast<double>(a.G) / E), w.cus, st);
 }
 
 }  // namespace qmm

