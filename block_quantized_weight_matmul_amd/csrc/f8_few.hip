@@ -1,10 +1,9 @@
 // f8_few.hip -- e4m3 products of few tokens, bound by reading the weights once.
 //
-// A workgroup owns 16 * RT weight rows and divides K among its waves (wave v takes groups v, v + KS, ..): a wave loads
+// A workgroup owns 16 weight rows and divides K among its waves (wave v takes groups v, v + KS, ..): a wave loads
 // its groups' codes straight into the registers of the matrix instruction (16 rows x 128 bytes, whole cache lines),
 // keeps its partial outputs, and the workgroup adds the waves' partials in wave order through LDS.  Nothing but the
-// partials and, for raw tokens, the tokens' codes passes through LDS.  Two batches of kBatch groups are in flight per
-// wave, so a row of 128 * 16 * 2 * kBatch values is requested before the first product.
+// partials and, for raw tokens, the tokens' codes passes through LDS.  Two batches of groups are in flight per wave.
 #include <algorithm>
 #include <climits>
 
@@ -15,7 +14,6 @@ namespace qmm {
 
 namespace {
 
-constexpr int kMaxWaves = 8;
 constexpr int kBatch = 4;
 constexpr int kFusedLds = 48 << 10;  // token codes a workgroup quantizes for itself
 
@@ -27,35 +25,36 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
   return v;
 }
 
-// Quantize `rows` tokens into LDS: codes [g][row][128], 16-byte pieces xored with the row's low bits, scales [g][row].
-// A team of 16 lanes takes one (row, group).  row_of(i): pointer to row i.
-template <int XT, class RowOf>
-__device__ __forceinline__ void quantize_to_lds(RowOf row_of, int rows, int64_t K, int G, bool vec, uint8_t* codes,
-                                                float* scales, int threads) {
-  typedef typename Elem<XT>::T T;
-  const int lane = threadIdx.x & 15;
-  for (int w = threadIdx.x >> 4; w < rows * G; w += threads >> 4) {
-    const int g = w / rows, t = w - g * rows;
-    const T* row = row_of(t);
-    const int64_t c = static_cast<int64_t>(g) * kF8Block + lane * 8;
-    float v[8];
-    if (vec && c + 8 <= K) {
-      load8<XT>(row + c, v);
-    } else {
+// A team of 16 lanes quantizes one (row, group) of a token into LDS: codes [g][row][128], 16-byte pieces xored with
+// bits 1..3 of the row (two rows fill the 64 banks, so 16 lanes that read one piece of 16 rows use every bank once),
+// scales [g][row].
+template <int XT>
+__device__ __forceinline__ void load_group(const typename Elem<XT>::T* row, int g, int64_t K, bool vec, float* v) {
+  const int64_t c = static_cast<int64_t>(g) * kF8Block + (threadIdx.x & 15) * 8;
+  if (vec && c + 8 <= K) {
+    load8<XT>(row + c, v);
+  } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c + i < K ? static_cast<float>(row[c + i]) : 0.0f;
-    }
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
-    const float s = f8_scale(max16(m)), rs = 1.0f / s;
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = f8_quotient(v[i], s, rs);
-    *reinterpret_cast<uint2*>(codes + static_cast<size_t>(w) * 128 + (((lane >> 1) ^ (t & 7)) * 16) + (lane & 1) * 8) =
-        make_uint2(f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7]));
-    if (lane == 0) scales[w] = s;
+    for (int i = 0; i < 8; ++i) v[i] = c + i < K ? static_cast<float>(row[c + i]) : 0.0f;
   }
+}
+__device__ __forceinline__ void store_group(const float* v, int w, int t, uint8_t* codes, float* scales) {
+  const int lane = threadIdx.x & 15;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+  const float s = f8_scale(max16(m)), rs = 1.0f / s;
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = f8_quotient(v[i], s, rs);
+  *reinterpret_cast<uint2*>(codes + static_cast<size_t>(w) * 128 + (((lane >> 1) ^ (t >> 1 & 7)) * 16) + (lane & 1) * 8) =
+      make_uint2(f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7]));
+  if (lane == 0) scales[w] = s;
+}
+// the two pieces of a row that quarter q of the lanes multiplies
+__device__ __forceinline__ void read_codes(const uint8_t* p, int t, int q, i32x4& lo, i32x4& hi) {
+  lo = *reinterpret_cast<const i32x4*>(p + 16 * ((2 * q) ^ (t >> 1 & 7)));
+  hi = *reinterpret_cast<const i32x4*>(p + 16 * ((2 * q + 1) ^ (t >> 1 & 7)));
 }
 
 struct FewArgs {
@@ -68,113 +67,132 @@ struct FewArgs {
   int N, G, waves, vec_x, vec_y;
 };
 
-template <int RT>
-struct Batch {
-  i32x4 lo[kBatch][RT], hi[kBatch][RT];
-};
-
-// RAW: element type of raw tokens, -1 for quantized ones
-template <int RT, int NT, int RAW, int OT>
-__global__ __launch_bounds__(64 * kMaxWaves) void k_f8_few(FewArgs a) {
+// RAW: element type of raw tokens, -1 for quantized ones.  B: groups of a batch.  W: most waves of a workgroup (128
+// registers a lane at 16, 256 at 8).
+template <int NT, int RAW, int OT, int B, int W>
+__global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
   extern __shared__ __align__(16) uint8_t sh[];
   constexpr bool kExact = OT == DT_F32;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, q = lane >> 4;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * (16 * RT);
-  const uint8_t* wrow[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) wrow[i] = a.w + std::min<int64_t>(r0 + i * 16 + row, a.M - 1) * a.Kp + q * 32;
-  const float* wsc = a.ws + r0 / 128 * a.G;  // 16 * RT divides 128: the rows share their scales
+  constexpr int kTokens = RAW >= 0 ? 1 : NT;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = lane & 15, q = lane >> 4;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 16;
   const int KS = a.waves, last = a.G - 1;
 
-  Batch<RT> b0, b1;
-  auto load = [&](Batch<RT>& b, int i0) {
+  // raw tokens first: everything waits for them, and loads return in order
+  constexpr int kItems = 4;
+  typedef typename Elem<RAW < 0 ? 0 : RAW>::T X;
+  float v[RAW >= 0 ? kItems : 1][8];
+  const int items = a.N * a.G, teams = KS * 4, team = threadIdx.x >> 4;
+  if constexpr (RAW >= 0) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
+    for (int i = 0; i < kItems; ++i) {
+      const int w = std::min(team + i * teams, items - 1), g = w / a.N;
+      if (i * teams < items) load_group<RAW>(static_cast<const X*>(a.x) + (w - g * a.N) * a.ldx, g, a.K, a.vec_x, v[i]);
+    }
+  }
+
+  const uint8_t* wrow = a.w + std::min<int64_t>(r0 + row, a.M - 1) * a.Kp + q * 32;
+  const float* wsc = a.ws + r0 / 128 * a.G;
+  const uint8_t* trow[kTokens];
+  const float* tsc[kTokens];
+  if constexpr (RAW < 0) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int t = std::min(j * 16 + row, a.N - 1);
+      trow[j] = static_cast<const uint8_t*>(a.x) + t * a.Kp + q * 32;
+      tsc[j] = a.xs + t;
+    }
+  }
+  // A group past the last is the last one again, its part multiplied by zero (what is NaN there is NaN anyway).
+  struct Batch {
+    i32x4 lo[B], hi[B], tlo[B][kTokens], thi[B][kTokens];
+    float sw[B], sx[B][kTokens];
+  } b0, b1;
+  auto load = [&](Batch& b, int i0) {
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
       const int64_t g = std::min(i0 + u * KS, last);
+      b.lo[u] = *reinterpret_cast<const i32x4*>(wrow + g * 128);
+      b.hi[u] = *reinterpret_cast<const i32x4*>(wrow + g * 128 + 16);
+      b.sw[u] = wsc[g];
+      if constexpr (RAW < 0) {
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        b.lo[u][i] = *reinterpret_cast<const i32x4*>(wrow[i] + g * 128);
-        b.hi[u][i] = *reinterpret_cast<const i32x4*>(wrow[i] + g * 128 + 16);
+        for (int j = 0; j < NT; ++j) {
+          b.tlo[u][j] = *reinterpret_cast<const i32x4*>(trow[j] + g * 128);
+          b.thi[u][j] = *reinterpret_cast<const i32x4*>(trow[j] + g * 128 + 16);
+          b.sx[u][j] = tsc[j][g * a.N];
+        }
       }
     }
   };
   load(b0, wave);
-  load(b1, wave + kBatch * KS);
+  if (wave + B * KS <= last) load(b1, wave + B * KS);
 
   uint8_t* codes = sh;
   float* scales = reinterpret_cast<float*>(sh + static_cast<size_t>(a.N) * a.Kp);
   if constexpr (RAW >= 0) {
-    typedef typename Elem<RAW < 0 ? 0 : RAW>::T T;
-    const T* x = static_cast<const T*>(a.x);
-    const int64_t ldx = a.ldx;
-    quantize_to_lds<RAW < 0 ? 0 : RAW>([=](int t) { return x + t * ldx; }, a.N, a.K, a.G, a.vec_x, codes, scales,
-                                       KS * 64);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int w = team + i * teams;
+      if (w < items) store_group(v[i], w, w % a.N, codes, scales);
+    }
+    for (int w = team + kItems * teams; w < items; w += teams) {
+      const int g = w / a.N;
+      load_group<RAW>(static_cast<const X*>(a.x) + (w - g * a.N) * a.ldx, g, a.K, a.vec_x, v[0]);
+      store_group(v[0], w, w - g * a.N, codes, scales);
+    }
     __syncthreads();
   }
 
-  f32x4 acc[RT][NT];
+  f32x4 acc[NT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](const Batch& b, int i0) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  auto multiply = [&](const Batch<RT>& b, int i0) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      // a group past the last is the last one again, its part multiplied by zero (what is NaN there is NaN anyway)
-      const int gu = i0 + u * KS, g = std::min(gu, last);
-      const float sw = gu <= last ? wsc[g] : 0.0f;
-      Frag<kExact> A[RT];
-#pragma unroll
-      for (int i = 0; i < RT; ++i) A[i].set(b.lo[u][i], b.hi[u][i]);
+    for (int u = 0; u < B; ++u) {
+      const float sw = i0 + u * KS <= last ? b.sw[u] : 0.0f;
+      Frag<kExact> A;
+      A.set(b.lo[u], b.hi[u]);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const int t = std::min(j * 16 + row, a.N - 1);
-        i32x4 lo, hi;
+        Frag<kExact> T;
         float s;
         if constexpr (RAW >= 0) {
-          const uint8_t* p = codes + (static_cast<size_t>(g) * a.N + t) * 128;
-          lo = *reinterpret_cast<const i32x4*>(p + 16 * ((2 * q) ^ (t & 7)));
-          hi = *reinterpret_cast<const i32x4*>(p + 16 * ((2 * q + 1) ^ (t & 7)));
+          const int g = std::min(i0 + u * KS, last), t = std::min(row, a.N - 1);
+          i32x4 lo, hi;
+          read_codes(codes + (static_cast<size_t>(g) * a.N + t) * 128, t, q, lo, hi);
+          T.set(lo, hi);
           s = scales[g * a.N + t] * sw;
         } else {
-          const uint8_t* p = static_cast<const uint8_t*>(a.x) + t * a.Kp + static_cast<int64_t>(g) * 128 + q * 32;
-          lo = *reinterpret_cast<const i32x4*>(p);
-          hi = *reinterpret_cast<const i32x4*>(p + 16);
-          s = a.xs[static_cast<int64_t>(g) * a.N + t] * sw;
+          T.set(b.tlo[u][j], b.thi[u][j]);
+          s = b.sx[u][j] * sw;
         }
-        Frag<kExact> B;
-        B.set(lo, hi);
+        const f32x4 p = group_sum(A, T);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const f32x4 p = group_sum(A[i], B);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], s, acc[i][j][e]);
-        }
+        for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(p[e], s, acc[j][e]);
       }
     }
   };
-  for (int i0 = wave; i0 <= last; i0 += 2 * kBatch * KS) {
+  for (int i0 = wave; i0 <= last; i0 += 2 * B * KS) {
     multiply(b0, i0);
-    if (i0 + 2 * kBatch * KS <= last) load(b0, i0 + 2 * kBatch * KS);
-    if (i0 + kBatch * KS <= last) multiply(b1, i0 + kBatch * KS);
-    if (i0 + 3 * kBatch * KS <= last) load(b1, i0 + 3 * kBatch * KS);
+    if (i0 + 2 * B * KS <= last) load(b0, i0 + 2 * B * KS);
+    if (i0 + B * KS <= last) multiply(b1, i0 + B * KS);
+    if (i0 + 3 * B * KS <= last) load(b1, i0 + 3 * B * KS);
   }
 
   __syncthreads();
-  f32x4* part = reinterpret_cast<f32x4*>(sh);  // [wave][RT][NT][lane]
+  f32x4* part = reinterpret_cast<f32x4*>(sh);  // [wave][NT][lane]
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) part[((wave * RT + i) * NT + j) * 64 + lane] = acc[i][j];
+  for (int j = 0; j < NT; ++j) part[(wave * NT + j) * 64 + lane] = acc[j];
   __syncthreads();
   typedef typename Elem<OT>::T T;
-  for (int p = wave; p < RT * NT; p += KS) {
-    f32x4 v = part[p * 64 + lane];
-    for (int k = 1; k < KS; ++k) v += part[(k * RT * NT + p) * 64 + lane];
-    const int i = p / NT, t = (p - i * NT) * 16 + row;
-    const int64_t r = r0 + i * 16 + q * 4, left = a.M - r;
+  for (int j = wave; j < NT; j += KS) {
+    f32x4 sum = part[j * 64 + lane];
+    for (int k = 1; k < KS; ++k) sum += part[(k * NT + j) * 64 + lane];
+    const int t = j * 16 + row;
+    const int64_t r = r0 + q * 4, left = a.M - r;
     if (t < a.N && left > 0)
-      store4<OT>(static_cast<T*>(a.y) + static_cast<int64_t>(t) * a.M + r, v, left < 4 ? static_cast<int>(left) : 4, a.vec_y);
+      store4<OT>(static_cast<T*>(a.y) + static_cast<int64_t>(t) * a.M + r, sum, left < 4 ? static_cast<int>(left) : 4, a.vec_y);
   }
 }
 
@@ -271,8 +289,12 @@ __global__ __launch_bounds__(kIdThreads) void k_f8_few_id(FewIdArgs a) {
       __syncthreads();  // the codes of the pass before are read
     }
     const T* x = static_cast<const T*>(a.x);
-    quantize_to_lds<XT>([&](int t) { return x + static_cast<int64_t>(mine[p0 + t] / a.slots) * a.K; }, n, a.K, a.G, a.vec_x,
-                        sh, scales, kIdThreads);
+    for (int w = tid >> 4; w < n * a.G; w += kIdThreads / 16) {
+      const int g = w / n, u = w - g * n;
+      float v[8];
+      load_group<XT>(x + static_cast<int64_t>(mine[p0 + u] / a.slots) * a.K, g, a.K, a.vec_x, v);
+      store_group(v, w, u, sh, scales);
+    }
     __syncthreads();
     const int t = std::min(row, n - 1);
     f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
@@ -283,9 +305,10 @@ __global__ __launch_bounds__(kIdThreads) void k_f8_few_id(FewIdArgs a) {
         const float sw = g0 + u <= last ? wsc[g] : 0.0f;
         const uint8_t* p = sh + (g * n + t) * 128;
         Frag<kExact> A, B;
+        i32x4 tlo, thi;
+        read_codes(p, t, q, tlo, thi);
         A.set(lo[u], hi[u]);
-        B.set(*reinterpret_cast<const i32x4*>(p + 16 * ((2 * q) ^ (t & 7))),
-              *reinterpret_cast<const i32x4*>(p + 16 * ((2 * q + 1) ^ (t & 7))));
+        B.set(tlo, thi);
         const f32x4 v = group_sum(A, B);
         const float s = scales[g * n + t] * sw;
 #pragma unroll
@@ -299,25 +322,28 @@ __global__ __launch_bounds__(kIdThreads) void k_f8_few_id(FewIdArgs a) {
   }
 }
 
-int few_waves(int G) { return std::max(1, std::min(kMaxWaves, (G + 1) / 2)); }
-
-template <int RT, int NT, int RAW, int OT>
-hipError_t few_run(const FewArgs& a, hipStream_t st) {
-  const int64_t blocks = (a.M + 16 * RT - 1) / (16 * RT);
+template <int NT, int RAW, int OT, int B, int W>
+hipError_t few_run(FewArgs a, hipStream_t st) {
+  a.waves = std::min(W, (a.G + 1) / 2);
+  const int64_t blocks = (a.M + 15) / 16;
   const size_t codes = RAW >= 0 ? static_cast<size_t>(a.N) * (a.Kp + a.G * 4) : 0;
-  const size_t lds = std::max(codes, static_cast<size_t>(a.waves) * RT * NT * 1024);
-  k_f8_few<RT, NT, RAW, OT><<<static_cast<unsigned>(blocks), 64 * a.waves, lds, st>>>(a);
+  const size_t lds = std::max(codes, static_cast<size_t>(a.waves) * NT * 1024);
+  k_f8_few<NT, RAW, OT, B, W><<<static_cast<unsigned>(blocks), 64 * a.waves, lds, st>>>(a);
   return hipGetLastError();
 }
 
 template <int RAW, int OT>
 hipError_t few_tokens(const FewArgs& a, hipStream_t st) {
-  if (RAW >= 0 || a.N <= 16) return few_run<1, 1, RAW, OT>(a, st);
-  if constexpr (RAW < 0) {
-    if (a.N <= 32) return few_run<1, 2, RAW, OT>(a, st);
-    return few_run<1, 4, RAW, OT>(a, st);
+  // Batches no longer than two of them need to cover a wave's groups: a load past the last group is a wasted one (20
+  // groups, 4096 rows, one token: 3.6 us with 16 waves and batches of 2, 4.0 with 8 waves, 4.4 and 5.3 with batches of 4
+  // and 6).  Rows of quantized tokens too long for two batches of 16 waves take 8 waves with 10 groups in flight each
+  // (2560 x 9728, 16 tokens: 11.9 us against 12.9).
+  if constexpr (RAW >= 0) {
+    return a.G <= 64 ? few_run<1, RAW, OT, 2, 16>(a, st) : few_run<1, RAW, OT, 3, 16>(a, st);
+  } else {
+    if (a.N > 16) return a.G <= 32 ? few_run<2, RAW, OT, 2, 8>(a, st) : few_run<2, RAW, OT, 3, 8>(a, st);
+    return a.G <= 64 ? few_run<1, RAW, OT, 2, 16>(a, st) : few_run<1, RAW, OT, 5, 8>(a, st);
   }
-  return hipErrorInvalidValue;
 }
 
 template <int RAW>
@@ -340,7 +366,6 @@ FewArgs few_args(const F8Desc& m, int64_t N, void* y, int yt) {
   a.Kp = m.Kp;
   a.N = static_cast<int>(N);
   a.G = static_cast<int>(m.Kp / kF8Block);
-  a.waves = few_waves(a.G);
   a.vec_y = store_vec(y, m.M, yt);
   return a;
 }
@@ -362,7 +387,9 @@ hipError_t few_id_out(const FewIdArgs& a, int yt, dim3 grid, size_t lds, hipStre
 
 }  // namespace
 
-bool f8_few_tokens(const F8Desc&, int64_t N) { return N <= 64; }
+// Above, the tiled kernel reads the tokens once a tile instead of once a workgroup (4096 x 2560: 32 tokens 7.4 us here,
+// 64 tokens 9.9 us here and 9 there; 2560 x 9728 at 64 tokens 26 and 17).
+bool f8_few_tokens(const F8Desc&, int64_t N) { return N <= 32; }
 
 hipError_t launch_f8_few(const F8Desc& m, const uint8_t* xc, const float* xs, int64_t N, void* y, int yt, hipStream_t st) {
   FewArgs a = few_args(m, N, y, yt);
