@@ -31,24 +31,19 @@ def _padded(n):
     return (n + BLOCK - 1) // BLOCK * BLOCK
 
 
-class _Device:
-    """The tensors' device made current for a library call, and its current stream."""
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
-    __slots__ = ("index", "back")
 
-    def __init__(self, device):
-        self.index, self.back = device.index, None
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if now != self.index:
-            torch.cuda.set_device(self.index)
-            self.back = now
-        return torch.cuda.current_stream(self.index).cuda_stream
-
-    def __exit__(self, *_):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _call(device, fn, *args):
+    """fn(*args, the current stream of device), with device (an index) current; raises on an error status."""
+    if _current_device() == device:
+        status = fn(*args, _current_stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _current_stream(device))
+    if status:
+        check(status)
 
 
 def _tensor(t, name, dtypes, dim=None):
@@ -61,19 +56,20 @@ def _tensor(t, name, dtypes, dim=None):
 
 
 def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
 
 
 def _place(device, *named):
-    """Every (tensor, name) is a contiguous tensor on `device` (None: the first one's)."""
+    """Every (tensor, name) is a contiguous tensor on device (an index; None: the first one's)."""
     for t, name in named:
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise ValueError(f"{name} must be a device tensor")
         if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}; expected {device}")
+            device = d
+        elif d != device:
+            raise ValueError(f"{name} is on cuda:{d}; expected cuda:{device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     return device
@@ -84,24 +80,28 @@ def _rows(x, name):
     if not x.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     N, K = x.shape
+    ld, step = x.stride()
     if N == 0 or K == 0:
         return K
-    if K > 1 and x.stride(1) != 1:
+    if K > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
     if N == 1:
         return K
-    if x.stride(0) < K:
+    if ld < K:
         raise ValueError(f"{name} has overlapping rows")
-    return x.stride(0)
+    return ld
 
 
 def _out(out, shape, dtype, device, name="out"):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _tensor(out, name, tuple(_DT))
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[device])
+    _tensor(out, name, _DT)
     _shape(out, name, shape)
     _place(device, (out, name))
     return out
+
+
+_DEVICES = [torch.device("cuda", i) for i in range(64)]
 
 
 def _dtype(t):
@@ -114,7 +114,7 @@ class F8Tokens:
     """Quantized rows: codes [R, padded C] uint8 and scales [padded C / 128, R] fp32.  C, the length of the quantized
     axis, is K for tokens ([N, K]) and the number of tokens for a transposed quantization (`channels` rows)."""
 
-    __slots__ = ("codes", "scales", "rows", "length", "plan")
+    __slots__ = ("codes", "scales", "rows", "length", "plan", "device")
 
     def __init__(self, codes, scales, rows, length, plan=None):
         _tensor(codes, "codes", _CODES, (2,))
@@ -122,8 +122,14 @@ class F8Tokens:
         pitch = codes.shape[1] if plan is not None else _padded(length)
         _shape(codes, "codes", (rows, pitch))
         _shape(scales, "scales", (pitch // BLOCK, rows))
-        _place(None, (codes, "codes"), (scales, "scales"))
+        self.device = _place(None, (codes, "codes"), (scales, "scales"))
         self.codes, self.scales, self.rows, self.length, self.plan = codes, scales, rows, length, plan
+
+    @classmethod
+    def _made(cls, codes, scales, rows, length, device, plan=None):
+        t = object.__new__(cls)
+        t.codes, t.scales, t.rows, t.length, t.plan, t.device = codes, scales, rows, length, plan, device
+        return t
 
     def values(self):
         """The values the codes stand for, [R, C] fp32 (in torch: for inspection, not a product path)."""
@@ -137,7 +143,7 @@ def _empty_tokens(rows, pitch, device):
 
 
 def _quantize(x, along_k, along_n):
-    _tensor(x, "x", tuple(_DT), (2, 3))
+    _tensor(x, "x", _DT, (2, 3))
     if x.dim() == 3:
         if not x.is_contiguous():
             raise ValueError("x of three dimensions must be contiguous")
@@ -146,12 +152,17 @@ def _quantize(x, along_k, along_n):
     if K == 0:
         raise ValueError("x has no columns")
     ld = _rows(x, "x")
-    r = _empty_tokens(N, _padded(K), x.device) if along_k else (None, None)
-    c = _empty_tokens(K, _padded(N), x.device) if along_n else (None, None)
-    p = [t.data_ptr() if t is not None else None for t in (*r, *c)]
-    with _Device(x.device) as stream:
-        check(lib.qmm_f8_quantize(x.data_ptr(), _DT[x.dtype], ld, N, K, *p, stream))
-    return (F8Tokens(*r, N, K) if along_k else None), (F8Tokens(*c, K, N) if along_n else None)
+    device, d = x.device, x.get_device()
+    r = c = (None, None)
+    rp = cp = (None, None)
+    if along_k:
+        r = _empty_tokens(N, _padded(K), device)
+        rp = r[0].data_ptr(), r[1].data_ptr()
+    if along_n:
+        c = _empty_tokens(K, _padded(N), device)
+        cp = c[0].data_ptr(), c[1].data_ptr()
+    _call(d, lib.qmm_f8_quantize, x.data_ptr(), _DT[x.dtype], ld, N, K, *rp, *cp)
+    return (F8Tokens._made(*r, N, K, d) if along_k else None), (F8Tokens._made(*c, K, N, d) if along_n else None)
 
 
 def f8_quantize(x: torch.Tensor) -> F8Tokens:
@@ -170,19 +181,19 @@ def f8_quantize_t(x: torch.Tensor, plan=None) -> F8Tokens:
     rows are the plan's pairs, expert by expert: x [N, K] (shared by a token's slots) or [N, S, K] / [N * S, K]."""
     if plan is None:
         return _quantize(x, False, True)[1]
-    _tensor(x, "x", tuple(_DT), (2, 3))
+    _tensor(x, "x", _DT, (2, 3))
     per_slot = plan.per_slot_rows(x, "x")
     x2 = x.reshape(-1, x.shape[-1]) if x.dim() == 3 else x
     K = x2.shape[1]
     if K == 0:
         raise ValueError("x has no columns")
     ld = _rows(x2, "x")
-    _place(x.device, (plan.data, "plan"))
+    d = x.get_device()
+    _place(d, (plan.data, "plan"))
     codes, scales = _empty_tokens(K, lib.qmm_f8_routed_tokens(plan.N * plan.S, plan.n_experts), x.device)
-    with _Device(x.device) as stream:
-        check(lib.qmm_f8_quantize_routed(x2.data_ptr(), _DT[x.dtype], ld, plan.N, plan.S, per_slot, K, plan.n_experts,
-                                         plan.data.data_ptr(), codes.data_ptr(), scales.data_ptr(), stream))
-    return F8Tokens(codes, scales, K, plan.N * plan.S, plan)
+    _call(d, lib.qmm_f8_quantize_routed, x2.data_ptr(), _DT[x.dtype], ld, plan.N, plan.S, per_slot, K, plan.n_experts,
+          plan.data.data_ptr(), codes.data_ptr(), scales.data_ptr())
+    return F8Tokens._made(codes, scales, K, plan.N * plan.S, d, plan)
 
 
 def f8_wgrad(g: F8Tokens, x: F8Tokens, plan=None, out: torch.Tensor = None, dtype=torch.float32) -> torch.Tensor:
@@ -191,18 +202,18 @@ def f8_wgrad(g: F8Tokens, x: F8Tokens, plan=None, out: torch.Tensor = None, dtyp
         raise ValueError(f"g has {g.length} tokens, x has {x.length}")
     if g.plan is not plan or x.plan is not plan:
         raise ValueError("g and x must be quantized with the plan of this call (none without one)")
-    M, K = g.rows, x.rows
-    device = _place(None, (g.codes, "g"), (x.codes, "x"))
+    M, K, device = g.rows, x.rows, g.device
+    if x.device != device:
+        raise ValueError(f"x is on cuda:{x.device}, g on cuda:{device}")
     shape = (M, K) if plan is None else (plan.n_experts, M, K)
     dw = _out(out, shape, _dtype(dtype), device)
     ptrs = g.codes.data_ptr(), g.scales.data_ptr(), x.codes.data_ptr(), x.scales.data_ptr()
-    with _Device(device) as stream:
-        if plan is None:
-            check(lib.qmm_f8_wgrad(*ptrs, g.length, M, K, dw.data_ptr(), _DT[dw.dtype], stream))
-        else:
-            _place(device, (plan.data, "plan"))
-            check(lib.qmm_f8_wgrad_id(*ptrs, plan.N, plan.S, M, K, plan.n_experts, plan.data.data_ptr(), dw.data_ptr(),
-                                      _DT[dw.dtype], stream))
+    if plan is None:
+        _call(device, lib.qmm_f8_wgrad, *ptrs, g.length, M, K, dw.data_ptr(), _DT[dw.dtype])
+    else:
+        _place(device, (plan.data, "plan"))
+        _call(device, lib.qmm_f8_wgrad_id, *ptrs, plan.N, plan.S, M, K, plan.n_experts, plan.data.data_ptr(), dw.data_ptr(),
+              _DT[dw.dtype])
     return dw
 
 
@@ -229,22 +240,24 @@ class F8Matrix:
         _shape(scales, "scales", ((E,) if scales.dim() == 3 or E > 1 else ()) + (R, G))
         device = _place(None, (codes, "codes"), (scales, "scales"))
         self.M, self.K, self.n_experts, self.codes, self.scales, self.device = M, K, E, codes, scales, device
+        self._need = {}  # workspace bytes of the calls seen
         h = ctypes.c_void_p()
-        with _Device(device):
+        with torch.cuda.device(device):
             check(lib.qmm_f8_create(ctypes.byref(h), codes.data_ptr(), scales.data_ptr(), E, M, K))
         self._h = h
 
     @classmethod
     def _empty(cls, E, M, K, device, stacked):
         lead = (E,) if stacked else ()
-        codes = torch.empty(lead + (M, _padded(K)), dtype=torch.uint8, device=device)
-        scales = torch.empty(lead + (_padded(M) // BLOCK, _padded(K) // BLOCK), dtype=torch.float32, device=device)
+        on = _DEVICES[device]
+        codes = torch.empty(lead + (M, _padded(K)), dtype=torch.uint8, device=on)
+        scales = torch.empty(lead + (_padded(M) // BLOCK, _padded(K) // BLOCK), dtype=torch.float32, device=on)
         return cls(codes, scales, M, K, E)
 
     @classmethod
     def quantize(cls, w: torch.Tensor) -> "F8Matrix":
         """w [M, K] or [E, M, K] (fp32, fp16 or bf16, contiguous)."""
-        _tensor(w, "w", tuple(_DT), (2, 3))
+        _tensor(w, "w", _DT, (2, 3))
         device = _place(None, (w, "w"))
         if w.numel() == 0:
             raise ValueError("w is empty")
@@ -273,16 +286,15 @@ class F8Matrix:
 
     def update(self, w: torch.Tensor, transposed: "F8Matrix" = None) -> None:
         """Quantize new weights into this matrix' buffers (and their transpose into `transposed`'s, from the same pass)."""
-        _tensor(w, "w", tuple(_DT), (2, 3))
+        _tensor(w, "w", _DT, (2, 3))
         _shape(w, "w", ((self.n_experts,) if w.dim() == 3 or self.n_experts > 1 else ()) + (self.M, self.K))
         _place(self.device, (w, "w"))
         t = (None, None)
         if transposed is not None:
             self._check_transpose(transposed)
             t = transposed.codes.data_ptr(), transposed.scales.data_ptr()
-        with _Device(self.device) as stream:
-            check(lib.qmm_f8_quantize_weight(w.data_ptr(), _DT[w.dtype], self.n_experts, self.M, self.K,
-                                             self.codes.data_ptr(), self.scales.data_ptr(), *t, stream))
+        _call(self.device, lib.qmm_f8_quantize_weight, w.data_ptr(), _DT[w.dtype], self.n_experts, self.M, self.K,
+              self.codes.data_ptr(), self.scales.data_ptr(), *t)
 
     def _check_transpose(self, m):
         if not isinstance(m, F8Matrix) or (m.M, m.K, m.n_experts) != (self.K, self.M, self.n_experts):
@@ -296,59 +308,57 @@ class F8Matrix:
         if out is None:
             out = F8Matrix._empty(self.n_experts, self.K, self.M, self.device, self.codes.dim() == 3)
         self._check_transpose(out)
-        with _Device(self.device) as stream:
-            check(lib.qmm_f8_transpose(self._h, out.codes.data_ptr(), out.scales.data_ptr(), stream))
+        _call(self.device, lib.qmm_f8_transpose, self._h, out.codes.data_ptr(), out.scales.data_ptr())
         return out
 
     def dequantize(self, expert: int = 0, dtype=torch.float32) -> torch.Tensor:
-        out = torch.empty((self.M, self.K), dtype=_dtype(dtype), device=self.device)
-        with _Device(self.device) as stream:
-            check(lib.qmm_f8_dequantize(self._h, int(expert), out.data_ptr(), _DT[dtype], stream))
+        out = _out(None, (self.M, self.K), _dtype(dtype), self.device)
+        _call(self.device, lib.qmm_f8_dequantize, self._h, int(expert), out.data_ptr(), _DT[dtype])
         return out
 
     def linear(self, x: torch.Tensor, out_dtype=None, out: torch.Tensor = None) -> torch.Tensor:
         """x [N, K] (rows may be strided) -> y [N, M] of x's type (or out_dtype): quantization and product."""
         self._dense("linear")
-        _tensor(x, "x", tuple(_DT), (2,))
-        N = x.shape[0]
-        if x.shape[1] != self.K:
-            raise ValueError(f"x has K={x.shape[1]}, matrix has K={self.K}")
-        if x.device != self.device:
-            raise ValueError(f"x is on {x.device}; the matrix is on {self.device}")
+        _tensor(x, "x", _DT, (2,))
+        N, K = x.shape
+        if K != self.K:
+            raise ValueError(f"x has K={K}, matrix has K={self.K}")
         ld = _rows(x, "x")
-        y = _out(out, (N, self.M), _dtype(out_dtype or x.dtype), self.device)
-        nb = lib.qmm_f8_linear_workspace_bytes(self._h, N)
-        ws = torch.empty(nb, dtype=torch.uint8, device=self.device) if nb else None
-        with _Device(self.device) as stream:
-            check(lib.qmm_f8_linear(self._h, x.data_ptr(), _DT[x.dtype], ld, N, y.data_ptr(), _DT[y.dtype],
-                                    ws.data_ptr() if nb else None, nb, stream))
+        d = self.device
+        if x.get_device() != d:
+            raise ValueError(f"x is on {x.device}; the matrix is on cuda:{d}")
+        y = _out(out, (N, self.M), _dtype(out_dtype or x.dtype), d)
+        nb = self._need.get(N)
+        if nb is None:
+            nb = self._need[N] = lib.qmm_f8_linear_workspace_bytes(self._h, N)
+        ws = torch.empty(nb, dtype=torch.uint8, device=x.device) if nb else None
+        _call(d, lib.qmm_f8_linear, self._h, x.data_ptr(), _DT[x.dtype], ld, N, y.data_ptr(), _DT[y.dtype],
+              ws.data_ptr() if nb else None, nb)
         return y
 
-    def _tokens(self, t, rows):
+    def _tokens(self, t):
         if not isinstance(t, F8Tokens) or t.plan is not None:
             raise ValueError("tokens must come from f8_quantize")
         if t.length != self.K:
             raise ValueError(f"tokens have K={t.length}, matrix has K={self.K}")
-        if rows is not None and t.rows != rows:
-            raise ValueError(f"{t.rows} rows of tokens; expected {rows}")
-        _place(self.device, (t.codes, "tokens"))
+        if t.device != self.device:
+            raise ValueError(f"tokens are on cuda:{t.device}; the matrix is on cuda:{self.device}")
 
     def gemm(self, tokens: F8Tokens, out_dtype=torch.float32, out: torch.Tensor = None) -> torch.Tensor:
         """Quantized tokens [N, K] -> y [N, M]."""
         self._dense("gemm")
-        self._tokens(tokens, None)
+        self._tokens(tokens)
         N = tokens.rows
         y = _out(out, (N, self.M), _dtype(out_dtype), self.device)
         nb = lib.qmm_f8_gemm_workspace_bytes(self._h, N)
-        ws = torch.empty(nb, dtype=torch.uint8, device=self.device) if nb else None
-        with _Device(self.device) as stream:
-            check(lib.qmm_f8_gemm(self._h, tokens.codes.data_ptr(), tokens.scales.data_ptr(), N, y.data_ptr(),
-                                  _DT[y.dtype], ws.data_ptr() if nb else None, nb, stream))
+        ws = _out(None, (nb // 4 + 1,), torch.float32, self.device) if nb else None
+        _call(self.device, lib.qmm_f8_gemm, self._h, tokens.codes.data_ptr(), tokens.scales.data_ptr(), N, y.data_ptr(),
+              _DT[y.dtype], ws.data_ptr() if nb else None, nb)
         return y
 
     def linear_id(self, x: torch.Tensor, ids: torch.Tensor, out_dtype=None, out: torch.Tensor = None) -> torch.Tensor:
         """ids [N, S] int32 (-1: an empty slot); x [N, S, K] (one row per slot) or [N, K], contiguous -> y [N, S, M]."""
-        _tensor(x, "x", tuple(_DT), (2, 3))
+        _tensor(x, "x", _DT, (2, 3))
         _tensor(ids, "ids", (torch.int32,), (2,))
         N, S = ids.shape
         if S < 1:
@@ -357,11 +367,12 @@ class F8Matrix:
         _shape(x, "x", (N, S, self.K) if per_slot else (N, self.K))
         _place(self.device, (x, "x"), (ids, "ids"))
         y = _out(out, (N, S, self.M), _dtype(out_dtype or x.dtype), self.device)
-        nb = lib.qmm_f8_linear_id_workspace_bytes(self._h, N, S, per_slot)
-        ws = torch.empty(nb, dtype=torch.uint8, device=self.device) if nb else None
-        with _Device(self.device) as stream:
-            check(lib.qmm_f8_linear_id(self._h, x.data_ptr(), _DT[x.dtype], N, S, per_slot, ids.data_ptr(), y.data_ptr(),
-                                       _DT[y.dtype], ws.data_ptr() if nb else None, nb, stream))
+        nb = self._need.get((N, S, per_slot))
+        if nb is None:
+            nb = self._need[N, S, per_slot] = lib.qmm_f8_linear_id_workspace_bytes(self._h, N, S, per_slot)
+        ws = torch.empty(nb, dtype=torch.uint8, device=x.device) if nb else None
+        _call(self.device, lib.qmm_f8_linear_id, self._h, x.data_ptr(), _DT[x.dtype], N, S, per_slot, ids.data_ptr(),
+              y.data_ptr(), _DT[y.dtype], ws.data_ptr() if nb else None, nb)
         return y
 
     def gemm_id(self, tokens: F8Tokens, plan, out_dtype=torch.float32, out: torch.Tensor = None) -> torch.Tensor:
@@ -369,10 +380,9 @@ class F8Matrix:
         if plan.n_experts != self.n_experts:
             raise ValueError(f"the plan has {plan.n_experts} experts, the matrix {self.n_experts}")
         per_slot = plan.per_slot(tokens.rows, "tokens")
-        self._tokens(tokens, None)
+        self._tokens(tokens)
         _place(self.device, (plan.data, "plan"))
         y = _out(out, (plan.N, plan.S, self.M), _dtype(out_dtype), self.device)
-        with _Device(self.device) as stream:
-            check(lib.qmm_f8_gemm_id(self._h, tokens.codes.data_ptr(), tokens.scales.data_ptr(), plan.N, plan.S, per_slot,
-                                     plan.data.data_ptr(), y.data_ptr(), _DT[y.dtype], stream))
+        _call(self.device, lib.qmm_f8_gemm_id, self._h, tokens.codes.data_ptr(), tokens.scales.data_ptr(), plan.N, plan.S,
+              per_slot, plan.data.data_ptr(), y.data_ptr(), _DT[y.dtype])
         return y

@@ -17,8 +17,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from ._lib import check, lib
-from .f8 import _DT, _Device, _out, _place, _shape, _tensor
+from ._lib import lib
+from .f8 import _DT, _call, _out, _place, _shape, _tensor
 
 
 class Routing(NamedTuple):
@@ -69,14 +69,13 @@ def route_plan(ids: torch.Tensor, n_experts: int) -> RoutePlan:
         raise ValueError("ids needs a slot and the plan an expert")
     device = _place(None, (ids, "ids"))
     nb = lib.qmm_route_plan_bytes(N * S, E)
-    data = torch.empty(max(nb, 16) // 4, dtype=torch.int32, device=device)
-    with _Device(device) as stream:
-        check(lib.qmm_route_plan(ids.data_ptr(), N, S, E, data.data_ptr(), nb, stream))
+    data = torch.empty(max(nb, 16) // 4, dtype=torch.int32, device=ids.device)
+    _call(device, lib.qmm_route_plan, ids.data_ptr(), N, S, E, data.data_ptr(), nb)
     return RoutePlan(data, N, S, E)
 
 
 def _logits(logits, valid):
-    _tensor(logits, "logits", tuple(_DT), (2,))
+    _tensor(logits, "logits", _DT, (2,))
     device = _place(None, (logits, "logits"))
     if valid is not None:
         _tensor(valid, "valid", (torch.uint8, torch.bool), (1,))
@@ -94,18 +93,18 @@ def route(logits: torch.Tensor, S: int, normalise: bool = True, coef: float = 0.
     S = int(S)
     if not 1 <= S <= min(E, 64):
         raise ValueError(f"S={S} outside [1, {min(E, 64)}]")
-    ids = torch.empty((N, S), dtype=torch.int32, device=device)
-    weights = torch.empty((N, S), dtype=torch.float32, device=device)
-    counts = torch.empty(E + 1, dtype=torch.int32, device=device)
+    on = logits.device
+    ids = torch.empty((N, S), dtype=torch.int32, device=on)
+    weights = torch.empty((N, S), dtype=torch.float32, device=on)
+    counts = torch.empty(E + 1, dtype=torch.int32, device=on)
     nb = lib.qmm_route_workspace_bytes(N, E)
     # sums over the rows, the loss and the workspace in one allocation
     pad = (E + 1 + 3) // 4 * 4
-    buf = torch.empty(pad + nb // 4, dtype=torch.float32, device=device)
-    psum, loss = buf[:E], buf[E]
-    with _Device(device) as stream:
-        check(lib.qmm_route(logits.data_ptr(), _DT[logits.dtype], N, E, S, valid.data_ptr() if valid is not None else None,
-                            int(bool(normalise)), float(coef), ids.data_ptr(), weights.data_ptr(), counts.data_ptr(),
-                            psum.data_ptr(), loss.data_ptr(), buf.data_ptr() + 4 * pad, nb, stream))
+    buf = torch.empty(pad + nb // 4, dtype=torch.float32, device=on)
+    psum, loss, at = buf[:E], buf[E], buf.data_ptr()
+    _call(device, lib.qmm_route, logits.data_ptr(), _DT[logits.dtype], N, E, S,
+          valid.data_ptr() if valid is not None else None, int(bool(normalise)), coef, ids.data_ptr(), weights.data_ptr(),
+          counts.data_ptr(), at, at + 4 * E, at + 4 * pad, nb)
     return Routing(ids, weights, counts, psum, loss, bool(normalise), float(coef), valid)
 
 
@@ -116,9 +115,8 @@ def balance_loss(counts: torch.Tensor, psum: torch.Tensor, S: int, coef: float) 
     E = psum.shape[0]
     _shape(counts, "counts", (E + 1,))
     device = _place(None, (counts, "counts"), (psum, "psum"))
-    loss = torch.empty((), dtype=torch.float32, device=device)
-    with _Device(device) as stream:
-        check(lib.qmm_balance_loss(counts.data_ptr(), psum.data_ptr(), E, int(S), float(coef), loss.data_ptr(), stream))
+    loss = torch.empty((), dtype=torch.float32, device=counts.device)
+    _call(device, lib.qmm_balance_loss, counts.data_ptr(), psum.data_ptr(), E, int(S), float(coef), loss.data_ptr())
     return loss
 
 
@@ -143,17 +141,15 @@ def route_backward(logits: torch.Tensor, routing: Routing, dweights: Optional[to
         _place(device, (dloss, "dloss"))
     valid = routing.valid
     dlogits = torch.empty_like(logits)
-    with _Device(device) as stream:
-        check(lib.qmm_route_backward(logits.data_ptr(), _DT[logits.dtype], N, E, S,
-                                     valid.data_ptr() if valid is not None else None, int(routing.normalise), routing.coef,
-                                     routing.ids.data_ptr(), dweights.data_ptr() if dweights is not None else None,
-                                     routing.counts.data_ptr(), dloss.data_ptr() if dloss is not None else None,
-                                     dlogits.data_ptr(), stream))
+    _call(device, lib.qmm_route_backward, logits.data_ptr(), _DT[logits.dtype], N, E, S,
+          valid.data_ptr() if valid is not None else None, int(routing.normalise), routing.coef, routing.ids.data_ptr(),
+          dweights.data_ptr() if dweights is not None else None, routing.counts.data_ptr(),
+          dloss.data_ptr() if dloss is not None else None, dlogits.data_ptr())
     return dlogits
 
 
 def _slots(y, weights):
-    _tensor(y, "y", tuple(_DT), (3,))
+    _tensor(y, "y", _DT, (3,))
     device = _place(None, (y, "y"))
     N, S, M = y.shape
     if S < 1 or M < 1:
@@ -172,9 +168,8 @@ def route_combine(y: torch.Tensor, weights: Optional[torch.Tensor] = None, out: 
     o = _out(out, (N, M), y.dtype, device)
     if o.dtype != y.dtype:
         raise ValueError("out must have y's dtype")
-    with _Device(device) as stream:
-        check(lib.qmm_route_combine(y.data_ptr(), _DT[y.dtype], weights.data_ptr() if weights is not None else None,
-                                    _DT[weights.dtype] if weights is not None else 0, N, S, M, o.data_ptr(), stream))
+    _call(device, lib.qmm_route_combine, y.data_ptr(), _DT[y.dtype], weights.data_ptr() if weights is not None else None,
+          _DT[weights.dtype] if weights is not None else 0, N, S, M, o.data_ptr())
     return o
 
 
@@ -187,7 +182,6 @@ def route_combine_backward(y: torch.Tensor, weights: torch.Tensor, dout: torch.T
     _shape(dout, "dout", (N, M))
     _place(device, (dout, "dout"))
     dy, dw = torch.empty_like(y), torch.empty_like(weights)
-    with _Device(device) as stream:
-        check(lib.qmm_route_combine_backward(y.data_ptr(), _DT[y.dtype], weights.data_ptr(), _DT[weights.dtype], N, S, M,
-                                             dout.data_ptr(), dy.data_ptr(), dw.data_ptr(), stream))
+    _call(device, lib.qmm_route_combine_backward, y.data_ptr(), _DT[y.dtype], weights.data_ptr(), _DT[weights.dtype], N, S, M,
+          dout.data_ptr(), dy.data_ptr(), dw.data_ptr())
     return dy, dw
