@@ -183,6 +183,24 @@ __device__ __forceinline__ float f8_quotient(float x, float s, float rs) {
   return __uint_as_float((odd & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u));  // the correction loses a -0
 }
 
+// Eight quotients at once.  x * rs is within 2 steps of fp32 of x / s; its e4m3 rounding can only differ from the
+// quotient's next to the middle of two codes, which for a normal code (|q| >= 2^-6) has the low 20 bits 0x80000.  Only a
+// wave that holds a value within 4 steps of that, or a smaller one, takes the exact form: 5 operations a value, not 12.
+__device__ __forceinline__ void f8_quotients(const float* x, float s, float rs, float* q) {
+  bool near = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    q[i] = x[i] * rs;
+    const uint32_t b = __float_as_uint(q[i]);
+    near |= ((b + (4 - 0x80000)) & 0xFFFFFu) <= 8u;
+    near |= fabsf(q[i]) < 0x1p-6f;
+  }
+  if (near) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = f8_quotient(x[i], s, rs);
+  }
+}
+
 // four codes in one word, lowest byte first
 __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d) {
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);

@@ -45,8 +45,7 @@ __device__ __forceinline__ void store_group(const float* v, int w, int t, uint8_
   for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
   const float s = f8_scale(max16(m)), rs = 1.0f / s;
   float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = f8_quotient(v[i], s, rs);
+  f8_quotients(v, s, rs, q);
   *reinterpret_cast<uint2*>(codes + static_cast<size_t>(w) * 128 + (((lane >> 1) ^ (t >> 1 & 7)) * 16) + (lane & 1) * 8) =
       make_uint2(f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7]));
   if (lane == 0) scales[w] = s;

@@ -34,8 +34,7 @@ __device__ __forceinline__ void load_row8(const typename Elem<DT>::T* row, int64
 
 __device__ __forceinline__ uint2 codes8(const float* v, float s, float rs) {
   float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = f8_quotient(v[i], s, rs);
+  f8_quotients(v, s, rs, q);
   return make_uint2(f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7]));
 }
 

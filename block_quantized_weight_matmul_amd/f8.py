@@ -114,7 +114,7 @@ class F8Tokens:
     """Quantized rows: codes [R, padded C] uint8 and scales [padded C / 128, R] fp32.  C, the length of the quantized
     axis, is K for tokens ([N, K]) and the number of tokens for a transposed quantization (`channels` rows)."""
 
-    __slots__ = ("codes", "scales", "rows", "length", "plan", "device")
+    __slots__ = ("_codes", "_scales", "_buffer", "ptrs", "pitch", "rows", "length", "plan", "device")
 
     def __init__(self, codes, scales, rows, length, plan=None):
         _tensor(codes, "codes", _CODES, (2,))
@@ -123,23 +123,37 @@ class F8Tokens:
         _shape(codes, "codes", (rows, pitch))
         _shape(scales, "scales", (pitch // BLOCK, rows))
         self.device = _place(None, (codes, "codes"), (scales, "scales"))
-        self.codes, self.scales, self.rows, self.length, self.plan = codes, scales, rows, length, plan
+        self._codes, self._scales, self._buffer = codes, scales, None
+        self.ptrs = codes.data_ptr(), scales.data_ptr()
+        self.pitch, self.rows, self.length, self.plan = pitch, rows, length, plan
 
     @classmethod
-    def _made(cls, codes, scales, rows, length, device, plan=None):
+    def _empty(cls, rows, pitch, length, on, device, plan=None):
+        """Room for codes and scales in one buffer; the tensors are made when asked for."""
         t = object.__new__(cls)
-        t.codes, t.scales, t.rows, t.length, t.plan, t.device = codes, scales, rows, length, plan, device
+        t._buffer = torch.empty(rows * pitch + rows * (pitch // BLOCK) * 4, dtype=torch.uint8, device=on)
+        t._codes = t._scales = None
+        at = t._buffer.data_ptr()
+        t.ptrs = at, at + rows * pitch
+        t.pitch, t.rows, t.length, t.plan, t.device = pitch, rows, length, plan, device
         return t
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._buffer[:self.rows * self.pitch].view(self.rows, self.pitch)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._buffer[self.rows * self.pitch:].view(torch.float32).view(self.pitch // BLOCK, self.rows)
+        return self._scales
 
     def values(self):
         """The values the codes stand for, [R, C] fp32 (in torch: for inspection, not a product path)."""
         v = self.codes.view(torch.float8_e4m3fn).float().unflatten(1, (-1, BLOCK)) * self.scales.t().unsqueeze(2)
         return v.flatten(1)[:, :self.length]
-
-
-def _empty_tokens(rows, pitch, device):
-    return (torch.empty((rows, pitch), dtype=torch.uint8, device=device),
-            torch.empty((pitch // BLOCK, rows), dtype=torch.float32, device=device))
 
 
 def _quantize(x, along_k, along_n):
@@ -153,16 +167,11 @@ def _quantize(x, along_k, along_n):
         raise ValueError("x has no columns")
     ld = _rows(x, "x")
     device, d = x.device, x.get_device()
-    r = c = (None, None)
-    rp = cp = (None, None)
-    if along_k:
-        r = _empty_tokens(N, _padded(K), device)
-        rp = r[0].data_ptr(), r[1].data_ptr()
-    if along_n:
-        c = _empty_tokens(K, _padded(N), device)
-        cp = c[0].data_ptr(), c[1].data_ptr()
-    _call(d, lib.qmm_f8_quantize, x.data_ptr(), _DT[x.dtype], ld, N, K, *rp, *cp)
-    return (F8Tokens._made(*r, N, K, d) if along_k else None), (F8Tokens._made(*c, K, N, d) if along_n else None)
+    r = F8Tokens._empty(N, _padded(K), K, device, d) if along_k else None
+    c = F8Tokens._empty(K, _padded(N), N, device, d) if along_n else None
+    _call(d, lib.qmm_f8_quantize, x.data_ptr(), _DT[x.dtype], ld, N, K, *(r.ptrs if along_k else (None, None)),
+          *(c.ptrs if along_n else (None, None)))
+    return r, c
 
 
 def f8_quantize(x: torch.Tensor) -> F8Tokens:
@@ -190,15 +199,15 @@ def f8_quantize_t(x: torch.Tensor, plan=None) -> F8Tokens:
     ld = _rows(x2, "x")
     d = x.get_device()
     _place(d, (plan.data, "plan"))
-    codes, scales = _empty_tokens(K, lib.qmm_f8_routed_tokens(plan.N * plan.S, plan.n_experts), x.device)
+    t = F8Tokens._empty(K, lib.qmm_f8_routed_tokens(plan.N * plan.S, plan.n_experts), plan.N * plan.S, x.device, d, plan)
     _call(d, lib.qmm_f8_quantize_routed, x2.data_ptr(), _DT[x.dtype], ld, plan.N, plan.S, per_slot, K, plan.n_experts,
-          plan.data.data_ptr(), codes.data_ptr(), scales.data_ptr())
-    return F8Tokens._made(codes, scales, K, plan.N * plan.S, d, plan)
+          plan.data.data_ptr(), *t.ptrs)
+    return t
 
 
 def f8_wgrad(g: F8Tokens, x: F8Tokens, plan=None, out: torch.Tensor = None, dtype=torch.float32) -> torch.Tensor:
     """dw [M, K] = g^T x (dw [E, M, K] with a plan), g and x quantized along the same tokens by f8_quantize_t."""
-    if g.length != x.length or g.codes.shape[1] != x.codes.shape[1]:
+    if g.length != x.length or g.pitch != x.pitch:
         raise ValueError(f"g has {g.length} tokens, x has {x.length}")
     if g.plan is not plan or x.plan is not plan:
         raise ValueError("g and x must be quantized with the plan of this call (none without one)")
@@ -207,7 +216,7 @@ def f8_wgrad(g: F8Tokens, x: F8Tokens, plan=None, out: torch.Tensor = None, dtyp
         raise ValueError(f"x is on cuda:{x.device}, g on cuda:{device}")
     shape = (M, K) if plan is None else (plan.n_experts, M, K)
     dw = _out(out, shape, _dtype(dtype), device)
-    ptrs = g.codes.data_ptr(), g.scales.data_ptr(), x.codes.data_ptr(), x.scales.data_ptr()
+    ptrs = g.ptrs + x.ptrs
     if plan is None:
         _call(device, lib.qmm_f8_wgrad, *ptrs, g.length, M, K, dw.data_ptr(), _DT[dw.dtype])
     else:
@@ -352,7 +361,7 @@ class F8Matrix:
         y = _out(out, (N, self.M), _dtype(out_dtype), self.device)
         nb = lib.qmm_f8_gemm_workspace_bytes(self._h, N)
         ws = _out(None, (nb // 4 + 1,), torch.float32, self.device) if nb else None
-        _call(self.device, lib.qmm_f8_gemm, self._h, tokens.codes.data_ptr(), tokens.scales.data_ptr(), N, y.data_ptr(),
+        _call(self.device, lib.qmm_f8_gemm, self._h, *tokens.ptrs, N, y.data_ptr(),
               _DT[y.dtype], ws.data_ptr() if nb else None, nb)
         return y
 
@@ -383,6 +392,6 @@ class F8Matrix:
         self._tokens(tokens)
         _place(self.device, (plan.data, "plan"))
         y = _out(out, (plan.N, plan.S, self.M), _dtype(out_dtype), self.device)
-        _call(self.device, lib.qmm_f8_gemm_id, self._h, tokens.codes.data_ptr(), tokens.scales.data_ptr(), plan.N, plan.S,
+        _call(self.device, lib.qmm_f8_gemm_id, self._h, *tokens.ptrs, plan.N, plan.S,
               per_slot, plan.data.data_ptr(), y.data_ptr(), _DT[y.dtype])
         return y

@@ -73,7 +73,7 @@ def test_product_refusals():
     expect(lambda: st.linear_id(f32(3, 200), i32(3, 0)), "no slots")
     expect(lambda: st.linear_id(f32(3, 200), i32(3, 2)), "device tensor")
     t = object.__new__(q.F8Tokens)
-    t.codes, t.scales, t.rows, t.length, t.plan, t.device = torch.zeros((3, 256), dtype=torch.uint8), f32(2, 3), 3, 200, None, 0
+    t.ptrs, t.pitch, t.rows, t.length, t.plan, t.device = (0, 0), 256, 3, 200, None, 0
     expect(lambda: st.gemm_id(t, plan(3, 2, 5)), "plan has 5 experts")
     expect(lambda: st.gemm_id(t, plan(4, 2, 4)), "3 rows")
     expect(lambda: matrix(48, 199).gemm(t), "tokens have K=200")
