@@ -146,18 +146,25 @@ template <> struct Elem<DT_F32> { typedef float T; };
 template <> struct Elem<DT_F16> { typedef _Float16 T; };
 template <> struct Elem<DT_BF16> { typedef __bf16 T; };
 
-// 8 consecutive elements as fp32; p is 16-byte aligned
+// 8 consecutive elements as fp32.  p is aligned to its elements only: vector loads of this GPU take any address, and a
+// 16-byte aligned one costs the same through either form.
 template <int DT>
 __device__ __forceinline__ void load8(const typename Elem<DT>::T* p, float* v) {
-  if constexpr (DT == DT_F32) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    typedef typename Elem<DT>::T T8 __attribute__((ext_vector_type(8)));
-    const T8 a = *reinterpret_cast<const T8*>(p);
+  typedef typename Elem<DT>::T T;
+  typedef T T8 __attribute__((ext_vector_type(8)));
+  typedef T8 T8u __attribute__((aligned(sizeof(T))));
+  const T8 a = *reinterpret_cast<const T8u*>(p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(a[i]);
+  for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(a[i]);
+}
+// the same of columns c .. c + 7 of a row of K: zeros from K on
+template <int DT>
+__device__ __forceinline__ void load_row8(const typename Elem<DT>::T* row, int64_t c, int64_t K, float* v) {
+  if (c + 8 <= K) {
+    load8<DT>(row + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < K ? static_cast<float>(row[c + i]) : 0.0f;
   }
 }
 
@@ -166,11 +173,15 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // Scale of a block whose largest |x| has these bits: max(a / 448, 2^-80), NaN if the block holds an Inf or a NaN.
 __device__ __forceinline__ float f8_scale(uint32_t amax_bits) {
   if (amax_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-  return fmaxf(__uint_as_float(amax_bits) / kF8Max, kF8MinScale);
+  // a / 448 correctly rounded: the product with the rounded inverse, corrected once by the exact remainder
+  const float a = __uint_as_float(amax_bits), c = 1.0f / kF8Max, r = a * c;
+  return fmaxf(fmaf(fmaf(-kF8Max, r, a), c, r), kF8MinScale);
 }
+// 1 / s to one step of fp32 (s is normal, and so is its inverse)
+__device__ __forceinline__ float f8_inverse(float s) { return __builtin_amdgcn_rcpf(s); }
 
-// x / s ready for the hardware's one rounding to e4m3.  q is x / s to within half a step of fp32 (one correction of
-// x * (1 / s) by the exact remainder); an inexact q takes the odd one of the two fp32 neighbours of the quotient,
+// x / s ready for the hardware's one rounding to e4m3 (rs = f8_inverse(s)).  q is the neighbour of x / s in fp32 (one
+// correction of x * rs by the exact remainder); an inexact q takes the odd one of the two fp32 neighbours of the quotient,
 // which an e4m3 rounding (4 of 24 bits) cannot tell from the quotient itself.  Rounding q directly would round
 // twice and miss the definition wherever q lands on the middle of two e4m3 values.
 __device__ __forceinline__ float f8_quotient(float x, float s, float rs) {
@@ -186,18 +197,19 @@ __device__ __forceinline__ float f8_quotient(float x, float s, float rs) {
 // Eight quotients at once.  x * rs is within 2 steps of fp32 of x / s; its e4m3 rounding can only differ from the
 // quotient's next to the middle of two codes, which for a normal code (|q| >= 2^-6) has the low 20 bits 0x80000.  Only a
 // wave that holds a value within 4 steps of that, or a smaller one, takes the exact form: 5 operations a value, not 12.
-__device__ __forceinline__ void f8_quotients(const float* x, float s, float rs, float* q) {
-  bool near = false;
+__device__ __forceinline__ void f8_quotients(const float* x, const float* s, const float* rs, float* q) {
+  uint32_t off = ~0u;    // distance from the nearest middle, plus 4 steps
+  float least = INFINITY;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    q[i] = x[i] * rs;
-    const uint32_t b = __float_as_uint(q[i]);
-    near |= ((b + (4 - 0x80000)) & 0xFFFFFu) <= 8u;
-    near |= fabsf(q[i]) < 0x1p-6f;
+    q[i] = x[i] * rs[i];
+    off = min(off, (__float_as_uint(q[i]) + (4 - 0x80000)) & 0xFFFFFu);
+    least = fminf(least, fabsf(q[i]));
   }
-  if (near) {
+  // (a NaN scale leaves q NaN either way)
+  if (off <= 8u || least < 0x1p-6f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = f8_quotient(x[i], s, rs);
+    for (int i = 0; i < 8; ++i) q[i] = f8_quotient(x[i], s[i], rs[i]);
   }
 }
 

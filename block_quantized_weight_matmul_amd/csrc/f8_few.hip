@@ -29,23 +29,19 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 // bits 1..3 of the row (two rows fill the 64 banks, so 16 lanes that read one piece of 16 rows use every bank once),
 // scales [g][row].
 template <int XT>
-__device__ __forceinline__ void load_group(const typename Elem<XT>::T* row, int g, int64_t K, bool vec, float* v) {
-  const int64_t c = static_cast<int64_t>(g) * kF8Block + (threadIdx.x & 15) * 8;
-  if (vec && c + 8 <= K) {
-    load8<XT>(row + c, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < K ? static_cast<float>(row[c + i]) : 0.0f;
-  }
+__device__ __forceinline__ void load_group(const typename Elem<XT>::T* row, int g, int64_t K, float* v) {
+  load_row8<XT>(row, static_cast<int64_t>(g) * kF8Block + (threadIdx.x & 15) * 8, K, v);
 }
 __device__ __forceinline__ void store_group(const float* v, int w, int t, uint8_t* codes, float* scales) {
   const int lane = threadIdx.x & 15;
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
-  const float s = f8_scale(max16(m)), rs = 1.0f / s;
-  float q[8];
-  f8_quotients(v, s, rs, q);
+  const float s = f8_scale(max16(m)), rs = f8_inverse(s);
+  float q[8], ss[8], rr[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) { ss[i] = s; rr[i] = rs; }
+  f8_quotients(v, ss, rr, q);
   *reinterpret_cast<uint2*>(codes + static_cast<size_t>(w) * 128 + (((lane >> 1) ^ (t >> 1 & 7)) * 16) + (lane & 1) * 8) =
       make_uint2(f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7]));
   if (lane == 0) scales[w] = s;
@@ -63,7 +59,7 @@ struct FewArgs {
   const float* xs;    // [G][N] (not RAW)
   void* y;
   int64_t M, K, Kp, ldx;
-  int N, G, waves, vec_x, vec_y;
+  int N, G, waves, vec_y;
 };
 
 // RAW: element type of raw tokens, -1 for quantized ones.  B: groups of a batch.  W: most waves of a workgroup (128
@@ -86,7 +82,7 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       const int w = std::min(team + i * teams, items - 1), g = w / a.N;
-      if (i * teams < items) load_group<RAW>(static_cast<const X*>(a.x) + (w - g * a.N) * a.ldx, g, a.K, a.vec_x, v[i]);
+      if (i * teams < items) load_group<RAW>(static_cast<const X*>(a.x) + (w - g * a.N) * a.ldx, g, a.K, v[i]);
     }
   }
 
@@ -137,7 +133,7 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
     }
     for (int w = team + kItems * teams; w < items; w += teams) {
       const int g = w / a.N;
-      load_group<RAW>(static_cast<const X*>(a.x) + (w - g * a.N) * a.ldx, g, a.K, a.vec_x, v[0]);
+      load_group<RAW>(static_cast<const X*>(a.x) + (w - g * a.N) * a.ldx, g, a.K, v[0]);
       store_group(v[0], w, w - g * a.N, codes, scales);
     }
     __syncthreads();
@@ -208,7 +204,7 @@ struct FewIdArgs {
   const int32_t* ids;
   void* y;
   int64_t M, K, Kp;
-  int E, pairs, slots, G, vec_x, vec_y;
+  int E, pairs, slots, G, vec_y;
 };
 
 // grid (row slices, distinct experts at most): workgroup (s, j) finds the j-th distinct expert among the ids (in order of
@@ -291,7 +287,7 @@ __global__ __launch_bounds__(kIdThreads) void k_f8_few_id(FewIdArgs a) {
     for (int w = tid >> 4; w < n * a.G; w += kIdThreads / 16) {
       const int g = w / n, u = w - g * n;
       float v[8];
-      load_group<XT>(x + static_cast<int64_t>(mine[p0 + u] / a.slots) * a.K, g, a.K, a.vec_x, v);
+      load_group<XT>(x + static_cast<int64_t>(mine[p0 + u] / a.slots) * a.K, g, a.K, v);
       store_group(v, w, u, sh, scales);
     }
     __syncthreads();
@@ -369,10 +365,6 @@ FewArgs few_args(const F8Desc& m, int64_t N, void* y, int yt) {
   return a;
 }
 
-bool rows_vec(const void* x, int xt, int64_t ldx, int64_t N) {
-  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && (N <= 1 || ldx * (xt == DT_F32 ? 4 : 2) % 16 == 0);
-}
-
 template <int XT>
 hipError_t few_id_out(const FewIdArgs& a, int yt, dim3 grid, size_t lds, hipStream_t st) {
   switch (yt) {
@@ -406,7 +398,6 @@ hipError_t launch_f8_linear(const F8Desc& m, const void* x, int xt, int64_t ldx,
   FewArgs a = few_args(m, N, y, yt);
   a.x = x;
   a.ldx = ldx;
-  a.vec_x = rows_vec(x, xt, ldx, N);
   switch (xt) {
     case DT_F32: return few_out<DT_F32>(a, yt, st);
     case DT_F16: return few_out<DT_F16>(a, yt, st);
@@ -434,7 +425,6 @@ hipError_t launch_f8_linear_id(const F8Desc& m, const void* x, int xt, int64_t p
   a.pairs = static_cast<int>(pairs);
   a.slots = slots;
   a.G = static_cast<int>(m.Kp / kF8Block);
-  a.vec_x = rows_vec(x, xt, m.K, pairs / slots);
   a.vec_y = store_vec(y, m.M, yt);
   const int64_t slices = (m.M + kIdRows - 1) / kIdRows;
   const dim3 grid(static_cast<unsigned>(slices), static_cast<unsigned>(std::min<int64_t>(pairs, m.n_experts)));

@@ -21,26 +21,17 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
   return v;
 }
 
-// 8 elements of a row from column c; columns from K on are zero.  VEC: every row and c are 16-byte aligned.
-template <int DT, bool VEC>
-__device__ __forceinline__ void load_row8(const typename Elem<DT>::T* row, int64_t c, int64_t K, float* v) {
-  if (VEC && c + 8 <= K) {
-    load8<DT>(row + c, v);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = c + i < K ? static_cast<float>(row[c + i]) : 0.0f;
-}
-
 __device__ __forceinline__ uint2 codes8(const float* v, float s, float rs) {
-  float q[8];
-  f8_quotients(v, s, rs, q);
+  float q[8], ss[8], rr[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) { ss[i] = s; rr[i] = rs; }
+  f8_quotients(v, ss, rr, q);
   return make_uint2(f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7]));
 }
 
 // Groups along K only: 16 lanes hold one token's group, 8 values each; a workgroup takes 16 tokens of one group, so
 // that their scales (group-major) are one 64-byte store.
-template <int DT, bool VEC>
+template <int DT>
 __global__ __launch_bounds__(256) void k_f8_quant_rows(F8QuantArgs a) {
   const int lane = threadIdx.x & 15;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
@@ -48,34 +39,43 @@ __global__ __launch_bounds__(256) void k_f8_quant_rows(F8QuantArgs a) {
   const int64_t g = blockIdx.y;
   const int64_t c = g * kF8Block + lane * 8;
   float v[8];
-  load_row8<DT, VEC>(static_cast<const typename Elem<DT>::T*>(a.x) + t * a.ldx, c, a.K, v);
+  load_row8<DT>(static_cast<const typename Elem<DT>::T*>(a.x) + t * a.ldx, c, a.K, v);
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
   const float s = f8_scale(max16(m));
-  *reinterpret_cast<uint2*>(a.codes_r + t * f8_pad(a.K) + c) = codes8(v, s, 1.0f / s);
+  *reinterpret_cast<uint2*>(a.codes_r + t * f8_pad(a.K) + c) = codes8(v, s, f8_inverse(s));
   if (lane == 0) a.scales_r[g * a.N + t] = s;
 }
 
-// Transposed write of a 128 x 128 tile of codes: thread (team, lane) gives, for each of its 8 columns, the 8 codes
-// of its 8 rows.  8-byte pieces are exchanged through LDS with the piece index xored by the column's lane, so that
-// both the writes (16 lanes, 16 columns) and the reads (one column, 16 pieces) use every bank once.
-__device__ __forceinline__ void lds_put(uint2* tile, int team, int lane, int j, uint2 v) {
-  tile[(lane * 8 + j) * 16 + (team ^ lane)] = v;
-}
-__device__ __forceinline__ uint2 lds_get(const uint2* tile, int col, int piece) {
-  return tile[col * 16 + (piece ^ (col >> 3))];
+// Transposed write of a 128 x 128 tile of codes through LDS: column by column of 128 bytes, whose 8-byte pieces are
+// xored with the column's lane, so that 16 lanes that write one piece of 16 columns, or read the 16 pieces of one, use
+// every bank once.  Rows r .. of column lane * 8 + j (r a multiple of the store's size):
+__device__ __forceinline__ uint8_t* lds_piece(uint8_t* tile, int col, int r) {
+  return tile + col * 128 + (((r >> 3) ^ (col >> 3)) * 8) + (r & 7);
 }
 
-// A 128 x 128 tile in registers, 8 x 8 values a thread (rows team * 8 .., columns lane * 8 ..).
-// ROWS: one scale per row of the tile; COLS: one per column, codes transposed; neither: one for the tile, codes as
-// they stand and (codes_c given) transposed.
-template <int DT, bool VEC, bool ROWS, bool COLS>
-__global__ __launch_bounds__(256) void k_f8_quant_tile(F8QuantArgs a, int64_t w_rows_pad) {
+constexpr int kTileThreads = 512;  // 32 teams of 16 lanes; a thread holds 4 rows x 8 columns
+constexpr int kTileRows = 4;
+
+// codes of 4 rows of one column, transposed from four words of 4 columns each
+__device__ __forceinline__ uint32_t column4(const uint2* q, int j) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) w |= (((j < 4 ? q[p].x : q[p].y) >> (8 * (j & 3))) & 0xFFu) << (8 * p);
+  return w;
+}
+
+// A 128 x 128 tile in registers.  ROWS: one scale per row of the tile; COLS: one per column, codes transposed; neither:
+// one for the tile, codes as they stand and (codes_c given) transposed.  4 rows a thread keep half the values in
+// registers that 8 would, and twice the threads on a tile: 777 x 515 fp32, 35 tiles, 11.6 -> 6.3 us.
+template <int DT, bool ROWS, bool COLS>
+__global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, int64_t w_rows_pad) {
   typedef typename Elem<DT>::T T;
-  __shared__ uint2 tile[128 * 16];
-  __shared__ uint32_t cmax[16][128];
-  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
+  __shared__ __align__(16) uint8_t tile[128 * 128];
+  __shared__ uint32_t cmax[kTileThreads / 64][128];
+  __shared__ float2 cscale[128];  // scale and its inverse
+  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4, wave = threadIdx.x >> 6;
   const int64_t Kp = f8_pad(a.K);
   const unsigned tiles_k = static_cast<unsigned>(Kp / kF8Block);
   const int64_t g = blockIdx.x % tiles_k;  // tile along K
@@ -85,89 +85,91 @@ __global__ __launch_bounds__(256) void k_f8_quant_tile(F8QuantArgs a, int64_t w_
   const int64_t e = blockIdx.y;  // expert of a weight
   if (!ROWS && !COLS) x += e * a.N * a.K;
   const int64_t c = g * kF8Block + lane * 8;
-  float v[8][8];
+  const int r0 = team * kTileRows;
+  float v[kTileRows][8];
+  int64_t src[kTileRows];  // row of x, -1 past the end
   if (a.plan) {
-    const int32_t* mp = a.plan + a.pd.map[3] + 3 * j;
+    const int32_t* mp = a.plan + a.pd.map[kPlanTileKinds - 1] + 3 * j;
     const int bucket = mp[0], first = mp[1], end = mp[2];
     if (bucket < 0 || bucket >= a.pd.E) return;  // no expert's pairs: no product reads this group
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int at = first + team * 8 + p;
-      if (at < end) {
-        const int64_t r = a.plan[a.pd.order + at] / a.slots;
-        load_row8<DT, VEC>(x + r * a.ldx, c, a.K, v[p]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
-      }
+    for (int p = 0; p < kTileRows; ++p) {
+      const int at = first + r0 + p;
+      src[p] = at < end ? a.plan[a.pd.order + at] / a.slots : -1;
     }
   } else {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int64_t r = j * kF8Block + team * 8 + p;
-      if (r < N) {
-        load_row8<DT, VEC>(x + r * a.ldx, c, a.K, v[p]);
-      } else {
+    for (int p = 0; p < kTileRows; ++p) {
+      src[p] = j * kF8Block + r0 + p;
+      if (src[p] >= N) src[p] = -1;
+    }
+  }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
-      }
+  for (int p = 0; p < kTileRows; ++p) {
+    if (src[p] >= 0) {
+      load_row8<DT>(x + src[p] * a.ldx, c, a.K, v[p]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
     }
   }
   if (ROWS) {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
+    for (int p = 0; p < kTileRows; ++p) {
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[p][i]));
       const float s = f8_scale(max16(m));
-      const int64_t r = j * kF8Block + team * 8 + p;
+      const int64_t r = j * kF8Block + r0 + p;
       if (r < N) {
-        *reinterpret_cast<uint2*>(a.codes_r + r * Kp + c) = codes8(v[p], s, 1.0f / s);
+        *reinterpret_cast<uint2*>(a.codes_r + r * Kp + c) = codes8(v[p], s, f8_inverse(s));
         if (lane == 0) a.scales_r[g * N + r] = s;
       }
     }
   }
-  const int64_t tiles = a.plan ? a.pd.cap[3] : (N + kF8Block - 1) / kF8Block;
-  const int64_t Np = tiles * kF8Block;
+  const int64_t tiles = a.plan ? a.pd.cap[kPlanTileKinds - 1] : (N + kF8Block - 1) / kF8Block;
+  const int64_t Np = COLS ? tiles * kF8Block : w_rows_pad;
   if (COLS) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t m = 0;
 #pragma unroll
-      for (int p = 0; p < 8; ++p) m = max(m, abs_bits(v[p][i]));
-      cmax[team][lane * 8 + i] = m;
+      for (int p = 0; p < kTileRows; ++p) m = max(m, abs_bits(v[p][i]));
+      m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
+      m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
+      if ((team & 3) == 0) cmax[wave][lane * 8 + i] = m;
     }
     __syncthreads();
     if (threadIdx.x < 128) {
       uint32_t m = 0;
 #pragma unroll
-      for (int t = 0; t < 16; ++t) m = max(m, cmax[t][threadIdx.x]);
+      for (int t = 0; t < kTileThreads / 64; ++t) m = max(m, cmax[t][threadIdx.x]);
       const float s = f8_scale(m);
-      cmax[0][threadIdx.x] = __float_as_uint(s);
+      cscale[threadIdx.x] = make_float2(s, f8_inverse(s));
       const int64_t k = g * kF8Block + threadIdx.x;
       if (k < a.K) a.scales_c[j * a.K + k] = s;
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float s = __uint_as_float(cmax[0][lane * 8 + i]);
-      float col[8];
+    for (int i = 0; i < 8; i += 2) {
+      float col[8], q[8], s[8], rs[8];
 #pragma unroll
-      for (int p = 0; p < 8; ++p) col[p] = v[p][i];
-      lds_put(tile, team, lane, i, codes8(col, s, 1.0f / s));
-    }
-    __syncthreads();
+      for (int n = 0; n < 8; ++n) {
+        const float2 sr = cscale[lane * 8 + i + n / 4];
+        col[n] = v[n % 4][i + n / 4];
+        s[n] = sr.x;
+        rs[n] = sr.y;
+      }
+      f8_quotients(col, s, rs, q);
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int col = p * 16 + team;
-      const int64_t k = g * kF8Block + col;
-      if (k < a.K) *reinterpret_cast<uint2*>(a.codes_c + k * Np + j * kF8Block + lane * 8) = lds_get(tile, col, lane);
+      for (int n = 0; n < 2; ++n)
+        *reinterpret_cast<uint32_t*>(lds_piece(tile, lane * 8 + i + n, r0)) = f8_pack4(q[4 * n], q[4 * n + 1], q[4 * n + 2], q[4 * n + 3]);
     }
   }
   if (!ROWS && !COLS) {
     uint32_t m = 0;
 #pragma unroll
-    for (int p = 0; p < 8; ++p)
+    for (int p = 0; p < kTileRows; ++p)
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[p][i]));
     m = max16(m);
@@ -175,69 +177,60 @@ __global__ __launch_bounds__(256) void k_f8_quant_tile(F8QuantArgs a, int64_t w_
     __syncthreads();
     m = 0;
 #pragma unroll
-    for (int t = 0; t < 16; ++t) m = max(m, cmax[0][t]);
-    const float s = f8_scale(m), rs = 1.0f / s;
+    for (int t = 0; t < kTileThreads / 16; ++t) m = max(m, cmax[0][t]);
+    const float s = f8_scale(m), rs = f8_inverse(s);
     const int64_t G = Kp / kF8Block, R = f8_pad(N) / kF8Block;
-    uint2 q[8];
+    uint2 q[kTileRows];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
+    for (int p = 0; p < kTileRows; ++p) {
       q[p] = codes8(v[p], s, rs);
-      const int64_t r = j * kF8Block + team * 8 + p;
+      const int64_t r = j * kF8Block + r0 + p;
       if (r < N) *reinterpret_cast<uint2*>(a.codes_r + (e * N + r) * Kp + c) = q[p];
     }
     if (threadIdx.x == 0) a.scales_r[(e * R + j) * G + g] = s;
-    if (a.codes_c) {
-      if (threadIdx.x == 0) a.scales_c[(e * G + g) * R + j] = s;
+    if (!a.codes_c) return;
+    if (threadIdx.x == 0) a.scales_c[(e * G + g) * R + j] = s;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t b[8];
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t*>(lds_piece(tile, lane * 8 + i, r0)) = column4(q, i);
+  }
+  if (COLS || !ROWS) {
+    __syncthreads();
+    const int64_t row0 = COLS ? 0 : e * a.K;
 #pragma unroll
-        for (int p = 0; p < 8; ++p) b[p] = ((i < 4 ? q[p].x : q[p].y) >> (8 * (i & 3))) & 0xFFu;
-        lds_put(tile, team, lane, i,
-                make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24));
-      }
-      __syncthreads();
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        const int col = p * 16 + team;
-        const int64_t k = g * kF8Block + col;
-        if (k < a.K)
-          *reinterpret_cast<uint2*>(a.codes_c + (e * a.K + k) * w_rows_pad + j * kF8Block + lane * 8) =
-              lds_get(tile, col, lane);
-      }
+    for (int p = 0; p < 128 / (kTileThreads / 16); ++p) {
+      const int col = p * (kTileThreads / 16) + team;
+      const int64_t k = g * kF8Block + col;
+      if (k < a.K)
+        *reinterpret_cast<uint2*>(a.codes_c + (row0 + k) * Np + j * kF8Block + lane * 8) =
+            *reinterpret_cast<const uint2*>(lds_piece(tile, col, lane * 8));
     }
   }
 }
 
 // The codes of the transposed matrix: the same bytes, tile by tile.
-__global__ __launch_bounds__(256) void k_f8_transpose(const uint8_t* codes, const float* scales, int64_t M, int64_t K,
-                                                      uint8_t* codes_t, float* scales_t) {
-  __shared__ uint2 tile[128 * 16];
-  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
+__global__ __launch_bounds__(kTileThreads) void k_f8_transpose(const uint8_t* codes, const float* scales, int64_t M,
+                                                               int64_t K, uint8_t* codes_t, float* scales_t) {
+  __shared__ __align__(16) uint8_t tile[128 * 128];
+  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4, r0 = team * kTileRows;
   const int64_t Kp = f8_pad(K), Mp = f8_pad(M), G = Kp / kF8Block, R = Mp / kF8Block;
   const int64_t g = blockIdx.x % static_cast<unsigned>(G), j = blockIdx.x / static_cast<unsigned>(G), e = blockIdx.y;
-  uint2 q[8];
+  uint2 q[kTileRows];
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int64_t r = j * kF8Block + team * 8 + p;
+  for (int p = 0; p < kTileRows; ++p) {
+    const int64_t r = j * kF8Block + r0 + p;
     q[p] = r < M ? *reinterpret_cast<const uint2*>(codes + (e * M + r) * Kp + g * kF8Block + lane * 8) : make_uint2(0, 0);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t b[8];
-#pragma unroll
-    for (int p = 0; p < 8; ++p) b[p] = ((i < 4 ? q[p].x : q[p].y) >> (8 * (i & 3))) & 0xFFu;
-    lds_put(tile, team, lane, i,
-            make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24));
-  }
+  for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t*>(lds_piece(tile, lane * 8 + i, r0)) = column4(q, i);
   if (threadIdx.x == 0) scales_t[(e * G + g) * R + j] = scales[(e * R + j) * G + g];
   __syncthreads();
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int col = p * 16 + team;
+  for (int p = 0; p < 128 / (kTileThreads / 16); ++p) {
+    const int col = p * (kTileThreads / 16) + team;
     const int64_t k = g * kF8Block + col;
     if (k < K)
-      *reinterpret_cast<uint2*>(codes_t + (e * K + k) * Mp + j * kF8Block + lane * 8) = lds_get(tile, col, lane);
+      *reinterpret_cast<uint2*>(codes_t + (e * K + k) * Mp + j * kF8Block + lane * 8) =
+          *reinterpret_cast<const uint2*>(lds_piece(tile, col, lane * 8));
   }
 }
 
@@ -255,37 +248,26 @@ __global__ __launch_bounds__(256) void k_f8_dequantize(const uint8_t* codes, con
 
 template <int DT>
 hipError_t quantize_dt(const F8QuantArgs& a, hipStream_t st) {
-  const int esz = DT == DT_F32 ? 4 : 2;
-  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ldx * esz % 16 == 0 || a.N <= 1);
   const int64_t G = f8_pad(a.K) / kF8Block;
   if (!a.codes_c) {
     const dim3 grid(static_cast<unsigned>((a.N + 15) / 16), static_cast<unsigned>(G));
-    if (vec) k_f8_quant_rows<DT, true><<<grid, 256, 0, st>>>(a);
-    else k_f8_quant_rows<DT, false><<<grid, 256, 0, st>>>(a);
+    k_f8_quant_rows<DT><<<grid, 256, 0, st>>>(a);
     return hipGetLastError();
   }
-  const int64_t tiles = a.plan ? a.pd.cap[3] : (a.N + kF8Block - 1) / kF8Block;
+  const int64_t tiles = a.plan ? a.pd.cap[kPlanTileKinds - 1] : (a.N + kF8Block - 1) / kF8Block;
   if (tiles * G > INT_MAX) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(tiles * G));
-  if (a.codes_r) {
-    if (vec) k_f8_quant_tile<DT, true, true, true><<<grid, 256, 0, st>>>(a, 0);
-    else k_f8_quant_tile<DT, false, true, true><<<grid, 256, 0, st>>>(a, 0);
-  } else {
-    if (vec) k_f8_quant_tile<DT, true, false, true><<<grid, 256, 0, st>>>(a, 0);
-    else k_f8_quant_tile<DT, false, false, true><<<grid, 256, 0, st>>>(a, 0);
-  }
+  if (a.codes_r) k_f8_quant_tile<DT, true, true><<<grid, kTileThreads, 0, st>>>(a, 0);
+  else k_f8_quant_tile<DT, false, true><<<grid, kTileThreads, 0, st>>>(a, 0);
   return hipGetLastError();
 }
 
 template <int DT>
 hipError_t quantize_weight_dt(const F8QuantArgs& a, int64_t E, hipStream_t st) {
-  const int esz = DT == DT_F32 ? 4 : 2;
-  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.K * esz % 16 == 0;
   const int64_t tiles = f8_pad(a.K) / kF8Block * (f8_pad(a.N) / kF8Block);
   if (tiles > INT_MAX) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(E));
-  if (vec) k_f8_quant_tile<DT, true, false, false><<<grid, 256, 0, st>>>(a, f8_pad(a.N));
-  else k_f8_quant_tile<DT, false, false, false><<<grid, 256, 0, st>>>(a, f8_pad(a.N));
+  k_f8_quant_tile<DT, false, false><<<grid, kTileThreads, 0, st>>>(a, f8_pad(a.N));
   return hipGetLastError();
 }
 
@@ -323,7 +305,7 @@ hipError_t launch_f8_transpose(const F8Desc& m, uint8_t* codes_t, float* scales_
   const int64_t tiles = m.Kp / kF8Block * (f8_pad(m.M) / kF8Block);
   if (tiles > INT_MAX) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(m.n_experts));
-  k_f8_transpose<<<grid, 256, 0, st>>>(m.codes, m.scales, m.M, m.K, codes_t, scales_t);
+  k_f8_transpose<<<grid, kTileThreads, 0, st>>>(m.codes, m.scales, m.M, m.K, codes_t, scales_t);
   return hipGetLastError();
 }
 

@@ -40,10 +40,10 @@ __device__ __forceinline__ float sum16f(float v) {
   return v + dppf<0x121>(v);
 }
 
-// V logits of this lane from expert lane * V on; experts from E on are -inf.  vec: rows are 16-byte aligned.
+// V logits of this lane from expert lane * V on; experts from E on are -inf
 template <int LT, int V>
-__device__ __forceinline__ void load_logits(const typename Elem<LT>::T* row, int lane, int E, bool vec, float* v) {
-  if (V >= 8 && vec && lane * V + V <= E) {
+__device__ __forceinline__ void load_logits(const typename Elem<LT>::T* row, int lane, int E, float* v) {
+  if (V >= 8 && lane * V + V <= E) {
 #pragma unroll
     for (int i = 0; i < V; i += 8) load8<LT>(row + lane * V + i, v + i);
   } else {
@@ -57,7 +57,7 @@ constexpr int kRouteTeams = kRouteThreads / 16;
 constexpr int kMaxSlotRegs = 4;  // slot s lives in lane s & 15, register s >> 4
 
 template <int LT, int V>
-__global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, float* part, int32_t* part_n, int vec) {
+__global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, float* part, int32_t* part_n) {
   extern __shared__ int32_t sh[];  // [E + 1] counts, then [waves][16 * V] probability sums
   const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
   float* shp = reinterpret_cast<float*>(sh + a.E + 1);
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, float* par
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteTeams;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteTeams + team; t < a.N; t += step) {
     float v[V], l[V];
-    load_logits<LT, V>(static_cast<const typename Elem<LT>::T*>(a.logits) + t * a.E, lane, a.E, vec, l);
+    load_logits<LT, V>(static_cast<const typename Elem<LT>::T*>(a.logits) + t * a.E, lane, a.E, l);
     if (a.valid && !a.valid[t]) {
 #pragma unroll
       for (int i = 0; i < V; ++i) l[i] = kNegInf;
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(1024) void k_balance_loss(const int32_t* counts, co
 
 // dl = p (dp - sum p dp), dp_e = dloss coef f_e / T + the chosen slots' gradients; p again from the logits.
 template <int LT, int V>
-__global__ __launch_bounds__(kRouteThreads) void k_route_backward(RouteBackwardArgs a, int vec) {
+__global__ __launch_bounds__(kRouteThreads) void k_route_backward(RouteBackwardArgs a) {
   typedef typename Elem<LT>::T T;
   const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
   float c[V];
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_backward(RouteBackwardA
     const T* row = static_cast<const T*>(a.logits) + t * a.E;
     T* out = static_cast<T*>(a.dlogits) + t * a.E;
     float l[V], p[V], dp[V];
-    load_logits<LT, V>(row, lane, a.E, vec, l);
+    load_logits<LT, V>(row, lane, a.E, l);
     float top = kNegInf;
 #pragma unroll
     for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);  // fmaxf passes over a NaN
@@ -288,14 +288,15 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_backward(RouteBackwardA
     dot = sum16f(dot);
 #pragma unroll
     for (int i = 0; i < V; ++i) dp[i] = p[i] * (dp[i] - dot);
-    if (V >= 8 && vec && lane * V + V <= a.E) {
+    if (V >= 8 && lane * V + V <= a.E) {
 #pragma unroll
       for (int i = 0; i < V; i += 8) {
         typedef T T8 __attribute__((ext_vector_type(8)));
+        typedef T8 T8u __attribute__((aligned(sizeof(T))));
         T8 o;
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = to_elem<LT>(dp[i + k]);
-        *reinterpret_cast<T8*>(out + lane * V + i) = o;
+        *reinterpret_cast<T8u*>(out + lane * V + i) = o;
       }
     } else {
 #pragma unroll
@@ -525,10 +526,9 @@ hipError_t launch_v(const RouteArgs& a, hipStream_t st) {
   const int nb = route_blocks(a.N);
   float* part = static_cast<float*>(a.ws);
   int32_t* part_n = reinterpret_cast<int32_t*>(part + static_cast<int64_t>(nb) * a.E);
-  const int vec = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.E % 8 == 0;
   const size_t lds = (a.E + 1) * 4 + static_cast<size_t>(kRouteTeams / 4) * 16 * V * 4;
   if (nb > 0) {
-    k_route<LT, V><<<nb, kRouteThreads, lds, st>>>(a, part, part_n, vec);
+    k_route<LT, V><<<nb, kRouteThreads, lds, st>>>(a, part, part_n);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -538,9 +538,8 @@ hipError_t launch_v(const RouteArgs& a, hipStream_t st) {
 
 template <int LT, int V>
 hipError_t launch_v(const RouteBackwardArgs& a, hipStream_t st) {
-  const int vec = (reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits)) % 16 == 0 && a.E % 8 == 0;
   const int nb = static_cast<int>(std::min<int64_t>((a.N + kRouteTeams - 1) / kRouteTeams, 2048));
-  k_route_backward<LT, V><<<nb, kRouteThreads, 0, st>>>(a, vec);
+  k_route_backward<LT, V><<<nb, kRouteThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
