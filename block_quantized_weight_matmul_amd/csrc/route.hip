@@ -6,6 +6,7 @@
 // per workgroup, added in a fixed order: the same input gives the same bits.
 #include <algorithm>
 #include <climits>
+#include <utility>
 
 #include "f8.hpp"
 
@@ -40,6 +41,82 @@ __device__ __forceinline__ float sum16f(float v) {
   return v + dppf<0x121>(v);
 }
 
+// e^x to 2 steps of fp32: 2^t with t = x log2(e) rounded, corrected by what the rounding left.  NaN stays NaN.
+__device__ __forceinline__ float fast_exp(float x) {
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  x = x < -150.0f ? -150.0f : x;  // 0 in fp32, and no infinity in the correction
+  const float t = x * kLog2e, r = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t));
+  const float y = __builtin_amdgcn_exp2f(t);
+  return fmaf(y, r * kLn2, y);
+}
+
+// 16-bit logits as unsigned keys that order like (value, lower index first): the value's bits made monotonic above the
+// complement of the expert; 0 is below every key that can be chosen.  -inf and NaN give 0, -0 counts as +0.
+template <int LT>
+__device__ __forceinline__ uint32_t logit_key(float v, int e) {
+  if (!(v > kNegInf)) return 0u;
+  uint32_t b;
+  if constexpr (LT == DT_F16) b = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+  else b = __float_as_uint(v) >> 16;
+  b = v == 0.0f ? 0x8000u : b & 0x8000u ? ~b & 0xFFFFu : b | 0x8000u;
+  return b << 16 | (0xFFFFu - static_cast<uint32_t>(e));
+}
+template <int LT>
+__device__ __forceinline__ float key_logit(uint32_t key) {
+  uint32_t b = key >> 16;
+  b = b & 0x8000u ? b & 0x7FFFu : ~b & 0xFFFFu;
+  if constexpr (LT == DT_F16) return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(b)));
+  else return __uint_as_float(b << 16);
+}
+__device__ __forceinline__ uint32_t max16u(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(dpp<0x128>(static_cast<int>(v))));
+  v = max(v, static_cast<uint32_t>(dpp<0x124>(static_cast<int>(v))));
+  v = max(v, static_cast<uint32_t>(dpp<0x122>(static_cast<int>(v))));
+  return max(v, static_cast<uint32_t>(dpp<0x121>(static_cast<int>(v))));
+}
+
+// The largest logits of 16 lanes, one a call, ties to the lower expert.  next() returns the expert (-1: none is left) and
+// its logit; the same in all 16 lanes.
+template <int LT, int V, bool KEYS = LT != DT_F32> struct Chooser;
+template <int LT, int V> struct Chooser<LT, V, true> {
+  uint32_t k[V];
+  __device__ __forceinline__ Chooser(const float* l, int lane) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) k[i] = logit_key<LT>(l[i], lane * V + i);
+  }
+  __device__ __forceinline__ int next(int, float& value) {
+    uint32_t m = k[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = max(m, k[i]);
+    m = max16u(m);
+#pragma unroll
+    for (int i = 0; i < V; ++i) k[i] = k[i] == m ? 0u : k[i];
+    value = key_logit<LT>(m);
+    return m ? static_cast<int>(0xFFFFu - (m & 0xFFFFu)) : -1;
+  }
+};
+template <int LT, int V> struct Chooser<LT, V, false> {
+  float v[V];
+  __device__ __forceinline__ Chooser(const float* l, int) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = l[i] == l[i] ? l[i] : kNegInf;
+  }
+  __device__ __forceinline__ int next(int lane, float& value) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
+    m = max16f(m);
+    int at = V;  // in this lane
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i) at = v[i] == m ? i : at;
+    const int e = min16i(at < V ? lane * V + at : INT_MAX), mine = e - lane * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = i == mine ? kNegInf : v[i];
+    value = m;
+    return m > kNegInf ? e : -1;
+  }
+};
+
 // V logits of this lane from expert lane * V on; experts from E on are -inf
 template <int LT, int V>
 __device__ __forceinline__ void load_logits(const typename Elem<LT>::T* row, int lane, int E, float* v) {
@@ -52,12 +129,33 @@ __device__ __forceinline__ void load_logits(const typename Elem<LT>::T* row, int
   }
 }
 
-constexpr int kRouteThreads = 256;
-constexpr int kRouteTeams = kRouteThreads / 16;
-constexpr int kMaxSlotRegs = 4;  // slot s lives in lane s & 15, register s >> 4
+// Threads of a workgroup: one register of every kind per expert of a lane, so many experts leave room for fewer waves.
+constexpr int route_threads(int V) { return V <= 8 ? 1024 : V <= 16 ? 512 : 256; }
+// Slot s lives in lane s & 15, register s >> 4: one register (SR) up to 16 slots, four up to 64.
+constexpr int kRouteOneBlock = 128;   // rows that one workgroup routes and sums by itself
 
-template <int LT, int V>
-__global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, float* part, int32_t* part_n) {
+// Sum of v over the workgroup's threads, in a fixed order, in thread 0.  red: 16 floats of LDS.
+__device__ __forceinline__ float block_sum(float v, float* red, int threads) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.0f;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < threads / 64; ++i) s += red[i];
+  return s;
+}
+
+// Expert e's part of sum_e f_e P_e times T, f_e = E counts_e / (S T).
+__device__ __forceinline__ float loss_part(int count, float psum, float T, int E, int S) {
+  return T > 0.0f ? static_cast<float>(count) * E / (S * T) * psum : 0.0f;
+}
+
+// part, part_n: the workgroups' sums over their rows, [E] and [E + 1] each, and behind part_n the counter of
+// k_route_sum.  A single workgroup writes the results itself.
+template <int LT, int V, int SR>
+__global__ __launch_bounds__(route_threads(V)) void k_route(RouteArgs a, float* part, int32_t* part_n) {
+  constexpr int kRouteThreads = route_threads(V), kRouteTeams = kRouteThreads / 16;
   extern __shared__ int32_t sh[];  // [E + 1] counts, then [waves][16 * V] probability sums
   const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
   float* shp = reinterpret_cast<float*>(sh + a.E + 1);
@@ -68,57 +166,47 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, float* par
   for (int i = 0; i < V; ++i) psum[i] = 0.0f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteTeams;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteTeams + team; t < a.N; t += step) {
-    float v[V], l[V];
+    float l[V];
     load_logits<LT, V>(static_cast<const typename Elem<LT>::T*>(a.logits) + t * a.E, lane, a.E, l);
     if (a.valid && !a.valid[t]) {
 #pragma unroll
       for (int i = 0; i < V; ++i) l[i] = kNegInf;
     }
+    Chooser<LT, V> choose(l, lane);
+    float top = kNegInf, chosen[SR];
+    int ids[SR];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = l[i] == l[i] ? l[i] : kNegInf;  // a NaN is never chosen
-    float top = 0.0f, chosen[kMaxSlotRegs];
-    int ids[kMaxSlotRegs];
-#pragma unroll
-    for (int k = 0; k < kMaxSlotRegs; ++k) { chosen[k] = kNegInf; ids[k] = -1; }
+    for (int k = 0; k < SR; ++k) { chosen[k] = kNegInf; ids[k] = -1; }
     for (int s = 0; s < a.S; ++s) {
-      float m = v[0];
+      float m;
+      const int e = choose.next(lane, m);
+      if (s == 0 && e >= 0) top = m;
 #pragma unroll
-      for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-      m = max16f(m);
-      if (s == 0) top = m;
-      int at = INT_MAX;
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i) at = v[i] == m ? lane * V + i : at;
-      at = min16i(at);
-      const bool some = m > kNegInf;
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = lane * V + i == at ? kNegInf : v[i];
-#pragma unroll
-      for (int k = 0; k < kMaxSlotRegs; ++k)
-        if (s == k * 16 + lane && some) { chosen[k] = m; ids[k] = at; }
+      for (int k = 0; k < SR; ++k)
+        if (s == k * 16 + lane) { chosen[k] = m; ids[k] = e; }
     }
     const bool alive = top > kNegInf;
     float z = 0.0f, p[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      p[i] = alive ? expf(l[i] - top) : 0.0f;
+      p[i] = alive ? fast_exp(l[i] - top) : 0.0f;
       z += p[i];
     }
     z = sum16f(z);
     const float rz = alive ? 1.0f / z : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) psum[i] = fmaf(p[i], rz, psum[i]);
-    float total = 0.0f, w[kMaxSlotRegs];
+    float total = 0.0f, w[SR];
 #pragma unroll
-    for (int k = 0; k < kMaxSlotRegs; ++k) {
-      w[k] = ids[k] >= 0 ? expf(chosen[k] - top) : 0.0f;
+    for (int k = 0; k < SR; ++k) {
+      w[k] = ids[k] >= 0 ? fast_exp(chosen[k] - top) : 0.0f;
       total += w[k];
     }
     total = a.normalise ? sum16f(total) : z;
     // a NaN among the logits makes the row's probabilities NaN, normalised or not
     if (!(z == z)) total = z;
 #pragma unroll
-    for (int k = 0; k < kMaxSlotRegs; ++k) {
+    for (int k = 0; k < SR; ++k) {
       const int s = k * 16 + lane;
       if (s < a.S) {
         a.ids[t * a.S + s] = ids[k];
@@ -136,6 +224,25 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, float* par
     if ((team & 3) == 0) shp[(team >> 2) * (16 * V) + lane * V + i] = psum[i];
   }
   __syncthreads();
+  if (gridDim.x == 1) {
+    __shared__ float red[16];
+    const float T = static_cast<float>(sh[a.E]);
+    float v = 0.0f;
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kRouteTeams / 4; ++k) s += shp[k * (16 * V) + e];
+      a.psum[e] = s;
+      a.counts[e] = sh[e];
+      v += loss_part(sh[e], s, T, a.E, a.S);
+    }
+    if (threadIdx.x == 0) a.counts[a.E] = sh[a.E];
+    if (a.loss) {
+      v = block_sum(v, red, kRouteThreads);
+      if (threadIdx.x == 0) *a.loss = T > 0.0f ? a.coef * v / T : 0.0f;
+    }
+    return;
+  }
   for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
     float s = 0.0f;
 #pragma unroll
@@ -143,78 +250,90 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(RouteArgs a, float* par
     part[static_cast<int64_t>(blockIdx.x) * a.E + e] = s;
   }
   for (int i = threadIdx.x; i <= a.E; i += kRouteThreads) part_n[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + i] = sh[i];
+  if (blockIdx.x == 0 && threadIdx.x == 0) part_n[static_cast<int64_t>(gridDim.x) * (a.E + 1)] = 0;
 }
 
-// loss = coef * sum_e f_e P_e, f_e = E counts_e / (S T), P_e = psum_e / T; 0 when no row has an expert.
-// Every thread of a 1024-thread workgroup calls it; red: 16 floats of LDS.
-__device__ void balance_loss(const int32_t* counts, const float* psum, int E, int S, float coef, float* loss, float* red) {
-  const float T = static_cast<float>(counts[E]);
-  float v = 0.0f;
-  for (int e = threadIdx.x; e < E; e += 1024)
-    v += T > 0.0f ? static_cast<float>(counts[e]) * E / (S * T) * psum[e] : 0.0f;
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float s = 0.0f;
-    for (int i = 0; i < 16; ++i) s += red[i];
-    *loss = T > 0.0f ? coef * s / T : 0.0f;
-  }
-}
+constexpr int kSumCols = 32, kSumSegs = 32;
 
-// Adds the workgroups' partials: thread (segment, expert) adds a run of them, the segments' sums are added in order.
-__global__ __launch_bounds__(1024) void k_route_sum(const float* part, const int32_t* part_n, int blocks, RouteArgs a) {
-  __shared__ float sp[1024];
-  __shared__ int32_t sn[1024];
-  __shared__ float psum[kRouteMaxExperts];
-  __shared__ int32_t counts[kRouteMaxExperts + 1];
-  __shared__ float red[16];
-  const int E1 = a.E + 1;
-  int segs = 1024 / E1;
-  if (segs < 1) segs = 1;
-  const int per = (blocks + segs - 1) / segs;
-  for (int e0 = 0; e0 < E1; e0 += 1024) {
-    const int e = e0 + static_cast<int>(threadIdx.x) % (E1 < 1024 ? E1 : 1024), seg = E1 < 1024 ? threadIdx.x / E1 : 0;
-    float s = 0.0f;
-    int n = 0;
-    if (e < E1 && seg < segs) {
-      const int end = min(blocks, (seg + 1) * per);
+// Adds the workgroups' partials: a workgroup takes 32 experts, a thread every 32nd partial of one, and the threads' sums
+// are added in order.  (One workgroup for all of them waited 17 us for 256 partials of 128 experts.)  The last workgroup
+// to finish, known by the counter, adds up the loss from the finished sums.
+__global__ __launch_bounds__(kSumCols * kSumSegs) void k_route_sum(const float* part, const int32_t* part_n, int blocks,
+                                                                   RouteArgs a, int32_t* counter) {
+  __shared__ float sp[kSumSegs][kSumCols + 1], red[16];
+  __shared__ int32_t sn[kSumSegs][kSumCols + 1];
+  __shared__ int last;
+  const int col = threadIdx.x % kSumCols, seg = threadIdx.x / kSumCols, e = blockIdx.x * kSumCols + col, E1 = a.E + 1;
+  float s = 0.0f;
+  int n = 0;
 #pragma unroll 8
-      for (int b = seg * per; b < end; ++b) {
-        if (e < a.E) s += part[static_cast<int64_t>(b) * a.E + e];
-        n += part_n[static_cast<int64_t>(b) * E1 + e];
-      }
-    }
-    sp[threadIdx.x] = s;
-    sn[threadIdx.x] = n;
-    __syncthreads();
-    if (e < E1 && seg == 0) {
-      for (int k = 1; k < segs; ++k) {
-        s += sp[k * E1 + e];
-        n += sn[k * E1 + e];
-      }
-      a.counts[e] = n;
-      counts[e] = n;
-      if (e < a.E) {
-        a.psum[e] = s;
-        psum[e] = s;
-      }
-    }
-    __syncthreads();
+  for (int b = seg; b < blocks; b += kSumSegs) {
+    if (e < a.E) s += part[static_cast<int64_t>(b) * a.E + e];
+    if (e < E1) n += part_n[static_cast<int64_t>(b) * E1 + e];
   }
-  if (a.loss) balance_loss(counts, psum, a.E, a.S, a.coef, a.loss, red);
+  sp[seg][col] = s;
+  sn[seg][col] = n;
+  __syncthreads();
+  if (seg == 0 && e < E1) {
+    for (int k = 1; k < kSumSegs; ++k) {
+      s += sp[k][col];
+      n += sn[k][col];
+    }
+    a.counts[e] = n;
+    if (e < a.E) a.psum[e] = s;
+  }
+  if (!a.loss) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(counter, 1) == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  const float T = static_cast<float>(__hip_atomic_load(a.counts + a.E, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+  float v = 0.0f;
+  for (int i = threadIdx.x; i < a.E; i += kSumCols * kSumSegs)
+    v += loss_part(__hip_atomic_load(a.counts + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
+                   __hip_atomic_load(a.psum + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), T, a.E, a.S);
+  v = block_sum(v, red, kSumCols * kSumSegs);
+  if (threadIdx.x == 0) *a.loss = T > 0.0f ? a.coef * v / T : 0.0f;
+}
+
+__global__ __launch_bounds__(1024) void k_route_none(RouteArgs a) {
+  for (int e = threadIdx.x; e <= a.E; e += 1024) {
+    a.counts[e] = 0;
+    if (e < a.E) a.psum[e] = 0.0f;
+  }
+  if (a.loss && threadIdx.x == 0) *a.loss = 0.0f;
 }
 
 __global__ __launch_bounds__(1024) void k_balance_loss(const int32_t* counts, const float* psum, int E, int S, float coef,
                                                        float* loss) {
   __shared__ float red[16];
-  balance_loss(counts, psum, E, S, coef, loss, red);
+  const float T = static_cast<float>(counts[E]);
+  float v = 0.0f;
+  for (int e = threadIdx.x; e < E; e += 1024) v += loss_part(counts[e], psum[e], T, E, S);
+  v = block_sum(v, red, 1024);
+  if (threadIdx.x == 0) *loss = T > 0.0f ? coef * v / T : 0.0f;
+}
+
+// adds the gradients d of the slots that lanes 0 .. left - 1 of a row hold to their experts id, slot by slot
+template <int V, int S>
+__device__ __forceinline__ void add_slot(int id, float d, int left, int e0, float* dp) {
+  if (S >= left) return;  // the same for all lanes
+  const int e = dpp<0x150 + S>(id) - e0;  // row_newbcast: lane S of the row
+  const float ds = dppf<0x150 + S>(d);
+#pragma unroll
+  for (int i = 0; i < V; ++i) dp[i] += i == e ? ds : 0.0f;
+}
+template <int V, int... S>
+__device__ __forceinline__ void add_slots(int id, float d, int left, int e0, float* dp, std::integer_sequence<int, S...>) {
+  (add_slot<V, S>(id, d, left, e0, dp), ...);
 }
 
 // dl = p (dp - sum p dp), dp_e = dloss coef f_e / T + the chosen slots' gradients; p again from the logits.
-template <int LT, int V>
-__global__ __launch_bounds__(kRouteThreads) void k_route_backward(RouteBackwardArgs a) {
+template <int LT, int V, int SR>
+__global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
+  constexpr int kRouteTeams = 16;
   typedef typename Elem<LT>::T T;
   const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
   float c[V];
@@ -241,21 +360,21 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_backward(RouteBackwardA
     float z = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      p[i] = alive ? expf(l[i] - top) : 0.0f;
+      p[i] = alive ? fast_exp(l[i] - top) : 0.0f;
       z += p[i];
       dp[i] = c[i];
     }
     z = sum16f(z);
     const float rz = alive ? 1.0f / z : 0.0f;
     if (a.dweights && alive) {
-      float w[kMaxSlotRegs], d[kMaxSlotRegs], total = 0.0f, dot = 0.0f;
-      int id[kMaxSlotRegs];
+      float w[SR], d[SR], total = 0.0f, dot = 0.0f;
+      int id[SR];
 #pragma unroll
-      for (int k = 0; k < kMaxSlotRegs; ++k) {
+      for (int k = 0; k < SR; ++k) {
         const int s = k * 16 + lane;
         id[k] = s < a.S ? a.ids[t * a.S + s] : -1;
         const bool some = id[k] >= 0 && id[k] < a.E;
-        w[k] = some ? expf(static_cast<float>(row[id[k]]) - top) : 0.0f;
+        w[k] = some ? fast_exp(static_cast<float>(row[id[k]]) - top) : 0.0f;
         d[k] = some ? a.dweights[t * a.S + s] : 0.0f;
         total += w[k];
         dot = fmaf(w[k], d[k], dot);
@@ -265,19 +384,10 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_backward(RouteBackwardA
         dot = sum16f(dot) / total;
         const float f = z / total;
 #pragma unroll
-        for (int k = 0; k < kMaxSlotRegs; ++k) d[k] = (d[k] - dot) * f;
+        for (int k = 0; k < SR; ++k) d[k] = (d[k] - dot) * f;
       }
-      for (int s = 0; s < a.S; ++s) {
-        int e = -1;
-        float ds = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kMaxSlotRegs; ++k)
-          if (s >> 4 == k) { e = id[k]; ds = d[k]; }
-        e = __shfl(e, s & 15, 16);
-        ds = __shfl(ds, s & 15, 16);
-#pragma unroll
-        for (int i = 0; i < V; ++i) dp[i] += lane * V + i == e ? ds : 0.0f;
-      }
+      for (int k = 0; k < SR; ++k) add_slots<V>(id[k], d[k], a.S - k * 16, lane * V, dp, std::make_integer_sequence<int, 16>());
     }
     float dot = 0.0f;
 #pragma unroll
@@ -312,6 +422,7 @@ __device__ __forceinline__ int bucket_of(int id, int E) { return id >= 0 && id <
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBlocks = 256;
+constexpr int64_t kPlanOneBlock = 4096;
 constexpr int kMaxBuckets = static_cast<int>(kRouteMaxExperts) + 2;
 
 // pairs per workgroup of the counting and scattering kernels, a multiple of 1024
@@ -320,102 +431,101 @@ __host__ __device__ inline int64_t plan_chunk(int64_t pairs) {
   return (per + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
 }
 
-__global__ __launch_bounds__(kPlanThreads) void k_plan_count(const int32_t* ids, PlanDesc d, int32_t* plan) {
-  __shared__ int32_t hist[kMaxBuckets];
-  const int E = static_cast<int>(d.E), B = E + 2;
-  for (int b = threadIdx.x; b < B; b += kPlanThreads) hist[b] = 0;
+// What the plan's kernels hold in LDS.
+struct PlanShared {
+  int32_t offs[kMaxBuckets + 1], cnt[kMaxBuckets], tiles[kPlanTileKinds][kMaxBuckets + 1];
+  int32_t base[kMaxBuckets];
+  int32_t wsum[kPlanTileKinds + 1][kPlanThreads / 64];
+  int32_t part[kPlanThreads];
+  uint16_t in_wave[kPlanThreads / 64][kMaxBuckets];
+};
+
+// counts of the pairs p0 .. p1 - 1 per bucket, in hist
+__device__ void plan_count(const int32_t* ids, int64_t p0, int64_t p1, int E, int32_t* hist) {
+  for (int b = threadIdx.x; b < E + 2; b += kPlanThreads) hist[b] = 0;
   __syncthreads();
-  const int64_t chunk = plan_chunk(d.pairs), p0 = blockIdx.x * chunk, p1 = std::min(p0 + chunk, d.pairs);
   for (int64_t p = p0 + threadIdx.x; p < p1; p += kPlanThreads) atomicAdd(&hist[bucket_of(ids[p], E)], 1);
   __syncthreads();
-  for (int b = threadIdx.x; b < B; b += kPlanThreads) plan[d.scratch + static_cast<int64_t>(blockIdx.x) * B + b] = hist[b];
 }
 
-// exclusive prefix sums of n <= 2 * 1024 values in LDS, v[n] the total (n + 1 <= 2048 + 1 entries); every thread calls
-__device__ void scan(int32_t* v, int n, int32_t* wsum) {
+// From cnt: the buckets' first pairs (offs) and first tiles of each kind (tiles), exclusive prefix sums with the total
+// behind; two buckets a thread, all five sums in one pass.
+__device__ void plan_prefix(PlanShared& sh, int B) {
+  constexpr int A = kPlanTileKinds + 1;
   const int i = 2 * threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int x = i < n ? v[i] : 0, y = i + 1 < n ? v[i + 1] : 0;
-  int s = x + y;
+  const int c0 = i < B ? sh.cnt[i] : 0, c1 = i + 1 < B ? sh.cnt[i + 1] : 0;
+  int x[A], s[A];
+#pragma unroll
+  for (int k = 0; k < A; ++k) {
+    const int T = k < kPlanTileKinds ? kPlanTiles[k] : 1;
+    x[k] = (c0 + T - 1) / T;
+    s[k] = x[k] + (c1 + T - 1) / T;
+  }
+  int incl[A];
+#pragma unroll
+  for (int k = 0; k < A; ++k) incl[k] = s[k];
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(s, o);
-    if (lane >= o) s += u;
-  }
-  if (lane == 63) wsum[wave] = s;
-  __syncthreads();
-  int before = 0, all = 0;
 #pragma unroll
-  for (int k = 0; k < kPlanThreads / 64; ++k) {
-    if (k < wave) before += wsum[k];
-    all += wsum[k];
+    for (int k = 0; k < A; ++k) {
+      const int u = __shfl_up(incl[k], o);
+      if (lane >= o) incl[k] += u;
+    }
   }
-  const int ex = before + s - x - y;
-  if (i < n) v[i] = ex;
-  if (i + 1 < n) v[i + 1] = ex + x;
-  if (threadIdx.x == 0) v[n] = all;
+  if (lane == 63)
+#pragma unroll
+    for (int k = 0; k < A; ++k) sh.wsum[k][wave] = incl[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < A; ++k) {
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 64; ++w) {
+      if (w < wave) before += sh.wsum[k][w];
+      all += sh.wsum[k][w];
+    }
+    const int ex = before + incl[k] - s[k];
+    int32_t* out = k < kPlanTileKinds ? sh.tiles[k] : sh.offs;
+    if (i < B) out[i] = ex;
+    if (i + 1 < B) out[i + 1] = ex + x[k];
+    if (threadIdx.x == 0) out[B] = all;
+  }
   __syncthreads();
 }
 
-__global__ __launch_bounds__(kPlanThreads) void k_plan_scan(PlanDesc d, int32_t* plan, int blocks) {
-  __shared__ int32_t offs[kMaxBuckets + 1], cnt[kMaxBuckets], tiles[kMaxBuckets + 1], wsum[kPlanThreads / 64];
+// The tiles' lists, entries first, first + step, .. of each kind.
+__device__ void plan_tiles(const PlanShared& sh, const PlanDesc& d, int32_t* plan, int64_t first, int64_t step) {
   const int B = static_cast<int>(d.E) + 2;
-  for (int b = threadIdx.x; b < B; b += kPlanThreads) {
-    int32_t* h = plan + d.scratch + b;
-    int n = 0;
-    for (int k = 0; k < blocks; ++k) {
-      const int c = h[static_cast<int64_t>(k) * B];
-      h[static_cast<int64_t>(k) * B] = n;
-      n += c;
-    }
-    cnt[b] = n;
-    offs[b] = n;
-    plan[d.counts + b] = n;
-  }
-  __syncthreads();
-  scan(offs, B, wsum);
-  for (int b = threadIdx.x; b <= B; b += kPlanThreads) plan[d.offsets + b] = offs[b];
+#pragma unroll
   for (int t = 0; t < kPlanTileKinds; ++t) {
-    const int T = kPlanTiles[t];
-    for (int b = threadIdx.x; b < B; b += kPlanThreads) tiles[b] = (cnt[b] + T - 1) / T;
-    __syncthreads();
-    scan(tiles, B, wsum);
-    if (t == kPlanTileKinds - 1)
-      for (int b = threadIdx.x; b <= B; b += kPlanThreads) plan[d.tile128 + b] = tiles[b];
-    const int total = tiles[B];
-    for (int64_t i = threadIdx.x; i < d.cap[t]; i += kPlanThreads) {
+    for (int64_t i = first; i < d.cap[t]; i += step) {
       int32_t* m = plan + d.map[t] + 3 * i;
-      if (i >= total) {
+      if (i >= sh.tiles[t][B]) {
         m[0] = -1;
         m[1] = 0;
         m[2] = 0;
         continue;
       }
-      int lo = 0, hi = B - 1;  // the last bucket whose first tile is at or before i and that has tiles
+      int lo = 0, hi = B - 1;  // the last bucket whose first tile is at or before i: the one that has it
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (tiles[mid] <= i) lo = mid;
+        if (sh.tiles[t][mid] <= i) lo = mid;
         else hi = mid - 1;
       }
       m[0] = lo;
-      m[1] = offs[lo] + (static_cast<int>(i) - tiles[lo]) * T;
-      m[2] = offs[lo + 1];
+      m[1] = sh.offs[lo] + (static_cast<int>(i) - sh.tiles[t][lo]) * kPlanTiles[t];
+      m[2] = sh.offs[lo + 1];
     }
-    __syncthreads();
   }
 }
 
-// Pairs to their places, in order inside a bucket: base of the workgroup's chunk, then the waves in order, then lanes.
-__global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t* ids, PlanDesc d, int32_t* plan) {
-  __shared__ int32_t base[kMaxBuckets];
-  __shared__ uint16_t in_wave[kPlanThreads / 64][kMaxBuckets];
-  const int E = static_cast<int>(d.E), B = E + 2, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int b = threadIdx.x; b < B; b += kPlanThreads) {
-    base[b] = plan[d.offsets + b] + plan[d.scratch + static_cast<int64_t>(blockIdx.x) * B + b];
+// Pairs p0 .. p1 - 1 to their places, in order inside a bucket: base, then the waves in order, then lanes.
+__device__ void plan_scatter(const int32_t* ids, int64_t p0, int64_t p1, int E, int32_t* order, PlanShared& sh) {
+  const int B = E + 2, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int b = threadIdx.x; b < B; b += kPlanThreads)
 #pragma unroll
-    for (int w = 0; w < kPlanThreads / 64; ++w) in_wave[w][b] = 0;
-  }
+    for (int w = 0; w < kPlanThreads / 64; ++w) sh.in_wave[w][b] = 0;
   __syncthreads();
-  const int64_t chunk = plan_chunk(d.pairs), p0 = blockIdx.x * chunk, p1 = std::min(p0 + chunk, d.pairs);
   for (int64_t q = p0; q < p1; q += kPlanThreads) {
     const int64_t p = q + threadIdx.x;
     const bool here = p < p1;
@@ -427,25 +537,105 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t* id
       same &= (b >> i) & 1 ? set : ~set;
     }
     const int rank = __popcll(same & ((1ull << lane) - 1));
-    if (here && rank == 0) in_wave[wave][b] = static_cast<uint16_t>(__popcll(same));
+    if (here && rank == 0) sh.in_wave[wave][b] = static_cast<uint16_t>(__popcll(same));
     __syncthreads();
     if (here) {
-      int at = base[b] + rank;
-      for (int w = 0; w < wave; ++w) at += in_wave[w][b];
-      plan[d.order + at] = static_cast<int32_t>(p);
+      int at = sh.base[b] + rank;
+      for (int w = 0; w < wave; ++w) at += sh.in_wave[w][b];
+      order[at] = static_cast<int32_t>(p);
     }
+    if (q + kPlanThreads >= p1) break;
     __syncthreads();
     for (int i = threadIdx.x; i < B; i += kPlanThreads) {
       int n = 0;
 #pragma unroll
       for (int w = 0; w < kPlanThreads / 64; ++w) {
-        n += in_wave[w][i];
-        in_wave[w][i] = 0;
+        n += sh.in_wave[w][i];
+        sh.in_wave[w][i] = 0;
       }
-      base[i] += n;
+      sh.base[i] += n;
     }
     __syncthreads();
   }
+}
+
+// Up to kPlanOneBlock pairs: everything in one workgroup.
+__global__ __launch_bounds__(kPlanThreads) void k_plan_small(const int32_t* ids, PlanDesc d, int32_t* plan) {
+  __shared__ PlanShared sh;
+  const int E = static_cast<int>(d.E), B = E + 2;
+  plan_count(ids, 0, d.pairs, E, sh.cnt);
+  plan_prefix(sh, B);
+  for (int b = threadIdx.x; b <= B; b += kPlanThreads) {
+    if (b < B) {
+      plan[d.counts + b] = sh.cnt[b];
+      sh.base[b] = sh.offs[b];
+    }
+    plan[d.offsets + b] = sh.offs[b];
+    plan[d.tile128 + b] = sh.tiles[kPlanTileKinds - 1][b];
+  }
+  plan_tiles(sh, d, plan, threadIdx.x, kPlanThreads);
+  plan_scatter(ids, 0, d.pairs, E, plan + d.order, sh);
+}
+
+// More: counts per chunk; their prefixes, by one workgroup; places and lists.
+__global__ __launch_bounds__(kPlanThreads) void k_plan_count(const int32_t* ids, PlanDesc d, int32_t* plan) {
+  __shared__ int32_t hist[kMaxBuckets];
+  const int E = static_cast<int>(d.E), B = E + 2;
+  const int64_t chunk = plan_chunk(d.pairs), p0 = blockIdx.x * chunk;
+  plan_count(ids, p0, std::min(p0 + chunk, d.pairs), E, hist);
+  for (int b = threadIdx.x; b < B; b += kPlanThreads) plan[d.scratch + static_cast<int64_t>(blockIdx.x) * B + b] = hist[b];
+}
+
+// Turns the chunks' counts into their exclusive prefixes, bucket by bucket.  Threads (segment, bucket) hold runs of the
+// chunks; the loads of a run do not wait for each other.
+__global__ __launch_bounds__(kPlanThreads) void k_plan_scan(PlanDesc d, int32_t* plan, int blocks) {
+  __shared__ PlanShared sh;
+  const int B = static_cast<int>(d.E) + 2, wide = std::min(B, kPlanThreads);
+  const int segs = std::max(1, kPlanThreads / B), per = (blocks + segs - 1) / segs;
+  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+    const int b = b0 + static_cast<int>(threadIdx.x) % wide, seg = threadIdx.x / wide;
+    const bool mine = b < B && seg < segs;
+    const int k0 = seg * per, k1 = std::min(blocks, k0 + per);
+    int32_t* h = plan + d.scratch + b;
+    int n = 0;
+    if (mine)
+#pragma unroll 8
+      for (int k = k0; k < k1; ++k) n += h[static_cast<int64_t>(k) * B];
+    sh.part[threadIdx.x] = n;
+    __syncthreads();
+    if (mine) {
+      int before = 0;
+      for (int s = 0; s < seg; ++s) before += sh.part[s * wide + static_cast<int>(threadIdx.x) % wide];
+      if (seg == segs - 1) sh.cnt[b] = plan[d.counts + b] = before + n;
+#pragma unroll 8
+      for (int k = k0; k < k1; ++k) {
+        const int c = h[static_cast<int64_t>(k) * B];
+        h[static_cast<int64_t>(k) * B] = before;
+        before += c;
+      }
+    }
+    __syncthreads();
+  }
+  plan_prefix(sh, B);
+  for (int b = threadIdx.x; b <= B; b += kPlanThreads) {
+    plan[d.offsets + b] = sh.offs[b];
+    plan[d.tile128 + b] = sh.tiles[kPlanTileKinds - 1][b];
+  }
+}
+
+__global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t* ids, PlanDesc d, int32_t* plan) {
+  __shared__ PlanShared sh;
+  const int E = static_cast<int>(d.E), B = E + 2;
+  for (int b = threadIdx.x; b < B; b += kPlanThreads) {
+    sh.cnt[b] = plan[d.counts + b];
+    sh.base[b] = plan[d.offsets + b] + plan[d.scratch + static_cast<int64_t>(blockIdx.x) * B + b];
+  }
+  __syncthreads();
+  plan_prefix(sh, B);
+  plan_tiles(sh, d, plan, static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x,
+             static_cast<int64_t>(gridDim.x) * kPlanThreads);
+  const int64_t chunk = plan_chunk(d.pairs), p0 = blockIdx.x * chunk;
+  plan_scatter(ids, p0, std::min(p0 + chunk, d.pairs), E, plan + d.order, sh);
 }
 
 // ---- weighted sum of the slots ------------------------------------------------------------------
@@ -519,27 +709,36 @@ int lanes_values(int64_t E) {
 }
 
 // workgroups of the router: each leaves one partial
-int route_blocks(int64_t N) { return static_cast<int>(std::min<int64_t>((N + kRouteTeams - 1) / kRouteTeams, 256)); }
+int route_blocks(int64_t N, int64_t E) {
+  const int teams = route_threads(lanes_values(E)) / 16;
+  return N <= kRouteOneBlock ? 1 : static_cast<int>(std::min<int64_t>((N + teams - 1) / teams, 256));
+}
 
 template <int LT, int V>
 hipError_t launch_v(const RouteArgs& a, hipStream_t st) {
-  const int nb = route_blocks(a.N);
+  if (a.N == 0) {
+    k_route_none<<<1, 1024, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  const int nb = route_blocks(a.N, a.E);
   float* part = static_cast<float*>(a.ws);
   int32_t* part_n = reinterpret_cast<int32_t*>(part + static_cast<int64_t>(nb) * a.E);
-  const size_t lds = (a.E + 1) * 4 + static_cast<size_t>(kRouteTeams / 4) * 16 * V * 4;
-  if (nb > 0) {
-    k_route<LT, V><<<nb, kRouteThreads, lds, st>>>(a, part, part_n);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  k_route_sum<<<1, 1024, 0, st>>>(part, part_n, nb, a);
+  constexpr int kThreads = route_threads(V);
+  const size_t lds = (a.E + 1) * 4 + static_cast<size_t>(kThreads / 64) * 16 * V * 4;
+  if (a.S <= 16) k_route<LT, V, 1><<<nb, kThreads, lds, st>>>(a, part, part_n);
+  else k_route<LT, V, 4><<<nb, kThreads, lds, st>>>(a, part, part_n);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || nb == 1) return e;
+  k_route_sum<<<(a.E + kSumCols) / kSumCols, kSumCols * kSumSegs, 0, st>>>(part, part_n, nb, a,
+                                                                          part_n + static_cast<int64_t>(nb) * (a.E + 1));
   return hipGetLastError();
 }
 
 template <int LT, int V>
 hipError_t launch_v(const RouteBackwardArgs& a, hipStream_t st) {
-  const int nb = static_cast<int>(std::min<int64_t>((a.N + kRouteTeams - 1) / kRouteTeams, 2048));
-  k_route_backward<LT, V><<<nb, kRouteThreads, 0, st>>>(a);
+  const int nb = static_cast<int>(std::min<int64_t>((a.N + 15) / 16, 2048));
+  if (a.S <= 16) k_route_backward<LT, V, 1><<<nb, 256, 0, st>>>(a);
+  else k_route_backward<LT, V, 4><<<nb, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -623,22 +822,24 @@ PlanDesc plan_desc(int64_t pairs, int64_t E) {
 
 hipError_t launch_route_plan(const int32_t* ids, int64_t pairs, int64_t E, int32_t* plan, hipStream_t st) {
   const PlanDesc d = plan_desc(pairs, E);
-  const int blocks = pairs > 0 ? static_cast<int>((pairs + plan_chunk(pairs) - 1) / plan_chunk(pairs)) : 0;
-  hipError_t e = hipSuccess;
-  if (pairs > 0) {
-    k_plan_count<<<blocks, kPlanThreads, 0, st>>>(ids, d, plan);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  if (pairs <= kPlanOneBlock) {
+    k_plan_small<<<1, kPlanThreads, 0, st>>>(ids, d, plan);
+    return hipGetLastError();
   }
+  const int blocks = static_cast<int>((pairs + plan_chunk(pairs) - 1) / plan_chunk(pairs));
+  k_plan_count<<<blocks, kPlanThreads, 0, st>>>(ids, d, plan);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   k_plan_scan<<<1, kPlanThreads, 0, st>>>(d, plan, blocks);
   e = hipGetLastError();
-  if (e != hipSuccess || pairs == 0) return e;
+  if (e != hipSuccess) return e;
   k_plan_scatter<<<blocks, kPlanThreads, 0, st>>>(ids, d, plan);
   return hipGetLastError();
 }
 
 size_t route_workspace_bytes(int64_t N, int64_t E) {
-  return N > 0 ? static_cast<size_t>(route_blocks(N)) * static_cast<size_t>(2 * E + 1) * 4 : 0;
+  const int nb = N > 0 ? route_blocks(N, E) : 0;
+  return nb > 1 ? static_cast<size_t>(nb) * static_cast<size_t>(2 * E + 1) * 4 + 4 : 0;
 }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t st) { return dispatch(a, st); }
