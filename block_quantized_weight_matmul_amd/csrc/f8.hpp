@@ -34,7 +34,8 @@ constexpr int kPlanTileKinds = 4;
 constexpr int kPlanTiles[kPlanTileKinds] = {16, 32, 64, 128};
 struct PlanDesc {
   int64_t pairs, E;
-  int64_t counts, offsets, tile128, order, map[kPlanTileKinds], scratch, total;  // int32 offsets in the buffer
+  // int32 offsets in the buffer; totals: tiles of each kind
+  int64_t counts, offsets, tile128, totals, order, map[kPlanTileKinds], scratch, total;
   int64_t cap[kPlanTileKinds];                                                    // entries of each map
 };
 PlanDesc plan_desc(int64_t pairs, int64_t E);

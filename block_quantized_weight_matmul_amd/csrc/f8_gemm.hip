@@ -40,58 +40,76 @@ struct GemmArgs {
 };
 
 // One workgroup: TM rows x TN tokens, its waves in a WM x WN grid; K in stages of one group, two stages in LDS.
-// A stage's rows are 128 bytes; their eight 16-byte pieces are stored xored with the row's low bits, so that the 8
-// lanes of a read phase (8 rows, one piece) use every bank once.
+// A stage's rows are 128 bytes, two to the 64 banks; their eight 16-byte pieces are stored xored with bits 1..3 of the
+// row, so that 16 lanes that read one piece of 16 rows use every bank once (xored with bits 0..2, the reads took twice
+// the cycles, and a 256 x 256 stage 4190 instead of 3570).
+//
+// The second bound, waves per SIMD, keeps the compiler at 256 registers: above, it puts the sums of the matrix cores into
+// the accumulation registers, which the vector units cannot read.
 template <int TM, int TN, int WM, int WN, int MODE, int OT>
-__global__ __launch_bounds__(64 * WM * WN) void k_f8_gemm(GemmArgs a) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
   constexpr int NT = 64 * WM * WN, RT = TM / WM / 32, CT = TN / WN / 32;
   constexpr int AI = TM * 8 / NT, BI = TN * 8 / NT;  // 16-byte pieces a thread stages
   static_assert(AI * NT == TM * 8 && BI * NT == TN * 8, "tile");
-  constexpr bool kRowScale = MODE == MODE_WGRAD;
+  constexpr bool kRowScale = MODE == MODE_WGRAD, kId = MODE == MODE_ID;
   constexpr int W = WM * WN;
   constexpr int TS = TN < 64 ? 64 : TN;                // room of the token scales: whole loads of 64
   constexpr int kScales = TS + (kRowScale ? TM : 64);  // then the rows' or the row blocks'
   constexpr int kUnitsPer = (kScales / 64 + W - 1) / W;  // loads of 64 scales a wave; those past the last repeat it
   constexpr int kStage = (TM + TN) * 128 + kUnitsPer * W * 256;
-  __shared__ __align__(128) uint8_t lds[2][kStage];
+  constexpr int kRows = RT * 32, kPitch = kRows * static_cast<int>(sizeof(typename Elem<OT>::T)) + 16;  // of a wave's outputs
+  // The two stages, and after the loop the waves' outputs.  One array: with a second one the compiler waits for a stage's
+  // loads before any read of the other stage (51 -> 43 us for 8 experts of 2048 x 2560 and 4096 pairs).
+  __shared__ __align__(128) uint8_t lds[2 * kStage];
   typedef typename Elem<OT>::T T;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WM, wn = wave / WM;
-  int64_t bid = blockIdx.x;
-  int tm;
+  // Tile indices, kept in scalar registers: divisions leave them in vector registers, and every staging load would then
+  // loop over the lanes' copies of its descriptor.
+  auto scalar = [](unsigned v) { return static_cast<unsigned>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))); };
+  unsigned bid = blockIdx.x, tm;
   if constexpr (MODE == MODE_DENSE) {
     // Workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles, kGroup row tiles by all token tiles after
     // another, so that the tiles it works on share their operands in its L2.
-    constexpr int kXcds = 8, kGroup = 1024 / TM;
-    const int64_t n = gridDim.x, per = n / kXcds, more = n % kXcds, x = bid % kXcds;
+    constexpr unsigned kXcds = 8, kGroup = 1024 / TM;
+    const unsigned n = gridDim.x, per = n / kXcds, more = n % kXcds, x = bid % kXcds;
     bid = x * per + std::min(x, more) + bid / kXcds;
-    const int64_t in = static_cast<int64_t>(kGroup) * a.tiles_n, gm = bid / in * kGroup;
-    const int64_t wide = std::min<int64_t>(kGroup, a.tiles_m - gm), off = bid % in;
-    tm = static_cast<int>(gm + off % wide);
-    bid = off / wide;
+    const unsigned in = kGroup * static_cast<unsigned>(a.tiles_n), gm = scalar(bid / in) * kGroup, off = bid - gm / kGroup * in;
+    const unsigned wide = std::min(kGroup, static_cast<unsigned>(a.tiles_m) - gm);
+    bid = scalar(off / wide);
+    tm = gm + off - bid * wide;
+  } else if constexpr (kId) {
+    // An XCD takes a run of the listed tiles: the token tiles of an expert share its weights in one L2.
+    const unsigned rows = static_cast<unsigned>(a.tiles_m);
+    const unsigned n = scalar(static_cast<unsigned>(a.plan[a.pd.totals + a.map])) * rows, per = (n + 7) / 8, k = bid / 8;
+    bid = bid % 8 * per + k;
+    if (k >= per || bid >= n) return;
+    const unsigned tile = scalar(bid / rows);
+    tm = bid - tile * rows;
+    bid = tile;
   } else {
-    tm = static_cast<int>(bid % a.tiles_m);
-    bid /= a.tiles_m;
+    const unsigned rest = scalar(bid / static_cast<unsigned>(a.tiles_m));
+    tm = bid - rest * static_cast<unsigned>(a.tiles_m);
+    bid = rest;
   }
   const int64_t r0 = static_cast<int64_t>(tm) * TM;
-  int64_t M = a.M, N = a.N;
+  const int64_t M = a.M, N = a.N;
   const uint8_t* w = a.w;
   const float* wsc = a.ws;
   T* y = static_cast<T*>(a.y);
   int g0 = 0, g1 = a.G;
   int64_t t0;
   int first = 0, count = 0;  // MODE_ID: the tile's pairs
-  if constexpr (MODE == MODE_ID) {
-    const int32_t* mp = a.plan + a.pd.map[a.map] + 3 * bid;
-    const int bucket = mp[0];
-    first = mp[1];
-    count = mp[2] - first;
-    if (bucket < 0) return;
+  if constexpr (kId) {
+    const int32_t* mp = a.plan + a.pd.map[a.map] + 3 * static_cast<int64_t>(bid);
+    const int bucket = static_cast<int>(scalar(static_cast<unsigned>(mp[0])));
+    first = static_cast<int>(scalar(static_cast<unsigned>(mp[1])));
+    count = static_cast<int>(scalar(static_cast<unsigned>(mp[2]))) - first;
     count = count < TN ? count : TN;
     if (bucket >= a.pd.E) {  // empty slots: zeros; ids that name no expert: NaN
       const float v = bucket == a.pd.E ? 0.0f : __uint_as_float(0x7FC00000u);
-      const int rows = static_cast<int>(M - r0 < TM ? M - r0 : TM);
+      const int rows = static_cast<int>(std::min<int64_t>(M - r0, TM));
       for (int i = tid; i < count * rows; i += NT)
         y[static_cast<int64_t>(a.plan[a.pd.order + first + i / rows]) * M + r0 + i % rows] = to_elem<OT>(v);
       return;
@@ -100,29 +118,32 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_gemm(GemmArgs a) {
     wsc += static_cast<int64_t>(bucket) * ((M + 127) / 128) * a.G;
     t0 = 0;
   } else if constexpr (MODE == MODE_WGRAD) {
-    t0 = (bid % a.tiles_n) * TN;
+    const unsigned e = scalar(bid / static_cast<unsigned>(a.tiles_n));
+    t0 = static_cast<int64_t>(bid - e * static_cast<unsigned>(a.tiles_n)) * TN;
     if (a.plan) {
-      const int64_t e = bid / a.tiles_n;
-      g0 = a.plan[a.pd.tile128 + e];
-      g1 = a.plan[a.pd.tile128 + e + 1];
-      y += e * M * N;
+      g0 = static_cast<int>(scalar(static_cast<unsigned>(a.plan[a.pd.tile128 + e])));
+      g1 = static_cast<int>(scalar(static_cast<unsigned>(a.plan[a.pd.tile128 + e + 1])));
+      y += static_cast<int64_t>(e) * M * N;
     }
   } else {
-    t0 = bid * TN;
+    t0 = static_cast<int64_t>(bid) * TN;
   }
 
   // What this thread stages: 16-byte pieces, offsets from the tile's first row (rows past the end repeat the last), and
   // scales, 64 to a wave's load.
-  const int64_t last_m = M - 1 - r0;
-  const __amdgpu_buffer_rsrc_t rw = rsrc(w + r0 * a.pitch, static_cast<uint32_t>(std::min<int64_t>(TM, M - r0) * a.pitch));
   const __amdgpu_buffer_rsrc_t rx =
-      MODE == MODE_ID ? rsrc(a.x, static_cast<uint32_t>(N * a.pitch))
+      kId ? rsrc(a.x, static_cast<uint32_t>(N * a.pitch))
                       : rsrc(a.x + t0 * a.pitch, static_cast<uint32_t>(std::min<int64_t>(TN, N - t0) * a.pitch));
   auto token = [&](int i) -> int64_t {  // tile row i: its row of x, from t0
-    if constexpr (MODE == MODE_ID) return a.plan[a.pd.order + first + (i < count ? i : count - 1)] / a.slots;
+    if constexpr (kId) return a.plan[a.pd.order + first + (i < count ? i : count - 1)] / a.slots;
     else return i < N - 1 - t0 ? i : N - 1 - t0;
   };
   uint32_t aoff[AI], boff[BI], soff[kUnitsPer];
+  const float* sbase[kUnitsPer];
+  int64_t sstep[kUnitsPer];
+  uint32_t sbytes[kUnitsPer];
+  const int64_t last_m = M - 1 - r0;
+  const __amdgpu_buffer_rsrc_t rw = rsrc(w + r0 * a.pitch, static_cast<uint32_t>(std::min<int64_t>(TM, M - r0) * a.pitch));
 #pragma unroll
   for (int i = 0; i < AI; ++i) {
     const int p = i * NT + tid, row = p >> 3;
@@ -133,14 +154,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_gemm(GemmArgs a) {
     const int p = i * NT + tid, row = p >> 3;
     boff[i] = static_cast<uint32_t>(token(row) * a.pitch) + 16 * ((p ^ (row >> 1)) & 7);
   }
-  const float* sbase[kUnitsPer];
-  int64_t sstep[kUnitsPer];
-  uint32_t sbytes[kUnitsPer];
 #pragma unroll
   for (int k = 0; k < kUnitsPer; ++k) {
     const int u = k * W + wave, i = std::min(u * 64 + lane, kScales - 1);
     const bool tokens = u * 64 < TS;  // the same for a whole wave
-    if (i < TS) soff[k] = 4 * static_cast<uint32_t>(t0 + token(std::min(i, TN - 1)));
+    if (tokens) soff[k] = 4 * static_cast<uint32_t>(t0 + token(std::min(i, TN - 1)));
     else if (kRowScale) soff[k] = 4 * static_cast<uint32_t>(r0 + (i - TS < last_m ? i - TS : last_m));
     else soff[k] = 4 * static_cast<uint32_t>(std::min<int64_t>(i - TS, (M - 1) / 128 - r0 / 128) * a.G);
     sbase[k] = tokens ? a.xs : kRowScale ? wsc : wsc + r0 / 128 * a.G;
@@ -149,8 +167,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_gemm(GemmArgs a) {
     sbytes[k] = tokens || kRowScale ? 0u : static_cast<uint32_t>(((M + 127) / 128 - r0 / 128) * a.G * 4);
   }
 
+  // a descriptor in scalar registers, whichever its parts are in
+  auto uniform = [&](const void* p, uint32_t bytes) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint64_t u = static_cast<uint64_t>(scalar(static_cast<unsigned>(v >> 32))) << 32 | scalar(static_cast<unsigned>(v));
+    return rsrc(reinterpret_cast<const void*>(u), scalar(bytes));
+  };
   auto stage = [&](int buf, int g) {
-    uint8_t* d = lds[buf];
+    uint8_t* d = lds + buf * kStage;
     const uint32_t ks = static_cast<uint32_t>(g) * 128u;
 #pragma unroll
     for (int i = 0; i < AI; ++i) load_lds16(rw, d + (i * NT + wave * 64) * 16, aoff[i], ks);
@@ -158,7 +182,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_gemm(GemmArgs a) {
     for (int i = 0; i < BI; ++i) load_lds16(rx, d + TM * 128 + (i * NT + wave * 64) * 16, boff[i], ks);
 #pragma unroll
     for (int k = 0; k < kUnitsPer; ++k)
-      load_lds4(rsrc(sbase[k] + g * sstep[k], sbytes[k] ? sbytes[k] - 4 * g : static_cast<uint32_t>(sstep[k]) * 4),
+      load_lds4(uniform(sbase[k] + g * sstep[k], sbytes[k] ? sbytes[k] - 4 * g : static_cast<uint32_t>(sstep[k]) * 4),
                 d + (TM + TN) * 128 + (k * W + wave) * 256, soff[k], 0);
   };
 
@@ -183,9 +207,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_gemm(GemmArgs a) {
     for (int m = 0; m < 2; ++m)
       f.set(m, *reinterpret_cast<const i32x4*>(p + piece[m][0]), *reinterpret_cast<const i32x4*>(p + piece[m][1]));
   };
-  const uint8_t* Abase = lds[0] + wm * (TM / WM) * 128;
-  const uint8_t* Bbase = lds[0] + (TM + wn * (TN / WN)) * 128;
-  const float* Sbase = reinterpret_cast<const float*>(lds[0] + (TM + TN) * 128);
+  const uint8_t* Abase = lds + wm * (TM / WM) * 128;
+  const uint8_t* Bbase = lds + (TM + wn * (TN / WN)) * 128;
+  const float* Sbase = reinterpret_cast<const float*>(lds + (TM + TN) * 128);
   F b[CT];
   float sc[CT];
   auto read_b = [&](int buf) {
@@ -209,6 +233,70 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_gemm(GemmArgs a) {
     for (int e = 0; e < 16; ++e) to[e] = fmaf(p[e], kRowScale ? s * rs[e / 4][e % 4] : s, to[e]);
   };
 
+  // Outputs leave through LDS, 32 tokens of the wave's rows at a time: a lane holds 4 rows of one token, and stores
+  // straight from there would be 16 bytes a token (10 us of the 60 at 4096 x 4096 outputs).
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  static_assert(W * 32 * kPitch <= 2 * kStage, "the waves' regions fit the stages");
+  uint8_t* mine = lds + wave * (32 * kPitch);
+  constexpr int kLanes = kRows / kVec;             // lanes that store one token's rows
+  constexpr int kStores = 32 * kLanes / 64;        // stores of a lane for 32 tokens
+  // MODE_ID: the output rows of this lane's tokens, looked up before the loop (a lookup in it waits for the stage's loads)
+  int32_t orow[kId ? CT * kStores : 1];
+  if constexpr (kId) {
+#pragma unroll
+    for (int j = 0; j < CT; ++j)
+#pragma unroll
+      for (int n = 0; n < kStores; ++n) {
+        const int t = wn * (TN / WN) + j * 32 + n * (64 / kLanes) + lane / kLanes;
+        orow[j * kStores + n] = a.plan[a.pd.order + first + std::min(t, count - 1)];
+      }
+  }
+  auto store = [&]() {
+    const int64_t rw0 = r0 + wm * kRows;
+    const int rows = static_cast<int>(std::min<int64_t>(kRows, M - rw0));  // may be negative
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+      const int tj = wn * (TN / WN) + j * 32;
+      int tokens = kId ? count - tj : static_cast<int>(std::min<int64_t>(32, N - t0 - tj));
+      tokens = std::min(tokens, 32);
+      auto out = [&](int t) -> T* {
+        if constexpr (kId) return y + static_cast<int64_t>(a.plan[a.pd.order + first + tj + t]) * M + rw0;
+        else return y + (t0 + tj + t) * M + rw0;
+      };
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          typedef T T4 __attribute__((ext_vector_type(4)));
+          T4 o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = to_elem<OT>(acc[i][j][4 * k + e]);
+          *reinterpret_cast<T4*>(mine + row * kPitch + (i * 32 + k * 8 + half * 4) * sizeof(T)) = o;
+        }
+      __builtin_amdgcn_wave_barrier();
+      if (a.vec) {  // M is a multiple of kVec and rows are 16-byte aligned
+        // every read before any store: a read of LDS waits for the memory operations before it
+        const int c = lane % kLanes * kVec;
+        uint4 v[kStores];
+#pragma unroll
+        for (int n = 0; n < kStores; ++n)
+          v[n] = *reinterpret_cast<const uint4*>(mine + (n * (64 / kLanes) + lane / kLanes) * kPitch + c * sizeof(T));
+#pragma unroll
+        for (int n = 0; n < kStores; ++n) {
+          const int t = n * (64 / kLanes) + lane / kLanes;
+          T* o = kId ? y + static_cast<int64_t>(orow[kId ? j * kStores + n : 0]) * M + rw0 : out(t);
+          if (t < tokens && c < rows) *reinterpret_cast<uint4*>(o + c) = v[n];
+        }
+      } else {
+        for (int n = lane; n < 32 * kRows; n += 64) {
+          const int t = n / kRows, c = n % kRows;
+          if (t < tokens && c < rows) out(t)[c] = *reinterpret_cast<const T*>(mine + t * kPitch + c * sizeof(T));
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  };
+
   if (g0 < g1) stage(0, g0);
   for (int g = g0; g < g1; ++g) {
     const int buf = (g - g0) & 1;
@@ -226,51 +314,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_gemm(GemmArgs a) {
       for (int j = 0; j < CT; ++j) add(acc[i][j], group_sum(av, b[j]), sc[j], rs);
     }
   }
-
-  // Outputs leave through LDS, 32 tokens of the wave's rows at a time: a lane holds 4 rows of one token, and stores
-  // straight from there would be 16 bytes a token (10 us of the 60 at 4096 x 4096 outputs).
-  constexpr int kRows = RT * 32, kPitch = kRows * static_cast<int>(sizeof(T)) + 16, kVec = 16 / static_cast<int>(sizeof(T));
-  static_assert(W * 32 * kPitch <= 2 * kStage, "the waves' regions fit the stages");
   __syncthreads();
-  uint8_t* mine = lds[0] + wave * (32 * kPitch);
-  const int64_t rw0 = r0 + wm * kRows;
-  const int rows = static_cast<int>(std::min<int64_t>(kRows, M - rw0));  // may be negative
-#pragma unroll
-  for (int j = 0; j < CT; ++j) {
-    const int tj = wn * (TN / WN) + j * 32;
-    int tokens = MODE == MODE_ID ? count - tj : static_cast<int>(std::min<int64_t>(32, N - t0 - tj));
-    tokens = std::min(tokens, 32);
-    auto out = [&](int t) -> T* {
-      if constexpr (MODE == MODE_ID) return y + static_cast<int64_t>(a.plan[a.pd.order + first + tj + t]) * M + rw0;
-      else return y + (t0 + tj + t) * M + rw0;
-    };
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        typedef T T4 __attribute__((ext_vector_type(4)));
-        T4 o;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = to_elem<OT>(acc[i][j][4 * k + e]);
-        *reinterpret_cast<T4*>(mine + row * kPitch + (i * 32 + k * 8 + half * 4) * sizeof(T)) = o;
-      }
-    __builtin_amdgcn_wave_barrier();
-    if (a.vec) {  // M is a multiple of kVec and rows are 16-byte aligned
-      constexpr int kLanes = kRows / kVec;  // lanes that store one token's rows
-#pragma unroll
-      for (int n = 0; n < 32 * kLanes / 64; ++n) {
-        const int t = n * (64 / kLanes) + lane / kLanes, c = lane % kLanes * kVec;
-        if (t < tokens && c < rows)
-          *reinterpret_cast<uint4*>(out(t) + c) = *reinterpret_cast<const uint4*>(mine + t * kPitch + c * sizeof(T));
-      }
-    } else {
-      for (int n = lane; n < 32 * kRows; n += 64) {
-        const int t = n / kRows, c = n % kRows;
-        if (t < tokens && c < rows) out(t)[c] = *reinterpret_cast<const T*>(mine + t * kPitch + c * sizeof(T));
-      }
-    }
-    __builtin_amdgcn_wave_barrier();
-  }
+  store();
 }
 
 template <int TM, int TN, int WM, int WN, int MODE>
@@ -278,7 +323,11 @@ hipError_t run_tile(const GemmArgs& a, int ot, int64_t blocks, hipStream_t st) {
   if (blocks > INT_MAX) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(64 * WM * WN);
   switch (ot) {
-    case DT_F32: k_f8_gemm<TM, TN, WM, WN, MODE, DT_F32><<<grid, block, 0, st>>>(a); break;
+    case DT_F32:
+      // (an fp32 output's operands are twice as wide in registers: no 256 x 256 tile)
+      if constexpr (TM * TN <= 128 * 128) k_f8_gemm<TM, TN, WM, WN, MODE, DT_F32><<<grid, block, 0, st>>>(a);
+      else return hipErrorInvalidValue;
+      break;
     case DT_F16: k_f8_gemm<TM, TN, WM, WN, MODE, DT_F16><<<grid, block, 0, st>>>(a); break;
     case DT_BF16: k_f8_gemm<TM, TN, WM, WN, MODE, DT_BF16><<<grid, block, 0, st>>>(a); break;
     default: return hipErrorInvalidValue;
@@ -304,9 +353,9 @@ enum { TILE_256 = 0, TILE_128 = 1, TILE_128_64 = 2, TILE_64 = 3, TILE_128_32 = 4
 constexpr TileKind kTiles[] = {
     {256, 256, 1, 5.0f, {1.95f}},
     {128, 128, 2, 2.0f, {0.85f, 1.21f}},
-    {128, 64, 3, 1.5f, {0.50f, 0.75f, 1.02f}},
+    {128, 64, 3, 1.5f, {0.52f, 0.79f, 1.07f}},
     {64, 64, 4, 1.0f, {0.33f, 0.48f, 0.75f, 0.99f}},
-    {128, 32, 4, 1.0f, {0.35f, 0.50f, 0.65f, 0.80f}},
+    {128, 32, 4, 1.5f, {0.50f, 0.80f, 1.10f, 1.40f}},  // experts only
 };
 
 // tiles: workgroups of a launch, of `stages` stages each
@@ -327,7 +376,6 @@ int best_tile(const int* kinds, int n, const double* tiles, double stages, int c
 // dense products: M rows, N tokens, `many` matrices
 template <int MODE>
 hipError_t run_dense(GemmArgs& a, int ot, int64_t many, double stages, int cus, hipStream_t st) {
-  // an fp32 output's operands are twice as wide in registers: no 256 x 256 tile
   const int kinds[] = {TILE_128, TILE_128_64, TILE_64, TILE_256};
   const int n = ot == DT_F32 ? 3 : 4;
   double tiles[4];
@@ -363,7 +411,7 @@ hipError_t run_experts(GemmArgs& a, int ot, int cus, hipStream_t st) {
   a.tiles_m = static_cast<int>((a.M + k.tm - 1) / k.tm);
   a.map = 0;
   while (kPlanTiles[a.map] != k.tn) ++a.map;
-  const int64_t blocks = static_cast<int64_t>(a.tiles_m) * a.pd.cap[a.map];
+  const int64_t blocks = static_cast<int64_t>(a.tiles_m) * a.pd.cap[a.map] + 7;  // a run of the listed ones for each XCD
   switch (kind) {
     case TILE_128: return run_tile<128, 128, 2, 2, MODE_ID>(a, ot, blocks, st);
     case TILE_128_64: return run_tile<128, 64, 2, 2, MODE_ID>(a, ot, blocks, st);

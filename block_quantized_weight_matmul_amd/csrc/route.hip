@@ -151,8 +151,7 @@ __device__ __forceinline__ float loss_part(int count, float psum, float T, int E
   return T > 0.0f ? static_cast<float>(count) * E / (S * T) * psum : 0.0f;
 }
 
-// part, part_n: the workgroups' sums over their rows, [E] and [E + 1] each, and behind part_n the counter of
-// k_route_sum.  A single workgroup writes the results itself.
+// part, part_n: the workgroups' sums over their rows, [E] and [E + 1] each.  A single workgroup writes the results itself.
 template <int LT, int V, int SR>
 __global__ __launch_bounds__(route_threads(V)) void k_route(RouteArgs a, float* part, int32_t* part_n) {
   constexpr int kRouteThreads = route_threads(V), kRouteTeams = kRouteThreads / 16;
@@ -250,25 +249,24 @@ __global__ __launch_bounds__(route_threads(V)) void k_route(RouteArgs a, float* 
     part[static_cast<int64_t>(blockIdx.x) * a.E + e] = s;
   }
   for (int i = threadIdx.x; i <= a.E; i += kRouteThreads) part_n[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + i] = sh[i];
-  if (blockIdx.x == 0 && threadIdx.x == 0) part_n[static_cast<int64_t>(gridDim.x) * (a.E + 1)] = 0;
 }
 
 constexpr int kSumCols = 32, kSumSegs = 32;
 
 // Adds the workgroups' partials: a workgroup takes 32 experts, a thread every 32nd partial of one, and the threads' sums
-// are added in order.  (One workgroup for all of them waited 17 us for 256 partials of 128 experts.)  The last workgroup
-// to finish, known by the counter, adds up the loss from the finished sums.
+// are added in order.  The loss, which needs all of them, is a launch of its own: one workgroup for everything waited 17
+// us for 256 partials of 128 experts, and a last workgroup that knows itself by a counter 14 us, most of it the fence
+// that makes the other dies' sums visible.  This way it is 3.4 us and 2.6.
 __global__ __launch_bounds__(kSumCols * kSumSegs) void k_route_sum(const float* part, const int32_t* part_n, int blocks,
-                                                                   RouteArgs a, int32_t* counter) {
-  __shared__ float sp[kSumSegs][kSumCols + 1], red[16];
+                                                                   int E, int32_t* counts, float* psum) {
+  __shared__ float sp[kSumSegs][kSumCols + 1];
   __shared__ int32_t sn[kSumSegs][kSumCols + 1];
-  __shared__ int last;
-  const int col = threadIdx.x % kSumCols, seg = threadIdx.x / kSumCols, e = blockIdx.x * kSumCols + col, E1 = a.E + 1;
+  const int col = threadIdx.x % kSumCols, seg = threadIdx.x / kSumCols, e = blockIdx.x * kSumCols + col, E1 = E + 1;
   float s = 0.0f;
   int n = 0;
 #pragma unroll 8
   for (int b = seg; b < blocks; b += kSumSegs) {
-    if (e < a.E) s += part[static_cast<int64_t>(b) * a.E + e];
+    if (e < E) s += part[static_cast<int64_t>(b) * E + e];
     if (e < E1) n += part_n[static_cast<int64_t>(b) * E1 + e];
   }
   sp[seg][col] = s;
@@ -279,23 +277,9 @@ __global__ __launch_bounds__(kSumCols * kSumSegs) void k_route_sum(const float* 
       s += sp[k][col];
       n += sn[k][col];
     }
-    a.counts[e] = n;
-    if (e < a.E) a.psum[e] = s;
+    counts[e] = n;
+    if (e < E) psum[e] = s;
   }
-  if (!a.loss) return;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(counter, 1) == static_cast<int>(gridDim.x) - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  const float T = static_cast<float>(__hip_atomic_load(a.counts + a.E, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-  float v = 0.0f;
-  for (int i = threadIdx.x; i < a.E; i += kSumCols * kSumSegs)
-    v += loss_part(__hip_atomic_load(a.counts + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
-                   __hip_atomic_load(a.psum + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), T, a.E, a.S);
-  v = block_sum(v, red, kSumCols * kSumSegs);
-  if (threadIdx.x == 0) *a.loss = T > 0.0f ? a.coef * v / T : 0.0f;
 }
 
 __global__ __launch_bounds__(1024) void k_route_none(RouteArgs a) {
@@ -493,31 +477,36 @@ __device__ void plan_prefix(PlanShared& sh, int B) {
   __syncthreads();
 }
 
-// The tiles' lists, entries first, first + step, .. of each kind.
-__device__ void plan_tiles(const PlanShared& sh, const PlanDesc& d, int32_t* plan, int64_t first, int64_t step) {
-  const int B = static_cast<int>(d.E) + 2;
+// The tiles' lists: a quarter of the workgroup's threads to each kind, the workgroups in turn.
+__device__ void plan_tiles(const PlanShared& sh, const PlanDesc& d, int32_t* plan) {
+  constexpr int kEach = kPlanThreads / kPlanTileKinds;
+  const int B = static_cast<int>(d.E) + 2, t = threadIdx.x / kEach, T = kPlanTiles[0] << t;
+  int64_t cap = 0, map = 0;
 #pragma unroll
-  for (int t = 0; t < kPlanTileKinds; ++t) {
-    for (int64_t i = first; i < d.cap[t]; i += step) {
-      int32_t* m = plan + d.map[t] + 3 * i;
-      if (i >= sh.tiles[t][B]) {
-        m[0] = -1;
-        m[1] = 0;
-        m[2] = 0;
-        continue;
-      }
-      int lo = 0, hi = B - 1;  // the last bucket whose first tile is at or before i: the one that has it
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (sh.tiles[t][mid] <= i) lo = mid;
-        else hi = mid - 1;
-      }
-      m[0] = lo;
-      m[1] = sh.offs[lo] + (static_cast<int>(i) - sh.tiles[t][lo]) * kPlanTiles[t];
-      m[2] = sh.offs[lo + 1];
+  for (int k = 0; k < kPlanTileKinds; ++k)
+    if (k == t) { cap = d.cap[k]; map = d.map[k]; }
+  const int32_t* tiles = sh.tiles[t];
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kEach + threadIdx.x % kEach; i < cap; i += static_cast<int64_t>(gridDim.x) * kEach) {
+    int32_t* m = plan + map + 3 * i;
+    if (i >= tiles[B]) {
+      m[0] = -1;
+      m[1] = 0;
+      m[2] = 0;
+      continue;
     }
+    int lo = 0, hi = B - 1;  // the last bucket whose first tile is at or before i: the one that has it
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tiles[mid] <= i) lo = mid;
+      else hi = mid - 1;
+    }
+    m[0] = lo;
+    m[1] = sh.offs[lo] + (static_cast<int>(i) - tiles[lo]) * T;
+    m[2] = sh.offs[lo + 1];
   }
 }
+static_assert(kPlanTiles[1] == 2 * kPlanTiles[0] && kPlanTiles[2] == 4 * kPlanTiles[0] && kPlanTiles[3] == 8 * kPlanTiles[0],
+              "each kind of tile is twice the one before");
 
 // Pairs p0 .. p1 - 1 to their places, in order inside a bucket: base, then the waves in order, then lanes.
 __device__ void plan_scatter(const int32_t* ids, int64_t p0, int64_t p1, int E, int32_t* order, PlanShared& sh) {
@@ -573,7 +562,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_small(const int32_t* ids,
     plan[d.offsets + b] = sh.offs[b];
     plan[d.tile128 + b] = sh.tiles[kPlanTileKinds - 1][b];
   }
-  plan_tiles(sh, d, plan, threadIdx.x, kPlanThreads);
+  if (threadIdx.x < kPlanTileKinds) plan[d.totals + threadIdx.x] = sh.tiles[threadIdx.x][B];
+  plan_tiles(sh, d, plan);
   plan_scatter(ids, 0, d.pairs, E, plan + d.order, sh);
 }
 
@@ -621,6 +611,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scan(PlanDesc d, int32_t*
     plan[d.offsets + b] = sh.offs[b];
     plan[d.tile128 + b] = sh.tiles[kPlanTileKinds - 1][b];
   }
+  if (threadIdx.x < kPlanTileKinds) plan[d.totals + threadIdx.x] = sh.tiles[threadIdx.x][B];
 }
 
 __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t* ids, PlanDesc d, int32_t* plan) {
@@ -632,8 +623,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t* id
   }
   __syncthreads();
   plan_prefix(sh, B);
-  plan_tiles(sh, d, plan, static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x,
-             static_cast<int64_t>(gridDim.x) * kPlanThreads);
+  plan_tiles(sh, d, plan);
   const int64_t chunk = plan_chunk(d.pairs), p0 = blockIdx.x * chunk;
   plan_scatter(ids, p0, std::min(p0 + chunk, d.pairs), E, plan + d.order, sh);
 }
@@ -729,9 +719,10 @@ hipError_t launch_v(const RouteArgs& a, hipStream_t st) {
   else k_route<LT, V, 4><<<nb, kThreads, lds, st>>>(a, part, part_n);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || nb == 1) return e;
-  k_route_sum<<<(a.E + kSumCols) / kSumCols, kSumCols * kSumSegs, 0, st>>>(part, part_n, nb, a,
-                                                                          part_n + static_cast<int64_t>(nb) * (a.E + 1));
-  return hipGetLastError();
+  k_route_sum<<<(a.E + kSumCols) / kSumCols, kSumCols * kSumSegs, 0, st>>>(part, part_n, nb, a.E, a.counts, a.psum);
+  const hipError_t es = hipGetLastError();
+  if (es != hipSuccess || !a.loss) return es;
+  return launch_balance_loss(a.counts, a.psum, a.E, a.S, a.coef, a.loss, st);
 }
 
 template <int LT, int V>
@@ -806,7 +797,8 @@ PlanDesc plan_desc(int64_t pairs, int64_t E) {
   d.counts = 0;
   d.offsets = d.counts + B;
   d.tile128 = d.offsets + B + 1;
-  d.order = d.tile128 + B + 1;
+  d.totals = d.tile128 + B + 1;
+  d.order = d.totals + kPlanTileKinds;
   int64_t at = d.order + pairs;
   for (int t = 0; t < kPlanTileKinds; ++t) {
     d.map[t] = at;
@@ -839,7 +831,7 @@ hipError_t launch_route_plan(const int32_t* ids, int64_t pairs, int64_t E, int32
 
 size_t route_workspace_bytes(int64_t N, int64_t E) {
   const int nb = N > 0 ? route_blocks(N, E) : 0;
-  return nb > 1 ? static_cast<size_t>(nb) * static_cast<size_t>(2 * E + 1) * 4 + 4 : 0;
+  return nb > 1 ? static_cast<size_t>(nb) * static_cast<size_t>(2 * E + 1) * 4 : 0;
 }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t st) { return dispatch(a, st); }
