@@ -36,6 +36,7 @@ struct GemmArgs {
   PlanDesc pd;
   int map;            // index of the token tile's map in the plan
   int slots;          // MODE_ID: pairs that share a token row
+  int share;          // groups of a workgroup where K is divided (gridDim.y > 1)
   int vec;            // 16 bytes of consecutive outputs may be stored at once
 };
 
@@ -46,7 +47,8 @@ struct GemmArgs {
 //
 // The second bound, waves per SIMD, keeps the compiler at 256 registers: above, it puts the sums of the matrix cores into
 // the accumulation registers, which the vector units cannot read.
-template <int TM, int TN, int WM, int WN, int MODE, int OT>
+// EXACT: the cores of an fp32 output (f8_mma.hpp); ST: the type stored.
+template <int TM, int TN, int WM, int WN, int MODE, bool EXACT, int ST>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
   constexpr int NT = 64 * WM * WN, RT = TM / WM / 32, CT = TN / WN / 32;
   constexpr int AI = TM * 8 / NT, BI = TN * 8 / NT;  // 16-byte pieces a thread stages
@@ -57,11 +59,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
   constexpr int kScales = TS + (kRowScale ? TM : 64);  // then the rows' or the row blocks'
   constexpr int kUnitsPer = (kScales / 64 + W - 1) / W;  // loads of 64 scales a wave; those past the last repeat it
   constexpr int kStage = (TM + TN) * 128 + kUnitsPer * W * 256;
-  constexpr int kRows = RT * 32, kPitch = kRows * static_cast<int>(sizeof(typename Elem<OT>::T)) + 16;  // of a wave's outputs
+  constexpr int kRows = RT * 32, kPitch = kRows * static_cast<int>(sizeof(typename Elem<ST>::T)) + 16;  // of a wave's outputs
   // The two stages, and after the loop the waves' outputs.  One array: with a second one the compiler waits for a stage's
   // loads before any read of the other stage (51 -> 43 us for 8 experts of 2048 x 2560 and 4096 pairs).
   __shared__ __align__(128) uint8_t lds[2 * kStage];
-  typedef typename Elem<OT>::T T;
+  typedef typename Elem<ST>::T T;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WM, wn = wave / WM;
@@ -111,7 +113,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
       const float v = bucket == a.pd.E ? 0.0f : __uint_as_float(0x7FC00000u);
       const int rows = static_cast<int>(std::min<int64_t>(M - r0, TM));
       for (int i = tid; i < count * rows; i += NT)
-        y[static_cast<int64_t>(a.plan[a.pd.order + first + i / rows]) * M + r0 + i % rows] = to_elem<OT>(v);
+        y[static_cast<int64_t>(a.plan[a.pd.order + first + i / rows]) * M + r0 + i % rows] = to_elem<ST>(v);
       return;
     }
     w += static_cast<int64_t>(bucket) * M * a.pitch;
@@ -127,6 +129,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
     }
   } else {
     t0 = static_cast<int64_t>(bid) * TN;
+    if (gridDim.y > 1) {  // a share of K, its sums to a slab of its own
+      g0 = static_cast<int>(blockIdx.y) * a.share;
+      g1 = std::min(a.G, g0 + a.share);
+      y += static_cast<int64_t>(blockIdx.y) * M * N;
+    }
   }
 
   // What this thread stages: 16-byte pieces, offsets from the tile's first row (rows past the end repeat the last), and
@@ -201,7 +208,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
     piece[m][0] = row * 128 + 16 * ((4 * m + 2 * half) ^ (row >> 1 & 7));
     piece[m][1] = row * 128 + 16 * ((4 * m + 2 * half + 1) ^ (row >> 1 & 7));
   }
-  typedef Frag32<OT == DT_F32> F;
+  typedef Frag32<EXACT> F;
   auto read_frag = [&](F& f, const uint8_t* p) {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -270,7 +277,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
           typedef T T4 __attribute__((ext_vector_type(4)));
           T4 o;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = to_elem<OT>(acc[i][j][4 * k + e]);
+          for (int e = 0; e < 4; ++e) o[e] = to_elem<ST>(acc[i][j][4 * k + e]);
           *reinterpret_cast<T4*>(mine + row * kPitch + (i * 32 + k * 8 + half * 4) * sizeof(T)) = o;
         }
       __builtin_amdgcn_wave_barrier();
@@ -325,13 +332,39 @@ hipError_t run_tile(const GemmArgs& a, int ot, int64_t blocks, hipStream_t st) {
   switch (ot) {
     case DT_F32:
       // (an fp32 output's operands are twice as wide in registers: no 256 x 256 tile)
-      if constexpr (TM * TN <= 128 * 128) k_f8_gemm<TM, TN, WM, WN, MODE, DT_F32><<<grid, block, 0, st>>>(a);
+      if constexpr (TM * TN <= 128 * 128) k_f8_gemm<TM, TN, WM, WN, MODE, true, DT_F32><<<grid, block, 0, st>>>(a);
       else return hipErrorInvalidValue;
       break;
-    case DT_F16: k_f8_gemm<TM, TN, WM, WN, MODE, DT_F16><<<grid, block, 0, st>>>(a); break;
-    case DT_BF16: k_f8_gemm<TM, TN, WM, WN, MODE, DT_BF16><<<grid, block, 0, st>>>(a); break;
+    case DT_F16: k_f8_gemm<TM, TN, WM, WN, MODE, false, DT_F16><<<grid, block, 0, st>>>(a); break;
+    case DT_BF16: k_f8_gemm<TM, TN, WM, WN, MODE, false, DT_BF16><<<grid, block, 0, st>>>(a); break;
     default: return hipErrorInvalidValue;
   }
+  return hipGetLastError();
+}
+
+// y = the sum of the slabs [splits][n], in order
+template <int OT>
+__global__ __launch_bounds__(256) void k_f8_join(const float* slabs, int splits, int64_t n, typename Elem<OT>::T* y) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  if (i + 4 <= n && n % 4 == 0) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(slabs + i);
+    for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(slabs + s * n + i);
+    store4<OT>(y + i, v, 4, reinterpret_cast<uintptr_t>(y) % (4 * sizeof(*y)) == 0);
+  } else {
+    for (int64_t k = i; k < n && k < i + 4; ++k) {
+      float v = slabs[k];
+      for (int s = 1; s < splits; ++s) v += slabs[s * n + k];
+      y[k] = to_elem<OT>(v);
+    }
+  }
+}
+
+template <int TM, int TN>
+hipError_t run_split(const GemmArgs& a, bool exact, int64_t blocks, int splits, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(splits)), block(256);
+  if (exact) k_f8_gemm<TM, TN, 2, 2, MODE_DENSE, true, DT_F32><<<grid, block, 0, st>>>(a);
+  else k_f8_gemm<TM, TN, 2, 2, MODE_DENSE, false, DT_F32><<<grid, block, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -366,29 +399,62 @@ float tile_cost(const TileKind& k, double tiles, double stages, int cus) {
   return static_cast<float>(full * (k.us[k.per_cu - 1] * stages + k.round) + (rest > 0 ? k.us[rest - 1] * stages + k.round : 0.0));
 }
 
-int best_tile(const int* kinds, int n, const double* tiles, double stages, int cus) {
-  int best = 0;
-  for (int i = 1; i < n; ++i)
-    if (tile_cost(kTiles[kinds[i]], tiles[i], stages, cus) < tile_cost(kTiles[kinds[best]], tiles[best], stages, cus)) best = i;
-  return kinds[best];
+// How a dense product of M rows, N tokens and `many` matrices runs: its tile, and the shares that K is divided into
+// (1: not at all).  Shares make their sums in slabs of fp32 that k_f8_join adds: worth it where the tiles leave CUs idle
+// and K is long (2560 x 9728, 64 tokens: 27 us undivided, 40 workgroups of 76 stages).
+struct DensePlan {
+  int kind, splits;
+};
+constexpr int kMinShare = 4;                              // stages
+constexpr int64_t kMaxSlabs = int64_t(64) << 20;          // bytes
+DensePlan dense_plan(int64_t M, int64_t N, int64_t many, double stages, bool f32, bool may_split, int cus) {
+  const int kinds[] = {TILE_128, TILE_128_64, TILE_64, TILE_256};
+  DensePlan best{TILE_128, 1};
+  float cost = INFINITY;
+  for (int i = 0; i < (f32 ? 3 : 4); ++i) {
+    const TileKind& k = kTiles[kinds[i]];
+    const double tiles = static_cast<double>((M + k.tm - 1) / k.tm) * static_cast<double>((N + k.tn - 1) / k.tn) * static_cast<double>(many);
+    for (int s = 1; s <= 16; s *= 2) {
+      if (s > 1 && (!may_split || kinds[i] == TILE_256 || kinds[i] == TILE_128 || stages < s * kMinShare || s * M * N * 4 > kMaxSlabs)) break;
+      // a second launch, and the slabs written and read
+      const float c = tile_cost(k, tiles * s, std::ceil(stages / s), cus) + (s > 1 ? 3.0f + static_cast<float>(s * M * N) * 8 / 4e6f : 0.0f);
+      if (c < cost) {
+        cost = c;
+        best = {kinds[i], s};
+      }
+    }
+  }
+  return best;
 }
 
-// dense products: M rows, N tokens, `many` matrices
 template <int MODE>
-hipError_t run_dense(GemmArgs& a, int ot, int64_t many, double stages, int cus, hipStream_t st) {
-  const int kinds[] = {TILE_128, TILE_128_64, TILE_64, TILE_256};
-  const int n = ot == DT_F32 ? 3 : 4;
-  double tiles[4];
-  for (int i = 0; i < n; ++i) {
-    const TileKind& k = kTiles[kinds[i]];
-    tiles[i] = static_cast<double>((a.M + k.tm - 1) / k.tm) * static_cast<double>((a.N + k.tn - 1) / k.tn) * static_cast<double>(many);
-  }
-  const int kind = best_tile(kinds, n, tiles, stages, cus);
-  const TileKind& k = kTiles[kind];
+hipError_t run_dense(GemmArgs& a, int ot, int64_t many, const DensePlan& plan, float* slabs, hipStream_t st) {
+  const TileKind& k = kTiles[plan.kind];
   a.tiles_m = static_cast<int>((a.M + k.tm - 1) / k.tm);
   a.tiles_n = static_cast<int>((a.N + k.tn - 1) / k.tn);
   const int64_t blocks = static_cast<int64_t>(a.tiles_m) * a.tiles_n * many;
-  switch (kind) {
+  if constexpr (MODE == MODE_DENSE) {
+    if (plan.splits > 1) {
+      if (blocks > INT_MAX) return hipErrorInvalidValue;
+      void* y = a.y;
+      const int64_t n = a.M * a.N;
+      a.y = slabs;
+      a.vec = store_vec16(slabs, a.M, DT_F32);
+      a.share = (a.G + plan.splits - 1) / plan.splits;
+      const int splits = (a.G + a.share - 1) / a.share;  // every share has groups
+      const hipError_t e = plan.kind == TILE_64 ? run_split<64, 64>(a, ot == DT_F32, blocks, splits, st)
+                                                : run_split<128, 64>(a, ot == DT_F32, blocks, splits, st);
+      if (e != hipSuccess) return e;
+      const unsigned grid = static_cast<unsigned>((n + 1023) / 1024);
+      switch (ot) {
+        case DT_F32: k_f8_join<DT_F32><<<grid, 256, 0, st>>>(slabs, splits, n, static_cast<float*>(y)); break;
+        case DT_F16: k_f8_join<DT_F16><<<grid, 256, 0, st>>>(slabs, splits, n, static_cast<_Float16*>(y)); break;
+        default: k_f8_join<DT_BF16><<<grid, 256, 0, st>>>(slabs, splits, n, static_cast<__bf16*>(y)); break;
+      }
+      return hipGetLastError();
+    }
+  }
+  switch (plan.kind) {
     case TILE_256: return run_tile<256, 256, 2, 4, MODE>(a, ot, blocks, st);
     case TILE_128: return run_tile<128, 128, 2, 2, MODE>(a, ot, blocks, st);
     case TILE_128_64: return run_tile<128, 64, 2, 2, MODE>(a, ot, blocks, st);
@@ -406,7 +472,15 @@ hipError_t run_experts(GemmArgs& a, int ot, int cus, hipStream_t st) {
     // about half a tile of each expert is padding
     tiles[i] = static_cast<double>((a.M + k.tm - 1) / k.tm) * (static_cast<double>(a.pd.pairs) / k.tn + experts * 0.5);
   }
-  const int kind = best_tile(kinds, 4, tiles, a.G, cus);
+  int kind = kinds[0];
+  float least = INFINITY;
+  for (int i = 0; i < 4; ++i) {
+    const float c = tile_cost(kTiles[kinds[i]], tiles[i], a.G, cus);
+    if (c < least) {
+      least = c;
+      kind = kinds[i];
+    }
+  }
   const TileKind& k = kTiles[kind];
   a.tiles_m = static_cast<int>((a.M + k.tm - 1) / k.tm);
   a.map = 0;
@@ -422,9 +496,15 @@ hipError_t run_experts(GemmArgs& a, int ot, int cus, hipStream_t st) {
 
 }  // namespace
 
-size_t f8_gemm_workspace_bytes(const F8Desc&, int64_t) { return 0; }
+size_t f8_gemm_workspace_bytes(const F8Desc& m, int64_t N) {
+  if (f8_few_tokens(m, N)) return 0;
+  int splits = 1;
+  for (int f32 = 0; f32 < 2; ++f32)  // for either kind of output
+    splits = std::max(splits, dense_plan(m.M, N, 1, static_cast<double>(m.Kp / kF8Block), f32, true, m.cus).splits);
+  return splits > 1 ? static_cast<size_t>(splits) * m.M * N * 4 : 0;
+}
 
-hipError_t launch_f8_gemm(const F8Desc& m, const uint8_t* xc, const float* xs, int64_t N, void* y, int yt, void*,
+hipError_t launch_f8_gemm(const F8Desc& m, const uint8_t* xc, const float* xs, int64_t N, void* y, int yt, void* ws,
                           hipStream_t st) {
   if (f8_few_tokens(m, N)) return launch_f8_few(m, xc, xs, N, y, yt, st);
   GemmArgs a{};
@@ -438,7 +518,7 @@ hipError_t launch_f8_gemm(const F8Desc& m, const uint8_t* xc, const float* xs, i
   a.pitch = m.Kp;
   a.G = static_cast<int>(m.Kp / kF8Block);
   a.vec = store_vec16(y, m.M, yt);
-  return run_dense<MODE_DENSE>(a, yt, 1, a.G, m.cus, st);
+  return run_dense<MODE_DENSE>(a, yt, 1, dense_plan(m.M, N, 1, a.G, yt == DT_F32, true, m.cus), static_cast<float*>(ws), st);
 }
 
 hipError_t launch_f8_gemm_id(const F8Desc& m, const uint8_t* xc, const float* xs, int64_t pairs, int slots,
@@ -475,7 +555,8 @@ hipError_t launch_f8_wgrad(const F8WgradArgs& w, hipStream_t st) {
   a.plan = w.plan;
   a.pd = w.pd;
   const int64_t E = w.plan ? w.pd.E : 1;
-  return run_dense<MODE_WGRAD>(a, w.dt, E, std::max(1.0, static_cast<double>(a.G) / E), w.cus, st);
+  const DensePlan plan = dense_plan(a.M, a.N, E, std::max(1.0, static_cast<double>(a.G) / E), w.dt == DT_F32, false, w.cus);
+  return run_dense<MODE_WGRAD>(a, w.dt, E, plan, nullptr, st);
 }
 
 }  // namespace qmm
