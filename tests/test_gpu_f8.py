@@ -361,6 +361,66 @@ def test_expert_gradients(N, S, E, M, K, per_slot):
         check(dw[e], a @ b.T, bounds(a, b), f"expert {e}")
 
 
+# ---- sizes at which every tile of the products is taken --------------------------------------------
+
+def device_check(y, a, b, label=""):
+    """y against a @ b^T in fp64 on the device, a [N, K] and b [M, K] the values (fp32, exact) of the operands."""
+    a, b = a.double(), b.double()
+    ref, size = a @ b.t(), a.abs() @ b.abs().t()
+    groups = -(-a.shape[1] // 128)
+    step = 128 * 2.0 ** -23 + (groups + 18) * 2.0 ** -24 + (2.0 ** -10 if y.dtype != torch.float32 else 0.0)  # product_bound
+    tol = size * step + (ref.abs() + size * step) * HALF_STEP[y.dtype] + SMALLEST[y.dtype]
+    # decoded values are code * scale rounded to fp32: another half step of each factor
+    tol = tol + size * 2.0 ** -22
+    assert bool(((y.double() - ref).abs() <= tol).all()), label
+
+
+LARGE = [  # tokens, M, K: 256 x 256, 128 x 128 and 128 x 64 tiles, the last with K divided too
+    (4000, 4000, 300), (2000, 8000, 250), (3000, 3000, 384), (2049, 4090, 2500), (60, 5000, 4000), (700, 130, 8000)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,M,K", LARGE)
+def test_large_products(N, M, K, dtype):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    dt = DTYPES[dtype]
+    m = q.F8Matrix.quantize(torch.randn((M, K), generator=g, device="cuda") * 0.02)
+    x = torch.randn((N, K), generator=g, device="cuda").to(dt)
+    t = q.f8_quantize(x)
+    y = m.linear(x)
+    device_check(y, t.values(), m.dequantize(), "y")
+    assert torch.equal(y, m.gemm(t, out_dtype=dt)) and torch.equal(y, m.linear(x))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("N,M,K", [(300, 4000, 4000), (250, 8000, 2000), (384, 3000, 3000), (5000, 200, 130)])
+def test_large_weight_gradients(N, M, K, dtype):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    gt, xt = (q.f8_quantize_t(torch.randn((N, c), generator=g, device="cuda").to(DTYPES[dtype])) for c in (M, K))
+    dw = q.f8_wgrad(gt, xt, dtype=DTYPES[dtype])
+    device_check(dw, gt.values(), xt.values(), "dw")
+    assert torch.equal(dw, q.f8_wgrad(gt, xt, dtype=DTYPES[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,S,E,M,K", [(4500, 2, 3, 3000, 200), (1500, 2, 3, 1000, 500), (300, 1, 250, 256, 1100), (1837, 1, 137, 925, 100),
+                                       (2000, 4, 4, 500, 130)])
+def test_large_expert_products(N, S, E, M, K, dtype):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    dt = DTYPES[dtype]
+    m = q.F8Matrix.quantize(torch.randn((E, M, K), generator=g, device="cuda") * 0.02)
+    x = torch.randn((N, K), generator=g, device="cuda").to(dt)
+    ids = torch.randint(-1, E, (N, S), generator=g, device="cuda", dtype=torch.int32)
+    y = m.linear_id(x, ids)
+    xv = q.f8_quantize(x).values()
+    assert bool((y[ids < 0] == 0).all())
+    for e in range(E):
+        t, s = (ids == e).nonzero(as_tuple=True)
+        if len(t):
+            device_check(y[t, s], xv[t], m.dequantize(e), f"expert {e}")
+    assert torch.equal(y, m.linear_id(x, ids))
+
+
 # ---- streams, graphs -----------------------------------------------------------------------------
 
 def test_side_stream_order():
@@ -418,6 +478,24 @@ def test_graph_replays():
             for a, b in zip(eager, out):
                 assert torch.equal(a, b), f"replay {rep}"
         _ = (x300.float() * 2).sum().item()
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls of one matrix on two streams, workspaces of their own: each gives the bits it gives alone."""
+    g = np.random.default_rng(28)
+    m, _ = weights(g, 512, 9728)
+    xs = [dev(g.standard_normal((n, 9728)), torch.bfloat16) for n in (48, 200)]
+    alone = [m.linear(x).clone() for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(5):
+        for i, (s, x) in enumerate(zip(streams, xs)):
+            with torch.cuda.stream(s):
+                outs[i].append(m.linear(x))
+    torch.cuda.synchronize()
+    for a, out in zip(alone, outs):
+        assert all(torch.equal(a, o) for o in out)
 
 
 def test_new_weights_are_seen():
