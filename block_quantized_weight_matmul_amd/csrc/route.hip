@@ -1,12 +1,12 @@
 // route.hip -- the expert router (softmax, the S largest, tokens per expert, balance loss, gradients), the plan that
 // sorts (token, slot) pairs by expert for the expert-indexed products, and the weighted sum of the slots' outputs.
 //
-// Router: 16 lanes (one DPP row) hold a token, V consecutive experts a lane, so that a reduction over the experts is
-// four DPP steps; nothing but the logits is read.  Sums over tokens (probabilities per expert) go through one partial
+// Router: 16 lanes (one DPP row) hold a token, V experts a lane, so that a reduction over the experts is four DPP steps;
+// nothing but the logits is read.  A lane's experts lie in runs of 16 bytes of logits with the other lanes' runs between:
+// loads and stores of V consecutive experts a lane took 1.2 times as long at 400 experts.  Sums over tokens (probabilities per expert) go through one partial
 // per workgroup, added in a fixed order: the same input gives the same bits.
 #include <algorithm>
 #include <climits>
-#include <utility>
 
 #include "f8.hpp"
 
@@ -28,12 +28,6 @@ __device__ __forceinline__ float max16f(float v) {
   v = fmaxf(v, dppf<0x122>(v));
   return fmaxf(v, dppf<0x121>(v));
 }
-__device__ __forceinline__ int min16i(int v) {
-  v = min(v, dpp<0x128>(v));
-  v = min(v, dpp<0x124>(v));
-  v = min(v, dpp<0x122>(v));
-  return min(v, dpp<0x121>(v));
-}
 __device__ __forceinline__ float sum16f(float v) {
   v += dppf<0x128>(v);
   v += dppf<0x124>(v);
@@ -50,87 +44,171 @@ __device__ __forceinline__ float fast_exp(float x) {
   return fmaf(y, r * kLn2, y);
 }
 
-// 16-bit logits as unsigned keys that order like (value, lower index first): the value's bits made monotonic above the
-// complement of the expert; 0 is below every key that can be chosen.  -inf and NaN give 0, -0 counts as +0.
-template <int LT>
-__device__ __forceinline__ uint32_t logit_key(float v, int e) {
-  if (!(v > kNegInf)) return 0u;
-  uint32_t b;
-  if constexpr (LT == DT_F16) b = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
-  else b = __float_as_uint(v) >> 16;
-  b = v == 0.0f ? 0x8000u : b & 0x8000u ? ~b & 0xFFFFu : b | 0x8000u;
-  return b << 16 | (0xFFFFu - static_cast<uint32_t>(e));
-}
-template <int LT>
-__device__ __forceinline__ float key_logit(uint32_t key) {
-  uint32_t b = key >> 16;
-  b = b & 0x8000u ? b & 0x7FFFu : ~b & 0xFFFFu;
-  if constexpr (LT == DT_F16) return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(b)));
-  else return __uint_as_float(b << 16);
-}
-__device__ __forceinline__ uint32_t max16u(uint32_t v) {
-  v = max(v, static_cast<uint32_t>(dpp<0x128>(static_cast<int>(v))));
-  v = max(v, static_cast<uint32_t>(dpp<0x124>(static_cast<int>(v))));
-  v = max(v, static_cast<uint32_t>(dpp<0x122>(static_cast<int>(v))));
-  return max(v, static_cast<uint32_t>(dpp<0x121>(static_cast<int>(v))));
-}
+// Logits as keys that order like (value, lower index first), with a largest and a smallest of two in one instruction
+// each; kNone, below every key that can be chosen, stands for -inf and NaN.  -0 counts as +0.  16-bit logits: the value's
+// bits made monotonic above the complement of the expert.
+template <int LT> struct Key {
+  typedef uint32_t T;
+  static constexpr T kNone = 0u;
+  static __device__ __forceinline__ T make(float v, int e) {
+    const uint32_t b = bits(v + 0.0f), k = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+    return v > kNegInf ? (k & 0xFFFF0000u) | (0xFFFFu - static_cast<uint32_t>(e)) : kNone;
+  }
+  static __device__ __forceinline__ int expert(T key) { return static_cast<int>(0xFFFFu - (key & 0xFFFFu)); }
+  static __device__ __forceinline__ float value(T key) {
+    const uint32_t b = (key & 0xFFFF0000u) ^ (key & 0x80000000u ? 0x80000000u : 0xFFFF0000u);
+    if constexpr (LT == DT_F16) return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(b >> 16)));
+    else return __uint_as_float(b);
+  }
+  // the 16-bit logit above 16 zeros
+  static __device__ __forceinline__ uint32_t bits(float v) {
+    if constexpr (LT == DT_F16) return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<_Float16>(v))) << 16;
+    else return __float_as_uint(v);
+  }
+  static __device__ __forceinline__ T larger(T a, T b) { return max(a, b); }
+  static __device__ __forceinline__ T smaller(T a, T b) { return min(a, b); }
+  template <int CTRL> static __device__ __forceinline__ T ror(T v) { return static_cast<T>(dpp<CTRL>(static_cast<int>(v))); }
+};
+// 32-bit logits: the value as a double, whose 29 spare bits have room for the expert.  +inf is 2^200, to stay a number.
+template <> struct Key<DT_F32> {
+  typedef double T;
+  static constexpr T kNone = -__builtin_inf();
+  static constexpr uint32_t kMask = 1023;  // experts
+  static __device__ __forceinline__ T make(float v, int e) {
+    const double d = fmin(static_cast<double>(v + 0.0f), 0x1p200);
+    const uint64_t b = __builtin_bit_cast(uint64_t, d) | static_cast<uint32_t>(v < 0.0f ? e : kMask - e);
+    return v > kNegInf ? __builtin_bit_cast(double, b) : kNone;
+  }
+  static __device__ __forceinline__ int expert(T key) {
+    const uint32_t low = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, key)) & kMask;
+    return static_cast<int>(__builtin_bit_cast(int64_t, key) < 0 ? low : kMask - low);
+  }
+  static __device__ __forceinline__ float value(T key) {
+    return static_cast<float>(__builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~static_cast<uint64_t>(kMask)));
+  }
+  static __device__ __forceinline__ T larger(T a, T b) { return fmax(a, b); }
+  static __device__ __forceinline__ T smaller(T a, T b) { return fmin(a, b); }
+  template <int CTRL> static __device__ __forceinline__ T ror(T v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = dpp<CTRL>(static_cast<int>(b)), hi = dpp<CTRL>(static_cast<int>(b >> 32));
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+  }
+};
+static_assert(kRouteMaxExperts <= 1024, "an expert's index has 10 bits");
+
+// Which experts a lane holds: its logit i is expert lane * kRun + offset(i), rising with i.
+template <int LT, int V> struct Spread {
+  static constexpr int kRun = std::min<int>(V, 16 / sizeof(typename Elem<LT>::T));
+  static __device__ __forceinline__ constexpr int offset(int i) { return i / kRun * (16 * kRun) + i % kRun; }
+  static __device__ __forceinline__ int expert(int lane, int i) { return lane * kRun + offset(i); }
+};
 
 // The largest logits of 16 lanes, one a call, ties to the lower expert.  next() returns the expert (-1: none is left) and
-// its logit; the same in all 16 lanes.
-template <int LT, int V, bool KEYS = LT != DT_F32> struct Chooser;
-template <int LT, int V> struct Chooser<LT, V, true> {
-  uint32_t k[V];
+// its logit; the same in all 16 lanes.  With LIST every lane has its L = min(V, 8) largest sorted, L of them being enough
+// for L calls, and a call compares the lanes' first; without, a call looks through all V.
+template <int LT, int V, bool LIST> struct Chooser {
+  typedef Key<LT> K;
+  typedef typename K::T T;
+  static constexpr int L = LIST ? std::min(V, 8) : V;
+  T k[L];
+
+  // Batcher's merge exchange: falling order
+  template <int N> static __device__ __forceinline__ void exchange(T (&x)[N], int i, int j) {
+    const T a = x[i], b = x[j];
+    x[i] = K::larger(a, b);
+    x[j] = K::smaller(a, b);
+  }
+  static __device__ __forceinline__ void sort(T (&x)[L]) {
+#pragma unroll
+    for (int p = 1; p < L; p *= 2)
+#pragma unroll
+      for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+        for (int j = q % p; j < L - q; j += 2 * q)
+#pragma unroll
+          for (int i = 0; i < q; ++i)
+            if (i + j + q < L && (i + j) / (2 * p) == (i + j + q) / (2 * p)) exchange(x, i + j, i + j + q);
+  }
+
   __device__ __forceinline__ Chooser(const float* l, int lane) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) k[i] = logit_key<LT>(l[i], lane * V + i);
+    for (int i = 0; i < L; ++i) k[i] = K::make(l[i], Spread<LT, V>::expert(lane, i));
+    if constexpr (LIST) {
+      sort(k);
+#pragma unroll
+      for (int g = L; g < V; g += L) {
+        T more[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) more[i] = K::make(l[g + i], Spread<LT, V>::expert(lane, g + i));
+        sort(more);
+        // the L largest of both, first rising then falling; then sorted by halves
+#pragma unroll
+        for (int i = 0; i < L; ++i) k[i] = K::larger(k[i], more[L - 1 - i]);
+#pragma unroll
+        for (int h = L / 2; h >= 1; h /= 2)
+#pragma unroll
+          for (int i = 0; i < L; ++i)
+            if (!(i & h)) exchange(k, i, i + h);
+      }
+    }
   }
-  __device__ __forceinline__ int next(int, float& value) {
-    uint32_t m = k[0];
+  __device__ __forceinline__ int next(float& value) {
+    T m = k[0];
+    if constexpr (!LIST) {
 #pragma unroll
-    for (int i = 1; i < V; ++i) m = max(m, k[i]);
-    m = max16u(m);
+      for (int i = 1; i < L; ++i) m = K::larger(m, k[i]);
+    }
+    m = K::larger(m, K::template ror<0x128>(m));
+    m = K::larger(m, K::template ror<0x124>(m));
+    m = K::larger(m, K::template ror<0x122>(m));
+    m = K::larger(m, K::template ror<0x121>(m));
+    if constexpr (LIST) {
+      const bool mine = k[0] == m;
 #pragma unroll
-    for (int i = 0; i < V; ++i) k[i] = k[i] == m ? 0u : k[i];
-    value = key_logit<LT>(m);
-    return m ? static_cast<int>(0xFFFFu - (m & 0xFFFFu)) : -1;
-  }
-};
-template <int LT, int V> struct Chooser<LT, V, false> {
-  float v[V];
-  __device__ __forceinline__ Chooser(const float* l, int) {
+      for (int i = 0; i < L; ++i) k[i] = !mine ? k[i] : i + 1 < L ? k[i + 1] : K::kNone;
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = l[i] == l[i] ? l[i] : kNegInf;
-  }
-  __device__ __forceinline__ int next(int lane, float& value) {
-    float m = v[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-    m = max16f(m);
-    int at = V;  // in this lane
-#pragma unroll
-    for (int i = V - 1; i >= 0; --i) at = v[i] == m ? i : at;
-    const int e = min16i(at < V ? lane * V + at : INT_MAX), mine = e - lane * V;
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = i == mine ? kNegInf : v[i];
-    value = m;
-    return m > kNegInf ? e : -1;
+      for (int i = 0; i < L; ++i) k[i] = k[i] == m ? K::kNone : k[i];
+    }
+    if (m == K::kNone) return -1;
+    value = K::value(m);
+    return K::expert(m);
   }
 };
 
-// V logits of this lane from expert lane * V on; experts from E on are -inf
+// LDS operations of a wave's lanes before this are done before those after it; a team lies inside a wave
+__device__ __forceinline__ void in_wave() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// The lane's logits of row t; experts from E on are -inf.  A row's last run is read into the next row, but where no row
+// follows that has as much: there the logits are read one by one.
 template <int LT, int V>
-__device__ __forceinline__ void load_logits(const typename Elem<LT>::T* row, int lane, int E, float* v) {
-  if (V >= 8 && lane * V + V <= E) {
+__device__ __forceinline__ void load_logits(const void* logits, int64_t N, int E, int64_t t, int lane, float* v) {
+  typedef typename Elem<LT>::T T;
+  typedef Spread<LT, V> Sp;
+  typedef T Run __attribute__((ext_vector_type(Sp::kRun)));
+  typedef Run RunU __attribute__((aligned(sizeof(T))));
+  const T* row = static_cast<const T*>(logits) + t * E;
+  if ((N - t) * E >= (E + Sp::kRun - 1) / Sp::kRun * Sp::kRun) {
 #pragma unroll
-    for (int i = 0; i < V; i += 8) load8<LT>(row + lane * V + i, v + i);
+    for (int i = 0; i < V; i += Sp::kRun) {
+      const int e = Sp::expert(lane, i);
+      const Run r = *reinterpret_cast<const RunU*>(row + (e < E ? e : 0));
+#pragma unroll
+      for (int k = 0; k < Sp::kRun; ++k) v[i + k] = static_cast<float>(r[k]);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = lane * V + i < E ? static_cast<float>(row[lane * V + i]) : kNegInf;
+    for (int i = 0; i < V; ++i) v[i] = static_cast<float>(row[std::min(Sp::expert(lane, i), E - 1)]);
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = Sp::expert(lane, i) < E ? v[i] : kNegInf;
 }
 
 // Threads of a workgroup: one register of every kind per expert of a lane, so many experts leave room for fewer waves.
-constexpr int route_threads(int V) { return V <= 8 ? 1024 : V <= 16 ? 512 : 256; }
+constexpr int route_threads(int V) { return V <= 8 ? 1024 : V <= 32 ? 512 : 256; }
 // Slot s lives in lane s & 15, register s >> 4: one register (SR) up to 16 slots, four up to 64.
 constexpr int kRouteOneBlock = 128;   // rows that one workgroup routes and sums by itself
 
@@ -152,11 +230,11 @@ __device__ __forceinline__ float loss_part(int count, float psum, float T, int E
 }
 
 // part, part_n: the workgroups' sums over their rows, [E] and [E + 1] each.  A single workgroup writes the results itself.
-template <int LT, int V, int SR>
+template <int LT, int V, int SR, bool LIST>
 __global__ __launch_bounds__(route_threads(V)) void k_route(RouteArgs a, float* part, int32_t* part_n) {
   constexpr int kRouteThreads = route_threads(V), kRouteTeams = kRouteThreads / 16;
   extern __shared__ int32_t sh[];  // [E + 1] counts, then [waves][16 * V] probability sums
-  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
+  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4, E = static_cast<int>(a.E);
   float* shp = reinterpret_cast<float*>(sh + a.E + 1);
   for (int i = threadIdx.x; i <= a.E; i += kRouteThreads) sh[i] = 0;
   __syncthreads();
@@ -166,29 +244,34 @@ __global__ __launch_bounds__(route_threads(V)) void k_route(RouteArgs a, float* 
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteTeams;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteTeams + team; t < a.N; t += step) {
     float l[V];
-    load_logits<LT, V>(static_cast<const typename Elem<LT>::T*>(a.logits) + t * a.E, lane, a.E, l);
+    load_logits<LT, V>(a.logits, a.N, E, t, lane, l);
     if (a.valid && !a.valid[t]) {
 #pragma unroll
       for (int i = 0; i < V; ++i) l[i] = kNegInf;
     }
-    Chooser<LT, V> choose(l, lane);
+    Chooser<LT, V, LIST> choose(l, lane);
     float top = kNegInf, chosen[SR];
     int ids[SR];
 #pragma unroll
     for (int k = 0; k < SR; ++k) { chosen[k] = kNegInf; ids[k] = -1; }
     for (int s = 0; s < a.S; ++s) {
-      float m;
-      const int e = choose.next(lane, m);
+      float m = kNegInf;
+      const int e = choose.next(m);
       if (s == 0 && e >= 0) top = m;
 #pragma unroll
       for (int k = 0; k < SR; ++k)
         if (s == k * 16 + lane) { chosen[k] = m; ids[k] = e; }
     }
     const bool alive = top > kNegInf;
+    if (!alive) {
+      top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = kNegInf;
+    }
     float z = 0.0f, p[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      p[i] = alive ? fast_exp(l[i] - top) : 0.0f;
+      p[i] = fast_exp(l[i] - top);
       z += p[i];
     }
     z = sum16f(z);
@@ -217,10 +300,12 @@ __global__ __launch_bounds__(route_threads(V)) void k_route(RouteArgs a, float* 
   }
   // the wave's four tokens, then the waves
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    psum[i] += __shfl_xor(psum[i], 16);
-    psum[i] += __shfl_xor(psum[i], 32);
-    if ((team & 3) == 0) shp[(team >> 2) * (16 * V) + lane * V + i] = psum[i];
+  for (int i = 0; i < V; ++i) psum[i] += __shfl_xor(psum[i], 16);
+#pragma unroll
+  for (int i = 0; i < V; ++i) psum[i] += __shfl_xor(psum[i], 32);
+  if ((team & 3) == 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) shp[(team >> 2) * (16 * V) + Spread<LT, V>::expert(lane, i)] = psum[i];
   }
   __syncthreads();
   if (gridDim.x == 1) {
@@ -264,10 +349,12 @@ __global__ __launch_bounds__(kSumCols * kSumSegs) void k_route_sum(const float* 
   const int col = threadIdx.x % kSumCols, seg = threadIdx.x / kSumCols, e = blockIdx.x * kSumCols + col, E1 = E + 1;
   float s = 0.0f;
   int n = 0;
+  const float* p = part + std::min(e, E - 1);  // no branch, so that the loads do not wait for each other
+  const int32_t* pn = part_n + std::min(e, E);
 #pragma unroll 8
   for (int b = seg; b < blocks; b += kSumSegs) {
-    if (e < E) s += part[static_cast<int64_t>(b) * E + e];
-    if (e < E1) n += part_n[static_cast<int64_t>(b) * E1 + e];
+    s += p[static_cast<int64_t>(b) * E];
+    n += pn[static_cast<int64_t>(b) * E1];
   }
   sp[seg][col] = s;
   sn[seg][col] = n;
@@ -300,66 +387,69 @@ __global__ __launch_bounds__(1024) void k_balance_loss(const int32_t* counts, co
   if (threadIdx.x == 0) *loss = T > 0.0f ? coef * v / T : 0.0f;
 }
 
-// adds the gradients d of the slots that lanes 0 .. left - 1 of a row hold to their experts id, slot by slot
-template <int V, int S>
-__device__ __forceinline__ void add_slot(int id, float d, int left, int e0, float* dp) {
-  if (S >= left) return;  // the same for all lanes
-  const int e = dpp<0x150 + S>(id) - e0;  // row_newbcast: lane S of the row
-  const float ds = dppf<0x150 + S>(d);
-#pragma unroll
-  for (int i = 0; i < V; ++i) dp[i] += i == e ? ds : 0.0f;
-}
-template <int V, int... S>
-__device__ __forceinline__ void add_slots(int id, float d, int left, int e0, float* dp, std::integer_sequence<int, S...>) {
-  (add_slot<V, S>(id, d, left, e0, dp), ...);
-}
+// tokens of a workgroup: their rows of LDS stay under 64 KB
+constexpr int route_backward_teams(int V) { return V <= 32 ? 16 : 8; }
 
-// dl = p (dp - sum p dp), dp_e = dloss coef f_e / T + the chosen slots' gradients; p again from the logits.
+// dl = p (dp - sum p dp), dp_e = dloss coef f_e / T + the chosen slots' gradients; p again from the logits.  The slots'
+// gradients reach the lanes that hold their experts through a row of LDS that holds the loss's
+// part between tokens.
 template <int LT, int V, int SR>
-__global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
-  constexpr int kRouteTeams = 16;
+__global__ __launch_bounds__(16 * route_backward_teams(V)) void k_route_backward(RouteBackwardArgs a) {
+  constexpr int kRouteTeams = route_backward_teams(V);
   typedef typename Elem<LT>::T T;
-  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
-  float c[V];
+  typedef Spread<LT, V> Sp;
+  __shared__ __align__(16) float balance[16 * V], given[kRouteTeams][16 * V];
+  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4, E = static_cast<int>(a.E);
+  float* mine = given[team];
   {
-    const float n = a.dloss ? static_cast<float>(a.counts[a.E]) : 0.0f;
-    const float k = n > 0.0f ? a.dloss[0] * a.coef / n : 0.0f;
+    const float n = a.dloss ? static_cast<float>(a.counts[E]) : 0.0f;
+    const float k = n > 0.0f ? a.dloss[0] * a.coef / n * (E / (a.S * n)) : 0.0f;
+    for (int e = threadIdx.x; e < 16 * V; e += 16 * kRouteTeams)
+      balance[e] = k != 0.0f ? k * static_cast<float>(a.counts[std::min(e, E)]) : 0.0f;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      c[i] = n > 0.0f && e < a.E ? k * (static_cast<float>(a.counts[e]) * a.E / (a.S * n)) : 0.0f;
-    }
+    for (int i = 0; i < V; ++i) mine[i * 16 + lane] = balance[i * 16 + lane];
+    in_wave();
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteTeams;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteTeams + team; t < a.N; t += step) {
     const T* row = static_cast<const T*>(a.logits) + t * a.E;
     T* out = static_cast<T*>(a.dlogits) + t * a.E;
     float l[V], p[V], dp[V];
-    load_logits<LT, V>(row, lane, a.E, l);
+    load_logits<LT, V>(a.logits, a.N, E, t, lane, l);
+    float w[SR], d[SR];
+    int id[SR];
+#pragma unroll
+    for (int k = 0; k < SR; ++k) {
+      const int s = k * 16 + lane;
+      const bool some = a.dweights && s < a.S;
+      id[k] = some ? a.ids[t * a.S + s] : -1;
+      d[k] = some ? a.dweights[t * a.S + s] : 0.0f;
+      if (id[k] < 0 || id[k] >= a.E) { id[k] = -1; d[k] = 0.0f; }
+    }
     float top = kNegInf;
 #pragma unroll
     for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);  // fmaxf passes over a NaN
     top = max16f(top);
     const bool alive = top > kNegInf && !(a.valid && !a.valid[t]);
+    if (!alive) {
+      top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = kNegInf;
+    }
     float z = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      p[i] = alive ? fast_exp(l[i] - top) : 0.0f;
+      p[i] = fast_exp(l[i] - top);
       z += p[i];
-      dp[i] = c[i];
     }
     z = sum16f(z);
     const float rz = alive ? 1.0f / z : 0.0f;
     if (a.dweights && alive) {
-      float w[SR], d[SR], total = 0.0f, dot = 0.0f;
-      int id[SR];
+      float total = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int k = 0; k < SR; ++k) {
-        const int s = k * 16 + lane;
-        id[k] = s < a.S ? a.ids[t * a.S + s] : -1;
-        const bool some = id[k] >= 0 && id[k] < a.E;
-        w[k] = some ? fast_exp(static_cast<float>(row[id[k]]) - top) : 0.0f;
-        d[k] = some ? a.dweights[t * a.S + s] : 0.0f;
+        w[k] = id[k] >= 0 ? fast_exp(static_cast<float>(row[id[k]]) - top) : 0.0f;
         total += w[k];
         dot = fmaf(w[k], d[k], dot);
       }
@@ -371,8 +461,17 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
         for (int k = 0; k < SR; ++k) d[k] = (d[k] - dot) * f;
       }
 #pragma unroll
-      for (int k = 0; k < SR; ++k) add_slots<V>(id[k], d[k], a.S - k * 16, lane * V, dp, std::make_integer_sequence<int, 16>());
+      for (int k = 0; k < SR; ++k)
+        if (id[k] >= 0) atomicAdd(&mine[id[k]], d[k]);
+      in_wave();
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) dp[i] = alive ? mine[Sp::expert(lane, i)] : 0.0f;
+    in_wave();
+#pragma unroll
+    for (int k = 0; k < SR; ++k)
+      if (id[k] >= 0) mine[id[k]] = balance[id[k]];
+    in_wave();
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -382,20 +481,21 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
     dot = sum16f(dot);
 #pragma unroll
     for (int i = 0; i < V; ++i) dp[i] = p[i] * (dp[i] - dot);
-    if (V >= 8 && lane * V + V <= a.E) {
+    typedef T Run __attribute__((ext_vector_type(Sp::kRun)));
+    typedef Run RunU __attribute__((aligned(sizeof(T))));
 #pragma unroll
-      for (int i = 0; i < V; i += 8) {
-        typedef T T8 __attribute__((ext_vector_type(8)));
-        typedef T8 T8u __attribute__((aligned(sizeof(T))));
-        T8 o;
+    for (int i = 0; i < V; i += Sp::kRun) {
+      const int e = Sp::expert(lane, i);
+      Run o;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = to_elem<LT>(dp[i + k]);
-        *reinterpret_cast<T8u*>(out + lane * V + i) = o;
+      for (int k = 0; k < Sp::kRun; ++k) o[k] = to_elem<LT>(dp[i + k]);
+      if (e + Sp::kRun <= E) {
+        *reinterpret_cast<RunU*>(out + e) = o;
+      } else {
+#pragma unroll
+        for (int k = 0; k < Sp::kRun; ++k)
+          if (e + k < E) out[e + k] = o[k];
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (lane * V + i < a.E) out[lane * V + i] = to_elem<LT>(dp[i]);
     }
   }
 }
@@ -715,8 +815,13 @@ hipError_t launch_v(const RouteArgs& a, hipStream_t st) {
   int32_t* part_n = reinterpret_cast<int32_t*>(part + static_cast<int64_t>(nb) * a.E);
   constexpr int kThreads = route_threads(V);
   const size_t lds = (a.E + 1) * 4 + static_cast<size_t>(kThreads / 64) * 16 * V * 4;
-  if (a.S <= 16) k_route<LT, V, 1><<<nb, kThreads, lds, st>>>(a, part, part_n);
-  else k_route<LT, V, 4><<<nb, kThreads, lds, st>>>(a, part, part_n);
+  if (V <= 8 || a.S <= 8) {
+    if (a.S <= 16) k_route<LT, V, 1, true><<<nb, kThreads, lds, st>>>(a, part, part_n);
+    else k_route<LT, V, 4, V <= 8><<<nb, kThreads, lds, st>>>(a, part, part_n);
+  } else {
+    if (a.S <= 16) k_route<LT, V, 1, V <= 8><<<nb, kThreads, lds, st>>>(a, part, part_n);
+    else k_route<LT, V, 4, V <= 8><<<nb, kThreads, lds, st>>>(a, part, part_n);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || nb == 1) return e;
   k_route_sum<<<(a.E + kSumCols) / kSumCols, kSumCols * kSumSegs, 0, st>>>(part, part_n, nb, a.E, a.counts, a.psum);
@@ -727,9 +832,10 @@ hipError_t launch_v(const RouteArgs& a, hipStream_t st) {
 
 template <int LT, int V>
 hipError_t launch_v(const RouteBackwardArgs& a, hipStream_t st) {
-  const int nb = static_cast<int>(std::min<int64_t>((a.N + 15) / 16, 2048));
-  if (a.S <= 16) k_route_backward<LT, V, 1><<<nb, 256, 0, st>>>(a);
-  else k_route_backward<LT, V, 4><<<nb, 256, 0, st>>>(a);
+  constexpr int kTeams = route_backward_teams(V);
+  const int nb = static_cast<int>(std::min<int64_t>((a.N + kTeams - 1) / kTeams, 2048));
+  if (a.S <= 16) k_route_backward<LT, V, 1><<<nb, 16 * kTeams, 0, st>>>(a);
+  else k_route_backward<LT, V, 4><<<nb, 16 * kTeams, 0, st>>>(a);
   return hipGetLastError();
 }
 
