@@ -390,11 +390,13 @@ __global__ __launch_bounds__(1024) void k_balance_loss(const int32_t* counts, co
 // tokens of a workgroup: their rows of LDS stay under 64 KB
 constexpr int route_backward_teams(int V) { return V <= 32 ? 16 : 8; }
 
+// Three waves a SIMD for 257 .. 512 experts: 12000 x 400 in bf16 14.0 -> 12.5 us; fp32 has more to spill, 15.0 -> 16.0.
+//
 // dl = p (dp - sum p dp), dp_e = dloss coef f_e / T + the chosen slots' gradients; p again from the logits.  The slots'
 // gradients reach the lanes that hold their experts through a row of LDS that holds the loss's
 // part between tokens.
 template <int LT, int V, int SR>
-__global__ __launch_bounds__(16 * route_backward_teams(V)) void k_route_backward(RouteBackwardArgs a) {
+__global__ __launch_bounds__(16 * route_backward_teams(V), LT != DT_F32 && V == 32 ? 3 : 1) void k_route_backward(RouteBackwardArgs a) {
   constexpr int kRouteTeams = route_backward_teams(V);
   typedef typename Elem<LT>::T T;
   typedef Spread<LT, V> Sp;
@@ -506,7 +508,7 @@ __device__ __forceinline__ int bucket_of(int id, int E) { return id >= 0 && id <
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBlocks = 256;
-constexpr int64_t kPlanOneBlock = 4096;
+constexpr int64_t kPlanOneLaunch = 32768;
 constexpr int kMaxBuckets = static_cast<int>(kRouteMaxExperts) + 2;
 
 // pairs per workgroup of the counting and scattering kernels, a multiple of 1024
@@ -648,23 +650,38 @@ __device__ void plan_scatter(const int32_t* ids, int64_t p0, int64_t p1, int E, 
   }
 }
 
-// Up to kPlanOneBlock pairs: everything in one workgroup.
+// Up to kPlanOneLaunch pairs: every workgroup counts all of them, those before its own kPlanThreads apart.  128 experts:
+// 9.6 us for 16384 pairs and 11.6 for 32768, where three launches take 19 and 19; at 131072 it would be 23 against 21.
 __global__ __launch_bounds__(kPlanThreads) void k_plan_small(const int32_t* ids, PlanDesc d, int32_t* plan) {
   __shared__ PlanShared sh;
-  const int E = static_cast<int>(d.E), B = E + 2;
-  plan_count(ids, 0, d.pairs, E, sh.cnt);
-  plan_prefix(sh, B);
-  for (int b = threadIdx.x; b <= B; b += kPlanThreads) {
-    if (b < B) {
-      plan[d.counts + b] = sh.cnt[b];
-      sh.base[b] = sh.offs[b];
-    }
-    plan[d.offsets + b] = sh.offs[b];
-    plan[d.tile128 + b] = sh.tiles[kPlanTileKinds - 1][b];
+  const int E = static_cast<int>(d.E), B = E + 2, pairs = static_cast<int>(d.pairs);
+  const int p0 = blockIdx.x * kPlanThreads;
+  for (int b = threadIdx.x; b < B; b += kPlanThreads) sh.base[b] = sh.cnt[b] = 0;
+  __syncthreads();
+  constexpr int kEach = 8;  // loads that do not wait for each other
+  for (int p = threadIdx.x; p < pairs; p += kEach * kPlanThreads) {
+    int id[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) id[i] = ids[std::min(p + i * kPlanThreads, pairs - 1)];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (p + i * kPlanThreads < pairs) atomicAdd((p + i * kPlanThreads < p0 ? sh.base : sh.cnt) + bucket_of(id[i], E), 1);
   }
-  if (threadIdx.x < kPlanTileKinds) plan[d.totals + threadIdx.x] = sh.tiles[threadIdx.x][B];
+  __syncthreads();
+  for (int b = threadIdx.x; b < B; b += kPlanThreads) sh.cnt[b] += sh.base[b];
+  __syncthreads();
+  plan_prefix(sh, B);
+  for (int b = threadIdx.x; b < B; b += kPlanThreads) sh.base[b] += sh.offs[b];
+  if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b <= B; b += kPlanThreads) {
+      if (b < B) plan[d.counts + b] = sh.cnt[b];
+      plan[d.offsets + b] = sh.offs[b];
+      plan[d.tile128 + b] = sh.tiles[kPlanTileKinds - 1][b];
+    }
+    if (threadIdx.x < kPlanTileKinds) plan[d.totals + threadIdx.x] = sh.tiles[threadIdx.x][B];
+  }
   plan_tiles(sh, d, plan);
-  plan_scatter(ids, 0, d.pairs, E, plan + d.order, sh);
+  plan_scatter(ids, p0, std::min(p0 + kPlanThreads, pairs), E, plan + d.order, sh);
 }
 
 // More: counts per chunk; their prefixes, by one workgroup; places and lists.
@@ -815,7 +832,9 @@ hipError_t launch_v(const RouteArgs& a, hipStream_t st) {
   int32_t* part_n = reinterpret_cast<int32_t*>(part + static_cast<int64_t>(nb) * a.E);
   constexpr int kThreads = route_threads(V);
   const size_t lds = (a.E + 1) * 4 + static_cast<size_t>(kThreads / 64) * 16 * V * 4;
-  if (V <= 8 || a.S <= 8) {
+  // Sorting pays from 4 calls on: 12000 x 400 in bf16 with S = 1, 4 and 8 12.8, 13.8 and 14.8 us with lists, 11.7, 13.8 and
+  // 20.7 without; in fp32 14.6 and 18.4 against 12.9 and 26 with S = 1 and 8.
+  if (V <= 8 || (a.S >= 4 && a.S <= 8)) {
     if (a.S <= 16) k_route<LT, V, 1, true><<<nb, kThreads, lds, st>>>(a, part, part_n);
     else k_route<LT, V, 4, V <= 8><<<nb, kThreads, lds, st>>>(a, part, part_n);
   } else {
@@ -920,8 +939,9 @@ PlanDesc plan_desc(int64_t pairs, int64_t E) {
 
 hipError_t launch_route_plan(const int32_t* ids, int64_t pairs, int64_t E, int32_t* plan, hipStream_t st) {
   const PlanDesc d = plan_desc(pairs, E);
-  if (pairs <= kPlanOneBlock) {
-    k_plan_small<<<1, kPlanThreads, 0, st>>>(ids, d, plan);
+  if (pairs <= kPlanOneLaunch) {
+    const int blocks = static_cast<int>(std::max<int64_t>(1, (pairs + kPlanThreads - 1) / kPlanThreads));
+    k_plan_small<<<blocks, kPlanThreads, 0, st>>>(ids, d, plan);
     return hipGetLastError();
   }
   const int blocks = static_cast<int>((pairs + plan_chunk(pairs) - 1) / plan_chunk(pairs));
