@@ -29,11 +29,14 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 // bits 1..3 of the row (two rows fill the 64 banks, so 16 lanes that read one piece of 16 rows use every bank once),
 // scales [g][row].
 template <int XT>
-__device__ __forceinline__ void load_group(const typename Elem<XT>::T* row, int g, int64_t K, float* v) {
-  load_row8<XT>(row, static_cast<int64_t>(g) * kF8Block + (threadIdx.x & 15) * 8, K, v);
+__device__ __forceinline__ void load_group(const typename Elem<XT>::T* row, int g, int64_t K, Raw8<XT>& r) {
+  r.load(row, static_cast<int64_t>(g) * kF8Block + (threadIdx.x & 15) * 8, K);
 }
-__device__ __forceinline__ void store_group(const float* v, int w, int t, uint8_t* codes, float* scales) {
+template <int XT>
+__device__ __forceinline__ void store_group(const Raw8<XT>& r, int w, int t, uint8_t* codes, float* scales) {
   const int lane = threadIdx.x & 15;
+  float v[8];
+  r.widen(v);
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
@@ -41,7 +44,7 @@ __device__ __forceinline__ void store_group(const float* v, int w, int t, uint8_
   float q[8], ss[8], rr[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) { ss[i] = s; rr[i] = rs; }
-  f8_quotients(v, ss, rr, q);
+  f8_quotients<XT>(v, ss, rr, q);
   *reinterpret_cast<uint2*>(codes + static_cast<size_t>(w) * 128 + (((lane >> 1) ^ (t >> 1 & 7)) * 16) + (lane & 1) * 8) =
       make_uint2(f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7]));
   if (lane == 0) scales[w] = s;
@@ -76,7 +79,7 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
   // raw tokens first: everything waits for them, and loads return in order
   constexpr int kItems = 4;
   typedef typename Elem<RAW < 0 ? 0 : RAW>::T X;
-  float v[RAW >= 0 ? kItems : 1][8];
+  Raw8<RAW < 0 ? 0 : RAW> v[RAW >= 0 ? kItems : 1];
   const int items = a.N * a.G, teams = KS * 4, team = threadIdx.x >> 4;
   if constexpr (RAW >= 0) {
 #pragma unroll
@@ -129,12 +132,12 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       const int w = team + i * teams;
-      if (w < items) store_group(v[i], w, w % a.N, codes, scales);
+      if (w < items) store_group<RAW>(v[i], w, w % a.N, codes, scales);
     }
     for (int w = team + kItems * teams; w < items; w += teams) {
       const int g = w / a.N;
       load_group<RAW>(static_cast<const X*>(a.x) + (w - g * a.N) * a.ldx, g, a.K, v[0]);
-      store_group(v[0], w, w - g * a.N, codes, scales);
+      store_group<RAW>(v[0], w, w - g * a.N, codes, scales);
     }
     __syncthreads();
   }
@@ -286,9 +289,9 @@ __global__ __launch_bounds__(kIdThreads) void k_f8_few_id(FewIdArgs a) {
     const T* x = static_cast<const T*>(a.x);
     for (int w = tid >> 4; w < n * a.G; w += kIdThreads / 16) {
       const int g = w / n, u = w - g * n;
-      float v[8];
+      Raw8<XT> v;
       load_group<XT>(x + static_cast<int64_t>(mine[p0 + u] / a.slots) * a.K, g, a.K, v);
-      store_group(v, w, u, sh, scales);
+      store_group<XT>(v, w, u, sh, scales);
     }
     __syncthreads();
     const int t = std::min(row, n - 1);

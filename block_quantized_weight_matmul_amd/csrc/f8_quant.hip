@@ -21,11 +21,12 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
   return v;
 }
 
+template <int DT>
 __device__ __forceinline__ uint2 codes8(const float* v, float s, float rs) {
   float q[8], ss[8], rr[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) { ss[i] = s; rr[i] = rs; }
-  f8_quotients(v, ss, rr, q);
+  f8_quotients<DT>(v, ss, rr, q);
   return make_uint2(f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7]));
 }
 
@@ -44,7 +45,7 @@ __global__ __launch_bounds__(256) void k_f8_quant_rows(F8QuantArgs a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
   const float s = f8_scale(max16(m));
-  *reinterpret_cast<uint2*>(a.codes_r + t * f8_pad(a.K) + c) = codes8(v, s, f8_inverse(s));
+  *reinterpret_cast<uint2*>(a.codes_r + t * f8_pad(a.K) + c) = codes8<DT>(v, s, f8_inverse(s));
   if (lane == 0) a.scales_r[g * a.N + t] = s;
 }
 
@@ -86,6 +87,7 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, i
   if (!ROWS && !COLS) x += e * a.N * a.K;
   const int64_t c = g * kF8Block + lane * 8;
   const int r0 = team * kTileRows;
+  Raw8<DT> raw[kTileRows];
   float v[kTileRows][8];
   int64_t src[kTileRows];  // row of x, -1 past the end
   if (a.plan) {
@@ -93,10 +95,10 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, i
     const int bucket = mp[0], first = mp[1], end = mp[2];
     if (bucket < 0 || bucket >= a.pd.E) return;  // no expert's pairs: no product reads this group
 #pragma unroll
-    for (int p = 0; p < kTileRows; ++p) {
-      const int at = first + r0 + p;
-      src[p] = at < end ? a.plan[a.pd.order + at] / a.slots : -1;
-    }
+    for (int p = 0; p < kTileRows; ++p) src[p] = a.plan[a.pd.order + std::min(first + r0 + p, end - 1)] / a.slots;
+#pragma unroll
+    for (int p = 0; p < kTileRows; ++p)
+      if (first + r0 + p >= end) src[p] = -1;
   } else {
 #pragma unroll
     for (int p = 0; p < kTileRows; ++p) {
@@ -105,13 +107,12 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, i
     }
   }
 #pragma unroll
-  for (int p = 0; p < kTileRows; ++p) {
-    if (src[p] >= 0) {
-      load_row8<DT>(x + src[p] * a.ldx, c, a.K, v[p]);
-    } else {
+  for (int p = 0; p < kTileRows; ++p) raw[p].load(x + std::max<int64_t>(src[p], 0) * a.ldx, c, a.K);  // absent: row 0
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
-    }
+  for (int p = 0; p < kTileRows; ++p) {
+    raw[p].widen(v[p]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[p][i] = src[p] >= 0 ? v[p][i] : 0.0f;
   }
   if (ROWS) {
 #pragma unroll
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, i
       const float s = f8_scale(max16(m));
       const int64_t r = j * kF8Block + r0 + p;
       if (r < N) {
-        *reinterpret_cast<uint2*>(a.codes_r + r * Kp + c) = codes8(v[p], s, f8_inverse(s));
+        *reinterpret_cast<uint2*>(a.codes_r + r * Kp + c) = codes8<DT>(v[p], s, f8_inverse(s));
         if (lane == 0) a.scales_r[g * N + r] = s;
       }
     }
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, i
         s[n] = sr.x;
         rs[n] = sr.y;
       }
-      f8_quotients(col, s, rs, q);
+      f8_quotients<DT>(col, s, rs, q);
 #pragma unroll
       for (int n = 0; n < 2; ++n)
         *reinterpret_cast<uint32_t*>(lds_piece(tile, lane * 8 + i + n, r0)) = f8_pack4(q[4 * n], q[4 * n + 1], q[4 * n + 2], q[4 * n + 3]);
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, i
     uint2 q[kTileRows];
 #pragma unroll
     for (int p = 0; p < kTileRows; ++p) {
-      q[p] = codes8(v[p], s, rs);
+      q[p] = codes8<DT>(v[p], s, rs);
       const int64_t r = j * kF8Block + r0 + p;
       if (r < N) *reinterpret_cast<uint2*>(a.codes_r + (e * N + r) * Kp + c) = q[p];
     }
