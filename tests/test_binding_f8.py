@@ -139,8 +139,8 @@ def test_c_argument_errors():
     assert lib.qmm_route(p, 0, 4, 8, 9, None, 1, 0.0, p, p, p, p, p, p, 1 << 20, None) == -3   # S > E
     assert lib.qmm_route(p, 0, 4, 128, 65, None, 1, 0.0, p, p, p, p, p, p, 1 << 20, None) == -3
     assert lib.qmm_route(p, 0, 4, 8, 2, None, 2, 0.0, p, p, p, p, p, p, 1 << 20, None) == -1
-    assert lib.qmm_route(p, 0, 4, 8, 2, None, 1, 0.0, p, p, p, p, p, p, 0, None) == -1         # workspace
-    assert lib.qmm_route(p, 0, 4, 8, 2, None, 1, 0.0, p, p, p, p, p, p + 4, 1 << 20, None) == -4
+    assert lib.qmm_route(p, 0, 4096, 8, 2, None, 1, 0.0, p, p, p, p, p, p, 0, None) == -1      # workspace
+    assert lib.qmm_route(p, 0, 4096, 8, 2, None, 1, 0.0, p, p, p, p, p, p + 4, 1 << 20, None) == -4
     assert lib.qmm_route_combine(p, 2, p, 1, 4, 2, 8, p, None) == -2                            # weights' type
     assert lib.qmm_route_combine(p, 0, None, 0, 4, 0, 8, p, None) == -3
     assert lib.qmm_route_combine_backward(p, 0, None, 0, 4, 2, 8, p, p, p, None) == -1
