@@ -158,13 +158,13 @@ class F8Tokens:
 
 def _quantize(x, along_k, along_n):
     _tensor(x, "x", _DT, (2, 3))
+    if x.shape[-1] == 0:
+        raise ValueError("x has no columns")
     if x.dim() == 3:
         if not x.is_contiguous():
             raise ValueError("x of three dimensions must be contiguous")
         x = x.view(-1, x.shape[2])
     N, K = x.shape
-    if K == 0:
-        raise ValueError("x has no columns")
     ld = _rows(x, "x")
     device, d = x.device, x.get_device()
     r = F8Tokens._empty(N, _padded(K), K, device, d) if along_k else None

@@ -518,9 +518,9 @@ qmm_status qmm_f8_wgrad_id(const void *g_codes, const float *g_scales, const voi
  *   loss     fp32 [1] or NULL: the balance loss coef * sum_e f_e P_e with
  *            f_e = E counts[e] / (S T) and P_e = psum[e] / T; 0 when T = 0.
  *   ws       DEVICE, 16-byte aligned, qmm_route_workspace_bytes(N, E).
- * A row with a NaN among its logits, or +inf as its largest, has NaN weights and makes psum
- * and loss NaN.  Sums over the tokens have a fixed order.  N = 0 writes zero counts, psum and
- * loss.
+ * A row that has an expert and a NaN among its logits, or +inf as its largest, has NaN weights
+ * and makes psum and loss NaN.  Sums over the tokens have a fixed order.  N = 0 writes zero
+ * counts, psum and loss.
  *
  * qmm_balance_loss -- the loss from counts and psum, for a caller that adds them over several
  * micro-batches or GPUs first.

@@ -94,6 +94,22 @@ def test_quantize_every_quotient():
         same(t.codes, t.scales, O.quantize_rows(x), f"amax {amax}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_quantize_every_16_bit_quotient(dtype):
+    """Every value of the 17 octaves below the block's largest, which takes every significand (bf16) or every 16th (fp16):
+    448 x / amax is a middle of two codes often, down to the smallest codes."""
+    bits, step = (7, 1) if dtype == "bf16" else (10, 16)
+    largest = 1.0 + np.arange(0, 2 ** bits, step) / 2.0 ** bits
+    x = np.outer(2.0 ** -np.arange(0.0, 17.0), 1.0 + np.arange(2 ** bits) / 2.0 ** bits).ravel()
+    rows = []
+    for i, a in enumerate(largest):
+        v = x[x <= a]
+        v = np.concatenate([v, np.zeros(-v.size % 127)]).reshape(-1, 127) * np.where(i % 2, -1.0, 1.0)
+        rows.append(np.concatenate([np.full((len(v), 1), a), v], 1))
+    t = dev(np.concatenate(rows), DTYPES[dtype])
+    same(*(lambda c: (c.codes, c.scales))(q.f8_quantize(t)), O.quantize_rows(host64(t)))
+
+
 @pytest.mark.parametrize("dtype", sorted(DTYPES))
 def test_quantize_extremes(dtype):
     big = {"f32": 3.0e38, "f16": 65504.0, "bf16": 3.0e38}[dtype]
@@ -307,6 +323,25 @@ def test_many_pairs(pairs_per_token):
     check(m.linear_id(x, dev_u8(ids)), ref, bound)
 
 
+@pytest.mark.parametrize("E", [1, 130, 1024])
+@pytest.mark.parametrize("N,S", [(1024, 1), (1025, 1), (683, 6), (4096, 8), (32769, 1)])
+def test_plan_sizes(N, S, E):
+    """Around the numbers of pairs at which the plan takes another workgroup, and another way."""
+    g = np.random.default_rng([23, N, E])
+    M, K = 8, 16
+    m, values = stack(g, E, M, K)
+    ids = g.integers(-1, E + 1, (N, S)).astype(np.int32)
+    plan = q.route_plan(dev_u8(ids), E)
+    assert np.array_equal(to_host(plan.counts), np.bincount(ids[(ids >= 0) & (ids < E)], minlength=E))
+    assert torch.equal(plan.data[:E + 2], q.route_plan(dev_u8(ids), E).data[:E + 2])
+    x = dev(g.standard_normal((N, K)))
+    y = m.gemm_id(q.f8_quantize(x), plan)
+    none = torch.from_numpy(ids >= E).cuda()
+    assert bool(torch.isnan(y[none]).all())
+    ref, bound = id_reference(quantized_values(x), ids, values, M)
+    check(torch.where(none[:, :, None], torch.zeros_like(y), y), ref, bound)
+
+
 # ---- gradients ---------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", sorted(DTYPES))
@@ -509,3 +544,46 @@ def test_new_weights_are_seen():
     second = m.linear(x)
     assert not torch.equal(first, second)
     assert torch.equal(second, q.F8Matrix.quantize(w[1]).linear(x))
+
+
+# ---- offsets past 32 bits ----------------------------------------------------------------------
+
+def test_outputs_past_32_bits():
+    """More than 2^31 outputs of a product, and of a sum over slots: the last rows are those of a small call."""
+    torch.manual_seed(1)
+    N, M, K = 270000, 8200, 130
+    m = q.F8Matrix.quantize(torch.randn(M, K, device="cuda"))
+    x = torch.randn(N, K, device="cuda").bfloat16()
+    y = m.linear(x)
+    assert torch.equal(y[-300:], m.linear(x[-300:]))
+    out = q.route_combine(y.view(N // 2, 2, M))
+    assert torch.equal(out[-100:], q.route_combine(y[-200:].view(100, 2, M)))
+
+
+def test_quantized_values_past_32_bits():
+    torch.manual_seed(2)
+    N, K = 1050000, 2056
+    x = torch.randn(N, K, device="cuda", dtype=torch.bfloat16)
+    rows, cols = q.f8_quantize_pair(x)
+    last, n = q.f8_quantize(x[-128:]), N % 128
+    assert torch.equal(rows.codes[-128:], last.codes) and torch.equal(rows.scales[:, -128:], last.scales)
+    tail = q.f8_quantize_t(x[-n - 256:])
+    assert torch.equal(cols.codes[:, -384:], tail.codes) and torch.equal(cols.scales[-3:], tail.scales)
+
+
+def test_weights_past_32_bits():
+    E, M, K = 128, 4100, 4352
+    w = torch.randn(M, K, device="cuda", dtype=torch.bfloat16)
+    one = q.F8Matrix.quantize(w)
+    codes = torch.zeros((E, M, K), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((E,) + tuple(one.scales.shape), device="cuda")
+    codes[E - 1], scales[E - 1] = one.codes, one.scales
+    m = q.F8Matrix(codes, scales, M, K, E)
+    for N in (3, 100):
+        x = torch.randn(N, K, device="cuda", dtype=torch.bfloat16)
+        ids = torch.tensor([[E - 1, 0]], dtype=torch.int32, device="cuda").expand(N, 2).contiguous()
+        y = m.linear_id(x, ids)
+        ref = one.linear(x, out_dtype=torch.float32)
+        assert bool((y[:, 1] == 0).all())
+        size = x.double().abs() @ w.double().abs().t()   # either way's error: 2^-10 of the terms (8-bit cores), 2^-8 of the result
+        assert bool(((y[:, 0].double() - ref.double()).abs() <= size * 2.0 ** -9 + ref.double().abs() * 2.0 ** -8).all())

@@ -35,7 +35,8 @@ def compare(r, want, N, label=""):
 
 
 SIZES = [(1, 1, 1), (1, 4, 2), (16, 128, 8), (33, 8, 2), (100, 60, 6), (64, 16, 16), (5, 17, 3), (7, 200, 64),
-         (300, 256, 8), (20, 500, 10), (3, 1000, 64), (9, 1024, 8), (9, 1023, 1), (5000, 64, 4)]
+         (300, 256, 8), (20, 500, 10), (3, 1000, 64), (9, 1024, 8), (9, 1023, 1), (5000, 64, 4),
+         (37, 201, 3), (37, 203, 4), (300, 399, 7), (37, 402, 12), (140, 402, 20), (37, 777, 5), (130, 513, 2)]
 
 
 @pytest.mark.parametrize("dtype", sorted(DTYPES))
@@ -61,6 +62,24 @@ def test_ties_go_to_the_lower_index():
         r = q.route(l, 4)
         assert r.ids.tolist()[0] == [0, 1, 2, 3] and r.ids.tolist()[1] == [E - 2, E - 1, 0, 1]
         assert r.ids.tolist()[2] == [0, 1, 2, 3]
+
+
+@pytest.mark.parametrize("S", [3, 8, 17, 40])
+@pytest.mark.parametrize("E", [70, 131, 250, 500, 1000])
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_order_of_extreme_logits(dtype, E, S):
+    """The largest and lowest numbers, subnormal ones, both zeros and close neighbours, each several times, in any place."""
+    g = np.random.default_rng([32, E, S])
+    t = DTYPES[dtype]
+    top, tiny = torch.finfo(t).max, float(torch.finfo(t).smallest_normal)
+    step = float(torch.finfo(t).eps)
+    some = [top, -top, top / 2, -top / 2, tiny, -tiny, tiny * step, -tiny * step, 0.0, -0.0, 1.0, 1.0 + step, -1.0, -1.0 - step, -np.inf]
+    l = dev(g.choice(some, (60, E)), t)
+    got = to_host(q.route(l, S).ids)
+    v = host64(l)
+    order = np.argsort(-v, axis=1, kind="stable")[:, :S]
+    want = np.where(np.take_along_axis(v, order, 1) > -np.inf, order, -1)
+    assert np.array_equal(got, want)
 
 
 def test_masks_that_leave_little():
@@ -274,3 +293,15 @@ def test_route_in_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(eager, outs)), rep
         _ = l.float().clamp(min=-10).sum().item()
+
+
+def test_logits_past_32_bits():
+    """More than 2^31 logits: the last rows, and their gradients, are those of a small call."""
+    N, E, S = 2100000, 1023, 2
+    l = torch.randn(N, E, device="cuda", dtype=torch.bfloat16)
+    r, few = q.route(l, S), q.route(l[-50:], S)
+    assert torch.equal(r.ids[-50:], few.ids) and torch.equal(r.weights[-50:], few.weights)
+    assert int(r.counts[:E].long().sum()) == N * S and int(r.counts[E]) == N
+    dw = torch.randn(N, S, device="cuda")
+    d = q.route_backward(l, r, dw)
+    assert torch.equal(d[-50:], q.route_backward(l[-50:], few, dw[-50:]))
