@@ -76,7 +76,7 @@ hipError_t launch_f8_few(const F8Desc& m, const uint8_t* xc, const float* xs, in
 // Expert-indexed: rows of x are tokens (slots = S) or pairs (slots = 1); y [pairs][M].
 hipError_t launch_f8_gemm_id(const F8Desc& m, const uint8_t* xc, const float* xs, int64_t pairs, int slots,
                              const int32_t* plan, void* y, int yt, hipStream_t s);
-bool f8_linear_id_fused(const F8Desc& m, int64_t pairs, int slots);
+bool f8_linear_id_fused(const F8Desc& m, int64_t pairs);
 hipError_t launch_f8_linear_id(const F8Desc& m, const void* x, int xt, int64_t pairs, int slots, const int32_t* ids,
                                void* y, int yt, hipStream_t s);
 // Weight gradients: dw[M][K] = g^T x over N tokens, both quantized along the tokens (codes_c layout); with a plan

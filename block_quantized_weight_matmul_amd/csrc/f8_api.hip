@@ -277,7 +277,7 @@ qmm_status qmm_route_plan(const int32_t* ids, int64_t N, int64_t S, int64_t E, v
 size_t qmm_f8_linear_id_workspace_bytes(const qmm_f8_matrix* h, int64_t N, int64_t S, int x_per_slot) {
   if (!h || N <= 0 || S < 1 || S > 64 || N > qmm::kRouteMaxPairs || N * S > qmm::kRouteMaxPairs ||
       h->d.n_experts > qmm::kRouteMaxExperts ||
-      qmm::f8_linear_id_fused(h->d, N * S, x_per_slot ? 1 : static_cast<int>(S)))
+      qmm::f8_linear_id_fused(h->d, N * S))
     return 0;
   return token_bytes(x_per_slot ? N * S : N, h->d.Kp) + qmm_route_plan_bytes(N * S, h->d.n_experts);
 }
@@ -312,7 +312,7 @@ qmm_status qmm_f8_linear_id(const qmm_f8_matrix* h, const void* x, qmm_dtype xt,
   const int slots = x_per_slot ? 1 : static_cast<int>(S);
   const int64_t rows = x_per_slot ? N * S : N;
   hipError_t e;
-  if (qmm::f8_linear_id_fused(h->d, N * S, slots)) {
+  if (qmm::f8_linear_id_fused(h->d, N * S)) {
     e = qmm::launch_f8_linear_id(h->d, x, xt, N * S, slots, ids, y, yt, st);
   } else {
     qmm::F8QuantArgs a{};

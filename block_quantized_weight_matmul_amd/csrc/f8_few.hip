@@ -339,7 +339,7 @@ hipError_t few_tokens(const FewArgs& a, hipStream_t st) {
   if constexpr (RAW >= 0) {
     return a.G <= 64 ? few_run<1, RAW, OT, 2, 16>(a, st) : few_run<1, RAW, OT, 3, 16>(a, st);
   } else {
-    if (a.N > 16) return a.G <= 32 ? few_run<2, RAW, OT, 2, 8>(a, st) : few_run<2, RAW, OT, 3, 8>(a, st);
+    if (a.N > 16) return few_run<2, RAW, OT, 2, 8>(a, st);
     return a.G <= 64 ? few_run<1, RAW, OT, 2, 16>(a, st) : few_run<1, RAW, OT, 5, 8>(a, st);
   }
 }
@@ -381,9 +381,11 @@ hipError_t few_id_out(const FewIdArgs& a, int yt, dim3 grid, size_t lds, hipStre
 
 }  // namespace
 
-// Above, the tiled kernel reads the tokens once a tile instead of once a workgroup (4096 x 2560: 32 tokens 7.4 us here,
-// 64 tokens 9.9 us here and 9 there; 2560 x 9728 at 64 tokens 26 and 17).
-bool f8_few_tokens(const F8Desc&, int64_t N) { return N <= 32; }
+// Above 16 tokens a workgroup's 8 waves fill a CU's registers, so that more than one workgroup a CU makes another round, and
+// long rows outlast the tiled kernel that divides K: 17 and 32 tokens of 4096 x 2560 take 5.9 and 6.9 us here and 7.8 in
+// tiles, of 5120 x 2560 9.4 and 11.4 against 7.9 and 9.1, of 1280 x 9728 13.4 and 17.0 against 11.7.  Above 32 tokens
+// (4096 x 2560, 64: 9.9 us) the tiles read them less often.
+bool f8_few_tokens(const F8Desc& m, int64_t N) { return N <= 16 || (N <= 32 && m.M <= 16 * m.cus && m.Kp <= 4096); }
 
 hipError_t launch_f8_few(const F8Desc& m, const uint8_t* xc, const float* xs, int64_t N, void* y, int yt, hipStream_t st) {
   FewArgs a = few_args(m, N, y, yt);
@@ -409,7 +411,7 @@ hipError_t launch_f8_linear(const F8Desc& m, const void* x, int xt, int64_t ldx,
   }
 }
 
-bool f8_linear_id_fused(const F8Desc& m, int64_t pairs, int) {
+bool f8_linear_id_fused(const F8Desc& m, int64_t pairs) {
   return pairs <= kIdPairs && 16 * (m.Kp + m.Kp / kF8Block * 4) <= kFusedLds;
 }
 
