@@ -56,23 +56,33 @@ __device__ __forceinline__ uint8_t* lds_piece(uint8_t* tile, int col, int r) {
   return tile + col * 128 + (((r >> 3) ^ (col >> 3)) * 8) + (r & 7);
 }
 
-constexpr int kTileThreads = 512;  // 32 teams of 16 lanes; a thread holds 4 rows x 8 columns
-constexpr int kTileRows = 4;
+// A tile's threads are teams of 16 lanes; a thread holds R rows x 8 columns.  4 rows a thread keep half the values in
+// registers that 8 would, and twice the threads on a tile (777 x 515 fp32, 35 tiles, 11.6 -> 6.3 us).  2 suit the two
+// quotients a value of rows and columns at once (4096 x 4096 in bf16 20.0 -> 18.8 us, 777 x 515 in fp32 6.5 -> 6.6), not
+// one (columns alone 12.9 -> 14.6; weights of 4096 x 2560 10.8 -> 12.0).
+constexpr int tile_rows(bool rows, bool cols) { return rows && cols ? 2 : 4; }
+constexpr int tile_threads(int R) { return 128 / R * 16; }
 
-// codes of 4 rows of one column, transposed from four words of 4 columns each
-__device__ __forceinline__ uint32_t column4(const uint2* q, int j) {
+// codes of R rows of one column, transposed from R words of 4 columns each, at dst
+template <int R>
+__device__ __forceinline__ void store_column(uint8_t* dst, uint32_t w) {
+  if constexpr (R == 4) *reinterpret_cast<uint32_t*>(dst) = w;
+  else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(w);
+}
+template <int R>
+__device__ __forceinline__ uint32_t column(const uint2* q, int j) {
   uint32_t w = 0;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) w |= (((j < 4 ? q[p].x : q[p].y) >> (8 * (j & 3))) & 0xFFu) << (8 * p);
+  for (int p = 0; p < R; ++p) w |= (((j < 4 ? q[p].x : q[p].y) >> (8 * (j & 3))) & 0xFFu) << (8 * p);
   return w;
 }
 
 // A 128 x 128 tile in registers.  ROWS: one scale per row of the tile; COLS: one per column, codes transposed; neither:
-// one for the tile, codes as they stand and (codes_c given) transposed.  4 rows a thread keep half the values in
-// registers that 8 would, and twice the threads on a tile: 777 x 515 fp32, 35 tiles, 11.6 -> 6.3 us.
+// one for the tile, codes as they stand and (codes_c given) transposed.
 template <int DT, bool ROWS, bool COLS>
-__global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, int64_t w_rows_pad) {
+__global__ __launch_bounds__(tile_threads(tile_rows(ROWS, COLS))) void k_f8_quant_tile(F8QuantArgs a, int64_t w_rows_pad) {
   typedef typename Elem<DT>::T T;
+  constexpr int R = tile_rows(ROWS, COLS), kTileThreads = tile_threads(R);
   __shared__ __align__(16) uint8_t tile[128 * 128];
   __shared__ uint32_t cmax[kTileThreads / 64][128];
   __shared__ float2 cscale[128];  // scale and its inverse
@@ -86,37 +96,37 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, i
   const int64_t e = blockIdx.y;  // expert of a weight
   if (!ROWS && !COLS) x += e * a.N * a.K;
   const int64_t c = g * kF8Block + lane * 8;
-  const int r0 = team * kTileRows;
-  Raw8<DT> raw[kTileRows];
-  float v[kTileRows][8];
-  int64_t src[kTileRows];  // row of x, -1 past the end
+  const int r0 = team * R;
+  Raw8<DT> raw[R];
+  float v[R][8];
+  int64_t src[R];  // row of x, -1 past the end
   if (a.plan) {
     const int32_t* mp = a.plan + a.pd.map[kPlanTileKinds - 1] + 3 * j;
     const int bucket = mp[0], first = mp[1], end = mp[2];
     if (bucket < 0 || bucket >= a.pd.E) return;  // no expert's pairs: no product reads this group
 #pragma unroll
-    for (int p = 0; p < kTileRows; ++p) src[p] = a.plan[a.pd.order + std::min(first + r0 + p, end - 1)] / a.slots;
+    for (int p = 0; p < R; ++p) src[p] = a.plan[a.pd.order + std::min(first + r0 + p, end - 1)] / a.slots;
 #pragma unroll
-    for (int p = 0; p < kTileRows; ++p)
+    for (int p = 0; p < R; ++p)
       if (first + r0 + p >= end) src[p] = -1;
   } else {
 #pragma unroll
-    for (int p = 0; p < kTileRows; ++p) {
+    for (int p = 0; p < R; ++p) {
       src[p] = j * kF8Block + r0 + p;
       if (src[p] >= N) src[p] = -1;
     }
   }
 #pragma unroll
-  for (int p = 0; p < kTileRows; ++p) raw[p].load(x + std::max<int64_t>(src[p], 0) * a.ldx, c, a.K);  // absent: row 0
+  for (int p = 0; p < R; ++p) raw[p].load(x + std::max<int64_t>(src[p], 0) * a.ldx, c, a.K);  // absent: row 0
 #pragma unroll
-  for (int p = 0; p < kTileRows; ++p) {
+  for (int p = 0; p < R; ++p) {
     raw[p].widen(v[p]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[p][i] = src[p] >= 0 ? v[p][i] : 0.0f;
   }
   if (ROWS) {
 #pragma unroll
-    for (int p = 0; p < kTileRows; ++p) {
+    for (int p = 0; p < R; ++p) {
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[p][i]));
@@ -135,7 +145,7 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, i
     for (int i = 0; i < 8; ++i) {
       uint32_t m = 0;
 #pragma unroll
-      for (int p = 0; p < kTileRows; ++p) m = max(m, abs_bits(v[p][i]));
+      for (int p = 0; p < R; ++p) m = max(m, abs_bits(v[p][i]));
       m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
       m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
       if ((team & 3) == 0) cmax[wave][lane * 8 + i] = m;
@@ -152,25 +162,25 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, i
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
+    for (int i = 0; i < 8; i += 8 / R) {
       float col[8], q[8], s[8], rs[8];
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        const float2 sr = cscale[lane * 8 + i + n / 4];
-        col[n] = v[n % 4][i + n / 4];
+        const float2 sr = cscale[lane * 8 + i + n / R];
+        col[n] = v[n % R][i + n / R];
         s[n] = sr.x;
         rs[n] = sr.y;
       }
       f8_quotients<DT>(col, s, rs, q);
+      const uint32_t w[2] = {f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7])};
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-        *reinterpret_cast<uint32_t*>(lds_piece(tile, lane * 8 + i + n, r0)) = f8_pack4(q[4 * n], q[4 * n + 1], q[4 * n + 2], q[4 * n + 3]);
+      for (int n = 0; n < 8 / R; ++n) store_column<R>(lds_piece(tile, lane * 8 + i + n, r0), w[n * R / 4] >> (n * R % 4 * 8));
     }
   }
   if (!ROWS && !COLS) {
     uint32_t m = 0;
 #pragma unroll
-    for (int p = 0; p < kTileRows; ++p)
+    for (int p = 0; p < R; ++p)
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[p][i]));
     m = max16(m);
@@ -180,19 +190,19 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, i
 #pragma unroll
     for (int t = 0; t < kTileThreads / 16; ++t) m = max(m, cmax[0][t]);
     const float s = f8_scale(m), rs = f8_inverse(s);
-    const int64_t G = Kp / kF8Block, R = f8_pad(N) / kF8Block;
-    uint2 q[kTileRows];
+    const int64_t G = Kp / kF8Block, blocks = f8_pad(N) / kF8Block;
+    uint2 q[R];
 #pragma unroll
-    for (int p = 0; p < kTileRows; ++p) {
+    for (int p = 0; p < R; ++p) {
       q[p] = codes8<DT>(v[p], s, rs);
       const int64_t r = j * kF8Block + r0 + p;
       if (r < N) *reinterpret_cast<uint2*>(a.codes_r + (e * N + r) * Kp + c) = q[p];
     }
-    if (threadIdx.x == 0) a.scales_r[(e * R + j) * G + g] = s;
+    if (threadIdx.x == 0) a.scales_r[(e * blocks + j) * G + g] = s;
     if (!a.codes_c) return;
-    if (threadIdx.x == 0) a.scales_c[(e * G + g) * R + j] = s;
+    if (threadIdx.x == 0) a.scales_c[(e * G + g) * blocks + j] = s;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t*>(lds_piece(tile, lane * 8 + i, r0)) = column4(q, i);
+    for (int i = 0; i < 8; ++i) store_column<R>(lds_piece(tile, lane * 8 + i, r0), column<R>(q, i));
   }
   if (COLS || !ROWS) {
     __syncthreads();
@@ -209,8 +219,9 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_quant_tile(F8QuantArgs a, i
 }
 
 // The codes of the transposed matrix: the same bytes, tile by tile.
-__global__ __launch_bounds__(kTileThreads) void k_f8_transpose(const uint8_t* codes, const float* scales, int64_t M,
+__global__ __launch_bounds__(tile_threads(4)) void k_f8_transpose(const uint8_t* codes, const float* scales, int64_t M,
                                                                int64_t K, uint8_t* codes_t, float* scales_t) {
+  constexpr int kTileRows = 4, kTileThreads = tile_threads(kTileRows);
   __shared__ __align__(16) uint8_t tile[128 * 128];
   const int lane = threadIdx.x & 15, team = threadIdx.x >> 4, r0 = team * kTileRows;
   const int64_t Kp = f8_pad(K), Mp = f8_pad(M), G = Kp / kF8Block, R = Mp / kF8Block;
@@ -222,7 +233,7 @@ __global__ __launch_bounds__(kTileThreads) void k_f8_transpose(const uint8_t* co
     q[p] = r < M ? *reinterpret_cast<const uint2*>(codes + (e * M + r) * Kp + g * kF8Block + lane * 8) : make_uint2(0, 0);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t*>(lds_piece(tile, lane * 8 + i, r0)) = column4(q, i);
+  for (int i = 0; i < 8; ++i) store_column<kTileRows>(lds_piece(tile, lane * 8 + i, r0), column<kTileRows>(q, i));
   if (threadIdx.x == 0) scales_t[(e * G + g) * R + j] = scales[(e * R + j) * G + g];
   __syncthreads();
 #pragma unroll
@@ -247,6 +258,14 @@ __global__ __launch_bounds__(256) void k_f8_dequantize(const uint8_t* codes, con
   out[r * K + k] = to_elem<DT>(v * s);
 }
 
+template <int DT, bool ROWS, bool COLS>
+hipError_t run_tiles(const F8QuantArgs& a, int64_t tiles, int64_t E, int64_t rows_pad, hipStream_t st) {
+  if (tiles > INT_MAX) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(E));
+  k_f8_quant_tile<DT, ROWS, COLS><<<grid, tile_threads(tile_rows(ROWS, COLS)), 0, st>>>(a, rows_pad);
+  return hipGetLastError();
+}
+
 template <int DT>
 hipError_t quantize_dt(const F8QuantArgs& a, hipStream_t st) {
   const int64_t G = f8_pad(a.K) / kF8Block;
@@ -256,20 +275,12 @@ hipError_t quantize_dt(const F8QuantArgs& a, hipStream_t st) {
     return hipGetLastError();
   }
   const int64_t tiles = a.plan ? a.pd.cap[kPlanTileKinds - 1] : (a.N + kF8Block - 1) / kF8Block;
-  if (tiles * G > INT_MAX) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(tiles * G));
-  if (a.codes_r) k_f8_quant_tile<DT, true, true><<<grid, kTileThreads, 0, st>>>(a, 0);
-  else k_f8_quant_tile<DT, false, true><<<grid, kTileThreads, 0, st>>>(a, 0);
-  return hipGetLastError();
+  return a.codes_r ? run_tiles<DT, true, true>(a, tiles * G, 1, 0, st) : run_tiles<DT, false, true>(a, tiles * G, 1, 0, st);
 }
 
 template <int DT>
 hipError_t quantize_weight_dt(const F8QuantArgs& a, int64_t E, hipStream_t st) {
-  const int64_t tiles = f8_pad(a.K) / kF8Block * (f8_pad(a.N) / kF8Block);
-  if (tiles > INT_MAX) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(E));
-  k_f8_quant_tile<DT, false, false><<<grid, kTileThreads, 0, st>>>(a, f8_pad(a.N));
-  return hipGetLastError();
+  return run_tiles<DT, false, false>(a, f8_pad(a.K) / kF8Block * (f8_pad(a.N) / kF8Block), E, f8_pad(a.N), st);
 }
 
 }  // namespace
@@ -306,7 +317,7 @@ hipError_t launch_f8_transpose(const F8Desc& m, uint8_t* codes_t, float* scales_
   const int64_t tiles = m.Kp / kF8Block * (f8_pad(m.M) / kF8Block);
   if (tiles > INT_MAX) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(m.n_experts));
-  k_f8_transpose<<<grid, kTileThreads, 0, st>>>(m.codes, m.scales, m.M, m.K, codes_t, scales_t);
+  k_f8_transpose<<<grid, tile_threads(4), 0, st>>>(m.codes, m.scales, m.M, m.K, codes_t, scales_t);
   return hipGetLastError();
 }
 
