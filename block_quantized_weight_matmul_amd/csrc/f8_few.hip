@@ -4,6 +4,8 @@
 // its groups' codes straight into the registers of the matrix instruction (16 rows x 128 bytes, whole cache lines),
 // keeps its partial outputs, and the workgroup adds the waves' partials in wave order through LDS.  Nothing but the
 // partials and, for raw tokens, the tokens' codes passes through LDS.  Two batches of groups are in flight per wave.
+// One token of 4096 x 2560 takes 3.6 us (10.5 MB, an empty launch 1.5), of 2560 x 9728 9.1 (25 MB).  The expert form: 32
+// pairs of 128 experts of 4096 x 512 13.6 us for 62 MB.
 #include <algorithm>
 #include <climits>
 

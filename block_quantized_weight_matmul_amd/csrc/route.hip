@@ -229,6 +229,9 @@ __device__ __forceinline__ float loss_part(int count, float psum, float T, int E
   return T > 0.0f ? static_cast<float>(count) * E / (S * T) * psum : 0.0f;
 }
 
+// 16384 x 128 in bf16, S = 8: 7.0 us, 4 MB read; bound by vector operations (keys, sorting, exponentials: some 400 a wave
+// of four tokens) and the latency of one pass.  12000 x 400: 14.8 us in bf16, 18.4 in fp32.
+//
 // part, part_n: the workgroups' sums over their rows, [E] and [E + 1] each.  A single workgroup writes the results itself.
 template <int LT, int V, int SR, bool LIST>
 __global__ __launch_bounds__(route_threads(V)) void k_route(RouteArgs a, float* part, int32_t* part_n) {
@@ -341,7 +344,7 @@ constexpr int kSumCols = 32, kSumSegs = 32;
 // Adds the workgroups' partials: a workgroup takes 32 experts, a thread every 32nd partial of one, and the threads' sums
 // are added in order.  The loss, which needs all of them, is a launch of its own: one workgroup for everything waited 17
 // us for 256 partials of 128 experts, and a last workgroup that knows itself by a counter 14 us, most of it the fence
-// that makes the other dies' sums visible.  This way it is 3.4 us and 2.6.
+// that makes the other dies' sums visible.  This way it is 3.1 us and 1.6.
 __global__ __launch_bounds__(kSumCols * kSumSegs) void k_route_sum(const float* part, const int32_t* part_n, int blocks,
                                                                    int E, int32_t* counts, float* psum) {
   __shared__ float sp[kSumSegs][kSumCols + 1];
@@ -390,7 +393,7 @@ __global__ __launch_bounds__(1024) void k_balance_loss(const int32_t* counts, co
 // tokens of a workgroup: their rows of LDS stay under 64 KB
 constexpr int route_backward_teams(int V) { return V <= 32 ? 16 : 8; }
 
-// Three waves a SIMD for 257 .. 512 experts: 12000 x 400 in bf16 14.0 -> 12.5 us; fp32 has more to spill, 15.0 -> 16.0.
+// 16384 x 128 in bf16 5.7 us, 8.4 MB.  Three waves a SIMD for 257 .. 512 experts: 12000 x 400 in bf16 14.0 -> 12.5 us; fp32 has more to spill, 15.0 -> 16.0.
 //
 // dl = p (dp - sum p dp), dp_e = dloss coef f_e / T + the chosen slots' gradients; p again from the logits.  The slots'
 // gradients reach the lanes that hold their experts through a row of LDS that holds the loss's
@@ -747,7 +750,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t* id
 
 // ---- weighted sum of the slots ------------------------------------------------------------------
 
-// WT: type of the weights, -1 for none (a plain sum).  8 columns a thread.
+// WT: type of the weights, -1 for none (a plain sum).  8 columns a thread.  Bound by memory: 2048 x 8 x 4096 in bf16 22.8
+// us, 6.6 TB/s.
 template <int YT, int WT, bool VEC>
 __global__ __launch_bounds__(256) void k_combine(const typename Elem<YT>::T* y, const void* w, int64_t N, int S, int64_t M,
                                                  typename Elem<YT>::T* out) {
@@ -775,6 +779,7 @@ __global__ __launch_bounds__(256) void k_combine(const typename Elem<YT>::T* y, 
 }
 
 // One token a workgroup, its slots dealt to the waves: dy = w dout (one rounding to fp32, one to the type), dw = <y, dout>.
+// Bound by memory: 2048 x 8 x 4096 in bf16 54 us, 5.3 TB/s.
 template <int YT, int WT, bool VEC>
 __global__ __launch_bounds__(256) void k_combine_backward(const typename Elem<YT>::T* y, const typename Elem<WT>::T* w, int S,
                                                           int64_t M, const typename Elem<YT>::T* dout,
