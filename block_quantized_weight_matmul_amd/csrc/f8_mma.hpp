@@ -11,8 +11,8 @@
 //   fp32 outputs    v_mfma_f32_16x16x32_f16 on the codes converted to fp16, which holds every e4m3 value: the same sums
 //                   kept to 24 bits (1e-8), at half the rate and two conversions a register.
 // Weight rows are the A rows of the instruction and tokens its columns, so that a lane holds 4 consecutive outputs of one
-// token and its token scale is one register.  The 128 values of a group may reach the instruction in any order as long as both operands use the
-// same one: lane (row l & 15, quarter l >> 4) takes bytes 32 * quarter .. + 31 of its row.
+// token and its token scale is one register.  The 128 values of a group may reach the instruction in any order as long as
+// both operands use the same one: lane (row l & 15, quarter l >> 4) takes bytes 32 * quarter .. + 31 of its row.
 #pragma once
 
 #include "f8.hpp"

@@ -3,8 +3,8 @@
 //
 // Router: 16 lanes (one DPP row) hold a token, V experts a lane, so that a reduction over the experts is four DPP steps;
 // nothing but the logits is read.  A lane's experts lie in runs of 16 bytes of logits with the other lanes' runs between:
-// loads and stores of V consecutive experts a lane took 1.2 times as long at 400 experts.  Sums over tokens (probabilities per expert) go through one partial
-// per workgroup, added in a fixed order: the same input gives the same bits.
+// loads and stores of V consecutive experts a lane took 1.2 times as long at 400 experts.  Sums over tokens (probabilities
+// per expert) go through one partial per workgroup, added in a fixed order: the same input gives the same bits.
 #include <algorithm>
 #include <climits>
 
@@ -398,7 +398,8 @@ constexpr int route_backward_teams(int V) { return V <= 32 ? 16 : 8; }
 // 16384 x 128 in bf16 5.7 us for 8.4 MB: vector operations and the latency of one pass.  Three waves a SIMD for 257 .. 512
 // experts: 12000 x 400 in bf16 14.0 -> 12.5 us; fp32 has more to spill, 15.0 -> 16.0.
 template <int LT, int V, int SR>
-__global__ __launch_bounds__(16 * route_backward_teams(V), LT != DT_F32 && V == 32 ? 3 : 1) void k_route_backward(RouteBackwardArgs a) {
+__global__ __launch_bounds__(16 * route_backward_teams(V), LT != DT_F32 && V == 32 ? 3 : 1)
+void k_route_backward(RouteBackwardArgs a) {
   constexpr int kRouteTeams = route_backward_teams(V);
   typedef typename Elem<LT>::T T;
   typedef Spread<LT, V> Sp;
