@@ -380,20 +380,21 @@ int store_vec16(const void* y, int64_t M, int ot) {
 // The tiles, the workgroups of each that a CU holds at once, and what one stage (128 values of K) of 1 .. per_cu of
 // them costs there, in us: 4096 x 4096 x 2560, 8192^3 and 512 x 4096 x 2560 with a 16-bit output.  A call takes the
 // tile with the least estimated time; against measurements of nine shapes the estimate is within 8%, and it is the
-// last round of a launch, its CUs part-filled, that decides (dx of 4096 x 2560, 32 stages: 256 x 256 tiles 60 us, 128 x
-// 128 67, 64 x 64 74; 512 x 4096: 33, 20, 14).
+// last round of a launch, its CUs part-filled, that decides (dx of 4096 x 2560, 32 stages: 256 x 256 tiles 60 us, 256 x
+// 192 53, 128 x 128 67, 64 x 64 74; 512 x 4096: 256 x 256 33, 128 x 128 20, 64 x 64 14).
 struct TileKind {
   int tm, tn, per_cu;
   float round;   // prologue and epilogue of a round
   float us[4];
 };
-enum { TILE_256 = 0, TILE_128 = 1, TILE_128_64 = 2, TILE_64 = 3, TILE_128_32 = 4 };
+enum { TILE_256 = 0, TILE_128 = 1, TILE_128_64 = 2, TILE_64 = 3, TILE_128_32 = 4, TILE_256_192 = 5 };
 constexpr TileKind kTiles[] = {
     {256, 256, 1, 5.0f, {1.95f}},
     {128, 128, 2, 2.0f, {0.85f, 1.21f}},
     {128, 64, 3, 1.5f, {0.52f, 0.79f, 1.07f}},
     {64, 64, 4, 1.0f, {0.33f, 0.48f, 0.75f, 0.99f}},
     {128, 32, 4, 1.5f, {0.50f, 0.80f, 1.10f, 1.40f}},  // experts only
+    {256, 192, 1, 4.5f, {1.50f}},
 };
 
 // tiles: workgroups of a launch, of `stages` stages each
@@ -413,14 +414,14 @@ struct DensePlan {
 constexpr int kMinShare = 4;                              // stages
 constexpr int64_t kMaxSlabs = int64_t(64) << 20;          // bytes
 DensePlan dense_plan(int64_t M, int64_t N, int64_t many, double stages, bool f32, bool may_split, int cus) {
-  const int kinds[] = {TILE_128, TILE_128_64, TILE_64, TILE_256};
+  const int kinds[] = {TILE_128, TILE_128_64, TILE_64, TILE_256, TILE_256_192};
   DensePlan best{TILE_128, 1};
   float cost = INFINITY;
-  for (int i = 0; i < (f32 ? 3 : 4); ++i) {
+  for (int i = 0; i < (f32 ? 3 : 5); ++i) {
     const TileKind& k = kTiles[kinds[i]];
     const double tiles = static_cast<double>((M + k.tm - 1) / k.tm) * static_cast<double>((N + k.tn - 1) / k.tn) * static_cast<double>(many);
     for (int s = 1; s <= 16; s *= 2) {
-      if (s > 1 && (!may_split || kinds[i] == TILE_256 || kinds[i] == TILE_128 || stages < s * kMinShare || s * M * N * 4 > kMaxSlabs)) break;
+      if (s > 1 && (!may_split || kinds[i] == TILE_256 || kinds[i] == TILE_256_192 || kinds[i] == TILE_128 || stages < s * kMinShare || s * M * N * 4 > kMaxSlabs)) break;
       // a second launch, and the slabs written and read
       const float c = tile_cost(k, tiles * s, std::ceil(stages / s), cus) + (s > 1 ? 3.0f + static_cast<float>(s * M * N) * 8 / 4e6f : 0.0f);
       if (c < cost) {
@@ -461,6 +462,7 @@ hipError_t run_dense(GemmArgs& a, int ot, int64_t many, const DensePlan& plan, f
   }
   switch (plan.kind) {
     case TILE_256: return run_tile<256, 256, 2, 4, MODE>(a, ot, blocks, st);
+    case TILE_256_192: return run_tile<256, 192, 4, 2, MODE>(a, ot, blocks, st);
     case TILE_128: return run_tile<128, 128, 2, 2, MODE>(a, ot, blocks, st);
     case TILE_128_64: return run_tile<128, 64, 2, 2, MODE>(a, ot, blocks, st);
     default: return run_tile<64, 64, 2, 2, MODE>(a, ot, blocks, st);
