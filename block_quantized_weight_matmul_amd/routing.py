@@ -18,7 +18,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from ._lib import lib
-from .f8 import _DT, _call, _out, _place, _shape, _tensor
+from .f8 import _DT, _call, _empty2, _out, _place, _shape, _tensor
 
 
 class Routing(NamedTuple):
@@ -84,6 +84,9 @@ def _logits(logits, valid):
     return device
 
 
+_route_need = {}  # workspace bytes of the sizes seen
+
+
 def route(logits: torch.Tensor, S: int, normalise: bool = True, coef: float = 0.0,
           valid: Optional[torch.Tensor] = None) -> Routing:
     """Softmax over logits [N, E], the S largest experts of each row and the balance loss.  valid [N] (uint8 or bool):
@@ -94,10 +97,11 @@ def route(logits: torch.Tensor, S: int, normalise: bool = True, coef: float = 0.
     if not 1 <= S <= min(E, 64):
         raise ValueError(f"S={S} outside [1, {min(E, 64)}]")
     on = logits.device
-    ids = torch.empty((N, S), dtype=torch.int32, device=on)
-    weights = torch.empty((N, S), dtype=torch.float32, device=on)
+    ids, weights = _empty2(N, S, torch.int32, on), _empty2(N, S, torch.float32, on)
     counts = torch.empty(E + 1, dtype=torch.int32, device=on)
-    nb = lib.qmm_route_workspace_bytes(N, E)
+    nb = _route_need.get((N, E))
+    if nb is None:
+        nb = _route_need[N, E] = lib.qmm_route_workspace_bytes(N, E)
     # sums over the rows, the loss and the workspace in one allocation
     pad = (E + 1 + 3) // 4 * 4
     buf = torch.empty(pad + nb // 4, dtype=torch.float32, device=on)
