@@ -378,10 +378,10 @@ int store_vec16(const void* y, int64_t M, int ot) {
 }
 
 // The tiles, the workgroups of each that a CU holds at once, and what one stage (128 values of K) of 1 .. per_cu of
-// them costs there, in us: 4096 x 4096 x 2560, 8192^3 and 512 x 4096 x 2560 with a 16-bit output.  A call takes the
-// tile with the least estimated time; against measurements of nine shapes the estimate is within 8%, and it is the
-// last round of a launch, its CUs part-filled, that decides (dx of 4096 x 2560, 32 stages: 256 x 256 tiles 60 us, 256 x
-// 192 53, 128 x 128 67, 64 x 64 74; 512 x 4096: 256 x 256 33, 128 x 128 20, 64 x 64 14).
+// them costs there, in us, from launches of 1 .. 8 of them a CU and 8, 20 and 60 stages with a 16-bit output.  A call takes
+// the tile with the least estimated time, which is within 12% of the measured one at 20 stages; it is the last round of a
+// launch, its CUs part-filled, that decides (dx of 4096 x 2560, 32 stages: 256 x 256 tiles 60 us, 256 x 192 53, 128 x 128
+// 67, 64 x 64 74; 512 x 4096: 256 x 256 33, 128 x 128 20, 64 x 64 14; 2048 x 9728, 20 stages: 256 x 192 65, 128 x 128 62).
 struct TileKind {
   int tm, tn, per_cu;
   float round;   // prologue and epilogue of a round
@@ -389,12 +389,12 @@ struct TileKind {
 };
 enum { TILE_256 = 0, TILE_128 = 1, TILE_128_64 = 2, TILE_64 = 3, TILE_128_32 = 4, TILE_256_192 = 5 };
 constexpr TileKind kTiles[] = {
-    {256, 256, 1, 5.0f, {1.95f}},
+    {256, 256, 1, 8.0f, {1.95f}},
     {128, 128, 2, 2.0f, {0.85f, 1.21f}},
     {128, 64, 3, 1.5f, {0.52f, 0.79f, 1.07f}},
     {64, 64, 4, 1.0f, {0.33f, 0.48f, 0.75f, 0.99f}},
     {128, 32, 4, 1.5f, {0.50f, 0.80f, 1.10f, 1.40f}},  // experts only
-    {256, 192, 1, 4.5f, {1.50f}},
+    {256, 192, 1, 7.0f, {1.50f}},
 };
 
 // tiles: workgroups of a launch, of `stages` stages each
