@@ -342,6 +342,22 @@ def test_plan_sizes(N, S, E):
     check(torch.where(none[:, :, None], torch.zeros_like(y), y), ref, bound)
 
 
+def test_operands_of_other_tensors():
+    """Codes and scales that the caller made: uint8 or float8_e4m3fn, a matrix alone or a stack of one."""
+    g = np.random.default_rng(24)
+    m, _ = weights(g, 140, 260)
+    x = dev(g.standard_normal((50, 260)), torch.float16)
+    t = q.f8_quantize(x)
+    own = q.F8Tokens(t.codes.clone().view(torch.float8_e4m3fn), t.scales.clone(), 50, 260)
+    y = m.gemm(t)
+    f8 = q.F8Matrix(m.codes.view(torch.float8_e4m3fn), m.scales, 140, 260)
+    one = q.F8Matrix(m.codes[None], m.scales[None], 140, 260, 1)
+    assert all(torch.equal(y, a.gemm(b)) for a in (m, f8, one) for b in (t, own))
+    ids = torch.zeros((50, 1), dtype=torch.int32, device="cuda")
+    assert torch.equal(f8.gemm_id(own, q.route_plan(ids, 1))[:, 0], m.gemm_id(t, q.route_plan(ids, 1))[:, 0])
+    assert torch.equal(f8.transposed().codes, m.transposed().codes) and torch.equal(f8.dequantize(), m.dequantize())
+
+
 # ---- gradients ---------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", sorted(DTYPES))
@@ -411,7 +427,8 @@ def device_check(y, a, b, label=""):
 
 
 LARGE = [  # tokens, M, K: 256 x 256, 256 x 192, 128 x 128 and 128 x 64 tiles, the last with K divided too
-    (4000, 4000, 300), (4090, 2500, 4000), (2000, 8000, 250), (3000, 3000, 384), (2049, 4090, 2500), (60, 5000, 4000), (700, 130, 8000)]
+    (4000, 4000, 300), (4090, 2500, 4000), (2000, 8000, 250), (3000, 3000, 384), (2049, 4090, 2500), (60, 5000, 4000), (700, 130, 8000),
+    (24, 4200, 300), (24, 4090, 4000), (20, 300, 4500)]  # 17 .. 32 tokens: tiles, few-token kernel, tiles
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

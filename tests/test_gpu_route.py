@@ -191,6 +191,27 @@ def test_backward_against_differences():
                 assert abs((value(a) - value(b)) / (2 * h) - d[t, e]) < 16 * h * h / 6 + 1e-4
 
 
+@pytest.mark.parametrize("normalise", [False, True])
+def test_counts_summed_over_parts_of_a_batch(normalise):
+    """A batch in three parts: loss and gradients from the summed counts and probabilities are those of the whole."""
+    g = np.random.default_rng(39)
+    N, E, S, coef = 300, 40, 3, 0.02
+    l = logits_of(g, N, E, "f32", 0.1)
+    dw, dloss = dev(g.standard_normal((N, S))), torch.full((1,), 2.0, device="cuda")
+    whole = q.route(l, S, normalise=normalise, coef=coef)
+    cuts = (0, 70, 71, N)
+    parts = [q.route(l[a:b], S, normalise=normalise, coef=coef) for a, b in zip(cuts, cuts[1:])]
+    counts = sum(p.counts for p in parts)
+    psum = sum(p.psum for p in parts)
+    assert torch.equal(counts, whole.counts)
+    want = O.route(host64(l), S, normalise, coef)
+    assert np.isclose(host64(q.balance_loss(counts, psum, S, coef)), want["loss"], rtol=P_REL * (N + 1))
+    d = q.route_backward(l, whole, dw, dloss)
+    for (a, b), p in zip(zip(cuts, cuts[1:]), parts):
+        assert torch.equal(p.ids, whole.ids[a:b]) and torch.equal(p.weights, whole.weights[a:b])
+        assert torch.equal(q.route_backward(l[a:b], p._replace(counts=counts), dw[a:b], dloss), d[a:b])
+
+
 @pytest.mark.parametrize("dtype", sorted(DTYPES))
 @pytest.mark.parametrize("N,S,M", [(1, 1, 1), (3, 2, 7), (5, 8, 520), (64, 3, 1024), (2, 64, 100), (1000, 2, 24)])
 def test_combine(N, S, M, dtype):
