@@ -18,7 +18,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from ._lib import lib
-from .f8 import _DT, _call, _empty2, _out, _place, _shape, _tensor
+from .f8 import _DT, _call, _empty, _out, _place, _shape, _tensor
 
 
 class Routing(NamedTuple):
@@ -35,10 +35,12 @@ class Routing(NamedTuple):
 class RoutePlan:
     """(token, slot) pairs of ids [N, S] sorted by expert; see route_plan."""
 
-    __slots__ = ("data", "N", "S", "n_experts")
+    __slots__ = ("data", "N", "S", "n_experts", "routed")
 
-    def __init__(self, data, N, S, n_experts):
+    def __init__(self, data, N, S, n_experts, routed=None):
         self.data, self.N, self.S, self.n_experts = data, N, S, n_experts
+        # tokens of a quantization along the plan's pairs
+        self.routed = lib.qmm_f8_routed_tokens(N * S, n_experts) if routed is None else routed
 
     @property
     def counts(self):
@@ -60,6 +62,9 @@ class RoutePlan:
         return self.per_slot(x.shape[0], name)
 
 
+_plan_sizes = {}  # of the pairs and experts seen: bytes, tokens of a routed quantization
+
+
 def route_plan(ids: torch.Tensor, n_experts: int) -> RoutePlan:
     """Sort the pairs of ids [N, S] (int32; -1: an empty slot) by expert, once for every product that reads them."""
     _tensor(ids, "ids", (torch.int32,), (2,))
@@ -68,10 +73,13 @@ def route_plan(ids: torch.Tensor, n_experts: int) -> RoutePlan:
     if S < 1 or E < 1:
         raise ValueError("ids needs a slot and the plan an expert")
     device = _place(None, (ids, "ids"))
-    nb = lib.qmm_route_plan_bytes(N * S, E)
+    sizes = _plan_sizes.get((N * S, E))
+    if sizes is None:
+        sizes = _plan_sizes[N * S, E] = lib.qmm_route_plan_bytes(N * S, E), lib.qmm_f8_routed_tokens(N * S, E)
+    nb, routed = sizes
     data = torch.empty(max(nb, 16) // 4, dtype=torch.int32, device=ids.device)
     _call(device, lib.qmm_route_plan, ids.data_ptr(), N, S, E, data.data_ptr(), nb)
-    return RoutePlan(data, N, S, E)
+    return RoutePlan(data, N, S, E, routed)
 
 
 def _logits(logits, valid):
@@ -97,7 +105,7 @@ def route(logits: torch.Tensor, S: int, normalise: bool = True, coef: float = 0.
     if not 1 <= S <= min(E, 64):
         raise ValueError(f"S={S} outside [1, {min(E, 64)}]")
     on = logits.device
-    ids, weights = _empty2(N, S, torch.int32, on), _empty2(N, S, torch.float32, on)
+    ids, weights = _empty((N, S), torch.int32, device), _empty((N, S), torch.float32, device)
     counts = torch.empty(E + 1, dtype=torch.int32, device=on)
     nb = _route_need.get((N, E))
     if nb is None:
