@@ -113,7 +113,7 @@ def route(logits: torch.Tensor, S: int, normalise: bool = True, coef: float = 0.
     # sums over the rows, the loss and the workspace in one allocation
     pad = (E + 1 + 3) // 4 * 4
     buf = torch.empty(pad + nb // 4, dtype=torch.float32, device=on)
-    psum, loss, at = buf[:E], buf[E], buf.data_ptr()
+    psum, loss, at = buf.as_strided((E,), (1,)), buf.as_strided((), (), E), buf.data_ptr()
     _call(device, lib.qmm_route, logits.data_ptr(), _DT[logits.dtype], N, E, S,
           valid.data_ptr() if valid is not None else None, int(bool(normalise)), coef, ids.data_ptr(), weights.data_ptr(),
           counts.data_ptr(), at, at + 4 * E, at + 4 * pad, nb)
