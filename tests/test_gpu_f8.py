@@ -385,6 +385,33 @@ def test_gradients(N, M, K, dtype):
     assert abs((dw * v).sum() - difference) <= (slack * np.abs(v)).sum()
 
 
+def test_gradients_against_differences():
+    """Operands of powers of two within a factor of 8 are their codes, so <dy, x W^T> is linear in x and in W as it is
+    computed: its differences are the gradients' products with the steps.  Error: a scale's rounding in each of two factors
+    of a product (2^-23), up to K or N terms of a sum in fp32."""
+    g = np.random.default_rng(25)
+    N, M, K = 300, 140, 260
+
+    def powers(*shape):
+        return dev(2.0 ** g.integers(0, 4, shape) * g.integers(-1, 2, shape))
+
+    x, x2, w, w2, dy = powers(N, K), powers(N, K), powers(M, K), powers(M, K), powers(N, M)
+
+    def value(x, w):
+        y = q.F8Matrix.quantize(w).linear(x)
+        return float((dy.double() * y.double()).sum())
+
+    size = float((dy.double().abs() * (8.0 * K * 8.0)).sum())
+    tol = size * (4 * 2.0 ** -23 + 2 * (K + N) * 2.0 ** -24)
+    dx = q.F8Matrix.quantize(w).transposed().gemm(q.f8_quantize(dy))
+    dw = q.f8_wgrad(q.f8_quantize_t(dy), q.f8_quantize_t(x))
+    assert abs(value(x2, w) - value(x, w) - float((dx.double() * (x2 - x).double()).sum())) < tol
+    assert abs(value(x, w2) - value(x, w) - float((dw.double() * (w2 - w).double()).sum())) < tol
+    # the values are exact up to that: each is the sum of its integers
+    assert float((dx.double() - dy.double() @ w.double()).abs().max()) < 64.0 * M * (2.0 ** -22 + M * 2.0 ** -24)
+    assert float((dw.double() - dy.double().t() @ x.double()).abs().max()) < 64.0 * N * (2.0 ** -22 + N * 2.0 ** -24)
+
+
 @pytest.mark.parametrize("per_slot", [False, True])
 @pytest.mark.parametrize("N,S,E,M,K", [(1, 1, 1, 5, 7), (40, 2, 4, 70, 130), (300, 3, 6, 33, 140), (2, 8, 64, 24, 40),
                                        (600, 2, 2, 128, 128)])

@@ -230,6 +230,21 @@ def test_combine(N, S, M, dtype):
         check(dw, (yv * dv[:, None, :]).sum(2), (np.abs(yv) * np.abs(dv)[:, None, :]).sum(2) * (M + 64) * 2.0 ** -24, "dw")
 
 
+def test_combine_against_differences():
+    """<dout, combine> is linear in y and in the weights: one step each, of whole numbers, is exact."""
+    g = np.random.default_rng(40)
+    N, S, M = 20, 3, 33
+    y, y2, dout = dev(g.integers(-8, 9, (N, S, M))), dev(g.integers(-8, 9, (N, S, M))), dev(g.integers(-4, 5, (N, M)))
+    w, w2 = dev(g.integers(-4, 5, (N, S))), dev(g.integers(-4, 5, (N, S)))
+
+    def value(y, w):
+        return float((q.route_combine(y, w).double() * dout.double()).sum())
+
+    dy, dw = q.route_combine_backward(y, w, dout)
+    assert value(y2, w) - value(y, w) == float((dy.double() * (y2 - y).double()).sum())
+    assert value(y, w2) - value(y, w) == float((dw.double() * (w2 - w).double()).sum())
+
+
 def test_unaligned_views():
     g = np.random.default_rng(36)
     buf = dev(g.standard_normal(3 * 2 * 16 + 1), torch.float16)
