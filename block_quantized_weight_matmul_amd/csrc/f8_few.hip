@@ -1,10 +1,10 @@
 // f8_few.hip -- e4m3 products of few tokens, bound by reading the weights once.
 //
-// A workgroup owns 16 weight rows and divides K among its waves (wave v takes groups v, v + KS, ..): a wave loads
+// A workgroup owns up to 16 weight rows and divides K among its waves (wave v takes groups v, v + KS, ..): a wave loads
 // its groups' codes straight into the registers of the matrix instruction (16 rows x 128 bytes, whole cache lines),
 // keeps its partial outputs, and the workgroup adds the waves' partials in wave order through LDS.  Nothing but the
 // partials and, for raw tokens, the tokens' codes passes through LDS.  Two batches of groups are in flight per wave.
-// One token of 4096 x 2560 takes 3.6 us (10.5 MB, an empty launch 1.5), of 2560 x 9728 9.1 (25 MB).  The expert form: 32
+// One token of 4096 x 2560 takes 3.6 us (10.5 MB, an empty launch 1.5), of 2560 x 9728 8.1 (25 MB).  The expert form: 32
 // pairs of 128 experts of 4096 x 512 13.6 us for 62 MB.
 #include <algorithm>
 #include <climits>
@@ -65,6 +65,7 @@ struct FewArgs {
   void* y;
   int64_t M, K, Kp, ldx;
   int N, G, waves, vec_y;
+  int rows;           // of a workgroup, 4 .. 16
 };
 
 // RAW: element type of raw tokens, -1 for quantized ones.  B: groups of a batch.  W: most waves of a workgroup (128
@@ -75,7 +76,7 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
   constexpr bool kExact = OT == DT_F32;
   constexpr int kTokens = RAW >= 0 ? 1 : NT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = lane & 15, q = lane >> 4;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.rows;
   const int KS = a.waves, last = a.G - 1;
 
   // raw tokens first: everything waits for them, and loads return in order
@@ -91,8 +92,10 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
     }
   }
 
-  const uint8_t* wrow = a.w + std::min<int64_t>(r0 + row, a.M - 1) * a.Kp + q * 32;
-  const float* wsc = a.ws + r0 / 128 * a.G;
+  const int64_t rl = std::min<int64_t>(r0 + a.rows, a.M) - 1;  // the last row; it may lie in another row block's scales
+  const uint8_t* wrow = a.w + std::min<int64_t>(r0 + row, rl) * a.Kp + q * 32;
+  const float *wsc = a.ws + r0 / 128 * a.G, *wsc2 = a.ws + rl / 128 * a.G;
+  const int upto = static_cast<int>(rl / 128 * 128 - r0) - q * 4;  // this lane's outputs from here on have the second
   const uint8_t* trow[kTokens];
   const float* tsc[kTokens];
   if constexpr (RAW < 0) {
@@ -106,7 +109,7 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
   // A group past the last is the last one again, its part multiplied by zero (what is NaN there is NaN anyway).
   struct Batch {
     i32x4 lo[B], hi[B], tlo[B][kTokens], thi[B][kTokens];
-    float sw[B], sx[B][kTokens];
+    float sw[B], sw2[B], sx[B][kTokens];
   } b0, b1;
   auto load = [&](Batch& b, int i0) {
 #pragma unroll
@@ -115,6 +118,7 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
       b.lo[u] = *reinterpret_cast<const i32x4*>(wrow + g * 128);
       b.hi[u] = *reinterpret_cast<const i32x4*>(wrow + g * 128 + 16);
       b.sw[u] = wsc[g];
+      b.sw2[u] = wsc2[g];
       if constexpr (RAW < 0) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -150,7 +154,8 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
   auto multiply = [&](const Batch& b, int i0) {
 #pragma unroll
     for (int u = 0; u < B; ++u) {
-      const float sw = i0 + u * KS <= last ? b.sw[u] : 0.0f;
+      const bool real = i0 + u * KS <= last;
+      const float sw = real ? b.sw[u] : 0.0f, sw2 = real ? b.sw2[u] : 0.0f;
       Frag<kExact> A;
       A.set(b.lo[u], b.hi[u]);
 #pragma unroll
@@ -162,14 +167,14 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
           i32x4 lo, hi;
           read_codes(codes + (static_cast<size_t>(g) * a.N + t) * 128, t, q, lo, hi);
           T.set(lo, hi);
-          s = scales[g * a.N + t] * sw;
+          s = scales[g * a.N + t];
         } else {
           T.set(b.tlo[u][j], b.thi[u][j]);
-          s = b.sx[u][j] * sw;
+          s = b.sx[u][j];
         }
         const f32x4 p = group_sum(A, T);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(p[e], s, acc[j][e]);
+        for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(p[e], s * (e < upto ? sw : sw2), acc[j][e]);
       }
     }
   };
@@ -190,7 +195,7 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
     f32x4 sum = part[j * 64 + lane];
     for (int k = 1; k < KS; ++k) sum += part[(k * NT + j) * 64 + lane];
     const int t = j * 16 + row;
-    const int64_t r = r0 + q * 4, left = a.M - r;
+    const int64_t r = r0 + q * 4, left = rl + 1 - r;
     if (t < a.N && left > 0)
       store4<OT>(static_cast<T*>(a.y) + static_cast<int64_t>(t) * a.M + r, sum, left < 4 ? static_cast<int>(left) : 4, a.vec_y);
   }
@@ -325,7 +330,7 @@ __global__ __launch_bounds__(kIdThreads) void k_f8_few_id(FewIdArgs a) {
 template <int NT, int RAW, int OT, int B, int W>
 hipError_t few_run(FewArgs a, hipStream_t st) {
   a.waves = std::min(W, (a.G + 1) / 2);
-  const int64_t blocks = (a.M + 15) / 16;
+  const int64_t blocks = (a.M + a.rows - 1) / a.rows;
   const size_t codes = RAW >= 0 ? static_cast<size_t>(a.N) * (a.Kp + a.G * 4) : 0;
   const size_t lds = std::max(codes, static_cast<size_t>(a.waves) * NT * 1024);
   k_f8_few<NT, RAW, OT, B, W><<<static_cast<unsigned>(blocks), 64 * a.waves, lds, st>>>(a);
@@ -366,7 +371,10 @@ FewArgs few_args(const F8Desc& m, int64_t N, void* y, int yt) {
   a.Kp = m.Kp;
   a.N = static_cast<int>(N);
   a.G = static_cast<int>(m.Kp / kF8Block);
-  a.vec_y = store_vec(y, m.M, yt);
+  // Fewer than 16 rows where 16 would leave CUs idle (2560 x 9728, 1 and 16 tokens: 8.9 and 12.2 us with 16 rows, 8.1 and
+  // 11.2 with 10; 512 x 4096: 4.9 and 6.3, 4.4 and 5.7 with 4).
+  a.rows = static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(4, (m.M + m.cus - 1) / m.cus)));
+  a.vec_y = a.rows % 4 == 0 && store_vec(y, m.M, yt);
   return a;
 }
 

@@ -455,7 +455,8 @@ def device_check(y, a, b, label=""):
 
 LARGE = [  # tokens, M, K: 256 x 256, 256 x 192, 128 x 128 and 128 x 64 tiles, the last with K divided too
     (4000, 4000, 300), (4090, 2500, 4000), (2000, 8000, 250), (3000, 3000, 384), (2049, 4090, 2500), (60, 5000, 4000), (700, 130, 8000),
-    (24, 4200, 300), (24, 4090, 4000), (20, 300, 4500)]  # 17 .. 32 tokens: tiles, few-token kernel, tiles
+    (24, 4200, 300), (24, 4090, 4000), (20, 300, 4500),  # 17 .. 32 tokens: tiles, few-token kernel, tiles
+    (1, 2500, 300), (16, 2500, 700), (20, 1300, 260), (3, 1, 5000)]  # rows of a workgroup across a block's edge; one row
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
