@@ -65,7 +65,8 @@ def _load():
         "qmm_f8_gemm_id": (c_int, [vp, vp, vp, i64, i64, c_int, vp, vp, c_int, vp]),
         "qmm_f8_routed_tokens": (i64, [i64, i64]),
         "qmm_f8_quantize_routed": (c_int, [vp, c_int, i64, i64, i64, c_int, i64, i64, vp, vp, vp, vp]),
-        "qmm_f8_wgrad": (c_int, [vp, vp, vp, vp, i64, i64, i64, vp, c_int, vp]),
+        "qmm_f8_wgrad_workspace_bytes": (size, [i64, i64, i64]),
+        "qmm_f8_wgrad": (c_int, [vp, vp, vp, vp, i64, i64, i64, vp, c_int, vp, size, vp]),
         "qmm_f8_wgrad_id": (c_int, [vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, c_int, vp]),
         "qmm_route_workspace_bytes": (size, [i64, i64]),
         "qmm_route": (c_int, [vp, c_int, i64, i64, i64, vp, c_int, f32, vp, vp, vp, vp, vp, vp, size, vp]),

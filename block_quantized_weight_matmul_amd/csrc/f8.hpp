@@ -92,7 +92,9 @@ struct F8WgradArgs {
   const int32_t* plan;
   PlanDesc pd;
   int cus;
+  void* ws;  // dense: f8_wgrad_workspace_bytes
 };
+size_t f8_wgrad_workspace_bytes(int64_t Np, int64_t M, int64_t K, int cus);
 hipError_t launch_f8_wgrad(const F8WgradArgs& a, hipStream_t s);
 
 // Router.

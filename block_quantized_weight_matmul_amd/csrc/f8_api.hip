@@ -362,8 +362,10 @@ qmm_status qmm_f8_quantize_routed(const void* x, qmm_dtype xt, int64_t ldx, int6
   return e == hipSuccess ? ok() : hip_fail(e, "f8 quantize launch");
 }
 
+constexpr int kWgradCus = 256;  // of gfx950; only the choice of tiles and shares depends on it
+
 static qmm_status wgrad(const void* gc, const float* gs, const void* xc, const float* xs, int64_t Np, int64_t M, int64_t K,
-                        const void* plan, const qmm::PlanDesc* pd, void* dw, int dt, qmm_stream_t stream) {
+                        const void* plan, const qmm::PlanDesc* pd, void* dw, int dt, void* ws, qmm_stream_t stream) {
   QMM_TRY(check_ptr(dw, size_of(dt), "dw"));
   if (Np > 0) {
     QMM_TRY(check_out(gc, gs, "g", false));
@@ -380,7 +382,8 @@ static qmm_status wgrad(const void* gc, const float* gs, const void* xc, const f
   a.Np = Np;
   a.dw = dw;
   a.dt = dt;
-  a.cus = 256;  // of gfx950; only the choice of a tile depends on it
+  a.cus = kWgradCus;
+  a.ws = ws;
   if (pd) {
     a.plan = static_cast<const int32_t*>(plan);
     a.pd = *pd;
@@ -389,13 +392,19 @@ static qmm_status wgrad(const void* gc, const float* gs, const void* xc, const f
   return e == hipSuccess ? ok() : hip_fail(e, "f8 wgrad launch");
 }
 
+size_t qmm_f8_wgrad_workspace_bytes(int64_t N, int64_t M, int64_t K) {
+  if (N <= 0 || N > kMaxWgradTokens || M < 1 || M > qmm::kF8MaxRows || K < 1 || K > kMaxK) return 0;
+  return qmm::f8_wgrad_workspace_bytes(f8_pad(N), M, K, kWgradCus);
+}
+
 qmm_status qmm_f8_wgrad(const void* g_codes, const float* g_scales, const void* x_codes, const float* x_scales, int64_t N,
-                        int64_t M, int64_t K, void* dw, qmm_dtype dt, qmm_stream_t stream) {
+                        int64_t M, int64_t K, void* dw, qmm_dtype dt, void* ws, size_t ws_bytes, qmm_stream_t stream) {
   QMM_TRY(check_dtype(dt, "gradient"));
   QMM_TRY(check_range(N, 0, kMaxWgradTokens, "N"));
   QMM_TRY(check_range(M, 1, qmm::kF8MaxRows, "M"));
   QMM_TRY(check_range(K, 1, kMaxK, "K"));
-  return wgrad(g_codes, g_scales, x_codes, x_scales, N > 0 ? f8_pad(N) : 0, M, K, nullptr, nullptr, dw, dt, stream);
+  QMM_TRY(check_ws(ws, ws_bytes, qmm_f8_wgrad_workspace_bytes(N, M, K), "ws"));
+  return wgrad(g_codes, g_scales, x_codes, x_scales, N > 0 ? f8_pad(N) : 0, M, K, nullptr, nullptr, dw, dt, ws, stream);
 }
 
 qmm_status qmm_f8_wgrad_id(const void* g_codes, const float* g_scales, const void* x_codes, const float* x_scales,
@@ -407,7 +416,7 @@ qmm_status qmm_f8_wgrad_id(const void* g_codes, const float* g_scales, const voi
   QMM_TRY(check_range(K, 1, kMaxK, "K"));
   const qmm::PlanDesc pd = qmm::plan_desc(N * S, E);
   const int64_t Np = qmm::kF8Block * pd.cap[qmm::kPlanTileKinds - 1];
-  return wgrad(g_codes, g_scales, x_codes, x_scales, Np, M, K, plan, &pd, dw, dt, stream);
+  return wgrad(g_codes, g_scales, x_codes, x_scales, Np, M, K, plan, &pd, dw, dt, nullptr, stream);
 }
 
 size_t qmm_route_workspace_bytes(int64_t N, int64_t E) {

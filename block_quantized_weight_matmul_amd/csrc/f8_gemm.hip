@@ -36,7 +36,7 @@ struct GemmArgs {
   PlanDesc pd;
   int map;            // index of the token tile's map in the plan
   int slots;          // MODE_ID: pairs that share a token row
-  int share;          // groups of a workgroup where K is divided (gridDim.y > 1)
+  int share;          // groups of a workgroup where the reduction is divided (gridDim.y > 1)
   int vec;            // 16 bytes of consecutive outputs may be stored at once
 };
 
@@ -108,6 +108,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
   int g0 = 0, g1 = a.G;
   int64_t t0;
   int first = 0, count = 0;  // MODE_ID: the tile's pairs
+  auto share = [&]() {  // of the reduction, the sums to a slab of their own
+    g0 = static_cast<int>(blockIdx.y) * a.share;
+    g1 = std::min(a.G, g0 + a.share);
+    y += static_cast<int64_t>(blockIdx.y) * M * N;
+  };
   if constexpr (kId) {
     const int32_t* mp = a.plan + a.pd.map[a.map] + 3 * static_cast<int64_t>(bid);
     const int bucket = static_cast<int>(scalar(static_cast<unsigned>(mp[0])));
@@ -131,14 +136,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
       g0 = static_cast<int>(scalar(static_cast<unsigned>(a.plan[a.pd.tile128 + e])));
       g1 = static_cast<int>(scalar(static_cast<unsigned>(a.plan[a.pd.tile128 + e + 1])));
       y += static_cast<int64_t>(e) * M * N;
+    } else if (gridDim.y > 1) {
+      share();
     }
   } else {
     t0 = static_cast<int64_t>(bid) * TN;
-    if (gridDim.y > 1) {  // a share of K, its sums to a slab of its own
-      g0 = static_cast<int>(blockIdx.y) * a.share;
-      g1 = std::min(a.G, g0 + a.share);
-      y += static_cast<int64_t>(blockIdx.y) * M * N;
-    }
+    if (gridDim.y > 1) share();
   }
 
   // What this thread stages: 16-byte pieces, offsets from the tile's first row (rows past the end repeat the last), and
@@ -365,11 +368,11 @@ __global__ __launch_bounds__(256) void k_f8_join(const float* slabs, int splits,
   }
 }
 
-template <int TM, int TN>
+template <int TM, int TN, int MODE>
 hipError_t run_split(const GemmArgs& a, bool exact, int64_t blocks, int splits, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(splits)), block(256);
-  if (exact) k_f8_gemm<TM, TN, 2, 2, MODE_DENSE, true, DT_F32><<<grid, block, 0, st>>>(a);
-  else k_f8_gemm<TM, TN, 2, 2, MODE_DENSE, false, DT_F32><<<grid, block, 0, st>>>(a);
+  if (exact) k_f8_gemm<TM, TN, 2, 2, MODE, true, DT_F32><<<grid, block, 0, st>>>(a);
+  else k_f8_gemm<TM, TN, 2, 2, MODE, false, DT_F32><<<grid, block, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -407,7 +410,8 @@ float tile_cost(const TileKind& k, double tiles, double stages, int cus) {
 
 // How a dense product of M rows, N tokens and `many` matrices runs: its tile, and the shares that K is divided into
 // (1: not at all).  Shares make their sums in slabs of fp32 that k_f8_join adds: worth it where the tiles leave CUs idle
-// and K is long (2560 x 9728, 64 tokens: 27 us undivided, 40 workgroups of 76 stages).
+// and K is long (2560 x 9728, 64 tokens: 27 us undivided, 40 workgroups of 76 stages, 12.7 divided; dW of 128 x 2560 over
+// 16384 tokens 59 and 20).
 struct DensePlan {
   int kind, splits;
 };
@@ -439,26 +443,24 @@ hipError_t run_dense(GemmArgs& a, int ot, int64_t many, const DensePlan& plan, f
   a.tiles_m = static_cast<int>((a.M + k.tm - 1) / k.tm);
   a.tiles_n = static_cast<int>((a.N + k.tn - 1) / k.tn);
   const int64_t blocks = static_cast<int64_t>(a.tiles_m) * a.tiles_n * many;
-  if constexpr (MODE == MODE_DENSE) {
-    if (plan.splits > 1) {
-      if (blocks > INT_MAX) return hipErrorInvalidValue;
-      void* y = a.y;
-      const int64_t n = a.M * a.N;
-      a.y = slabs;
-      a.vec = store_vec16(slabs, a.M, DT_F32);
-      a.share = (a.G + plan.splits - 1) / plan.splits;
-      const int splits = (a.G + a.share - 1) / a.share;  // every share has groups
-      const hipError_t e = plan.kind == TILE_64 ? run_split<64, 64>(a, ot == DT_F32, blocks, splits, st)
-                                                : run_split<128, 64>(a, ot == DT_F32, blocks, splits, st);
-      if (e != hipSuccess) return e;
-      const unsigned grid = static_cast<unsigned>((n + 1023) / 1024);
-      switch (ot) {
-        case DT_F32: k_f8_join<DT_F32><<<grid, 256, 0, st>>>(slabs, splits, n, static_cast<float*>(y)); break;
-        case DT_F16: k_f8_join<DT_F16><<<grid, 256, 0, st>>>(slabs, splits, n, static_cast<_Float16*>(y)); break;
-        default: k_f8_join<DT_BF16><<<grid, 256, 0, st>>>(slabs, splits, n, static_cast<__bf16*>(y)); break;
-      }
-      return hipGetLastError();
+  if (plan.splits > 1) {
+    if (blocks > INT_MAX) return hipErrorInvalidValue;
+    void* y = a.y;
+    const int64_t n = a.M * a.N;
+    a.y = slabs;
+    a.vec = store_vec16(slabs, a.M, DT_F32);
+    a.share = (a.G + plan.splits - 1) / plan.splits;
+    const int splits = (a.G + a.share - 1) / a.share;  // every share has groups
+    const hipError_t e = plan.kind == TILE_64 ? run_split<64, 64, MODE>(a, ot == DT_F32, blocks, splits, st)
+                                              : run_split<128, 64, MODE>(a, ot == DT_F32, blocks, splits, st);
+    if (e != hipSuccess) return e;
+    const unsigned grid = static_cast<unsigned>((n + 1023) / 1024);
+    switch (ot) {
+      case DT_F32: k_f8_join<DT_F32><<<grid, 256, 0, st>>>(slabs, splits, n, static_cast<float*>(y)); break;
+      case DT_F16: k_f8_join<DT_F16><<<grid, 256, 0, st>>>(slabs, splits, n, static_cast<_Float16*>(y)); break;
+      default: k_f8_join<DT_BF16><<<grid, 256, 0, st>>>(slabs, splits, n, static_cast<__bf16*>(y)); break;
     }
+    return hipGetLastError();
   }
   switch (plan.kind) {
     case TILE_256: return run_tile<256, 256, 2, 4, MODE>(a, ot, blocks, st);
@@ -503,12 +505,20 @@ hipError_t run_experts(GemmArgs& a, int ot, int cus, hipStream_t st) {
 
 }  // namespace
 
-size_t f8_gemm_workspace_bytes(const F8Desc& m, int64_t N) {
-  if (f8_few_tokens(m, N)) return 0;
+// room for the slabs of a product of M x N outputs, for either kind of output
+static size_t slab_bytes(int64_t M, int64_t N, int64_t stages, int cus) {
   int splits = 1;
-  for (int f32 = 0; f32 < 2; ++f32)  // for either kind of output
-    splits = std::max(splits, dense_plan(m.M, N, 1, static_cast<double>(m.Kp / kF8Block), f32, true, m.cus).splits);
-  return splits > 1 ? static_cast<size_t>(splits) * m.M * N * 4 : 0;
+  for (int f32 = 0; f32 < 2; ++f32)
+    splits = std::max(splits, dense_plan(M, N, 1, static_cast<double>(stages), f32, true, cus).splits);
+  return splits > 1 ? static_cast<size_t>(splits) * M * N * 4 : 0;
+}
+
+size_t f8_gemm_workspace_bytes(const F8Desc& m, int64_t N) {
+  return f8_few_tokens(m, N) ? 0 : slab_bytes(m.M, N, m.Kp / kF8Block, m.cus);
+}
+
+size_t f8_wgrad_workspace_bytes(int64_t Np, int64_t M, int64_t K, int cus) {
+  return Np > 0 ? slab_bytes(K, M, Np / kF8Block, cus) : 0;
 }
 
 hipError_t launch_f8_gemm(const F8Desc& m, const uint8_t* xc, const float* xs, int64_t N, void* y, int yt, void* ws,
@@ -562,8 +572,9 @@ hipError_t launch_f8_wgrad(const F8WgradArgs& w, hipStream_t st) {
   a.plan = w.plan;
   a.pd = w.pd;
   const int64_t E = w.plan ? w.pd.E : 1;
-  const DensePlan plan = dense_plan(a.M, a.N, E, std::max(1.0, static_cast<double>(a.G) / E), w.dt == DT_F32, false, w.cus);
-  return run_dense<MODE_WGRAD>(a, w.dt, E, plan, nullptr, st);
+  const DensePlan plan = dense_plan(a.M, a.N, E, std::max(1.0, static_cast<double>(a.G) / E), w.dt == DT_F32,
+                                    !w.plan, w.cus);
+  return run_dense<MODE_WGRAD>(a, w.dt, E, plan, static_cast<float*>(w.ws), st);
 }
 
 }  // namespace qmm

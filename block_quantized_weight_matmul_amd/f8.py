@@ -212,6 +212,9 @@ def f8_quantize_t(x: torch.Tensor, plan=None) -> F8Tokens:
     return t
 
 
+_wgrad_need = {}  # workspace bytes of the sizes seen
+
+
 def f8_wgrad(g: F8Tokens, x: F8Tokens, plan=None, out: torch.Tensor = None, dtype=torch.float32) -> torch.Tensor:
     """dw [M, K] = g^T x (dw [E, M, K] with a plan), g and x quantized along the same tokens by f8_quantize_t."""
     if g.length != x.length or g.pitch != x.pitch:
@@ -225,7 +228,12 @@ def f8_wgrad(g: F8Tokens, x: F8Tokens, plan=None, out: torch.Tensor = None, dtyp
     dw = _out(out, shape, _dtype(dtype), device)
     ptrs = g.ptrs + x.ptrs
     if plan is None:
-        _call(device, lib.qmm_f8_wgrad, *ptrs, g.length, M, K, dw.data_ptr(), _DT[dw.dtype])
+        nb = _wgrad_need.get((g.length, M, K))
+        if nb is None:
+            nb = _wgrad_need[g.length, M, K] = lib.qmm_f8_wgrad_workspace_bytes(g.length, M, K)
+        ws = torch.empty(nb, dtype=torch.uint8, device=_DEVICES[device]) if nb else None
+        _call(device, lib.qmm_f8_wgrad, *ptrs, g.length, M, K, dw.data_ptr(), _DT[dw.dtype],
+              ws.data_ptr() if nb else None, nb)
     else:
         _place(device, (plan.data, "plan"))
         _call(device, lib.qmm_f8_wgrad_id, *ptrs, plan.N, plan.S, M, K, plan.n_experts, plan.data.data_ptr(), dw.data_ptr(),

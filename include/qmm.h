@@ -488,6 +488,7 @@ qmm_status qmm_f8_gemm_id(const qmm_f8_matrix *h, const void *codes, const float
  * qmm_f8_wgrad -- dw[M, K] = g^T x over N tokens, every element written.
  *   g_codes, g_scales  codes_t / scales_t of g [N, M];  x_codes, x_scales those of x [N, K].
  *   dw  DEVICE of type dt, element-aligned.  N = 0 writes zeros.  N <= 2^23.
+ *   ws  DEVICE, 16-byte aligned, qmm_f8_wgrad_workspace_bytes(N, M, K) bytes, as qmm_f8_linear.
  * qmm_f8_wgrad_id -- dw[E, M, K], each expert over its own pairs (zeros where it has none);
  *   both operands from qmm_f8_quantize_routed with the same plan.
  */
@@ -496,9 +497,10 @@ qmm_status qmm_f8_quantize_routed(const void *x, qmm_dtype xt, int64_t ldx, int6
                                   int64_t S, int x_per_slot, int64_t K, int64_t E,
                                   const void *plan, void *codes_t, float *scales_t,
                                   qmm_stream_t stream);
+size_t qmm_f8_wgrad_workspace_bytes(int64_t N, int64_t M, int64_t K);
 qmm_status qmm_f8_wgrad(const void *g_codes, const float *g_scales, const void *x_codes,
                         const float *x_scales, int64_t N, int64_t M, int64_t K, void *dw,
-                        qmm_dtype dt, qmm_stream_t stream);
+                        qmm_dtype dt, void *ws, size_t ws_bytes, qmm_stream_t stream);
 qmm_status qmm_f8_wgrad_id(const void *g_codes, const float *g_scales, const void *x_codes,
                            const float *x_scales, int64_t N, int64_t S, int64_t M, int64_t K,
                            int64_t E, const void *plan, void *dw, qmm_dtype dt,

@@ -132,9 +132,13 @@ def test_c_argument_errors():
     assert lib.qmm_route_plan(p, 4, 65, 4, p, 1 << 20, None) == -3
     assert lib.qmm_route_plan(p, 4, 2, 1025, p, 1 << 20, None) == -3
     assert lib.qmm_route_plan(p, 1 << 22, 2, 4, p, 1 << 40, None) == -3
-    assert lib.qmm_f8_wgrad(p, p, p, p, 1 << 24, 4, 4, p, 0, None) == -3
-    assert lib.qmm_f8_wgrad(p, p, p, p, 4, 4, 4, p, 5, None) == -2
-    assert lib.qmm_f8_wgrad(p, p, None, p, 4, 4, 4, p, 0, None) == -1
+    assert lib.qmm_f8_wgrad(p, p, p, p, 1 << 24, 4, 4, p, 0, None, 0, None) == -3
+    assert lib.qmm_f8_wgrad(p, p, p, p, 4, 4, 4, p, 5, None, 0, None) == -2
+    assert lib.qmm_f8_wgrad(p, p, None, p, 4, 4, 4, p, 0, None, 0, None) == -1
+    need = lib.qmm_f8_wgrad_workspace_bytes(1 << 14, 128, 256)
+    assert need > 0 and lib.qmm_f8_wgrad_workspace_bytes(0, 128, 256) == 0
+    assert lib.qmm_f8_wgrad(p, p, p, p, 1 << 14, 128, 256, p, 0, p, need - 4, None) == -1
+    assert lib.qmm_f8_wgrad(p, p, p, p, 1 << 14, 128, 256, p, 0, p + 4, need, None) == -4
     assert lib.qmm_f8_wgrad_id(p, p, p, p, 4, 1, 4, 4, 4, None, p, 0, None) == -1
     assert lib.qmm_route(p, 0, 4, 8, 9, None, 1, 0.0, p, p, p, p, p, p, 1 << 20, None) == -3   # S > E
     assert lib.qmm_route(p, 0, 4, 128, 65, None, 1, 0.0, p, p, p, p, p, p, 1 << 20, None) == -3

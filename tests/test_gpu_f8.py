@@ -474,7 +474,7 @@ def test_large_products(N, M, K, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 @pytest.mark.parametrize("N,M,K", [(300, 4000, 4000), (250, 8000, 2000), (384, 3000, 3000), (5000, 200, 130),
-                                   (4000, 4090, 2500)])
+                                   (4000, 4090, 2500), (16300, 100, 300), (9000, 64, 1), (2300, 700, 130)])
 def test_large_weight_gradients(N, M, K, dtype):
     g = torch.Generator(device="cuda").manual_seed(N)
     gt, xt = (q.f8_quantize_t(torch.randn((N, c), generator=g, device="cuda").to(DTYPES[dtype])) for c in (M, K))
