@@ -10,7 +10,8 @@ Backward, every gradient a call:
     dlogits = route_backward(logits, r, dweights, dloss)
 
 A trainer that adds counts and psum over GPUs before the loss calls balance_loss on the sums and hands a Routing with
-the summed counts to route_backward.
+the summed counts to route_backward.  Counts stay int32 (torch.sum of int32 gives int64, which both calls refuse: pass
+dtype=torch.int32).
 """
 
 from typing import NamedTuple, Optional
@@ -84,10 +85,11 @@ def route_plan(ids: torch.Tensor, n_experts: int) -> RoutePlan:
 
 def _logits(logits, valid):
     _tensor(logits, "logits", _DT, (2,))
-    device = _place(None, (logits, "logits"))
     if valid is not None:
         _tensor(valid, "valid", (torch.uint8, torch.bool), (1,))
         _shape(valid, "valid", (logits.shape[0],))
+    device = _place(None, (logits, "logits"))
+    if valid is not None:
         _place(device, (valid, "valid"))
     return device
 
@@ -135,12 +137,15 @@ def balance_loss(counts: torch.Tensor, psum: torch.Tensor, S: int, coef: float) 
 def route_backward(logits: torch.Tensor, routing: Routing, dweights: Optional[torch.Tensor] = None,
                    dloss: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dlogits [N, E] of logits' type from the gradients with respect to the weights ([N, S] fp32) and the loss (fp32, one
-    element on the device); either may be None."""
-    device = _logits(logits, routing.valid)
+    element on the device); either may be None.  ids and counts are int32, as route gives them."""
+    _tensor(logits, "logits", _DT, (2,))
+    _tensor(routing.ids, "ids", (torch.int32,), (2,))
+    _tensor(routing.counts, "counts", (torch.int32,), (1,))
     N, E = logits.shape
     S = routing.ids.shape[1]
     _shape(routing.ids, "ids", (N, S))
     _shape(routing.counts, "counts", (E + 1,))
+    device = _logits(logits, routing.valid)
     _place(device, (routing.ids, "ids"), (routing.counts, "counts"))
     if dweights is not None:
         _tensor(dweights, "dweights", (torch.float32,), (2,))

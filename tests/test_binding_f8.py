@@ -156,3 +156,16 @@ def test_row_layouts_need_no_device():
     x = f32(4, 8)
     from block_quantized_weight_matmul_amd import f8
     expect(lambda: f8._rows(x, "x"), "device tensor")
+
+
+def test_route_backward_refuses_other_types():
+    """The kernels read counts and ids as int32: a sum over stacked counts is int64."""
+    l, ids, w, counts = f32(4, 8), i32(4, 2), f32(4, 2), i32(9)
+    r = q.Routing(ids, w, counts, f32(8), f32(), True, 0.1, None)
+    summed = torch.stack([counts, counts]).sum(0)
+    assert summed.dtype == torch.int64
+    expect(lambda: q.route_backward(l, r._replace(counts=summed), w, f32(1)), "counts has dtype")
+    expect(lambda: q.route_backward(l, r._replace(counts=counts.float()), w, f32(1)), "counts has dtype")
+    expect(lambda: q.route_backward(l, r._replace(ids=ids.long()), w, f32(1)), "ids has dtype")
+    expect(lambda: q.route_backward(l, r._replace(ids=i32(8)), w, f32(1)), "ids must be a tensor of 2")
+    expect(lambda: q.route_backward(l, r._replace(valid=i32(4)), w, f32(1)), "valid has dtype")
