@@ -119,14 +119,18 @@ def _dtype(t):
 
 class F8Tokens:
     """Quantized rows: codes [R, padded C] uint8 and scales [padded C / 128, R] fp32.  C, the length of the quantized
-    axis, is K for tokens ([N, K]) and the number of tokens for a transposed quantization (`channels` rows)."""
+    axis, is K for tokens ([N, K]) and the number of tokens for a transposed quantization (`channels` rows).  With a plan
+    (f8_quantize_t) C is its pairs and a row has plan.routed codes, each expert's pairs padded on their own."""
 
     __slots__ = ("_codes", "_scales", "_buffer", "ptrs", "pitch", "rows", "length", "plan", "device")
 
     def __init__(self, codes, scales, rows, length, plan=None):
         _tensor(codes, "codes", _CODES, (2,))
         _tensor(scales, "scales", (torch.float32,), (2,))
-        pitch = codes.shape[1] if plan is not None else _padded(length)
+        # with a plan the native calls take the pitch from the plan's sizes
+        pitch = plan.routed if plan is not None else _padded(length)
+        if plan is not None and length != plan.N * plan.S:
+            raise ValueError(f"{length} tokens; the plan has {plan.N} x {plan.S} pairs")
         _shape(codes, "codes", (rows, pitch))
         _shape(scales, "scales", (pitch // BLOCK, rows))
         self.device = _place(None, (codes, "codes"), (scales, "scales"))

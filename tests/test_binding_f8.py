@@ -169,3 +169,20 @@ def test_route_backward_refuses_other_types():
     expect(lambda: q.route_backward(l, r._replace(ids=ids.long()), w, f32(1)), "ids has dtype")
     expect(lambda: q.route_backward(l, r._replace(ids=i32(8)), w, f32(1)), "ids must be a tensor of 2")
     expect(lambda: q.route_backward(l, r._replace(valid=i32(4)), w, f32(1)), "valid has dtype")
+
+
+def test_quantized_operands_of_a_plan_have_its_sizes():
+    """The products take the width of a row of codes from the plan's sizes: operands of another width would be read at
+    wrong places and past their end."""
+    p = plan(40, 2, 3)
+    assert p.routed == 128 * 5 and p.routed % 128 == 0
+    u8 = torch.uint8
+
+    def tokens(width, length):
+        return lambda: q.F8Tokens(torch.zeros((6, width), dtype=u8), f32(width // 128, 6), 6, length, p)
+
+    expect(tokens(128, 80), "codes has shape")               # the pairs padded to 128, not the experts' own
+    expect(tokens(p.routed + 128, 80), "codes has shape")
+    expect(tokens(p.routed, 79), "79 tokens")
+    expect(tokens(p.routed, 40), "40 tokens")
+    expect(tokens(p.routed, 80), "device tensor")            # right: only its place is not
