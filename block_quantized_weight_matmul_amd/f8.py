@@ -209,10 +209,10 @@ def f8_quantize_t(x: torch.Tensor, plan=None) -> F8Tokens:
         raise ValueError("x has no columns")
     ld = K if x2.is_contiguous() and x2.is_cuda else _rows(x2, "x")
     d = x.get_device()
-    _place(d, (plan.data, "plan"))
+    at = plan.place(d)
     t = F8Tokens._empty(K, plan.routed, plan.N * plan.S, x.device, d, plan)
     _call(d, lib.qmm_f8_quantize_routed, x2.data_ptr(), _DT[x.dtype], ld, plan.N, plan.S, per_slot, K, plan.n_experts,
-          plan.data.data_ptr(), *t.ptrs)
+          at, *t.ptrs)
     return t
 
 
@@ -229,6 +229,7 @@ def f8_wgrad(g: F8Tokens, x: F8Tokens, plan=None, out: torch.Tensor = None, dtyp
     if x.device != device:
         raise ValueError(f"x is on cuda:{x.device}, g on cuda:{device}")
     shape = (M, K) if plan is None else (plan.n_experts, M, K)
+    at = None if plan is None else plan.place(device)
     dw = _out(out, shape, _dtype(dtype), device)
     ptrs = g.ptrs + x.ptrs
     if plan is None:
@@ -239,8 +240,7 @@ def f8_wgrad(g: F8Tokens, x: F8Tokens, plan=None, out: torch.Tensor = None, dtyp
         _call(device, lib.qmm_f8_wgrad, *ptrs, g.length, M, K, dw.data_ptr(), _DT[dw.dtype],
               ws.data_ptr() if nb else None, nb)
     else:
-        _place(device, (plan.data, "plan"))
-        _call(device, lib.qmm_f8_wgrad_id, *ptrs, plan.N, plan.S, M, K, plan.n_experts, plan.data.data_ptr(), dw.data_ptr(),
+        _call(device, lib.qmm_f8_wgrad_id, *ptrs, plan.N, plan.S, M, K, plan.n_experts, at, dw.data_ptr(),
               _DT[dw.dtype])
     return dw
 
@@ -414,8 +414,8 @@ class F8Matrix:
             raise ValueError(f"the plan has {plan.n_experts} experts, the matrix {self.n_experts}")
         per_slot = plan.per_slot(tokens.rows, "tokens")
         self._tokens(tokens)
-        _place(self.device, (plan.data, "plan"))
+        at = plan.place(self.device)
         y = _out(out, (plan.N, plan.S, self.M), _dtype(out_dtype), self.device)
         _call(self.device, lib.qmm_f8_gemm_id, self._h, *tokens.ptrs, plan.N, plan.S,
-              per_slot, plan.data.data_ptr(), y.data_ptr(), _DT[y.dtype])
+              per_slot, at, y.data_ptr(), _DT[y.dtype])
         return y

@@ -34,14 +34,23 @@ class Routing(NamedTuple):
 
 
 class RoutePlan:
-    """(token, slot) pairs of ids [N, S] sorted by expert; see route_plan."""
+    """(token, slot) pairs of ids [N, S] sorted by expert; see route_plan.  data is qmm_route_plan's buffer, int32, of
+    these sizes: every call that reads it checks that it holds as much."""
 
-    __slots__ = ("data", "N", "S", "n_experts", "routed")
+    __slots__ = ("data", "N", "S", "n_experts", "routed", "bytes")
 
-    def __init__(self, data, N, S, n_experts, routed=None):
+    def __init__(self, data, N, S, n_experts):
+        _tensor(data, "data", (torch.int32,), (1,))
         self.data, self.N, self.S, self.n_experts = data, N, S, n_experts
-        # tokens of a quantization along the plan's pairs
-        self.routed = lib.qmm_f8_routed_tokens(N * S, n_experts) if routed is None else routed
+        self.bytes, self.routed = _plan_size(N * S, n_experts)
+
+    def place(self, device):
+        """Pointer of the plan's buffer, which is as large as its sizes need and on device."""
+        if self.data.numel() * 4 < self.bytes or self.bytes == 0:
+            raise ValueError(f"the plan's data has {self.data.numel() * 4} bytes; {self.N} x {self.S} ids of {self.n_experts} "
+                             f"experts need {self.bytes}")
+        _place(device, (self.data, "plan"))
+        return self.data.data_ptr()
 
     @property
     def counts(self):
@@ -63,7 +72,15 @@ class RoutePlan:
         return self.per_slot(x.shape[0], name)
 
 
-_plan_sizes = {}  # of the pairs and experts seen: bytes, tokens of a routed quantization
+_plan_sizes = {}  # of the pairs and experts seen
+
+
+def _plan_size(pairs, E):
+    """Bytes of a plan, tokens of a quantization along its pairs."""
+    size = _plan_sizes.get((pairs, E))
+    if size is None:
+        size = _plan_sizes[pairs, E] = lib.qmm_route_plan_bytes(pairs, E), lib.qmm_f8_routed_tokens(pairs, E)
+    return size
 
 
 def route_plan(ids: torch.Tensor, n_experts: int) -> RoutePlan:
@@ -74,13 +91,10 @@ def route_plan(ids: torch.Tensor, n_experts: int) -> RoutePlan:
     if S < 1 or E < 1:
         raise ValueError("ids needs a slot and the plan an expert")
     device = _place(None, (ids, "ids"))
-    sizes = _plan_sizes.get((N * S, E))
-    if sizes is None:
-        sizes = _plan_sizes[N * S, E] = lib.qmm_route_plan_bytes(N * S, E), lib.qmm_f8_routed_tokens(N * S, E)
-    nb, routed = sizes
+    nb = _plan_size(N * S, E)[0]
     data = torch.empty(max(nb, 16) // 4, dtype=torch.int32, device=ids.device)
     _call(device, lib.qmm_route_plan, ids.data_ptr(), N, S, E, data.data_ptr(), nb)
-    return RoutePlan(data, N, S, E, routed)
+    return RoutePlan(data, N, S, E)
 
 
 def _logits(logits, valid):

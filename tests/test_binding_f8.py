@@ -186,3 +186,23 @@ def test_quantized_operands_of_a_plan_have_its_sizes():
     expect(tokens(p.routed, 79), "79 tokens")
     expect(tokens(p.routed, 40), "40 tokens")
     expect(tokens(p.routed, 80), "device tensor")            # right: only its place is not
+
+
+def test_plan_refuses_other_buffers():
+    """The products read tile lists and pairs from a plan: its buffer has qmm_route_plan_bytes, as int32."""
+    need = L.lib.qmm_route_plan_bytes(80, 3) // 4
+    expect(lambda: q.RoutePlan(i32(need).long(), 40, 2, 3), "data has dtype")
+    expect(lambda: q.RoutePlan(i32(need, 1), 40, 2, 3), "dimensions")
+    expect(lambda: q.RoutePlan([0] * need, 40, 2, 3), "torch tensor")
+    expect(lambda: q.RoutePlan(i32(need - 4), 40, 2, 3).place(0), "need")
+    expect(lambda: q.RoutePlan(i32(need), 60, 2, 3).place(0), "need")
+    expect(lambda: q.RoutePlan(i32(need), 40, 2, 1025).place(0), "need")       # no such plan
+    expect(lambda: q.RoutePlan(i32(need), 40, 2, 3).place(0), "device tensor")  # right: only its place is not
+    # and the calls that read one ask for it
+    short, m = q.RoutePlan(i32(need - 4), 40, 2, 3), matrix(6, 200, 3)
+    t = object.__new__(q.F8Tokens)
+    t.ptrs, t.pitch, t.rows, t.length, t.plan, t.device = (0, 0), 256, 40, 200, None, 0
+    expect(lambda: m.gemm_id(t, short), "need")
+    t = object.__new__(q.F8Tokens)
+    t.ptrs, t.pitch, t.rows, t.length, t.plan, t.device = (0, 0), short.routed, 6, 80, short, 0
+    expect(lambda: q.f8_wgrad(t, t, short), "need")
