@@ -92,6 +92,12 @@ def _rows(x, name):
     return ld
 
 
+def _overlap(a, b):
+    """Whether two contiguous tensors share memory."""
+    pa, pb = a.data_ptr(), b.data_ptr()
+    return pa < pb + b.numel() * b.element_size() and pb < pa + a.numel() * a.element_size()
+
+
 def _empty(shape, dtype, device):
     """torch.empty of two or three dimensions; with the strides named it takes 1.3 us, not 1.7."""
     n = shape[-1]
@@ -327,9 +333,9 @@ class F8Matrix:
     def _check_transpose(self, m):
         if not isinstance(m, F8Matrix) or (m.M, m.K, m.n_experts) != (self.K, self.M, self.n_experts):
             raise ValueError(f"the transpose must be an F8Matrix of {self.n_experts} x [{self.K}, {self.M}]")
-        if m is self or m.codes.data_ptr() == self.codes.data_ptr():
+        if any(_overlap(a, b) for a in (self.codes, self.scales) for b in (m.codes, m.scales)):
             raise ValueError("the transpose must have buffers of its own")
-        _place(self.device, (m.codes, "the transpose's codes"))
+        _place(self.device, (m.codes, "the transpose's codes"), (m.scales, "the transpose's scales"))
 
     def transposed(self, out: "F8Matrix" = None) -> "F8Matrix":
         """The matrix of W^T: the same codes and scales, transposed (into `out`'s buffers if given)."""

@@ -206,3 +206,21 @@ def test_plan_refuses_other_buffers():
     t = object.__new__(q.F8Tokens)
     t.ptrs, t.pitch, t.rows, t.length, t.plan, t.device = (0, 0), short.routed, 6, 80, short, 0
     expect(lambda: q.f8_wgrad(t, t, short), "need")
+
+
+def test_transpose_refuses_shared_buffers():
+    """Codes and scales are read while the transpose's are written: none of the four buffers may share memory."""
+    def square(codes, scales):
+        m = matrix(256, 256)
+        m.codes, m.scales = codes, scales
+        return m
+
+    u8 = torch.uint8
+    room, other = torch.zeros((512, 256), dtype=u8), torch.zeros((256, 256), dtype=u8)
+    m = square(room[:256], f32(2, 2))
+    expect(lambda: m.transposed(m), "buffers of its own")
+    expect(lambda: m.transposed(square(m.codes, f32(2, 2))), "buffers of its own")
+    expect(lambda: m.transposed(square(room[128:384], f32(2, 2))), "buffers of its own")
+    expect(lambda: m.transposed(square(other, m.scales)), "buffers of its own")
+    expect(lambda: m.transposed(square(other, room[:1, :16].view(torch.float32).view(2, 2))), "buffers of its own")
+    expect(lambda: m.transposed(square(room[256:], f32(2, 2))), "device tensor")   # right: only its place is not
