@@ -126,9 +126,10 @@ def _dtype(t):
 class F8Tokens:
     """Quantized rows: codes [R, padded C] uint8 and scales [padded C / 128, R] fp32.  C, the length of the quantized
     axis, is K for tokens ([N, K]) and the number of tokens for a transposed quantization (`channels` rows).  With a plan
-    (f8_quantize_t) C is its pairs and a row has plan.routed codes, each expert's pairs padded on their own."""
+    (f8_quantize_t) C is its pairs and a row has plan.routed codes, each expert's pairs padded on their own.  transposed:
+    True and False as f8_quantize_t and f8_quantize made it, None for a caller's own codes, which may be either."""
 
-    __slots__ = ("_codes", "_scales", "_buffer", "ptrs", "pitch", "rows", "length", "plan", "device")
+    __slots__ = ("_codes", "_scales", "_buffer", "ptrs", "pitch", "rows", "length", "plan", "device", "transposed")
 
     def __init__(self, codes, scales, rows, length, plan=None):
         _tensor(codes, "codes", _CODES, (2,))
@@ -142,17 +143,17 @@ class F8Tokens:
         self.device = _place(None, (codes, "codes"), (scales, "scales"))
         self._codes, self._scales, self._buffer = codes, scales, None
         self.ptrs = codes.data_ptr(), scales.data_ptr()
-        self.pitch, self.rows, self.length, self.plan = pitch, rows, length, plan
+        self.pitch, self.rows, self.length, self.plan, self.transposed = pitch, rows, length, plan, None
 
     @classmethod
-    def _empty(cls, rows, pitch, length, on, device, plan=None):
+    def _empty(cls, rows, pitch, length, on, device, transposed, plan=None):
         """Room for codes and scales in one buffer; the tensors are made when asked for."""
         t = object.__new__(cls)
         t._buffer = torch.empty(rows * pitch + rows * (pitch // BLOCK) * 4, dtype=torch.uint8, device=on)
         t._codes = t._scales = None
         at = t._buffer.data_ptr()
         t.ptrs = at, at + rows * pitch
-        t.pitch, t.rows, t.length, t.plan, t.device = pitch, rows, length, plan, device
+        t.pitch, t.rows, t.length, t.plan, t.device, t.transposed = pitch, rows, length, plan, device, transposed
         return t
 
     @property
@@ -184,8 +185,8 @@ def _quantize(x, along_k, along_n):
     N, K = x.shape
     ld = K if x.is_contiguous() and x.is_cuda else _rows(x, "x")
     device, d = x.device, x.get_device()
-    r = F8Tokens._empty(N, _padded(K), K, device, d) if along_k else None
-    c = F8Tokens._empty(K, _padded(N), N, device, d) if along_n else None
+    r = F8Tokens._empty(N, _padded(K), K, device, d, False) if along_k else None
+    c = F8Tokens._empty(K, _padded(N), N, device, d, True) if along_n else None
     _call(d, lib.qmm_f8_quantize, x.data_ptr(), _DT[x.dtype], ld, N, K, *(r.ptrs if along_k else (None, None)),
           *(c.ptrs if along_n else (None, None)))
     return r, c
@@ -216,7 +217,7 @@ def f8_quantize_t(x: torch.Tensor, plan=None) -> F8Tokens:
     ld = K if x2.is_contiguous() and x2.is_cuda else _rows(x2, "x")
     d = x.get_device()
     at = plan.place(d)
-    t = F8Tokens._empty(K, plan.routed, plan.N * plan.S, x.device, d, plan)
+    t = F8Tokens._empty(K, plan.routed, plan.N * plan.S, x.device, d, True, plan)
     _call(d, lib.qmm_f8_quantize_routed, x2.data_ptr(), _DT[x.dtype], ld, plan.N, plan.S, per_slot, K, plan.n_experts,
           at, *t.ptrs)
     return t
@@ -231,6 +232,8 @@ def f8_wgrad(g: F8Tokens, x: F8Tokens, plan=None, out: torch.Tensor = None, dtyp
         raise ValueError(f"g has {g.length} tokens, x has {x.length}")
     if g.plan is not plan or x.plan is not plan:
         raise ValueError("g and x must be quantized with the plan of this call (none without one)")
+    if g.transposed is False or x.transposed is False:
+        raise ValueError("g and x must be quantized along the tokens (f8_quantize_t)")
     M, K, device = g.rows, x.rows, g.device
     if x.device != device:
         raise ValueError(f"x is on cuda:{x.device}, g on cuda:{device}")
@@ -378,6 +381,8 @@ class F8Matrix:
             raise ValueError("tokens must come from f8_quantize")
         if t.length != self.K:
             raise ValueError(f"tokens have K={t.length}, matrix has K={self.K}")
+        if t.transposed:
+            raise ValueError("tokens are quantized along the tokens (f8_quantize_t); a product takes them along K (f8_quantize)")
         if t.device != self.device:
             raise ValueError(f"tokens are on cuda:{t.device}; the matrix is on cuda:{self.device}")
 

@@ -201,10 +201,10 @@ def test_plan_refuses_other_buffers():
     # and the calls that read one ask for it
     short, m = q.RoutePlan(i32(need - 4), 40, 2, 3), matrix(6, 200, 3)
     t = object.__new__(q.F8Tokens)
-    t.ptrs, t.pitch, t.rows, t.length, t.plan, t.device = (0, 0), 256, 40, 200, None, 0
+    t.ptrs, t.pitch, t.rows, t.length, t.plan, t.device, t.transposed = (0, 0), 256, 40, 200, None, 0, None
     expect(lambda: m.gemm_id(t, short), "need")
     t = object.__new__(q.F8Tokens)
-    t.ptrs, t.pitch, t.rows, t.length, t.plan, t.device = (0, 0), short.routed, 6, 80, short, 0
+    t.ptrs, t.pitch, t.rows, t.length, t.plan, t.device, t.transposed = (0, 0), short.routed, 6, 80, short, 0, None
     expect(lambda: q.f8_wgrad(t, t, short), "need")
 
 
@@ -224,3 +224,19 @@ def test_transpose_refuses_shared_buffers():
     expect(lambda: m.transposed(square(other, m.scales)), "buffers of its own")
     expect(lambda: m.transposed(square(other, room[:1, :16].view(torch.float32).view(2, 2))), "buffers of its own")
     expect(lambda: m.transposed(square(room[256:], f32(2, 2))), "device tensor")   # right: only its place is not
+
+
+def test_operands_quantized_along_the_other_axis():
+    """Where N equals K (or M) the shapes do not tell f8_quantize from f8_quantize_t: what made them does."""
+    def square(transposed):
+        t = object.__new__(q.F8Tokens)
+        t.ptrs, t.pitch, t.rows, t.length, t.plan, t.device, t.transposed = (0, 0), 256, 200, 200, None, 0, transposed
+        return t
+
+    along_k, along_tokens, own = square(False), square(True), square(None)
+    expect(lambda: matrix(48, 200).gemm(along_tokens), "along K")
+    expect(lambda: matrix(48, 200, 4).gemm_id(along_tokens, plan(200, 1, 4)), "along K")
+    expect(lambda: q.f8_wgrad(along_k, along_tokens), "along the tokens")
+    expect(lambda: q.f8_wgrad(along_tokens, along_k), "along the tokens")
+    for t in (along_k, own):     # accepted: refused for the plan's buffer only
+        expect(lambda: matrix(48, 200, 4).gemm_id(t, plan(200, 1, 4)), "need")
