@@ -2,12 +2,15 @@
 are refused for their placement, before a C call) and the C ABI's checks before it looks for a device."""
 
 import ctypes
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import block_quantized_weight_matmul_amd as q
 from block_quantized_weight_matmul_amd import _lib as L
+from tests.conftest import ROOT
 
 
 def expect(fn, text):
@@ -240,3 +243,26 @@ def test_operands_quantized_along_the_other_axis():
     expect(lambda: q.f8_wgrad(along_tokens, along_k), "along the tokens")
     for t in (along_k, own):     # accepted: refused for the plan's buffer only
         expect(lambda: matrix(48, 200, 4).gemm_id(t, plan(200, 1, 4)), "need")
+
+
+def test_import_needs_no_private_names_of_torch():
+    """Without torch's private shortcuts for the current device and stream the binding takes the public calls."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import block_quantized_weight_matmul_amd as q
+from block_quantized_weight_matmul_amd import f8
+
+class Stream:
+    cuda_stream = 77
+
+torch.cuda.current_device = lambda: 3
+torch.cuda.current_stream = lambda device: Stream if device == 3 else None
+seen = []
+f8._call(3, lambda *a: seen.append(a) or 0, 1, 2)
+assert seen == [(1, 2, 77)], seen
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
