@@ -27,6 +27,15 @@ _DT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
+class _Seen(dict):
+    """Sizes of calls seen before, which only the library computes: 1024 at most, then it starts anew."""
+
+    def __setitem__(self, key, value):
+        if len(self) >= 1024:
+            self.clear()
+        super().__setitem__(key, value)
+
+
 def _padded(n):
     return (n + BLOCK - 1) // BLOCK * BLOCK
 
@@ -225,7 +234,7 @@ def f8_quantize_t(x: torch.Tensor, plan=None) -> F8Tokens:
     return t
 
 
-_wgrad_need = {}  # workspace bytes of the sizes seen
+_wgrad_need = _Seen()  # workspace bytes of the sizes seen
 
 
 def f8_wgrad(g: F8Tokens, x: F8Tokens, plan=None, out: torch.Tensor = None, dtype=torch.float32) -> torch.Tensor:
@@ -279,7 +288,7 @@ class F8Matrix:
         _shape(scales, "scales", ((E,) if scales.dim() == 3 or E > 1 else ()) + (R, G))
         device = _place(None, (codes, "codes"), (scales, "scales"))
         self.M, self.K, self.n_experts, self.codes, self.scales, self.device = M, K, E, codes, scales, device
-        self._need = {}  # workspace bytes of the calls seen: N of linear, ~N of gemm, (N, S, per_slot) of linear_id
+        self._need = _Seen()  # workspace bytes of the calls seen: N of linear, ~N of gemm, (N, S, per_slot) of linear_id
         h = ctypes.c_void_p()
         with torch.cuda.device(device):
             check(lib.qmm_f8_create(ctypes.byref(h), codes.data_ptr(), scales.data_ptr(), E, M, K))

@@ -19,7 +19,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from ._lib import lib
-from .f8 import _DT, _call, _empty, _out, _place, _shape, _tensor
+from .f8 import _DT, _Seen, _call, _empty, _out, _place, _shape, _tensor
 
 
 class Routing(NamedTuple):
@@ -72,7 +72,7 @@ class RoutePlan:
         return self.per_slot(x.shape[0], name)
 
 
-_plan_sizes = {}  # of the pairs and experts seen
+_plan_sizes = _Seen()  # of the pairs and experts seen
 
 
 def _plan_size(pairs, E):
@@ -108,7 +108,7 @@ def _logits(logits, valid):
     return device
 
 
-_route_need = {}  # workspace bytes of the sizes seen
+_route_need = _Seen()  # workspace bytes of the sizes seen
 
 
 def route(logits: torch.Tensor, S: int, normalise: bool = True, coef: float = 0.0,

@@ -266,3 +266,17 @@ assert seen == [(1, 2, 77)], seen
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_sizes_kept_between_calls_are_bounded():
+    """A server with any number of tokens meets ever new sizes: what is kept of them does not grow with it."""
+    from block_quantized_weight_matmul_amd import f8, routing
+    for n in range(1, 3000):
+        q.RoutePlan(i32(4), n, 1, 5)
+    assert len(routing._plan_sizes) <= 1024
+    assert q.RoutePlan(i32(4), 7, 1, 5).bytes == L.lib.qmm_route_plan_bytes(7, 5)
+    assert all(type(d) is f8._Seen for d in (routing._plan_sizes, routing._route_need, f8._wgrad_need))
+    d = f8._Seen()
+    for n in range(3000):
+        v = d[n] = n + 1
+        assert v == n + 1 and d.get(n) == n + 1 and len(d) <= 1024
