@@ -750,8 +750,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t* id
 
 // ---- weighted sum of the slots ------------------------------------------------------------------
 
-// WT: type of the weights, -1 for none (a plain sum).  8 columns a thread.  Bound by memory: 2048 x 8 x 4096 in bf16 22.8
-// us, 6.6 TB/s.
+// WT: type of the weights, -1 for none (a plain sum).  8 columns a thread.  A slot of weight 0 is left out whatever its row
+// holds: an empty slot's row is NaN where the block formats made it.  Bound by memory: 2048 x 8 x 4096 in bf16 22.8 us, 6.6
+// TB/s.
 template <int YT, int WT, bool VEC>
 __global__ __launch_bounds__(256) void k_combine(const typename Elem<YT>::T* y, const void* w, int64_t N, int S, int64_t M,
                                                  typename Elem<YT>::T* out) {
@@ -771,7 +772,7 @@ __global__ __launch_bounds__(256) void k_combine(const typename Elem<YT>::T* y, 
     }
     if constexpr (WT >= 0) k = static_cast<float>(static_cast<const typename Elem<WT < 0 ? 0 : WT>::T*>(w)[t * S + s]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = fmaf(k, v[e], o[e]);
+    for (int e = 0; e < 8; ++e) o[e] = fmaf(k, k == 0.0f ? 0.0f : v[e], o[e]);
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e)

@@ -194,7 +194,7 @@ def _slots(y, weights):
 
 def route_combine(y: torch.Tensor, weights: Optional[torch.Tensor] = None, out: torch.Tensor = None) -> torch.Tensor:
     """out [N, M] = sum over the slots of weights [N, S] (fp32 or y's type) times y [N, S, M]; without weights the plain
-    sum (the gradient of a row that a token's slots share)."""
+    sum (the gradient of a row that a token's slots share).  A slot of weight 0 adds nothing, whatever its row holds."""
     device, N, S, M = _slots(y, weights)
     o = _out(out, (N, M), y.dtype, device)
     if o.dtype != y.dtype:

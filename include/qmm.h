@@ -548,9 +548,12 @@ qmm_status qmm_route_backward(const void *logits, qmm_dtype lt, int64_t N, int64
 /*
  * qmm_route_combine -- out[t] = sum_s weights[t, s] y[t, s] over y [N, S, M], in fp32, slots in
  * order, rounded once to y's type (out [N, M] has it too).  weights [N, S] fp32 or of y's type
- * (wt); NULL: the plain sum, the gradient of a token row that its slots share.
+ * (wt); NULL: the plain sum, the gradient of a token row that its slots share.  A slot of weight
+ * 0 adds nothing, whatever its row holds: qmm_gemm_id and qmm_gemm_id_tiled fill the row of an
+ * empty slot (id -1, to which qmm_route gives the weight 0) with NaN.
  * qmm_route_combine_backward -- dy[t, s] = weights[t, s] dout[t] (fp32 product, rounded to y's
- * type) and dweights[t, s] = <y[t, s], dout[t]> (fp32 sum, rounded to wt).
+ * type) and dweights[t, s] = <y[t, s], dout[t]> (fp32 sum, rounded to wt), also where the weight
+ * is 0: NaN for a NaN row.  qmm_route_backward takes no gradient of an empty slot.
  * All contiguous and element-aligned.  S 1..64.
  */
 qmm_status qmm_route_combine(const void *y, qmm_dtype yt, const void *weights, qmm_dtype wt,

@@ -62,5 +62,9 @@ def route_backward(logits, r, normalise, coef, dweights=None, dloss=None):
 
 
 def combine(y, w=None):
+    """Sum over the slots, a slot of weight 0 left out whatever it holds."""
     y = np.asarray(y, dtype=np.float64)
-    return y.sum(1) if w is None else (y * np.asarray(w, dtype=np.float64)[:, :, None]).sum(1)
+    if w is None:
+        return y.sum(1)
+    w = np.asarray(w, dtype=np.float64)[:, :, None]
+    return (np.where(w == 0, 0, y) * w).sum(1)

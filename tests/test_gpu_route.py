@@ -341,3 +341,47 @@ def test_logits_past_32_bits():
     dw = torch.randn(N, S, device="cuda")
     d = q.route_backward(l, r, dw)
     assert torch.equal(d[-50:], q.route_backward(l[-50:], few, dw[-50:]))
+
+
+@pytest.mark.parametrize("tiled", [False, True])
+def test_router_ids_through_the_block_formats(tiled):
+    """The router's ids go into the block formats' expert products, where an id of -1 makes a NaN row: its weight is 0, and
+    the sum leaves the slot out.  Backward, an empty slot has no gradient."""
+    g = np.random.default_rng(41)
+    N, E, S, M, K = 24, 5, 3, 64, 512
+    values = g.standard_normal((E, M, K)).astype(np.float32) * 0.05
+    blocks = torch.cat([q.quantize(dev(v), "q8_0").view(-1) for v in values])
+    experts = q.QMatrix(blocks, "q8_0", M, K, E)
+    l = logits_of(g, N, E, "f32", 0.5)
+    r = q.route(l, S, coef=0.01)
+    assert bool((r.ids == -1).any()) and int(r.counts[E]) < N
+    x, dout = dev(g.standard_normal((N, K))), dev(g.standard_normal((N, M)))
+    y = (experts.gemm_id_tiled if tiled else experts.gemm_id)(x, r.ids)
+    empty = r.ids == -1
+    assert bool(torch.isnan(y[empty]).all()) and bool((r.weights[empty] == 0).all())
+    w = host64(r.weights)
+    for dt in DTYPES.values():
+        yt = y.to(dt)
+        yv = np.where(to_host(empty)[:, :, None], 0, host64(yt))
+        check(q.route_combine(yt, r.weights), O.combine(yv, w), O.combine(np.abs(yv), w) * S * 2.0 ** -24, f"out {dt}")
+    dy, dw = q.route_combine_backward(y, r.weights, dout)
+    assert bool((dy[empty] == 0).all())
+    d = q.route_backward(l, r, dw, torch.ones((), device="cuda"))
+    want = O.route(host64(l), S, True, 0.01)
+    dwv = np.where(to_host(empty), 0, host64(dw))
+    assert_gradient(d, O.route_backward(host64(l), want, True, 0.01, dwv, 1.0), want, dwv, True, 0.01)
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("M", [5, 24])
+def test_slots_of_weight_zero_add_nothing(dtype, M):
+    dt = DTYPES[dtype]
+    y = torch.ones((3, 2, M), device="cuda", dtype=dt)
+    y[0, 1], y[1, 0], y[2] = float("nan"), float("inf"), float("nan")
+    for wt in {torch.float32, dt}:
+        w = torch.tensor([[2.0, 0.0], [-0.0, 3.0], [0.0, 0.0]], device="cuda", dtype=wt)
+        out = q.route_combine(y, w)
+        assert out[:, 0].tolist() == [2.0, 3.0, 0.0] and torch.equal(out, out[:, :1].expand(3, M))
+        w[1, 0] = float("nan")      # a NaN weight stays one
+        assert bool(torch.isnan(q.route_combine(y, w)[1]).all())
+    assert bool(torch.isnan(q.route_combine(y)[0]).all())   # a plain sum has every slot
