@@ -173,8 +173,9 @@ __global__ __launch_bounds__(64 * W) void k_f8_few(FewArgs a) {
           s = b.sx[u][j];
         }
         const f32x4 p = group_sum(A, T);
+        const float2 o1 = scale_order(s, sw), o2 = scale_order(s, sw2);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(p[e], s * (e < upto ? sw : sw2), acc[j][e]);
+        for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(p[e] * (e < upto ? o1.x : o2.x), e < upto ? o1.y : o2.y, acc[j][e]);
       }
     }
   };
@@ -315,9 +316,9 @@ __global__ __launch_bounds__(kIdThreads) void k_f8_few_id(FewIdArgs a) {
         A.set(lo[u], hi[u]);
         B.set(tlo, thi);
         const f32x4 v = group_sum(A, B);
-        const float s = scales[g * n + t] * sw;
+        const float2 s = scale_order(scales[g * n + t], sw);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fmaf(v[i], s, acc[i]);
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(v[i] * s.x, s.y, acc[i]);
       }
       if (g0 + kBatch <= last) load(g0 + kBatch);
     }

@@ -40,13 +40,16 @@ struct GemmArgs {
   int vec;            // 16 bytes of consecutive outputs may be stored at once
 };
 
+// waves a SIMD that the LDS of a tile's stages leaves room for
+constexpr int tile_waves(int TM, int TN) { return TM + TN > 192 ? 2 : TM + TN > 128 ? 3 : 4; }
+
 // One workgroup: TM rows x TN tokens, its waves in a WM x WN grid; K in stages of one group, two stages in LDS.
 // A stage's rows are 128 bytes, two to the 64 banks; their eight 16-byte pieces are stored xored with bits 1..3 of the
 // row, so that 16 lanes that read one piece of 16 rows use every bank once (xored with bits 0..2, the reads took twice
 // the cycles, and a 256 x 256 stage 4190 instead of 3570).
 //
-// The second bound, waves per SIMD, keeps the compiler at 256 registers: above, it puts the sums of the matrix cores into
-// the accumulation registers, which the vector units cannot read.
+// The second bound, waves per SIMD, keeps the compiler at 256 registers or fewer: above, it puts the sums of the matrix
+// cores into the accumulation registers, which the vector units cannot read.
 // EXACT: the cores of an fp32 output (f8_mma.hpp); ST: the type stored.
 //
 // 16-bit outputs: 4096 x 4096 x 2560 47 us, 1.83 PFLOP/s; 8192^3 481 us, 2.29; dW of the former 66 us; 128 experts of 4096
@@ -54,7 +57,7 @@ struct GemmArgs {
 // instructions: the fma of the group sums (promotion) and the reads of LDS do not hide behind them entirely, and power
 // holds the clock at 1.7 to 2.1 GHz.
 template <int TM, int TN, int WM, int WN, int MODE, bool EXACT, int ST>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
+__global__ __launch_bounds__(64 * WM * WN, tile_waves(TM, TN)) void k_f8_gemm(GemmArgs a) {
   constexpr int NT = 64 * WM * WN, RT = TM / WM / 32, CT = TN / WN / 32;
   constexpr int AI = TM * 8 / NT, BI = TN * 8 / NT;  // 16-byte pieces a thread stages
   static_assert(AI * NT == TM * 8 && BI * NT == TN * 8, "tile");
@@ -225,8 +228,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
   const uint8_t* Abase = lds + wm * (TM / WM) * 128;
   const uint8_t* Bbase = lds + (TM + wn * (TN / WN)) * 128;
   const float* Sbase = reinterpret_cast<const float*>(lds + (TM + TN) * 128);
+  // Scales.  The sweep over the groups multiplies a group's sum by its token's and its row block's scale in one step
+  // (kRowScale: by one after the other), which is right unless their product leaves fp32's normal range (the sum times the
+  // token's may overflow).  A wave that met such scales, from operands with both largest values around 2^-55 or a product
+  // of them above 2^145, makes its outputs anew behind the sweep, the scales in order of size.  That costs the others 0 to
+  // 2% (8192^3 474 -> 477 us).  Asking in every stage made each wait for its scales (480 us); a second sweep by the whole
+  // workgroup had it agree on one (experts +3%).
   F b[CT];
   float sc[CT];
+  uint32_t least = ~0u, most = 0u;  // bits of the smallest and the largest factor; a NaN counts as large
   auto read_b = [&](int buf) {
     const float* S = Sbase + buf * (kStage / 4);
     const float wscale = kRowScale ? 1.0f : S[TS + wm * (TM / WM) / 128];
@@ -245,7 +255,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
   };
   auto add = [&](f32x16& to, const f32x16& p, float s, const f32x4* rs) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) to[e] = fmaf(p[e], kRowScale ? s * rs[e / 4][e % 4] : s, to[e]);
+    for (int e = 0; e < 16; ++e) to[e] = kRowScale ? fmaf(p[e] * s, rs[e / 4][e % 4], to[e]) : fmaf(p[e], s, to[e]);
   };
 
   // Outputs leave through LDS, 32 tokens of the wave's rows at a time: a lane holds 4 rows of one token, and stores
@@ -328,9 +338,61 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_f8_gemm(GemmArgs a) {
 #pragma unroll
       for (int j = 0; j < CT; ++j) add(acc[i][j], group_sum(av, b[j]), sc[j], rs);
     }
+    __builtin_amdgcn_sched_barrier(0);  // the scales are looked at behind the products
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+      if (!kRowScale) least = min(least, __float_as_uint(sc[j]));
+      most = max(most, __float_as_uint(sc[j]));
+    }
+  }
+  const bool ordered = __any(kRowScale ? most > 0x71800000u : least < 0x00800000u || most >= 0x7F800000u);  // 2^100; 2^-126, infinity
+  if (ordered) {
+    // 32 x 32 outputs at a time, straight from and to global memory, in few registers
+#pragma unroll 1
+    for (int ij = 0; ij < RT * CT; ++ij) {
+      const int ra = wm * (TM / WM) + ij / CT * 32, tb = wn * (TN / WN) + ij % CT * 32 + row;  // first row; token
+      auto at = [&](int r) { return r0 + (r < last_m ? r : last_m); };  // rows past the end repeat the last
+      const int64_t t = t0 + token(std::min(tb, TN - 1));
+      const uint8_t *pa = w + at(ra + row) * a.pitch + 32 * half, *pb = a.x + t * a.pitch + 32 * half;
+      const float* sa = wsc + std::min((r0 + ra) / 128, (M - 1) / 128) * a.G;  // not kRowScale
+      f32x16 sum{};
+#pragma unroll 1
+      for (int64_t g = g0; g < g1; ++g) {
+        F fa, fb;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const uint8_t *qa = pa + g * 128 + 64 * m, *qb = pb + g * 128 + 64 * m;
+          fa.set(m, *reinterpret_cast<const i32x4*>(qa), *reinterpret_cast<const i32x4*>(qa + 16));
+          fb.set(m, *reinterpret_cast<const i32x4*>(qb), *reinterpret_cast<const i32x4*>(qb + 16));
+        }
+        const f32x16 p = group_sum(fa, fb);
+        const float s = a.xs[g * N + t];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          i32x4 rs;
+          if (kRowScale)  // 0 past the last row
+            rs = __builtin_amdgcn_raw_buffer_load_b128(uniform(wsc + g * M, static_cast<uint32_t>(M) * 4),
+                                                       4 * static_cast<uint32_t>(r0 + ra + 8 * k + 4 * half), 0, 0);
+          else
+            rs = __float_as_int(sa[g]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 o = scale_order(s, __int_as_float(rs[e]));
+            sum[4 * k + e] = fmaf(p[4 * k + e] * o.x, o.y, sum[4 * k + e]);
+          }
+        }
+      }
+      const bool mine_t = kId ? tb < count : t0 + tb < N;
+      T* out = y + (kId ? static_cast<int64_t>(a.plan[a.pd.order + first + std::min(tb, count - 1)]) : t0 + tb) * M;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t r = r0 + ra + e / 4 * 8 + half * 4 + e % 4;
+        if (mine_t && r < M) out[r] = to_elem<ST>(sum[e]);
+      }
+    }
   }
   __syncthreads();
-  store();
+  if (!ordered) store();
 }
 
 template <int TM, int TN, int WM, int WN, int MODE>

@@ -84,6 +84,11 @@ __device__ __forceinline__ f32x16 group_sum(const Frag32<true>& a, const Frag32<
   return c;
 }
 
+// The two scales of a group as the smaller and the larger (a NaN stays one of them).  Their product leaves fp32's range
+// where both are small or both large, though the sum times both does not: p * lo keeps its bits, since |p| >= 2^-18 and
+// lo >= 2^-80, and overflows only where the result does.
+__device__ __forceinline__ float2 scale_order(float a, float b) { return a < b ? make_float2(a, b) : make_float2(b, a); }
+
 template <int OT>
 __device__ __forceinline__ void store4(typename Elem<OT>::T* p, f32x4 v, int n, bool vec) {
   typedef typename Elem<OT>::T T;

@@ -633,3 +633,86 @@ def test_weights_past_32_bits():
         assert bool((y[:, 1] == 0).all())
         size = x.double().abs() @ w.double().abs().t()   # either way's error: 2^-10 of the terms (8-bit cores), 2^-8 of the result
         assert bool(((y[:, 0].double() - ref.double()).abs() <= size * 2.0 ** -9 + ref.double().abs() * 2.0 ** -8).all())
+
+
+# ---- scales whose product leaves fp32's range -----------------------------------------------------
+
+# Operands of one of three kinds.  "small": all positive, near 2^-66, so that every output is near K 2^-132, a normal fp32,
+# and the two scales near 2^-75 have a product below the smallest number.  "floor": the tokens near 2^-74, where the scale
+# is 2^-80, the rows near 2^-56.  "large": columns 0 of every four have tokens near 2^74 and rows of zero, columns 1 the
+# other way round, columns 2 codes of 1 .. 3 steps of 2^-9 in both, columns 3 none: the scales' product is past 2^128, the
+# outputs are finite.
+SCALE_KINDS = ["small", "floor", "large"]
+
+
+def extreme(g, kind, N, M, K, dtype):
+    u = lambda r: torch.rand((r, K), generator=g, device="cuda") / 2 + 0.5  # noqa: E731
+    if kind != "large":
+        a, b = (2.0 ** -66, 2.0 ** -66) if kind == "small" else (2.0 ** -74, 2.0 ** -56)
+        return (u(N) * a).to(dtype), (u(M) * b).to(dtype)
+    out = []
+    for rows, column in ((N, 0), (M, 1)):
+        t = torch.zeros((rows, K), device="cuda")
+        t[:, column::4] = u(rows)[:, column::4] * 2.0 ** 74
+        t[:, 2::4] = torch.randint(-3, 4, (rows, K), generator=g, device="cuda")[:, 2::4] * 2.0 ** (74 - 9 - 8.8)
+        out.append(t.to(dtype))
+    return out
+
+
+@pytest.mark.parametrize("kind", SCALE_KINDS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,M,K", [(1, 300, 515), (16, 2500, 700), (20, 300, 2560), (3, 40, 9728), (100, 130, 2560), (60, 700, 4000),
+                                   (300, 4000, 260), (2049, 4090, 2500), (4090, 2500, 2500)])
+def test_products_of_extreme_scales(N, M, K, dtype, kind):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x, w = extreme(g, kind, N, M, K, DTYPES[dtype])
+    m, t = q.F8Matrix.quantize(w), q.f8_quantize(x)
+    y = m.linear(x)
+    device_check(y, t.values(), m.dequantize(), kind)
+    assert bool((y != 0).any()) and torch.equal(y, m.gemm(t, out_dtype=DTYPES[dtype]))
+
+
+@pytest.mark.parametrize("kind", SCALE_KINDS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,K,N", [(130, 257, 300), (100, 300, 16300), (2500, 700, 130), (4090, 2500, 700), (4000, 4090, 500)])
+def test_weight_gradients_of_extreme_scales(M, K, N, dtype, kind):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    dy, x = (t.t() for t in extreme(g, kind, M, K, N, DTYPES[dtype]))   # the pattern of columns lies along the tokens
+    gt, xt = q.f8_quantize_t(dy.contiguous()), q.f8_quantize_t(x.contiguous())
+    assert gt.transposed and xt.transposed and not q.f8_quantize(x.contiguous()).transposed
+    dw = q.f8_wgrad(gt, xt, dtype=DTYPES[dtype])
+    device_check(dw, gt.values(), xt.values(), kind)
+    assert bool((dw != 0).any())
+
+
+@pytest.mark.parametrize("kind", SCALE_KINDS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,S,E,M,K", [(4, 8, 32, 300, 512), (40, 2, 3, 70, 4000), (300, 3, 4, 520, 700), (2000, 2, 4, 300, 260)])
+def test_expert_products_of_extreme_scales(N, S, E, M, K, dtype, kind):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x, w = extreme(g, kind, N, E * M, K, DTYPES[dtype])
+    m, ids = q.F8Matrix.quantize(w.view(E, M, K)), torch.randint(-1, E, (N, S), generator=g, device="cuda", dtype=torch.int32)
+    y, xv = m.linear_id(x, ids), q.f8_quantize(x).values()
+    for e in range(E):
+        t, s = (ids == e).nonzero(as_tuple=True)
+        if len(t):
+            device_check(y[t, s], xv[t], m.dequantize(e), f"expert {e}")
+    assert bool((y[ids < 0] == 0).all())
+
+
+def test_bad_scales_of_a_few_rows_stay_theirs():
+    """A tile whose first sweep meets scales out of range, rows of zeros, and rows with a NaN among the others."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    N, M, K = 300, 260, 520
+    x, w = torch.randn((N, K), generator=g, device="cuda"), torch.randn((M, K), generator=g, device="cuda")
+    w[128:] *= 2.0 ** -70
+    x[3] = 0.0
+    x[5] *= 2.0 ** -70
+    x[7, 200] = float("nan")
+    m, t = q.F8Matrix.quantize(w), q.f8_quantize(x)
+    y = m.gemm(t)
+    keep = torch.arange(N, device="cuda") != 7
+    assert bool(torch.isnan(y[7]).all()) and bool(torch.isfinite(y[keep]).all()) and bool((y[3] == 0).all())
+    device_check(y[keep], t.values()[keep], m.dequantize())
+    plain = q.F8Matrix.quantize(w[:128].contiguous())   # alone, without the second sweep: within its last bits
+    device_check(plain.gemm(t)[keep], t.values()[keep], plain.dequantize())
