@@ -136,7 +136,18 @@ hipError_t launch_route_combine(const void* y, int yt, const void* w, int wt, in
 hipError_t launch_route_combine_backward(const void* y, int yt, const void* w, int wt, int64_t N, int S, int64_t M,
                                          const void* dout, void* dy, void* dw, hipStream_t s);
 
+// A launch has fewer than 2^32 threads along x: one with more ends without an error and leaves outputs as they were (with
+// 2^32 exactly it is refused).  Grid of `blocks` workgroups, numbered by block_index(), in `many` layers along z, those
+// past 2^31 threads along y.  Workgroups from `blocks` on have nothing to do.
+inline dim3 long_grid(int64_t blocks, int threads = 256, int64_t many = 1) {
+  const int64_t most = (int64_t(1) << 31) / threads, x = blocks < most ? blocks : most;
+  return dim3(static_cast<unsigned>(x), static_cast<unsigned>((blocks + x - 1) / x), static_cast<unsigned>(many));
+}
+inline bool fits_grid(int64_t blocks, int threads) { return blocks * threads < (int64_t(1) << 32); }
+
 #ifdef __HIPCC__
+__device__ __forceinline__ int64_t block_index() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
+
 // ---- device helpers ----------------------------------------------------------------------------
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));

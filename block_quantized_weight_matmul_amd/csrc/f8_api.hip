@@ -2,7 +2,6 @@
 // and dispatch.  No device memory is allocated here and nothing synchronises.
 #include <string.h>
 
-#include <climits>
 #include <new>
 
 #include "api_common.hpp"

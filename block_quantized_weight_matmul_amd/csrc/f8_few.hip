@@ -7,7 +7,6 @@
 // One token of 4096 x 2560 takes 3.6 us (10.5 MB, an empty launch 1.5), of 2560 x 9728 8.1 (25 MB).  The expert form: 32
 // pairs of 128 experts of 4096 x 512 13.6 us for 62 MB.
 #include <algorithm>
-#include <climits>
 
 #include "f8.hpp"
 #include "f8_mma.hpp"

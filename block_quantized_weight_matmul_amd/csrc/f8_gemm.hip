@@ -2,7 +2,6 @@
 //
 // Tiled kernel for many tokens; the arithmetic and the choice of matrix cores are f8_mma.hpp's, few tokens f8_few.hip's.
 #include <algorithm>
-#include <climits>
 #include <cmath>
 
 #include "f8.hpp"
@@ -397,7 +396,7 @@ __global__ __launch_bounds__(64 * WM * WN, tile_waves(TM, TN)) void k_f8_gemm(Ge
 
 template <int TM, int TN, int WM, int WN, int MODE>
 hipError_t run_tile(const GemmArgs& a, int ot, int64_t blocks, hipStream_t st) {
-  if (blocks > INT_MAX) return hipErrorInvalidValue;
+  if (!fits_grid(blocks, 64 * WM * WN)) return hipErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks)), block(64 * WM * WN);
   switch (ot) {
     case DT_F32:
@@ -506,7 +505,7 @@ hipError_t run_dense(GemmArgs& a, int ot, int64_t many, const DensePlan& plan, f
   a.tiles_n = static_cast<int>((a.N + k.tn - 1) / k.tn);
   const int64_t blocks = static_cast<int64_t>(a.tiles_m) * a.tiles_n * many;
   if (plan.splits > 1) {
-    if (blocks > INT_MAX) return hipErrorInvalidValue;
+    if (!fits_grid(blocks, 256)) return hipErrorInvalidConfiguration;
     void* y = a.y;
     const int64_t n = a.M * a.N;
     a.y = slabs;

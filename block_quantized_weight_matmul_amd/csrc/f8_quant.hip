@@ -89,12 +89,13 @@ __global__ __launch_bounds__(tile_threads(tile_rows(ROWS, COLS))) void k_f8_quan
   __shared__ float2 cscale[128];  // scale and its inverse
   const int lane = threadIdx.x & 15, team = threadIdx.x >> 4, wave = threadIdx.x >> 6;
   const int64_t Kp = f8_pad(a.K);
-  const unsigned tiles_k = static_cast<unsigned>(Kp / kF8Block);
-  const int64_t g = blockIdx.x % tiles_k;  // tile along K
-  const int64_t j = blockIdx.x / tiles_k;  // tile along the rows
+  const int64_t N = a.N, tiles = a.plan ? a.pd.cap[kPlanTileKinds - 1] : (N + kF8Block - 1) / kF8Block;
+  const unsigned tiles_k = static_cast<unsigned>(Kp / kF8Block), b = static_cast<unsigned>(block_index());
+  const int64_t g = b % tiles_k;  // tile along K
+  const int64_t j = b / tiles_k;  // tile along the rows
+  if (j >= tiles) return;
   const T* x = static_cast<const T*>(a.x);
-  const int64_t N = a.N;
-  const int64_t e = blockIdx.y;  // expert of a weight
+  const int64_t e = blockIdx.z;  // expert of a weight
   if (!ROWS && !COLS) x += e * a.N * a.K;
   const int64_t c = g * kF8Block + lane * 8;
   const int r0 = team * R;
@@ -139,7 +140,6 @@ __global__ __launch_bounds__(tile_threads(tile_rows(ROWS, COLS))) void k_f8_quan
       }
     }
   }
-  const int64_t tiles = a.plan ? a.pd.cap[kPlanTileKinds - 1] : (N + kF8Block - 1) / kF8Block;
   const int64_t Np = COLS ? tiles * kF8Block : w_rows_pad;
   if (COLS) {
 #pragma unroll
@@ -226,7 +226,9 @@ __global__ __launch_bounds__(tile_threads(4)) void k_f8_transpose(const uint8_t*
   __shared__ __align__(16) uint8_t tile[128 * 128];
   const int lane = threadIdx.x & 15, team = threadIdx.x >> 4, r0 = team * kTileRows;
   const int64_t Kp = f8_pad(K), Mp = f8_pad(M), G = Kp / kF8Block, R = Mp / kF8Block;
-  const int64_t g = blockIdx.x % static_cast<unsigned>(G), j = blockIdx.x / static_cast<unsigned>(G), e = blockIdx.y;
+  const unsigned b = static_cast<unsigned>(block_index());
+  const int64_t g = b % static_cast<unsigned>(G), j = b / static_cast<unsigned>(G), e = blockIdx.z;
+  if (j >= R) return;
   uint2 q[kTileRows];
 #pragma unroll
   for (int p = 0; p < kTileRows; ++p) {
@@ -255,7 +257,7 @@ __global__ __launch_bounds__(256) void k_f8_dequantize(const uint8_t* codes, con
   typedef typename Elem<DT>::T T;
   typedef T T8 __attribute__((ext_vector_type(8)));
   typedef T8 T8u __attribute__((aligned(sizeof(T))));
-  const int64_t Kp = f8_pad(K), i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  const int64_t Kp = f8_pad(K), i = (block_index() * 256 + threadIdx.x) * 8;
   if (i >= M * Kp) return;
   const int64_t r = i / Kp, k = i - r * Kp;
   const uint2 w = *reinterpret_cast<const uint2*>(codes + i);
@@ -276,8 +278,8 @@ __global__ __launch_bounds__(256) void k_f8_dequantize(const uint8_t* codes, con
 template <int DT, bool ROWS, bool COLS>
 hipError_t run_tiles(const F8QuantArgs& a, int64_t tiles, int64_t E, int64_t rows_pad, hipStream_t st) {
   if (tiles > INT_MAX) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(E));
-  k_f8_quant_tile<DT, ROWS, COLS><<<grid, tile_threads(tile_rows(ROWS, COLS)), 0, st>>>(a, rows_pad);
+  constexpr int kThreads = tile_threads(tile_rows(ROWS, COLS));
+  k_f8_quant_tile<DT, ROWS, COLS><<<long_grid(tiles, kThreads, E), kThreads, 0, st>>>(a, rows_pad);
   return hipGetLastError();
 }
 
@@ -331,17 +333,14 @@ hipError_t launch_f8_quantize_weight(const void* w, int dt, int64_t E, int64_t M
 hipError_t launch_f8_transpose(const F8Desc& m, uint8_t* codes_t, float* scales_t, hipStream_t st) {
   const int64_t tiles = m.Kp / kF8Block * (f8_pad(m.M) / kF8Block);
   if (tiles > INT_MAX) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(m.n_experts));
-  k_f8_transpose<<<grid, tile_threads(4), 0, st>>>(m.codes, m.scales, m.M, m.K, codes_t, scales_t);
+  k_f8_transpose<<<long_grid(tiles, tile_threads(4), m.n_experts), tile_threads(4), 0, st>>>(m.codes, m.scales, m.M, m.K, codes_t, scales_t);
   return hipGetLastError();
 }
 
 hipError_t launch_f8_dequantize(const F8Desc& m, int64_t expert, void* out, int dt, hipStream_t st) {
   const uint8_t* c = m.codes + expert * m.M * m.Kp;
   const float* s = m.scales + expert * (f8_pad(m.M) / kF8Block) * (m.Kp / kF8Block);
-  const int64_t blocks = (m.M * m.Kp / 8 + 255) / 256;
-  if (blocks > INT_MAX) return hipErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(blocks);
+  const dim3 grid = long_grid((m.M * m.Kp / 8 + 255) / 256);
   switch (dt) {
     case DT_F32: k_f8_dequantize<DT_F32><<<grid, 256, 0, st>>>(c, s, m.M, m.K, static_cast<float*>(out)); break;
     case DT_F16: k_f8_dequantize<DT_F16><<<grid, 256, 0, st>>>(c, s, m.M, m.K, static_cast<_Float16*>(out)); break;

@@ -6,7 +6,6 @@
 // loads and stores of V consecutive experts a lane took 1.2 times as long at 400 experts.  Sums over tokens (probabilities
 // per expert) go through one partial per workgroup, added in a fixed order: the same input gives the same bits.
 #include <algorithm>
-#include <climits>
 
 #include "f8.hpp"
 
@@ -757,7 +756,7 @@ template <int YT, int WT, bool VEC>
 __global__ __launch_bounds__(256) void k_combine(const typename Elem<YT>::T* y, const void* w, int64_t N, int S, int64_t M,
                                                  typename Elem<YT>::T* out) {
   typedef typename Elem<YT>::T T;
-  const int64_t cols = (M + 7) / 8, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t cols = (M + 7) / 8, i = block_index() * 256 + threadIdx.x;
   if (i >= N * cols) return;
   const int64_t t = i / cols, c = i % cols * 8;
   float o[8] = {};
@@ -782,10 +781,11 @@ __global__ __launch_bounds__(256) void k_combine(const typename Elem<YT>::T* y, 
 // One token a workgroup, its slots dealt to the waves: dy = w dout (one rounding to fp32, one to the type), dw = <y, dout>.
 // Bound by memory: 2048 x 8 x 4096 in bf16 54 us, 5.3 TB/s.
 template <int YT, int WT, bool VEC>
-__global__ __launch_bounds__(256) void k_combine_backward(const typename Elem<YT>::T* y, const typename Elem<WT>::T* w, int S,
-                                                          int64_t M, const typename Elem<YT>::T* dout,
+__global__ __launch_bounds__(256) void k_combine_backward(const typename Elem<YT>::T* y, const typename Elem<WT>::T* w, int64_t N,
+                                                          int S, int64_t M, const typename Elem<YT>::T* dout,
                                                           typename Elem<YT>::T* dy, typename Elem<WT>::T* dw) {
-  const int64_t t = blockIdx.x;
+  const int64_t t = block_index();
+  if (t >= N) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int s = wave; s < S; s += 4) {
     const float k = static_cast<float>(w[t * S + s]);
@@ -893,9 +893,7 @@ hipError_t combine_t(const void* y, const void* w, int64_t N, int S, int64_t M, 
   typedef typename Elem<YT>::T T;
   const int esz = YT == DT_F32 ? 4 : 2;
   const bool vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && M % 8 == 0 && (M * esz) % 16 == 0;
-  const int64_t blocks = (N * ((M + 7) / 8) + 255) / 256;
-  if (blocks > INT_MAX) return hipErrorInvalidValue;
-  const unsigned g = static_cast<unsigned>(blocks);
+  const dim3 g = long_grid((N * ((M + 7) / 8) + 255) / 256);
   if (vec) k_combine<YT, WT, true><<<g, 256, 0, st>>>(static_cast<const T*>(y), w, N, S, M, static_cast<T*>(out));
   else k_combine<YT, WT, false><<<g, 256, 0, st>>>(static_cast<const T*>(y), w, N, S, M, static_cast<T*>(out));
   return hipGetLastError();
@@ -908,12 +906,12 @@ hipError_t combine_backward_t(const void* y, const void* w, int64_t N, int S, in
   typedef typename Elem<WT>::T W;
   const bool vec = (reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(dout)) % 16 == 0 && M % 8 == 0;
   if (vec)
-    k_combine_backward<YT, WT, true><<<static_cast<unsigned>(N), 256, 0, st>>>(
-        static_cast<const T*>(y), static_cast<const W*>(w), S, M, static_cast<const T*>(dout), static_cast<T*>(dy),
+    k_combine_backward<YT, WT, true><<<long_grid(N), 256, 0, st>>>(
+        static_cast<const T*>(y), static_cast<const W*>(w), N, S, M, static_cast<const T*>(dout), static_cast<T*>(dy),
         static_cast<W*>(dw));
   else
-    k_combine_backward<YT, WT, false><<<static_cast<unsigned>(N), 256, 0, st>>>(
-        static_cast<const T*>(y), static_cast<const W*>(w), S, M, static_cast<const T*>(dout), static_cast<T*>(dy),
+    k_combine_backward<YT, WT, false><<<long_grid(N), 256, 0, st>>>(
+        static_cast<const T*>(y), static_cast<const W*>(w), N, S, M, static_cast<const T*>(dout), static_cast<T*>(dy),
         static_cast<W*>(dw));
   return hipGetLastError();
 }

@@ -716,3 +716,20 @@ def test_bad_scales_of_a_few_rows_stay_theirs():
     device_check(y[keep], t.values()[keep], m.dequantize())
     plain = q.F8Matrix.quantize(w[:128].contiguous())   # alone, without the second sweep: within its last bits
     device_check(plain.gemm(t)[keep], t.values()[keep], plain.dequantize())
+
+
+def test_dequantize_more_than_32_bits_of_threads():
+    M, K = 1 << 24, 2100
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 120e9:
+        pytest.skip("needs 120 GB")
+    codes = torch.zeros((M, 2176), dtype=torch.uint8, device="cuda")
+    codes[-5:, :K] = torch.randint(0, 126, (5, K), device="cuda", dtype=torch.uint8)
+    codes[3, :K] = codes[-1, :K]
+    m = q.F8Matrix(codes, torch.full((M // 128, 17), 0.5, device="cuda"), M, K)
+    w = m.dequantize(dtype=torch.bfloat16)
+    last = codes[-5:, :K].view(torch.float8_e4m3fn).bfloat16() * 0.5
+    assert torch.equal(w[-5:], last) and torch.equal(w[3], last[-1])
+    assert all(bool((w[i:i + 8] == 0).all()) for i in (4, M // 2, M // 2 - 8, M - 13))
+    del w, m, codes
+    torch.cuda.empty_cache()

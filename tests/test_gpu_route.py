@@ -385,3 +385,34 @@ def test_slots_of_weight_zero_add_nothing(dtype, M):
         w[1, 0] = float("nan")      # a NaN weight stays one
         assert bool(torch.isnan(q.route_combine(y, w)[1]).all())
     assert bool(torch.isnan(q.route_combine(y)[0]).all())   # a plain sum has every slot
+
+
+def test_sums_of_the_most_tokens():
+    """2^24 tokens: as many workgroups of 256 threads as HIP takes no longer along one axis."""
+    N = 1 << 24
+    g = torch.Generator(device="cuda").manual_seed(1)
+    y, dout = (torch.randn((N, 1, 1), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    w = torch.rand((N, 1), generator=g, device="cuda")
+    dy, dw = q.route_combine_backward(y, w, dout[:, 0])
+    assert torch.equal(dy, (w[:, :, None] * dout.float()).bfloat16()) and torch.equal(dw, (y.float() * dout.float())[:, 0])
+    assert torch.equal(q.route_combine(y, w), (w[:, :, None] * y.float()).bfloat16()[:, 0])
+
+
+def room(gigabytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gigabytes * 1e9:
+        pytest.skip(f"needs {gigabytes} GB")
+
+
+def test_sums_of_more_than_32_bits_of_threads():
+    N, M = 1 << 24, 2056
+    room(150)
+    y, w = torch.zeros((N, 1, M), device="cuda", dtype=torch.bfloat16), torch.full((N, 1), 2.0, device="cuda")
+    y[-3:] = torch.randn((3, 1, M), device="cuda")
+    y[5] = torch.randn((1, M), device="cuda")
+    out = torch.full((N, M), 7.0, device="cuda", dtype=torch.bfloat16)
+    q.route_combine(y, w, out=out)
+    assert torch.equal(out[-3:], 2 * y[-3:, 0]) and torch.equal(out[5], 2 * y[5, 0])
+    assert all(bool((out[i:i + 8] == 0).all()) for i in (6, 1 << 23, (1 << 23) - 8, N - 11))
+    del y, out
+    torch.cuda.empty_cache()
