@@ -30,8 +30,8 @@ struct F8Desc {
 // Routing plan: int32 arrays in one device buffer (route.hip builds it, the expert products read it).  Pairs are
 // sorted by bucket, ascending inside one: buckets 0 .. E-1 the experts, E the empty slots (id -1), E+1 ids that
 // name no expert.  map[t] lists, per token tile of kPlanTiles[t] pairs, (bucket, first position, end position).
-constexpr int kPlanTileKinds = 4;
-constexpr int kPlanTiles[kPlanTileKinds] = {16, 32, 64, 128};
+constexpr int kPlanTileKinds = 3;
+constexpr int kPlanTiles[kPlanTileKinds] = {32, 64, 128};
 struct PlanDesc {
   int64_t pairs, E;
   // int32 offsets in the buffer; totals: tiles of each kind

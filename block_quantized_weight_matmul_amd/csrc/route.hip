@@ -581,16 +581,18 @@ __device__ void plan_prefix(PlanShared& sh, int B) {
   __syncthreads();
 }
 
-// The tiles' lists: a quarter of the workgroup's threads to each kind, the workgroups in turn.
+// The tiles' lists: half of the workgroup's threads to the smallest tiles, which are as many as the others together, a
+// quarter to each of those; the workgroups in turn.
 __device__ void plan_tiles(const PlanShared& sh, const PlanDesc& d, int32_t* plan) {
-  constexpr int kEach = kPlanThreads / kPlanTileKinds;
-  const int B = static_cast<int>(d.E) + 2, t = threadIdx.x / kEach, T = kPlanTiles[0] << t;
+  constexpr int kQuarter = kPlanThreads / 4;
+  const int B = static_cast<int>(d.E) + 2, quarter = threadIdx.x / kQuarter, t = std::max(quarter - 1, 0);
+  const int T = kPlanTiles[0] << t, each = t == 0 ? 2 * kQuarter : kQuarter, at = threadIdx.x % each;
   int64_t cap = 0, map = 0;
 #pragma unroll
   for (int k = 0; k < kPlanTileKinds; ++k)
     if (k == t) { cap = d.cap[k]; map = d.map[k]; }
   const int32_t* tiles = sh.tiles[t];
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kEach + threadIdx.x % kEach; i < cap; i += static_cast<int64_t>(gridDim.x) * kEach) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * each + at; i < cap; i += static_cast<int64_t>(gridDim.x) * each) {
     int32_t* m = plan + map + 3 * i;
     if (i >= tiles[B]) {
       m[0] = -1;
@@ -609,7 +611,7 @@ __device__ void plan_tiles(const PlanShared& sh, const PlanDesc& d, int32_t* pla
     m[2] = sh.offs[lo + 1];
   }
 }
-static_assert(kPlanTiles[1] == 2 * kPlanTiles[0] && kPlanTiles[2] == 4 * kPlanTiles[0] && kPlanTiles[3] == 8 * kPlanTiles[0],
+static_assert(kPlanTileKinds == 3 && kPlanTiles[1] == 2 * kPlanTiles[0] && kPlanTiles[2] == 4 * kPlanTiles[0],
               "each kind of tile is twice the one before");
 
 // Pairs p0 .. p1 - 1 to their places, in order inside a bucket: base, then the waves in order, then lanes.
@@ -936,7 +938,7 @@ PlanDesc plan_desc(int64_t pairs, int64_t E) {
     at += 3 * d.cap[t];
   }
   d.scratch = at;
-  const int64_t blocks = pairs > 0 ? (pairs + plan_chunk(pairs) - 1) / plan_chunk(pairs) : 0;
+  const int64_t blocks = pairs > kPlanOneLaunch ? (pairs + plan_chunk(pairs) - 1) / plan_chunk(pairs) : 0;
   d.total = at + blocks * B;
   return d;
 }

@@ -280,3 +280,15 @@ def test_sizes_kept_between_calls_are_bounded():
     for n in range(3000):
         v = d[n] = n + 1
         assert v == n + 1 and d.get(n) == n + 1 and len(d) <= 1024
+
+
+def test_plan_holds_what_is_read():
+    """Counts, offsets, first tiles, the pairs in order, lists of the tiles of 32, 64 and 128 pairs, and above 32768 pairs
+    the counts of the chunks that its three launches share."""
+    for pairs, E in ((1, 1), (80, 3), (16384, 128), (32768, 8), (32769, 8), (1 << 22, 1024)):
+        B = E + 2
+        words = B + 2 * (B + 1) + 3 + pairs + sum(3 * (pairs // t + min(B, pairs)) for t in (32, 64, 128))
+        if pairs > 32768:
+            per = -(-pairs // 256)
+            words += -(-pairs // (-(-per // 1024) * 1024)) * B
+        assert L.lib.qmm_route_plan_bytes(pairs, E) == -(-words // 4) * 16, (pairs, E)
