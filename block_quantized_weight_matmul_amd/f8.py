@@ -103,10 +103,10 @@ def _rows(x, name):
     return ld
 
 
-def _overlap(a, b):
-    """Whether two contiguous tensors share memory."""
-    pa, pb = a.data_ptr(), b.data_ptr()
-    return pa < pb + b.numel() * b.element_size() and pb < pa + a.numel() * a.element_size()
+def _spans(codes, scales):
+    """First byte and the byte behind the last of two contiguous tensors."""
+    c, s = codes.data_ptr(), scales.data_ptr()
+    return c, c + codes.numel() * codes.element_size(), s, s + scales.numel() * scales.element_size()
 
 
 def _empty(shape, dtype, device):
@@ -288,6 +288,7 @@ class F8Matrix:
         _shape(scales, "scales", ((E,) if scales.dim() == 3 or E > 1 else ()) + (R, G))
         device = _place(None, (codes, "codes"), (scales, "scales"))
         self.M, self.K, self.n_experts, self.codes, self.scales, self.device = M, K, E, codes, scales, device
+        self._spans = _spans(codes, scales)
         self._need = _Seen()  # workspace bytes of the calls seen: N of linear, ~N of gemm, (N, S, per_slot) of linear_id
         h = ctypes.c_void_p()
         with torch.cuda.device(device):
@@ -347,9 +348,11 @@ class F8Matrix:
     def _check_transpose(self, m):
         if not isinstance(m, F8Matrix) or (m.M, m.K, m.n_experts) != (self.K, self.M, self.n_experts):
             raise ValueError(f"the transpose must be an F8Matrix of {self.n_experts} x [{self.K}, {self.M}]")
-        if any(_overlap(a, b) for a in (self.codes, self.scales) for b in (m.codes, m.scales)):
+        (c0, c1, s0, s1), (tc0, tc1, ts0, ts1) = self._spans, m._spans
+        if (c0 < tc1 and tc0 < c1) or (s0 < ts1 and ts0 < s1) or (c0 < ts1 and ts0 < c1) or (s0 < tc1 and tc0 < s1):
             raise ValueError("the transpose must have buffers of its own")
-        _place(self.device, (m.codes, "the transpose's codes"), (m.scales, "the transpose's scales"))
+        if m.device != self.device:
+            raise ValueError(f"the transpose is on cuda:{m.device}; the matrix is on cuda:{self.device}")
 
     def transposed(self, out: "F8Matrix" = None) -> "F8Matrix":
         """The matrix of W^T: the same codes and scales, transposed (into `out`'s buffers if given)."""

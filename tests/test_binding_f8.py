@@ -213,9 +213,11 @@ def test_plan_refuses_other_buffers():
 
 def test_transpose_refuses_shared_buffers():
     """Codes and scales are read while the transpose's are written: none of the four buffers may share memory."""
+    from block_quantized_weight_matmul_amd import f8
+
     def square(codes, scales):
         m = matrix(256, 256)
-        m.codes, m.scales = codes, scales
+        m.codes, m.scales, m._spans = codes, scales, f8._spans(codes, scales)
         return m
 
     u8 = torch.uint8
@@ -226,7 +228,10 @@ def test_transpose_refuses_shared_buffers():
     expect(lambda: m.transposed(square(room[128:384], f32(2, 2))), "buffers of its own")
     expect(lambda: m.transposed(square(other, m.scales)), "buffers of its own")
     expect(lambda: m.transposed(square(other, room[:1, :16].view(torch.float32).view(2, 2))), "buffers of its own")
-    expect(lambda: m.transposed(square(room[256:], f32(2, 2))), "device tensor")   # right: only its place is not
+    other_device = square(room[256:], f32(2, 2))
+    m._check_transpose(other_device)             # buffers of its own
+    other_device.device = 1
+    expect(lambda: m.transposed(other_device), "on cuda:1")
 
 
 def test_operands_quantized_along_the_other_axis():
