@@ -733,3 +733,76 @@ def test_dequantize_more_than_32_bits_of_threads():
     assert all(bool((w[i:i + 8] == 0).all()) for i in (4, M // 2, M // 2 - 8, M - 13))
     del w, m, codes
     torch.cuda.empty_cache()
+
+
+# ---- 16-bit outputs to one rounding ---------------------------------------------------------------
+
+# Codes of -8 .. 8 and scales of 1/2, 1 and 2: products of an octet span 6 bits, which the 8-bit cores hold, a group's sum
+# is a whole number below 2^13 and the sum over 32 groups of it times 1/4 .. 4 has 22 bits.  Every order of the sums is
+# exact in fp32, so that an output is its exact value rounded once.
+
+def whole_codes(g, rows, K, lead=()):
+    codes = torch.zeros(lead + (rows, O.padded(K)), device="cuda")
+    codes[..., :K] = torch.randint(-8, 9, lead + (rows, K), generator=g, device="cuda").float()
+    return codes.to(torch.float8_e4m3fn)
+
+
+def powers_of_two(g, *shape):
+    return 2.0 ** torch.randint(-1, 2, shape, generator=g, device="cuda").float()
+
+
+def whole_tokens(g, rows, K):
+    t = q.F8Tokens(whole_codes(g, rows, K), powers_of_two(g, O.padded(K) // 128, rows), rows, K)
+    return t, t.values().double()
+
+
+@pytest.mark.parametrize("N,M,K", LARGE + [(32, 2000, 4096), (8, 515, 130), (300, 257, 3900)])
+def test_products_to_one_rounding(N, M, K):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    blocks = powers_of_two(g, O.padded(M) // 128, O.padded(K) // 128)
+    m = q.F8Matrix(whole_codes(g, M, K), blocks, M, K)
+    t, x = whole_tokens(g, N, K)
+    y = x @ m.dequantize().double().t()
+    for dt in DTYPES.values():
+        assert torch.equal(m.gemm(t, out_dtype=dt), y.to(dt)), dt
+
+
+@pytest.mark.parametrize("N,M,K", [(300, 4000, 4000), (4000, 4090, 2500), (250, 8000, 2000), (384, 3000, 3000), (4000, 100, 300), (1000, 700, 130)])
+def test_weight_gradients_to_one_rounding(N, M, K):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    (gt, a), (xt, b) = whole_tokens(g, M, N), whole_tokens(g, K, N)
+    dw = a @ b.t()
+    for dt in DTYPES.values():
+        assert torch.equal(q.f8_wgrad(gt, xt, dtype=dt), dw.to(dt)), dt
+
+
+@pytest.mark.parametrize("N,S,E,M,K", [(4500, 2, 3, 3000, 200), (1500, 2, 3, 1000, 500), (300, 1, 250, 256, 1100), (2000, 4, 4, 500, 130),
+                                       (40, 2, 8, 64, 4000)])
+def test_expert_products_to_one_rounding(N, S, E, M, K):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    m = q.F8Matrix(whole_codes(g, M, K, (E,)), powers_of_two(g, E, O.padded(M) // 128, O.padded(K) // 128), M, K, E)
+    t, x = whole_tokens(g, N, K)
+    ids = torch.randint(-1, E, (N, S), generator=g, device="cuda", dtype=torch.int32)
+    plan = q.route_plan(ids, E)
+    for dt in DTYPES.values():
+        y = m.gemm_id(t, plan, out_dtype=dt)
+        for e in range(E):
+            n, s = (ids == e).nonzero(as_tuple=True)
+            assert torch.equal(y[n, s], (x[n] @ m.dequantize(e).double().t()).to(dt)), (e, dt)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("N", [1, 16, 300, 2049])
+def test_a_channel_300_times_larger(N, dtype):
+    """Hidden states have such channels: their octet's other products lose bits on the 8-bit cores, within the bound."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    M, K = 1000, 2560
+    x = torch.randn((N, K), generator=g, device="cuda")
+    x[:, 77] *= 300.0
+    m, t = q.F8Matrix.quantize(torch.randn((M, K), generator=g, device="cuda") * 0.02), q.f8_quantize(x)
+    y = m.gemm(t, out_dtype=DTYPES[dtype])
+    device_check(y, t.values(), m.dequantize(), "channel")
+    # beside the output's own rounding the cores cost at most what the header says of such data, 2^-13 of the root mean square
+    ref = t.values().double() @ m.dequantize().double().t()
+    own, all_ = ((v.double() - ref).pow(2).mean().sqrt() / ref.pow(2).mean().sqrt() for v in (ref.to(y.dtype), y))
+    assert float(all_) ** 2 <= float(own) ** 2 * 1.02 + 2.0 ** -26

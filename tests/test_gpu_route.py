@@ -416,3 +416,36 @@ def test_sums_of_more_than_32_bits_of_threads():
     assert all(bool((out[i:i + 8] == 0).all()) for i in (6, 1 << 23, (1 << 23) - 8, N - 11))
     del y, out
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,S", [(16, 3), (128, 8), (600, 20)])
+def test_more_rows_than_one_pass(E, S, dtype):
+    """40000 rows are two or more for each of a launch's teams of lanes: what a team carries from row to row (sums, a row of
+    LDS with the loss's gradient) is right after the first.  Ids, weights and gradients are those of calls on 4000 rows,
+    which are one a team, bit for bit; the sums are those of fp64."""
+    g = np.random.default_rng([42, E])
+    N, coef, part = 40000, 0.03, 4000
+    l = logits_of(g, N, E, dtype, 0.1)
+    valid = dev_u8((g.random(N) < 0.9).astype(np.uint8))
+    dw, dloss = dev(g.standard_normal((N, S))), torch.full((), 1.5e4, device="cuda")
+    for normalise in (False, True):
+        r = q.route(l, S, normalise=normalise, coef=coef, valid=valid)
+        counts = torch.zeros(E + 1, dtype=torch.int64, device="cuda")
+        d = q.route_backward(l, r, dw, dloss)
+        loss_only = q.route_backward(l, r, None, dloss)
+        for a in range(0, N, part):
+            s = slice(a, a + part)
+            p = q.route(l[s], S, normalise=normalise, coef=coef, valid=valid[s])
+            assert torch.equal(p.ids, r.ids[s]) and torch.equal(p.weights, r.weights[s])
+            counts += p.counts
+            p = p._replace(counts=r.counts)
+            assert torch.equal(q.route_backward(l[s], p, dw[s], dloss), d[s]), a
+            assert torch.equal(q.route_backward(l[s], p, None, dloss), loss_only[s]), a
+        assert torch.equal(counts, r.counts.long()) and bool((loss_only != 0).any())
+        alive = (l > -float("inf")).any(1) & valid.bool()
+        assert int(alive.sum()) == int(r.counts[E])
+        psum = to_host(torch.softmax(l[alive].double(), 1).sum(0))
+        assert np.allclose(host64(r.psum), psum, rtol=P_REL + N * 2.0 ** -24)
+        want = O.balance_loss(to_host(r.counts).astype(np.int64), psum, S, coef)
+        assert np.isclose(host64(r.loss), want, rtol=P_REL + N * 2.0 ** -24 + (E + 8) * 2.0 ** -23)
