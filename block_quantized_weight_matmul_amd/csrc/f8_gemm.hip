@@ -230,12 +230,13 @@ __global__ __launch_bounds__(64 * WM * WN, tile_waves(TM, TN)) void k_f8_gemm(Ge
   // Scales.  The sweep over the groups multiplies a group's sum by its token's and its row block's scale in one step
   // (kRowScale: by one after the other), which is right unless their product leaves fp32's normal range (the sum times the
   // token's may overflow).  A wave that met such scales, from operands with both largest values around 2^-55 or a product
-  // of them above 2^145, makes its outputs anew behind the sweep, the scales in order of size.  That costs the others 0 to
-  // 2% (8192^3 474 -> 477 us).  Asking in every stage made each wait for its scales (480 us); a second sweep by the whole
-  // workgroup had it agree on one (experts +3%).
+  // of them above 2^145, makes its outputs anew behind the sweep, the scales in order of size.  Two blocks of the smallest
+  // scale, 2^-80, which zeros have, do not count: what they add is below 2^-135.  That costs the others 0 to 2% (8192^3
+  // 474 -> 477 us).  Asking at the start of every stage made each wait for its scales (480 us); a second sweep by the
+  // whole workgroup had it agree on one (experts +3%); telling zeros in the sweep took 7% of small tiles.
   F b[CT];
   float sc[CT];
-  uint32_t least = ~0u, most = 0u;  // bits of the smallest and the largest factor; a NaN counts as large
+  uint32_t least = ~0u, most = 0u;  // bits of the smallest and the largest factor; a NaN is large
   auto read_b = [&](int buf) {
     const float* S = Sbase + buf * (kStage / 4);
     const float wscale = kRowScale ? 1.0f : S[TS + wm * (TM / WM) / 128];
@@ -344,7 +345,21 @@ __global__ __launch_bounds__(64 * WM * WN, tile_waves(TM, TN)) void k_f8_gemm(Ge
       most = max(most, __float_as_uint(sc[j]));
     }
   }
-  const bool ordered = __any(kRowScale ? most > 0x71800000u : least < 0x00800000u || most >= 0x7F800000u);  // 2^100; 2^-126, infinity
+  bool ordered = __any(kRowScale ? most > 0x71800000u : least < 0x00800000u || most >= 0x7F800000u);  // 2^100; 2^-126, infinity
+  if (ordered) {  // unless from zeros and NaN alone
+    bool out = false;
+    const float* sa = wsc + std::min((r0 + wm * (TM / WM)) / 128, (M - 1) / 128) * a.G;
+#pragma unroll 1
+    for (int i = lane; i < TN / WN; i += 64) {
+      const float* st = a.xs + t0 + token(wn * (TN / WN) + i);
+#pragma unroll 4
+      for (int64_t g = g0; g < g1; ++g) {
+        const float s = st[g * N], f = kRowScale ? s : s * sa[g];
+        out |= kRowScale ? s > 0x1p100f : (f < 0x1p-126f && fmaxf(s, sa[g]) > kF8MinScale) || f > 0x1.fffffep127f;
+      }
+    }
+    ordered = __any(out);
+  }
   if (ordered) {
     // 32 x 32 outputs at a time, straight from and to global memory, in few registers
 #pragma unroll 1

@@ -369,7 +369,8 @@ qmm_status qmm_quantize(qmm_type type, const float *w, int64_t M, int64_t K, voi
  * Sums are fp32 and y is rounded once to its type.  For an fp32 y a group's 128 products are
  * summed to 24 bits.  For a 16-bit y they run on the 8-bit matrix cores, which cut each of 8
  * products at 2^-13 of the largest one's exponent: about 2e-5 of the result on ordinary
- * data, far below the type's own rounding, and twice as fast.
+ * data, far below the type's own rounding, and twice as fast.  (Two blocks that both have the
+ * smallest scale may be left out of a sum: they add less than 2^-135.)
  * The path and with it the order of the sums depends on the shapes only: the same call
  * gives the same bits.  Conventions are those at the top of this file; in addition every
  * call with nothing to compute (N = 0) returns QMM_OK without looking at its pointers.

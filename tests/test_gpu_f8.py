@@ -806,3 +806,26 @@ def test_a_channel_300_times_larger(N, dtype):
     ref = t.values().double() @ m.dequantize().double().t()
     own, all_ = ((v.double() - ref).pow(2).mean().sqrt() / ref.pow(2).mean().sqrt() for v in (ref.to(y.dtype), y))
     assert float(all_) ** 2 <= float(own) ** 2 * 1.02 + 2.0 ** -26
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,M,K", [(300, 260, 520), (2049, 4090, 300), (60, 700, 4000)])
+def test_blocks_of_zeros_and_of_small_values(N, M, K, dtype):
+    """Zero rows against zero blocks, beside rows and blocks of ordinary, of small and of the smallest values."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x, w = torch.randn((N, K), generator=g, device="cuda"), torch.randn((M, K), generator=g, device="cuda")
+    x[::3] = 0.0
+    x[1::7] *= 2.0 ** -90
+    x[2::11] *= 2.0 ** -62
+    w[:128] = 0.0
+    w[128:256] *= 2.0 ** -90
+    w[256:] *= 2.0 ** -62
+    x, w = x.to(DTYPES[dtype]), w.to(DTYPES[dtype])
+    m, t = q.F8Matrix.quantize(w), q.f8_quantize(x)
+    y = m.gemm(t, out_dtype=DTYPES[dtype])
+    assert bool((y[::3] == 0).all()) and bool((y[:, :128] == 0).all())
+    a, b = t.values(), m.dequantize()
+    ref, size = a.double() @ b.double().t(), a.double().abs() @ b.double().abs().t()
+    groups = -(-K // 128)
+    tol = size * (2.0 ** -10 + 2.0 ** -21) + (ref.abs() + size * 2.0 ** -9) * HALF_STEP[y.dtype] + SMALLEST[y.dtype] + groups * 2.0 ** -135
+    assert bool(((y.double() - ref).abs() <= tol).all())
