@@ -102,10 +102,12 @@ def _logits(logits, valid):
     if valid is not None:
         _tensor(valid, "valid", (torch.uint8, torch.bool), (1,))
         _shape(valid, "valid", (logits.shape[0],))
-    device = _place(None, (logits, "logits"))
+
+
+def _place_logits(logits, valid, *named):
     if valid is not None:
-        _place(device, (valid, "valid"))
-    return device
+        named += ((valid, "valid"),)
+    return _place(None, (logits, "logits"), *named)
 
 
 _route_need = _Seen()  # workspace bytes of the sizes seen
@@ -115,7 +117,8 @@ def route(logits: torch.Tensor, S: int, normalise: bool = True, coef: float = 0.
           valid: Optional[torch.Tensor] = None) -> Routing:
     """Softmax over logits [N, E], the S largest experts of each row and the balance loss.  valid [N] (uint8 or bool):
     0 marks padded rows."""
-    device = _logits(logits, valid)
+    _logits(logits, valid)
+    device = _place_logits(logits, valid)
     N, E = logits.shape
     S = int(S)
     if not 1 <= S <= min(E, 64):
@@ -152,15 +155,15 @@ def route_backward(logits: torch.Tensor, routing: Routing, dweights: Optional[to
                    dloss: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dlogits [N, E] of logits' type from the gradients with respect to the weights ([N, S] fp32) and the loss (fp32, one
     element on the device); either may be None.  ids and counts are int32, as route gives them."""
-    _tensor(logits, "logits", _DT, (2,))
-    _tensor(routing.ids, "ids", (torch.int32,), (2,))
-    _tensor(routing.counts, "counts", (torch.int32,), (1,))
+    ids, _, counts, _, _, normalise, coef, valid = routing
+    _logits(logits, valid)
+    _tensor(ids, "ids", (torch.int32,), (2,))
+    _tensor(counts, "counts", (torch.int32,), (1,))
     N, E = logits.shape
-    S = routing.ids.shape[1]
-    _shape(routing.ids, "ids", (N, S))
-    _shape(routing.counts, "counts", (E + 1,))
-    device = _logits(logits, routing.valid)
-    _place(device, (routing.ids, "ids"), (routing.counts, "counts"))
+    S = ids.shape[1]
+    _shape(ids, "ids", (N, S))
+    _shape(counts, "counts", (E + 1,))
+    device = _place_logits(logits, valid, (ids, "ids"), (counts, "counts"))
     if dweights is not None:
         _tensor(dweights, "dweights", (torch.float32,), (2,))
         _shape(dweights, "dweights", (N, S))
@@ -170,11 +173,10 @@ def route_backward(logits: torch.Tensor, routing: Routing, dweights: Optional[to
         if dloss.numel() != 1:
             raise ValueError("dloss must have one element")
         _place(device, (dloss, "dloss"))
-    valid = routing.valid
     dlogits = torch.empty_like(logits)
     _call(device, lib.qmm_route_backward, logits.data_ptr(), _DT[logits.dtype], N, E, S,
-          valid.data_ptr() if valid is not None else None, int(routing.normalise), routing.coef, routing.ids.data_ptr(),
-          dweights.data_ptr() if dweights is not None else None, routing.counts.data_ptr(),
+          valid.data_ptr() if valid is not None else None, int(normalise), coef, ids.data_ptr(),
+          dweights.data_ptr() if dweights is not None else None, counts.data_ptr(),
           dloss.data_ptr() if dloss is not None else None, dlogits.data_ptr())
     return dlogits
 
