@@ -315,9 +315,11 @@ class F8Matrix:
         return m
 
     def close(self):
-        if getattr(self, "_h", None) is not None and self._h.value is not None:
-            check(lib.qmm_f8_destroy(self._h))
-            self._h = None
+        h, self._h = getattr(self, "_h", None), None
+        if h is not None and h.value is not None:
+            p = ctypes.c_void_p(h.value)
+            h.value = None  # a copy of this object has the same one
+            check(lib.qmm_f8_destroy(p))
 
     def __del__(self):
         try:

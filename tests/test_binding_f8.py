@@ -1,6 +1,7 @@
 """Refusals of the e4m3 and router calls, without a GPU: the binding's checks of metadata (host tensors that pass them
 are refused for their placement, before a C call) and the C ABI's checks before it looks for a device."""
 
+import copy
 import ctypes
 import subprocess
 import sys
@@ -297,3 +298,16 @@ def test_plan_holds_what_is_read():
             per = -(-pairs // 256)
             words += -(-pairs // (-(-per // 1024) * 1024)) * B
         assert L.lib.qmm_route_plan_bytes(pairs, E) == -(-words // 4) * 16, (pairs, E)
+
+
+def test_a_copied_matrix_does_not_free_the_handle_twice(monkeypatch):
+    seen = []
+    monkeypatch.setattr(L.lib, "qmm_f8_destroy", lambda h: seen.append(h.value) or 0)
+    m = matrix(48, 200)
+    m._h = ctypes.c_void_p(4096)
+    twin = copy.copy(m)
+    m.close()
+    twin.close()
+    m.close()
+    assert seen == [4096]
+    assert twin.handle is None or twin.handle.value is None     # refused by the library: no handle
