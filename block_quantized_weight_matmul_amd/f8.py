@@ -318,8 +318,12 @@ class F8Matrix:
         h, self._h = getattr(self, "_h", None), None
         if h is not None and h.value is not None:
             p = ctypes.c_void_p(h.value)
-            h.value = None  # a copy of this object has the same one
+            h.value = None  # whoever else has it sees that it is gone
             check(lib.qmm_f8_destroy(p))
+
+    def __copy__(self):
+        """Another handle of the same codes and scales."""
+        return F8Matrix(self.codes, self.scales, self.M, self.K, self.n_experts)
 
     def __del__(self):
         try:

@@ -829,3 +829,19 @@ def test_blocks_of_zeros_and_of_small_values(N, M, K, dtype):
     groups = -(-K // 128)
     tol = size * (2.0 ** -10 + 2.0 ** -21) + (ref.abs() + size * 2.0 ** -9) * HALF_STEP[y.dtype] + SMALLEST[y.dtype] + groups * 2.0 ** -135
     assert bool(((y.double() - ref).abs() <= tol).all())
+
+
+def test_a_copy_outlives_its_matrix():
+    import copy
+    g = torch.Generator(device="cuda").manual_seed(6)
+    m = q.F8Matrix.quantize(torch.randn((3, 70, 200), generator=g, device="cuda"))
+    x = torch.randn((5, 200), generator=g, device="cuda")
+    ids = torch.randint(0, 3, (5, 2), generator=g, device="cuda", dtype=torch.int32)
+    y = m.linear_id(x, ids)
+    twin, third = copy.copy(m), copy.copy(m)
+    del third
+    assert torch.equal(m.linear_id(x, ids), y)
+    m.close()
+    assert torch.equal(twin.linear_id(x, ids), y) and twin.codes is m.codes
+    with pytest.raises(q.QmmError, match="handle"):
+        m.linear_id(x, ids)

@@ -83,3 +83,9 @@ def test_route_backward_against_differences(normalise):
             h = np.zeros_like(l)
             h[t, e] = 1e-6
             assert np.isclose((value(l + h) - value(l - h)) / 2e-6, got[t, e], atol=1e-8)
+
+
+def test_combine_leaves_slots_of_weight_zero_out():
+    y = np.array([[[1.0, 2.0], [np.nan, np.inf]], [[3.0, 4.0], [5.0, 6.0]]])
+    assert np.array_equal(route.combine(y, [[2.0, 0.0], [1.0, -1.0]]), [[2.0, 4.0], [-2.0, -2.0]])
+    assert np.isnan(route.combine(y)[0, 0]) and np.isnan(route.combine(y, [[1.0, np.nan], [0.0, 0.0]])[0]).all()
