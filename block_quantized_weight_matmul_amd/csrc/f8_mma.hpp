@@ -6,10 +6,11 @@
 // vector units.  Which cores depends on the output's type:
 //   16-bit outputs  v_mfma_f32_16x16x128_f8f6f4, whose depth is the group.  It takes the codes as they are, but it
 //                   aligns the products of every 8 values to 13 bits below their largest exponent (measured: a product
-//                   2^-14 of its octet's largest is lost), an error of 1.5e-5 of the result on normal data and 6e-5 on
-//                   data of a wide range: 1/16 of half a step of fp16, 1/130 of bf16's.
+//                   2^-14 of its octet's largest is lost).  Of the outputs' root mean square that is 1.4e-5 on normal
+//                   data and 6e-5 to 7e-5 with one channel 300 times larger, beside 2.1e-4 for an output's rounding to
+//                   fp16 and 1.7e-3 to bf16 (512 and 16 tokens of 1024 x 2560).
 //   fp32 outputs    v_mfma_f32_16x16x32_f16 on the codes converted to fp16, which holds every e4m3 value: the same sums
-//                   kept to 24 bits (1e-8), at half the rate and two conversions a register.
+//                   kept to 24 bits (1e-7), at half the rate and two conversions a register.
 // Weight rows are the A rows of the instruction and tokens its columns, so that a lane holds 4 consecutive outputs of one
 // token and its token scale is one register.  The 128 values of a group may reach the instruction in any order as long as
 // both operands use the same one: lane (row l & 15, quarter l >> 4) takes bytes 32 * quarter .. + 31 of its row.

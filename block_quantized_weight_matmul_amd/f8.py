@@ -5,7 +5,7 @@
     y = m.linear_id(x, ids)            # expert-indexed: ids [N, S]
     t = f8_quantize(x); y = m.gemm(t)  # one quantization for several matrices
 
-Training (no autograd: every gradient is a call):
+Training (no autograd: results carry no gradient history whatever their inputs require, every gradient is a call):
 
     xq, xt = f8_quantize_pair(x)                  # along K, and along the tokens
     gq, gt = f8_quantize_pair(dy)

@@ -4,7 +4,7 @@
     y = experts.linear_id(x, r.ids)                      # F8Matrix, or QMatrix.gemm_id
     out = route_combine(y, r.weights)
 
-Backward, every gradient a call:
+Backward (no autograd: results carry no gradient history whatever their inputs require, every gradient is a call):
 
     dy, dweights = route_combine_backward(y, r.weights, dout)
     dlogits = route_backward(logits, r, dweights, dloss)

@@ -87,7 +87,7 @@ def weight_values(codes, scales, K):
 
 def product_bound(xv, wv, f8_cores=False):
     """|y - exact| allowed for an fp32 product over values xv [N, K], wv [M, K], before y's own rounding: 128 terms of a
-    group summed with a step's error each (2^-23, rounded or cut), a rounding of the product of the scales, one per
+    group summed with a step's error each (2^-23, rounded or cut), a rounding of the product with a scale (or of the scales'), one per
     group's fma and one per partial sum that is joined (at most 16).  f8_cores: the matrix cores also drop what is below
     2^-13 of the largest of 8 products' exponents, at most 8 * 2^-13 of that largest product."""
     groups = padded(xv.shape[1]) // BLOCK
