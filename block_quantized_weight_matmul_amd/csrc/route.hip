@@ -655,7 +655,8 @@ __device__ void plan_scatter(const int32_t* ids, int64_t p0, int64_t p1, int E, 
 }
 
 // Up to kPlanOneLaunch pairs: every workgroup counts all of them, those before its own kPlanThreads apart.  128 experts:
-// 9.6 us for 16384 pairs and 11.6 for 32768, where three launches take 19 and 19; at 131072 it would be 23 against 21.
+// 8.6 us for 16384 pairs and 10.5 for 32768, where three launches took 19 and 19; at 131072, where these take 18.6, it
+// took 2 us more than they.
 __global__ __launch_bounds__(kPlanThreads) void k_plan_small(const int32_t* ids, PlanDesc d, int32_t* plan) {
   __shared__ PlanShared sh;
   const int E = static_cast<int>(d.E), B = E + 2, pairs = static_cast<int>(d.pairs);
