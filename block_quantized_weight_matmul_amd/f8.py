@@ -12,8 +12,9 @@ Training (no autograd: results carry no gradient history whatever their inputs r
     dx = m.transposed().gemm(gq)
     dw = f8_wgrad(gt, xt)
 
-As everywhere in this package the functions check tensor metadata, allocate outputs and workspaces with torch and
-pass pointers; the current stream of the tensors' device is used, whichever device is current.
+Where a call takes `out`, that tensor's type is the output's.  As everywhere in this package the functions check tensor
+metadata, allocate outputs and workspaces with torch and pass pointers; the current stream of the tensors' device is used,
+whichever device is current.
 """
 
 import ctypes
