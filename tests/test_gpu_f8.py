@@ -845,3 +845,17 @@ def test_a_copy_outlives_its_matrix():
     assert torch.equal(twin.linear_id(x, ids), y) and twin.codes is m.codes
     with pytest.raises(q.QmmError, match="handle"):
         m.linear_id(x, ids)
+
+
+@pytest.mark.parametrize("swap", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,M,K", [(1, 130, 300), (20, 300, 700), (130, 257, 300), (2500, 700, 130), (4090, 2500, 700), (4000, 4090, 500), (100, 300, 16300)])
+def test_one_operand_past_2_100(N, M, K, dtype, swap):
+    """Values near 2^114 against values near 2^-40, of one sign: a group's sum times the larger scale alone overflows."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    a, b = (((torch.rand((rows, K), generator=g, device="cuda") / 4 + 0.75) * s).to(DTYPES[dtype])
+            for rows, s in ((N, 2.0 ** (-40 if swap else 114)), (M, 2.0 ** (114 if swap else -40))))
+    m, t = q.F8Matrix.quantize(b), q.f8_quantize(a)
+    device_check(m.gemm(t, out_dtype=DTYPES[dtype]), t.values(), m.dequantize(), "product")
+    gt, xt = q.f8_quantize_t(a.t().contiguous()), q.f8_quantize_t(b.t().contiguous())
+    device_check(q.f8_wgrad(gt, xt, dtype=DTYPES[dtype]), gt.values(), xt.values(), "weight gradient")
