@@ -14,13 +14,15 @@ check tensor metadata, allocate outputs with torch and marshal pointers.
     w = qm.dequantize()          # exact fp32 weights (or fp16 staging values)
 
 8-bit float weights and tokens with a scale per block of 128 are in ``f8`` (F8Matrix), the
-expert router that makes the expert-indexed calls' ids in ``routing``.
+expert router that makes the expert-indexed calls' ids in ``routing``; what a decoder layer does between
+its projections (head norms and rotation, the paged cache, attention) in ``attention``.
 """
 
 import ctypes
 
 import torch
 
+from .attention import KVCache, attend_prompt, head_norm_rope  # noqa: F401
 from .f8 import F8Matrix, F8Tokens, f8_quantize, f8_quantize_pair, f8_quantize_t, f8_wgrad  # noqa: F401
 from .routing import (  # noqa: F401
     RoutePlan, Routing, balance_loss, route, route_backward, route_combine, route_combine_backward, route_plan)
@@ -35,6 +37,7 @@ __all__ = [
     "F8Matrix", "F8Tokens", "f8_quantize", "f8_quantize_pair", "f8_quantize_t", "f8_wgrad",
     "Routing", "RoutePlan", "route", "route_plan", "balance_loss", "route_backward", "route_combine",
     "route_combine_backward",
+    "KVCache", "head_norm_rope", "attend_prompt",
 ]
 
 _XT = {torch.float32: DTYPES["f32"], torch.float16: DTYPES["f16"]}

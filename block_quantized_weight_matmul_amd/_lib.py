@@ -16,7 +16,7 @@ STATUS = {
 }
 TYPES = {"q4_0": 0, "q8_0": 1, "q4_k": 2, "q6_k": 3, "a4g64": 4,
          "q4_1": 5, "q5_0": 6, "q5_1": 7, "q2_k": 8, "q3_k": 9, "q5_k": 10}
-DTYPES = {"f32": 0, "f16": 1, "bf16": 2}  # bf16: the qmm_f8_* and qmm_route* calls only
+DTYPES = {"f32": 0, "f16": 1, "bf16": 2}  # bf16: not the block formats' calls
 TILES = {"auto": 0, 32: 32, 64: 64}
 NOALLOC_SCRATCH_BYTES = 64 << 20  # QMM_NOALLOC_SCRATCH_BYTES of include/qmm.h
 
@@ -74,6 +74,18 @@ def _load():
         "qmm_route_backward": (c_int, [vp, c_int, i64, i64, i64, vp, c_int, f32, vp, vp, vp, vp, vp, vp]),
         "qmm_route_combine": (c_int, [vp, c_int, vp, c_int, i64, i64, i64, vp, vp]),
         "qmm_route_combine_backward": (c_int, [vp, c_int, vp, c_int, i64, i64, i64, vp, vp, vp, vp]),
+        "qmm_head_norm_rope": (c_int, [vp, i64, i64, vp, i64, i64, c_int, i64, i64, i64, i64, vp, vp, c_int, f32, vp, vp, i64,
+                                       c_int, vp, vp, c_int, vp]),
+        "qmm_cache_create": (c_int, [ctypes.POINTER(vp), vp, vp, vp, vp, c_int, i64, i64, i64, i64]),
+        "qmm_cache_destroy": (c_int, [vp]),
+        "qmm_cache_write": (c_int, [vp, vp, i64, i64, vp, i64, i64, c_int, i64, vp, vp]),
+        "qmm_cache_norm_rope_write": (c_int, [vp, vp, i64, i64, vp, i64, i64, vp, i64, i64, c_int, i64, i64, vp, vp, c_int, f32,
+                                              vp, vp, i64, c_int, vp, vp, c_int, vp]),
+        "qmm_cache_read": (c_int, [vp, vp, i64, i64, vp, i64, vp, vp, c_int, vp]),
+        "qmm_cache_attend_workspace_bytes": (size, [vp, i64, i64, i64]),
+        "qmm_cache_attend": (c_int, [vp, vp, c_int, i64, i64, i64, i64, vp, i64, vp, i64, f32, vp, vp, size, vp]),
+        "qmm_attend_prompt": (c_int, [vp, i64, i64, vp, i64, i64, vp, i64, i64, c_int, vp, vp, i64, i64, i64, i64, i64, i64,
+                                      c_int, f32, vp, vp]),
         "qmm_tile_for_tokens": (c_int, [i64]),
         "qmm_row_bytes": (ctypes.c_size_t, [c_int, i64]),
         "qmm_block_weights": (c_int, [c_int]),

@@ -15,37 +15,19 @@ struct qmm_f8_matrix {
 namespace {
 
 using qmm::aligned;
+using qmm::check_dtype;
+using qmm::check_ptr;
+using qmm::check_range;
+using qmm::check_ws;
+using qmm::dtype_ok;
 using qmm::fail;
 using qmm::hip_fail;
 using qmm::ok;
 using qmm::f8_pad;
+using qmm::ll;
+using qmm::size_of;
+using qmm::stream_of;
 
-typedef long long ll;
-
-hipStream_t stream_of(qmm_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
-bool dtype_ok(int t) { return t == QMM_F32 || t == QMM_F16 || t == QMM_BF16; }
-int64_t size_of(int t) { return t == QMM_F32 ? 4 : 2; }
-
-qmm_status check_dtype(int t, const char* what) {
-  return dtype_ok(t) ? QMM_OK : fail(QMM_E_TYPE, "unknown %s dtype %d", what, t);
-}
-qmm_status check_ptr(const void* p, uintptr_t align, const char* what) {
-  if (!p) return fail(QMM_E_ARG, "%s is NULL", what);
-  if (!aligned(p, align)) return fail(QMM_E_ALIGN, "%s must be %d-byte aligned", what, static_cast<int>(align));
-  return QMM_OK;
-}
-qmm_status check_range(int64_t v, int64_t lo, int64_t hi, const char* what) {
-  return v >= lo && v <= hi ? QMM_OK
-                            : fail(QMM_E_SHAPE, "%s=%lld outside [%lld, %lld]", what, static_cast<ll>(v),
-                                   static_cast<ll>(lo), static_cast<ll>(hi));
-}
-qmm_status check_ws(const void* ws, size_t have, size_t need, const char* what) {
-  if (need == 0) return QMM_OK;
-  if (!ws) return fail(QMM_E_ARG, "%s is NULL; this call needs %zu bytes", what, need);
-  if (have < need) return fail(QMM_E_ARG, "%s holds %zu bytes; this call needs %zu", what, have, need);
-  if (!aligned(ws, 16)) return fail(QMM_E_ALIGN, "%s must be 16-byte aligned", what);
-  return QMM_OK;
-}
 qmm_status check_device(const qmm_f8_matrix* h) {
   int dev = -1;
   const hipError_t e = hipGetDevice(&dev);
@@ -53,12 +35,6 @@ qmm_status check_device(const qmm_f8_matrix* h) {
   if (dev != h->device) return fail(QMM_E_DEVICE, "current device %d is not the handle's device %d", dev, h->device);
   return QMM_OK;
 }
-
-#define QMM_TRY(expr)                     \
-  do {                                    \
-    const qmm_status s_ = (expr);         \
-    if (s_ != QMM_OK) return s_;          \
-  } while (0)
 
 constexpr int64_t kMaxK = qmm::kF8MaxK - qmm::kF8Block;
 constexpr int64_t kMaxWgradTokens = int64_t(1) << 23;

@@ -1,0 +1,377 @@
+// heads.hip -- norms and rotation of query and key heads, and the paged cache: written (quantized where its type is
+// e4m3) and read back.
+#include "attn.hpp"
+
+namespace qmm {
+
+namespace {
+
+template <int DT> struct Quad { typedef typename Elem<DT>::T V __attribute__((ext_vector_type(4))); };
+
+// four elements as they are (aligned to the elements only)
+template <int DT>
+__device__ __forceinline__ typename Quad<DT>::V load4(const typename Elem<DT>::T* p) {
+  typedef typename Quad<DT>::V Vu __attribute__((aligned(sizeof(typename Elem<DT>::T))));
+  return *reinterpret_cast<const Vu*>(p);
+}
+template <int DT>
+__device__ __forceinline__ void store4(typename Elem<DT>::T* p, const float* v) {
+  typedef typename Quad<DT>::V V;
+  typedef V Vu __attribute__((aligned(sizeof(typename Elem<DT>::T))));
+  V w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = static_cast<typename Elem<DT>::T>(v[i]);
+  *reinterpret_cast<Vu*>(p) = w;
+}
+
+__device__ __forceinline__ float weight_at(const void* w, int wt, int i) {
+  if (wt == DT_F32) return static_cast<const float*>(w)[i];
+  if (wt == DT_F16) return static_cast<float>(static_cast<const _Float16*>(w)[i]);
+  return static_cast<float>(static_cast<const __bf16*>(w)[i]);
+}
+
+// sine and cosine of an angle of any size, to fp32's rounding: the angle less a multiple of pi / 2 (a two-part constant;
+// fma keeps the first difference exact), then the Taylor series on [-pi/4, pi/4], whose remainder is below 3e-14
+__device__ __forceinline__ void turn(double angle, float& sine, float& cosine) {
+  const double n = __builtin_rint(angle * 0.63661977236758134308);
+  double r = fma(-n, 0x1.921fb54442d18p+0, angle);
+  r = fma(-n, 0x1.1a62633145c07p-54, r);
+  const double x = r * r;
+  double s = 1.0 / 6227020800.0;
+  s = fma(s, x, -1.0 / 39916800.0);
+  s = fma(s, x, 1.0 / 362880.0);
+  s = fma(s, x, -1.0 / 5040.0);
+  s = fma(s, x, 1.0 / 120.0);
+  s = fma(s, x, -1.0 / 6.0);
+  s = fma(s * x, r, r);
+  double c = -1.0 / 87178291200.0;
+  c = fma(c, x, 1.0 / 479001600.0);
+  c = fma(c, x, -1.0 / 3628800.0);
+  c = fma(c, x, 1.0 / 40320.0);
+  c = fma(c, x, -1.0 / 720.0);
+  c = fma(c, x, 1.0 / 24.0);
+  c = fma(c, x, -0.5);
+  c = fma(c, x, 1.0);
+  const int quarter = static_cast<int>(static_cast<int64_t>(n)) & 3;
+  const float fs = static_cast<float>(s), fc = static_cast<float>(c);
+  const float a = quarter & 1 ? fc : fs, b = quarter & 1 ? fs : fc;
+  sine = quarter & 2 ? -a : a;
+  cosine = (quarter + 1) & 2 ? -b : b;
+}
+
+// A head's rows in a cache: where slot `slot` of head h lies.
+struct SlotRow {
+  int64_t row;  // in rows of D
+  bool there;
+};
+__device__ __forceinline__ SlotRow slot_row(const CacheDesc& c, int32_t slot, int h) {
+  const int64_t page = slot >> c.shift, at = slot & ((1 << c.shift) - 1);
+  return {((page * c.heads + h) << c.shift) + at, slot >= 0 && page < c.pages};
+}
+
+// Eight values of a lane of a team that holds a head, to row `row` of a cache of type CT: columns a .. a + 3 and b .. b +
+// 3.  DT: the type the values were rounded to, which decides the form of the quotient.
+template <int CT, int DT, int L>
+__device__ __forceinline__ void to_cache(const float* v, uint8_t* data, float* scales, const SlotRow& r, int D, int a,
+                                         int b, bool mine) {
+  if constexpr (CT == DT_E4M3) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+    const float s = f8_scale(team_max<L>(mine ? m : 0u)), rs = f8_inverse(s);
+    float q[8], ss[8], rr[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) { ss[i] = s; rr[i] = rs; }
+    f8_quotients<DT>(v, ss, rr, q);
+    if (r.there && mine) {
+      uint8_t* d = data + r.row * D;
+      *reinterpret_cast<uint32_t*>(d + a) = f8_pack4(q[0], q[1], q[2], q[3]);
+      *reinterpret_cast<uint32_t*>(d + b) = f8_pack4(q[4], q[5], q[6], q[7]);
+      if (a == 0) scales[r.row] = s;
+    }
+  } else {
+    if (r.there && mine) {
+      typename Elem<CT>::T* d = reinterpret_cast<typename Elem<CT>::T*>(data) + r.row * D;
+      store4<CT>(d + a, v);
+      store4<CT>(d + b, v + 4);
+    }
+  }
+}
+
+// Norms and rotation.  A team of L lanes takes a token and every parts-th share of its heads.  A lane holds eight columns
+// of a head, the two members of each of its four pairs among them (halves of the rotated part, or neighbours), so that a
+// rotation needs no other lane, and the four angles serve every head of the token.
+//
+//   y = x * w / sqrt(mean(x^2) + eps);   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq
+//
+// Sums in fp32, the angle and its reduction in 64 bits (a position of 2^20 loses all of a fast pair's angle in 32), one
+// rounding at the end.  CACHE: keys and values go to their slots; a key is rounded to the queries' type first, so that the
+// call leaves the bits of the two calls it stands for.
+template <int XT, int QT, int CT, bool CACHE, int L>
+__global__ __launch_bounds__(256) void k_heads(HeadsArgs a) {
+  constexpr int kTeams = 256 / L, kAhead = 4;
+  typedef typename Elem<XT>::T X;
+  const int lane = threadIdx.x % L;
+  const int64_t unit = block_index() * kTeams + threadIdx.x / L;
+  if (unit >= a.T * a.parts) return;  // whole teams: no lane of this one is asked for
+  const int part = static_cast<int>(unit / a.T);
+  const int64_t t = unit - part * a.T;
+  const int heads = a.Hq + a.H + (CACHE ? a.H : 0), per = (heads + a.parts - 1) / a.parts;
+  const int h0 = part * per, h1 = min(heads, h0 + per);
+  const int D = a.D, R = a.R;
+  const bool mine = lane * 8 < D, turned = lane * 8 < R;
+  const int pair0 = lane * 4;
+  const bool halves = !a.interleaved;
+  const int ca = turned && halves ? pair0 : lane * 8;  // the eight columns: ca .. ca + 3, cb .. cb + 3
+  const int cb = turned && halves ? R / 2 + pair0 : lane * 8 + 4;
+
+  int32_t slot = -1;
+  if constexpr (CACHE) slot = a.slots[t];
+
+  float sine[4], cosine[4];
+  if (a.inv_freq) {
+    const double p = a.positions[t];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turn(p * static_cast<double>(a.inv_freq[turned ? pair0 + i : 0]), sine[i], cosine[i]);
+  }
+  float qw[8], kw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = mine ? (i < 4 ? ca : cb - 4) + i : 0;
+    qw[i] = a.qw ? weight_at(a.qw, a.wt, c) : 1.0f;
+    kw[i] = a.kw ? weight_at(a.kw, a.wt, c) : 1.0f;
+  }
+
+  auto row = [&](int h) -> const X* {
+    if (h < a.Hq) return static_cast<const X*>(a.q.p) + t * a.q.st + h * a.q.sh;
+    if (h < a.Hq + a.H) return static_cast<const X*>(a.k.p) + t * a.k.st + (h - a.Hq) * a.k.sh;
+    return static_cast<const X*>(a.v.p) + t * a.v.st + (h - a.Hq - a.H) * a.v.sh;
+  };
+  typedef typename Quad<XT>::V V4;
+  for (int h = h0; h < h1; h += kAhead) {
+    V4 lo[kAhead], hi[kAhead];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const X* p = row(min(h + n, h1 - 1));
+      lo[n] = load4<XT>(p + (mine ? ca : 0));
+      hi[n] = load4<XT>(p + (mine ? cb : 0));
+    }
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const int g = h + n;
+      if (g >= h1) break;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = static_cast<float>(lo[n][i]);
+        v[4 + i] = static_cast<float>(hi[n][i]);
+      }
+      if (CACHE && g >= a.Hq + a.H) {
+        const SlotRow r = slot_row(a.cache, slot, g - a.Hq - a.H);
+        to_cache<CT, XT, L>(v, a.cache.v, a.cache.vs, r, D, ca, cb, mine);
+        continue;
+      }
+      const bool query = g < a.Hq;
+      if (query ? a.qw != nullptr : a.kw != nullptr) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(v[i], v[i], sum);
+        const float m = team_sum<L>(mine ? sum : 0.0f) / static_cast<float>(D) + a.eps;
+        const float r = 1.0f / sqrtf(m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * r * (query ? qw[i] : kw[i]);
+      }
+      if (a.inv_freq && turned) {
+        if (halves) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = v[i], y = v[4 + i];
+            v[i] = fmaf(x, cosine[i], -(y * sine[i]));
+            v[4 + i] = fmaf(y, cosine[i], x * sine[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = v[2 * i], y = v[2 * i + 1];
+            v[2 * i] = fmaf(x, cosine[i], -(y * sine[i]));
+            v[2 * i + 1] = fmaf(y, cosine[i], x * sine[i]);
+          }
+        }
+      }
+      if (query || !CACHE) {
+        typename Elem<QT>::T* o = static_cast<typename Elem<QT>::T*>(query ? a.qo : a.ko);
+        o += query ? (t * a.Hq + g) * D : (t * a.H + (g - a.Hq)) * D;
+        if (mine) {
+          store4<QT>(o + ca, v);
+          store4<QT>(o + cb, v + 4);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(static_cast<typename Elem<QT>::T>(v[i]));
+        to_cache<CT, QT, L>(v, a.cache.k, a.cache.ks, slot_row(a.cache, slot, g - a.Hq), D, ca, cb, mine);
+      }
+    }
+  }
+}
+
+// Keys and values of T tokens to their slots: a team of L lanes takes a token's head, of both.
+template <int XT, int CT, int L>
+__global__ __launch_bounds__(256) void k_cache_write(CacheDesc c, HeadRows k, HeadRows v, int64_t T, const int32_t* slots) {
+  typedef typename Elem<XT>::T X;
+  const int lane = threadIdx.x % L, D = c.D;
+  const int64_t unit = block_index() * (256 / L) + threadIdx.x / L;
+  if (unit >= T * c.heads) return;
+  const int64_t t = unit / c.heads;
+  const int h = static_cast<int>(unit - t * c.heads);
+  const bool mine = lane * 8 < D;
+  const int at = mine ? lane * 8 : 0;
+  float kv[8], vv[8];
+  load8<XT>(static_cast<const X*>(k.p) + t * k.st + h * k.sh + at, kv);
+  load8<XT>(static_cast<const X*>(v.p) + t * v.st + h * v.sh + at, vv);
+  const SlotRow r = slot_row(c, slots[t], h);
+  to_cache<CT, XT, L>(kv, c.k, c.ks, r, D, at, at + 4, mine);
+  to_cache<CT, XT, L>(vv, c.v, c.vs, r, D, at, at + 4, mine);
+}
+
+// Packed rows from the cache: a team of L lanes takes a row and a share of its heads.
+template <int CT, int OT, int L>
+__global__ __launch_bounds__(256) void k_cache_read(CacheDesc c, const int32_t* table, int64_t B, int64_t W,
+                                                    const int32_t* starts, int64_t total, void* ko, void* vo) {
+  constexpr int kTeams = 256 / L;
+  typedef typename Elem<OT>::T O;
+  const int lane = threadIdx.x % L, D = c.D, H = c.heads;
+  const int64_t first = block_index() * kTeams, row = first + threadIdx.x / L;
+  int64_t b = find_sequence(starts, B, first);
+  if (row >= total) return;
+  while (b < B && starts[b + 1] <= row) ++b;  // the workgroup's rows may end a sequence
+  if (b >= B) return;                         // behind the last sequence
+  const int64_t t = row - starts[b];
+  if (t < 0) return;                          // before the first
+  const int64_t column = t >> c.shift;
+  const int64_t page = column < W ? table[b * W + column] : -1;
+  const bool there = page >= 0 && page < c.pages;
+  const int64_t base = ((there ? page * H : 0) << c.shift) + (t & ((1 << c.shift) - 1));
+  const bool mine = lane * 8 < D;
+  const int at = mine ? lane * 8 : 0;
+  const int h0 = blockIdx.z, step = gridDim.z;
+  constexpr int kAhead = 4;
+  for (int h = h0; h < H; h += kAhead * step) {
+    float kx[kAhead][8], vx[kAhead][8];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const int64_t r = base + (static_cast<int64_t>(min(h + n * step, H - 1)) << c.shift);
+      if constexpr (CT == DT_E4M3) {
+        const uint2 kc = *reinterpret_cast<const uint2*>(c.k + r * D + at), vc = *reinterpret_cast<const uint2*>(c.v + r * D + at);
+        const float ks = c.ks[r], vs = c.vs[r];
+        const uint32_t kw[2] = {kc.x, kc.y}, vw[2] = {vc.x, vc.y};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const auto k0 = __builtin_amdgcn_cvt_pk_f32_fp8(kw[i], false), k1 = __builtin_amdgcn_cvt_pk_f32_fp8(kw[i], true);
+          const auto v0 = __builtin_amdgcn_cvt_pk_f32_fp8(vw[i], false), v1 = __builtin_amdgcn_cvt_pk_f32_fp8(vw[i], true);
+          kx[n][4 * i] = k0[0] * ks, kx[n][4 * i + 1] = k0[1] * ks, kx[n][4 * i + 2] = k1[0] * ks, kx[n][4 * i + 3] = k1[1] * ks;
+          vx[n][4 * i] = v0[0] * vs, vx[n][4 * i + 1] = v0[1] * vs, vx[n][4 * i + 2] = v1[0] * vs, vx[n][4 * i + 3] = v1[1] * vs;
+        }
+      } else {
+        load8<CT>(reinterpret_cast<const typename Elem<CT>::T*>(c.k) + r * D + at, kx[n]);
+        load8<CT>(reinterpret_cast<const typename Elem<CT>::T*>(c.v) + r * D + at, vx[n]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      if (h + n * step >= H || !mine) break;
+      if (!there) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) kx[n][i] = vx[n][i] = __uint_as_float(0x7FC00000u);
+      }
+      const int64_t o = (row * H + h + n * step) * D + at;
+      store4<OT>(static_cast<O*>(ko) + o, kx[n]);
+      store4<OT>(static_cast<O*>(ko) + o + 4, kx[n] + 4);
+      store4<OT>(static_cast<O*>(vo) + o, vx[n]);
+      store4<OT>(static_cast<O*>(vo) + o + 4, vx[n] + 4);
+    }
+  }
+}
+
+template <int DT> struct Int { static constexpr int value = DT; };
+
+// f(Int<DT>) for one of the three element types
+template <typename F>
+hipError_t with_type(int dt, F f) {
+  if (dt == DT_F32) return f(Int<DT_F32>{});
+  if (dt == DT_F16) return f(Int<DT_F16>{});
+  return f(Int<DT_BF16>{});
+}
+// f(Int<lanes>) for the team that holds D columns, eight a lane
+template <typename F>
+hipError_t with_team(int D, F f) {
+  if (D <= 64) return f(Int<8>{});
+  if (D <= 128) return f(Int<16>{});
+  return f(Int<32>{});
+}
+
+}  // namespace
+
+hipError_t launch_heads(HeadsArgs a, int xt, int qt, hipStream_t s) {
+  const bool cache = a.slots != nullptr;
+  const int heads = a.Hq + a.H + (cache ? a.H : 0);
+  return with_team(a.D, [&](auto l) {
+    constexpr int L = decltype(l)::value;
+    // Long calls: a team takes all heads of its token, so that the angles are made once.  Few tokens: the heads are
+    // divided until the teams fill a wave of every SIMD (4 a compute unit), at least four heads each, one round of loads.
+    const int64_t want = 256 * 4 * (64 / L);
+    int64_t parts = a.T >= want ? 1 : (want + a.T - 1) / a.T;
+    const int64_t most = (heads + 3) / 4;
+    a.parts = static_cast<int>(parts < most ? parts : most);
+    const int64_t blocks = (a.T * a.parts + 256 / L - 1) / (256 / L);
+    return with_type(xt, [&](auto x) {
+      constexpr int XT = decltype(x)::value;
+      auto go = [&](auto q, auto c, auto w) {
+        hipLaunchKernelGGL((k_heads<XT, decltype(q)::value, decltype(c)::value, decltype(w)::value != 0, L>),
+                           long_grid(blocks), dim3(256), 0, s, a);
+        return hipGetLastError();
+      };
+      if (!cache) return with_type(qt, [&](auto q) { return go(q, q, Int<0>{}); });
+      if (a.cache.type == DT_E4M3) return with_type(qt, [&](auto q) { return go(q, Int<DT_E4M3>{}, Int<1>{}); });
+      return a.cache.type == DT_F16 ? go(Int<DT_F16>{}, Int<DT_F16>{}, Int<1>{}) : go(Int<DT_BF16>{}, Int<DT_BF16>{}, Int<1>{});
+    });
+  });
+}
+
+hipError_t launch_cache_write(const CacheDesc& c, const HeadRows& k, const HeadRows& v, int xt, int64_t T,
+                              const int32_t* slots, hipStream_t s) {
+  return with_team(c.D, [&](auto l) {
+    constexpr int L = decltype(l)::value;
+    const int64_t blocks = (T * c.heads + 256 / L - 1) / (256 / L);
+    return with_type(xt, [&](auto x) {
+      constexpr int XT = decltype(x)::value;
+      auto go = [&](auto ct) {
+        hipLaunchKernelGGL((k_cache_write<XT, decltype(ct)::value, L>), long_grid(blocks), dim3(256), 0, s, c, k, v, T, slots);
+        return hipGetLastError();
+      };
+      if (c.type == DT_E4M3) return go(Int<DT_E4M3>{});
+      return c.type == DT_F16 ? go(Int<DT_F16>{}) : go(Int<DT_BF16>{});
+    });
+  });
+}
+
+hipError_t launch_cache_read(const CacheDesc& c, const int32_t* table, int64_t B, int64_t W, const int32_t* starts,
+                             int64_t total, void* k, void* v, int ot, hipStream_t s) {
+  return with_team(c.D, [&](auto l) {
+    constexpr int L = decltype(l)::value;
+    const int64_t blocks = (total + 256 / L - 1) / (256 / L);
+    const int64_t quads = (c.heads + 3) / 4;
+    const int64_t share = blocks >= 4 * c.cus ? 1 : quads;  // few rows: four heads a team
+    return with_type(ot, [&](auto o) {
+      constexpr int OT = decltype(o)::value;
+      auto go = [&](auto ct) {
+        hipLaunchKernelGGL((k_cache_read<decltype(ct)::value, OT, L>), long_grid(blocks, 256, share), dim3(256), 0, s, c, table,
+                           B, W, starts, total, k, v);
+        return hipGetLastError();
+      };
+      if (c.type == DT_E4M3) return go(Int<DT_E4M3>{});
+      return c.type == DT_F16 ? go(Int<DT_F16>{}) : go(Int<DT_BF16>{});
+    });
+  });
+}
+
+}  // namespace qmm

@@ -1,0 +1,352 @@
+// prompt.hip -- attention of whole prompts: packed sequences, grouped heads, causal.
+//
+//   out[i, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q_i.k_j - max),  j <= i + (m - n)  (m keys, n queries)
+//
+// Bound by the matrix cores.  A workgroup takes 128 queries of one head and sweeps the keys they may see in tiles of 64:
+// keys and values go straight into LDS, two tiles deep, while the waves, 32 queries each, work on the tile before.
+#include "attn.hpp"
+
+namespace qmm {
+
+namespace {
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int kQueries = 128, kKeys = 64, kWaves = 4;
+
+template <int QT> struct Half8 { typedef typename Elem<QT>::T V __attribute__((ext_vector_type(8))); };
+template <int QT> using H8 = typename Half8<QT>::V;
+
+__device__ __forceinline__ f32x16 mma(H8<DT_F16> a, H8<DT_F16> b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(H8<DT_BF16> a, H8<DT_BF16> b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), 0x00020000);
+}
+// 16 bytes a lane straight into LDS: lane i's at dst + 16 i (dst: the wave's base)
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, voff, 0, 0, 0);
+}
+
+// the larger (the sum) of a value and the one of the lane 32 further
+__device__ __forceinline__ float both_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float both_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// A tile of 64 rows of DP columns in LDS, in 16-byte pieces xored with a function of the row: 16 lanes that read one piece
+// of 16 rows (keys), and 32 that read four neighbouring pieces of four rows (values), use every bank once.
+template <int DP>
+struct Tile {
+  static constexpr int kRow = DP * 2, kPieces = kRow / 16;
+  __device__ static __forceinline__ int key(int row, int piece) { return piece ^ (DP >= 128 ? row & 15 : row >> 1 & 7); }
+  __device__ static __forceinline__ int value(int row, int piece) {
+    return piece ^ (DP >= 128 ? 4 * (row & 3) : 4 * (row >> 1 & 1));
+  }
+};
+
+// The tile of queries of a workgroup: the i-th of all sequences' tiles.
+struct Work {
+  int64_t q0, n, k0, m;  // first row and number of the sequence's queries, of its keys
+  int64_t first;         // first query of the tile
+  bool some;
+};
+// Starts are taken as they come, kept within [0, total]: no row outside the tensors is touched whatever they hold.
+__device__ __forceinline__ int64_t start_at(const int32_t* s, int64_t i, int64_t total) {
+  const int64_t v = s[i];
+  return v < 0 ? 0 : v > total ? total : v;
+}
+__device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index) {
+  Work w{};
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;
+  for (int64_t b0 = 0; b0 < a.B; b0 += 64) {
+    const int64_t b = b0 + lane;
+    const int64_t lo = b < a.B ? start_at(a.q_starts, b, a.Tq) : 0, hi = b < a.B ? start_at(a.q_starts, b + 1, a.Tq) : 0;
+    const int tiles = hi > lo ? static_cast<int>((hi - lo + kQueries - 1) / kQueries) : 0;
+    int upto = tiles;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) {
+      const int y = __shfl_up(upto, x);
+      if (lane >= x) upto += y;
+    }
+    const uint64_t past = __ballot(before + upto > index);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      const int64_t seq = b0 + at;
+      const int64_t mine = index - before - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(tiles, at));
+      w.q0 = start_at(a.q_starts, seq, a.Tq);
+      w.n = start_at(a.q_starts, seq + 1, a.Tq) - w.q0;
+      w.k0 = start_at(a.k_starts, seq, a.Tk);
+      w.m = start_at(a.k_starts, seq + 1, a.Tk) - w.k0;
+      if (w.m < 0) w.m = 0;
+      // the last tile, which sees the most keys, first
+      const int64_t all = (w.n + kQueries - 1) / kQueries;
+      w.first = (all - 1 - mine) * kQueries;
+      w.some = true;
+      return w;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return w;
+}
+
+// One row at a time, with nothing of a key that the row does not see: for a workgroup that met an infinity or a NaN among
+// the values of a tile which some of its rows see in part.  (A product of matrices adds 0 * Inf = NaN to the others.)
+template <int DT, int DP>
+__device__ void careful_rows(const PromptArgs& a, const Work& w, int head, int kv, float factor) {
+  typedef typename Elem<DT>::T T;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kOwn = DP / 64;
+  for (int r = wave; r < kQueries; r += kWaves) {
+    const int64_t i = w.first + r;
+    if (i >= w.n) continue;
+    const int64_t seen = min(w.m, a.causal ? max(int64_t(0), i + (w.m - w.n) + 1) : w.m);
+    const T* q = static_cast<const T*>(a.q.p) + (w.q0 + i) * a.q.st + head * a.q.sh;
+    float most = -INFINITY, total = 0.0f, o[kOwn] = {};
+    for (int64_t j0 = 0; j0 < seen; j0 += 64) {
+      const int64_t j = min(j0 + lane, seen - 1);
+      const T* k = static_cast<const T*>(a.k.p) + (w.k0 + j) * a.k.st + kv * a.k.sh;
+      float s = 0.0f;
+      for (int d = 0; d < a.D; ++d) s = fmaf(static_cast<float>(q[d]), static_cast<float>(k[d]), s);
+      s = j0 + lane < seen ? s * factor : -INFINITY;
+      float top = s;
+      for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+      top = fmaxf(most, top);
+      const float zero = top == -INFINITY ? 0.0f : top, shrink = __builtin_amdgcn_exp2f(most - zero);
+      most = top;
+      const float p = __builtin_amdgcn_exp2f(s - zero);
+      float sum = p;
+      for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
+      total = total * shrink + sum;
+      for (int e = 0; e < kOwn; ++e) o[e] *= shrink;
+      for (int n = 0; n < min(int64_t(64), seen - j0); ++n) {
+        const T* v = static_cast<const T*>(a.v.p) + (w.k0 + j0 + n) * a.v.st + kv * a.v.sh;
+        const float pn = __shfl(p, n);
+        for (int e = 0; e < kOwn; ++e)
+          if (e * 64 + lane < a.D) o[e] = fmaf(pn, static_cast<float>(v[e * 64 + lane]), o[e]);
+      }
+    }
+    T* out = static_cast<T*>(a.out) + ((w.q0 + i) * a.Hq + head) * a.D;
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    for (int e = 0; e < kOwn; ++e)
+      if (e * 64 + lane < a.D) out[e * 64 + lane] = static_cast<T>(o[e] * inv);
+  }
+}
+
+// DT: type of everything but the sums; DP: columns, D rounded up to 64, 128 or 256.
+//
+// Scores are computed transposed, S^T = K Q^T (keys x queries): a lane then holds, for one query, the scores of the keys
+// that its operand of O^T = V^T P^T takes, in the order in which that product's other operand, V^T, can be read from
+// row-major LDS by transposing reads; the probabilities never leave their lane, and a row's maximum takes one exchange
+// between two lanes.  P is rounded to DT once: its 2^-9 (bf16) of each term, with independent signs, stays below the
+// rounding of the output.  (fp16: P times 2^8, so that small ones keep their bits.)
+template <int DT, int DP>
+__global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(PromptArgs a) {
+  typedef typename Elem<DT>::T T;
+  typedef Tile<DP> L;
+  constexpr int kBytes = kKeys * L::kRow, kLoads = kBytes / 1024 / kWaves, kOut = DP / 32;
+  constexpr int kPer = 64 / L::kPieces > 0 ? 64 / L::kPieces : 1;  // rows of a load of a wave
+  static_assert(L::kPieces <= 64, "a load holds whole rows");
+  constexpr float kLift = DT == DT_F16 ? 8.0f : 0.0f;
+  // One array: with a second one the compiler tells what is loaded into LDS apart by its variable, and makes every read of
+  // `lds` wait for the loads of the next tile.
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes + 16];
+  int& met = *reinterpret_cast<int*>(lds + 4 * kBytes);
+
+  const int G = a.Hq / a.H;
+  // key heads vary fastest: workgroup i runs on die i mod 8, so that a key head's rows stay in one die's L2 cache
+  const int64_t block = block_index();
+  const int hx = static_cast<int>(block % a.Hq), kv = hx % a.H, head = kv * G + hx / a.H;
+  const Work w = find_work(a, block / a.Hq);
+  if (!w.some) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  const float factor = a.scale * 1.44269504088896340736f;
+  const int64_t shift = w.m - w.n;  // query i sees keys 0 .. i + shift
+  const int64_t i0 = w.first + wave * 32;
+  const int64_t last = min(w.n, w.first + kQueries) - 1;
+  int64_t end = a.causal ? min(w.m, last + shift + 1) : w.m;  // keys that some row here sees
+  if (end < 0) end = 0;
+  const int64_t mine = a.causal ? min(w.m, i0 + 31 + shift + 1) : w.m;   // of this wave's rows
+  const int64_t whole = a.causal ? min(w.m, i0 + shift + 1) : w.m;       // keys that all of its rows see
+  const int64_t whole_all = a.causal ? min(w.m, w.first + shift + 1) : w.m;
+  const int count = static_cast<int>((end + kKeys - 1) / kKeys);
+  if (threadIdx.x == 0) met = 0;
+
+  H8<DT> q[DP / 16];
+  {
+    const T* p = static_cast<const T*>(a.q.p) + (w.q0 + min(i0 + col, w.n - 1)) * a.q.st + head * a.q.sh;
+    typedef H8<DT> Qu __attribute__((aligned(sizeof(T))));
+#pragma unroll
+    for (int j = 0; j < DP / 16; ++j) {
+      const int d = j * 16 + half * 8;
+      q[j] = *reinterpret_cast<const Qu*>(p + (d < a.D ? d : 0));
+      if (d >= a.D) q[j] = H8<DT>{};
+    }
+  }
+
+  // loads of a tile: this wave's lanes take pieces of rows (wave * kLoads + n) * kPer ..; a lane whose piece lies past D
+  // reads past the descriptor's end, which gives zeros, as do rows past the last key
+  const uint32_t kst = static_cast<uint32_t>(a.k.st * 2), vst = static_cast<uint32_t>(a.v.st * 2);
+  uint32_t koff[kLoads], voff[kLoads];
+#pragma unroll
+  for (int n = 0; n < kLoads; ++n) {
+    const int row = (wave * kLoads + n) * kPer + lane / L::kPieces, p = lane % L::kPieces;
+    const int kp = L::key(row, p), vp = L::value(row, p);  // the xor is its own inverse
+    koff[n] = kp * 8 < a.D ? row * kst + kp * 16 : 0x7FFFFFF0u;
+    voff[n] = vp * 8 < a.D ? row * vst + vp * 16 : 0x7FFFFFF0u;
+  }
+  const T* const kbase = static_cast<const T*>(a.k.p) + w.k0 * a.k.st + kv * a.k.sh;
+  const T* const vbase = static_cast<const T*>(a.v.p) + w.k0 * a.v.st + kv * a.v.sh;
+  auto load_tile = [&](int i) {
+    const int64_t j = static_cast<int64_t>(i) * kKeys;
+    const uint32_t rows = static_cast<uint32_t>(min(w.m - j, int64_t(kKeys)));
+    const __amdgpu_buffer_rsrc_t kr = rsrc(kbase + j * a.k.st, (rows - 1) * kst + a.D * 2);
+    const __amdgpu_buffer_rsrc_t vr = rsrc(vbase + j * a.v.st, (rows - 1) * vst + a.D * 2);
+    uint8_t* d = lds + (i & 1) * 2 * kBytes + wave * kLoads * 1024;
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) load_lds16(kr, d + n * 1024, koff[n]);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) load_lds16(vr, d + kBytes + n * 1024, voff[n]);
+  };
+
+  float most = -INFINITY, total = 0.0f;  // of query col; the sum over this lane's keys only
+  f32x16 o[kOut];
+#pragma unroll
+  for (int d = 0; d < kOut; ++d) o[d] = f32x16{};
+
+  if (count > 0) load_tile(0);
+  for (int i = 0; i < count; ++i) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this tile's loads, issued a tile ago
+    __syncthreads();
+    if (i + 1 < count) load_tile(i + 1);
+    const uint8_t* const lk = lds + (i & 1) * 2 * kBytes;
+    const uint8_t* const lv = lk + kBytes;
+    const int64_t j0 = static_cast<int64_t>(i) * kKeys;
+    if (a.causal && j0 + kKeys > whole_all) {  // rows see parts of this tile: infinities and NaN among its values
+      uint32_t worst = 0;
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) {
+        const uint4 x = *reinterpret_cast<const uint4*>(lv + (wave * kLoads + n) * 1024 + lane * 16);
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) worst = max(worst, max(y[e] << 1 & 0xFFFFu, y[e] >> 15 & 0xFFFEu));
+      }
+      if (__any(worst >= (DT == DT_F16 ? 0xF800u : 0xFF00u))) met = 1;
+    }
+    if (j0 >= mine) continue;  // this wave's rows see nothing of it (nor of later ones)
+
+    f32x16 s[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      s[k] = f32x16{};
+      const int row = k * 32 + col;
+#pragma unroll
+      for (int j = 0; j < DP / 16; ++j)
+        s[k] = mma(*reinterpret_cast<const H8<DT>*>(lk + row * L::kRow + L::key(row, 2 * j + half) * 16), q[j], s[k]);
+    }
+    if (j0 + kKeys > whole) {
+      const int64_t lim = min(w.m, a.causal ? i0 + col + shift + 1 : w.m) - j0;  // keys of the tile that row col sees
+      const int seen = static_cast<int>(min(lim, int64_t(kKeys)));
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (k * 32 + e / 4 * 8 + half * 4 + e % 4 >= seen) s[k][e] = -INFINITY;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[k][e]);
+    top = fmaxf(most, both_max(top) * factor);  // factor > 0
+    const float zero = top == -INFINITY ? 0.0f : top;
+    const float shrink = __builtin_amdgcn_exp2f(most - zero);
+    most = top;
+    float f = factor;
+    if (__any(fabsf(top) > 0x1p20f && top < INFINITY && top > -INFINITY)) {
+      // scores so large that the rounding of the maximum, which the fma below does not share, would show
+#pragma unroll
+      for (int k = 0; k < 2; ++k) s[k] *= factor;
+      f = 1.0f;
+    }
+    total *= shrink;
+#pragma unroll
+    for (int d = 0; d < kOut; ++d) o[d] *= shrink;
+    H8<DT> p[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(s[u / 2][u % 2 * 8 + e], f, kLift - zero));
+        total += x;
+        p[u][e] = static_cast<T>(x);
+      }
+    // key slots of step u: 16 u + 4 half + 0 .. 3 and 8 more, as the scores lie
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) {
+        union { i16x4 w[2]; H8<DT> v; } x;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = u * 16 + e * 8 + half * 4 + (lane & 15) / 4, piece = d * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1);
+          x.w[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) i16x4*)(lv + row * L::kRow + L::value(row, piece) * 16 + (lane & 1) * 8));
+        }
+        o[d] = mma(x.v, p[u], o[d]);
+      }
+  }
+  total = both_sum(total);
+  __syncthreads();
+  if (met) {
+    careful_rows<DT, DP>(a, w, head, kv, factor);
+    return;
+  }
+  if (i0 + col >= w.n) return;
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  T* out = static_cast<T*>(a.out) + ((w.q0 + i0 + col) * a.Hq + head) * a.D;
+#pragma unroll
+  for (int d = 0; d < kOut; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = d * 32 + e * 8 + half * 4;
+      if (c < a.D) {
+        typedef T V4 __attribute__((ext_vector_type(4)));
+        typedef V4 V4u __attribute__((aligned(sizeof(T))));
+        V4 v;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = static_cast<T>(o[d][4 * e + x] * inv);
+        *reinterpret_cast<V4u*>(out + c) = v;
+      }
+    }
+}
+
+template <int DT, int DP>
+hipError_t prompt(const PromptArgs& a, hipStream_t s) {
+  const int64_t tiles = (a.Tq + kQueries - 1) / kQueries + a.B;  // at least the sequences' tiles
+  hipLaunchKernelGGL((k_prompt<DT, DP>), long_grid(tiles * a.Hq), dim3(64 * kWaves), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_prompt(const PromptArgs& a, int dt, hipStream_t s) {
+  if (dt == DT_F16) {
+    if (a.D <= 64) return prompt<DT_F16, 64>(a, s);
+    return a.D <= 128 ? prompt<DT_F16, 128>(a, s) : prompt<DT_F16, 256>(a, s);
+  }
+  if (a.D <= 64) return prompt<DT_BF16, 64>(a, s);
+  return a.D <= 128 ? prompt<DT_BF16, 128>(a, s) : prompt<DT_BF16, 256>(a, s);
+}
+
+}  // namespace qmm

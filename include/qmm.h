@@ -101,8 +101,9 @@ typedef enum {
 } qmm_type;
 
 /* Element type of activations (x) and of qmm_dequantize's output.  QMM_BF16 is taken by
- * the qmm_f8_* and qmm_route* calls only. */
-typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_dtype;
+ * the qmm_f8_*, qmm_route*, qmm_cache*, qmm_head* and qmm_attend* calls only, QMM_E4M3 as
+ * the type of a cache by qmm_cache_create only. */
+typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2, QMM_E4M3 = 3 } qmm_dtype;
 
 /* Token tile of the matrix-matrix path (candle pull request, sections "What
  * changes" and "Where the 64-token tile is used"): AUTO applies
@@ -565,6 +566,133 @@ qmm_status qmm_route_combine_backward(const void *y, qmm_dtype yt, const void *w
                                       qmm_dtype wt, int64_t N, int64_t S, int64_t M,
                                       const void *dout, void *dy, void *dweights,
                                       qmm_stream_t stream);
+
+/*
+ * Between the projections of a served layer
+ * -----------------------------------------
+ * Norms and rotation of the query and key heads, a paged key-value cache, and attention over
+ * it and over prompts.  Inputs x [T, heads, D] are given with the strides of a token and of a
+ * head in elements (the last axis is contiguous), so that slices of one projection's output are
+ * taken as they are; outputs are contiguous.  D is a multiple of 16, 16..256; T up to 2^30.
+ * Serving: no gradients.  Conventions are those at the top of this file; a call with nothing
+ * to compute (T = 0, B = 0) returns QMM_OK without looking at its pointers.
+ *
+ * qmm_head_norm_rope -- queries q [T, Hq, D] and keys k [T, H, D] (type xt; Hq or H may be 0):
+ *   y = x / sqrt(mean(x^2) + eps) * w     over each head (not where the weight is NULL)
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = positions[token] * inv_freq[i]
+ *                                         for the pairs i of the first R columns
+ *   q_weight, k_weight  DEVICE [D] of type wt, or NULL: no norm.   eps >= 0.
+ *   positions  DEVICE int32 [T].   inv_freq  DEVICE fp32 [R / 2].
+ *   R          a multiple of 8, 0 (no rotation; positions and inv_freq may be NULL) .. D.
+ *   interleaved  0: pair i is columns i and i + R / 2; 1: columns 2 i and 2 i + 1.
+ *   q_out, k_out  DEVICE, contiguous, type ot, element-aligned; may be q and k themselves
+ *              where those are contiguous and of type ot.
+ * Sums are fp32, angles 64-bit; one rounding to ot.
+ */
+qmm_status qmm_head_norm_rope(const void *q, int64_t q_token, int64_t q_head, const void *k,
+                              int64_t k_token, int64_t k_head, qmm_dtype xt, int64_t T,
+                              int64_t Hq, int64_t H, int64_t D, const void *q_weight,
+                              const void *k_weight, qmm_dtype wt, float eps,
+                              const int32_t *positions, const float *inv_freq, int64_t R,
+                              int interleaved, void *q_out, void *k_out, qmm_dtype ot,
+                              qmm_stream_t stream);
+
+/*
+ * qmm_cache_create / qmm_cache_destroy -- describe a paged key-value cache (as qmm_create).
+ *   k, v      DEVICE, 16-byte aligned, [pages][heads][page][D] of `type`: QMM_F16, QMM_BF16, or
+ *             QMM_E4M3: codes with one fp32 scale per token and head,
+ *               s = max(fp32(max |x| / 448), 2^-80),  code = the e4m3 value nearest to x / s
+ *             (one rounding, ties to even; a head that holds an Inf or a NaN gets the scale NaN).
+ *   k_scales, v_scales  DEVICE fp32, 16-byte aligned, [pages][heads][page]; NULL for 16-bit types.
+ *   page      tokens of a page: a power of two, 16..4096.   pages * page <= 2^30.
+ * All are borrowed; calls in stream order read and write them.
+ *
+ * A token's place is its slot, page * (tokens of a page) + row.  A sequence's places are a row of
+ * a table int32 [B][W]: its token t lies on page table[b][t / page].  Entries past a sequence's
+ * last page are not read.
+ */
+typedef struct qmm_cache qmm_cache;
+qmm_status qmm_cache_create(qmm_cache **out, void *k, void *v, float *k_scales, float *v_scales,
+                            qmm_dtype type, int64_t pages, int64_t page, int64_t heads,
+                            int64_t D);
+qmm_status qmm_cache_destroy(qmm_cache *h);
+
+/*
+ * qmm_cache_write -- keys and values [T, heads, D] (type xt) to their slots, converted or
+ * quantized on the way.
+ *   slots  DEVICE int32 [T]; a negative one, or one past the last page, leaves its token out.
+ *          The slots of a call are distinct: of two tokens with one slot it is not specified
+ *          which is left there, nor that all parts left are of the same one.
+ * qmm_cache_norm_rope_write -- qmm_head_norm_rope of q and k, then qmm_cache_write of the keys
+ * (as rounded to ot) and of v, in one launch and with the same bits.  ot is the cache's type
+ * unless that is e4m3.
+ * qmm_cache_read -- B sequences from the cache, packed one after another: sequence b's tokens 0,
+ * 1, .. become rows starts[b] .. starts[b + 1] - 1 of k and v [total, heads, D] (type ot,
+ * contiguous, element-aligned).
+ *   starts  DEVICE int32 [B + 1], not decreasing.  Rows before starts[0] and from starts[B] on
+ *           are left as they were.
+ * A token whose table entry names no page, or that lies past the table's columns, gives NaN.
+ */
+qmm_status qmm_cache_write(const qmm_cache *h, const void *k, int64_t k_token, int64_t k_head,
+                           const void *v, int64_t v_token, int64_t v_head, qmm_dtype xt,
+                           int64_t T, const int32_t *slots, qmm_stream_t stream);
+qmm_status qmm_cache_norm_rope_write(const qmm_cache *h, const void *q, int64_t q_token,
+                                     int64_t q_head, const void *k, int64_t k_token,
+                                     int64_t k_head, const void *v, int64_t v_token,
+                                     int64_t v_head, qmm_dtype xt, int64_t T, int64_t Hq,
+                                     const void *q_weight, const void *k_weight, qmm_dtype wt,
+                                     float eps, const int32_t *positions, const float *inv_freq,
+                                     int64_t R, int interleaved, const int32_t *slots,
+                                     void *q_out, qmm_dtype ot, qmm_stream_t stream);
+qmm_status qmm_cache_read(const qmm_cache *h, const int32_t *table, int64_t B, int64_t W,
+                          const int32_t *starts, int64_t total, void *k, void *v, qmm_dtype ot,
+                          qmm_stream_t stream);
+
+/*
+ * qmm_cache_attend -- attention of one new token per sequence over the cache:
+ *   out[b, h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q[b, h].k_t - max),
+ * t over the first lengths[b] tokens of the sequence, k and v of key head h / (Hq / heads).
+ *   q        DEVICE [B, Hq, D] with strides, fp16 or bf16 (qt); a 16-bit cache's own type, either
+ *            with an e4m3 cache.  Hq a multiple of the cache's heads.  B up to 65535.
+ *   lengths  DEVICE int32 [B]; 0 gives a row of zeros; above the table's reach W * page it counts
+ *            as that.  A table entry that names no page makes the sequence's outputs NaN.
+ *   max_length  the longest length, as far as the caller knows it: it decides into how many
+ *            pieces a sequence is divided and nothing else.
+ *   scale    positive, of the scores (1 / sqrt(D) as a rule).
+ *   out      DEVICE [B, Hq, D] of type qt, contiguous, element-aligned.
+ *   ws       DEVICE, 16-byte aligned, qmm_cache_attend_workspace_bytes(h, B, Hq, max_length)
+ *            bytes (0 for an argument that the call refuses).  Borrowed until the stream passes the
+ *            call; concurrent calls need separate ones.
+ * Softmax in fp32; probabilities keep 16 bits or more; outputs are rounded once.  What the cache
+ * holds past a sequence's last token has no influence, whatever it is.  A row whose scores are all
+ * -inf is zeros; an infinite value gives NaN.
+ */
+size_t qmm_cache_attend_workspace_bytes(const qmm_cache *h, int64_t B, int64_t Hq,
+                                        int64_t max_length);
+qmm_status qmm_cache_attend(const qmm_cache *h, const void *q, qmm_dtype qt, int64_t q_token,
+                            int64_t q_head, int64_t B, int64_t Hq, const int32_t *table, int64_t W,
+                            const int32_t *lengths, int64_t max_length, float scale, void *out,
+                            void *ws, size_t ws_bytes, qmm_stream_t stream);
+
+/*
+ * qmm_attend_prompt -- attention of B packed sequences: queries q [Tq, Hq, D], keys and values
+ * [Tk, H, D], all fp16 or all bf16 (dt), Hq a multiple of H.
+ *   q_starts, k_starts  DEVICE int32 [B + 1], not decreasing: sequence b has the n queries from
+ *            q_starts[b] and the m keys from k_starts[b] on (the same array without a prefix).
+ *   causal   1: query i of n sees keys 0 .. i + m - n, so that the last query sees all keys; a
+ *            query that sees none (n > m) gives zeros.  0: all of its sequence's keys.
+ *   k, v     rows 16-byte aligned; a token's stride D .. 2^23 elements.
+ *   scale    positive.    out  DEVICE [Tq, Hq, D], contiguous; rows of no sequence are left as they were.
+ * Softmax in fp32, probabilities rounded to dt, outputs rounded once.  A key or value that a query
+ * does not see has no influence on it, whatever it holds.  A row whose scores are all -inf is
+ * zeros.
+ */
+qmm_status qmm_attend_prompt(const void *q, int64_t q_token, int64_t q_head, const void *k,
+                             int64_t k_token, int64_t k_head, const void *v, int64_t v_token,
+                             int64_t v_head, qmm_dtype dt, const int32_t *q_starts,
+                             const int32_t *k_starts, int64_t B, int64_t Tq, int64_t Tk,
+                             int64_t Hq, int64_t H, int64_t D, int causal, float scale, void *out,
+                             qmm_stream_t stream);
 
 /* qmm_tile_for_tokens -- 64 when a 64-token tile pads no more tokens than a
  * 32-token tile, else 32 (candle pull request, section "Where the 64-token tile

@@ -18,6 +18,7 @@ Contents
              check for the library's GPU quantizer.
 ``f8``       e4m3 codes with a scale per block of 128: quantizers and decoding.
 ``route``    the expert router, balance loss and their gradients.
+``attention``  head norms and rotation, a cache's quantization, attention.
 ``tile``     the 32/64-token tile rule of the candle pull request
              "Metal: 64-token tile for the quantized matrix-matrix kernel",
              section "Where the 64-token tile is used".
@@ -38,4 +39,4 @@ from .formats import (  # noqa: F401
 from .matmul import matmul_ref, matmul_id_ref, tolerance_scale, tolerance_scale_id  # noqa: F401
 from .tile import tile_for_tokens, pad_tokens  # noqa: F401
 from .quantize import quantize_blocks  # noqa: F401
-from . import f8, route  # noqa: F401
+from . import attention, f8, route  # noqa: F401
