@@ -7,6 +7,8 @@
 // `splits` pieces of whole 32-token tiles, a piece among the four waves of a workgroup; each wave keeps its own running
 // maximum, sum and output, which are joined in wave order through LDS and, where there is more than one piece, in piece
 // order by a second small launch.
+#include <algorithm>
+
 #include "attn.hpp"
 
 namespace qmm {
@@ -15,6 +17,8 @@ namespace {
 
 constexpr int kWaves = 4, kTile = 32;  // waves of a workgroup, tokens of a wave's tile
 constexpr int kRows = 16;              // query heads of a workgroup
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 template <int QT> struct Half8 { typedef typename Elem<QT>::T V __attribute__((ext_vector_type(8))); };
 template <int QT> using H8 = typename Half8<QT>::V;
@@ -60,27 +64,27 @@ __device__ __forceinline__ float column_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Pieces of a sequence: whole tiles for every wave.
-__device__ __forceinline__ int64_t piece_of(int64_t len, int splits) {
-  const int64_t step = kWaves * kTile;
-  return ((len + splits - 1) / splits + step - 1) / step * step;
+// A wave's tile in LDS, rows of ROW bytes in 16-byte pieces xored with a function of the row, so that the reads of one piece
+// of 16 rows (keys) and of two neighbouring pieces of four rows (values, transposed on the way; of codes one piece of eight
+// rows) use different banks.  Keys and values share it, and with it the pieces past D, which stay zeros.
+template <int ROW>
+__device__ __forceinline__ int tile_at(int row, int piece) {
+  const int x = ROW >= 256 ? (2 * row | (row >> 3 & 1)) & 15 : ROW == 128 ? (row >> 1 ^ row >> 3) & 7 : (row >> 2) & 3;
+  return row * ROW + (piece ^ x) * 16;
 }
 
-// Rows of a wave's tile in LDS: DP columns of `size` bytes each, in 16-byte pieces xored with a function of the row, so
-// that the reads of one piece of many rows (keys) and of two neighbouring pieces of four or eight rows (values, transposed
-// on the way) use different banks.
-template <int ROW>  // bytes
-struct Rows {
-  static constexpr int kPieces = ROW / 16;
-  __device__ static __forceinline__ int key(int row, int piece) {
-    const int x = ROW >= 256 ? row & 15 : ROW == 128 ? (row >> 1 ^ row >> 3) & 7 : (row >> 2) & 3;
-    return row * ROW + ((piece ^ x) * 16);
-  }
-  __device__ static __forceinline__ int value(int row, int piece) {
-    const int x = ROW >= 256 ? 2 * row & 15 : ROW == 128 ? (row >> 1 ^ row >> 3) & 7 : (row >> 2) & 3;
-    return row * ROW + ((piece ^ x) * 16);
-  }
-};
+// LDS by byte address: the piece of the same row whose number differs by the bits of `by`, which is one xor.  `fresh` keeps
+// the compiler from making the addresses of all pieces ahead of the loop, which would cost it a register each.
+#define LDS_AS __attribute__((address_space(3)))
+template <typename T>
+__device__ __forceinline__ LDS_AS T* lds_piece(uint32_t at, int by) {
+  return reinterpret_cast<LDS_AS T*>(at ^ static_cast<uint32_t>(by * 16));
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) { return reinterpret_cast<uintptr_t>((LDS_AS const void*)p); }
+__device__ __forceinline__ uint32_t fresh(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 
 // QT: type of the queries and outputs; CT: QT or DT_E4M3; DP: columns, D rounded up to 64, 128 or 256.
 //
@@ -101,7 +105,9 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
   constexpr float kLift = PT == DT_F16 ? 8.0f : 0.0f;  // P in fp16 times 2^8: small ones keep their bits
   typedef typename Elem<QT>::T Q;
   typedef typename Elem<PT>::T P;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves][2][kTile * kRow];
+  // a wave's tile, first its keys, then its values; at the end its outputs
+  constexpr int kRoom = kTile * kRow > kRows * DP * 4 ? kTile * kRow : kRows * DP * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves][kRoom];
   __shared__ float sums[kWaves][2][kRows];
 
   const CacheDesc& c = a.cache;
@@ -112,11 +118,17 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
   const int64_t b = blockIdx.z;
   const int rows = min(kRows, G - g0);                 // heads here
   const int64_t room = a.W << c.shift;
+  const int64_t t0 = split * a.piece;
+  const int32_t* table = a.table + b * a.W;
+  // the first tile's pages are asked for before the length is known; a place past the table reads its last entry
+  auto page_at = [&](int64_t t) { return table[min(t >> c.shift, a.W - 1)]; };
+  int32_t page[kBlocks];
+#pragma unroll
+  for (int k = 0; k < kBlocks; ++k) page[k] = a.W ? page_at(t0 + wave * kTile + k * 16) : 0;
   int64_t len = a.lengths[b];
   len = len < 0 ? 0 : len > room ? room : len;
-  const int64_t piece = piece_of(len, a.splits), t0 = split * piece, t1 = min(len, t0 + piece);
   if (t0 >= len && split > 0) return;                  // the join reads the pieces that there are
-  const int32_t* table = a.table + b * a.W;
+  const int64_t t1 = split + 1 == a.splits ? len : min(len, t0 + a.piece);
 
   // queries: column col of the products, 8 columns of the head at a time
   H8<QT> q[DP / 32];
@@ -132,48 +144,52 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
     }
   }
 
-  uint8_t* const lk = lds[wave][0];
-  uint8_t* const lv = lds[wave][1];
+  uint8_t* const mine_lds = lds[wave];
   // a lane's share of 16 tokens' rows, which lie one after another in a page: 16-byte pieces lane, lane + 64, ..
   const int pieces = D * kSize / 16;                   // of a row
+  const int inverse = (65536 + pieces - 1) / pieces;   // i / pieces = i * inverse >> 16 for i < 512
   int at[kLoads], row_of[kLoads], piece_at[kLoads];
   bool some[kLoads];
 #pragma unroll
   for (int n = 0; n < kLoads; ++n) {
     const int i = n * 64 + lane;
-    row_of[n] = DP == D ? i / (kRow / 16) : i / pieces;
-    piece_at[n] = i - row_of[n] * pieces;
     some[n] = i < 16 * pieces;
+    row_of[n] = some[n] ? i * inverse >> 16 : 0;
+    piece_at[n] = some[n] ? i - row_of[n] * pieces : 0;
     at[n] = some[n] ? i * 16 : 0;
   }
   if (D < DP) {  // columns past D: zeros, once
-    for (int i = lane; i < kTile * kRow / 16; i += 64) {
-      reinterpret_cast<uint4*>(lk)[i] = uint4{};
-      reinterpret_cast<uint4*>(lv)[i] = uint4{};
-    }
+    for (int i = lane; i < kTile * kRow / 16; i += 64) reinterpret_cast<u32x4*>(mine_lds)[i] = u32x4{};
+  }
+
+  // where the lane reads: keys, a token a lane; values, eight bytes of which the transposing read makes its operand
+  const int vrow = kCodes ? ((lane & 8) * 2 + quarter * 4 + (lane >> 1 & 3)) : quarter * 4 + ((lane & 15) >> 2);
+  uint32_t key_at[kBlocks], value_at[kBlocks];  // (codes: one read for both blocks)
+#pragma unroll
+  for (int k = 0; k < kBlocks; ++k) {
+    key_at[k] = lds_address(mine_lds) + tile_at<kRow>(k * 16 + col, quarter);
+    value_at[k] = lds_address(mine_lds) + tile_at<kRow>(kCodes ? vrow : k * 16 + vrow, kCodes ? 0 : (lane & 3) >> 1) + (lane & 1) * 8;
   }
 
   const float factor = a.scale * 1.44269504088896340736f;
   const int count = t1 > t0 ? static_cast<int>((t1 - t0 + kTile - 1) / kTile) : 0;
   bool bad = false;
-  uint4 kr[kBlocks][kLoads], vr[kBlocks][kLoads];
+  u32x4 kr[kBlocks][kLoads], vr[kBlocks][kLoads];
   f32x4 ks[kBlocks], vs[kBlocks];
 
-  // where a tile's 16-token block lies; a block past the sequence's last one repeats that
-  auto block_base = [&](int64_t t) -> int64_t {
-    t = min(t, (len - 1) & ~int64_t(15));
-    int64_t page = table[t >> c.shift];
-    if (page < 0 || page >= c.pages) bad = true, page = 0;
+  // where a tile's 16-token block lies; what is past the sequence's last block is not looked at: any page will do
+  auto block_base = [&](int64_t t, int64_t page) -> int64_t {
+    if (page < 0 || page >= c.pages) bad |= t < len, page = 0;
     return ((page * H + h) << c.shift) + (t & ((int64_t(1) << c.shift) - 1));
   };
-  auto load_rows = [&](const uint8_t* data, const int64_t* base, uint4 (*r)[kLoads]) {
+  auto load_rows = [&](const uint8_t* data, const int64_t (&base)[kBlocks], u32x4 (&r)[kBlocks][kLoads]) {
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
       for (int n = 0; n < kLoads; ++n)
-        r[k][n] = *reinterpret_cast<const uint4*>(data + base[k] * (D * kSize) + at[n]);
+        r[k][n] = *reinterpret_cast<const u32x4*>(data + base[k] * (D * kSize) + at[n]);
   };
-  auto load_scales = [&](const float* data, const int64_t* base, f32x4* r) {
+  auto load_scales = [&](const float* data, const int64_t (&base)[kBlocks], f32x4 (&r)[kBlocks]) {
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k) r[k] = *reinterpret_cast<const f32x4*>(data + base[k] + quarter * 4);
   };
@@ -181,7 +197,10 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
   int64_t base[kBlocks];
   if (wave < count) {
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k) base[k] = block_base(t0 + wave * kTile + k * 16);
+    for (int k = 0; k < kBlocks; ++k) {
+      base[k] = block_base(t0 + wave * kTile + k * 16, page[k]);
+      page[k] = page_at(t0 + (wave + kWaves) * kTile + k * 16);
+    }
     load_rows(c.k, base, kr);
     load_rows(c.v, base, vr);
     if constexpr (kCodes) load_scales(c.ks, base, ks), load_scales(c.vs, base, vs);
@@ -205,17 +224,14 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
     for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
       for (int n = 0; n < kLoads; ++n)
-        if (some[n]) {
-          uint4 v = vr[k][n];
-          if (left < kTile && k * 16 + row_of[n] >= left) v = uint4{};  // what a page holds past the sequence stays out
-          *reinterpret_cast<uint4*>(lk + Rows<kRow>::key(k * 16 + row_of[n], piece_at[n])) = kr[k][n];
-          *reinterpret_cast<uint4*>(lv + Rows<kRow>::value(k * 16 + row_of[n], piece_at[n])) = v;
-        }
+        if (some[n]) *reinterpret_cast<u32x4*>(mine_lds + tile_at<kRow>(k * 16 + row_of[n], piece_at[n])) = kr[k][n];
     if (more) {
 #pragma unroll
-      for (int k = 0; k < kBlocks; ++k) base[k] = block_base(t + kWaves * kTile + k * 16);
+      for (int k = 0; k < kBlocks; ++k) {
+        base[k] = block_base(t + kWaves * kTile + k * 16, page[k]);
+        page[k] = page_at(t + 2 * kWaves * kTile + k * 16);  // a tile ahead
+      }
       load_rows(c.k, base, kr);
-      load_rows(c.v, base, vr);
       if constexpr (kCodes) load_scales(c.ks, base, ks), load_scales(c.vs, base, vs);
     }
 
@@ -224,17 +240,18 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k) {
       s[k] = f32x4{};
+      const uint32_t key = fresh(key_at[k]);
       if constexpr (kCodes) {
 #pragma unroll
         for (int j = 0; j < DP / 64; ++j) {
-          const uint4 w = *reinterpret_cast<const uint4*>(lk + Rows<kRow>::key(k * 16 + col, 4 * j + quarter));
+          const u32x4 w = *lds_piece<const u32x4>(key, 4 * j);
           s[k] = mma(widen<QT>(w.x, w.y), q[2 * j], s[k]);
           s[k] = mma(widen<QT>(w.z, w.w), q[2 * j + 1], s[k]);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < DP / 32; ++j)
-          s[k] = mma(*reinterpret_cast<const H8<QT>*>(lk + Rows<kRow>::key(k * 16 + col, 4 * j + quarter)), q[j], s[k]);
+          s[k] = mma(*lds_piece<const H8<QT>>(key, 4 * j), q[j], s[k]);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -242,6 +259,17 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
         if (left < kTile && k * 16 + quarter * 4 + e >= left) s[k][e] = -INFINITY;
       }
     }
+    // every read of the keys lies before this in the wave's order, as do the products that wait for them
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n)
+        if (some[n]) {
+          u32x4 v = vr[k][n];
+          if (left < kTile && k * 16 + row_of[n] >= left) v = u32x4{};  // what a page holds past the sequence stays out
+          *reinterpret_cast<u32x4*>(mine_lds + tile_at<kRow>(k * 16 + row_of[n], piece_at[n])) = v;
+        }
+    if (more) load_rows(c.v, base, vr);
     float top = s[0][0];
 #pragma unroll
     for (int e = 1; e < 4 * kBlocks; ++e) top = fmaxf(top, s[e / 4][e % 4]);
@@ -264,23 +292,20 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
       lo[e] = static_cast<P>(p - static_cast<float>(r));
     }
     total = total * shrink + sum;
+    const uint32_t value[kBlocks] = {fresh(value_at[0]), fresh(value_at[1])};
 #pragma unroll
     for (int d = 0; d < kOut; ++d) {
       o[d] *= shrink;
       H8<PT> v;
       if constexpr (kCodes) {
-        const int r = (lane & 15) >> 1, row = (r & 4) * 4 + quarter * 4 + (r & 3);
-        const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (__attribute__((address_space(3))) i32x2*)(lv + Rows<kRow>::value(row, d) + (lane & 1) * 8));
+        const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(lds_piece<i32x2>(value[0], d));
         v = widen<PT>(w[0], w[1]);
       } else {
-        const int r = quarter * 4 + ((lane & 15) >> 2), p = 2 * d + ((lane & 3) >> 1);
-        union { i16x4 w[2]; H8<PT> v; } u;
+        union { i16x4 w[kBlocks]; H8<PT> v; } x;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          u.w[k] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) i16x4*)(lv + Rows<kRow>::value(k * 16 + r, p) + (lane & 1) * 8));
-        v = u.v;
+        for (int k = 0; k < kBlocks; ++k)
+          x.w[k] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_piece<i16x4>(value[k], 2 * d));
+        v = x.v;
       }
       o[d] = mma(v, hi, o[d]);
       o[d] = mma(v, lo, o[d]);
@@ -296,8 +321,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) best = fmaxf(best, sums[w][0][col]);
   const float mine = most == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(most - best);
-  static_assert(sizeof(lds) >= kWaves * kRows * DP * 4, "the outputs fit the tiles' room");
-  float* part = reinterpret_cast<float*>(lds) + wave * kRows * DP;
+  float* part = reinterpret_cast<float*>(mine_lds);
 #pragma unroll
   for (int d = 0; d < kOut; ++d) *reinterpret_cast<f32x4*>(part + col * DP + d * 16 + quarter * 4) = o[d] * mine;
   __syncthreads();
@@ -313,7 +337,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
     for (int w = 0; w < kWaves; ++w) {
       const float m = sums[w][0][r], l = sums[w][1][r];
       sum += m == -INFINITY && l == 0.0f ? 0.0f : l * (m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top));
-      v += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(lds) + (w * kRows + r) * DP + d);
+      v += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(lds[w]) + r * DP + d);
     }
     const int64_t head = b * a.Hq + h * G + g0 + r;
     if (a.splits == 1) {
@@ -332,46 +356,65 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
   }
 }
 
-// The pieces of a sequence joined, in piece order: a workgroup takes a head of a sequence.
-template <int QT>
+// The pieces of a sequence joined: a workgroup takes a head of a sequence, teams of L lanes every (256 / L)-th piece, and
+// the teams' sums are added in order.  The first pieces are asked for before it is known which there are.
+template <int QT, int L>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
+  constexpr int kTeams = 256 / L, kAhead = 4;
   __shared__ float weight[256];
-  __shared__ float part[4][kMaxHeadDim];
+  __shared__ f32x4 part[kTeams][L];
   __shared__ float red[8];
   typedef typename Elem<QT>::T Q;
   const int D = a.cache.D, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int64_t head = block_index(), b = head / a.Hq;
+  const int team = tid / L, d = tid % L * 4;
+  const float* o = a.ws + head * a.splits * D + (d < D ? d : 0);
+  auto load = [&](int s) { return *reinterpret_cast<const f32x4*>(o + static_cast<int64_t>(min(s, a.splits - 1)) * D); };
+  f32x4 x[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) x[i] = load(team + i * kTeams);
+  const float* ml = a.ws + a.B * a.Hq * a.splits * D + head * a.splits * 2;
+  const int at = min(tid, a.splits - 1);
+  float m = ml[2 * at], l = ml[2 * at + 1];
   const int64_t room = a.W << a.cache.shift;
   int64_t len = a.lengths[b];
   len = len < 0 ? 0 : len > room ? room : len;
-  const int64_t piece = piece_of(len, a.splits);
-  const int n = len == 0 ? 1 : static_cast<int>((len + piece - 1) / piece);  // an empty sequence has an empty piece
-  const float* ml = a.ws + a.B * a.Hq * a.splits * D + head * a.splits * 2;
-  const float m = tid < n ? ml[2 * tid] : -INFINITY, l = tid < n ? ml[2 * tid + 1] : 0.0f;
+  // pieces that there are: one at least, of an empty sequence too
+  const int n = static_cast<int>(min(max((len + a.piece - 1) / a.piece, int64_t(1)), int64_t(a.splits)));
+  if (tid >= n) m = -INFINITY, l = 0.0f;
   float top = m;
-  for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+#pragma unroll
+  for (int i = 32; i; i >>= 1) top = fmaxf(top, __shfl_xor(top, i));
   if (lane == 0) red[wave] = top;
   __syncthreads();
   top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   const float w = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
   float sum = l != l ? l : l * w;  // NaN also where nothing else is
-  for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
+#pragma unroll
+  for (int i = 32; i; i >>= 1) sum += __shfl_xor(sum, i);
   if (lane == 0) red[4 + wave] = sum;
   weight[tid] = w;
   __syncthreads();
   sum = (red[4] + red[5]) + (red[6] + red[7]);
-  const float* o = a.ws + head * a.splits * D;
-  for (int d = lane * 4; d < D; d += 256) {
-    f32x4 v{};
-    for (int s = wave; s < n; s += 4)
-      if (weight[s] != 0.0f) v += weight[s] * *reinterpret_cast<const f32x4*>(o + static_cast<int64_t>(s) * D + d);
-    *reinterpret_cast<f32x4*>(&part[wave][d]) = v;
+  f32x4 v{};
+  for (int s = team; s < n; s += kAhead * kTeams) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int p = s + i * kTeams;
+      if (p < n && weight[p] != 0.0f) v += weight[p] * x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) x[i] = load(s + (kAhead + i) * kTeams);
   }
+  part[team][tid % L] = v;
   __syncthreads();
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  if (tid < D) {
-    const float v = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
-    static_cast<Q*>(a.out)[head * D + tid] = static_cast<Q>(v * inv);
+  if (team == 0 && d < D) {
+#pragma unroll
+    for (int i = 1; i < kTeams; ++i) v += part[i][tid];
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    Q* out = static_cast<Q*>(a.out) + head * D + d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = static_cast<Q>(v[e] * inv);
   }
 }
 
@@ -384,20 +427,26 @@ hipError_t attend(const AttendArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((k_attend<QT, CT, 256>), grid, dim3(64 * kWaves), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((k_attend_join<QT>), long_grid(a.B * a.Hq), dim3(256), 0, s, a);
+  const dim3 heads = long_grid(a.B * a.Hq);
+  if (a.cache.D <= 64) hipLaunchKernelGGL((k_attend_join<QT, 16>), heads, dim3(256), 0, s, a);
+  else if (a.cache.D <= 128) hipLaunchKernelGGL((k_attend_join<QT, 32>), heads, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_attend_join<QT, 64>), heads, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Pieces a sequence is divided into: enough workgroups for two on every compute unit, none of fewer than a tile for every
-// wave by the bound on the lengths, 256 at most.
-int attend_splits(const CacheDesc& c, int64_t B, int Hq, int64_t bound) {
+// Pieces: so long that sequences of the bound's length give two workgroups a compute unit, as many as reside (four: 64 x
+// 8192 tokens 251 -> 255 us, 2 x 131072 codes 78 -> 89: each piece begins with two round trips to memory), but not
+// longer than 8192 tokens, so that one sequence much longer than the others does not end alone; whole tiles for every
+// wave, and at most 256 a sequence.
+AttendSplit attend_split(const CacheDesc& c, int64_t B, int Hq, int64_t bound) {
+  constexpr int64_t kMost = 8192, kStep = kWaves * kTile;
   const int64_t G = Hq / c.heads, units = B * c.heads * ((G + kRows - 1) / kRows);
-  int64_t n = (2 * c.cus + units - 1) / units;
-  const int64_t most = (bound + kWaves * kTile - 1) / (kWaves * kTile);
-  n = n < most ? n : most;
-  return static_cast<int>(n < 1 ? 1 : n > 256 ? 256 : n);
+  int64_t n = std::max((2 * c.cus + units - 1) / units, (bound + kMost - 1) / kMost);
+  n = std::min<int64_t>(n, 256);
+  const int64_t piece = std::max<int64_t>((bound + n * kStep - 1) / (n * kStep), 1) * kStep;
+  return {static_cast<int>(std::max<int64_t>((bound + piece - 1) / piece, 1)), piece};
 }
 
 hipError_t launch_attend(const AttendArgs& a, int qt, hipStream_t s) {

@@ -65,10 +65,15 @@ struct AttendArgs {
   const int32_t* lengths;
   float scale;  // of the scores
   void* out;    // [B][Hq][D]
-  int splits;
+  int splits;     // pieces of a sequence, of `piece` tokens each, the last of all that is left
+  int64_t piece;
   float* ws;    // splits > 1: partial outputs [B][Hq][splits][D], then (maximum, sum) [B][Hq][splits]
 };
-int attend_splits(const CacheDesc& c, int64_t B, int Hq, int64_t bound);
+struct AttendSplit {
+  int splits;
+  int64_t piece;
+};
+AttendSplit attend_split(const CacheDesc& c, int64_t B, int Hq, int64_t bound);
 hipError_t launch_attend(const AttendArgs& a, int qt, hipStream_t s);
 
 struct PromptArgs {

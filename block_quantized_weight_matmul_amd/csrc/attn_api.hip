@@ -240,7 +240,7 @@ qmm_status qmm_cache_norm_rope_write(const qmm_cache* h, const void* q, int64_t 
 
 size_t qmm_cache_attend_workspace_bytes(const qmm_cache* h, int64_t B, int64_t Hq, int64_t max_length) {
   if (check_attend(h, B, Hq, max_length) != QMM_OK || B == 0) return 0;
-  return attend_bytes(h->d, B, Hq, qmm::attend_splits(h->d, B, static_cast<int>(Hq), max_length));
+  return attend_bytes(h->d, B, Hq, qmm::attend_split(h->d, B, static_cast<int>(Hq), max_length).splits);
 }
 
 qmm_status qmm_cache_attend(const qmm_cache* h, const void* q, qmm_dtype qt, int64_t q_sb, int64_t q_sh, int64_t B, int64_t Hq,
@@ -258,7 +258,9 @@ qmm_status qmm_cache_attend(const qmm_cache* h, const void* q, qmm_dtype qt, int
   QMM_TRY(check_ptr(lengths, 4, "lengths"));
   QMM_TRY(check_ptr(out, size_of(qt), "out"));
   qmm::AttendArgs a{};
-  a.splits = qmm::attend_splits(h->d, B, static_cast<int>(Hq), max_length);
+  const qmm::AttendSplit split = qmm::attend_split(h->d, B, static_cast<int>(Hq), max_length);
+  a.splits = split.splits;
+  a.piece = split.piece;
   QMM_TRY(check_ws(ws, ws_bytes, attend_bytes(h->d, B, Hq, a.splits), "ws"));
   QMM_TRY(check_device(h));
   a.cache = h->d;

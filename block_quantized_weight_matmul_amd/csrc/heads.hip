@@ -6,6 +6,8 @@ namespace qmm {
 
 namespace {
 
+typedef f32x4 f32x4u __attribute__((aligned(4)));
+
 template <int DT> struct Quad { typedef typename Elem<DT>::T V __attribute__((ext_vector_type(4))); };
 
 // four elements as they are (aligned to the elements only)
@@ -24,10 +26,21 @@ __device__ __forceinline__ void store4(typename Elem<DT>::T* p, const float* v) 
   *reinterpret_cast<Vu*>(p) = w;
 }
 
-__device__ __forceinline__ float weight_at(const void* w, int wt, int i) {
-  if (wt == DT_F32) return static_cast<const float*>(w)[i];
-  if (wt == DT_F16) return static_cast<float>(static_cast<const _Float16*>(w)[i]);
-  return static_cast<float>(static_cast<const __bf16*>(w)[i]);
+// A lane's eight weights for queries and for keys (null: ones), of a type known at run time: one branch around all loads, so
+// that they are in flight together.
+template <int DT>
+__device__ __forceinline__ void load_weights(const void* qw, const void* kw, int a, int b, float* q, float* k) {
+  typedef typename Elem<DT>::T T;
+  const void* some = qw ? qw : kw;
+  const T *pq = static_cast<const T*>(qw ? qw : some), *pk = static_cast<const T*>(kw ? kw : some);
+  const typename Quad<DT>::V v[4] = {load4<DT>(pq + a), load4<DT>(pq + b), load4<DT>(pk + a), load4<DT>(pk + b)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    q[i] = static_cast<float>(v[0][i]);
+    q[4 + i] = static_cast<float>(v[1][i]);
+    k[i] = static_cast<float>(v[2][i]);
+    k[4 + i] = static_cast<float>(v[3][i]);
+  }
 }
 
 // sine and cosine of an angle of any size, to fp32's rounding: the angle less a multiple of pi / 2 (a two-part constant;
@@ -128,34 +141,43 @@ __global__ __launch_bounds__(256) void k_heads(HeadsArgs a) {
   int32_t slot = -1;
   if constexpr (CACHE) slot = a.slots[t];
 
-  float sine[4], cosine[4];
-  if (a.inv_freq) {
-    const double p = a.positions[t];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) turn(p * static_cast<double>(a.inv_freq[turned ? pair0 + i : 0]), sine[i], cosine[i]);
-  }
+  const int wa = mine ? ca : 0, wb = mine ? cb : 0;
   float qw[8], kw[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = mine ? (i < 4 ? ca : cb - 4) + i : 0;
-    qw[i] = a.qw ? weight_at(a.qw, a.wt, c) : 1.0f;
-    kw[i] = a.kw ? weight_at(a.kw, a.wt, c) : 1.0f;
+  if (a.qw || a.kw) {
+    if (a.wt == DT_F32) load_weights<DT_F32>(a.qw, a.kw, wa, wb, qw, kw);
+    else if (a.wt == DT_F16) load_weights<DT_F16>(a.qw, a.kw, wa, wb, qw, kw);
+    else load_weights<DT_BF16>(a.qw, a.kw, wa, wb, qw, kw);
   }
-
   auto row = [&](int h) -> const X* {
     if (h < a.Hq) return static_cast<const X*>(a.q.p) + t * a.q.st + h * a.q.sh;
     if (h < a.Hq + a.H) return static_cast<const X*>(a.k.p) + t * a.k.st + (h - a.Hq) * a.k.sh;
     return static_cast<const X*>(a.v.p) + t * a.v.st + (h - a.Hq - a.H) * a.v.sh;
   };
   typedef typename Quad<XT>::V V4;
-  for (int h = h0; h < h1; h += kAhead) {
-    V4 lo[kAhead], hi[kAhead];
+  V4 lo[kAhead], hi[kAhead];
+  auto load = [&](int h) {
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
       const X* p = row(min(h + n, h1 - 1));
-      lo[n] = load4<XT>(p + (mine ? ca : 0));
-      hi[n] = load4<XT>(p + (mine ? cb : 0));
+      lo[n] = load4<XT>(p + wa);
+      hi[n] = load4<XT>(p + wb);
     }
+  };
+  if (h0 < h1) load(h0);
+
+  float sine[4], cosine[4];  // while the first heads are on their way
+  if (a.inv_freq) {
+    const double p = a.positions[t];
+    const f32x4 f = *reinterpret_cast<const f32x4u*>(a.inv_freq + (turned ? pair0 : 0));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turn(p * static_cast<double>(f[i]), sine[i], cosine[i]);
+  }
+
+  for (int h = h0; h < h1; h += kAhead) {
+    V4 x0[kAhead], x1[kAhead];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) x0[n] = lo[n], x1[n] = hi[n];
+    if (h + kAhead < h1) load(h + kAhead);
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
       const int g = h + n;
@@ -163,8 +185,8 @@ __global__ __launch_bounds__(256) void k_heads(HeadsArgs a) {
       float v[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] = static_cast<float>(lo[n][i]);
-        v[4 + i] = static_cast<float>(hi[n][i]);
+        v[i] = static_cast<float>(x0[n][i]);
+        v[4 + i] = static_cast<float>(x1[n][i]);
       }
       if (CACHE && g >= a.Hq + a.H) {
         const SlotRow r = slot_row(a.cache, slot, g - a.Hq - a.H);
@@ -316,9 +338,9 @@ hipError_t launch_heads(HeadsArgs a, int xt, int qt, hipStream_t s) {
   const int heads = a.Hq + a.H + (cache ? a.H : 0);
   return with_team(a.D, [&](auto l) {
     constexpr int L = decltype(l)::value;
-    // Long calls: a team takes all heads of its token, so that the angles are made once.  Few tokens: the heads are
-    // divided until the teams fill a wave of every SIMD (4 a compute unit), at least four heads each, one round of loads.
-    const int64_t want = 256 * 4 * (64 / L);
+    // A token's heads are divided among teams until these fill four waves of every SIMD, at least four heads each, one
+    // round of loads; each share makes the token's angles anew.
+    const int64_t want = 256 * 16 * (64 / L);
     int64_t parts = a.T >= want ? 1 : (want + a.T - 1) / a.T;
     const int64_t most = (heads + 3) / 4;
     a.parts = static_cast<int>(parts < most ? parts : most);
