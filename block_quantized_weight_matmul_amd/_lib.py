@@ -74,18 +74,16 @@ def _load():
         "qmm_route_backward": (c_int, [vp, c_int, i64, i64, i64, vp, c_int, f32, vp, vp, vp, vp, vp, vp]),
         "qmm_route_combine": (c_int, [vp, c_int, vp, c_int, i64, i64, i64, vp, vp]),
         "qmm_route_combine_backward": (c_int, [vp, c_int, vp, c_int, i64, i64, i64, vp, vp, vp, vp]),
-        "qmm_head_norm_rope": (c_int, [vp, i64, i64, vp, i64, i64, c_int, i64, i64, i64, i64, vp, vp, c_int, f32, vp, vp, i64,
-                                       c_int, vp, vp, c_int, vp]),
+        # (the argument structs are packed bytes: one conversion, not one for each field)
+        "qmm_head_norm_rope": (c_int, [ctypes.c_char_p, vp]),
         "qmm_cache_create": (c_int, [ctypes.POINTER(vp), vp, vp, vp, vp, c_int, i64, i64, i64, i64]),
         "qmm_cache_destroy": (c_int, [vp]),
-        "qmm_cache_write": (c_int, [vp, vp, i64, i64, vp, i64, i64, c_int, i64, vp, vp]),
-        "qmm_cache_norm_rope_write": (c_int, [vp, vp, i64, i64, vp, i64, i64, vp, i64, i64, c_int, i64, i64, vp, vp, c_int, f32,
-                                              vp, vp, i64, c_int, vp, vp, c_int, vp]),
-        "qmm_cache_read": (c_int, [vp, vp, i64, i64, vp, i64, vp, vp, c_int, vp]),
+        "qmm_cache_write": (c_int, [vp, ctypes.c_char_p, vp]),
+        "qmm_cache_norm_rope_write": (c_int, [vp, ctypes.c_char_p, vp]),
+        "qmm_cache_read": (c_int, [vp, ctypes.c_char_p, vp]),
         "qmm_cache_attend_workspace_bytes": (size, [vp, i64, i64, i64]),
-        "qmm_cache_attend": (c_int, [vp, vp, c_int, i64, i64, i64, i64, vp, i64, vp, i64, f32, vp, vp, size, vp]),
-        "qmm_attend_prompt": (c_int, [vp, i64, i64, vp, i64, i64, vp, i64, i64, c_int, vp, vp, i64, i64, i64, i64, i64, i64,
-                                      c_int, f32, vp, vp]),
+        "qmm_cache_attend": (c_int, [vp, ctypes.c_char_p, vp]),
+        "qmm_attend_prompt": (c_int, [ctypes.c_char_p, vp]),
         "qmm_tile_for_tokens": (c_int, [i64]),
         "qmm_row_bytes": (ctypes.c_size_t, [c_int, i64]),
         "qmm_block_weights": (c_int, [c_int]),

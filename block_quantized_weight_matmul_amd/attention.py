@@ -20,35 +20,60 @@ pointers; the current stream of the tensors' device is used, whichever device is
 """
 
 import ctypes
+import struct
 
 import torch
 
 from ._lib import check, lib
 from .f8 import _DT, _call, _empty, _out, _place, _shape, _tensor
 
-_HALF = (torch.float16, torch.bfloat16)
+_HALF = {torch.float16: 1, torch.bfloat16: 2}
 _CACHE = {torch.float16: 1, torch.bfloat16: 2, torch.uint8: 3, torch.float8_e4m3fn: 3}
+_INT = torch.int32
 _I32 = (torch.int32,)
 _F32 = (torch.float32,)
 
+# the argument structs of include/qmm.h
+_pack_heads = struct.Struct("21q4if4x").pack
+_pack_write = struct.Struct("8qi4x").pack
+_pack_read = struct.Struct("7qi4x").pack
+_pack_attend = struct.Struct("12qif").pack
+_pack_prompt = struct.Struct("18q2if4x").pack
+
+
+# --- argument checks ---------------------------------------------------------------------------
+# A tensor that passes is looked at in as few steps as possible (a step is some 70 ns of host time, and a decode step's
+# call takes less on the device than on the host); one that does not goes through the slow checks, which say why.
 
 def _heads(x, name, dtypes, device=None):
     """(device, T, heads, D, stride of a token, stride of a head) of a [T, heads, D] device tensor."""
+    try:
+        T, H, D = x.shape
+        st, sh, step = x.stride()
+        d = x.get_device()
+        if x.dtype in dtypes and step == 1 and d >= 0 and (device is None or d == device):
+            return d, T, H, D, st, sh
+    except (AttributeError, TypeError, ValueError):
+        pass
     _tensor(x, name, dtypes, (3,))
     d = x.get_device()
     if d < 0:
         raise ValueError(f"{name} must be a device tensor")
     if device is not None and d != device:
         raise ValueError(f"{name} is on cuda:{d}; expected cuda:{device}")
-    T, H, D = x.shape
-    st, sh, step = x.stride()
-    if step != 1 and D > 1:
+    if x.shape[2] > 1:
         raise ValueError(f"{name} must have a contiguous last axis")
-    return d, T, H, D, st, sh
+    return (d, *x.shape, *x.stride()[:2])
 
 
-def _vector(t, name, dtypes, length, device):
-    _tensor(t, name, dtypes, (1,))
+def _vector(t, name, dtype, length, device):
+    """Pointer of a contiguous vector of `length` elements on device."""
+    try:
+        if t.dtype is dtype and t.shape == (length,) and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _tensor(t, name, (dtype,), (1,))
     if t.shape[0] != length:
         raise ValueError(f"{name} has {t.shape[0]} elements; expected {length}")
     _place(device, (t, name))
@@ -56,46 +81,52 @@ def _vector(t, name, dtypes, length, device):
 
 
 def _rotation(positions, inv_freq, T, device):
+    """Pointers of the positions and frequencies, columns rotated."""
     if inv_freq is None:
-        return None, None, 0
+        return 0, 0, 0
     if positions is None:
         raise ValueError("inv_freq needs positions")
     _tensor(inv_freq, "inv_freq", _F32, (1,))
     n = inv_freq.shape[0]
-    return _vector(positions, "positions", _I32, T, device), _vector(inv_freq, "inv_freq", _F32, n, device), 2 * n
+    return _vector(positions, "positions", _INT, T, device), _vector(inv_freq, "inv_freq", torch.float32, n, device), 2 * n
 
 
 def _weights(q_weight, k_weight, D, device):
-    first = q_weight if q_weight is not None else k_weight
-    if first is None:
-        return None, None, 0
-    dtypes = _DT if q_weight is None or k_weight is None else (first.dtype,)
-    _tensor(first, "q_weight" if q_weight is not None else "k_weight", _DT)
-    return tuple(None if w is None else _vector(w, name, dtypes, D, device)
-                 for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight"))) + (_DT[first.dtype],)
+    """Pointers of the weights, their type."""
+    if q_weight is None and k_weight is None:
+        return 0, 0, 0
+    dtype = k_weight.dtype if q_weight is None else getattr(q_weight, "dtype", None)
+    if dtype not in _DT:
+        _tensor(k_weight if q_weight is None else q_weight, "k_weight" if q_weight is None else "q_weight", _DT)
+    return (0 if q_weight is None else _vector(q_weight, "q_weight", dtype, D, device),
+            0 if k_weight is None else _vector(k_weight, "k_weight", dtype, D, device), _DT[dtype])
+
+
+def _result_type(dtype):
+    if dtype not in _DT:
+        raise ValueError(f"dtype {dtype}; expected one of {[str(d) for d in _DT]}")
 
 
 def head_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, dtype=None):
     """(q', k'): every head of q [T, Hq, D] and k [T, H, D] divided by its root mean square and multiplied by its weight [D]
     (None: no norm), then its first 2 len(inv_freq) columns rotated by positions [T] (int32) times inv_freq (fp32; None: no
     rotation), column i with column i + len(inv_freq), or 2 i with 2 i + 1 where interleaved.  dtype: of the results."""
-    device, T, Hq, D, qt, qh = _heads(q, "q", _DT)
-    _, Tk, H, Dk, kt, kh = _heads(k, "k", (q.dtype,), device)
+    d, T, Hq, D, qt, qh = _heads(q, "q", _DT)
+    xt = q.dtype
+    _, Tk, H, Dk, kt, kh = _heads(k, "k", (xt,), d)
     if Tk != T or Dk != D:
         raise ValueError(f"k has shape {tuple(k.shape)}; q has {tuple(q.shape)}")
-    dtype = q.dtype if dtype is None else dtype
-    _tensor_type(dtype)
-    pos, freq, R = _rotation(positions, inv_freq, T, device)
-    qw, kw, wt = _weights(q_weight, k_weight, D, device)
-    qo, ko = _empty((T, Hq, D), dtype, device), _empty((T, H, D), dtype, device)
-    _call(device, lib.qmm_head_norm_rope, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, _DT[q.dtype], T, Hq, H, D, qw, kw, wt,
-          eps, pos, freq, R, int(bool(interleaved)), qo.data_ptr(), ko.data_ptr(), _DT[dtype])
+    if dtype is None:
+        dtype = xt
+    else:
+        _result_type(dtype)
+    pos, freq, R = _rotation(positions, inv_freq, T, d)
+    qw, kw, wt = _weights(q_weight, k_weight, D, d)
+    qo, ko = _empty((T, Hq, D), dtype, d), _empty((T, H, D), dtype, d)
+    _call(d, lib.qmm_head_norm_rope, _pack_heads(
+        q.data_ptr(), k.data_ptr(), 0, qw, kw, pos, freq, 0, qo.data_ptr(), ko.data_ptr(), qt, qh, kt, kh, 0, 0, T, Hq, H, D, R,
+        _DT[xt], wt, _DT[dtype], 1 if interleaved else 0, eps))
     return qo, ko
-
-
-def _tensor_type(dtype):
-    if dtype not in _DT:
-        raise ValueError(f"dtype {dtype}; expected one of {[str(d) for d in _DT]}")
 
 
 class KVCache:
@@ -161,21 +192,22 @@ class KVCache:
     def __reduce__(self):
         return KVCache, (self.k, self.v, self.k_scales, self.v_scales)
 
-    def _kv(self, k, v, device):
-        _, T, H, D, kt, kh = _heads(k, "k", _DT, device)
-        _, Tv, Hv, Dv, vt, vh = _heads(v, "v", (k.dtype,), device)
-        if (H, D) != (self.heads, self.D):
+    def _kv(self, k, v):
+        """Type, tokens and strides of keys and values."""
+        _, T, H, D, kt, kh = _heads(k, "k", _DT, self.device)
+        _, Tv, Hv, Dv, vt, vh = _heads(v, "v", (k.dtype,), self.device)
+        if H != self.heads or D != self.D:
             raise ValueError(f"k has {H} heads of {D}; the cache has {self.heads} of {self.D}")
-        if (Tv, Hv, Dv) != (T, H, D):
+        if Tv != T or Hv != H or Dv != D:
             raise ValueError(f"v has shape {tuple(v.shape)}; k has {tuple(k.shape)}")
-        return T, (k.data_ptr(), kt, kh, v.data_ptr(), vt, vh)
+        return k.dtype, T, kt, kh, vt, vh
 
     def write(self, k, v, slots):
         """k and v [T, heads, D] to slots [T] (int32; negative ones and those past the last page are left out).  The slots
         of a call are distinct."""
-        T, rows = self._kv(k, v, self.device)
-        at = _vector(slots, "slots", _I32, T, self.device)
-        _call(self.device, lib.qmm_cache_write, self._h, *rows, _DT[k.dtype], T, at)
+        xt, T, kt, kh, vt, vh = self._kv(k, v)
+        at = _vector(slots, "slots", _INT, T, self.device)
+        _call(self.device, lib.qmm_cache_write, self._h, _pack_write(k.data_ptr(), v.data_ptr(), at, kt, kh, vt, vh, T, _DT[xt]))
 
     def norm_rope_write(self, q, k, v, slots, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
                         dtype=None):
@@ -183,25 +215,33 @@ class KVCache:
         dtype: of q' and, before they are quantized, of the keys; the cache's own unless that is e4m3 (then q's)."""
         d = self.device
         _, T, Hq, D, qt, qh = _heads(q, "q", _DT, d)
-        Tk, rows = self._kv(k, v, d)
-        if k.dtype != q.dtype:
-            raise ValueError(f"k has dtype {k.dtype}; q has {q.dtype}")
+        xt, Tk, kt, kh, vt, vh = self._kv(k, v)
+        if xt != q.dtype:
+            raise ValueError(f"k has dtype {xt}; q has {q.dtype}")
         if Tk != T or D != self.D:
             raise ValueError(f"q has shape {tuple(q.shape)}; k has {tuple(k.shape)}")
         if dtype is None:
-            dtype = self.dtype if self.dtype in _HALF else q.dtype
-        _tensor_type(dtype)
-        if self.dtype in _HALF and dtype != self.dtype:
-            raise ValueError(f"dtype {dtype}; the cache has {self.dtype}")
+            dtype = self.dtype if self.dtype in _HALF else xt
+        else:
+            _result_type(dtype)
+            if self.dtype in _HALF and dtype != self.dtype:
+                raise ValueError(f"dtype {dtype}; the cache has {self.dtype}")
         pos, freq, R = _rotation(positions, inv_freq, T, d)
         qw, kw, wt = _weights(q_weight, k_weight, D, d)
-        at = _vector(slots, "slots", _I32, T, d)
+        at = _vector(slots, "slots", _INT, T, d)
         o = _empty((T, Hq, D), dtype, d)
-        _call(d, lib.qmm_cache_norm_rope_write, self._h, q.data_ptr(), qt, qh, *rows, _DT[q.dtype], T, Hq, qw, kw, wt, eps, pos,
-              freq, R, int(bool(interleaved)), at, o.data_ptr(), _DT[dtype])
+        _call(d, lib.qmm_cache_norm_rope_write, self._h, _pack_heads(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), qw, kw, pos, freq, at, o.data_ptr(), 0, qt, qh, kt, kh, vt, vh, T, Hq,
+            self.heads, D, R, _DT[xt], wt, _DT[dtype], 1 if interleaved else 0, eps))
         return o
 
     def _table(self, table, B):
+        try:
+            n, W = table.shape
+            if n == B and table.dtype is _INT and table.get_device() == self.device and table.is_contiguous():
+                return table.data_ptr(), W
+        except (AttributeError, ValueError):
+            pass
         _tensor(table, "table", _I32, (2,))
         if table.shape[0] != B:
             raise ValueError(f"table has {table.shape[0]} rows; expected {B}")
@@ -215,24 +255,25 @@ class KVCache:
         B = starts.shape[0] - 1
         if B < 0:
             raise ValueError("starts is empty")
+        d = self.device
         at, W = self._table(table, B)
-        _place(self.device, (starts, "starts"))
+        first = _vector(starts, "starts", _INT, B + 1, d)
         total = int(total)
         if total < 0:
             raise ValueError(f"total={total} is negative")
         shape = (total, self.heads, self.D)
         if out is None:
             dtype = (self.dtype if self.dtype in _HALF else torch.bfloat16) if dtype is None else dtype
-            _tensor_type(dtype)
-            k, v = _empty(shape, dtype, self.device), _empty(shape, dtype, self.device)
+            _result_type(dtype)
+            k, v = _empty(shape, dtype, d), _empty(shape, dtype, d)
         else:
             k, v = out
-            _out(k, shape, None, self.device, "out[0]")
-            _out(v, shape, None, self.device, "out[1]")
+            _out(k, shape, None, d, "out[0]")
+            _out(v, shape, None, d, "out[1]")
             if v.dtype != k.dtype or dtype not in (None, k.dtype):
                 raise ValueError("out must be two tensors of one dtype, that of the call")
-        _call(self.device, lib.qmm_cache_read, self._h, at, B, W, starts.data_ptr(), total, k.data_ptr(), v.data_ptr(),
-              _DT[k.dtype])
+            dtype = k.dtype
+        _call(d, lib.qmm_cache_read, self._h, _pack_read(at, first, k.data_ptr(), v.data_ptr(), B, W, total, _DT[dtype]))
         return k, v
 
     def attend(self, q, table, lengths, scale=None, max_length=None, out=None):
@@ -242,27 +283,31 @@ class KVCache:
         is divided and nothing else."""
         d = self.device
         _, B, Hq, D, qt, qh = _heads(q, "q", _HALF, d)
+        t = q.dtype
         if D != self.D or Hq == 0 or Hq % self.heads:
             raise ValueError(f"q has {Hq} heads of {D}; the cache has {self.heads} of {self.D}")
-        if self.dtype in _HALF and q.dtype != self.dtype:
-            raise ValueError(f"q has dtype {q.dtype}; the cache has {self.dtype}")
+        if t != self.dtype and self.dtype in _HALF:
+            raise ValueError(f"q has dtype {t}; the cache has {self.dtype}")
         at, W = self._table(table, B)
-        lens = _vector(lengths, "lengths", _I32, B, d)
-        reach = W * self.page
-        bound = reach if max_length is None else min(max(int(max_length), 0), reach)
+        lens = _vector(lengths, "lengths", _INT, B, d)
+        bound = W * self.page
+        if max_length is not None and max_length < bound:
+            bound = max(int(max_length), 0)
         key = B, Hq, bound
         nb = self._sizes.get(key)
         if nb is None:
             if len(self._sizes) >= 1024:
                 self._sizes.clear()
             nb = self._sizes[key] = lib.qmm_cache_attend_workspace_bytes(self._h, B, Hq, bound)
-        o = _out(out, (B, Hq, D), q.dtype, d)
-        if o.dtype != q.dtype:
+        if out is None:
+            out = _empty((B, Hq, D), t, d)
+        elif _out(out, (B, Hq, D), None, d).dtype != t:
             raise ValueError("out must have q's dtype")
-        ws = torch.empty(nb, dtype=torch.uint8, device=o.device) if nb else None
-        _call(d, lib.qmm_cache_attend, self._h, q.data_ptr(), _DT[q.dtype], qt, qh, B, Hq, at, W, lens, bound,
-              D ** -0.5 if scale is None else scale, o.data_ptr(), ws.data_ptr() if nb else None, nb)
-        return o
+        ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+        _call(d, lib.qmm_cache_attend, self._h, _pack_attend(
+            q.data_ptr(), at, lens, out.data_ptr(), ws.data_ptr() if nb else 0, qt, qh, B, Hq, W, bound, nb, _HALF[t],
+            D ** -0.5 if scale is None else scale))
+        return out
 
 
 def attend_prompt(q, k, v, starts, k_starts=None, causal=True, scale=None, out=None):
@@ -271,23 +316,29 @@ def attend_prompt(q, k, v, starts, k_starts=None, causal=True, scale=None, out=N
     decreasing; k_starts: starts by default).  causal: query i of n sees the keys 0 .. i + m - n of its m; one that sees
     none gives zeros.  Rows of no sequence are not written: they stay as they were in `out`."""
     d, Tq, Hq, D, qt, qh = _heads(q, "q", _HALF)
-    _, Tk, H, Dk, kt, kh = _heads(k, "k", (q.dtype,), d)
-    _, Tv, Hv, Dv, vt, vh = _heads(v, "v", (q.dtype,), d)
+    t = q.dtype
+    _, Tk, H, Dk, kt, kh = _heads(k, "k", (t,), d)
+    _, Tv, Hv, Dv, vt, vh = _heads(v, "v", (t,), d)
     if Dk != D or H == 0 or Hq == 0 or Hq % H:
         raise ValueError(f"k has {H} heads of {Dk}; q has {Hq} of {D}")
-    if (Tv, Hv, Dv) != (Tk, H, Dk):
+    if Tv != Tk or Hv != H or Dv != D:
         raise ValueError(f"v has shape {tuple(v.shape)}; k has {tuple(k.shape)}")
-    k_starts = starts if k_starts is None else k_starts
     _tensor(starts, "starts", _I32, (1,))
     n = starts.shape[0]
     if n < 1:
         raise ValueError("starts is empty")
-    if k_starts is starts and Tk != Tq:
-        raise ValueError(f"{Tk} keys for {Tq} queries need k_starts")
-    qs, ks = _vector(starts, "starts", _I32, n, d), _vector(k_starts, "k_starts", _I32, n, d)
-    o = _out(out, (Tq, Hq, D), q.dtype, d)
-    if o.dtype != q.dtype:
+    qs = _vector(starts, "starts", _INT, n, d)
+    if k_starts is None or k_starts is starts:
+        if Tk != Tq:
+            raise ValueError(f"{Tk} keys for {Tq} queries need k_starts")
+        ks = qs
+    else:
+        ks = _vector(k_starts, "k_starts", _INT, n, d)
+    if out is None:
+        out = _empty((Tq, Hq, D), t, d)
+    elif _out(out, (Tq, Hq, D), None, d).dtype != t:
         raise ValueError("out must have q's dtype")
-    _call(d, lib.qmm_attend_prompt, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _DT[q.dtype], qs, ks,
-          n - 1, Tq, Tk, Hq, H, D, int(bool(causal)), D ** -0.5 if scale is None else scale, o.data_ptr())
-    return o
+    _call(d, lib.qmm_attend_prompt, _pack_prompt(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, out.data_ptr(), qt, qh, kt, kh, vt, vh, n - 1, Tq, Tk, Hq, H, D, _HALF[t],
+        1 if causal else 0, D ** -0.5 if scale is None else scale))
+    return out

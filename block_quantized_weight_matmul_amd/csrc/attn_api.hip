@@ -51,49 +51,48 @@ qmm_status check_head(int64_t D) {
   return D % 16 == 0 ? QMM_OK : fail(QMM_E_SHAPE, "D=%lld is not a multiple of 16", static_cast<ll>(D));
 }
 
-// norms and rotation: weights, angles, and the tensors that the call reads and writes
-qmm_status check_heads(const qmm::HeadsArgs& a, int xt, int64_t Hq, int64_t H, int64_t D, int64_t R) {
-  QMM_TRY(check_dtype(xt, "input"));
-  QMM_TRY(check_dtype(a.wt, "weight"));
-  QMM_TRY(check_range(a.T, 0, qmm::kMaxTokens, "T"));
-  QMM_TRY(check_range(Hq, 0, qmm::kMaxHeads, "query heads"));
-  QMM_TRY(check_range(H, 0, qmm::kMaxHeads, "key heads"));
-  if (Hq + H == 0) return fail(QMM_E_SHAPE, "no heads");
-  QMM_TRY(check_head(D));
-  if (R < 0 || R > D || R % 8) return fail(QMM_E_SHAPE, "R=%lld is not a multiple of 8 up to D", static_cast<ll>(R));
-  if (!(a.eps >= 0.0f) || a.eps > 3e38f) return fail(QMM_E_ARG, "eps must be finite and not negative");
-  if (a.interleaved != 0 && a.interleaved != 1) return fail(QMM_E_ARG, "interleaved must be 0 or 1");
-  if (a.T == 0) return QMM_OK;
-  if (Hq) QMM_TRY(check_rows(a.q, xt, "q"));
-  if (H) QMM_TRY(check_rows(a.k, xt, "k"));
-  if (R) {
-    QMM_TRY(check_ptr(a.positions, 4, "positions"));
-    QMM_TRY(check_ptr(a.inv_freq, 4, "inv_freq"));
+// norms and rotation: weights, angles, and the tensors that the call reads; *r is what the launch takes
+qmm_status check_heads(const qmm_head_args* a, qmm::HeadsArgs* r) {
+  QMM_TRY(check_dtype(a->xt, "input"));
+  QMM_TRY(check_dtype(a->wt, "weight"));
+  QMM_TRY(check_dtype(a->ot, "output"));
+  QMM_TRY(check_range(a->T, 0, qmm::kMaxTokens, "T"));
+  QMM_TRY(check_range(a->Hq, 0, qmm::kMaxHeads, "query heads"));
+  QMM_TRY(check_range(a->H, 0, qmm::kMaxHeads, "key heads"));
+  if (a->Hq + a->H == 0) return fail(QMM_E_SHAPE, "no heads");
+  QMM_TRY(check_head(a->D));
+  if (a->R < 0 || a->R > a->D || a->R % 8)
+    return fail(QMM_E_SHAPE, "R=%lld is not a multiple of 8 up to D", static_cast<ll>(a->R));
+  if (!(a->eps >= 0.0f) || a->eps > 3e38f) return fail(QMM_E_ARG, "eps must be finite and not negative");
+  if (a->interleaved != 0 && a->interleaved != 1) return fail(QMM_E_ARG, "interleaved must be 0 or 1");
+  if (a->T == 0) return QMM_OK;
+  r->q = {a->q, a->q_token, a->q_head};
+  r->k = {a->k, a->k_token, a->k_head};
+  if (a->Hq) {
+    QMM_TRY(check_rows(r->q, a->xt, "q"));
+    QMM_TRY(check_ptr(a->q_out, size_of(a->ot), "q_out"));
   }
-  if (a.qw && !aligned(a.qw, size_of(a.wt))) return fail(QMM_E_ALIGN, "q_weight must be element-aligned");
-  if (a.kw && !aligned(a.kw, size_of(a.wt))) return fail(QMM_E_ALIGN, "k_weight must be element-aligned");
+  if (a->H) QMM_TRY(check_rows(r->k, a->xt, "k"));
+  if (a->R) {
+    QMM_TRY(check_ptr(a->positions, 4, "positions"));
+    QMM_TRY(check_ptr(a->inv_freq, 4, "inv_freq"));
+  }
+  if (a->q_weight && !aligned(a->q_weight, size_of(a->wt))) return fail(QMM_E_ALIGN, "q_weight must be element-aligned");
+  if (a->k_weight && !aligned(a->k_weight, size_of(a->wt))) return fail(QMM_E_ALIGN, "k_weight must be element-aligned");
+  r->T = a->T;
+  r->Hq = static_cast<int>(a->Hq);
+  r->H = static_cast<int>(a->H);
+  r->D = static_cast<int>(a->D);
+  r->R = static_cast<int>(a->R);
+  r->positions = a->positions;
+  r->inv_freq = a->R ? a->inv_freq : nullptr;
+  r->qw = a->q_weight;
+  r->kw = a->k_weight;
+  r->wt = a->wt;
+  r->eps = a->eps;
+  r->interleaved = a->interleaved;
+  r->qo = a->q_out;
   return QMM_OK;
-}
-
-qmm::HeadsArgs heads_args(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh, int64_t T,
-                          int64_t Hq, int64_t H, int64_t D, const void* qw, const void* kw, int wt, float eps,
-                          const int32_t* positions, const float* inv_freq, int64_t R, int interleaved) {
-  qmm::HeadsArgs a{};
-  a.q = {q, q_st, q_sh};
-  a.k = {k, k_st, k_sh};
-  a.T = T;
-  a.Hq = static_cast<int>(Hq);
-  a.H = static_cast<int>(H);
-  a.D = static_cast<int>(D);
-  a.R = static_cast<int>(R);
-  a.positions = positions;
-  a.inv_freq = R ? inv_freq : nullptr;
-  a.qw = qw;
-  a.kw = kw;
-  a.wt = wt;
-  a.eps = eps;
-  a.interleaved = interleaved;
-  return a;
 }
 
 qmm_status check_scale(float scale) {
@@ -165,76 +164,63 @@ qmm_status qmm_cache_destroy(qmm_cache* h) {
   return ok();
 }
 
-qmm_status qmm_cache_write(const qmm_cache* h, const void* k, int64_t k_st, int64_t k_sh, const void* v, int64_t v_st,
-                           int64_t v_sh, qmm_dtype xt, int64_t T, const int32_t* slots, qmm_stream_t stream) {
-  if (!h) return fail(QMM_E_ARG, "handle is NULL");
-  QMM_TRY(check_dtype(xt, "input"));
-  QMM_TRY(check_range(T, 0, qmm::kMaxTokens, "T"));
-  if (T == 0) return ok();
-  const HeadRows kr{k, k_st, k_sh}, vr{v, v_st, v_sh};
-  QMM_TRY(check_rows(kr, xt, "k"));
-  QMM_TRY(check_rows(vr, xt, "v"));
-  QMM_TRY(check_ptr(slots, 4, "slots"));
+qmm_status qmm_cache_write(const qmm_cache* h, const qmm_cache_write_args* a, qmm_stream_t stream) {
+  if (!h || !a) return fail(QMM_E_ARG, "%s is NULL", h ? "a" : "handle");
+  QMM_TRY(check_dtype(a->xt, "input"));
+  QMM_TRY(check_range(a->T, 0, qmm::kMaxTokens, "T"));
+  if (a->T == 0) return ok();
+  const HeadRows k{a->k, a->k_token, a->k_head}, v{a->v, a->v_token, a->v_head};
+  QMM_TRY(check_rows(k, a->xt, "k"));
+  QMM_TRY(check_rows(v, a->xt, "v"));
+  QMM_TRY(check_ptr(a->slots, 4, "slots"));
   QMM_TRY(check_device(h));
-  const hipError_t e = qmm::launch_cache_write(h->d, kr, vr, xt, T, slots, stream_of(stream));
+  const hipError_t e = qmm::launch_cache_write(h->d, k, v, a->xt, a->T, a->slots, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "cache write launch");
 }
 
-qmm_status qmm_cache_read(const qmm_cache* h, const int32_t* table, int64_t B, int64_t W, const int32_t* starts,
-                          int64_t total, void* k, void* v, qmm_dtype ot, qmm_stream_t stream) {
-  if (!h) return fail(QMM_E_ARG, "handle is NULL");
-  QMM_TRY(check_dtype(ot, "output"));
-  QMM_TRY(check_range(B, 0, 1 << 20, "B"));
-  QMM_TRY(check_range(W, 0, qmm::kMaxTokens, "table columns"));
-  QMM_TRY(check_range(total, 0, qmm::kMaxTokens, "total"));
-  if (total == 0 || B == 0) return ok();
-  if (W) QMM_TRY(check_ptr(table, 4, "table"));
-  QMM_TRY(check_ptr(starts, 4, "starts"));
-  QMM_TRY(check_ptr(k, size_of(ot), "k"));
-  QMM_TRY(check_ptr(v, size_of(ot), "v"));
+qmm_status qmm_cache_read(const qmm_cache* h, const qmm_cache_read_args* a, qmm_stream_t stream) {
+  if (!h || !a) return fail(QMM_E_ARG, "%s is NULL", h ? "a" : "handle");
+  QMM_TRY(check_dtype(a->ot, "output"));
+  QMM_TRY(check_range(a->B, 0, 1 << 20, "B"));
+  QMM_TRY(check_range(a->W, 0, qmm::kMaxTokens, "table columns"));
+  QMM_TRY(check_range(a->total, 0, qmm::kMaxTokens, "total"));
+  if (a->total == 0 || a->B == 0) return ok();
+  if (a->W) QMM_TRY(check_ptr(a->table, 4, "table"));
+  QMM_TRY(check_ptr(a->starts, 4, "starts"));
+  QMM_TRY(check_ptr(a->k, size_of(a->ot), "k"));
+  QMM_TRY(check_ptr(a->v, size_of(a->ot), "v"));
   QMM_TRY(check_device(h));
-  const hipError_t e = qmm::launch_cache_read(h->d, table, B, W, starts, total, k, v, ot, stream_of(stream));
+  const hipError_t e = qmm::launch_cache_read(h->d, a->table, a->B, a->W, a->starts, a->total, a->k, a->v, a->ot, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "cache read launch");
 }
 
-qmm_status qmm_head_norm_rope(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh,
-                              qmm_dtype xt, int64_t T, int64_t Hq, int64_t H, int64_t D, const void* q_weight,
-                              const void* k_weight, qmm_dtype wt, float eps, const int32_t* positions, const float* inv_freq,
-                              int64_t R, int interleaved, void* q_out, void* k_out, qmm_dtype ot, qmm_stream_t stream) {
-  qmm::HeadsArgs a = heads_args(q, q_st, q_sh, k, k_st, k_sh, T, Hq, H, D, q_weight, k_weight, wt, eps, positions, inv_freq, R,
-                                interleaved);
-  QMM_TRY(check_heads(a, xt, Hq, H, D, R));
-  QMM_TRY(check_dtype(ot, "output"));
-  if (T == 0) return ok();
-  if (Hq) QMM_TRY(check_ptr(q_out, size_of(ot), "q_out"));
-  if (H) QMM_TRY(check_ptr(k_out, size_of(ot), "k_out"));
-  a.qo = q_out;
-  a.ko = k_out;
-  const hipError_t e = qmm::launch_heads(a, xt, ot, stream_of(stream));
+qmm_status qmm_head_norm_rope(const qmm_head_args* a, qmm_stream_t stream) {
+  if (!a) return fail(QMM_E_ARG, "a is NULL");
+  qmm::HeadsArgs r{};
+  QMM_TRY(check_heads(a, &r));
+  if (a->T == 0) return ok();
+  if (a->H) QMM_TRY(check_ptr(a->k_out, size_of(a->ot), "k_out"));
+  r.ko = a->k_out;
+  const hipError_t e = qmm::launch_heads(r, a->xt, a->ot, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "head norm launch");
 }
 
-qmm_status qmm_cache_norm_rope_write(const qmm_cache* h, const void* q, int64_t q_st, int64_t q_sh, const void* k,
-                                     int64_t k_st, int64_t k_sh, const void* v, int64_t v_st, int64_t v_sh, qmm_dtype xt,
-                                     int64_t T, int64_t Hq, const void* q_weight, const void* k_weight, qmm_dtype wt,
-                                     float eps, const int32_t* positions, const float* inv_freq, int64_t R, int interleaved,
-                                     const int32_t* slots, void* q_out, qmm_dtype ot, qmm_stream_t stream) {
-  if (!h) return fail(QMM_E_ARG, "handle is NULL");
-  qmm::HeadsArgs a = heads_args(q, q_st, q_sh, k, k_st, k_sh, T, Hq, h->d.heads, h->d.D, q_weight, k_weight, wt, eps, positions,
-                                inv_freq, R, interleaved);
-  QMM_TRY(check_heads(a, xt, Hq, h->d.heads, h->d.D, R));
-  QMM_TRY(check_dtype(ot, "output"));
-  if (h->d.type != QMM_E4M3 && ot != h->d.type) return fail(QMM_E_TYPE, "a 16-bit cache gives queries of its own type");
-  if (T == 0) return ok();
-  a.v = {v, v_st, v_sh};
-  QMM_TRY(check_rows(a.v, xt, "v"));
-  QMM_TRY(check_ptr(slots, 4, "slots"));
-  if (Hq) QMM_TRY(check_ptr(q_out, size_of(ot), "q_out"));
+qmm_status qmm_cache_norm_rope_write(const qmm_cache* h, const qmm_head_args* a, qmm_stream_t stream) {
+  if (!h || !a) return fail(QMM_E_ARG, "%s is NULL", h ? "a" : "handle");
+  qmm::HeadsArgs r{};
+  QMM_TRY(check_heads(a, &r));
+  if (a->H != h->d.heads || a->D != h->d.D)
+    return fail(QMM_E_SHAPE, "%lld key heads of %lld; the cache has %d of %d", static_cast<ll>(a->H), static_cast<ll>(a->D),
+                h->d.heads, h->d.D);
+  if (h->d.type != QMM_E4M3 && a->ot != h->d.type) return fail(QMM_E_TYPE, "a 16-bit cache gives queries of its own type");
+  if (a->T == 0) return ok();
+  r.v = {a->v, a->v_token, a->v_head};
+  QMM_TRY(check_rows(r.v, a->xt, "v"));
+  QMM_TRY(check_ptr(a->slots, 4, "slots"));
   QMM_TRY(check_device(h));
-  a.cache = h->d;
-  a.slots = slots;
-  a.qo = q_out;
-  const hipError_t e = qmm::launch_heads(a, xt, ot, stream_of(stream));
+  r.cache = h->d;
+  r.slots = a->slots;
+  const hipError_t e = qmm::launch_heads(r, a->xt, a->ot, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "head norm launch");
 }
 
@@ -243,84 +229,81 @@ size_t qmm_cache_attend_workspace_bytes(const qmm_cache* h, int64_t B, int64_t H
   return attend_bytes(h->d, B, Hq, qmm::attend_split(h->d, B, static_cast<int>(Hq), max_length).splits);
 }
 
-qmm_status qmm_cache_attend(const qmm_cache* h, const void* q, qmm_dtype qt, int64_t q_sb, int64_t q_sh, int64_t B, int64_t Hq,
-                            const int32_t* table, int64_t W, const int32_t* lengths, int64_t max_length, float scale,
-                            void* out, void* ws, size_t ws_bytes, qmm_stream_t stream) {
-  QMM_TRY(check_attend(h, B, Hq, max_length));
-  if (qt != QMM_F16 && qt != QMM_BF16) return fail(QMM_E_TYPE, "queries are fp16 or bf16 (got %d)", qt);
-  if (h->d.type != QMM_E4M3 && qt != h->d.type) return fail(QMM_E_TYPE, "a 16-bit cache takes queries of its own type");
-  QMM_TRY(check_range(W, 0, qmm::kMaxTokens >> h->d.shift, "table columns"));
-  QMM_TRY(check_scale(scale));
-  if (B == 0) return ok();
-  const HeadRows rows{q, q_sb, q_sh};
-  QMM_TRY(check_rows(rows, qt, "q"));
-  if (W) QMM_TRY(check_ptr(table, 4, "table"));
-  QMM_TRY(check_ptr(lengths, 4, "lengths"));
-  QMM_TRY(check_ptr(out, size_of(qt), "out"));
-  qmm::AttendArgs a{};
-  const qmm::AttendSplit split = qmm::attend_split(h->d, B, static_cast<int>(Hq), max_length);
-  a.splits = split.splits;
-  a.piece = split.piece;
-  QMM_TRY(check_ws(ws, ws_bytes, attend_bytes(h->d, B, Hq, a.splits), "ws"));
+qmm_status qmm_cache_attend(const qmm_cache* h, const qmm_attend_args* a, qmm_stream_t stream) {
+  if (!a) return fail(QMM_E_ARG, "a is NULL");
+  QMM_TRY(check_attend(h, a->B, a->Hq, a->max_length));
+  if (a->qt != QMM_F16 && a->qt != QMM_BF16) return fail(QMM_E_TYPE, "queries are fp16 or bf16 (got %d)", a->qt);
+  if (h->d.type != QMM_E4M3 && a->qt != h->d.type) return fail(QMM_E_TYPE, "a 16-bit cache takes queries of its own type");
+  QMM_TRY(check_range(a->W, 0, qmm::kMaxTokens >> h->d.shift, "table columns"));
+  QMM_TRY(check_scale(a->scale));
+  if (a->B == 0) return ok();
+  qmm::AttendArgs r{};
+  r.q = {a->q, a->q_token, a->q_head};
+  QMM_TRY(check_rows(r.q, a->qt, "q"));
+  if (a->W) QMM_TRY(check_ptr(a->table, 4, "table"));
+  QMM_TRY(check_ptr(a->lengths, 4, "lengths"));
+  QMM_TRY(check_ptr(a->out, size_of(a->qt), "out"));
+  const qmm::AttendSplit split = qmm::attend_split(h->d, a->B, static_cast<int>(a->Hq), a->max_length);
+  QMM_TRY(check_ws(a->ws, a->ws_bytes, attend_bytes(h->d, a->B, a->Hq, split.splits), "ws"));
   QMM_TRY(check_device(h));
-  a.cache = h->d;
-  a.q = rows;
-  a.B = B;
-  a.Hq = static_cast<int>(Hq);
-  a.table = table;
-  a.W = W;
-  a.lengths = lengths;
-  a.scale = scale;
-  a.out = out;
-  a.ws = static_cast<float*>(ws);
-  const hipError_t e = qmm::launch_attend(a, qt, stream_of(stream));
+  r.cache = h->d;
+  r.B = a->B;
+  r.Hq = static_cast<int>(a->Hq);
+  r.table = a->table;
+  r.W = a->W;
+  r.lengths = a->lengths;
+  r.scale = a->scale;
+  r.out = a->out;
+  r.splits = split.splits;
+  r.piece = split.piece;
+  r.ws = static_cast<float*>(a->ws);
+  const hipError_t e = qmm::launch_attend(r, a->qt, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "attend launch");
 }
 
-qmm_status qmm_attend_prompt(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh,
-                             const void* v, int64_t v_st, int64_t v_sh, qmm_dtype dt, const int32_t* q_starts,
-                             const int32_t* k_starts, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t H, int64_t D,
-                             int causal, float scale, void* out, qmm_stream_t stream) {
-  if (dt != QMM_F16 && dt != QMM_BF16) return fail(QMM_E_TYPE, "prompts are fp16 or bf16 (got %d)", dt);
-  QMM_TRY(check_range(B, 0, 1 << 20, "B"));
-  QMM_TRY(check_range(Tq, 0, qmm::kMaxTokens, "queries"));
-  QMM_TRY(check_range(Tk, 0, qmm::kMaxTokens, "keys"));
-  QMM_TRY(check_range(H, 1, qmm::kMaxHeads, "key heads"));
-  QMM_TRY(check_range(Hq, 1, 8192, "query heads"));
-  if (Hq % H) return fail(QMM_E_SHAPE, "%lld query heads are no multiple of %lld key heads", static_cast<ll>(Hq), static_cast<ll>(H));
-  QMM_TRY(check_head(D));
-  if (causal != 0 && causal != 1) return fail(QMM_E_ARG, "causal must be 0 or 1");
-  QMM_TRY(check_scale(scale));
-  if (B == 0 || Tq == 0) return ok();
-  qmm::PromptArgs a{};
-  a.q = {q, q_st, q_sh};
-  a.k = {k, k_st, k_sh};
-  a.v = {v, v_st, v_sh};
-  QMM_TRY(check_rows(a.q, dt, "q"));
-  if (Tk) {
-    for (HeadRows* r : {&a.k, &a.v}) {
-      const char* what = r == &a.k ? "k" : "v";
-      QMM_TRY(check_rows(*r, dt, what));
-      if (Tk == 1) r->st = D;
-      if (r->st < D || r->st > (1 << 23)) return fail(QMM_E_SHAPE, "the token stride of %s is outside [D, 2^23]", what);
-      if (!aligned(r->p, 16) || r->st % 8 || r->sh % 8) return fail(QMM_E_ALIGN, "rows of %s must be 16-byte aligned", what);
+qmm_status qmm_attend_prompt(const qmm_prompt_args* a, qmm_stream_t stream) {
+  if (!a) return fail(QMM_E_ARG, "a is NULL");
+  if (a->dt != QMM_F16 && a->dt != QMM_BF16) return fail(QMM_E_TYPE, "prompts are fp16 or bf16 (got %d)", a->dt);
+  QMM_TRY(check_range(a->B, 0, 1 << 20, "B"));
+  QMM_TRY(check_range(a->Tq, 0, qmm::kMaxTokens, "queries"));
+  QMM_TRY(check_range(a->Tk, 0, qmm::kMaxTokens, "keys"));
+  QMM_TRY(check_range(a->H, 1, qmm::kMaxHeads, "key heads"));
+  QMM_TRY(check_range(a->Hq, 1, 8192, "query heads"));
+  if (a->Hq % a->H)
+    return fail(QMM_E_SHAPE, "%lld query heads are no multiple of %lld key heads", static_cast<ll>(a->Hq), static_cast<ll>(a->H));
+  QMM_TRY(check_head(a->D));
+  if (a->causal != 0 && a->causal != 1) return fail(QMM_E_ARG, "causal must be 0 or 1");
+  QMM_TRY(check_scale(a->scale));
+  if (a->B == 0 || a->Tq == 0) return ok();
+  qmm::PromptArgs r{};
+  r.q = {a->q, a->q_token, a->q_head};
+  r.k = {a->k, a->k_token, a->k_head};
+  r.v = {a->v, a->v_token, a->v_head};
+  QMM_TRY(check_rows(r.q, a->dt, "q"));
+  if (a->Tk) {
+    for (HeadRows* x : {&r.k, &r.v}) {
+      const char* what = x == &r.k ? "k" : "v";
+      QMM_TRY(check_rows(*x, a->dt, what));
+      if (a->Tk == 1) x->st = a->D;
+      if (x->st < a->D || x->st > (1 << 23)) return fail(QMM_E_SHAPE, "the token stride of %s is outside [D, 2^23]", what);
+      if (!aligned(x->p, 16) || x->st % 8 || x->sh % 8) return fail(QMM_E_ALIGN, "rows of %s must be 16-byte aligned", what);
     }
   }
-  QMM_TRY(check_ptr(q_starts, 4, "q_starts"));
-  QMM_TRY(check_ptr(k_starts, 4, "k_starts"));
-  QMM_TRY(check_ptr(out, size_of(dt), "out"));
-  a.B = B;
-  a.Tq = Tq;
-  a.Tk = Tk;
-  a.Hq = static_cast<int>(Hq);
-  a.H = static_cast<int>(H);
-  a.D = static_cast<int>(D);
-  a.q_starts = q_starts;
-  a.k_starts = k_starts;
-  a.causal = causal;
-  a.scale = scale;
-  a.out = out;
-  const hipError_t e = qmm::launch_prompt(a, dt, stream_of(stream));
+  QMM_TRY(check_ptr(a->q_starts, 4, "q_starts"));
+  QMM_TRY(check_ptr(a->k_starts, 4, "k_starts"));
+  QMM_TRY(check_ptr(a->out, size_of(a->dt), "out"));
+  r.B = a->B;
+  r.Tq = a->Tq;
+  r.Tk = a->Tk;
+  r.Hq = static_cast<int>(a->Hq);
+  r.H = static_cast<int>(a->H);
+  r.D = static_cast<int>(a->D);
+  r.q_starts = a->q_starts;
+  r.k_starts = a->k_starts;
+  r.causal = a->causal;
+  r.scale = a->scale;
+  r.out = a->out;
+  const hipError_t e = qmm::launch_prompt(r, a->dt, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "prompt launch");
 }
 

@@ -572,10 +572,12 @@ qmm_status qmm_route_combine_backward(const void *y, qmm_dtype yt, const void *w
  * -----------------------------------------
  * Norms and rotation of the query and key heads, a paged key-value cache, and attention over
  * it and over prompts.  Inputs x [T, heads, D] are given with the strides of a token and of a
- * head in elements (the last axis is contiguous), so that slices of one projection's output are
- * taken as they are; outputs are contiguous.  D is a multiple of 16, 16..256; T up to 2^30.
- * Serving: no gradients.  Conventions are those at the top of this file; a call with nothing
- * to compute (T = 0, B = 0) returns QMM_OK without looking at its pointers.
+ * head in elements (`q_token`, `q_head` and so on; the last axis is contiguous), so that slices
+ * of one projection's output are taken as they are; outputs are contiguous.  D is a multiple of
+ * 16, 16..256; T up to 2^30.  Serving: no gradients.  The calls take their arguments in a struct
+ * in HOST memory, which is read during the call only.  Conventions are those at the top of this
+ * file; a call with nothing to compute (T = 0, B = 0) returns QMM_OK without looking at its
+ * pointers.
  *
  * qmm_head_norm_rope -- queries q [T, Hq, D] and keys k [T, H, D] (type xt; Hq or H may be 0):
  *   y = x / sqrt(mean(x^2) + eps) * w     over each head (not where the weight is NULL)
@@ -587,15 +589,22 @@ qmm_status qmm_route_combine_backward(const void *y, qmm_dtype yt, const void *w
  *   interleaved  0: pair i is columns i and i + R / 2; 1: columns 2 i and 2 i + 1.
  *   q_out, k_out  DEVICE, contiguous, type ot, element-aligned; may be q and k themselves
  *              where those are contiguous and of type ot.
- * Sums are fp32, angles 64-bit; one rounding to ot.
+ * Sums are fp32, angles 64-bit; one rounding to ot.  v and slots are not looked at.
  */
-qmm_status qmm_head_norm_rope(const void *q, int64_t q_token, int64_t q_head, const void *k,
-                              int64_t k_token, int64_t k_head, qmm_dtype xt, int64_t T,
-                              int64_t Hq, int64_t H, int64_t D, const void *q_weight,
-                              const void *k_weight, qmm_dtype wt, float eps,
-                              const int32_t *positions, const float *inv_freq, int64_t R,
-                              int interleaved, void *q_out, void *k_out, qmm_dtype ot,
-                              qmm_stream_t stream);
+typedef struct {
+  const void *q, *k, *v;
+  const void *q_weight, *k_weight;
+  const int32_t *positions;
+  const float *inv_freq;
+  const int32_t *slots;
+  void *q_out, *k_out;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  int64_t T, Hq, H, D, R;
+  int32_t xt, wt, ot; /* qmm_dtype */
+  int32_t interleaved;
+  float eps;
+} qmm_head_args;
+qmm_status qmm_head_norm_rope(const qmm_head_args *a, qmm_stream_t stream);
 
 /*
  * qmm_cache_create / qmm_cache_destroy -- describe a paged key-value cache (as qmm_create).
@@ -624,8 +633,8 @@ qmm_status qmm_cache_destroy(qmm_cache *h);
  *          The slots of a call are distinct: of two tokens with one slot it is not specified
  *          which is left there, nor that all parts left are of the same one.
  * qmm_cache_norm_rope_write -- qmm_head_norm_rope of q and k, then qmm_cache_write of the keys
- * (as rounded to ot) and of v, in one launch and with the same bits.  ot is the cache's type
- * unless that is e4m3.
+ * (as rounded to ot) and of v [T, H, D], in one launch and with the same bits.  H and D are the
+ * cache's, ot is its type unless that is e4m3; k_out is not looked at.
  * qmm_cache_read -- B sequences from the cache, packed one after another: sequence b's tokens 0,
  * 1, .. become rows starts[b] .. starts[b + 1] - 1 of k and v [total, heads, D] (type ot,
  * contiguous, element-aligned).
@@ -633,20 +642,23 @@ qmm_status qmm_cache_destroy(qmm_cache *h);
  *           are left as they were.
  * A token whose table entry names no page, or that lies past the table's columns, gives NaN.
  */
-qmm_status qmm_cache_write(const qmm_cache *h, const void *k, int64_t k_token, int64_t k_head,
-                           const void *v, int64_t v_token, int64_t v_head, qmm_dtype xt,
-                           int64_t T, const int32_t *slots, qmm_stream_t stream);
-qmm_status qmm_cache_norm_rope_write(const qmm_cache *h, const void *q, int64_t q_token,
-                                     int64_t q_head, const void *k, int64_t k_token,
-                                     int64_t k_head, const void *v, int64_t v_token,
-                                     int64_t v_head, qmm_dtype xt, int64_t T, int64_t Hq,
-                                     const void *q_weight, const void *k_weight, qmm_dtype wt,
-                                     float eps, const int32_t *positions, const float *inv_freq,
-                                     int64_t R, int interleaved, const int32_t *slots,
-                                     void *q_out, qmm_dtype ot, qmm_stream_t stream);
-qmm_status qmm_cache_read(const qmm_cache *h, const int32_t *table, int64_t B, int64_t W,
-                          const int32_t *starts, int64_t total, void *k, void *v, qmm_dtype ot,
-                          qmm_stream_t stream);
+typedef struct {
+  const void *k, *v;
+  const int32_t *slots;
+  int64_t k_token, k_head, v_token, v_head;
+  int64_t T;
+  int32_t xt; /* qmm_dtype */
+} qmm_cache_write_args;
+typedef struct {
+  const int32_t *table, *starts;
+  void *k, *v;
+  int64_t B, W, total;
+  int32_t ot; /* qmm_dtype */
+} qmm_cache_read_args;
+qmm_status qmm_cache_write(const qmm_cache *h, const qmm_cache_write_args *a, qmm_stream_t stream);
+qmm_status qmm_cache_norm_rope_write(const qmm_cache *h, const qmm_head_args *a,
+                                     qmm_stream_t stream);
+qmm_status qmm_cache_read(const qmm_cache *h, const qmm_cache_read_args *a, qmm_stream_t stream);
 
 /*
  * qmm_cache_attend -- attention of one new token per sequence over the cache:
@@ -667,12 +679,19 @@ qmm_status qmm_cache_read(const qmm_cache *h, const int32_t *table, int64_t B, i
  * holds past a sequence's last token has no influence, whatever it is.  A row whose scores are all
  * -inf is zeros; an infinite value gives NaN.
  */
+typedef struct {
+  const void *q;
+  const int32_t *table, *lengths;
+  void *out, *ws;
+  int64_t q_token, q_head;
+  int64_t B, Hq, W, max_length;
+  uint64_t ws_bytes;
+  int32_t qt; /* qmm_dtype */
+  float scale;
+} qmm_attend_args;
 size_t qmm_cache_attend_workspace_bytes(const qmm_cache *h, int64_t B, int64_t Hq,
                                         int64_t max_length);
-qmm_status qmm_cache_attend(const qmm_cache *h, const void *q, qmm_dtype qt, int64_t q_token,
-                            int64_t q_head, int64_t B, int64_t Hq, const int32_t *table, int64_t W,
-                            const int32_t *lengths, int64_t max_length, float scale, void *out,
-                            void *ws, size_t ws_bytes, qmm_stream_t stream);
+qmm_status qmm_cache_attend(const qmm_cache *h, const qmm_attend_args *a, qmm_stream_t stream);
 
 /*
  * qmm_attend_prompt -- attention of B packed sequences: queries q [Tq, Hq, D], keys and values
@@ -687,12 +706,17 @@ qmm_status qmm_cache_attend(const qmm_cache *h, const void *q, qmm_dtype qt, int
  * does not see has no influence on it, whatever it holds.  A row whose scores are all -inf is
  * zeros.
  */
-qmm_status qmm_attend_prompt(const void *q, int64_t q_token, int64_t q_head, const void *k,
-                             int64_t k_token, int64_t k_head, const void *v, int64_t v_token,
-                             int64_t v_head, qmm_dtype dt, const int32_t *q_starts,
-                             const int32_t *k_starts, int64_t B, int64_t Tq, int64_t Tk,
-                             int64_t Hq, int64_t H, int64_t D, int causal, float scale, void *out,
-                             qmm_stream_t stream);
+typedef struct {
+  const void *q, *k, *v;
+  const int32_t *q_starts, *k_starts;
+  void *out;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  int64_t B, Tq, Tk, Hq, H, D;
+  int32_t dt; /* qmm_dtype */
+  int32_t causal;
+  float scale;
+} qmm_prompt_args;
+qmm_status qmm_attend_prompt(const qmm_prompt_args *a, qmm_stream_t stream);
 
 /* qmm_tile_for_tokens -- 64 when a 64-token tile pads no more tokens than a
  * 32-token tile, else 32 (candle pull request, section "Where the 64-token tile

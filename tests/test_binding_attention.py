@@ -2,6 +2,7 @@
 them are refused for their placement, before a C call) and the C ABI's checks before it looks for a device."""
 
 import ctypes
+import struct
 
 import pytest
 import torch
@@ -109,92 +110,86 @@ def test_c_cache_create_errors():
     assert L.lib.qmm_cache_destroy(None) == 0
 
 
+def refusals(call, layout, good):
+    """refused(changes, status): the call with some of the struct's fields changed."""
+    def refused(changes, status):
+        args = dict(good)
+        args.update(changes)
+        assert call(struct.pack(layout, *args.values()), None) == status, changes
+    return refused
+
+
+HEADS = ("q k v q_weight k_weight positions inv_freq slots q_out k_out q_token q_head k_token k_head v_token v_head "
+         "T Hq H D R xt wt ot interleaved eps").split()
+PROMPT = "q k v q_starts k_starts out q_token q_head k_token k_head v_token v_head B Tq Tk Hq H D dt causal scale".split()
+
+
 def test_c_null_handles():
     c = Calls()
-    p, lib = c.p, L.lib
-    assert lib.qmm_cache_write(None, p, 64, 32, p, 64, 32, 0, 3, p, None) == -1
-    assert lib.qmm_cache_read(None, p, 1, 1, p, 3, p, p, 1, None) == -1
-    assert lib.qmm_cache_attend(None, p, 1, 64, 32, 1, 2, p, 1, p, 16, 1.0, p, None, 0, None) == -1
+    lib, a = L.lib, ctypes.string_at(c.p, 256)
+    assert lib.qmm_cache_write(None, a, None) == -1
+    assert lib.qmm_cache_read(None, a, None) == -1
+    assert lib.qmm_cache_attend(None, a, None) == -1
+    assert lib.qmm_cache_norm_rope_write(None, a, None) == -1
     assert lib.qmm_cache_attend_workspace_bytes(None, 1, 2, 16) == 0
-    assert lib.qmm_cache_norm_rope_write(None, p, 64, 32, p, 64, 32, p, 64, 32, 0, 3, 2, None, None, 0, 1e-6, None, None, 0, 0, p,
-                                         p, 1, None) == -1
+    assert lib.qmm_head_norm_rope(None, None) == -1
+    assert lib.qmm_attend_prompt(None, None) == -1
 
 
 def test_c_head_errors():
-    c = Calls()
-    p = c.p
-    #       q  st  sh  k  st  sh xt T  Hq H  D  qw    kw    wt eps   pos fr R  int qo ko ot stream
-    good = [p, 64, 32, p, 64, 32, 0, 3, 2, 2, 32, None, None, 0, 1e-6, p, p, 32, 0, p, p, 1, None]
-
-    def refused(at, value, status):
-        args = list(good)
-        args[at] = value
-        assert L.lib.qmm_head_norm_rope(*args) == status, (at, value)
-
-    for at in (0, 3, 15, 16, 19, 20):
-        refused(at, None, -1)
-    for at in (0, 3, 15, 16):
-        refused(at, p + 2, -4)
-    for at in (11, 12):
-        refused(at, p + 1, -4)
-    for at in (1, 2, 4, 5):
-        refused(at, -1, -3)
-        refused(at, 1 << 41, -3)
-    for at in (6, 13, 21):
-        refused(at, 3, -2)
-    for at, values in ((7, (-1, 1 << 31)), (8, (-1, 1025)), (9, (-1, 1025)), (10, (0, 24, 272)), (17, (-8, 4, 40))):
+    p = Calls().p
+    good = dict(zip(HEADS, [p, p, 0, 0, 0, p, p, 0, p, p, 64, 32, 64, 32, 0, 0, 3, 2, 2, 32, 32, 0, 0, 1, 0, 1e-6]))
+    refused = refusals(L.lib.qmm_head_norm_rope, "21q4if4x", good)
+    for n in ("q", "k", "positions", "inv_freq", "q_out", "k_out"):
+        refused({n: 0}, -1)
+    for n in ("q", "k", "positions", "inv_freq"):
+        refused({n: p + 2}, -4)
+    for n in ("q_weight", "k_weight", "q_out", "k_out"):
+        refused({n: p + 1}, -4)
+    for n in ("q_token", "q_head", "k_token", "k_head"):
+        refused({n: -1}, -3)
+        refused({n: 1 << 41}, -3)
+    for n in ("xt", "wt", "ot"):
+        refused({n: 3}, -2)
+        refused({n: -1}, -2)
+    for n, values in (("T", (-1, 1 << 31)), ("Hq", (-1, 1025)), ("H", (-1, 1025)), ("D", (0, 24, 272)), ("R", (-8, 4, 40))):
         for v in values:
-            refused(at, v, -3)
-    refused(14, -1.0, -1)
-    refused(14, float("nan"), -1)
-    refused(14, float("inf"), -1)
-    refused(18, 2, -1)
-    args = list(good)
-    args[8] = args[9] = 0
-    assert L.lib.qmm_head_norm_rope(*args) == -3
-    args = [None] * 6 + good[6:]
-    args[1] = args[2] = args[4] = args[5] = 0
-    args[7] = 0
-    assert L.lib.qmm_head_norm_rope(*args) == 0  # no tokens: nothing is looked at
+            refused({n: v}, -3)
+    for v in (-1.0, float("nan"), float("inf")):
+        refused({"eps": v}, -1)
+    refused({"interleaved": 2}, -1)
+    refused({"Hq": 0, "H": 0}, -3)
+    refused({"T": 0, "q": 0, "k": 0, "positions": 0, "inv_freq": 0, "q_out": 0, "k_out": 0}, 0)  # nothing to look at
 
 
 def test_c_prompt_errors():
-    c = Calls()
-    p = c.p
-    #       q  st  sh  k  st  sh  v  st  sh  dt qs ks B  Tq Tk Hq H  D causal scale out stream
-    good = [p, 64, 32, p, 64, 32, p, 64, 32, 1, p, p, 1, 3, 3, 2, 2, 32, 1, 0.2, p, None]
-
-    def refused(at, value, status):
-        args = list(good)
-        args[at] = value
-        assert L.lib.qmm_attend_prompt(*args) == status, (at, value)
-
-    for at in (0, 3, 6, 10, 11, 20):
-        refused(at, None, -1)
-    for at in (3, 6):
-        refused(at, p + 8, -4)
-    for at in (4, 5, 7, 8):
-        refused(at, 68, -4)
-    for at in (4, 7):
-        refused(at, 16, -3)
-        refused(at, 1 << 24, -3)
-    for at in (1, 2, 4, 5, 7, 8):
-        refused(at, -8, -3)
+    p = Calls().p
+    good = dict(zip(PROMPT, [p, p, p, p, p, p, 64, 32, 64, 32, 64, 32, 1, 3, 3, 2, 2, 32, 1, 1, 0.2]))
+    refused = refusals(L.lib.qmm_attend_prompt, "18q2if4x", good)
+    for n in ("q", "k", "v", "q_starts", "k_starts", "out"):
+        refused({n: 0}, -1)
+        refused({n: p + 1}, -4)
+    for n in ("k", "v"):
+        refused({n: p + 8}, -4)
+    for n in ("k_token", "k_head", "v_token", "v_head"):
+        refused({n: 68}, -4)
+    for n in ("k_token", "v_token"):
+        refused({n: 16}, -3)
+        refused({n: 1 << 24}, -3)
+    for n in ("q_token", "q_head", "k_token", "k_head", "v_token", "v_head"):
+        refused({n: -8}, -3)
     for t in (0, 3, -1):
-        refused(9, t, -2)
-    for at, values in ((12, (-1, 1 << 21)), (13, (-1, 1 << 31)), (14, (-1, 1 << 31)), (15, (0, 3, 8193)), (16, (0, 3, 1025)),
-                       (17, (0, 8, 40, 512))):
+        refused({"dt": t}, -2)
+    for n, values in (("B", (-1, 1 << 21)), ("Tq", (-1, 1 << 31)), ("Tk", (-1, 1 << 31)), ("Hq", (0, 3, 8193)), ("H", (0, 3, 1025)),
+                      ("D", (0, 8, 40, 512))):
         for v in values:
-            refused(at, v, -3)
-    refused(18, 2, -1)
+            refused({n: v}, -3)
+    refused({"causal": 2}, -1)
     for v in (0.0, -1.0, float("nan"), float("inf")):
-        refused(19, v, -1)
-    for at in (12, 13):
-        args = [None] * 9 + good[9:]
-        for i in (1, 2, 4, 5, 7, 8):
-            args[i] = 0
-        args[at] = 0
-        assert L.lib.qmm_attend_prompt(*args) == 0
+        refused({"scale": v}, -1)
+    none = {n: 0 for n in PROMPT[:6]}
+    refused({"B": 0, **none}, 0)
+    refused({"Tq": 0, **none}, 0)
 
 
 def test_checks_in_order_of_use():
