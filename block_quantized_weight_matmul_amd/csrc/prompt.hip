@@ -148,7 +148,7 @@ __device__ void careful_rows(const PromptArgs& a, const Work& w, int head, int k
 // that its operand of O^T = V^T P^T takes, in the order in which that product's other operand, V^T, can be read from
 // row-major LDS by transposing reads; the probabilities never leave their lane, and a row's maximum takes one exchange
 // between two lanes.  P is rounded to DT once: its 2^-9 (bf16) of each term, with independent signs, stays below the
-// rounding of the output.  (fp16: P times 2^8, so that small ones keep their bits.)
+// rounding of the output.
 template <int DT, int DP>
 __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(PromptArgs a) {
   typedef typename Elem<DT>::T T;
@@ -156,7 +156,9 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
   constexpr int kBytes = kKeys * L::kRow, kLoads = kBytes / 1024 / kWaves, kOut = DP / 32;
   constexpr int kPer = 64 / L::kPieces > 0 ? 64 / L::kPieces : 1;  // rows of a load of a wave
   static_assert(L::kPieces <= 64, "a load holds whole rows");
-  constexpr float kLift = DT == DT_F16 ? 8.0f : 0.0f;
+  // The maximum that P is relative to is moved, and with it every output so far, only where a score exceeds it by 2^kSlack:
+  // P is at most 2^(kLift + kSlack), and in fp16 keeps small probabilities' bits by 2^kLift.
+  constexpr float kSlack = 8.0f, kLift = DT == DT_F16 ? 6.0f : 0.0f;
   // One array: with a second one the compiler tells what is loaded into LDS apart by its variable, and makes every read of
   // `lds` wait for the loads of the next tile.
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes + 16];
@@ -219,7 +221,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
     for (int n = 0; n < kLoads; ++n) load_lds16(vr, d + kBytes + n * 1024, voff[n]);
   };
 
-  float most = -INFINITY, total = 0.0f;  // of query col; the sum over this lane's keys only
+  float most = -INFINITY, zero = 0.0f, total = 0.0f;  // of query col; the sum over this lane's keys only
+  bool huge = false;
   f32x16 o[kOut];
 #pragma unroll
   for (int d = 0; d < kOut; ++d) o[d] = f32x16{};
@@ -268,20 +271,24 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, s[k][e]);
-    top = fmaxf(most, both_max(top) * factor);  // factor > 0
-    const float zero = top == -INFINITY ? 0.0f : top;
-    const float shrink = __builtin_amdgcn_exp2f(most - zero);
-    most = top;
-    float f = factor;
-    if (__any(fabsf(top) > 0x1p20f && top < INFINITY && top > -INFINITY)) {
+    top = both_max(top) * factor;  // factor > 0
+    if (__any(top > most + kSlack)) {
+      top = fmaxf(most, top);
+      zero = top == -INFINITY ? 0.0f : top;  // nothing but -inf so far: exp of it is 0
+      const float shrink = __builtin_amdgcn_exp2f(most - zero);
+      most = top;
+      total *= shrink;
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) o[d] *= shrink;
       // scores so large that the rounding of the maximum, which the fma below does not share, would show
+      huge = __any(fabsf(top) > 0x1p20f && fabsf(top) < INFINITY);
+    }
+    float f = factor;
+    if (huge) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) s[k] *= factor;
       f = 1.0f;
     }
-    total *= shrink;
-#pragma unroll
-    for (int d = 0; d < kOut; ++d) o[d] *= shrink;
     H8<DT> p[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
