@@ -45,10 +45,9 @@ struct HeadsArgs {
   void *qo, *ko;             // contiguous
   CacheDesc cache;
   const int32_t* slots;
-  int parts;                 // workgroup teams that share a token's heads
 };
 // xt: type of q, k, v; qt: of qo and ko.  With a.slots the keys and values go to a.cache instead of ko.
-hipError_t launch_heads(HeadsArgs a, int xt, int qt, hipStream_t s);
+hipError_t launch_heads(const HeadsArgs& a, int xt, int qt, hipStream_t s);
 
 hipError_t launch_cache_write(const CacheDesc& c, const HeadRows& k, const HeadRows& v, int xt, int64_t T,
                               const int32_t* slots, hipStream_t s);

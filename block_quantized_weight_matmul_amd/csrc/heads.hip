@@ -1,5 +1,7 @@
 // heads.hip -- norms and rotation of query and key heads, and the paged cache: written (quantized where its type is
 // e4m3) and read back.
+#include <algorithm>
+
 #include "attn.hpp"
 
 namespace qmm {
@@ -111,9 +113,18 @@ __device__ __forceinline__ void to_cache(const float* v, uint8_t* data, float* s
   }
 }
 
-// Norms and rotation.  A team of L lanes takes a token and every parts-th share of its heads.  A lane holds eight columns
-// of a head, the two members of each of its four pairs among them (halves of the rotated part, or neighbours), so that a
-// rotation needs no other lane, and the four angles serve every head of the token.
+// 1 / sqrt(m) to about half a step: the hardware's is good to one, and a Newton step halves that.  (A root of a number too
+// small for it takes the division.)
+__device__ __forceinline__ float inverse_root(float m) {
+  float r = __builtin_amdgcn_rsqf(m);
+  r = m < INFINITY ? fmaf(fmaf(-m * r, r, 1.0f), 0.5f * r, r) : r;
+  if (__any(m < 0x1p-100f)) r = 1.0f / sqrtf(m);
+  return r;
+}
+
+// Norms and rotation.  A team of L lanes takes a token, and the launch's layers along z a share of the heads each.  A lane
+// holds eight columns of a head, the two members of each of its four pairs among them (halves of the rotated part, or
+// neighbours), so that a rotation needs no other lane, and the four angles serve every head of the token.
 //
 //   y = x * w / sqrt(mean(x^2) + eps);   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq
 //
@@ -124,54 +135,88 @@ template <int XT, int QT, int CT, bool CACHE, int L>
 __global__ __launch_bounds__(256) void k_heads(HeadsArgs a) {
   constexpr int kTeams = 256 / L, kAhead = 4;
   typedef typename Elem<XT>::T X;
-  const int lane = threadIdx.x % L;
-  const int64_t unit = block_index() * kTeams + threadIdx.x / L;
-  if (unit >= a.T * a.parts) return;  // whole teams: no lane of this one is asked for
-  const int part = static_cast<int>(unit / a.T);
-  const int64_t t = unit - part * a.T;
-  const int heads = a.Hq + a.H + (CACHE ? a.H : 0), per = (heads + a.parts - 1) / a.parts;
-  const int h0 = part * per, h1 = min(heads, h0 + per);
-  const int D = a.D, R = a.R;
-  const bool mine = lane * 8 < D, turned = lane * 8 < R;
-  const int pair0 = lane * 4;
-  const bool halves = !a.interleaved;
-  const int ca = turned && halves ? pair0 : lane * 8;  // the eight columns: ca .. ca + 3, cb .. cb + 3
-  const int cb = turned && halves ? R / 2 + pair0 : lane * 8 + 4;
-
-  int32_t slot = -1;
-  if constexpr (CACHE) slot = a.slots[t];
-
-  const int wa = mine ? ca : 0, wb = mine ? cb : 0;
-  float qw[8], kw[8];
-  if (a.qw || a.kw) {
-    if (a.wt == DT_F32) load_weights<DT_F32>(a.qw, a.kw, wa, wb, qw, kw);
-    else if (a.wt == DT_F16) load_weights<DT_F16>(a.qw, a.kw, wa, wb, qw, kw);
-    else load_weights<DT_BF16>(a.qw, a.kw, wa, wb, qw, kw);
-  }
-  auto row = [&](int h) -> const X* {
-    if (h < a.Hq) return static_cast<const X*>(a.q.p) + t * a.q.st + h * a.q.sh;
-    if (h < a.Hq + a.H) return static_cast<const X*>(a.k.p) + t * a.k.st + (h - a.Hq) * a.k.sh;
-    return static_cast<const X*>(a.v.p) + t * a.v.st + (h - a.Hq - a.H) * a.v.sh;
-  };
   typedef typename Quad<XT>::V V4;
+  const int lane = threadIdx.x % L;
+  const int64_t t = block_index() * kTeams + threadIdx.x / L;
+  if (t >= a.T) return;  // whole teams: no lane of this one is asked for
+  const int heads = a.Hq + a.H + (CACHE ? a.H : 0), per = (heads + gridDim.z - 1) / gridDim.z;
+  const int h0 = blockIdx.z * per, h1 = min(heads, h0 + per);
+  if (h0 >= h1) return;
+  const int D = a.D, R = a.R;
+  const bool mine = lane * 8 < D, turned = lane * 8 < R, halves = !a.interleaved;
+  const int pair0 = turned ? lane * 4 : 0;
+  // the eight columns: ca .. ca + 3, cb .. cb + 3
+  const int ca = !mine ? 0 : turned && halves ? pair0 : lane * 8;
+  const int cb = !mine ? 0 : turned && halves ? R / 2 + pair0 : lane * 8 + 4;
+
+  const X* const q = static_cast<const X*>(a.q.p) + t * a.q.st;
+  const X* const k = static_cast<const X*>(a.k.p) + t * a.k.st - a.Hq * a.k.sh;
+  const X* const v = CACHE ? static_cast<const X*>(a.v.p) + t * a.v.st - (a.Hq + a.H) * a.v.sh : nullptr;
   V4 lo[kAhead], hi[kAhead];
   auto load = [&](int h) {
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
-      const X* p = row(min(h + n, h1 - 1));
-      lo[n] = load4<XT>(p + wa);
-      hi[n] = load4<XT>(p + wb);
+      const int g = min(h + n, h1 - 1);
+      const X* p = g < a.Hq ? q + g * a.q.sh : !CACHE || g < a.Hq + a.H ? k + g * a.k.sh : v + g * a.v.sh;
+      lo[n] = load4<XT>(p + ca);
+      hi[n] = load4<XT>(p + cb);
     }
   };
-  if (h0 < h1) load(h0);
-
+  load(h0);
+  int32_t slot = -1;
+  if constexpr (CACHE) slot = a.slots[t];
+  float qw[8], kw[8];
+  if (a.qw || a.kw) {
+    if (a.wt == DT_F32) load_weights<DT_F32>(a.qw, a.kw, ca, cb, qw, kw);
+    else if (a.wt == DT_F16) load_weights<DT_F16>(a.qw, a.kw, ca, cb, qw, kw);
+    else load_weights<DT_BF16>(a.qw, a.kw, ca, cb, qw, kw);
+  }
   float sine[4], cosine[4];  // while the first heads are on their way
   if (a.inv_freq) {
     const double p = a.positions[t];
-    const f32x4 f = *reinterpret_cast<const f32x4u*>(a.inv_freq + (turned ? pair0 : 0));
+    const f32x4 f = *reinterpret_cast<const f32x4u*>(a.inv_freq + pair0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) turn(p * static_cast<double>(f[i]), sine[i], cosine[i]);
   }
+  const float share = 1.0f / static_cast<float>(D);
+
+  // one head, normed and rotated
+  auto norm_turn = [&](const V4& x0, const V4& x1, bool normed, const float* w, float* y) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = static_cast<float>(x0[i]);
+      y[4 + i] = static_cast<float>(x1[i]);
+    }
+    if (normed) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
+      const float r = inverse_root(fmaf(team_sum<L>(mine ? sum : 0.0f), share, a.eps));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
+    }
+    if (a.inv_freq) {
+      float z[8];
+      if (halves) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[i] = fmaf(y[i], cosine[i], -(y[4 + i] * sine[i]));
+          z[4 + i] = fmaf(y[4 + i], cosine[i], y[i] * sine[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[2 * i] = fmaf(y[2 * i], cosine[i], -(y[2 * i + 1] * sine[i]));
+          z[2 * i + 1] = fmaf(y[2 * i + 1], cosine[i], y[2 * i] * sine[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = turned ? z[i] : y[i];
+    }
+  };
+  typedef typename Elem<QT>::T Q;
+  Q* const qo = static_cast<Q*>(a.qo) + t * a.Hq * D;
+  Q* const ko = CACHE ? nullptr : static_cast<Q*>(a.ko) + (t * a.H - a.Hq) * D;
 
   for (int h = h0; h < h1; h += kAhead) {
     V4 x0[kAhead], x1[kAhead];
@@ -182,55 +227,30 @@ __global__ __launch_bounds__(256) void k_heads(HeadsArgs a) {
     for (int n = 0; n < kAhead; ++n) {
       const int g = h + n;
       if (g >= h1) break;
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = static_cast<float>(x0[n][i]);
-        v[4 + i] = static_cast<float>(x1[n][i]);
-      }
-      if (CACHE && g >= a.Hq + a.H) {
-        const SlotRow r = slot_row(a.cache, slot, g - a.Hq - a.H);
-        to_cache<CT, XT, L>(v, a.cache.v, a.cache.vs, r, D, ca, cb, mine);
-        continue;
-      }
-      const bool query = g < a.Hq;
-      if (query ? a.qw != nullptr : a.kw != nullptr) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(v[i], v[i], sum);
-        const float m = team_sum<L>(mine ? sum : 0.0f) / static_cast<float>(D) + a.eps;
-        const float r = 1.0f / sqrtf(m);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * r * (query ? qw[i] : kw[i]);
-      }
-      if (a.inv_freq && turned) {
-        if (halves) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = v[i], y = v[4 + i];
-            v[i] = fmaf(x, cosine[i], -(y * sine[i]));
-            v[4 + i] = fmaf(y, cosine[i], x * sine[i]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = v[2 * i], y = v[2 * i + 1];
-            v[2 * i] = fmaf(x, cosine[i], -(y * sine[i]));
-            v[2 * i + 1] = fmaf(y, cosine[i], x * sine[i]);
-          }
-        }
-      }
-      if (query || !CACHE) {
-        typename Elem<QT>::T* o = static_cast<typename Elem<QT>::T*>(query ? a.qo : a.ko);
-        o += query ? (t * a.Hq + g) * D : (t * a.H + (g - a.Hq)) * D;
+      float y[8];
+      if (g < a.Hq) {
+        norm_turn(x0[n], x1[n], a.qw != nullptr, qw, y);
         if (mine) {
-          store4<QT>(o + ca, v);
-          store4<QT>(o + cb, v + 4);
+          store4<QT>(qo + g * D + ca, y);
+          store4<QT>(qo + g * D + cb, y + 4);
         }
-      } else {
+      } else if (!CACHE || g < a.Hq + a.H) {
+        norm_turn(x0[n], x1[n], a.kw != nullptr, kw, y);
+        if constexpr (CACHE) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(static_cast<typename Elem<QT>::T>(v[i]));
-        to_cache<CT, QT, L>(v, a.cache.k, a.cache.ks, slot_row(a.cache, slot, g - a.Hq), D, ca, cb, mine);
+          for (int i = 0; i < 8; ++i) y[i] = static_cast<float>(static_cast<Q>(y[i]));
+          to_cache<CT, QT, L>(y, a.cache.k, a.cache.ks, slot_row(a.cache, slot, g - a.Hq), D, ca, cb, mine);
+        } else if (mine) {
+          store4<QT>(ko + g * D + ca, y);
+          store4<QT>(ko + g * D + cb, y + 4);
+        }
+      } else if constexpr (CACHE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[i] = static_cast<float>(x0[n][i]);
+          y[4 + i] = static_cast<float>(x1[n][i]);
+        }
+        to_cache<CT, XT, L>(y, a.cache.v, a.cache.vs, slot_row(a.cache, slot, g - a.Hq - a.H), D, ca, cb, mine);
       }
     }
   }
@@ -333,23 +353,21 @@ hipError_t with_team(int D, F f) {
 
 }  // namespace
 
-hipError_t launch_heads(HeadsArgs a, int xt, int qt, hipStream_t s) {
+hipError_t launch_heads(const HeadsArgs& a, int xt, int qt, hipStream_t s) {
   const bool cache = a.slots != nullptr;
   const int heads = a.Hq + a.H + (cache ? a.H : 0);
   return with_team(a.D, [&](auto l) {
     constexpr int L = decltype(l)::value;
-    // A token's heads are divided among teams until these fill four waves of every SIMD, at least four heads each, one
-    // round of loads; each share makes the token's angles anew.
-    const int64_t want = 256 * 16 * (64 / L);
-    int64_t parts = a.T >= want ? 1 : (want + a.T - 1) / a.T;
-    const int64_t most = (heads + 3) / 4;
-    a.parts = static_cast<int>(parts < most ? parts : most);
-    const int64_t blocks = (a.T * a.parts + 256 / L - 1) / (256 / L);
+    // A token's heads are divided among layers until the teams fill four waves of every SIMD, at least four heads each, one
+    // round of loads; each layer makes the tokens' angles anew.
+    const int64_t want = 256 * 16 * (64 / L), most = (heads + 3) / 4;
+    const int64_t layers = std::min(most, (want + a.T - 1) / a.T);
+    const int64_t blocks = (a.T + 256 / L - 1) / (256 / L);
     return with_type(xt, [&](auto x) {
       constexpr int XT = decltype(x)::value;
       auto go = [&](auto q, auto c, auto w) {
         hipLaunchKernelGGL((k_heads<XT, decltype(q)::value, decltype(c)::value, decltype(w)::value != 0, L>),
-                           long_grid(blocks), dim3(256), 0, s, a);
+                           long_grid(blocks, 256, layers), dim3(256), 0, s, a);
         return hipGetLastError();
       };
       if (!cache) return with_type(qt, [&](auto q) { return go(q, q, Int<0>{}); });
