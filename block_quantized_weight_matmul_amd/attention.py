@@ -80,14 +80,25 @@ def _vector(t, name, dtype, length, device):
     return t.data_ptr()
 
 
+def _length(t, name, dtype):
+    """Elements of a vector; where it lies, _vector looks at."""
+    try:
+        (n,) = t.shape
+        if t.dtype is dtype:
+            return n
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _tensor(t, name, (dtype,), (1,))
+    return t.shape[0]
+
+
 def _rotation(positions, inv_freq, T, device):
     """Pointers of the positions and frequencies, columns rotated."""
     if inv_freq is None:
         return 0, 0, 0
     if positions is None:
         raise ValueError("inv_freq needs positions")
-    _tensor(inv_freq, "inv_freq", _F32, (1,))
-    n = inv_freq.shape[0]
+    n = _length(inv_freq, "inv_freq", torch.float32)
     return _vector(positions, "positions", _INT, T, device), _vector(inv_freq, "inv_freq", torch.float32, n, device), 2 * n
 
 
@@ -251,8 +262,7 @@ class KVCache:
     def read(self, table, starts, total, dtype=None, out=None):
         """(k, v) [total, heads, D]: sequence b's tokens as rows starts[b] .. starts[b + 1] - 1 (starts int32 [B + 1], not
         decreasing).  Rows of no sequence are not written: they stay as they were in `out`, a pair of tensors."""
-        _tensor(starts, "starts", _I32, (1,))
-        B = starts.shape[0] - 1
+        B = _length(starts, "starts", _INT) - 1
         if B < 0:
             raise ValueError("starts is empty")
         d = self.device
@@ -323,8 +333,7 @@ def attend_prompt(q, k, v, starts, k_starts=None, causal=True, scale=None, out=N
         raise ValueError(f"k has {H} heads of {Dk}; q has {Hq} of {D}")
     if Tv != Tk or Hv != H or Dv != D:
         raise ValueError(f"v has shape {tuple(v.shape)}; k has {tuple(k.shape)}")
-    _tensor(starts, "starts", _I32, (1,))
-    n = starts.shape[0]
+    n = _length(starts, "starts", _INT)
     if n < 1:
         raise ValueError("starts is empty")
     qs = _vector(starts, "starts", _INT, n, d)
