@@ -126,15 +126,21 @@ __device__ __forceinline__ uint32_t team_max(uint32_t v) {
   return team<L>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
-// The sequence that row r of packed sequences belongs to: the number of i < B with starts[i + 1] <= r (B where it lies
-// behind the last).  All lanes of the wave ask for one row.
-__device__ __forceinline__ int64_t find_sequence(const int32_t* starts, int64_t B, int64_t r) {
-  int64_t n = 0;
-  for (int64_t i = 0; i < B; i += 64) {
-    const int64_t j = i + (threadIdx.x & 63);
-    n += __popcll(__ballot(j < B && starts[j + 1] <= r));
+// The number of i < n for which f holds, f first true and then false: a search by 64 lanes at a time, the same in every
+// lane of the wave.  (Of an f that is not so, some number 0 .. n.)
+template <typename F>
+__device__ __forceinline__ int64_t count_first(int64_t n, F f) {
+  const int lane = threadIdx.x & 63;
+  int64_t at = 0;
+  while (n > 0) {
+    const int64_t step = (n + 63) / 64, i = lane * step;
+    const int some = __popcll(__ballot(i < n && f(at + i)));
+    if (some == 0) break;
+    const int64_t known = (some - 1) * step + 1;  // f holds up to here
+    at += known;
+    n = min(n - known, step - 1);
   }
-  return n;
+  return at;
 }
 
 #endif  // __HIPCC__

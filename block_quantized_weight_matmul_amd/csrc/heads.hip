@@ -283,7 +283,7 @@ __global__ __launch_bounds__(256) void k_cache_read(CacheDesc c, const int32_t* 
   typedef typename Elem<OT>::T O;
   const int lane = threadIdx.x % L, D = c.D, H = c.heads;
   const int64_t first = block_index() * kTeams, row = first + threadIdx.x / L;
-  int64_t b = find_sequence(starts, B, first);
+  int64_t b = count_first(B, [&](int64_t i) { return starts[i + 1] <= first; });
   if (row >= total) return;
   while (b < B && starts[b + 1] <= row) ++b;  // the workgroup's rows may end a sequence
   if (b >= B) return;                         // behind the last sequence

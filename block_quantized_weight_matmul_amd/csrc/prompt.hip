@@ -53,10 +53,11 @@ struct Tile {
   }
 };
 
-// The tile of queries of a workgroup: the i-th of all sequences' tiles.
+// The tile of queries of a workgroup.
 struct Work {
-  int64_t q0, n, k0, m;  // first row and number of the sequence's queries, of its keys
-  int64_t first;         // first query of the tile
+  int64_t q0, k0;  // first row of the sequence's queries, of its keys
+  int n, m;        // their numbers, up to 2^30
+  int first;       // first query of the tile
   bool some;
 };
 // Starts are taken as they come, kept within [0, total]: no row outside the tensors is touched whatever they hold.
@@ -64,38 +65,20 @@ __device__ __forceinline__ int64_t start_at(const int32_t* s, int64_t i, int64_t
   const int64_t v = s[i];
   return v < 0 ? 0 : v > total ? total : v;
 }
+// Sequence b's tiles have the indexes from start_b / kQueries + b on: the next one's begin late enough for all of them, one
+// index or none is left over, and no sum over the sequences before is needed.
 __device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index) {
   Work w{};
-  const int lane = threadIdx.x & 63;
-  int64_t before = 0;
-  for (int64_t b0 = 0; b0 < a.B; b0 += 64) {
-    const int64_t b = b0 + lane;
-    const int64_t lo = b < a.B ? start_at(a.q_starts, b, a.Tq) : 0, hi = b < a.B ? start_at(a.q_starts, b + 1, a.Tq) : 0;
-    const int tiles = hi > lo ? static_cast<int>((hi - lo + kQueries - 1) / kQueries) : 0;
-    int upto = tiles;
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) {
-      const int y = __shfl_up(upto, x);
-      if (lane >= x) upto += y;
-    }
-    const uint64_t past = __ballot(before + upto > index);
-    if (past) {
-      const int at = __builtin_ctzll(past);
-      const int64_t seq = b0 + at;
-      const int64_t mine = index - before - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(tiles, at));
-      w.q0 = start_at(a.q_starts, seq, a.Tq);
-      w.n = start_at(a.q_starts, seq + 1, a.Tq) - w.q0;
-      w.k0 = start_at(a.k_starts, seq, a.Tk);
-      w.m = start_at(a.k_starts, seq + 1, a.Tk) - w.k0;
-      if (w.m < 0) w.m = 0;
-      // the last tile, which sees the most keys, first
-      const int64_t all = (w.n + kQueries - 1) / kQueries;
-      w.first = (all - 1 - mine) * kQueries;
-      w.some = true;
-      return w;
-    }
-    before += __builtin_amdgcn_readlane(upto, 63);
-  }
+  const int64_t b = count_first(a.B, [&](int64_t i) { return start_at(a.q_starts, i, a.Tq) / kQueries + i <= index; }) - 1;
+  if (b < 0) return w;
+  w.q0 = start_at(a.q_starts, b, a.Tq);
+  w.n = static_cast<int>(start_at(a.q_starts, b + 1, a.Tq) - w.q0);
+  w.k0 = start_at(a.k_starts, b, a.Tk);
+  w.m = static_cast<int>(max(start_at(a.k_starts, b + 1, a.Tk) - w.k0, int64_t(0)));
+  const int all = (w.n + kQueries - 1) / kQueries, mine = static_cast<int>(index - (w.q0 / kQueries + b));
+  // the last tile, which sees the most keys, first
+  w.first = (all - 1 - mine) * kQueries;
+  w.some = w.n > 0 && mine < all;
   return w;
 }
 
@@ -107,13 +90,13 @@ __device__ void careful_rows(const PromptArgs& a, const Work& w, int head, int k
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   constexpr int kOwn = DP / 64;
   for (int r = wave; r < kQueries; r += kWaves) {
-    const int64_t i = w.first + r;
+    const int i = w.first + r;
     if (i >= w.n) continue;
-    const int64_t seen = min(w.m, a.causal ? max(int64_t(0), i + (w.m - w.n) + 1) : w.m);
+    const int seen = min(w.m, a.causal ? max(0, i + (w.m - w.n) + 1) : w.m);
     const T* q = static_cast<const T*>(a.q.p) + (w.q0 + i) * a.q.st + head * a.q.sh;
     float most = -INFINITY, total = 0.0f, o[kOwn] = {};
-    for (int64_t j0 = 0; j0 < seen; j0 += 64) {
-      const int64_t j = min(j0 + lane, seen - 1);
+    for (int j0 = 0; j0 < seen; j0 += 64) {
+      const int j = min(j0 + lane, seen - 1);
       const T* k = static_cast<const T*>(a.k.p) + (w.k0 + j) * a.k.st + kv * a.k.sh;
       float s = 0.0f;
       for (int d = 0; d < a.D; ++d) s = fmaf(static_cast<float>(q[d]), static_cast<float>(k[d]), s);
@@ -128,7 +111,7 @@ __device__ void careful_rows(const PromptArgs& a, const Work& w, int head, int k
       for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
       total = total * shrink + sum;
       for (int e = 0; e < kOwn; ++e) o[e] *= shrink;
-      for (int n = 0; n < min(int64_t(64), seen - j0); ++n) {
+      for (int n = 0; n < min(64, seen - j0); ++n) {
         const T* v = static_cast<const T*>(a.v.p) + (w.k0 + j0 + n) * a.v.st + kv * a.v.sh;
         const float pn = __shfl(p, n);
         for (int e = 0; e < kOwn; ++e)
@@ -173,15 +156,15 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const float factor = a.scale * 1.44269504088896340736f;
-  const int64_t shift = w.m - w.n;  // query i sees keys 0 .. i + shift
-  const int64_t i0 = w.first + wave * 32;
-  const int64_t last = min(w.n, w.first + kQueries) - 1;
-  int64_t end = a.causal ? min(w.m, last + shift + 1) : w.m;  // keys that some row here sees
+  const int shift = w.m - w.n;  // query i sees keys 0 .. i + shift
+  const int i0 = w.first + wave * 32;
+  const int last = min(w.n, w.first + kQueries) - 1;
+  int end = a.causal ? min(w.m, last + shift + 1) : w.m;  // keys that some row here sees
   if (end < 0) end = 0;
-  const int64_t mine = a.causal ? min(w.m, i0 + 31 + shift + 1) : w.m;   // of this wave's rows
-  const int64_t whole = a.causal ? min(w.m, i0 + shift + 1) : w.m;       // keys that all of its rows see
-  const int64_t whole_all = a.causal ? min(w.m, w.first + shift + 1) : w.m;
-  const int count = static_cast<int>((end + kKeys - 1) / kKeys);
+  const int mine = a.causal ? min(w.m, i0 + 31 + shift + 1) : w.m;   // of this wave's rows
+  const int whole = a.causal ? min(w.m, i0 + shift + 1) : w.m;       // keys that all of its rows see
+  const int whole_all = a.causal ? min(w.m, w.first + shift + 1) : w.m;
+  const int count = (end + kKeys - 1) / kKeys;
   if (threadIdx.x == 0) met = 0;
 
   H8<DT> q[DP / 16];
@@ -211,7 +194,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
   const T* const vbase = static_cast<const T*>(a.v.p) + w.k0 * a.v.st + kv * a.v.sh;
   auto load_tile = [&](int i) {
     const int64_t j = static_cast<int64_t>(i) * kKeys;
-    const uint32_t rows = static_cast<uint32_t>(min(w.m - j, int64_t(kKeys)));
+    const uint32_t rows = min(w.m - i * kKeys, kKeys);
     const __amdgpu_buffer_rsrc_t kr = rsrc(kbase + j * a.k.st, (rows - 1) * kst + a.D * 2);
     const __amdgpu_buffer_rsrc_t vr = rsrc(vbase + j * a.v.st, (rows - 1) * vst + a.D * 2);
     uint8_t* d = lds + (i & 1) * 2 * kBytes + wave * kLoads * 1024;
@@ -234,7 +217,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
     if (i + 1 < count) load_tile(i + 1);
     const uint8_t* const lk = lds + (i & 1) * 2 * kBytes;
     const uint8_t* const lv = lk + kBytes;
-    const int64_t j0 = static_cast<int64_t>(i) * kKeys;
+    const int j0 = i * kKeys;
     if (a.causal && j0 + kKeys > whole_all) {  // rows see parts of this tile: infinities and NaN among its values
       uint32_t worst = 0;
 #pragma unroll
@@ -258,8 +241,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
         s[k] = mma(*reinterpret_cast<const H8<DT>*>(lk + row * L::kRow + L::key(row, 2 * j + half) * 16), q[j], s[k]);
     }
     if (j0 + kKeys > whole) {
-      const int64_t lim = min(w.m, a.causal ? i0 + col + shift + 1 : w.m) - j0;  // keys of the tile that row col sees
-      const int seen = static_cast<int>(min(lim, int64_t(kKeys)));
+      const int seen = min(w.m, a.causal ? i0 + col + shift + 1 : w.m) - j0;  // keys of the tile that row col sees
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -343,7 +325,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
 
 template <int DT, int DP>
 hipError_t prompt(const PromptArgs& a, hipStream_t s) {
-  const int64_t tiles = (a.Tq + kQueries - 1) / kQueries + a.B;  // at least the sequences' tiles
+  const int64_t tiles = a.Tq / kQueries + a.B;  // indexes of tiles (find_work)
   hipLaunchKernelGGL((k_prompt<DT, DP>), long_grid(tiles * a.Hq), dim3(64 * kWaves), 0, s, a);
   return hipGetLastError();
 }

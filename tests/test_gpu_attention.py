@@ -477,6 +477,40 @@ def test_prompt(ns, ms, Hq, H, D, t):
     within(out, ref, bound, "scale")
 
 
+@pytest.mark.parametrize("B", [63, 64, 65, 4097, 5000])
+def test_many_short_sequences(B):
+    """More sequences than lanes, many of them empty: the tiles' search for theirs, and that of packed rows for theirs."""
+    g = np.random.default_rng([90, B])
+    H, D, page = 1, 16, 16
+    ns = g.choice([0, 1, 2, 5], B)
+    ns[B // 2], ns[-1] = 300, 130
+    before = g.choice([0, 3], B)
+    ms = ns + before
+    T, Tk = int(ns.sum()), int(ms.sum())
+    qx, k, v = prompt_inputs(g, ns, ms, 2, H, D, torch.bfloat16, False)
+    got = host64(q.attend_prompt(qx, k, v, starts(ns), starts(ms)))
+    ends, kends = np.cumsum(ns), np.cumsum(ms)
+    seen = np.zeros((T, Tk), bool)  # a block of keys for every row
+    for b in range(B):
+        seen[ends[b] - ns[b]:ends[b], kends[b] - ms[b]:kends[b]] = A.causal(ns[b], ms[b])
+    for h in range(2):
+        o, spread, noise, reach = A.attend(host64(qx[:, h]), host64(k[:, 0]), host64(v[:, 0]), D ** -0.5, seen)
+        bound = spread * (score_error(reach, D) + 400 * 2.0 ** -24) + rounding_noise(spread, noise, HALF_STEP[torch.bfloat16])
+        tol = bound + (np.abs(o) + bound) * HALF_STEP[torch.bfloat16] + SMALLEST[torch.bfloat16]
+        assert np.all(np.abs(got[:, h] - o) <= tol)
+    need = -(-ms // page)
+    table = np.full((B, int(need.max())), -1, np.int32)
+    order = g.permutation(int(need.sum()))
+    at = np.cumsum(need) - need
+    for b in range(B):
+        table[b, :need[b]] = order[at[b]:at[b] + need[b]]
+    c = blank(int(need.sum()), page, H, D, "bf16")
+    owner, t = np.repeat(np.arange(B), ms), np.concatenate([np.arange(n) for n in ms])
+    c.write(k, v, i32(table[owner, t // page] * page + t % page))
+    rk, rv = c.read(i32(table.flatten()).view(B, -1), starts(ms), Tk)
+    assert torch.equal(rk, k) and torch.equal(rv, v)
+
+
 def test_prompt_rows_of_no_sequence():
     g = np.random.default_rng(82)
     qx, k, v = prompt_inputs(g, [100], [100], 2, 1, 64, torch.bfloat16, True)
