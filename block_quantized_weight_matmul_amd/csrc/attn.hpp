@@ -83,8 +83,9 @@ struct PromptArgs {
   int causal;
   float scale;
   void* out;  // [Tq][Hq][D]
+  int group;  // 1 << group heads share a workgroup (set by the launch)
 };
-hipError_t launch_prompt(const PromptArgs& a, int dt, hipStream_t s);
+hipError_t launch_prompt(PromptArgs a, int dt, hipStream_t s);
 
 #ifdef __HIPCC__
 

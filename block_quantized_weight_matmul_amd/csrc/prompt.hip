@@ -2,8 +2,9 @@
 //
 //   out[i, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q_i.k_j - max),  j <= i + (m - n)  (m keys, n queries)
 //
-// Bound by the matrix cores.  A workgroup takes 128 queries of one head and sweeps the keys they may see in tiles of 64:
-// keys and values go straight into LDS, two tiles deep, while the waves, 32 queries each, work on the tile before.
+// Bound by the matrix cores.  A workgroup takes 128 rows, queries of up to four heads that share a key head, and sweeps the
+// keys they may see in tiles of 64: keys and values go straight into LDS, two tiles deep, while the waves, 32 queries of
+// one head each, work on the tile before.
 #include "attn.hpp"
 
 namespace qmm {
@@ -12,7 +13,7 @@ namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-constexpr int kQueries = 128, kKeys = 64, kWaves = 4;
+constexpr int kRows = 128, kKeys = 64, kWaves = 4;  // of a workgroup: queries times heads, keys of a tile
 
 template <int QT> struct Half8 { typedef typename Elem<QT>::T V __attribute__((ext_vector_type(8))); };
 template <int QT> using H8 = typename Half8<QT>::V;
@@ -65,19 +66,19 @@ __device__ __forceinline__ int64_t start_at(const int32_t* s, int64_t i, int64_t
   const int64_t v = s[i];
   return v < 0 ? 0 : v > total ? total : v;
 }
-// Sequence b's tiles have the indexes from start_b / kQueries + b on: the next one's begin late enough for all of them, one
-// index or none is left over, and no sum over the sequences before is needed.
-__device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index) {
+// Sequence b's tiles, of 1 << shift queries, have the indexes from (start_b >> shift) + b on: the next one's begin late enough
+// for all of them, one index or none is left over, and no sum over the sequences before is needed.
+__device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index, int shift) {
   Work w{};
-  const int64_t b = count_first(a.B, [&](int64_t i) { return start_at(a.q_starts, i, a.Tq) / kQueries + i <= index; }) - 1;
+  const int64_t b = count_first(a.B, [&](int64_t i) { return (start_at(a.q_starts, i, a.Tq) >> shift) + i <= index; }) - 1;
   if (b < 0) return w;
   w.q0 = start_at(a.q_starts, b, a.Tq);
   w.n = static_cast<int>(start_at(a.q_starts, b + 1, a.Tq) - w.q0);
   w.k0 = start_at(a.k_starts, b, a.Tk);
   w.m = static_cast<int>(max(start_at(a.k_starts, b + 1, a.Tk) - w.k0, int64_t(0)));
-  const int all = (w.n + kQueries - 1) / kQueries, mine = static_cast<int>(index - (w.q0 / kQueries + b));
+  const int all = (w.n + (1 << shift) - 1) >> shift, mine = static_cast<int>(index - ((w.q0 >> shift) + b));
   // the last tile, which sees the most keys, first
-  w.first = (all - 1 - mine) * kQueries;
+  w.first = (all - 1 - mine) << shift;
   w.some = w.n > 0 && mine < all;
   return w;
 }
@@ -85,12 +86,12 @@ __device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index) {
 // One row at a time, with nothing of a key that the row does not see: for a workgroup that met an infinity or a NaN among
 // the values of a tile which some of its rows see in part.  (A product of matrices adds 0 * Inf = NaN to the others.)
 template <int DT, int DP>
-__device__ void careful_rows(const PromptArgs& a, const Work& w, int head, int kv, float factor) {
+__device__ void careful_rows(const PromptArgs& a, const Work& w, int head0, int kv, float factor) {
   typedef typename Elem<DT>::T T;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   constexpr int kOwn = DP / 64;
-  for (int r = wave; r < kQueries; r += kWaves) {
-    const int i = w.first + r;
+  for (int r = wave; r < kRows; r += kWaves) {
+    const int block = r / 32, head = head0 + (block & (1 << a.group) - 1), i = w.first + (block >> a.group) * 32 + r % 32;
     if (i >= w.n) continue;
     const int seen = min(w.m, a.causal ? max(0, i + (w.m - w.n) + 1) : w.m);
     const T* q = static_cast<const T*>(a.q.p) + (w.q0 + i) * a.q.st + head * a.q.sh;
@@ -150,15 +151,17 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
   const int G = a.Hq / a.H;
   // key heads vary fastest: workgroup i runs on die i mod 8, so that a key head's rows stay in one die's L2 cache
   const int64_t block = block_index();
-  const int hx = static_cast<int>(block % a.Hq), kv = hx % a.H, head = kv * G + hx / a.H;
-  const Work w = find_work(a, block / a.Hq);
+  const int groups = a.Hq >> a.group, hx = static_cast<int>(block % groups), kv = hx % a.H;
+  const int rows = kRows >> a.group;  // queries of a head
+  const Work w = find_work(a, block / groups, __builtin_ctz(kRows) - a.group);
   if (!w.some) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
+  const int head0 = kv * G + (hx / a.H << a.group), head = head0 + (wave & (1 << a.group) - 1);
   const float factor = a.scale * 1.44269504088896340736f;
   const int shift = w.m - w.n;  // query i sees keys 0 .. i + shift
-  const int i0 = w.first + wave * 32;
-  const int last = min(w.n, w.first + kQueries) - 1;
+  const int i0 = w.first + (wave >> a.group) * 32;
+  const int last = min(w.n, w.first + rows) - 1;
   int end = a.causal ? min(w.m, last + shift + 1) : w.m;  // keys that some row here sees
   if (end < 0) end = 0;
   const int mine = a.causal ? min(w.m, i0 + 31 + shift + 1) : w.m;   // of this wave's rows
@@ -194,9 +197,9 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
   const T* const vbase = static_cast<const T*>(a.v.p) + w.k0 * a.v.st + kv * a.v.sh;
   auto load_tile = [&](int i) {
     const int64_t j = static_cast<int64_t>(i) * kKeys;
-    const uint32_t rows = min(w.m - i * kKeys, kKeys);
-    const __amdgpu_buffer_rsrc_t kr = rsrc(kbase + j * a.k.st, (rows - 1) * kst + a.D * 2);
-    const __amdgpu_buffer_rsrc_t vr = rsrc(vbase + j * a.v.st, (rows - 1) * vst + a.D * 2);
+    const uint32_t left = min(w.m - i * kKeys, kKeys);
+    const __amdgpu_buffer_rsrc_t kr = rsrc(kbase + j * a.k.st, (left - 1) * kst + a.D * 2);
+    const __amdgpu_buffer_rsrc_t vr = rsrc(vbase + j * a.v.st, (left - 1) * vst + a.D * 2);
     uint8_t* d = lds + (i & 1) * 2 * kBytes + wave * kLoads * 1024;
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) load_lds16(kr, d + n * 1024, koff[n]);
@@ -301,7 +304,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
   total = both_sum(total);
   __syncthreads();
   if (met) {
-    careful_rows<DT, DP>(a, w, head, kv, factor);
+    careful_rows<DT, DP>(a, w, head0, kv, factor);
     return;
   }
   if (i0 + col >= w.n) return;
@@ -325,14 +328,18 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
 
 template <int DT, int DP>
 hipError_t prompt(const PromptArgs& a, hipStream_t s) {
-  const int64_t tiles = a.Tq / kQueries + a.B;  // indexes of tiles (find_work)
-  hipLaunchKernelGGL((k_prompt<DT, DP>), long_grid(tiles * a.Hq), dim3(64 * kWaves), 0, s, a);
+  const int64_t tiles = a.Tq / (kRows >> a.group) + a.B;  // indexes of tiles (find_work)
+  hipLaunchKernelGGL((k_prompt<DT, DP>), long_grid(tiles * (a.Hq >> a.group)), dim3(64 * kWaves), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_prompt(const PromptArgs& a, int dt, hipStream_t s) {
+hipError_t launch_prompt(PromptArgs a, int dt, hipStream_t s) {
+  // The query heads of a key head share a workgroup, four or two where their number allows it, so that its queries, 32 or 64
+  // of each, end later in fewer tiles that they see in part.
+  const int G = a.Hq / a.H;
+  a.group = G % 4 == 0 ? 2 : G % 2 == 0 ? 1 : 0;
   if (dt == DT_F16) {
     if (a.D <= 64) return prompt<DT_F16, 64>(a, s);
     return a.D <= 128 ? prompt<DT_F16, 128>(a, s) : prompt<DT_F16, 256>(a, s);
