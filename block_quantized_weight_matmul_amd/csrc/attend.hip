@@ -113,8 +113,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
   const CacheDesc& c = a.cache;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quarter = lane >> 4;
-  const int D = c.D, H = c.heads, G = a.Hq / H, tiles = (G + kRows - 1) / kRows;
-  const int split = blockIdx.x, h = blockIdx.y / tiles, g0 = (blockIdx.y % tiles) * kRows;
+  const int D = c.D, H = c.heads, G = a.G;
+  const int split = blockIdx.x, h = a.tiles == 1 ? blockIdx.y : blockIdx.y / a.tiles, g0 = (blockIdx.y - h * a.tiles) * kRows;
   const int64_t b = blockIdx.z;
   const int rows = min(kRows, G - g0);                 // heads here
   const int64_t room = a.W << c.shift;
@@ -420,8 +420,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 
 template <int QT, int CT>
 hipError_t attend(const AttendArgs& a, hipStream_t s) {
-  const int G = a.Hq / a.cache.heads, tiles = (G + kRows - 1) / kRows;
-  const dim3 grid(a.splits, a.cache.heads * tiles, static_cast<unsigned>(a.B));
+  const dim3 grid(a.splits, a.cache.heads * a.tiles, static_cast<unsigned>(a.B));
   if (a.cache.D <= 64) hipLaunchKernelGGL((k_attend<QT, CT, 64>), grid, dim3(64 * kWaves), 0, s, a);
   else if (a.cache.D <= 128) hipLaunchKernelGGL((k_attend<QT, CT, 128>), grid, dim3(64 * kWaves), 0, s, a);
   else hipLaunchKernelGGL((k_attend<QT, CT, 256>), grid, dim3(64 * kWaves), 0, s, a);
@@ -450,7 +449,9 @@ AttendSplit attend_split(const CacheDesc& c, int64_t B, int Hq, int64_t bound) {
   return {static_cast<int>(std::max<int64_t>((bound + piece - 1) / piece, 1)), piece};
 }
 
-hipError_t launch_attend(const AttendArgs& a, int qt, hipStream_t s) {
+hipError_t launch_attend(AttendArgs a, int qt, hipStream_t s) {
+  a.G = a.Hq / a.cache.heads;
+  a.tiles = (a.G + kRows - 1) / kRows;
   if (a.cache.type == DT_E4M3) return qt == DT_F16 ? attend<DT_F16, DT_E4M3>(a, s) : attend<DT_BF16, DT_E4M3>(a, s);
   return qt == DT_F16 ? attend<DT_F16, DT_F16>(a, s) : attend<DT_BF16, DT_BF16>(a, s);
 }

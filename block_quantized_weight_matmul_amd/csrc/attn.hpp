@@ -66,6 +66,7 @@ struct AttendArgs {
   void* out;    // [B][Hq][D]
   int splits;     // pieces of a sequence, of `piece` tokens each, the last of all that is left
   int64_t piece;
+  int G, tiles;   // query heads of a key head, row tiles of them (set by the launch)
   float* ws;    // splits > 1: partial outputs [B][Hq][splits][D], then (maximum, sum) [B][Hq][splits]
 };
 struct AttendSplit {
@@ -73,7 +74,7 @@ struct AttendSplit {
   int64_t piece;
 };
 AttendSplit attend_split(const CacheDesc& c, int64_t B, int Hq, int64_t bound);
-hipError_t launch_attend(const AttendArgs& a, int qt, hipStream_t s);
+hipError_t launch_attend(AttendArgs a, int qt, hipStream_t s);
 
 struct PromptArgs {
   HeadRows q, k, v;
@@ -83,7 +84,7 @@ struct PromptArgs {
   int causal;
   float scale;
   void* out;  // [Tq][Hq][D]
-  int group;  // 1 << group heads share a workgroup (set by the launch)
+  int G, group;  // query heads of a key head; 1 << group of them share a workgroup (both set by the launch)
 };
 hipError_t launch_prompt(PromptArgs a, int dt, hipStream_t s);
 

@@ -5,6 +5,8 @@
 // Bound by the matrix cores.  A workgroup takes 128 rows, queries of up to four heads that share a key head, and sweeps the
 // keys they may see in tiles of 64: keys and values go straight into LDS, two tiles deep, while the waves, 32 queries of
 // one head each, work on the tile before.
+#include <algorithm>
+
 #include "attn.hpp"
 
 namespace qmm {
@@ -148,16 +150,14 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes + 16];
   int& met = *reinterpret_cast<int*>(lds + 4 * kBytes);
 
-  const int G = a.Hq / a.H;
   // key heads vary fastest: workgroup i runs on die i mod 8, so that a key head's rows stay in one die's L2 cache
-  const int64_t block = block_index();
-  const int groups = a.Hq >> a.group, hx = static_cast<int>(block % groups), kv = hx % a.H;
+  const int share = blockIdx.x / a.H, kv = blockIdx.x - share * a.H;
   const int rows = kRows >> a.group;  // queries of a head
-  const Work w = find_work(a, block / groups, __builtin_ctz(kRows) - a.group);
+  const Work w = find_work(a, static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y, __builtin_ctz(kRows) - a.group);
   if (!w.some) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
-  const int head0 = kv * G + (hx / a.H << a.group), head = head0 + (wave & (1 << a.group) - 1);
+  const int head0 = kv * a.G + (share << a.group), head = head0 + (wave & (1 << a.group) - 1);
   const float factor = a.scale * 1.44269504088896340736f;
   const int shift = w.m - w.n;  // query i sees keys 0 .. i + shift
   const int i0 = w.first + (wave >> a.group) * 32;
@@ -328,8 +328,9 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
 
 template <int DT, int DP>
 hipError_t prompt(const PromptArgs& a, hipStream_t s) {
-  const int64_t tiles = a.Tq / (kRows >> a.group) + a.B;  // indexes of tiles (find_work)
-  hipLaunchKernelGGL((k_prompt<DT, DP>), long_grid(tiles * (a.Hq >> a.group)), dim3(64 * kWaves), 0, s, a);
+  const int64_t tiles = a.Tq / (kRows >> a.group) + a.B, y = std::min<int64_t>(tiles, 65535);  // indexes of tiles (find_work)
+  const dim3 grid(a.Hq >> a.group, static_cast<unsigned>(y), static_cast<unsigned>((tiles + y - 1) / y));
+  hipLaunchKernelGGL((k_prompt<DT, DP>), grid, dim3(64 * kWaves), 0, s, a);
   return hipGetLastError();
 }
 
@@ -339,6 +340,7 @@ hipError_t launch_prompt(PromptArgs a, int dt, hipStream_t s) {
   // The query heads of a key head share a workgroup, four or two where their number allows it, so that its queries, 32 or 64
   // of each, end later in fewer tiles that they see in part.
   const int G = a.Hq / a.H;
+  a.G = G;
   a.group = G % 4 == 0 ? 2 : G % 2 == 0 ? 1 : 0;
   if (dt == DT_F16) {
     if (a.D <= 64) return prompt<DT_F16, 64>(a, s);
