@@ -72,12 +72,25 @@ __device__ __forceinline__ int64_t start_at(const int32_t* s, int64_t i, int64_t
 // for all of them, one index or none is left over, and no sum over the sequences before is needed.
 __device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index, int shift) {
   Work w{};
-  const int64_t b = count_first(a.B, [&](int64_t i) { return (start_at(a.q_starts, i, a.Tq) >> shift) + i <= index; }) - 1;
-  if (b < 0) return w;
-  w.q0 = start_at(a.q_starts, b, a.Tq);
-  w.n = static_cast<int>(start_at(a.q_starts, b + 1, a.Tq) - w.q0);
-  w.k0 = start_at(a.k_starts, b, a.Tk);
-  w.m = static_cast<int>(max(start_at(a.k_starts, b + 1, a.Tk) - w.k0, int64_t(0)));
+  int64_t b;
+  if (a.B < 64) {  // all starts in the wave's registers: one round trip to memory, not two
+    const int lane = threadIdx.x & 63, at = min(lane, static_cast<int>(a.B));
+    const int qs = static_cast<int>(start_at(a.q_starts, at, a.Tq)), ks = static_cast<int>(start_at(a.k_starts, at, a.Tk));
+    const int i = __popcll(__ballot(lane < a.B && (qs >> shift) + lane <= index)) - 1;
+    if (i < 0) return w;
+    w.q0 = __builtin_amdgcn_readlane(qs, i);
+    w.n = __builtin_amdgcn_readlane(qs, i + 1) - static_cast<int>(w.q0);
+    w.k0 = __builtin_amdgcn_readlane(ks, i);
+    w.m = max(__builtin_amdgcn_readlane(ks, i + 1) - static_cast<int>(w.k0), 0);
+    b = i;
+  } else {
+    b = count_first(a.B, [&](int64_t i) { return (start_at(a.q_starts, i, a.Tq) >> shift) + i <= index; }) - 1;
+    if (b < 0) return w;
+    w.q0 = start_at(a.q_starts, b, a.Tq);
+    w.n = static_cast<int>(start_at(a.q_starts, b + 1, a.Tq) - w.q0);
+    w.k0 = start_at(a.k_starts, b, a.Tk);
+    w.m = static_cast<int>(max(start_at(a.k_starts, b + 1, a.Tk) - w.k0, int64_t(0)));
+  }
   const int all = (w.n + (1 << shift) - 1) >> shift, mine = static_cast<int>(index - ((w.q0 >> shift) + b));
   // the last tile, which sees the most keys, first
   w.first = (all - 1 - mine) << shift;
