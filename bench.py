@@ -37,7 +37,8 @@ Also reported:
                 both token tiles, the batch of 2 x 65 tokens on 128 x 768 in all
                 five formats, the expert-indexed matvec at 2..24 tokens with ids
                 re-drawn per call and its matrix-core form at 64..1024 tokens,
-                and the GPU quantizer.
+                the GPU quantizer, and what the decode layer does between its
+                projections (norms, cache, attention).
 """
 
 import argparse
@@ -725,6 +726,49 @@ def extra_moe(torch, q, W, args):
             "prefill_tiled": {"workload": "same experts, fp16 tokens, qmm_gemm_id_tiled, auto tile", "results": pre}}
 
 
+def extra_attention(torch, q, W, args):
+    """Between the decode layer's projections (32 query and 8 key heads of 128, from their row counts): a decode step's
+    norms, rotation and cache write with the attention over the cache, rotated over > 1 GiB of caches; a prompt's attention."""
+    D = 128
+    Hq, H = W.DECODE_SHAPES[0][1] // D, W.DECODE_SHAPES[1][1] // D
+    page, length = 64, 4096
+    w, freq = torch.ones(D, device="cuda"), 1e6 ** (-torch.arange(0, D, 2, device="cuda") / D)
+    res = []
+    for kind in ("f16", "e4m3"):
+        for B in (1, 16):
+            row = 2 * H * (D + 4 if kind == "e4m3" else 2 * D)
+            copies = max(2, math.ceil(ROTATE_BYTES / (B * length * row)))
+            pages = B * length // page
+            caches = [q.KVCache.empty(pages, page, H, D, "e4m3" if kind == "e4m3" else torch.float16) for _ in range(copies)]
+            x = torch.randn((B, Hq + 2 * H, D), device="cuda")
+            qx, kx, vx = x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:]
+            table = torch.randperm(pages, device="cuda").to(torch.int32).view(B, -1)
+            fill = torch.randn((page, H, D), device="cuda")
+            for c in caches:
+                for p in range(pages):
+                    c.write(fill, fill, torch.arange(p * page, (p + 1) * page, dtype=torch.int32, device="cuda"))
+            lengths = torch.full((B,), length, dtype=torch.int32, device="cuda")
+            slots, positions = table[:, -1] * page + page - 1, lengths - 1
+
+            def step():
+                for c in caches:
+                    qr = c.norm_rope_write(qx, kx, vx, slots, positions, freq, w, w, dtype=torch.float16)
+                    c.attend(qr, table, lengths)
+            g = capture(torch, step)
+            us = time_graph(torch, g, args.rounds) * 1e3 / copies
+            del g
+            res.append({"cache": kind, "sequences": B, "length": length, "us_per_step": us,
+                        "cache_gbs": B * length * row / (us * 1e-6) / 1e9, "copies": copies})
+            del caches
+    T = 2048
+    x = torch.randn((T, Hq + 2 * H, D), device="cuda").to(torch.float16)
+    starts = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    g = capture(torch, lambda: q.attend_prompt(x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], starts))
+    us = time_graph(torch, g, args.rounds) * 1e3
+    return {"workload": f"{Hq} query and {H} key heads of {D}, fp32 projections, pages of {page}", "decode_step": res,
+            "prompt": {"tokens": T, "us": us, "tflops": 2 * Hq * D * T * (T + 1) / (us * 1e-6) / 1e12}}
+
+
 def extra_quantize(torch, q, W, mats, args):
     """The GPU quantizer on the decode layer's fp32 weights (regenerated from the
     same seeds), fp32 bytes read per second."""
@@ -1052,7 +1096,8 @@ def main():
                          ("prefill_batch_2x65", lambda: extra_prefill_batch(torch, q, W, args)),
                          ("formats", lambda: extra_formats(torch, q, W, args)),
                          ("expert_matvec", lambda: extra_moe(torch, q, W, args)),
-                         ("quantize", lambda: extra_quantize(torch, q, W, mats, args))):
+                         ("quantize", lambda: extra_quantize(torch, q, W, mats, args)),
+                         ("attention", lambda: extra_attention(torch, q, W, args))):
             t0 = time.time()
             extras[name] = fn()
             log(f"[bench] extra {name} done in {time.time() - t0:.1f}s")

@@ -35,6 +35,12 @@ __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint8_t* ds
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, voff, 0, 0, 0);
 }
 
+// Four rows' elements of a column, transposed on the way from LDS.  `restrict`: the compiler takes a read through a pointer
+// that it knows nothing of for one of what is on its way into LDS, and waits for the next tile.
+__device__ __forceinline__ i16x4 read_transposed(__attribute__((address_space(3))) i16x4* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+}
+
 // the larger (the sum) of a value and the one of the lane 32 further
 __device__ __forceinline__ float both_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -307,7 +313,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int row = u * 16 + e * 8 + half * 4 + (lane & 15) / 4, piece = d * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1);
-          x.w[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          x.w[e] = read_transposed(
               (__attribute__((address_space(3))) i16x4*)(lv + row * L::kRow + L::value(row, piece) * 16 + (lane & 1) * 8));
         }
         o[d] = mma(x.v, p[u], o[d]);
