@@ -262,6 +262,15 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
       for (int j = 0; j < DP / 16; ++j)
         s[k] = mma(*reinterpret_cast<const H8<DT>*>(lk + row * L::kRow + L::key(row, 2 * j + half) * 16), q[j], s[k]);
     }
+    // four reads ahead of the products (one or two, as the compiler has it: 2048 queries of 8 heads 43.0 -> 40.7 us, 8192 of 32
+    // 526 -> 519; eight: 41.9)
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+    for (int n = 0; n < DP / 8 - 4; ++n) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
     if (j0 + kKeys > whole) {
       const int seen = min(w.m, a.causal ? i0 + col + shift + 1 : w.m) - j0;  // keys of the tile that row col sees
 #pragma unroll
@@ -293,20 +302,12 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
       for (int k = 0; k < 2; ++k) s[k] *= factor;
       f = 1.0f;
     }
-    H8<DT> p[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = __builtin_amdgcn_exp2f(fmaf(s[u / 2][u % 2 * 8 + e], f, kLift - zero));
-        total += x;
-        p[u][e] = static_cast<T>(x);
-      }
     // ahead of the SIMD's other wave while the matrix cores have work (8192 tokens 538 -> 527 us)
     __builtin_amdgcn_s_setprio(1);
-    // key slots of step u: 16 u + 4 half + 0 .. 3 and 8 more, as the scores lie
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
+    // Step by step, so that the next step's exponentials run beside this one's products (all of P first: 2048 queries of 8 heads
+    // 45.0 us, not 43.0).  Key slots of step u: 16 u + 4 half + 0 .. 3 and 8 more, as the scores lie
+    H8<DT> vf[2][kOut];
+    auto read_values = [&](int u) {
 #pragma unroll
       for (int d = 0; d < kOut; ++d) {
         union { i16x4 w[2]; H8<DT> v; } x;
@@ -316,8 +317,23 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
           x.w[e] = read_transposed(
               (__attribute__((address_space(3))) i16x4*)(lv + row * L::kRow + L::value(row, piece) * 16 + (lane & 1) * 8));
         }
-        o[d] = mma(x.v, p[u], o[d]);
+        vf[u & 1][d] = x.v;
       }
+    };
+    read_values(0);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      H8<DT> p;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(s[u / 2][u % 2 * 8 + e], f, kLift - zero));
+        total += x;
+        p[e] = static_cast<T>(x);
+      }
+      if (u < 3) read_values(u + 1);
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) o[d] = mma(vf[u & 1][d], p, o[d]);
+    }
     __builtin_amdgcn_s_setprio(0);
   }
   total = both_sum(total);
