@@ -100,7 +100,7 @@ __device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index, in
   const int all = (w.n + (1 << shift) - 1) >> shift, mine = static_cast<int>(index - ((w.q0 >> shift) + b));
   // the last tile, which sees the most keys, first
   w.first = (all - 1 - mine) << shift;
-  w.some = w.n > 0 && mine < all;
+  w.some = w.n > 0 && mine >= 0 && mine < all;  // (below 0 only where starts decrease)
   return w;
 }
 

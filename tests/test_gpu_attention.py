@@ -742,3 +742,86 @@ def test_cache_handles():
     assert all(torch.equal(a, b) for a, b in zip(other.read(rows, i32([0, 20]), 20, dtype=torch.float32), want))
     codes = q.KVCache(other.k.view(torch.float8_e4m3fn), other.v.view(torch.float8_e4m3fn), other.k_scales, other.v_scales)
     assert all(torch.equal(a, b) for a, b in zip(codes.read(rows, i32([0, 20]), 20, dtype=torch.float32), want))
+
+
+def test_starts_that_decrease_stay_inside():
+    """Not allowed, and harmless: rows of the tensors only, some of them written."""
+    g = np.random.default_rng(91)
+    T = 700
+    qx, k, v = prompt_inputs(g, [T], [T], 4, 2, 64, torch.bfloat16, False)
+    guard = torch.full((T + 64, 4, 64), 9.0, device="cuda", dtype=torch.bfloat16)
+    c = blank(50, 16, 2, 64, "bf16")
+    c.write(k, v, i32(range(T)))
+    rows = i32(range(44)).view(1, 44).expand(4, 44).contiguous()
+    for s in ([0, 300, 100, 700, 650], [700, 0, 700, 0, 700], [0, -50, 2 ** 31 - 1, -(2 ** 31), 40], [500, 400, 300, 200, 100]):
+        out = guard[32:T + 32]
+        q.attend_prompt(qx, k, v, i32(s), out=out)
+        assert bool((guard[:32] == 9).all()) and bool((guard[T + 32:] == 9).all())
+        assert bool(torch.isfinite(guard).all())
+        into = tuple(torch.full((T + 64, 2, 64), 9.0, device="cuda") for _ in "kv")
+        c.read(rows, i32(s), T, out=tuple(t[32:T + 32] for t in into))
+        assert all(bool((t[:32] == 9).all()) and bool((t[T + 32:] == 9).all()) for t in into)
+
+
+def test_refusals_on_the_device():
+    def refused(text, fn):
+        with pytest.raises((ValueError, q.QmmError), match=text):
+            fn()
+
+    def z(*shape, dtype=torch.float16):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+
+    x, w, pos, freq = z(5, 4, 32), z(32, dtype=torch.float32), i32([0] * 5), z(16, dtype=torch.float32)
+    refused("k has shape", lambda: q.head_norm_rope(x, z(4, 4, 32), None, None))
+    refused("k has shape", lambda: q.head_norm_rope(x, z(5, 4, 16), None, None))
+    refused("k has dtype", lambda: q.head_norm_rope(x, x.float(), None, None))
+    refused("contiguous last axis", lambda: q.head_norm_rope(z(5, 4, 64)[..., ::2], x, None, None))
+    refused("needs positions", lambda: q.head_norm_rope(x, x, None, freq))
+    refused("positions has 4", lambda: q.head_norm_rope(x, x, pos[:4], freq))
+    refused("positions has dtype", lambda: q.head_norm_rope(x, x, pos.long(), freq))
+    refused("inv_freq has dtype", lambda: q.head_norm_rope(x, x, pos, freq.half()))
+    refused("inv_freq must be contiguous", lambda: q.head_norm_rope(x, x, pos, z(32, dtype=torch.float32)[::2]))
+    refused("R=34", lambda: q.head_norm_rope(x, x, pos, z(17, dtype=torch.float32)))
+    refused("R=4 ", lambda: q.head_norm_rope(x, x, pos, z(2, dtype=torch.float32)))
+    refused("q_weight has 16", lambda: q.head_norm_rope(x, x, None, None, w[:16], w))
+    refused("k_weight has dtype", lambda: q.head_norm_rope(x, x, None, None, w, w.half()))
+    refused("q_weight has dtype", lambda: q.head_norm_rope(x, x, None, None, w.double(), w))
+    refused("eps", lambda: q.head_norm_rope(x, x, None, None, w, w, eps=-1.0))
+    refused("dtype", lambda: q.head_norm_rope(x, x, None, None, dtype=torch.float64))
+    refused("D=24", lambda: q.head_norm_rope(z(5, 4, 24), z(5, 4, 24), None, None))
+    for shape, text in (((4, 2, 24, 32), "power of two"), ((4, 2, 8, 32), "page=8"), ((4, 2, 16, 40), "D=40"), ((4, 2, 16, 272), "D=272")):
+        refused(text, lambda: q.KVCache(z(*shape), z(*shape)))
+    flat = z(4 * 2 * 16 * 32 + 4)
+    refused("16-byte", lambda: q.KVCache(flat[4:].view(4, 2, 16, 32), z(4, 2, 16, 32)))
+    refused("must be contiguous", lambda: q.KVCache(z(4, 16, 2, 32).transpose(1, 2), z(4, 2, 16, 32)))
+    c = q.KVCache.empty(4, 16, 2, 32, torch.float16)
+    k = z(5, 2, 32)
+    refused("the cache has 2 of 32", lambda: c.write(x, x, pos))
+    refused("v has shape", lambda: c.write(k, z(4, 2, 32), pos))
+    refused("slots has 4", lambda: c.write(k, k, pos[:4]))
+    refused("slots has dtype", lambda: c.write(k, k, pos.long()))
+    refused("slots must be a device", lambda: c.write(k, k, pos.cpu()))
+    refused("the cache has torch.float16", lambda: c.norm_rope_write(x, k, k, pos, None, None, dtype=torch.bfloat16))
+    refused("k has dtype", lambda: c.norm_rope_write(x, k.float(), k.float(), pos, None, None))
+    table, n = i32(range(4)).view(2, 2), i32([3, 3])
+    refused("the cache has 2 of 32", lambda: c.attend(z(2, 3, 32), table, n))
+    refused("the cache has 2 of 32", lambda: c.attend(z(2, 4, 16), table, n))
+    refused("the cache has torch.float16", lambda: c.attend(z(2, 4, 32, dtype=torch.bfloat16), table, n))
+    refused("table has 2 rows", lambda: c.attend(z(3, 4, 32), table, i32([1, 1, 1])))
+    refused("lengths has 3", lambda: c.attend(z(2, 4, 32), table, i32([1, 1, 1])))
+    refused("out has shape", lambda: c.attend(z(2, 4, 32), table, n, out=z(2, 4, 16)))
+    refused("out must have q's dtype", lambda: c.attend(z(2, 4, 32), table, n, out=z(2, 4, 32, dtype=torch.bfloat16)))
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        refused("scale", lambda: c.attend(z(2, 4, 32), table, n, scale=scale))
+        refused("scale", lambda: q.attend_prompt(x, x, x, i32([0, 5]), scale=scale))
+    refused("negative", lambda: c.read(table, i32([0, 1, 2]), -1))
+    refused("two tensors", lambda: c.read(table, i32([0, 1, 2]), 2, out=(z(2, 2, 32), z(2, 2, 32).float())))
+    refused("k has 3 heads", lambda: q.attend_prompt(x, z(5, 3, 32), z(5, 3, 32), i32([0, 5])))
+    refused("v has shape", lambda: q.attend_prompt(x, k, z(5, 1, 32), i32([0, 5])))
+    refused("need k_starts", lambda: q.attend_prompt(x, z(7, 2, 32), z(7, 2, 32), i32([0, 5])))
+    refused("k_starts has 3", lambda: q.attend_prompt(x, k, k, i32([0, 5]), i32([0, 2, 5])))
+    wide = z(5, 2 * 32 + 8)
+    refused("16-byte", lambda: q.attend_prompt(x, wide[:, 4:68].unflatten(1, (2, 32)), k, i32([0, 5])))
+    refused("token stride", lambda: q.attend_prompt(x, z(1, 2, 32).expand(5, 2, 32), k, i32([0, 5])))
+    got = q.attend_prompt(x, k[:, :1].expand(5, 2, 32), k, i32([0, 5]))  # heads may share their rows
+    assert got.shape == x.shape
