@@ -25,12 +25,16 @@ import struct
 import torch
 
 from ._lib import check, lib
-from .f8 import _DT, _call, _empty, _out, _place, _shape, _tensor
+from .f8 import _DT, _call, _current_device, _current_stream, _empty, _out, _place, _shape, _tensor
+
+try:
+    from . import _calls  # csrc/calls.cpp
+except ImportError:  # another torch than it was built against: the same calls, through ctypes
+    _calls = None
 
 _HALF = {torch.float16: 1, torch.bfloat16: 2}
 _CACHE = {torch.float16: 1, torch.bfloat16: 2, torch.uint8: 3, torch.float8_e4m3fn: 3}
 _INT = torch.int32
-_I32 = (torch.int32,)
 _F32 = (torch.float32,)
 
 # the argument structs of include/qmm.h
@@ -42,54 +46,39 @@ _pack_prompt = struct.Struct("18q2if4x").pack
 
 
 # --- argument checks ---------------------------------------------------------------------------
-# A tensor that passes is looked at in as few steps as possible (a step is some 70 ns of host time, and a decode step's
-# call takes less on the device than on the host); one that does not goes through the slow checks, which say why.
+# _calls makes the checks of a call that is as it should be, and the call; a decode step's takes a few microseconds on the
+# device, and here as long.  What it declines comes here, to be told what is wrong, or to be made: a tensor of a subclass,
+# one on another device than the current one, an `out`.
+
+def _here(x):
+    """The current device, where native calls are made, if the tensor x lies there, else -1."""
+    try:
+        d = x.get_device()
+    except AttributeError:
+        return -1
+    return d if _calls is not None and d >= 0 and d == _current_device() else -1
+
 
 def _heads(x, name, dtypes, device=None):
     """(device, T, heads, D, stride of a token, stride of a head) of a [T, heads, D] device tensor."""
-    try:
-        T, H, D = x.shape
-        st, sh, step = x.stride()
-        d = x.get_device()
-        if x.dtype in dtypes and step == 1 and d >= 0 and (device is None or d == device):
-            return d, T, H, D, st, sh
-    except (AttributeError, TypeError, ValueError):
-        pass
     _tensor(x, name, dtypes, (3,))
     d = x.get_device()
     if d < 0:
         raise ValueError(f"{name} must be a device tensor")
     if device is not None and d != device:
         raise ValueError(f"{name} is on cuda:{d}; expected cuda:{device}")
-    if x.shape[2] > 1:
+    if x.stride(2) != 1 and x.shape[2] > 1:
         raise ValueError(f"{name} must have a contiguous last axis")
     return (d, *x.shape, *x.stride()[:2])
 
 
 def _vector(t, name, dtype, length, device):
     """Pointer of a contiguous vector of `length` elements on device."""
-    try:
-        if t.dtype is dtype and t.shape == (length,) and t.get_device() == device and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
     _tensor(t, name, (dtype,), (1,))
     if t.shape[0] != length:
         raise ValueError(f"{name} has {t.shape[0]} elements; expected {length}")
     _place(device, (t, name))
     return t.data_ptr()
-
-
-def _length(t, name, dtype):
-    """Elements of a vector; where it lies, _vector looks at."""
-    try:
-        (n,) = t.shape
-        if t.dtype is dtype:
-            return n
-    except (AttributeError, TypeError, ValueError):
-        pass
-    _tensor(t, name, (dtype,), (1,))
-    return t.shape[0]
 
 
 def _rotation(positions, inv_freq, T, device):
@@ -98,7 +87,8 @@ def _rotation(positions, inv_freq, T, device):
         return 0, 0, 0
     if positions is None:
         raise ValueError("inv_freq needs positions")
-    n = _length(inv_freq, "inv_freq", torch.float32)
+    _tensor(inv_freq, "inv_freq", _F32, (1,))
+    n = inv_freq.shape[0]
     return _vector(positions, "positions", _INT, T, device), _vector(inv_freq, "inv_freq", torch.float32, n, device), 2 * n
 
 
@@ -122,6 +112,11 @@ def head_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=
     """(q', k'): every head of q [T, Hq, D] and k [T, H, D] divided by its root mean square and multiplied by its weight [D]
     (None: no norm), then its first 2 len(inv_freq) columns rotated by positions [T] (int32) times inv_freq (fp32; None: no
     rotation), column i with column i + len(inv_freq), or 2 i with 2 i + 1 where interleaved.  dtype: of the results."""
+    d = _here(q)
+    if d >= 0:
+        made = _calls.head_norm_rope(d, _current_stream(d), q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype)
+        if made is not None:
+            return made
     d, T, Hq, D, qt, qh = _heads(q, "q", _DT)
     xt = q.dtype
     _, Tk, H, Dk, kt, kh = _heads(k, "k", (xt,), d)
@@ -164,12 +159,14 @@ class KVCache:
         self.device = _place(None, *named)
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.dtype = k.dtype if k.dtype in _HALF else torch.float8_e4m3fn
-        self._sizes = {}
         h = ctypes.c_void_p()
         with torch.cuda.device(self.device):
             check(lib.qmm_cache_create(ctypes.byref(h), *(t.data_ptr() for t, _ in named), *([None] * (4 - len(named))),
                                        _CACHE[k.dtype], self.pages, self.page, self.heads, self.D))
         self._h = h
+        # what the native calls take of it
+        self._id = h.value, self.heads, self.D
+        self._type = _CACHE[k.dtype]
 
     @classmethod
     def empty(cls, pages, page, heads, D, dtype=torch.bfloat16, device="cuda"):
@@ -185,6 +182,7 @@ class KVCache:
 
     def close(self):
         h, self._h = getattr(self, "_h", None), None
+        self._id = 0, 0, 0
         if h is not None and h.value is not None:
             lib.qmm_cache_destroy(h)
 
@@ -216,6 +214,9 @@ class KVCache:
     def write(self, k, v, slots):
         """k and v [T, heads, D] to slots [T] (int32; negative ones and those past the last page are left out).  The slots
         of a call are distinct."""
+        d = self.device
+        if _here(k) == d and _calls.write(d, _current_stream(d), *self._id, k, v, slots):
+            return
         xt, T, kt, kh, vt, vh = self._kv(k, v)
         at = _vector(slots, "slots", _INT, T, self.device)
         _call(self.device, lib.qmm_cache_write, self._h, _pack_write(k.data_ptr(), v.data_ptr(), at, kt, kh, vt, vh, T, _DT[xt]))
@@ -225,6 +226,11 @@ class KVCache:
         """head_norm_rope of q and k, then write of the keys and of v, in one launch and with the same bits; returns q'.
         dtype: of q' and, before they are quantized, of the keys; the cache's own unless that is e4m3 (then q's)."""
         d = self.device
+        if _here(q) == d:
+            made = _calls.norm_rope_write(d, _current_stream(d), *self._id, self._type, q, k, v, slots, positions, inv_freq, q_weight,
+                                          k_weight, eps, interleaved, dtype)
+            if made is not None:
+                return made
         _, T, Hq, D, qt, qh = _heads(q, "q", _DT, d)
         xt, Tk, kt, kh, vt, vh = self._kv(k, v)
         if xt != q.dtype:
@@ -247,13 +253,7 @@ class KVCache:
         return o
 
     def _table(self, table, B):
-        try:
-            n, W = table.shape
-            if n == B and table.dtype is _INT and table.get_device() == self.device and table.is_contiguous():
-                return table.data_ptr(), W
-        except (AttributeError, ValueError):
-            pass
-        _tensor(table, "table", _I32, (2,))
+        _tensor(table, "table", (_INT,), (2,))
         if table.shape[0] != B:
             raise ValueError(f"table has {table.shape[0]} rows; expected {B}")
         _place(self.device, (table, "table"))
@@ -262,10 +262,15 @@ class KVCache:
     def read(self, table, starts, total, dtype=None, out=None):
         """(k, v) [total, heads, D]: sequence b's tokens as rows starts[b] .. starts[b + 1] - 1 (starts int32 [B + 1], not
         decreasing).  Rows of no sequence are not written: they stay as they were in `out`, a pair of tensors."""
-        B = _length(starts, "starts", _INT) - 1
+        d = self.device
+        if out is None and _here(table) == d:
+            made = _calls.read(d, _current_stream(d), *self._id, self._type, table, starts, total, dtype)
+            if made is not None:
+                return made
+        _tensor(starts, "starts", (_INT,), (1,))
+        B = starts.shape[0] - 1
         if B < 0:
             raise ValueError("starts is empty")
-        d = self.device
         at, W = self._table(table, B)
         first = _vector(starts, "starts", _INT, B + 1, d)
         total = int(total)
@@ -292,6 +297,10 @@ class KVCache:
         default.  max_length: the longest length where the host knows it, else the table's reach; it decides how the work
         is divided and nothing else."""
         d = self.device
+        if out is None and _here(q) == d:
+            made = _calls.attend(d, _current_stream(d), *self._id, self._type, self.page, q, table, lengths, scale, max_length)
+            if made is not None:
+                return made
         _, B, Hq, D, qt, qh = _heads(q, "q", _HALF, d)
         t = q.dtype
         if D != self.D or Hq == 0 or Hq % self.heads:
@@ -303,12 +312,7 @@ class KVCache:
         bound = W * self.page
         if max_length is not None and max_length < bound:
             bound = max(int(max_length), 0)
-        key = B, Hq, bound
-        nb = self._sizes.get(key)
-        if nb is None:
-            if len(self._sizes) >= 1024:
-                self._sizes.clear()
-            nb = self._sizes[key] = lib.qmm_cache_attend_workspace_bytes(self._h, B, Hq, bound)
+        nb = lib.qmm_cache_attend_workspace_bytes(self._h, B, Hq, bound)
         if out is None:
             out = _empty((B, Hq, D), t, d)
         elif _out(out, (B, Hq, D), None, d).dtype != t:
@@ -325,6 +329,11 @@ def attend_prompt(q, k, v, starts, k_starts=None, causal=True, scale=None, out=N
     multiple of H.  Sequence b has the queries from starts[b] and the keys from k_starts[b] on (int32 [B + 1], not
     decreasing; k_starts: starts by default).  causal: query i of n sees the keys 0 .. i + m - n of its m; one that sees
     none gives zeros.  Rows of no sequence are not written: they stay as they were in `out`."""
+    d = _here(q)
+    if out is None and d >= 0:
+        made = _calls.attend_prompt(d, _current_stream(d), q, k, v, starts, k_starts, causal, scale)
+        if made is not None:
+            return made
     d, Tq, Hq, D, qt, qh = _heads(q, "q", _HALF)
     t = q.dtype
     _, Tk, H, Dk, kt, kh = _heads(k, "k", (t,), d)
@@ -333,7 +342,8 @@ def attend_prompt(q, k, v, starts, k_starts=None, causal=True, scale=None, out=N
         raise ValueError(f"k has {H} heads of {Dk}; q has {Hq} of {D}")
     if Tv != Tk or Hv != H or Dv != D:
         raise ValueError(f"v has shape {tuple(v.shape)}; k has {tuple(k.shape)}")
-    n = _length(starts, "starts", _INT)
+    _tensor(starts, "starts", (_INT,), (1,))
+    n = starts.shape[0]
     if n < 1:
         raise ValueError("starts is empty")
     qs = _vector(starts, "starts", _INT, n, d)

@@ -1,9 +1,10 @@
-"""Build libqmm.so (the C-ABI library) for gfx950 with hipcc, in-tree.
+"""Build libqmm.so (the C-ABI library) for gfx950 with hipcc, and _calls.so (the binding's native calls), in-tree.
 
     python block_quantized_weight_matmul_amd/build.py [-v]
 
 Every HIP source under csrc/ is compiled to an object under _build/ (in
-parallel), then linked into block_quantized_weight_matmul_amd/libqmm.so.
+parallel), then linked into block_quantized_weight_matmul_amd/libqmm.so; csrc/calls.cpp,
+host code against Python's and torch's headers, into _calls.so next to it.
 Cross-compiles without a GPU.
 """
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqmm.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = "gfx950"
 FLAGS = [
@@ -54,19 +57,39 @@ def _compile(src, verbose):
     return obj
 
 
+def _run(cmd, what, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}")
+
+
+def _compile_calls(verbose):
+    from torch.utils import cpp_extension
+    obj = os.path.join(BUILD, "calls.host.o")
+    paths = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden", *(a for p in paths for a in ("-I", p)), "-c",
+          os.path.join(CSRC, "calls.cpp"), "-o", obj], "g++ on calls.cpp", verbose)
+    libs = [a for p in cpp_extension.library_paths() for a in ("-L", p)]
+    return [obj, "-L", PKG, "-lqmm", *libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(verbose=False, jobs=None):
-    """Compile every HIP source and link libqmm.so; returns the library path."""
+    """Compile every source and link libqmm.so and _calls.so; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs), os.cpu_count() or 1, 16)
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
+        calls = ex.submit(_compile_calls, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        calls = calls.result()
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
-    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}")
+    _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], "link", verbose)
     os.replace(tmp, LIB)
+    tmp = CALLS + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, *calls], "link of _calls.so", verbose)
+    os.replace(tmp, CALLS)
     return LIB
 
 

@@ -24,7 +24,8 @@ def meta(*shape, dtype=H):
 
 def cache(pages=4, page=16, heads=2, D=32, dtype=H):
     c = object.__new__(q.KVCache)
-    c.pages, c.page, c.heads, c.D, c.dtype, c.device, c._h, c._sizes = pages, page, heads, D, dtype, 0, None, {}
+    c.pages, c.page, c.heads, c.D, c.dtype, c.device, c._h = pages, page, heads, D, dtype, 0, None
+    c._id, c._type = (0, heads, D), 1
     c.k = c.v = c.k_scales = c.v_scales = None
     return c
 

@@ -763,6 +763,31 @@ def test_starts_that_decrease_stay_inside():
         assert all(bool((t[:32] == 9).all()) and bool((t[T + 32:] == 9).all()) for t in into)
 
 
+def test_calls_through_ctypes_are_the_same(monkeypatch):
+    """What the native calls decline is made in Python: with the same results."""
+    from block_quantized_weight_matmul_amd import attention
+    assert attention._calls is not None
+    g = np.random.default_rng(92)
+    c, table, _, _ = filled(g, [500, 300], 16, 2, 64, "e4m3")
+    other, tab, n = copy.deepcopy(c), i32(table.flatten()).view(2, -1), i32([500, 300])
+    qx, kx, vx = head_inputs(g, 2, 4, 2, 64, torch.bfloat16, True)
+    pos, freq, w = i32([499, 299]), dev(frequencies(64)), dev(1 + g.random(64))
+    slots = i32([int(table[0, 499 // 16]) * 16 + 499 % 16, int(table[1, 299 // 16]) * 16 + 299 % 16])
+    ps, pk = starts([1, 1]), starts([500, 300])
+
+    def step(c):
+        c.write(kx, vx, slots)
+        qr = c.norm_rope_write(qx, kx, vx, slots, pos, freq, w, w, interleaved=True, dtype=torch.float16)
+        k, v = c.read(tab, pk, 800, dtype=torch.float16)
+        return (*q.head_norm_rope(qx, kx, pos, freq, w, None, eps=1e-5, dtype=torch.float32), qr, k, v,
+                c.attend(qr, tab, n), c.attend(qr, tab, n, scale=0.5, max_length=300), q.attend_prompt(qr, k, v, ps, pk, scale=0.2),
+                q.attend_prompt(qr, k, v, ps, pk, causal=False), c.read(tab, pk, 800)[0], c.k, c.v, c.k_scales, c.v_scales)
+
+    native = step(c)
+    monkeypatch.setattr(attention, "_calls", None)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(native, step(other), strict=True))
+
+
 def test_refusals_on_the_device():
     def refused(text, fn):
         with pytest.raises((ValueError, q.QmmError), match=text):
