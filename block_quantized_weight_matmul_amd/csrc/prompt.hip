@@ -6,6 +6,7 @@
 // keys they may see in tiles of 64: keys and values go straight into LDS, two tiles deep, while the waves, 32 queries of
 // one head each, work on the tile before.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.hpp"
 
@@ -104,49 +105,6 @@ __device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index, in
   return w;
 }
 
-// One row at a time, with nothing of a key that the row does not see: for a workgroup that met an infinity or a NaN among
-// the values of a tile which some of its rows see in part.  (A product of matrices adds 0 * Inf = NaN to the others.)
-template <int DT, int DP>
-__device__ void careful_rows(const PromptArgs& a, const Work& w, int head0, int kv, float factor) {
-  typedef typename Elem<DT>::T T;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  constexpr int kOwn = DP / 64;
-  for (int r = wave; r < kRows; r += kWaves) {
-    const int block = r / 32, head = head0 + (block & (1 << a.group) - 1), i = w.first + (block >> a.group) * 32 + r % 32;
-    if (i >= w.n) continue;
-    const int seen = min(w.m, a.causal ? max(0, i + (w.m - w.n) + 1) : w.m);
-    const T* q = static_cast<const T*>(a.q.p) + (w.q0 + i) * a.q.st + head * a.q.sh;
-    float most = -INFINITY, total = 0.0f, o[kOwn] = {};
-    for (int j0 = 0; j0 < seen; j0 += 64) {
-      const int j = min(j0 + lane, seen - 1);
-      const T* k = static_cast<const T*>(a.k.p) + (w.k0 + j) * a.k.st + kv * a.k.sh;
-      float s = 0.0f;
-      for (int d = 0; d < a.D; ++d) s = fmaf(static_cast<float>(q[d]), static_cast<float>(k[d]), s);
-      s = j0 + lane < seen ? s * factor : -INFINITY;
-      float top = s;
-      for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-      top = fmaxf(most, top);
-      const float zero = top == -INFINITY ? 0.0f : top, shrink = __builtin_amdgcn_exp2f(most - zero);
-      most = top;
-      const float p = __builtin_amdgcn_exp2f(s - zero);
-      float sum = p;
-      for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
-      total = total * shrink + sum;
-      for (int e = 0; e < kOwn; ++e) o[e] *= shrink;
-      for (int n = 0; n < min(64, seen - j0); ++n) {
-        const T* v = static_cast<const T*>(a.v.p) + (w.k0 + j0 + n) * a.v.st + kv * a.v.sh;
-        const float pn = __shfl(p, n);
-        for (int e = 0; e < kOwn; ++e)
-          if (e * 64 + lane < a.D) o[e] = fmaf(pn, static_cast<float>(v[e * 64 + lane]), o[e]);
-      }
-    }
-    T* out = static_cast<T*>(a.out) + ((w.q0 + i) * a.Hq + head) * a.D;
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    for (int e = 0; e < kOwn; ++e)
-      if (e * 64 + lane < a.D) out[e * 64 + lane] = static_cast<T>(o[e] * inv);
-  }
-}
-
 // DT: type of everything but the sums; DP: columns, D rounded up to 64, 128 or 256.
 //
 // Scores are computed transposed, S^T = K Q^T (keys x queries): a lane then holds, for one query, the scores of the keys
@@ -232,116 +190,162 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
 #pragma unroll
   for (int d = 0; d < kOut; ++d) o[d] = f32x16{};
 
-  if (count > 0) load_tile(0);
-  for (int i = 0; i < count; ++i) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this tile's loads, issued a tile ago
-    __syncthreads();
-    if (i + 1 < count) load_tile(i + 1);
-    const uint8_t* const lk = lds + (i & 1) * 2 * kBytes;
-    const uint8_t* const lv = lk + kBytes;
-    const int j0 = i * kKeys;
-    if (a.causal && j0 + kKeys > whole_all) {  // rows see parts of this tile: infinities and NaN among its values
-      uint32_t worst = 0;
-#pragma unroll
-      for (int n = 0; n < kLoads; ++n) {
-        const uint4 x = *reinterpret_cast<const uint4*>(lv + (wave * kLoads + n) * 1024 + lane * 16);
-        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) worst = max(worst, max(y[e] << 1 & 0xFFFFu, y[e] >> 15 & 0xFFFEu));
+  auto sweep = [&](auto careful) {
+    constexpr bool kCareful = decltype(careful)::value;
+    if (!kCareful && count > 0) load_tile(0);
+    for (int i = 0; i < count; ++i) {
+      int lane = threadIdx.x & 63;
+      if constexpr (kCareful) asm volatile("" : "+v"(lane));  // addresses made where they are used: no registers are left
+      const int col = lane & 31, half = lane >> 5;
+      if constexpr (kCareful) {
+        __syncthreads();  // the tile before, and the probabilities beside it, are done with
+        load_tile(i);
       }
-      if (__any(worst >= (DT == DT_F16 ? 0xF800u : 0xFF00u))) met = 1;
-    }
-    if (j0 >= mine) continue;  // this wave's rows see nothing of it (nor of later ones)
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this tile's loads, issued a tile ago
+      __syncthreads();
+      if (!kCareful && i + 1 < count) load_tile(i + 1);
+      const uint8_t* const lk = lds + (i & 1) * 2 * kBytes;
+      const uint8_t* const lv = lk + kBytes;
+      const int j0 = i * kKeys;
+      if (!kCareful && a.causal && j0 + kKeys > whole_all) {  // rows see parts of this tile: infinities and NaN among its values
+        uint32_t worst = 0;
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) {
+          const uint4 x = *reinterpret_cast<const uint4*>(lv + (wave * kLoads + n) * 1024 + lane * 16);
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) worst = max(worst, max(y[e] << 1 & 0xFFFFu, y[e] >> 15 & 0xFFFEu));
+        }
+        if (__any(worst >= (DT == DT_F16 ? 0xF800u : 0xFF00u))) met = 1;
+      }
+      if (j0 >= mine) continue;  // this wave's rows see nothing of it (nor of later ones)
 
-    f32x16 s[2];
+      f32x16 s[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      s[k] = f32x16{};
-      const int row = k * 32 + col;
+      for (int k = 0; k < 2; ++k) {
+        s[k] = f32x16{};
+        const int row = k * 32 + col;
 #pragma unroll
-      for (int j = 0; j < DP / 16; ++j)
-        s[k] = mma(*reinterpret_cast<const H8<DT>*>(lk + row * L::kRow + L::key(row, 2 * j + half) * 16), q[j], s[k]);
-    }
-    // four reads ahead of the products (one or two, as the compiler has it: 2048 queries of 8 heads 43.0 -> 40.7 us, 8192 of 32
-    // 526 -> 519; eight: 41.9)
-    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+        for (int j = 0; j < DP / 16; ++j)
+          s[k] = mma(*reinterpret_cast<const H8<DT>*>(lk + row * L::kRow + L::key(row, 2 * j + half) * 16), q[j], s[k]);
+      }
+      // four reads ahead of the products (one or two, as the compiler has it: 2048 queries of 8 heads 43.0 -> 40.7 us, 8192 of 32
+      // 526 -> 519; eight: 41.9)
+      __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
-    for (int n = 0; n < DP / 8 - 4; ++n) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
-    if (j0 + kKeys > whole) {
-      const int seen = min(w.m, a.causal ? i0 + col + shift + 1 : w.m) - j0;  // keys of the tile that row col sees
+      for (int n = 0; n < DP / 8 - 4; ++n) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+      if (j0 + kKeys > whole) {
+        const int seen = min(w.m, a.causal ? i0 + col + shift + 1 : w.m) - j0;  // keys of the tile that row col sees
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (k * 32 + e / 4 * 8 + half * 4 + e % 4 >= seen) s[k][e] = -INFINITY;
+      }
+      float top = -INFINITY;
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (k * 32 + e / 4 * 8 + half * 4 + e % 4 >= seen) s[k][e] = -INFINITY;
-    }
-    float top = -INFINITY;
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[k][e]);
+      top = both_max(top) * factor;  // factor > 0
+      if (__any(top > most + kSlack)) {
+        top = fmaxf(most, top);
+        zero = top == -INFINITY ? 0.0f : top;  // nothing but -inf so far: exp of it is 0
+        const float shrink = __builtin_amdgcn_exp2f(most - zero);
+        most = top;
+        total *= shrink;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+        for (int d = 0; d < kOut; ++d) o[d] *= shrink;
+        // scores so large that the rounding of the maximum, which the fma below does not share, would show
+        huge = __any(fabsf(top) > 0x1p20f && fabsf(top) < INFINITY);
+      }
+      float f = factor;
+      if (huge) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[k][e]);
-    top = both_max(top) * factor;  // factor > 0
-    if (__any(top > most + kSlack)) {
-      top = fmaxf(most, top);
-      zero = top == -INFINITY ? 0.0f : top;  // nothing but -inf so far: exp of it is 0
-      const float shrink = __builtin_amdgcn_exp2f(most - zero);
-      most = top;
-      total *= shrink;
+        for (int k = 0; k < 2; ++k) s[k] *= factor;
+        f = 1.0f;
+      }
+      if constexpr (kCareful) {
+        if (j0 + kKeys > whole) {
+          // Key by key, each added to the rows that see it.  The probabilities pass through the other tile's room.
+          T* const pw = reinterpret_cast<T*>(lds + ((i + 1) & 1) * 2 * kBytes) + wave * kKeys * 32;
 #pragma unroll
-      for (int d = 0; d < kOut; ++d) o[d] *= shrink;
-      // scores so large that the rounding of the maximum, which the fma below does not share, would show
-      huge = __any(fabsf(top) > 0x1p20f && fabsf(top) < INFINITY);
-    }
-    float f = factor;
-    if (huge) {
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) s[k] *= factor;
-      f = 1.0f;
-    }
-    // ahead of the SIMD's other wave while the matrix cores have work (8192 tokens 538 -> 527 us)
-    __builtin_amdgcn_s_setprio(1);
-    // Step by step, so that the next step's exponentials run beside this one's products (all of P first: 2048 queries of 8 heads
-    // 45.0 us, not 43.0).  Key slots of step u: 16 u + 4 half + 0 .. 3 and 8 more, as the scores lie
-    H8<DT> vf[2][kOut];
-    auto read_values = [&](int u) {
+            for (int e = 0; e < 16; ++e) {
+              const float x = __builtin_amdgcn_exp2f(fmaf(s[k][e], f, kLift - zero));
+              total += x;
+              pw[(k * 32 + e / 4 * 8 + half * 4 + e % 4) * 32 + col] = static_cast<T>(x);
+            }
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          const int seen = min(w.m, i0 + col + shift + 1) - j0;
+#pragma unroll 1
+          for (int j = 0; j < kKeys; ++j) {
+            if (j >= seen) continue;
+            const float x = static_cast<float>(pw[j * 32 + col]);
 #pragma unroll
-      for (int d = 0; d < kOut; ++d) {
-        union { i16x4 w[2]; H8<DT> v; } x;
+            for (int d = 0; d < kOut * 4; ++d) {
+              typedef T V4 __attribute__((ext_vector_type(4)));
+              const V4 v = *reinterpret_cast<const V4*>(lv + j * L::kRow + L::value(j, d) * 16 + half * 8);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = u * 16 + e * 8 + half * 4 + (lane & 15) / 4, piece = d * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1);
-          x.w[e] = read_transposed(
-              (__attribute__((address_space(3))) i16x4*)(lv + row * L::kRow + L::value(row, piece) * 16 + (lane & 1) * 8));
+              for (int e = 0; e < 4; ++e) o[d / 4][d % 4 * 4 + e] = fmaf(x, static_cast<float>(v[e]), o[d / 4][d % 4 * 4 + e]);
+              __builtin_amdgcn_sched_barrier(0);  // a read at a time: registers again
+            }
+          }
+          continue;
         }
-        vf[u & 1][d] = x.v;
       }
-    };
-    read_values(0);
+      // ahead of the SIMD's other wave while the matrix cores have work (8192 tokens 538 -> 527 us)
+      __builtin_amdgcn_s_setprio(1);
+      // Step by step, so that the next step's exponentials run beside this one's products (all of P first: 2048 queries of 8 heads
+      // 45.0 us, not 43.0).  Key slots of step u: 16 u + 4 half + 0 .. 3 and 8 more, as the scores lie
+      H8<DT> vf[2][kOut];
+      auto read_values = [&](int u) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      H8<DT> p;
+        for (int d = 0; d < kOut; ++d) {
+          union { i16x4 w[2]; H8<DT> v; } x;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = __builtin_amdgcn_exp2f(fmaf(s[u / 2][u % 2 * 8 + e], f, kLift - zero));
-        total += x;
-        p[e] = static_cast<T>(x);
+          for (int e = 0; e < 2; ++e) {
+            const int row = u * 16 + e * 8 + half * 4 + (lane & 15) / 4, piece = d * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1);
+            x.w[e] = read_transposed(
+                (__attribute__((address_space(3))) i16x4*)(lv + row * L::kRow + L::value(row, piece) * 16 + (lane & 1) * 8));
+          }
+          vf[u & 1][d] = x.v;
+        }
+      };
+      read_values(0);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        H8<DT> p;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = __builtin_amdgcn_exp2f(fmaf(s[u / 2][u % 2 * 8 + e], f, kLift - zero));
+          total += x;
+          p[e] = static_cast<T>(x);
+        }
+        if (u < 3) read_values(u + 1);
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) o[d] = mma(vf[u & 1][d], p, o[d]);
       }
-      if (u < 3) read_values(u + 1);
-#pragma unroll
-      for (int d = 0; d < kOut; ++d) o[d] = mma(vf[u & 1][d], p, o[d]);
+      __builtin_amdgcn_s_setprio(0);
     }
-    __builtin_amdgcn_s_setprio(0);
-  }
-  total = both_sum(total);
+  };
+  sweep(std::false_type{});
   __syncthreads();
   if (met) {
-    careful_rows<DT, DP>(a, w, head0, kv, factor);
-    return;
+    // An infinity or a NaN among the values of a tile which some of the rows see in part: a product of matrices has added 0 *
+    // Inf = NaN to the others.  Once more, with sums of what each row sees in such tiles.
+    most = -INFINITY, zero = total = 0.0f;
+    huge = false;
+#pragma unroll
+    for (int d = 0; d < kOut; ++d) o[d] = f32x16{};
+    sweep(std::true_type{});
   }
+  total = both_sum(total);
   if (i0 + col >= w.n) return;
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   T* out = static_cast<T*>(a.out) + ((w.q0 + i0 + col) * a.Hq + head) * a.D;
