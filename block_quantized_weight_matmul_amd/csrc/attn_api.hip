@@ -285,6 +285,7 @@ qmm_status qmm_attend_prompt(const qmm_prompt_args* a, qmm_stream_t stream) {
       const char* what = x == &r.k ? "k" : "v";
       QMM_TRY(check_rows(*x, a->dt, what));
       if (a->Tk == 1) x->st = a->D;
+      if (a->H == 1) x->sh = 0;
       if (x->st < a->D || x->st > (1 << 23)) return fail(QMM_E_SHAPE, "the token stride of %s is outside [D, 2^23]", what);
       if (!aligned(x->p, 16) || x->st % 8 || x->sh % 8) return fail(QMM_E_ALIGN, "rows of %s must be 16-byte aligned", what);
     }

@@ -228,7 +228,7 @@ PyObject* attend(PyObject*, PyObject* const* o, Py_ssize_t n) {
     qmm_attend_args a{};
     if (n != 12 || !integer(o[0], &device) || !integer(o[1], &stream) || !integer(o[2], &h) || !integer(o[3], &H) ||
         !integer(o[4], &D) || !integer(o[5], &type) || !integer(o[6], &page) || !q.get(o[7], device) || q.type == QMM_F32 ||
-        (type != QMM_E4M3 && q.type != type) || q.D != D || q.H == 0 || q.H % H || !table_of(o[8], device, q.T, &a.table, &a.W) ||
+        (type != QMM_E4M3 && q.type != type) || q.D != D || H < 1 || q.H == 0 || q.H % H || !table_of(o[8], device, q.T, &a.table, &a.W) ||
         !vector(o[9], device, at::kInt, q.T, &a.lengths))
       return nullptr;
     a.max_length = a.W * page;

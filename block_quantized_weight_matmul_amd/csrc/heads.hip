@@ -285,7 +285,11 @@ __global__ __launch_bounds__(256) void k_cache_read(CacheDesc c, const int32_t* 
   const int64_t first = block_index() * kTeams, row = first + threadIdx.x / L;
   int64_t b = count_first(B, [&](int64_t i) { return starts[i + 1] <= first; });
   if (row >= total) return;
-  while (b < B && starts[b + 1] <= row) ++b;  // the workgroup's rows may end a sequence
+  // the workgroup's rows may end a sequence, and any number of empty ones follow
+  int64_t more = 1;
+  for (; b + more <= B && starts[b + more] <= row; more *= 2) b += more;
+  while (more /= 2)
+    if (b + more <= B && starts[b + more] <= row) b += more;
   if (b >= B) return;                         // behind the last sequence
   const int64_t t = row - starts[b];
   if (t < 0) return;                          // before the first

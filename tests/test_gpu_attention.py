@@ -559,6 +559,48 @@ def test_prompt_infinities_in_masked_places(D, t):
     del want
 
 
+@pytest.mark.parametrize("t", sorted(HALF))
+@pytest.mark.parametrize("ns,ms,Hq,H,D", [([260, 70, 1], [400, 500, 90], 8, 2, 128), ([150], [150], 3, 3, 64), ([200, 65], [200, 70], 4, 2, 256),
+                                          ([130], [100], 2, 2, 48)])
+def test_prompt_infinities_among_many_values(ns, ms, Hq, H, D, t):
+    """NaN and infinite values in a tenth of the rows: what a row sees of a column decides, tile by tile."""
+    g = np.random.default_rng([96, D])
+    qx, k, v = prompt_inputs(g, ns, ms, Hq, H, D, HALF[t], False)
+    Tk = sum(ms)
+    bad = np.zeros((Tk, H, D), bool)
+    rows = g.random(Tk) < 0.1
+    bad[rows] = g.random((int(rows.sum()), H, D)) < 0.02
+    spoiled = np.where(bad, g.choice([np.nan, np.inf, -np.inf], bad.shape), host64(v))
+    ref, bound = prompt_reference(qx, k, dev(np.where(bad, 0, host64(v)), HALF[t]), ns, ms, D ** -0.5, True, HALF_STEP[HALF[t]])
+    got = host64(q.attend_prompt(qx, k, dev(spoiled, HALF[t]), starts(ns), starts(ms)))
+    a = b = 0
+    met = np.zeros(ref.shape, bool)
+    for n, m in zip(ns, ms):
+        seen = A.causal(n, m)
+        for h in range(Hq):
+            met[a:a + n, h] = seen.astype(int) @ bad[b:b + m, h * H // Hq].astype(int) > 0
+        a, b = a + n, b + m
+    assert met.any() and not met.all()
+    assert not np.isfinite(got[met]).any()
+    tol = bound + (np.abs(ref) + bound) * HALF_STEP[HALF[t]] + SMALLEST[HALF[t]]
+    assert np.all(np.abs(got - ref)[~met] <= tol[~met])
+
+
+def test_read_past_many_empty_sequences():
+    """Rows of one workgroup on both sides of thousands of empty sequences."""
+    g = np.random.default_rng(97)
+    ns = np.zeros(9000, int)
+    ns[[0, 1, 4000, 4001, 8999]] = 3, 2, 1, 4, 5
+    c = blank(5, 16, 2, 32, "bf16")
+    k, v = (dev(g.standard_normal((15, 2, 32)), torch.bfloat16) for _ in "kv")
+    owner, t = np.repeat(np.arange(9000), ns), np.concatenate([np.arange(n) for n in ns])
+    table = np.full((9000, 1), -1, np.int32)
+    table[ns > 0, 0] = g.permutation(5)
+    c.write(k, v, i32(table[owner, 0] * 16 + t))
+    rk, rv = c.read(i32(table.flatten()).view(-1, 1), starts(ns), 15)
+    assert torch.equal(rk, k) and torch.equal(rv, v)
+
+
 def test_prompt_sharp_and_flat():
     g = np.random.default_rng(84)
     n, D = 700, 64
@@ -736,6 +778,9 @@ def test_cache_handles():
     c.close()
     with pytest.raises(q.QmmError, match="NULL"):
         c.write(x, x, i32(range(20)))
+    for columns in (0, 32):
+        with pytest.raises((q.QmmError, ValueError)):
+            c.attend(torch.zeros((1, 1, columns), device="cuda", dtype=torch.bfloat16), i32([0]).view(1, 1), i32([1]))
     rows = torch.arange(2, dtype=torch.int32, device="cuda").view(1, 2)
     want = deep.read(rows, i32([0, 20]), 20, dtype=torch.float32)
     del c
