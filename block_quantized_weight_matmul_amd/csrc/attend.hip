@@ -2,9 +2,10 @@
 //
 //   out[b, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q.k_j - max),  j over the sequence's tokens
 //
-// Bound by reading the cache once.  The query heads that share a key head are the 16 columns of one matrix product (more
+// Bound by reading the cache once: 64 sequences of 2048 to 8192 tokens, 32 / 8 heads of 128, bf16, 252 us or 5.4 TB/s; 2 of up
+// to 131072 in e4m3 80 us or 4.7 TB/s; one of 777 tokens two launches' latency, 8.7 us.  The query heads that share a key head are the 16 columns of one matrix product (more
 // than 16: further row tiles), so a token's keys and values are read once for all of them.  A sequence is divided into
-// `splits` pieces of whole 32-token tiles, a piece among the four waves of a workgroup; each wave keeps its own running
+// `splits` pieces of whole 32-token tiles, a piece among the four or eight waves of a workgroup; each wave keeps its own running
 // maximum, sum and output, which are joined in wave order through LDS and, where there is more than one piece, in piece
 // order by a second small launch.
 #include <algorithm>
@@ -15,7 +16,7 @@ namespace qmm {
 
 namespace {
 
-constexpr int kWaves = 4, kTile = 32;  // waves of a workgroup, tokens of a wave's tile
+constexpr int kWaves = 4, kTile = 32;  // waves of a workgroup (or twice as many), tokens of a wave's tile
 constexpr int kRows = 16;              // query heads of a workgroup
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -95,8 +96,8 @@ __device__ __forceinline__ uint32_t fresh(uint32_t v) {
 // P is fed to the matrix cores as the sum of two 16-bit numbers, its rounding and the rest (2^-17 of it in bf16): the
 // cores have time to spare here, and one rounding of P to bf16 would add as much to the output's error as the output's
 // own rounding.  With an e4m3 cache the tokens' scales of the values multiply P, in bf16, which has fp32's range.
-template <int QT, int CT, int DP>
-__global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(AttendArgs a) {
+template <int QT, int CT, int DP, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attend(AttendArgs a) {
   constexpr bool kCodes = CT == DT_E4M3;
   constexpr int PT = kCodes ? DT_BF16 : QT;            // type of P and V on the matrix cores
   constexpr int kSize = kCodes ? 1 : 2, kRow = DP * kSize;
@@ -107,8 +108,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
   typedef typename Elem<PT>::T P;
   // a wave's tile, first its keys, then its values; at the end its outputs
   constexpr int kRoom = kTile * kRow > kRows * DP * 4 ? kTile * kRow : kRows * DP * 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves][kRoom];
-  __shared__ float sums[kWaves][2][kRows];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[WAVES][kRoom];
+  __shared__ float sums[WAVES][2][kRows];
 
   const CacheDesc& c = a.cache;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k) {
       base[k] = block_base(t0 + wave * kTile + k * 16, page[k]);
-      page[k] = page_at(t0 + (wave + kWaves) * kTile + k * 16);
+      page[k] = page_at(t0 + (wave + WAVES) * kTile + k * 16);
     }
     load_rows(c.k, base, kr);
     load_rows(c.v, base, vr);
@@ -211,10 +212,10 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
 #pragma unroll
   for (int d = 0; d < kOut; ++d) o[d] = f32x4{};
 
-  for (int i = wave; i < count; i += kWaves) {
+  for (int i = wave; i < count; i += WAVES) {
     const int64_t t = t0 + static_cast<int64_t>(i) * kTile;
     const int left = static_cast<int>(min(len - t, int64_t(kTile)));  // tokens of this tile
-    const bool more = i + kWaves < count;
+    const bool more = i + WAVES < count;
     f32x4 kscale[kBlocks], vscale[kBlocks];
     if constexpr (kCodes) {
 #pragma unroll
@@ -228,8 +229,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
     if (more) {
 #pragma unroll
       for (int k = 0; k < kBlocks; ++k) {
-        base[k] = block_base(t + kWaves * kTile + k * 16, page[k]);
-        page[k] = page_at(t + 2 * kWaves * kTile + k * 16);  // a tile ahead
+        base[k] = block_base(t + WAVES * kTile + k * 16, page[k]);
+        page[k] = page_at(t + 2 * WAVES * kTile + k * 16);  // a tile ahead
       }
       load_rows(c.k, base, kr);
       if constexpr (kCodes) load_scales(c.ks, base, ks), load_scales(c.vs, base, vs);
@@ -319,22 +320,22 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_attend(Atten
   __syncthreads();  // also: the tiles are done with
   float best = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) best = fmaxf(best, sums[w][0][col]);
+  for (int w = 0; w < WAVES; ++w) best = fmaxf(best, sums[w][0][col]);
   const float mine = most == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(most - best);
   float* part = reinterpret_cast<float*>(mine_lds);
 #pragma unroll
   for (int d = 0; d < kOut; ++d) *reinterpret_cast<f32x4*>(part + col * DP + d * 16 + quarter * 4) = o[d] * mine;
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * (DP / 4); i += 64 * kWaves) {
+  for (int i = threadIdx.x; i < rows * (DP / 4); i += 64 * WAVES) {
     const int r = i / (DP / 4), d = i % (DP / 4) * 4;
     if (d >= D) continue;
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sums[w][0][r]);
+    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sums[w][0][r]);
     float sum = 0.0f;
     f32x4 v{};
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
       const float m = sums[w][0][r], l = sums[w][1][r];
       sum += m == -INFINITY && l == 0.0f ? 0.0f : l * (m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top));
       v += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(lds[w]) + r * DP + d);
@@ -421,9 +422,13 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 template <int QT, int CT>
 hipError_t attend(const AttendArgs& a, hipStream_t s) {
   const dim3 grid(a.splits, a.cache.heads * a.tiles, static_cast<unsigned>(a.B));
-  if (a.cache.D <= 64) hipLaunchKernelGGL((k_attend<QT, CT, 64>), grid, dim3(64 * kWaves), 0, s, a);
-  else if (a.cache.D <= 128) hipLaunchKernelGGL((k_attend<QT, CT, 128>), grid, dim3(64 * kWaves), 0, s, a);
-  else hipLaunchKernelGGL((k_attend<QT, CT, 256>), grid, dim3(64 * kWaves), 0, s, a);
+  const dim3 threads(64 * a.waves);
+  if (a.waves > kWaves) {
+    if (a.cache.D <= 64) hipLaunchKernelGGL((k_attend<QT, CT, 64, 2 * kWaves>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((k_attend<QT, CT, 128, 2 * kWaves>), grid, threads, 0, s, a);
+  } else if (a.cache.D <= 64) hipLaunchKernelGGL((k_attend<QT, CT, 64, kWaves>), grid, threads, 0, s, a);
+  else if (a.cache.D <= 128) hipLaunchKernelGGL((k_attend<QT, CT, 128, kWaves>), grid, threads, 0, s, a);
+  else hipLaunchKernelGGL((k_attend<QT, CT, 256, kWaves>), grid, threads, 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const dim3 heads = long_grid(a.B * a.Hq);
@@ -440,13 +445,22 @@ hipError_t attend(const AttendArgs& a, hipStream_t s) {
 // longer than 8192 tokens, so that one sequence much longer than the others does not end alone; whole tiles for every
 // wave, and at most 256 a sequence.  Up to two tiles a wave are one piece: 200 tokens of 8 heads 7.3 us, in two pieces and
 // joined 8.9; 777 tokens in pieces of one tile a wave 10.4, of two 12.0.
+//
+// Two pieces become one of a workgroup with twice the waves, and need no join: 32 x 300 tokens of 8 heads 16.2 -> 10.8 us,
+// 32 x 2000 42.7 -> 38.1, 48 x 4000 119 -> 105, 64 x 10000 332 -> 298; in codes 14.5 -> 9.3, 29.4 -> 25.8, 64 -> 70 and 220
+// -> 167.  So do, two by two, long ones of 16-bit caches (2 x 131072 tokens 140 -> 126 us, 8 x 16384 78 -> 73; codes 86 ->
+// 86 and 49 -> 52; pieces below 512 tokens: 777 tokens 9.0 -> 10.3) where it is the sequences that are too few, not the
+// pieces too long (64 x 20000 581 -> 599).  Heads of more than 128 columns take the registers of twice the waves.
 AttendSplit attend_split(const CacheDesc& c, int64_t B, int Hq, int64_t bound) {
   constexpr int64_t kMost = 8192, kStep = kWaves * kTile;
   const int64_t G = Hq / c.heads, units = B * c.heads * ((G + kRows - 1) / kRows);
-  int64_t n = std::max((2 * c.cus + units - 1) / units, (bound + kMost - 1) / kMost);
-  n = bound <= 2 * kStep ? 1 : std::min<int64_t>(n, 256);
-  const int64_t piece = std::max<int64_t>((bound + n * kStep - 1) / (n * kStep), 1) * kStep;
-  return {static_cast<int>(std::max<int64_t>((bound + piece - 1) / piece, 1)), piece};
+  const int64_t few = (2 * c.cus + units - 1) / units;
+  int64_t n = bound <= 2 * kStep ? 1 : std::min<int64_t>(std::max(few, (bound + kMost - 1) / kMost), 256);
+  const bool twice = c.D <= 128 && (n == 2 || (n > 2 && few > 1 && c.type != DT_E4M3 && bound >= 512 * n));
+  const int64_t step = twice ? 2 * kStep : kStep;
+  if (twice) n = (n + 1) / 2;
+  const int64_t piece = std::max<int64_t>((bound + n * step - 1) / (n * step), 1) * step;
+  return {static_cast<int>(std::max<int64_t>((bound + piece - 1) / piece, 1)), piece, twice ? 2 * kWaves : kWaves};
 }
 
 hipError_t launch_attend(AttendArgs a, int qt, hipStream_t s) {

@@ -66,12 +66,14 @@ struct AttendArgs {
   void* out;    // [B][Hq][D]
   int splits;     // pieces of a sequence, of `piece` tokens each, the last of all that is left
   int64_t piece;
+  int waves;      // of a workgroup
   int G, tiles;   // query heads of a key head, row tiles of them (set by the launch)
   float* ws;    // splits > 1: partial outputs [B][Hq][splits][D], then (maximum, sum) [B][Hq][splits]
 };
 struct AttendSplit {
   int splits;
   int64_t piece;
+  int waves;
 };
 AttendSplit attend_split(const CacheDesc& c, int64_t B, int Hq, int64_t bound);
 hipError_t launch_attend(AttendArgs a, int qt, hipStream_t s);

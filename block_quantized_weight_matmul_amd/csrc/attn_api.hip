@@ -256,6 +256,7 @@ qmm_status qmm_cache_attend(const qmm_cache* h, const qmm_attend_args* a, qmm_st
   r.out = a->out;
   r.splits = split.splits;
   r.piece = split.piece;
+  r.waves = split.waves;
   r.ws = static_cast<float*>(a->ws);
   const hipError_t e = qmm::launch_attend(r, a->qt, stream_of(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "attend launch");

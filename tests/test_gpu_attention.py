@@ -310,6 +310,8 @@ ATTEND = [  # B lengths, page, Hq, H, D
     ([1], 16, 1, 1, 16), ([0], 16, 2, 2, 32), ([777], 64, 16, 8, 128), ([5, 0, 31, 32, 33, 127, 128, 129, 500], 16, 8, 4, 128),
     ([300, 17, 64], 32, 21, 3, 80), ([1, 2, 15, 16, 17], 128, 6, 1, 256), ([2000, 1999], 256, 40, 2, 64),
     ([100] * 40, 16, 4, 4, 112), ([4097], 64, 17, 1, 96), ([3000, 10], 16, 33, 1, 128), ([600], 16, 7, 7, 144),
+    ([300, 257, 1, 0] + [40] * 60, 16, 10, 5, 64), ([400] + [33] * 36, 32, 8, 8, 128), ([2300, 2049, 0] + [20] * 30, 16, 4, 4, 96),
+    ([300] + [16] * 140, 16, 2, 2, 160),
 ]
 
 
