@@ -2,12 +2,14 @@
 //
 //   out[b, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q.k_j - max),  j over the sequence's tokens
 //
-// Bound by reading the cache once: 64 sequences of 2048 to 8192 tokens, 32 / 8 heads of 128, bf16, 252 us or 5.4 TB/s; 2 of up
-// to 131072 in e4m3 80 us or 4.7 TB/s; one of 777 tokens two launches' latency, 8.7 us.  The query heads that share a key head are the 16 columns of one matrix product (more
-// than 16: further row tiles), so a token's keys and values are read once for all of them.  A sequence is divided into
-// `splits` pieces of whole 32-token tiles, a piece among the four or eight waves of a workgroup; each wave keeps its own running
-// maximum, sum and output, which are joined in wave order through LDS and, where there is more than one piece, in piece
-// order by a second small launch.
+// Bound by reading the cache once: 64 sequences of 2048 to 8192 tokens, 32 / 8 heads of 128, bf16, take 252 us (5.4 TB/s), 2
+// of up to 131072 in e4m3 80 us (4.7 TB/s), and one of 777 tokens the latency of two launches, 8.7 us.
+//
+// The query heads that share a key head are the 16 columns of one matrix product (more than 16: further row tiles), so a
+// token's keys and values are read once for all of them.  A sequence is divided into `splits` pieces of whole 32-token
+// tiles, a piece among the four or eight waves of a workgroup; each wave keeps its own running maximum, sum and output,
+// which are joined in wave order through LDS and, where there is more than one piece, in piece order by a second small
+// launch.
 #include <algorithm>
 
 #include "attn.hpp"

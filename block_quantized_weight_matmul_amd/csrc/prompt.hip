@@ -2,9 +2,14 @@
 //
 //   out[i, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q_i.k_j - max),  j <= i + (m - n)  (m keys, n queries)
 //
-// Bound by the matrix cores.  A workgroup takes 128 rows, queries of up to four heads that share a key head, and sweeps the
-// keys they may see in tiles of 64: keys and values go straight into LDS, two tiles deep, while the waves, 32 queries of
-// one head each, work on the tile before.
+// Bound by the matrix cores, of which the card's power allows a part: 8192 tokens, 32 / 8 heads of 128, bf16, take 515 us,
+// 1.07 PFLOP/s at 1.9 GHz (with zeros for inputs 440 us), 16 packed prompts of 50 to 1024 queries with up to 1024 keys before
+// them 176 us.
+//
+// A workgroup takes 128 rows, queries of up to four heads that share a key head, and sweeps the keys they may see in tiles
+// of 64: keys and values go straight into LDS, two tiles deep, while the waves, 32 queries of one head each, work on the
+// tile before.  Where such workgroups are few, each has twice the waves and sweeps two tiles at a time, or has half the
+// rows and as many waves.
 #include <algorithm>
 #include <type_traits>
 
@@ -16,7 +21,8 @@ namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-constexpr int kRows = 128, kKeys = 64, kWaves = 4;  // of a workgroup: queries times heads, keys of a tile
+constexpr int kKeys = 64;   // of a tile
+constexpr int kCus = 256;   // compute units
 
 template <int QT> struct Half8 { typedef typename Elem<QT>::T V __attribute__((ext_vector_type(8))); };
 template <int QT> using H8 = typename Half8<QT>::V;
@@ -112,8 +118,11 @@ __device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index, in
 // row-major LDS by transposing reads; the probabilities never leave their lane, and a row's maximum takes one exchange
 // between two lanes.  P is rounded to DT once: its 2^-9 (bf16) of each term, with independent signs, stays below the
 // rounding of the output.
-template <int DT, int DP>
-__global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(PromptArgs a) {
+//
+// A workgroup has kWaves waves for its rows, 32 each, in PARTS parts, which take every PARTS-th tile of keys.
+template <int DT, int DP, int kWaves, int PARTS>
+__global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 || kWaves == 2 ? 1 : 2) void k_prompt(PromptArgs a) {
+  constexpr int kRows = 32 * kWaves;
   typedef typename Elem<DT>::T T;
   typedef Tile<DP> L;
   constexpr int kBytes = kKeys * L::kRow, kLoads = kBytes / 1024 / kWaves, kOut = DP / 32;
@@ -124,15 +133,17 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
   constexpr float kSlack = 8.0f, kLift = DT == DT_F16 ? 6.0f : 0.0f;
   // One array: with a second one the compiler tells what is loaded into LDS apart by its variable, and makes every read of
   // `lds` wait for the loads of the next tile.
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes + 16];
-  int& met = *reinterpret_cast<int*>(lds + 4 * kBytes);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBytes * PARTS + 16];
+  int& met = *reinterpret_cast<int*>(lds + 4 * kBytes * PARTS);
 
   // key heads vary fastest: workgroup i runs on die i mod 8, so that a key head's rows stay in one die's L2 cache
   const int share = blockIdx.x / a.H, kv = blockIdx.x - share * a.H;
   const int rows = kRows >> a.group;  // queries of a head
   const Work w = find_work(a, static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y, __builtin_ctz(kRows) - a.group);
   if (!w.some) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6 & kWaves - 1);
+  const int part = PARTS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * kWaves));
+  uint8_t* const room = lds + part * 4 * kBytes;  // of this part's waves
   const int col = lane & 31, half = lane >> 5;
   const int head0 = kv * a.G + (share << a.group), head = head0 + (wave & (1 << a.group) - 1);
   const float factor = a.scale * 1.44269504088896340736f;
@@ -172,12 +183,12 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
   }
   const T* const kbase = static_cast<const T*>(a.k.p) + w.k0 * a.k.st + kv * a.k.sh;
   const T* const vbase = static_cast<const T*>(a.v.p) + w.k0 * a.v.st + kv * a.v.sh;
-  auto load_tile = [&](int i) {
+  auto load_tile = [&](int i, int buffer) {
     const int64_t j = static_cast<int64_t>(i) * kKeys;
     const uint32_t left = min(w.m - i * kKeys, kKeys);
     const __amdgpu_buffer_rsrc_t kr = rsrc(kbase + j * a.k.st, (left - 1) * kst + a.D * 2);
     const __amdgpu_buffer_rsrc_t vr = rsrc(vbase + j * a.v.st, (left - 1) * vst + a.D * 2);
-    uint8_t* d = lds + (i & 1) * 2 * kBytes + wave * kLoads * 1024;
+    uint8_t* d = room + buffer * 2 * kBytes + wave * kLoads * 1024;
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) load_lds16(kr, d + n * 1024, koff[n]);
 #pragma unroll
@@ -192,19 +203,21 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
 
   auto sweep = [&](auto careful) {
     constexpr bool kCareful = decltype(careful)::value;
-    if (!kCareful && count > 0) load_tile(0);
-    for (int i = 0; i < count; ++i) {
+    if (!kCareful && part < count) load_tile(part, 0);
+    for (int n = 0; n * PARTS < count; ++n) {
+      const int i = n * PARTS + part;
       int lane = threadIdx.x & 63;
       if constexpr (kCareful) asm volatile("" : "+v"(lane));  // addresses made where they are used: no registers are left
       const int col = lane & 31, half = lane >> 5;
       if constexpr (kCareful) {
         __syncthreads();  // the tile before, and the probabilities beside it, are done with
-        load_tile(i);
+        if (i < count) load_tile(i, n & 1);
       }
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this tile's loads, issued a tile ago
       __syncthreads();
-      if (!kCareful && i + 1 < count) load_tile(i + 1);
-      const uint8_t* const lk = lds + (i & 1) * 2 * kBytes;
+      if (!kCareful && i + PARTS < count) load_tile(i + PARTS, n + 1 & 1);
+      if (PARTS > 1 && i >= count) continue;
+      const uint8_t* const lk = room + (n & 1) * 2 * kBytes;
       const uint8_t* const lv = lk + kBytes;
       const int j0 = i * kKeys;
       if (!kCareful && a.causal && j0 + kKeys > whole_all) {  // rows see parts of this tile: infinities and NaN among its values
@@ -272,7 +285,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
       if constexpr (kCareful) {
         if (j0 + kKeys > whole) {
           // Key by key, each added to the rows that see it.  The probabilities pass through the other tile's room.
-          T* const pw = reinterpret_cast<T*>(lds + ((i + 1) & 1) * 2 * kBytes) + wave * kKeys * 32;
+          T* const pw = reinterpret_cast<T*>(room + (n + 1 & 1) * 2 * kBytes) + wave * kKeys * 32;
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -346,6 +359,24 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
     sweep(std::true_type{});
   }
   total = both_sum(total);
+  if constexpr (PARTS == 2) {  // the second part's sums to the first
+    __syncthreads();
+    float* const sums = reinterpret_cast<float*>(lds) + wave * 128 + lane;
+    float* const rest = reinterpret_cast<float*>(lds + 4 * kBytes) + wave * kOut * 16 * 64 + lane;
+    if (part) {
+      sums[0] = most, sums[64] = total;
+#pragma unroll
+      for (int d = 0; d < kOut * 16; ++d) rest[d * 64] = o[d / 16][d % 16];
+    }
+    __syncthreads();
+    if (part) return;
+    const float top = fmaxf(most, sums[0]);
+    const float w0 = most == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(most - top);
+    const float w1 = sums[0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sums[0] - top);
+    total = total * w0 + sums[64] * w1;
+#pragma unroll
+    for (int d = 0; d < kOut * 16; ++d) o[d / 16][d % 16] = o[d / 16][d % 16] * w0 + rest[d * 64] * w1;
+  }
   if (i0 + col >= w.n) return;
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   T* out = static_cast<T*>(a.out) + ((w.q0 + i0 + col) * a.Hq + head) * a.D;
@@ -365,22 +396,43 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) void k_prompt(Promp
     }
 }
 
-template <int DT, int DP>
-hipError_t prompt(const PromptArgs& a, hipStream_t s) {
-  const int64_t tiles = a.Tq / (kRows >> a.group) + a.B, y = std::min<int64_t>(tiles, 65535);  // indexes of tiles (find_work)
+template <int DT, int DP, int kWaves, int PARTS>
+hipError_t launch(const PromptArgs& a, hipStream_t s) {
+  const int64_t tiles = a.Tq / (32 * kWaves >> a.group) + a.B, y = std::min<int64_t>(tiles, 65535);  // their indexes (find_work)
   const dim3 grid(a.Hq >> a.group, static_cast<unsigned>(y), static_cast<unsigned>((tiles + y - 1) / y));
-  hipLaunchKernelGGL((k_prompt<DT, DP>), grid, dim3(64 * kWaves), 0, s, a);
+  hipLaunchKernelGGL((k_prompt<DT, DP, kWaves, PARTS>), grid, dim3(64 * kWaves * PARTS), 0, s, a);
   return hipGetLastError();
+}
+
+// Few workgroups of 128 rows: the longest sweep is what a call waits for, and 64 or 128 rows in two parts halve it (each
+// workgroup has a compute unit to itself).
+//   - Half the rows where a unit is left for each: 512 tokens of 16 heads 15.3 -> 13.3 us (128 rows in parts 14.6), 1024 of
+//     32 heads 25.0 -> 27.1 (22.5).  Not where most sequences are a tile of keys or two: 5 of 40 tokens 7.0 -> 8.3.
+//   - 128 rows in parts where a unit is left for each and the sequences are long enough to have some: 2048 tokens of 8
+//     heads 40.4 -> 33.0, 4096 76 -> 60.  Or where two would share a unit and one of them sweep much longer than the
+//     other, in long sequences without much of a prefix: 2048 tokens of 32 heads 52 -> 47, 8192 of 8 180 -> 144; 8 of 256 of 32
+//     heads 18 -> 24.  More workgroups than that keep the units busy: 4096 tokens of 32 heads 139 -> 152.
+template <int DT, int DP>
+hipError_t prompt(PromptArgs a, hipStream_t s) {
+  // The query heads of a key head share a workgroup, four or two where their number allows it, so that its queries, 32 or 64
+  // of each, end later in fewer tiles that they see in part.
+  a.G = a.Hq / a.H;
+  a.group = a.G % 4 == 0 ? 2 : a.G % 2 == 0 ? 1 : 0;
+  if constexpr (DP <= 128) {
+    const int64_t rows = a.Tq * a.Hq;
+    if (rows <= 64 * kCus && a.Tk >= 128 * a.B) {
+      a.group = std::min(a.group, 1);
+      return launch<DT, DP, 2, 2>(a, s);
+    }
+    if (rows <= 128 * kCus ? a.Tk >= 256 * a.B : rows <= 256 * kCus && a.causal && a.Tk >= 1024 * a.B && a.Tk < 2 * a.Tq)
+      return launch<DT, DP, 4, 2>(a, s);
+  }
+  return launch<DT, DP, 4, 1>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_prompt(PromptArgs a, int dt, hipStream_t s) {
-  // The query heads of a key head share a workgroup, four or two where their number allows it, so that its queries, 32 or 64
-  // of each, end later in fewer tiles that they see in part.
-  const int G = a.Hq / a.H;
-  a.G = G;
-  a.group = G % 4 == 0 ? 2 : G % 2 == 0 ? 1 : 0;
   if (dt == DT_F16) {
     if (a.D <= 64) return prompt<DT_F16, 64>(a, s);
     return a.D <= 128 ? prompt<DT_F16, 128>(a, s) : prompt<DT_F16, 256>(a, s);

@@ -457,6 +457,8 @@ PROMPTS = [  # queries, keys, Hq, H, D
     ([1], [1], 1, 1, 16), ([7], [7], 4, 2, 128), ([128], [128], 2, 2, 128), ([130, 1, 0, 64, 63, 65, 33], None, 4, 2, 64),
     ([200], [260], 6, 2, 80), ([5, 40], [300, 41], 3, 1, 256), ([9], [4], 2, 1, 32), ([150, 30], [100, 0], 2, 1, 64),
     ([0, 0, 3], [5, 0, 3], 2, 2, 96), ([1] * 70 + [2, 129], None, 1, 1, 48), ([321], [321], 2, 1, 112), ([64, 64], [64, 128], 16, 8, 128),
+    ([265], [300], 63, 21, 64), ([260, 5], [270, 260], 64, 4, 128), ([540], [1030], 61, 61, 32), ([300], [301], 222, 2, 32),
+    ([150, 160], [250, 160], 224, 8, 128), ([1, 513], None, 6, 6, 80),
 ]
 
 
@@ -563,7 +565,7 @@ def test_prompt_infinities_in_masked_places(D, t):
 
 @pytest.mark.parametrize("t", sorted(HALF))
 @pytest.mark.parametrize("ns,ms,Hq,H,D", [([260, 70, 1], [400, 500, 90], 8, 2, 128), ([150], [150], 3, 3, 64), ([200, 65], [200, 70], 4, 2, 256),
-                                          ([130], [100], 2, 2, 48)])
+                                          ([130], [100], 2, 2, 48), ([265], [300], 64, 4, 128), ([300], [301], 224, 2, 64)])
 def test_prompt_infinities_among_many_values(ns, ms, Hq, H, D, t):
     """NaN and infinite values in a tenth of the rows: what a row sees of a column decides, tile by tile."""
     g = np.random.default_rng([96, D])
