@@ -2,9 +2,9 @@
 //
 //   out[i, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q_i.k_j - max),  j <= i + (m - n)  (m keys, n queries)
 //
-// Bound by the matrix cores, of which the card's power allows a part: 8192 tokens, 32 / 8 heads of 128, bf16, take 515 us,
-// 1.07 PFLOP/s at 1.9 GHz (with zeros for inputs 440 us), 16 packed prompts of 50 to 1024 queries with up to 1024 keys before
-// them 176 us.
+// Bound by the matrix cores, of which the card's power allows a part: 8192 tokens, 32 / 8 heads of 128, bf16, take 504 us,
+// 1.09 PFLOP/s at 1.9 GHz (with zeros for inputs 440 us), 16 packed prompts of 50 to 1024 queries with up to 1024 keys before
+// them 166 us; of many short sequences by memory: 128 of 64 tokens 37 us, 4.5 TB/s.
 //
 // A workgroup takes 128 rows, queries of up to four heads that share a key head, and sweeps the keys they may see in tiles
 // of 64: keys and values go straight into LDS, two tiles deep, while the waves, 32 queries of one head each, work on the
@@ -56,6 +56,13 @@ __device__ __forceinline__ float both_max(float v) {
 __device__ __forceinline__ float both_sum(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The lane's number (or the like) as a value that the compiler knows nothing of, so that addresses are made where they are used:
+// kept over the loop they would cost it registers that it does not have.
+__device__ __forceinline__ int again(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
 }
 
 // A tile of 64 rows of DP columns in LDS, in 16-byte pieces xored with a function of the row: 16 lanes that read one piece
@@ -144,7 +151,6 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 || kWaves == 2 ? 1 :
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6 & kWaves - 1);
   const int part = PARTS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * kWaves));
   uint8_t* const room = lds + part * 4 * kBytes;  // of this part's waves
-  const int col = lane & 31, half = lane >> 5;
   const int head0 = kv * a.G + (share << a.group), head = head0 + (wave & (1 << a.group) - 1);
   const float factor = a.scale * 1.44269504088896340736f;
   const int shift = w.m - w.n;  // query i sees keys 0 .. i + shift
@@ -157,18 +163,6 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 || kWaves == 2 ? 1 :
   const int whole_all = a.causal ? min(w.m, w.first + shift + 1) : w.m;
   const int count = (end + kKeys - 1) / kKeys;
   if (threadIdx.x == 0) met = 0;
-
-  H8<DT> q[DP / 16];
-  {
-    const T* p = static_cast<const T*>(a.q.p) + (w.q0 + min(i0 + col, w.n - 1)) * a.q.st + head * a.q.sh;
-    typedef H8<DT> Qu __attribute__((aligned(sizeof(T))));
-#pragma unroll
-    for (int j = 0; j < DP / 16; ++j) {
-      const int d = j * 16 + half * 8;
-      q[j] = *reinterpret_cast<const Qu*>(p + (d < a.D ? d : 0));
-      if (d >= a.D) q[j] = H8<DT>{};
-    }
-  }
 
   // loads of a tile: this wave's lanes take pieces of rows (wave * kLoads + n) * kPer ..; a lane whose piece lies past D
   // reads past the descriptor's end, which gives zeros, as do rows past the last key
@@ -195,6 +189,37 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 || kWaves == 2 ? 1 :
     for (int n = 0; n < kLoads; ++n) load_lds16(vr, d + kBytes + n * 1024, voff[n]);
   };
 
+  // Queries and outputs pass through the second tile's room, so that their rows are read and written whole (as the products have
+  // them, 16 or 32 bytes of a row at a time: 64 sequences of 128 tokens 49 -> 40 us, 16 of 1000 203 -> 191): a wave's 32
+  // rows, 16-byte piece lane % kPieces of row lane / kPieces and of every kPer-th after it.
+  typedef H8<DT> H8u __attribute__((aligned(sizeof(T))));
+  const auto rows_at = [&](uint8_t* base, int row, int piece) { return base + row * L::kRow + L::key(row, piece) * 16; };
+  H8<DT> q[DP / 16];
+  {
+    const int lane = again(threadIdx.x & 63), col = lane & 31, half = lane >> 5;
+    uint8_t* const own = room + 2 * kBytes + wave * 32 * L::kRow;
+    const T* const p = static_cast<const T*>(a.q.p) + w.q0 * a.q.st + head * a.q.sh;
+    const int piece = lane % L::kPieces;
+    constexpr int kAtOnce = 32 / kPer < 8 ? 32 / kPer : 8;  // (more of 256 columns take registers from the loop)
+#pragma unroll
+    for (int n0 = 0; n0 < 32 / kPer; n0 += kAtOnce) {
+      H8<DT> x[kAtOnce];
+#pragma unroll
+      for (int n = 0; n < kAtOnce; ++n) {
+        const int row = (n0 + n) * kPer + lane / L::kPieces;
+        x[n] = *reinterpret_cast<const H8u*>(p + min(i0 + row, w.n - 1) * a.q.st + (piece * 8 < a.D ? piece * 8 : 0));
+        if (piece * 8 >= a.D) x[n] = H8<DT>{};
+      }
+      if (n0 + kAtOnce >= 32 / kPer && part < count) load_tile(part, 0);
+#pragma unroll
+      for (int n = 0; n < kAtOnce; ++n)
+        *reinterpret_cast<H8<DT>*>(rows_at(own, (n0 + n) * kPer + lane / L::kPieces, piece)) = x[n];
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int j = 0; j < DP / 16; ++j) q[j] = *reinterpret_cast<const H8<DT>*>(rows_at(own, col, 2 * j + half));
+  }
+
   float most = -INFINITY, zero = 0.0f, total = 0.0f;  // of query col; the sum over this lane's keys only
   bool huge = false;
   f32x16 o[kOut];
@@ -203,11 +228,9 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 || kWaves == 2 ? 1 :
 
   auto sweep = [&](auto careful) {
     constexpr bool kCareful = decltype(careful)::value;
-    if (!kCareful && part < count) load_tile(part, 0);
     for (int n = 0; n * PARTS < count; ++n) {
       const int i = n * PARTS + part;
-      int lane = threadIdx.x & 63;
-      if constexpr (kCareful) asm volatile("" : "+v"(lane));  // addresses made where they are used: no registers are left
+      const int lane = kCareful ? again(threadIdx.x & 63) : threadIdx.x & 63;
       const int col = lane & 31, half = lane >> 5;
       if constexpr (kCareful) {
         __syncthreads();  // the tile before, and the probabilities beside it, are done with
@@ -357,6 +380,7 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 || kWaves == 2 ? 1 :
 #pragma unroll
     for (int d = 0; d < kOut; ++d) o[d] = f32x16{};
     sweep(std::true_type{});
+    __syncthreads();
   }
   total = both_sum(total);
   if constexpr (PARTS == 2) {  // the second part's sums to the first
@@ -377,23 +401,27 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 || kWaves == 2 ? 1 :
 #pragma unroll
     for (int d = 0; d < kOut * 16; ++d) o[d / 16][d % 16] = o[d / 16][d % 16] * w0 + rest[d * 64] * w1;
   }
-  if (i0 + col >= w.n) return;
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  T* out = static_cast<T*>(a.out) + ((w.q0 + i0 + col) * a.Hq + head) * a.D;
+  uint8_t* const own = lds + 2 * kBytes + wave * 32 * L::kRow;
+  const int lane1 = again(threadIdx.x & 63), col1 = lane1 & 31, half1 = lane1 >> 5;
 #pragma unroll
   for (int d = 0; d < kOut; ++d)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int c = d * 32 + e * 8 + half * 4;
-      if (c < a.D) {
-        typedef T V4 __attribute__((ext_vector_type(4)));
-        typedef V4 V4u __attribute__((aligned(sizeof(T))));
-        V4 v;
+      typedef T V4 __attribute__((ext_vector_type(4)));
+      V4 v;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) v[x] = static_cast<T>(o[d][4 * e + x] * inv);
-        *reinterpret_cast<V4u*>(out + c) = v;
-      }
+      for (int x = 0; x < 4; ++x) v[x] = static_cast<T>(o[d][4 * e + x] * inv);
+      *reinterpret_cast<V4*>(rows_at(own, col1, d * 4 + e) + half1 * 8) = v;
     }
+  T* const out = static_cast<T*>(a.out) + (w.q0 * a.Hq + head) * a.D;
+#pragma unroll
+  for (int n = 0; n < 32 / kPer; ++n) {
+    const int row = n * kPer + lane1 / L::kPieces, piece = lane1 % L::kPieces;
+    const H8<DT> v = *reinterpret_cast<const H8<DT>*>(rows_at(own, row, piece));
+    if (i0 + row < w.n && piece * 8 < a.D)
+      *reinterpret_cast<H8u*>(out + static_cast<int64_t>(i0 + row) * a.Hq * a.D + piece * 8) = v;
+  }
 }
 
 template <int DT, int DP, int kWaves, int PARTS>
