@@ -8,8 +8,7 @@
 //
 // A workgroup takes 128 rows, queries of up to four heads that share a key head, and sweeps the keys they may see in tiles
 // of 64: keys and values go straight into LDS, two tiles deep, while the waves, 32 queries of one head each, work on the
-// tile before.  Where such workgroups are few, each has twice the waves and sweeps two tiles at a time, or has half the
-// rows and as many waves.
+// tile before.  Where such workgroups are few, each has twice the waves and sweeps two tiles at a time.
 #include <algorithm>
 #include <type_traits>
 
@@ -21,8 +20,9 @@ namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-constexpr int kKeys = 64;   // of a tile
-constexpr int kCus = 256;   // compute units
+constexpr int kRows = 128, kWaves = 4;  // of a workgroup: queries times heads, waves that they are divided among
+constexpr int kKeys = 64;               // of a tile
+constexpr int kCus = 256;               // compute units
 
 template <int QT> struct Half8 { typedef typename Elem<QT>::T V __attribute__((ext_vector_type(8))); };
 template <int QT> using H8 = typename Half8<QT>::V;
@@ -126,10 +126,9 @@ __device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index, in
 // between two lanes.  P is rounded to DT once: its 2^-9 (bf16) of each term, with independent signs, stays below the
 // rounding of the output.
 //
-// A workgroup has kWaves waves for its rows, 32 each, in PARTS parts, which take every PARTS-th tile of keys.
-template <int DT, int DP, int kWaves, int PARTS>
-__global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 || kWaves == 2 ? 1 : 2) void k_prompt(PromptArgs a) {
-  constexpr int kRows = 32 * kWaves;
+// PARTS: as often a workgroup has four waves for its rows, and each four take every PARTS-th tile of keys.
+template <int DT, int DP, int PARTS>
+__global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 ? 1 : 2) void k_prompt(PromptArgs a) {
   typedef typename Elem<DT>::T T;
   typedef Tile<DP> L;
   constexpr int kBytes = kKeys * L::kRow, kLoads = kBytes / 1024 / kWaves, kOut = DP / 32;
@@ -189,9 +188,9 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 || kWaves == 2 ? 1 :
     for (int n = 0; n < kLoads; ++n) load_lds16(vr, d + kBytes + n * 1024, voff[n]);
   };
 
-  // Queries and outputs pass through the second tile's room, so that their rows are read and written whole (as the products have
-  // them, 16 or 32 bytes of a row at a time: 64 sequences of 128 tokens 49 -> 40 us, 16 of 1000 203 -> 191): a wave's 32
-  // rows, 16-byte piece lane % kPieces of row lane / kPieces and of every kPer-th after it.
+  // Queries and outputs pass through the second tile's room, so that their rows are read and written whole (not as the
+  // products have them, 16 or 32 bytes of a row at a time: 64 sequences of 128 tokens 49 -> 40 us, 16 of 1000 203 -> 191): a
+  // wave's 32 rows, 16-byte piece lane % kPieces of row lane / kPieces and of every kPer-th after it.
   typedef H8<DT> H8u __attribute__((aligned(sizeof(T))));
   const auto rows_at = [&](uint8_t* base, int row, int piece) { return base + row * L::kRow + L::key(row, piece) * 16; };
   H8<DT> q[DP / 16];
@@ -424,43 +423,38 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 || kWaves == 2 ? 1 :
   }
 }
 
-template <int DT, int DP, int kWaves, int PARTS>
+template <int DT, int DP, int PARTS>
 hipError_t launch(const PromptArgs& a, hipStream_t s) {
-  const int64_t tiles = a.Tq / (32 * kWaves >> a.group) + a.B, y = std::min<int64_t>(tiles, 65535);  // their indexes (find_work)
+  const int64_t tiles = a.Tq / (kRows >> a.group) + a.B, y = std::min<int64_t>(tiles, 65535);  // their indexes (find_work)
   const dim3 grid(a.Hq >> a.group, static_cast<unsigned>(y), static_cast<unsigned>((tiles + y - 1) / y));
-  hipLaunchKernelGGL((k_prompt<DT, DP, kWaves, PARTS>), grid, dim3(64 * kWaves * PARTS), 0, s, a);
+  hipLaunchKernelGGL((k_prompt<DT, DP, PARTS>), grid, dim3(64 * kWaves * PARTS), 0, s, a);
   return hipGetLastError();
 }
 
-// Few workgroups of 128 rows: the longest sweep is what a call waits for, and 64 or 128 rows in two parts halve it (each
-// workgroup has a compute unit to itself).
-//   - Half the rows where a unit is left for each: 512 tokens of 16 heads 15.3 -> 13.3 us (128 rows in parts 14.6), 1024 of
-//     32 heads 25.0 -> 27.1 (22.5).  Not where most sequences are a tile of keys or two: 5 of 40 tokens 7.0 -> 8.3.
-//   - 128 rows in parts where a unit is left for each and the sequences are long enough to have some: 2048 tokens of 8
-//     heads 40.4 -> 33.0, 4096 76 -> 60.  Or where two would share a unit and one of them sweep much longer than the
-//     other, in long sequences without much of a prefix: 2048 tokens of 32 heads 52 -> 47, 8192 of 8 180 -> 144; 8 of 256 of 32
-//     heads 18 -> 24.  More workgroups than that keep the units busy: 4096 tokens of 32 heads 139 -> 152.
+// Few workgroups: the longest sweep is what a call waits for, and two parts halve it (a workgroup then has a compute unit to
+// itself).  Where a unit is left for each and the sequences have a few tiles: 512 tokens of 16 heads 14.0 -> 13.1 us, 2048
+// of 8 heads 40.5 -> 32.7, 4096 75 -> 60; 128 of 16 heads 7.6 -> 8.2, 16 of those 10.4 -> 16.0.  And where two would share a
+// unit, one of which sweeps much longer than the other, in long sequences without much of a prefix: 2048 tokens of 32 heads
+// 53.7 -> 47.1, 8192 of 8 180 -> 146; four of 512 of 32 heads 21.6 -> 26.2.  More workgroups than that keep the units busy:
+// 4096 tokens of 32 heads 139 -> 152.
 template <int DT, int DP>
-hipError_t prompt(PromptArgs a, hipStream_t s) {
-  // The query heads of a key head share a workgroup, four or two where their number allows it, so that its queries, 32 or 64
-  // of each, end later in fewer tiles that they see in part.
-  a.G = a.Hq / a.H;
-  a.group = a.G % 4 == 0 ? 2 : a.G % 2 == 0 ? 1 : 0;
+hipError_t prompt(const PromptArgs& a, hipStream_t s) {
   if constexpr (DP <= 128) {
     const int64_t rows = a.Tq * a.Hq;
-    if (rows <= 64 * kCus && a.Tk >= 128 * a.B) {
-      a.group = std::min(a.group, 1);
-      return launch<DT, DP, 2, 2>(a, s);
-    }
-    if (rows <= 128 * kCus ? a.Tk >= 256 * a.B : rows <= 256 * kCus && a.causal && a.Tk >= 1024 * a.B && a.Tk < 2 * a.Tq)
-      return launch<DT, DP, 4, 2>(a, s);
+    if (rows <= kRows * kCus ? a.Tk >= 256 * a.B
+                             : rows <= 2 * kRows * kCus && a.causal && a.Tk >= 1024 * a.B && a.Tk < 2 * a.Tq)
+      return launch<DT, DP, 2>(a, s);
   }
-  return launch<DT, DP, 4, 1>(a, s);
+  return launch<DT, DP, 1>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_prompt(PromptArgs a, int dt, hipStream_t s) {
+  // The query heads of a key head share a workgroup, four or two where their number allows it, so that its queries, 32 or 64
+  // of each, end later in fewer tiles that they see in part.
+  a.G = a.Hq / a.H;
+  a.group = a.G % 4 == 0 ? 2 : a.G % 2 == 0 ? 1 : 0;
   if (dt == DT_F16) {
     if (a.D <= 64) return prompt<DT_F16, 64>(a, s);
     return a.D <= 128 ? prompt<DT_F16, 128>(a, s) : prompt<DT_F16, 256>(a, s);
