@@ -128,6 +128,9 @@ __device__ __forceinline__ float inverse_root(float m) {
 //
 //   y = x * w / sqrt(mean(x^2) + eps);   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq
 //
+// Bound by memory: 8192 tokens of 32 + 8 heads of 128 in bf16 take 37.7 us, 4.45 TB/s of what is read and written (heads chosen
+// by each lane, with their branches, 67; a weight behind a branch of its own 46).  A decode step's launch is latency, 4.3 us.
+//
 // Sums in fp32, the angle and its reduction in 64 bits (a position of 2^20 loses all of a fast pair's angle in 32), one
 // rounding at the end.  CACHE: keys and values go to their slots; a key is rounded to the queries' type first, so that the
 // call leaves the bits of the two calls it stands for.
@@ -256,7 +259,8 @@ __global__ __launch_bounds__(256) void k_heads(HeadsArgs a) {
   }
 }
 
-// Keys and values of T tokens to their slots: a team of L lanes takes a token's head, of both.
+// Keys and values of T tokens to their slots: a team of L lanes takes a token's head, of both.  Bound by memory: 2048 tokens of
+// 8 heads of 128, bf16 to e4m3, 7 us (1.8 TB/s; few tokens are latency, 2 us).
 template <int XT, int CT, int L>
 __global__ __launch_bounds__(256) void k_cache_write(CacheDesc c, HeadRows k, HeadRows v, int64_t T, const int32_t* slots) {
   typedef typename Elem<XT>::T X;
@@ -275,7 +279,8 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheDesc c, HeadRows k, He
   to_cache<CT, XT, L>(vv, c.v, c.vs, r, D, at, at + 4, mine);
 }
 
-// Packed rows from the cache: a team of L lanes takes a row and a share of its heads.
+// Packed rows from the cache: a team of L lanes takes a row and a share of its heads, four at a time, for that many loads on
+// their way.  Bound by memory: 52553 tokens of 8 heads of 128, e4m3 to bf16, 63.5 us, 5.1 TB/s of what is read and written.
 template <int CT, int OT, int L>
 __global__ __launch_bounds__(256) void k_cache_read(CacheDesc c, const int32_t* table, int64_t B, int64_t W,
                                                     const int32_t* starts, int64_t total, void* ko, void* vo) {
