@@ -359,55 +359,68 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attend(Attend
   }
 }
 
+// over a wave, the same bits in every lane
+template <typename F>
+__device__ __forceinline__ float over_wave(float v, F f) {
+  const auto g = [&](uint32_t a, uint32_t b) { return __float_as_uint(f(__uint_as_float(a), __uint_as_float(b))); };
+  const uint32_t u = team<32>(__float_as_uint(v), g);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(g(r[0], r[1]));
+}
+
 // The pieces of a sequence joined: a workgroup takes a head of a sequence, teams of L lanes every (256 / L)-th piece, and
-// the teams' sums are added in order.  The first pieces are asked for before it is known which there are.
+// the teams' sums are added in order.  Bound by latency: every wave looks at all maxima and sums itself, and the first pieces
+// are asked for before it is known which there are.
 template <int QT, int L>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   constexpr int kTeams = 256 / L, kAhead = 4;
-  __shared__ float weight[256];
   __shared__ f32x4 part[kTeams][L];
-  __shared__ float red[8];
   typedef typename Elem<QT>::T Q;
-  const int D = a.cache.D, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const int D = a.cache.D, tid = threadIdx.x, lane = tid & 63;
   const int64_t head = block_index(), b = head / a.Hq;
   const int team = tid / L, d = tid % L * 4;
-  const float* o = a.ws + head * a.splits * D + (d < D ? d : 0);
-  auto load = [&](int s) { return *reinterpret_cast<const f32x4*>(o + static_cast<int64_t>(min(s, a.splits - 1)) * D); };
+  const float* const o = a.ws + head * a.splits * D + (d < D ? d : 0);
+  const f32x2* const ml = reinterpret_cast<const f32x2*>(a.ws + a.B * a.Hq * a.splits * D) + head * a.splits;
   f32x4 x[kAhead];
+  float at[kAhead];  // the pieces' maxima
+  auto load = [&](int s) {
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) x[i] = load(team + i * kTeams);
-  const float* ml = a.ws + a.B * a.Hq * a.splits * D + head * a.splits * 2;
-  const int at = min(tid, a.splits - 1);
-  float m = ml[2 * at], l = ml[2 * at + 1];
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t p = min(s + i * kTeams, a.splits - 1);
+      x[i] = *reinterpret_cast<const f32x4*>(o + p * D);
+      at[i] = ml[p][0];
+    }
+  };
+  f32x2 of[4];  // of pieces lane, lane + 64, ..: up to 256
+#pragma unroll
+  for (int k = 0; k < 4; ++k) of[k] = k * 64 < a.splits ? ml[min(k * 64 + lane, a.splits - 1)] : f32x2{-INFINITY, 0.0f};
+  load(team);
   const int64_t room = a.W << a.cache.shift;
   int64_t len = a.lengths[b];
   len = len < 0 ? 0 : len > room ? room : len;
   // pieces that there are: one at least, of an empty sequence too
   const int n = static_cast<int>(min(max((len + a.piece - 1) / a.piece, int64_t(1)), int64_t(a.splits)));
-  if (tid >= n) m = -INFINITY, l = 0.0f;
-  float top = m;
+  float top = -INFINITY;
 #pragma unroll
-  for (int i = 32; i; i >>= 1) top = fmaxf(top, __shfl_xor(top, i));
-  if (lane == 0) red[wave] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const float w = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-  float sum = l != l ? l : l * w;  // NaN also where nothing else is
+  for (int k = 0; k < 4; ++k) {
+    if (k * 64 + lane >= n) of[k] = f32x2{-INFINITY, 0.0f};
+    top = fmaxf(top, of[k][0]);
+  }
+  top = over_wave(top, [](float u, float v) { return fmaxf(u, v); });
+  const auto weight = [&](float m) { return m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top); };
+  float sum = 0.0f;
 #pragma unroll
-  for (int i = 32; i; i >>= 1) sum += __shfl_xor(sum, i);
-  if (lane == 0) red[4 + wave] = sum;
-  weight[tid] = w;
-  __syncthreads();
-  sum = (red[4] + red[5]) + (red[6] + red[7]);
+  for (int k = 0; k < 4; ++k) sum += of[k][1] != of[k][1] ? of[k][1] : of[k][1] * weight(of[k][0]);  // NaN also where nothing else is
+  sum = over_wave(sum, [](float u, float v) { return u + v; });
   f32x4 v{};
   for (int s = team; s < n; s += kAhead * kTeams) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int p = s + i * kTeams;
-      if (p < n && weight[p] != 0.0f) v += weight[p] * x[i];
+      const float w = weight(at[i]);
+      if (s + i * kTeams < n && w != 0.0f) v += w * x[i];
     }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) x[i] = load(s + (kAhead + i) * kTeams);
+    if (s + kAhead * kTeams < n) load(s + kAhead * kTeams);
   }
   part[team][tid % L] = v;
   __syncthreads();
