@@ -118,7 +118,8 @@ __device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index, in
   return w;
 }
 
-// DT: type of everything but the sums; DP: columns, D rounded up to 64, 128 or 256.
+// DT: type of everything but the sums; COLS: columns of the products, D rounded up to 32, 64, 96, 128, 192 or 256 (of 64,
+// 128 or 256 alone: 4096 tokens of 32 heads of 80 117 -> 129 us, 32 heads of 32 74 -> 84, 16 heads of 160 146 -> 171).
 //
 // Scores are computed transposed, S^T = K Q^T (keys x queries): a lane then holds, for one query, the scores of the keys
 // that its operand of O^T = V^T P^T takes, in the order in which that product's other operand, V^T, can be read from
@@ -127,11 +128,12 @@ __device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index, in
 // rounding of the output.
 //
 // PARTS: as often a workgroup has four waves for its rows, and each four take every PARTS-th tile of keys.
-template <int DT, int DP, int PARTS>
-__global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 ? 1 : 2) void k_prompt(PromptArgs a) {
+template <int DT, int COLS, int PARTS>
+__global__ __launch_bounds__(64 * kWaves * PARTS, COLS > 128 ? 1 : 2) void k_prompt(PromptArgs a) {
+  constexpr int DP = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;  // of a row in LDS
   typedef typename Elem<DT>::T T;
   typedef Tile<DP> L;
-  constexpr int kBytes = kKeys * L::kRow, kLoads = kBytes / 1024 / kWaves, kOut = DP / 32;
+  constexpr int kBytes = kKeys * L::kRow, kLoads = kBytes / 1024 / kWaves, kOut = COLS / 32;
   constexpr int kPer = 64 / L::kPieces > 0 ? 64 / L::kPieces : 1;  // rows of a load of a wave
   static_assert(L::kPieces <= 64, "a load holds whole rows");
   // The maximum that P is relative to is moved, and with it every output so far, only where a score exceeds it by 2^kSlack:
@@ -193,7 +195,7 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 ? 1 : 2) void k_prom
   // wave's 32 rows, 16-byte piece lane % kPieces of row lane / kPieces and of every kPer-th after it.
   typedef H8<DT> H8u __attribute__((aligned(sizeof(T))));
   const auto rows_at = [&](uint8_t* base, int row, int piece) { return base + row * L::kRow + L::key(row, piece) * 16; };
-  H8<DT> q[DP / 16];
+  H8<DT> q[COLS / 16];
   {
     const int lane = again(threadIdx.x & 63), col = lane & 31, half = lane >> 5;
     uint8_t* const own = room + 2 * kBytes + wave * 32 * L::kRow;
@@ -216,7 +218,7 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 ? 1 : 2) void k_prom
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int j = 0; j < DP / 16; ++j) q[j] = *reinterpret_cast<const H8<DT>*>(rows_at(own, col, 2 * j + half));
+    for (int j = 0; j < COLS / 16; ++j) q[j] = *reinterpret_cast<const H8<DT>*>(rows_at(own, col, 2 * j + half));
   }
 
   float most = -INFINITY, zero = 0.0f, total = 0.0f;  // of query col; the sum over this lane's keys only
@@ -261,14 +263,14 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 ? 1 : 2) void k_prom
         s[k] = f32x16{};
         const int row = k * 32 + col;
 #pragma unroll
-        for (int j = 0; j < DP / 16; ++j)
+        for (int j = 0; j < COLS / 16; ++j)
           s[k] = mma(*reinterpret_cast<const H8<DT>*>(lk + row * L::kRow + L::key(row, 2 * j + half) * 16), q[j], s[k]);
       }
       // four reads ahead of the products (one or two, as the compiler has it: 2048 queries of 8 heads 43.0 -> 40.7 us, 8192 of 32
       // 526 -> 519; eight: 41.9)
       __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
-      for (int n = 0; n < DP / 8 - 4; ++n) {
+      for (int n = 0; n < COLS / 8 - 4; ++n) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
@@ -423,11 +425,11 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, DP == 256 ? 1 : 2) void k_prom
   }
 }
 
-template <int DT, int DP, int PARTS>
+template <int DT, int COLS, int PARTS>
 hipError_t launch(const PromptArgs& a, hipStream_t s) {
   const int64_t tiles = a.Tq / (kRows >> a.group) + a.B, y = std::min<int64_t>(tiles, 65535);  // their indexes (find_work)
   const dim3 grid(a.Hq >> a.group, static_cast<unsigned>(y), static_cast<unsigned>((tiles + y - 1) / y));
-  hipLaunchKernelGGL((k_prompt<DT, DP, PARTS>), grid, dim3(64 * kWaves * PARTS), 0, s, a);
+  hipLaunchKernelGGL((k_prompt<DT, COLS, PARTS>), grid, dim3(64 * kWaves * PARTS), 0, s, a);
   return hipGetLastError();
 }
 
@@ -437,15 +439,24 @@ hipError_t launch(const PromptArgs& a, hipStream_t s) {
 // unit, one of which sweeps much longer than the other, in long sequences without much of a prefix: 2048 tokens of 32 heads
 // 53.7 -> 47.1, 8192 of 8 180 -> 146; four of 512 of 32 heads 21.6 -> 26.2.  More workgroups than that keep the units busy:
 // 4096 tokens of 32 heads 139 -> 152.
-template <int DT, int DP>
+template <int DT, int COLS>
 hipError_t prompt(const PromptArgs& a, hipStream_t s) {
-  if constexpr (DP <= 128) {
+  if constexpr (COLS <= 128) {
     const int64_t rows = a.Tq * a.Hq;
     if (rows <= kRows * kCus ? a.Tk >= 256 * a.B
                              : rows <= 2 * kRows * kCus && a.causal && a.Tk >= 1024 * a.B && a.Tk < 2 * a.Tq)
-      return launch<DT, DP, 2>(a, s);
+      return launch<DT, COLS, 2>(a, s);
   }
-  return launch<DT, DP, 1>(a, s);
+  return launch<DT, COLS, 1>(a, s);
+}
+
+template <int DT>
+hipError_t prompt_of(const PromptArgs& a, hipStream_t s) {
+  if (a.D <= 32) return prompt<DT, 32>(a, s);
+  if (a.D <= 64) return prompt<DT, 64>(a, s);
+  if (a.D <= 96) return prompt<DT, 96>(a, s);
+  if (a.D <= 128) return prompt<DT, 128>(a, s);
+  return a.D <= 192 ? prompt<DT, 192>(a, s) : prompt<DT, 256>(a, s);
 }
 
 }  // namespace
@@ -455,12 +466,7 @@ hipError_t launch_prompt(PromptArgs a, int dt, hipStream_t s) {
   // of each, end later in fewer tiles that they see in part.
   a.G = a.Hq / a.H;
   a.group = a.G % 4 == 0 ? 2 : a.G % 2 == 0 ? 1 : 0;
-  if (dt == DT_F16) {
-    if (a.D <= 64) return prompt<DT_F16, 64>(a, s);
-    return a.D <= 128 ? prompt<DT_F16, 128>(a, s) : prompt<DT_F16, 256>(a, s);
-  }
-  if (a.D <= 64) return prompt<DT_BF16, 64>(a, s);
-  return a.D <= 128 ? prompt<DT_BF16, 128>(a, s) : prompt<DT_BF16, 256>(a, s);
+  return dt == DT_F16 ? prompt_of<DT_F16>(a, s) : prompt_of<DT_BF16>(a, s);
 }
 
 }  // namespace qmm

@@ -459,6 +459,7 @@ PROMPTS = [  # queries, keys, Hq, H, D
     ([0, 0, 3], [5, 0, 3], 2, 2, 96), ([1] * 70 + [2, 129], None, 1, 1, 48), ([321], [321], 2, 1, 112), ([64, 64], [64, 128], 16, 8, 128),
     ([265], [300], 63, 21, 64), ([260, 5], [270, 260], 64, 4, 128), ([540], [1030], 61, 61, 32), ([300], [301], 222, 2, 32),
     ([150, 160], [250, 160], 224, 8, 128), ([1, 513], None, 6, 6, 80),
+    ([70, 9], [90, 9], 2, 1, 160), ([40, 130], None, 3, 3, 192), ([129], [140], 8, 2, 224), ([300], [300], 4, 2, 32),
 ]
 
 
@@ -565,10 +566,12 @@ def test_prompt_infinities_in_masked_places(D, t):
 
 @pytest.mark.parametrize("t", sorted(HALF))
 @pytest.mark.parametrize("ns,ms,Hq,H,D", [([260, 70, 1], [400, 500, 90], 8, 2, 128), ([150], [150], 3, 3, 64), ([200, 65], [200, 70], 4, 2, 256),
-                                          ([130], [100], 2, 2, 48), ([265], [300], 64, 4, 128), ([300], [301], 224, 2, 64)])
+                                          ([130], [100], 2, 2, 48), ([265], [300], 64, 4, 128), ([300], [301], 224, 2, 64),
+                                          ([100], [130], 4, 2, 176), ([140, 70], None, 2, 1, 96), ([300], [300], 2, 2, 32)])
 def test_prompt_infinities_among_many_values(ns, ms, Hq, H, D, t):
     """NaN and infinite values in a tenth of the rows: what a row sees of a column decides, tile by tile."""
     g = np.random.default_rng([96, D])
+    ms = ns if ms is None else ms
     qx, k, v = prompt_inputs(g, ns, ms, Hq, H, D, HALF[t], False)
     Tk = sum(ms)
     bad = np.zeros((Tk, H, D), bool)
