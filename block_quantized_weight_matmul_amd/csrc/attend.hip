@@ -89,7 +89,8 @@ __device__ __forceinline__ uint32_t fresh(uint32_t v) {
   return v;
 }
 
-// QT: type of the queries and outputs; CT: QT or DT_E4M3; DP: columns, D rounded up to 64, 128 or 256.
+// QT: type of the queries and outputs; CT: QT or DT_E4M3; COLS: columns of the products, D rounded up to 32, 64, 96, 128, 192
+// or 256.
 //
 // Scores are computed transposed, S^T = K Q^T (tokens x heads): a lane then holds, for one head, the scores of the eight
 // tokens that its operand of O^T = V^T P^T takes, in the order in which that product's other operand, V^T, can be read
@@ -98,13 +99,14 @@ __device__ __forceinline__ uint32_t fresh(uint32_t v) {
 // P is fed to the matrix cores as the sum of two 16-bit numbers, its rounding and the rest (2^-17 of it in bf16): the
 // cores have time to spare here, and one rounding of P to bf16 would add as much to the output's error as the output's
 // own rounding.  With an e4m3 cache the tokens' scales of the values multiply P, in bf16, which has fp32's range.
-template <int QT, int CT, int DP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attend(AttendArgs a) {
+template <int QT, int CT, int COLS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, COLS > 128 ? 1 : 2) void k_attend(AttendArgs a) {
   constexpr bool kCodes = CT == DT_E4M3;
   constexpr int PT = kCodes ? DT_BF16 : QT;            // type of P and V on the matrix cores
+  constexpr int DP = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;  // of a row in LDS
   constexpr int kSize = kCodes ? 1 : 2, kRow = DP * kSize;
-  constexpr int kLoads = kRow * 16 / 1024;             // of a wave, for 16 tokens
-  constexpr int kBlocks = kTile / 16, kOut = DP / 16;
+  constexpr int kLoads = (COLS * kSize * 16 + 1023) / 1024;  // of a wave, for 16 tokens
+  constexpr int kBlocks = kTile / 16, kOut = COLS / 16;
   constexpr float kLift = PT == DT_F16 ? 8.0f : 0.0f;  // P in fp16 times 2^8: small ones keep their bits
   typedef typename Elem<QT>::T Q;
   typedef typename Elem<PT>::T P;
@@ -134,11 +136,12 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attend(Attend
   const int64_t t1 = split + 1 == a.splits ? len : min(len, t0 + a.piece);
 
   // queries: column col of the products, 8 columns of the head at a time
-  H8<QT> q[DP / 32];
+  constexpr int kSteps = kCodes ? DP / 32 : COLS / 32;  // of 32 columns; a piece of codes holds two
+  H8<QT> q[kSteps];
   {
     const Q* p = static_cast<const Q*>(a.q.p) + b * a.q.st + (h * G + g0 + min(col, rows - 1)) * a.q.sh;
 #pragma unroll
-    for (int j = 0; j < DP / 32; ++j) {
+    for (int j = 0; j < kSteps; ++j) {
       // codes: a 16-byte piece of a row holds the operands of two steps
       const int d = kCodes ? (j / 2) * 64 + quarter * 16 + (j % 2) * 8 : j * 32 + quarter * 8;
       typedef H8<QT> Qu __attribute__((aligned(sizeof(Q))));
@@ -246,14 +249,14 @@ __global__ __launch_bounds__(64 * WAVES, DP == 256 ? 1 : 2) void k_attend(Attend
       const uint32_t key = fresh(key_at[k]);
       if constexpr (kCodes) {
 #pragma unroll
-        for (int j = 0; j < DP / 64; ++j) {
+        for (int j = 0; j < kSteps / 2; ++j) {
           const u32x4 w = *lds_piece<const u32x4>(key, 4 * j);
           s[k] = mma(widen<QT>(w.x, w.y), q[2 * j], s[k]);
           s[k] = mma(widen<QT>(w.z, w.w), q[2 * j + 1], s[k]);
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < DP / 32; ++j)
+        for (int j = 0; j < kSteps; ++j)
           s[k] = mma(*lds_piece<const H8<QT>>(key, 4 * j), q[j], s[k]);
       }
 #pragma unroll
@@ -434,23 +437,28 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   }
 }
 
-template <int QT, int CT>
+template <int QT, int CT, int COLS>
 hipError_t attend(const AttendArgs& a, hipStream_t s) {
-  const dim3 grid(a.splits, a.cache.heads * a.tiles, static_cast<unsigned>(a.B));
-  const dim3 threads(64 * a.waves);
-  if (a.waves > kWaves) {
-    if (a.cache.D <= 64) hipLaunchKernelGGL((k_attend<QT, CT, 64, 2 * kWaves>), grid, threads, 0, s, a);
-    else hipLaunchKernelGGL((k_attend<QT, CT, 128, 2 * kWaves>), grid, threads, 0, s, a);
-  } else if (a.cache.D <= 64) hipLaunchKernelGGL((k_attend<QT, CT, 64, kWaves>), grid, threads, 0, s, a);
-  else if (a.cache.D <= 128) hipLaunchKernelGGL((k_attend<QT, CT, 128, kWaves>), grid, threads, 0, s, a);
-  else hipLaunchKernelGGL((k_attend<QT, CT, 256, kWaves>), grid, threads, 0, s, a);
-  hipError_t e = hipGetLastError();
+  const dim3 grid(a.splits, a.cache.heads * a.tiles, static_cast<unsigned>(a.B)), threads(64 * a.waves);
+  if constexpr (COLS <= 128) {
+    if (a.waves > kWaves) hipLaunchKernelGGL((k_attend<QT, CT, COLS, 2 * kWaves>), grid, threads, 0, s, a);
+  }
+  if (a.waves == kWaves) hipLaunchKernelGGL((k_attend<QT, CT, COLS, kWaves>), grid, threads, 0, s, a);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  const dim3 heads = long_grid(a.B * a.Hq);
-  if (a.cache.D <= 64) hipLaunchKernelGGL((k_attend_join<QT, 16>), heads, dim3(256), 0, s, a);
-  else if (a.cache.D <= 128) hipLaunchKernelGGL((k_attend_join<QT, 32>), heads, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_attend_join<QT, 64>), heads, dim3(256), 0, s, a);
+  constexpr int L = COLS <= 64 ? 16 : COLS <= 128 ? 32 : 64;
+  hipLaunchKernelGGL((k_attend_join<QT, L>), long_grid(a.B * a.Hq), dim3(256), 0, s, a);
   return hipGetLastError();
+}
+
+template <int QT, int CT>
+hipError_t attend_of(const AttendArgs& a, hipStream_t s) {
+  const int D = a.cache.D;
+  if (D <= 32) return attend<QT, CT, 32>(a, s);
+  if (D <= 64) return attend<QT, CT, 64>(a, s);
+  if (D <= 96) return attend<QT, CT, 96>(a, s);
+  if (D <= 128) return attend<QT, CT, 128>(a, s);
+  return D <= 192 ? attend<QT, CT, 192>(a, s) : attend<QT, CT, 256>(a, s);
 }
 
 }  // namespace
@@ -481,8 +489,8 @@ AttendSplit attend_split(const CacheDesc& c, int64_t B, int Hq, int64_t bound) {
 hipError_t launch_attend(AttendArgs a, int qt, hipStream_t s) {
   a.G = a.Hq / a.cache.heads;
   a.tiles = (a.G + kRows - 1) / kRows;
-  if (a.cache.type == DT_E4M3) return qt == DT_F16 ? attend<DT_F16, DT_E4M3>(a, s) : attend<DT_BF16, DT_E4M3>(a, s);
-  return qt == DT_F16 ? attend<DT_F16, DT_F16>(a, s) : attend<DT_BF16, DT_BF16>(a, s);
+  if (a.cache.type == DT_E4M3) return qt == DT_F16 ? attend_of<DT_F16, DT_E4M3>(a, s) : attend_of<DT_BF16, DT_E4M3>(a, s);
+  return qt == DT_F16 ? attend_of<DT_F16, DT_F16>(a, s) : attend_of<DT_BF16, DT_BF16>(a, s);
 }
 
 }  // namespace qmm
