@@ -89,6 +89,10 @@ __device__ __forceinline__ uint32_t fresh(uint32_t v) {
   return v;
 }
 
+// Whether two waves' registers find room in a SIMD: all but those of the widest 16-bit rows (64 x 4000 tokens of 16 / 4 heads of
+// 192 119 -> 110 us, in e4m3 of 256 112 -> 81).
+constexpr bool two_a_simd(int type, int D) { return D <= 192 || type == DT_E4M3; }
+
 // QT: type of the queries and outputs; CT: QT or DT_E4M3; COLS: columns of the products, D rounded up to 32, 64, 96, 128, 192
 // or 256.
 //
@@ -100,7 +104,7 @@ __device__ __forceinline__ uint32_t fresh(uint32_t v) {
 // cores have time to spare here, and one rounding of P to bf16 would add as much to the output's error as the output's
 // own rounding.  With an e4m3 cache the tokens' scales of the values multiply P, in bf16, which has fp32's range.
 template <int QT, int CT, int COLS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, COLS > 128 ? 1 : 2) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(64 * WAVES, two_a_simd(CT, COLS) ? 2 : 1) void k_attend(AttendArgs a) {
   constexpr bool kCodes = CT == DT_E4M3;
   constexpr int PT = kCodes ? DT_BF16 : QT;            // type of P and V on the matrix cores
   constexpr int DP = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;  // of a row in LDS
@@ -440,7 +444,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 template <int QT, int CT, int COLS>
 hipError_t attend(const AttendArgs& a, hipStream_t s) {
   const dim3 grid(a.splits, a.cache.heads * a.tiles, static_cast<unsigned>(a.B)), threads(64 * a.waves);
-  if constexpr (COLS <= 128) {
+  if constexpr (two_a_simd(CT, COLS)) {
     if (a.waves > kWaves) hipLaunchKernelGGL((k_attend<QT, CT, COLS, 2 * kWaves>), grid, threads, 0, s, a);
   }
   if (a.waves == kWaves) hipLaunchKernelGGL((k_attend<QT, CT, COLS, kWaves>), grid, threads, 0, s, a);
@@ -473,13 +477,13 @@ hipError_t attend_of(const AttendArgs& a, hipStream_t s) {
 // 32 x 2000 42.7 -> 38.1, 48 x 4000 119 -> 105, 64 x 10000 332 -> 298; in codes 14.5 -> 9.3, 29.4 -> 25.8, 64 -> 70 and 220
 // -> 167.  So do, two by two, long ones of 16-bit caches (2 x 131072 tokens 140 -> 126 us, 8 x 16384 78 -> 73; codes 86 ->
 // 86 and 49 -> 52; pieces below 512 tokens: 777 tokens 9.0 -> 10.3) where it is the sequences that are too few, not the
-// pieces too long (64 x 20000 581 -> 599).  Heads of more than 128 columns take the registers of twice the waves.
+// pieces too long (64 x 20000 581 -> 599).
 AttendSplit attend_split(const CacheDesc& c, int64_t B, int Hq, int64_t bound) {
   constexpr int64_t kMost = 8192, kStep = kWaves * kTile;
   const int64_t G = Hq / c.heads, units = B * c.heads * ((G + kRows - 1) / kRows);
   const int64_t few = (2 * c.cus + units - 1) / units;
   int64_t n = bound <= 2 * kStep ? 1 : std::min<int64_t>(std::max(few, (bound + kMost - 1) / kMost), 256);
-  const bool twice = c.D <= 128 && (n == 2 || (n > 2 && few > 1 && c.type != DT_E4M3 && bound >= 512 * n));
+  const bool twice = two_a_simd(c.type, c.D) && (n == 2 || (n > 2 && few > 1 && c.type != DT_E4M3 && bound >= 512 * n));
   const int64_t step = twice ? 2 * kStep : kStep;
   if (twice) n = (n + 1) / 2;
   const int64_t piece = std::max<int64_t>((bound + n * step - 1) / (n * step), 1) * step;

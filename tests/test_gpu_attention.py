@@ -311,7 +311,8 @@ ATTEND = [  # B lengths, page, Hq, H, D
     ([300, 17, 64], 32, 21, 3, 80), ([1, 2, 15, 16, 17], 128, 6, 1, 256), ([2000, 1999], 256, 40, 2, 64),
     ([100] * 40, 16, 4, 4, 112), ([4097], 64, 17, 1, 96), ([3000, 10], 16, 33, 1, 128), ([600], 16, 7, 7, 144),
     ([300, 257, 1, 0] + [40] * 60, 16, 10, 5, 64), ([400] + [33] * 36, 32, 8, 8, 128), ([2300, 2049, 0] + [20] * 30, 16, 4, 4, 96),
-    ([300] + [16] * 140, 16, 2, 2, 160),
+    ([300] + [16] * 140, 16, 2, 2, 160), ([290] + [20] * 140, 16, 2, 2, 256), ([400] + [33] * 36, 32, 8, 8, 192),
+    ([300, 20], 16, 4, 2, 32), ([700, 90], 64, 3, 1, 176),
 ]
 
 
