@@ -517,6 +517,20 @@ def test_many_short_sequences(B):
     assert torch.equal(rk, k) and torch.equal(rv, v)
 
 
+@pytest.mark.parametrize("n,Hq,D", [(70, 2, 128), (300, 4, 96), (65, 2, 256), (40, 1, 32)])
+def test_prompt_queries_and_outputs_at_any_element(n, Hq, D):
+    g = np.random.default_rng([98, D])
+    qx, k, v = prompt_inputs(g, [n], [n], Hq, 1, D, torch.bfloat16, False)
+    want = q.attend_prompt(qx, k, v, starts([n]))
+    rows = torch.full((n, Hq * D + 3), float("nan"), device="cuda", dtype=torch.bfloat16)
+    odd = rows[:, 1:1 + Hq * D].unflatten(1, (Hq, D))
+    odd.copy_(qx)
+    room = torch.full((n * Hq * D + 2,), 9.0, device="cuda", dtype=torch.bfloat16)
+    out = room[1:-1].view(n, Hq, D)
+    q.attend_prompt(odd, k, v, starts([n]), out=out)
+    assert torch.equal(out, want) and room[0] == 9 and room[-1] == 9
+
+
 def test_prompt_rows_of_no_sequence():
     g = np.random.default_rng(82)
     qx, k, v = prompt_inputs(g, [100], [100], 2, 1, 64, torch.bfloat16, True)
