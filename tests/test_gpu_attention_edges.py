@@ -37,3 +37,18 @@ def test_join_of_more_than_2_23_heads():
     for n in range(4):  # of one length: the same bits
         rows = out[dev(lengths == n, torch.bool) & rest]
         assert torch.equal(rows, out[n or 4].expand_as(rows))
+
+
+@pytest.mark.parametrize("D", [32, 128, 256])
+def test_a_token_of_zeros_leaves_its_neighbours_bits(D):
+    """Without eps, a token of zeros takes the root's other form; the tokens that share its wave do not."""
+    g = np.random.default_rng([102, D])
+    x = dev(g.standard_normal((64, 4, D)) * 2)
+    w = dev(1 + 0.2 * g.standard_normal(D))
+    want = q.head_norm_rope(x, x, None, None, w, w, eps=0.0)
+    spoiled = x.clone()
+    spoiled[::4] = 0
+    spoiled[1::8, 2] = 1e-18  # a mean square below 2^-100
+    keep = (spoiled == x).all(2)
+    for a, b in zip(want, q.head_norm_rope(spoiled, spoiled, None, None, w, w, eps=0.0)):
+        assert torch.equal(a[keep], b[keep])
