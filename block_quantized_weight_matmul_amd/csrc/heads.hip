@@ -114,8 +114,8 @@ __device__ __forceinline__ void to_cache(const float* v, uint8_t* data, float* s
 }
 
 // 1 / sqrt(m) to about half a step: the hardware's is good to one, and a Newton step halves that.  (A root of a number too
-// small for it takes the division; a lane by its own number only: the vote is a branch, no token's
-// bits depend on the ones beside it.)
+// small for it takes the division, by a lane's own number: the vote is a branch, and no token's bits depend on the ones beside
+// it.)
 __device__ __forceinline__ float inverse_root(float m) {
   float r = __builtin_amdgcn_rsqf(m);
   r = m < INFINITY ? fmaf(fmaf(-m * r, r, 1.0f), 0.5f * r, r) : r;

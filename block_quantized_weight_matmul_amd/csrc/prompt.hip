@@ -58,6 +58,9 @@ __device__ __forceinline__ float both_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// scores so large that the rounding of the maximum, which the fma of a score does not share, would show
+__device__ __forceinline__ bool far_out(float most) { return fabsf(most) > 0x1p20f && fabsf(most) < INFINITY; }
+
 // The lane's number (or the like) as a value that the compiler knows nothing of, so that addresses are made where they are used:
 // kept over the loop they would cost it registers that it does not have.
 __device__ __forceinline__ int again(int v) {
@@ -289,22 +292,24 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, COLS > 128 ? 1 : 2) void k_pro
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, s[k][e]);
       top = both_max(top) * factor;  // factor > 0
+      // The votes are branches: a row's maximum moves, and its scores are scaled ahead, by what the row itself sees, so that its
+      // output has the same bits whatever the rows beside it see.
       if (__any(top > most + kSlack)) {
-        top = fmaxf(most, top);
+        top = top > most + kSlack ? top : most;
         zero = top == -INFINITY ? 0.0f : top;  // nothing but -inf so far: exp of it is 0
         const float shrink = __builtin_amdgcn_exp2f(most - zero);
         most = top;
         total *= shrink;
 #pragma unroll
         for (int d = 0; d < kOut; ++d) o[d] *= shrink;
-        // scores so large that the rounding of the maximum, which the fma below does not share, would show
-        huge = __any(fabsf(top) > 0x1p20f && fabsf(top) < INFINITY);
+        huge = __any(far_out(most));
       }
       float f = factor;
       if (huge) {
+        const bool own = far_out(most);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) s[k] *= factor;
-        f = 1.0f;
+        for (int k = 0; k < 2; ++k) s[k] *= own ? factor : 1.0f;
+        f = own ? 1.0f : factor;
       }
       if constexpr (kCareful) {
         if (j0 + kKeys > whole) {

@@ -52,3 +52,46 @@ def test_a_token_of_zeros_leaves_its_neighbours_bits(D):
     keep = (spoiled == x).all(2)
     for a, b in zip(want, q.head_norm_rope(spoiled, spoiled, None, None, w, w, eps=0.0)):
         assert torch.equal(a[keep], b[keep])
+
+
+def alone(n, at, Hq, H, D, dtype, g):
+    """Queries, keys and values of one sequence in which the scores of token `at` and later ones can be raised, whatever the query:
+    a column of ones meets what the keys hold there."""
+    qx = g.standard_normal((n, Hq, D)) * 1.5
+    qx[..., 3] = 1.0
+    k, v = g.standard_normal((2, n, H, D))
+    k[..., 3] = 0.0
+    return dev(qx, dtype), dev(k, dtype), dev(v, dtype)
+
+
+PREFIXES = [(300, 205, 2, 1, 48), (300, 205, 2, 1, 128), (300, 205, 2, 1, 256), (70, 33, 8, 2, 128), (1100, 1000, 8, 2, 64), (129, 100, 3, 3, 96),
+            (900, 515, 16, 4, 128), (400, 70, 1, 1, 32), (200, 199, 4, 2, 192)]
+
+
+@pytest.mark.parametrize("t", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,at,Hq,H,D", PREFIXES)
+def test_prompt_rows_keep_their_bits_whatever_follows(n, at, Hq, H, D, t):
+    """Keys and values that come after a query do not change a bit of its output: not by how large their scores are (a maximum
+    that moves by much or by little, scores past 2^20), nor by their values."""
+    g = np.random.default_rng([103, n, D])
+    qx, k, v = alone(n, at, Hq, H, D, t, g)
+    s = i32([0, n])
+    for scale in (D ** -0.5, 0.0625):
+        want = q.attend_prompt(qx, k, v, s, scale=scale)
+        # scores higher by 12 (2^17 and more), by 100, and past 2^20
+        for raised in (12 / scale, 100 / scale, 6e4, *([2.0 ** 30] if t == torch.bfloat16 else [])):
+            k2, v2 = k.clone(), v.clone()
+            k2[at:, :, 3] = raised
+            k2[at + 1::2, :, 3] *= -1
+            v2[at:] *= -3
+            got = q.attend_prompt(qx, k2, v2, s, scale=scale)
+            assert torch.equal(got[:at], want[:at]), (scale, raised)
+            assert not torch.equal(got[at:], want[at:])
+    # rows whose own scores are past 2^20, beside rows whose are not
+    if t == torch.bfloat16:
+        far = qx.clone()
+        far[::3] *= 2.0 ** 24
+        some = torch.ones(n, dtype=torch.bool)
+        some[::3] = False
+        got, want = q.attend_prompt(far, k, v, s), q.attend_prompt(qx, k, v, s)
+        assert torch.equal(got[some], want[some])
