@@ -48,6 +48,15 @@ __device__ __forceinline__ i16x4 read_transposed(__attribute__((address_space(3)
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
 }
 
+// 16-bit values with zeros for infinities and NaN
+template <int DT>
+__device__ __forceinline__ i16x4 finite_or_zero(i16x4 v) {
+  constexpr short kExponent = DT == DT_F16 ? 0x7C00 : 0x7F80;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (v[i] & kExponent) == kExponent ? short(0) : v[i];
+  return v;
+}
+
 // the larger (the sum) of a value and the one of the lane 32 further
 __device__ __forceinline__ float both_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -311,18 +320,18 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, COLS > 128 ? 1 : 2) void k_pro
         for (int k = 0; k < 2; ++k) s[k] *= own ? factor : 1.0f;
         f = own ? 1.0f : factor;
       }
+      const bool clean = kCareful && j0 + kKeys > whole;
       if constexpr (kCareful) {
-        if (j0 + kKeys > whole) {
-          // Key by key, each added to the rows that see it.  The probabilities pass through the other tile's room.
+        if (clean) {
+          // Key by key, the values that are not finite, each added to the rows that see it; the products below take zeros for
+          // them.  The probabilities pass through the other tile's room.
           T* const pw = reinterpret_cast<T*>(room + (n + 1 & 1) * 2 * kBytes) + wave * kKeys * 32;
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = __builtin_amdgcn_exp2f(fmaf(s[k][e], f, kLift - zero));
-              total += x;
-              pw[(k * 32 + e / 4 * 8 + half * 4 + e % 4) * 32 + col] = static_cast<T>(x);
-            }
+            for (int e = 0; e < 16; ++e)
+              pw[(k * 32 + e / 4 * 8 + half * 4 + e % 4) * 32 + col] =
+                  static_cast<T>(__builtin_amdgcn_exp2f(fmaf(s[k][e], f, kLift - zero)));
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
           const int seen = min(w.m, i0 + col + shift + 1) - j0;
 #pragma unroll 1
@@ -334,11 +343,13 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, COLS > 128 ? 1 : 2) void k_pro
               typedef T V4 __attribute__((ext_vector_type(4)));
               const V4 v = *reinterpret_cast<const V4*>(lv + j * L::kRow + L::value(j, d) * 16 + half * 8);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[d / 4][d % 4 * 4 + e] = fmaf(x, static_cast<float>(v[e]), o[d / 4][d % 4 * 4 + e]);
+              for (int e = 0; e < 4; ++e) {
+                const float y = static_cast<float>(v[e]);
+                if (!(fabsf(y) < INFINITY)) o[d / 4][d % 4 * 4 + e] = fmaf(x, y, o[d / 4][d % 4 * 4 + e]);
+              }
               __builtin_amdgcn_sched_barrier(0);  // a read at a time: registers again
             }
           }
-          continue;
         }
       }
       // ahead of the SIMD's other wave while the matrix cores have work (8192 tokens 538 -> 527 us)
@@ -355,6 +366,7 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, COLS > 128 ? 1 : 2) void k_pro
             const int row = u * 16 + e * 8 + half * 4 + (lane & 15) / 4, piece = d * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1);
             x.w[e] = read_transposed(
                 (__attribute__((address_space(3))) i16x4*)(lv + row * L::kRow + L::value(row, piece) * 16 + (lane & 1) * 8));
+            if (clean) x.w[e] = finite_or_zero<DT>(x.w[e]);
           }
           vf[u & 1][d] = x.v;
         }
@@ -380,7 +392,8 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, COLS > 128 ? 1 : 2) void k_pro
   __syncthreads();
   if (met) {
     // An infinity or a NaN among the values of a tile which some of the rows see in part: a product of matrices has added 0 *
-    // Inf = NaN to the others.  Once more, with sums of what each row sees in such tiles.
+    // Inf = NaN to the others.  Once more, with such values of such tiles left to the rows that see them: the others' outputs
+    // have the bits that any finite value there would have given them.
     most = -INFINITY, zero = total = 0.0f;
     huge = false;
 #pragma unroll

@@ -703,8 +703,9 @@ qmm_status qmm_cache_attend(const qmm_cache *h, const qmm_attend_args *a, qmm_st
  *   k, v     rows 16-byte aligned; a token's stride D .. 2^23 elements.
  *   scale    positive.    out  DEVICE [Tq, Hq, D], contiguous; rows of no sequence are left as they were.
  * Softmax in fp32, probabilities rounded to dt, outputs rounded once.  A key or value that a query
- * does not see has no influence on it, whatever it holds.  A row whose scores are all -inf is
- * zeros.
+ * does not see changes no bit of its output, whatever it holds.  A row whose scores are all -inf is
+ * zeros.  An infinite value that a row sees gives it an infinity, or NaN where its probability is
+ * rounded to zero.
  */
 typedef struct {
   const void *q, *k, *v;

@@ -95,3 +95,56 @@ def test_prompt_rows_keep_their_bits_whatever_follows(n, at, Hq, H, D, t):
         some[::3] = False
         got, want = q.attend_prompt(far, k, v, s), q.attend_prompt(qx, k, v, s)
         assert torch.equal(got[some], want[some])
+
+
+@pytest.mark.parametrize("t", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,at,Hq,H,D", PREFIXES)
+def test_prompt_rows_keep_their_bits_before_infinities(n, at, Hq, H, D, t):
+    """The same for infinite and NaN keys and values; what does not see the column keeps its bits too."""
+    g = np.random.default_rng([104, n, D])
+    qx, k, v = alone(n, at, Hq, H, D, t, g)
+    s = i32([0, n])
+    want = q.attend_prompt(qx, k, v, s)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for rows in (slice(at, at + 1), slice(at, None, 3), slice(at, None)):
+            k2, v2 = k.clone(), v.clone()
+            k2[rows, H - 1, 5] = bad
+            assert torch.equal(q.attend_prompt(qx, k2, v, s)[:at], want[:at])
+            v2[rows, H - 1, 5] = bad
+            got = q.attend_prompt(qx, k, v2, s)
+            assert torch.equal(got[:at], want[:at])
+            other = torch.ones((Hq, D), dtype=torch.bool)
+            other[Hq - Hq // H:, 5] = False
+            assert torch.equal(got[:, other], want[:, other])
+            assert not bool(torch.isfinite(got[at:, ~other]).any())
+        v2 = v.clone()
+        v2[at:] = bad
+        assert torch.equal(q.attend_prompt(qx, k, v2, s)[:at], want[:at])
+
+
+def limit_of(v, weights):
+    """The definition's outputs where values [m] are infinite or NaN and all weights [n, m] are 0 or well above it."""
+    with np.errstate(invalid="ignore"):
+        return np.array([sum((w * x for w, x in zip(row, v) if w), 0.0) for row in weights])
+
+
+@pytest.mark.parametrize("t", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,H", [(100, 1), (700, 8)])
+def test_prompt_infinite_values_that_are_seen(n, H, t):
+    """With equal scores: an infinity of one sign is the output, two signs or a NaN are NaN."""
+    g = np.random.default_rng([105, n])
+    D = 64
+    v = g.standard_normal((n, H, D))
+    v[n // 4, :, 3] = np.inf
+    v[n // 2, :, 4], v[n // 2 + 3, :, 4] = -np.inf, -np.inf
+    v[n // 3, :, 5], v[n - 9, :, 5] = -np.inf, np.inf
+    v[0, :, 6] = np.nan
+    z = torch.zeros((n, H, D), device="cuda", dtype=t)
+    got = q.attend_prompt(z, z, dev(v, t), i32([0, n])).double().cpu().numpy()
+    for column in (3, 4, 5, 6):
+        want = limit_of(v[:, 0, column], np.tri(n))
+        spoiled = ~np.isfinite(want)
+        assert spoiled.any()
+        for h in range(H):
+            assert np.array_equal(got[spoiled, h, column], want[spoiled], equal_nan=True), column
+            assert np.isfinite(got[~spoiled, h, column]).all()
