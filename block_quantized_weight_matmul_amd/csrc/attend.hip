@@ -89,6 +89,30 @@ __device__ __forceinline__ uint32_t fresh(uint32_t v) {
   return v;
 }
 
+// What the infinite values among columns d .. d + 3 of tokens t0 .. t1 - 1 of key head h add up to, 0 where there are none (an
+// infinity of each sign, or a NaN: NaN).  16 tokens lie one after another in a page.
+template <typename P>
+__device__ __forceinline__ f32x4 infinite_values(const CacheDesc& c, const int32_t* table, int h, int64_t t0, int64_t t1, int d) {
+  typedef P P4 __attribute__((ext_vector_type(4)));
+  f32x4 sum{};
+  for (int64_t t = t0; t < t1; t += 16) {
+    const int64_t page = table[t >> c.shift];
+    if (page < 0 || page >= c.pages) continue;  // (the outputs are NaN anyhow)
+    const int64_t row = ((page * c.heads + h) << c.shift) + (t & ((int64_t(1) << c.shift) - 1));
+    P4 v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = *reinterpret_cast<const P4*>(reinterpret_cast<const P*>(c.v) + (row + i) * c.D + d);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = static_cast<float>(v[i][e]);
+        if (t + i < t1 && !(fabsf(x) < INFINITY)) sum[e] += x;
+      }
+  }
+  return sum;
+}
+
 // Whether two waves' registers find room in a SIMD: all but those of the widest 16-bit rows (64 x 4000 tokens of 16 / 4 heads of
 // 192 119 -> 110 us, in e4m3 of 256 112 -> 81).
 constexpr bool two_a_simd(int type, int D) { return D <= 192 || type == DT_E4M3; }
@@ -348,6 +372,15 @@ __global__ __launch_bounds__(64 * WAVES, two_a_simd(CT, COLS) ? 2 : 1) void k_at
       const float m = sums[w][0][r], l = sums[w][1][r];
       sum += m == -INFINITY && l == 0.0f ? 0.0f : l * (m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top));
       v += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(lds[w]) + r * DP + d);
+    }
+    if constexpr (!kCodes) {  // (codes have no infinity)
+      const f32x4 x = v * 0.0f;
+      if (x[0] + x[1] + x[2] + x[3] != 0.0f && sum == sum) {
+        // Infinite values: with rests of P that are 0 or negative they have become NaN.
+        const f32x4 y = infinite_values<Q>(c, table, h, t0, t1, d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = y[e] == 0.0f ? v[e] : y[e];
+      }
     }
     const int64_t head = b * a.Hq + h * G + g0 + r;
     if (a.splits == 1) {

@@ -677,7 +677,8 @@ qmm_status qmm_cache_read(const qmm_cache *h, const qmm_cache_read_args *a, qmm_
  *            call; concurrent calls need separate ones.
  * Softmax in fp32; probabilities keep 16 bits or more; outputs are rounded once.  What the cache
  * holds past a sequence's last token has no influence, whatever it is.  A row whose scores are all
- * -inf is zeros; an infinite value gives NaN.
+ * -inf is zeros.  An infinite value that a row sees gives it an infinity, or NaN where its
+ * probability is rounded to zero; one of each sign, or a NaN, gives NaN.
  */
 typedef struct {
   const void *q;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import block_quantized_weight_matmul_amd as q
-from tests.test_gpu_attention import attend_reference, i32, within
+from tests.test_gpu_attention import attend_reference, filled, i32, within
 from tests.test_gpu_f8 import dev
 
 pytestmark = pytest.mark.gpu
@@ -148,3 +148,54 @@ def test_prompt_infinite_values_that_are_seen(n, H, t):
         for h in range(H):
             assert np.array_equal(got[spoiled, h, column], want[spoiled], equal_nan=True), column
             assert np.isfinite(got[~spoiled, h, column]).all()
+
+
+ONE_KIND = [([40], 1), ([100, 33], 2), ([500], 8), ([260] * 40, 8), ([3000, 700], 1), ([5000], 2)]  # lengths, key heads
+
+
+@pytest.mark.parametrize("D", [64, 80, 128, 192, 256])
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("lengths,H", ONE_KIND)
+def test_decode_infinite_values(lengths, H, kind, D):
+    """With equal scores: an infinity of one sign is the output, two signs or a NaN are NaN, and the columns beside them keep
+    their bits, however the work is divided."""
+    g = np.random.default_rng([106, len(lengths), D])
+    c, table, owner, tok = filled(g, lengths, 16, H, D, kind)
+    slots = i32(table[owner, tok // 16] * 16 + tok % 16)
+    tab, n = i32(table.flatten()).view(len(lengths), -1), i32(lengths)
+    k, v = torch.zeros((len(tok), H, D), device="cuda"), g.standard_normal((len(tok), H, D))
+    qx = torch.zeros((len(lengths), 2 * H, D), device="cuda", dtype=c.dtype)
+    bounds = (None, 0, 5000)
+    c.write(k, dev(v), slots)
+    want = [c.attend(qx, tab, n, max_length=m) for m in bounds]
+    for b, m in enumerate(lengths):
+        first = int(np.flatnonzero(owner == b)[0])
+        v[first + m // 4, :, 3] = np.inf
+        v[[first + m // 2, first + m // 2 + 3], :, 4] = -np.inf
+        v[first + m // 3, :, 5], v[first + m - 9, :, 5] = -np.inf, np.inf
+        v[first, :, 6] = np.nan
+    c.write(k, dev(v), slots)
+    others = [i for i in range(D) if not 3 <= i <= 6]
+    for m, y in zip(bounds, want):
+        got = c.attend(qx, tab, n, max_length=m)
+        assert bool((got[..., 3] == float("inf")).all()) and bool((got[..., 4] == -float("inf")).all())
+        assert bool(torch.isnan(got[..., 5:7]).all())
+        assert torch.equal(got[..., others], y[..., others])
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_decode_infinite_values_of_any_probability(kind):
+    """Probabilities from 1 down to 2^-24, at places of every kind in a tile: infinities all the same."""
+    g = np.random.default_rng(107)
+    H, D, m = 1, 64, 64
+    c, table, _, tok = filled(g, [m], 16, H, D, kind)
+    slots = i32(table[0, tok // 16] * 16 + tok % 16)
+    k = np.zeros((m, H, D))
+    k[:, 0, 0] = -np.linspace(0, 24, m) * np.log(2)  # scores of a query of ones, in powers of two
+    v = g.standard_normal((m, H, D))
+    v[np.arange(m), 0, np.arange(m)] = np.inf  # column j: token j's
+    qx = torch.zeros((1, 1, D), device="cuda", dtype=c.dtype)
+    qx[..., 0] = 1
+    c.write(dev(k), dev(v), slots)
+    got = c.attend(qx, i32(table.flatten()).view(1, -1), i32([m]), scale=1.0)
+    assert bool((got == float("inf")).all())
