@@ -459,7 +459,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const float w = weight(at[i]);
-      if (s + i * kTeams < n && w != 0.0f) v += w * x[i];
+      if (s + i * kTeams < n) v += w * x[i];  // (also where w is 0: what is infinite or NaN there has been seen)
     }
     if (s + kAhead * kTeams < n) load(s + kAhead * kTeams);
   }

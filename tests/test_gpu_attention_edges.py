@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import block_quantized_weight_matmul_amd as q
-from tests.test_gpu_attention import attend_reference, filled, i32, within
+from tests.test_gpu_attention import CACHES, attend_reference, filled, i32, within
 from tests.test_gpu_f8 import dev
 
 pytestmark = pytest.mark.gpu
@@ -199,3 +199,30 @@ def test_decode_infinite_values_of_any_probability(kind):
     c.write(dev(k), dev(v), slots)
     got = c.attend(qx, i32(table.flatten()).view(1, -1), i32([m]), scale=1.0)
     assert bool((got == float("inf")).all())
+
+
+@pytest.mark.parametrize("kind", CACHES)
+def test_decode_joins_what_pieces_of_no_weight_hold(kind):
+    """A NaN or infinite value in a piece whose probabilities are rounded to zero beside another piece's: seen all the same, in
+    one piece or many."""
+    g = np.random.default_rng(108)
+    H, D, m = 1, 128, 4000
+    c, table, _, tok = filled(g, [m], 16, H, D, kind)
+    at = table[0, tok // 16] * 16 + tok % 16
+    k, v = np.zeros((m, H, D)), g.standard_normal((m, H, D))
+    k[:-100, 0, 0] = -400.0
+    qx = torch.ones((1, 2, D), device="cuda", dtype=torch.float16 if kind == "e4m3" else c.dtype)
+    c.write(dev(k), dev(v), i32(at))
+    tab = i32(table.flatten()).view(1, -1)
+    want = [c.attend(qx, tab, i32([m]), scale=1.0, max_length=bound) for bound in (None, 0)]
+    assert all(bool(torch.isfinite(y).all()) for y in want)
+    for bad in (float("nan"), float("inf")):
+        v2 = dev(v)
+        v2[50, 0, 5] = bad
+        c.write(dev(k), v2, i32(at))
+        for bound, y in zip((None, 0), want):
+            got = c.attend(qx, tab, i32([m]), scale=1.0, max_length=bound)
+            assert not bool(torch.isfinite(got[..., 5]).any())
+            if kind != "e4m3":
+                others = [i for i in range(D) if i != 5]
+                assert torch.equal(got[..., others], y[..., others])
