@@ -1,11 +1,14 @@
-"""Build libqmm.so (the C-ABI library) for gfx950 with hipcc, and _calls.so (the binding's native calls), in-tree.
+"""Build libqmm.so (the C-ABI library) for gfx950 with hipcc, and _calls.so (the binding's native calls) where it can be
+built, in-tree.
 
     python block_quantized_weight_matmul_amd/build.py [-v]
 
 Every HIP source under csrc/ is compiled to an object under _build/ (in
 parallel), then linked into block_quantized_weight_matmul_amd/libqmm.so; csrc/calls.cpp,
-host code against Python's and torch's headers, into _calls.so next to it.
-Cross-compiles without a GPU.
+host code against Python's and torch's headers, into _calls.so next to it.  The
+library needs hipcc only.  Where _calls.so cannot be built (no torch, headers or
+g++) it is left out, with a message, and the binding makes its calls through
+ctypes.  Cross-compiles without a GPU.
 """
 
 import concurrent.futures
@@ -75,21 +78,31 @@ def _compile_calls(verbose):
     return [obj, "-L", PKG, "-lqmm", *libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
 
 
+def _build_calls(compiled, verbose):
+    """Link _calls.so of what `compiled` (a future of _compile_calls) has made.  One of an earlier build goes first: it may
+    take another library's arguments."""
+    if os.path.exists(CALLS):
+        os.remove(CALLS)
+    try:
+        tmp = CALLS + ".tmp"
+        _run(["g++", "-shared", "-o", tmp, *compiled.result()], "link of _calls.so", verbose)
+        os.replace(tmp, CALLS)
+    except (ImportError, OSError, RuntimeError) as e:
+        print(f"_calls.so is not built; the attention calls go through ctypes: {e}", file=sys.stderr, flush=True)
+
+
 def build(verbose=False, jobs=None):
-    """Compile every source and link libqmm.so and _calls.so; returns the library's path."""
+    """Compile every source and link libqmm.so, and _calls.so where that can be built; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs), os.cpu_count() or 1, 16)
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
         calls = ex.submit(_compile_calls, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        calls = calls.result()
     tmp = LIB + ".tmp"
     _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], "link", verbose)
     os.replace(tmp, LIB)
-    tmp = CALLS + ".tmp"
-    _run(["g++", "-shared", "-o", tmp, *calls], "link of _calls.so", verbose)
-    os.replace(tmp, CALLS)
+    _build_calls(calls, verbose)
     return LIB
 
 
