@@ -29,7 +29,7 @@ from .f8 import _DT, _call, _current_device, _current_stream, _empty, _out, _pla
 
 try:
     from . import _calls  # csrc/calls.cpp
-except ImportError:  # another torch than it was built against: the same calls, through ctypes
+except ImportError:  # not built, or for another torch or Python, which it tells: the same calls, through ctypes
     _calls = None
 
 _HALF = {torch.float16: 1, torch.bfloat16: 2}

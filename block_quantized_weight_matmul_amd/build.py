@@ -69,10 +69,12 @@ def _run(cmd, what, verbose):
 
 
 def _compile_calls(verbose):
+    import torch
     from torch.utils import cpp_extension
     obj = os.path.join(BUILD, "calls.host.o")
     paths = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
-    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden", *(a for p in paths for a in ("-I", p)), "-c",
+    built_for = f'-DQMM_BUILT_FOR="{torch.__version__} {sys.version_info[0]}.{sys.version_info[1]}"'
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden", built_for, *(a for p in paths for a in ("-I", p)), "-c",
           os.path.join(CSRC, "calls.cpp"), "-o", obj], "g++ on calls.cpp", verbose)
     libs = [a for p in cpp_extension.library_paths() for a in ("-L", p)]
     return [obj, "-L", PKG, "-lqmm", *libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]

@@ -11,6 +11,9 @@
 
 #include <ATen/ATen.h>
 
+#include <cmath>
+#include <initializer_list>
+
 #include "qmm.h"
 
 namespace {
@@ -295,4 +298,17 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&kModule); }
+// QMM_BUILT_FOR: torch.__version__ and Python's of the build.  Tensors' insides and Python's are inlined above, so a module of
+// another build is refused, whether its symbols resolve or not; attention.py then goes without.
+PyMODINIT_FUNC PyInit__calls() {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  PyObject* python = PySys_GetObject("version_info");  // borrowed
+  PyObject* major = version && python ? PySequence_GetItem(python, 0) : nullptr;
+  PyObject* minor = major ? PySequence_GetItem(python, 1) : nullptr;
+  PyObject* here = minor ? PyUnicode_FromFormat("%S %S.%S", version, major, minor) : nullptr;
+  const bool same = here && PyUnicode_CompareWithASCIIString(here, QMM_BUILT_FOR) == 0;
+  if (here && !same) PyErr_Format(PyExc_ImportError, "built for torch and Python %s, not %U", QMM_BUILT_FOR, here);
+  for (PyObject* o : {torch, version, major, minor, here}) Py_XDECREF(o);
+  return same ? PyModule_Create(&kModule) : nullptr;
+}
