@@ -103,6 +103,11 @@ def _weights(q_weight, k_weight, D, device):
             0 if k_weight is None else _vector(k_weight, "k_weight", dtype, D, device), _DT[dtype])
 
 
+def _single(v):
+    """A number as fp32 holds it; one beyond its range is infinite, which the library refuses."""
+    return ctypes.c_float(v).value
+
+
 def _result_type(dtype):
     if dtype not in _DT:
         raise ValueError(f"dtype {dtype}; expected one of {[str(d) for d in _DT]}")
@@ -131,7 +136,7 @@ def head_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=
     qo, ko = _empty((T, Hq, D), dtype, d), _empty((T, H, D), dtype, d)
     _call(d, lib.qmm_head_norm_rope, _pack_heads(
         q.data_ptr(), k.data_ptr(), 0, qw, kw, pos, freq, 0, qo.data_ptr(), ko.data_ptr(), qt, qh, kt, kh, 0, 0, T, Hq, H, D, R,
-        _DT[xt], wt, _DT[dtype], 1 if interleaved else 0, eps))
+        _DT[xt], wt, _DT[dtype], 1 if interleaved else 0, _single(eps)))
     return qo, ko
 
 
@@ -249,7 +254,7 @@ class KVCache:
         o = _empty((T, Hq, D), dtype, d)
         _call(d, lib.qmm_cache_norm_rope_write, self._h, _pack_heads(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), qw, kw, pos, freq, at, o.data_ptr(), 0, qt, qh, kt, kh, vt, vh, T, Hq,
-            self.heads, D, R, _DT[xt], wt, _DT[dtype], 1 if interleaved else 0, eps))
+            self.heads, D, R, _DT[xt], wt, _DT[dtype], 1 if interleaved else 0, _single(eps)))
         return o
 
     def _table(self, table, B):
@@ -320,7 +325,7 @@ class KVCache:
         ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
         _call(d, lib.qmm_cache_attend, self._h, _pack_attend(
             q.data_ptr(), at, lens, out.data_ptr(), ws.data_ptr() if nb else 0, qt, qh, B, Hq, W, bound, nb, _HALF[t],
-            D ** -0.5 if scale is None else scale))
+            D ** -0.5 if scale is None else _single(scale)))
         return out
 
 
@@ -359,5 +364,5 @@ def attend_prompt(q, k, v, starts, k_starts=None, causal=True, scale=None, out=N
         raise ValueError("out must have q's dtype")
     _call(d, lib.qmm_attend_prompt, _pack_prompt(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, out.data_ptr(), qt, qh, kt, kh, vt, vh, n - 1, Tq, Tk, Hq, H, D, _HALF[t],
-        1 if causal else 0, D ** -0.5 if scale is None else scale))
+        1 if causal else 0, D ** -0.5 if scale is None else _single(scale)))
     return out

@@ -226,3 +226,16 @@ def test_decode_joins_what_pieces_of_no_weight_hold(kind):
             if kind != "e4m3":
                 others = [i for i in range(D) if i != 5]
                 assert torch.equal(got[..., others], y[..., others])
+
+
+def test_numbers_beyond_fp32_are_refused():
+    x, w = torch.zeros((5, 4, 32), device="cuda", dtype=torch.float16), torch.ones(32, device="cuda")
+    c = q.KVCache.empty(4, 16, 2, 32, torch.float16)
+    table, n = i32(range(4)).view(2, 2), i32([3, 3])
+    for far in (1e39, -1e39, 1e300):
+        for what, call in (("eps", lambda: q.head_norm_rope(x, x, None, None, w, w, eps=far)),
+                           ("eps", lambda: c.norm_rope_write(x, x[:, :2], x[:, :2], i32([0] * 5), None, None, w, w, eps=far)),
+                           ("scale", lambda: c.attend(x[:2], table, n, scale=far)),
+                           ("scale", lambda: q.attend_prompt(x, x, x, i32([0, 5]), scale=far))):
+            with pytest.raises(q.QmmError, match=what):
+                call()
