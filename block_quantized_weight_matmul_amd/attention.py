@@ -146,7 +146,7 @@ class KVCache:
     to 256.  The tensors are kept referenced and written in place.
 
     A token's slot is its page times `page` plus its row there; a table int32 [B, W] names the pages of B sequences in
-    order, entries past a sequence's last page are not read."""
+    order, entries past a sequence's last page may hold anything: no result depends on them."""
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
         _tensor(k, "k", _CACHE, (4,))

@@ -618,7 +618,8 @@ qmm_status qmm_head_norm_rope(const qmm_head_args *a, qmm_stream_t stream);
  *
  * A token's place is its slot, page * (tokens of a page) + row.  A sequence's places are a row of
  * a table int32 [B][W]: its token t lies on page table[b][t / page].  Entries past a sequence's
- * last page are not read.
+ * last page may hold anything: the calls may read them, and the cache's rows that they name, but
+ * nothing of it reaches a result.
  */
 typedef struct qmm_cache qmm_cache;
 qmm_status qmm_cache_create(qmm_cache **out, void *k, void *v, float *k_scales, float *v_scales,

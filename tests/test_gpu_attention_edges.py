@@ -239,3 +239,24 @@ def test_numbers_beyond_fp32_are_refused():
                            ("scale", lambda: q.attend_prompt(x, x, x, i32([0, 5]), scale=far))):
             with pytest.raises(q.QmmError, match=what):
                 call()
+
+
+@pytest.mark.parametrize("kind", CACHES)
+def test_table_entries_past_the_last_page(kind):
+    """Whatever they hold: pages of NaN, of other sequences, or none at all."""
+    g = np.random.default_rng(109)
+    lengths, page, H, D = [40, 33, 0, 1500, 129], 16, 2, 64
+    c, table, _, _ = filled(g, lengths, page, H, D, kind)
+    B, n = len(lengths), i32(lengths)
+    past = np.arange(table.shape[1])[None] >= -(-np.array(lengths) // page)[:, None]
+    qx = dev(g.standard_normal((B, 4, D)), torch.float16 if kind == "e4m3" else c.dtype)
+    first = i32(np.concatenate([[0], np.cumsum(lengths)]))
+
+    def calls(entries):
+        tab = i32(np.where(past, entries, table).flatten()).view(B, -1)
+        return (*(c.attend(qx, tab, n, max_length=m) for m in (None, 0, 200)), *c.read(tab, first, sum(lengths)))
+
+    want = calls(-1)
+    assert all(bool(torch.isfinite(y).all()) for y in want)
+    for entries in (g.integers(0, c.pages, table.shape), c.pages, (1 << 31) - 1, -(1 << 31)):
+        assert all(torch.equal(a, b) for a, b in zip(calls(entries), want))
