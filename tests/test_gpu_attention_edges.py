@@ -1,12 +1,15 @@
 """Head norms, the paged cache and attention where their ranges end, and what may stand beside a row: on the device, against
 the fp64 oracle or bit for bit."""
 
+import struct
+
 import numpy as np
 import pytest
 import torch
 
 import block_quantized_weight_matmul_amd as q
-from tests.test_gpu_attention import CACHES, attend_reference, filled, i32, within
+from block_quantized_weight_matmul_amd import _lib as L
+from tests.test_gpu_attention import CACHES, attend_reference, filled, frequencies, i32, within
 from tests.test_gpu_f8 import dev
 
 pytestmark = pytest.mark.gpu
@@ -260,3 +263,39 @@ def test_table_entries_past_the_last_page(kind):
     assert all(bool(torch.isfinite(y).all()) for y in want)
     for entries in (g.integers(0, c.pages, table.shape), c.pages, (1 << 31) - 1, -(1 << 31)):
         assert all(torch.equal(a, b) for a, b in zip(calls(entries), want))
+
+
+@pytest.mark.parametrize("kind", CACHES)
+def test_a_page_that_is_none_among_many_pieces(kind):
+    """A table entry that names no page makes its sequence's outputs NaN, in one piece or many, and no other's."""
+    g = np.random.default_rng(110)
+    lengths, page, H, D = [5000, 40, 3000], 16, 1, 128
+    c, table, _, _ = filled(g, lengths, page, H, D, kind)
+    for t in (torch.float16, torch.bfloat16) if kind == "e4m3" else (c.dtype,):
+        qx = dev(g.standard_normal((3, 2, D)), t)
+        for bound in (None, 0, 300):
+            want = c.attend(qx, i32(table.flatten()).view(3, -1), i32(lengths), max_length=bound)
+            assert bool(torch.isfinite(want).all())
+            for b, at, entry in ((0, 0, -1), (0, 150, c.pages), (0, 312, -9), (1, 2, 1 << 30), (2, 187, -1), (2, 100, c.pages)):
+                bad = table.copy()
+                bad[b, at] = entry
+                got = c.attend(qx, i32(bad.flatten()).view(3, -1), i32(lengths), max_length=bound)
+                others = [i for i in range(3) if i != b]
+                assert bool(torch.isnan(got[b]).all()) and torch.equal(got[others], want[others])
+
+
+@pytest.mark.parametrize("interleaved", [0, 1])
+@pytest.mark.parametrize("t", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("T,Hq,H,D,R", [(1, 40, 13, 128, 128), (300, 9, 6, 80, 48), (40, 33, 7, 256, 256), (8192, 5, 5, 64, 16)])
+def test_head_norm_in_place(T, Hq, H, D, R, t, interleaved):
+    """q_out and k_out may be q and k themselves: more heads than a layer loads at once, with the bits of the call that gives
+    new tensors."""
+    g = np.random.default_rng([111, T, D])
+    qx, kx = (dev(g.standard_normal((T, n, D)), t) for n in (Hq, H))
+    w, freq, pos = dev(1 + 0.2 * g.standard_normal(D)), dev(frequencies(R)), i32(g.integers(0, 1 << 20, T))
+    want = q.head_norm_rope(qx, kx, pos, freq, w, w, interleaved=bool(interleaved))
+    dt = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}[t]
+    args = struct.pack("21q4if4x", qx.data_ptr(), kx.data_ptr(), 0, w.data_ptr(), w.data_ptr(), pos.data_ptr(), freq.data_ptr(), 0,
+                       qx.data_ptr(), kx.data_ptr(), Hq * D, D, H * D, D, 0, 0, T, Hq, H, D, R, dt, 0, dt, interleaved, 1e-6)
+    L.check(L.lib.qmm_head_norm_rope(args, torch.cuda.current_stream().cuda_stream))
+    assert torch.equal(qx, want[0]) and torch.equal(kx, want[1])
