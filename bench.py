@@ -728,7 +728,8 @@ def extra_moe(torch, q, W, args):
 
 def extra_attention(torch, q, W, args):
     """Between the decode layer's projections (32 query and 8 key heads of 128, from their row counts): a decode step's
-    norms, rotation and cache write with the attention over the cache, rotated over > 1 GiB of caches; a prompt's attention."""
+    norms, rotation and cache write with the attention over the cache, rotated over > 1 GiB of caches; prompts' attention, one after
+    another."""
     D = 128
     Hq, H = W.DECODE_SHAPES[0][1] // D, W.DECODE_SHAPES[1][1] // D
     page, length = 64, 4096
@@ -760,13 +761,17 @@ def extra_attention(torch, q, W, args):
             res.append({"cache": kind, "sequences": B, "length": length, "us_per_step": us,
                         "cache_gbs": B * length * row / (us * 1e-6) / 1e9, "copies": copies})
             del caches
-    T = 2048
-    x = torch.randn((T, Hq + 2 * H, D), device="cuda").to(torch.float16)
+    T, copies = 2048, 16
+    xs = [torch.randn((T, Hq + 2 * H, D), device="cuda").to(torch.float16) for _ in range(copies)]
     starts = torch.tensor([0, T], dtype=torch.int32, device="cuda")
-    g = capture(torch, lambda: q.attend_prompt(x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], starts))
-    us = time_graph(torch, g, args.rounds) * 1e3
+
+    def prompts():
+        for x in xs:
+            q.attend_prompt(x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], starts)
+    g = capture(torch, prompts)
+    us = time_graph(torch, g, args.rounds) * 1e3 / copies
     return {"workload": f"{Hq} query and {H} key heads of {D}, fp32 projections, pages of {page}", "decode_step": res,
-            "prompt": {"tokens": T, "us": us, "tflops": 2 * Hq * D * T * (T + 1) / (us * 1e-6) / 1e12}}
+            "prompt": {"tokens": T, "copies": copies, "us": us, "tflops": 2 * Hq * D * T * (T + 1) / (us * 1e-6) / 1e12}}
 
 
 def extra_quantize(torch, q, W, mats, args):
