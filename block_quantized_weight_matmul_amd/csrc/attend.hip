@@ -170,8 +170,10 @@ __global__ __launch_bounds__(64 * WAVES, two_a_simd(CT, COLS) ? 2 : 1) void k_at
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quarter = lane >> 4;
   const int D = c.D, H = c.heads, G = a.G;
-  const int split = blockIdx.x, h = a.tiles == 1 ? blockIdx.y : blockIdx.y / a.tiles, g0 = (blockIdx.y - h * a.tiles) * kRows;
-  const int64_t b = blockIdx.z;
+  // Pieces vary slowest: workgroup i runs on die i mod 8, and where the bound is far above the lengths it is the first pieces that
+  // there are (fastest, 64 x 8192 tokens of a table that reaches 131072 ran on one die of eight: 254 us, not 1539).
+  const int split = blockIdx.z, h = a.tiles == 1 ? blockIdx.x : blockIdx.x / a.tiles, g0 = (blockIdx.x - h * a.tiles) * kRows;
+  const int64_t b = blockIdx.y;
   const int rows = min(kRows, G - g0);                 // heads here
   const int64_t room = a.W << c.shift;
   const int64_t t0 = split * a.piece;
@@ -500,7 +502,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 
 template <int QT, int CT, int COLS>
 hipError_t attend(const AttendArgs& a, hipStream_t s) {
-  const dim3 grid(a.splits, a.cache.heads * a.tiles, static_cast<unsigned>(a.B)), threads(64 * a.waves);
+  const dim3 grid(a.cache.heads * a.tiles, static_cast<unsigned>(a.B), a.splits), threads(64 * a.waves);
   if constexpr (two_a_simd(CT, COLS)) {
     if (a.waves > kWaves) hipLaunchKernelGGL((k_attend<QT, CT, COLS, 2 * kWaves>), grid, threads, 0, s, a);
   }
