@@ -2,9 +2,10 @@
 //
 //   out[i, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q_i.k_j - max),  j <= i + (m - n)  (m keys, n queries)
 //
-// Bound by the matrix cores, of which the card's power allows a part: 8192 tokens, 32 / 8 heads of 128, bf16, take 504 us,
-// 1.09 PFLOP/s at 1.9 GHz (with zeros for inputs 440 us), 16 packed prompts of 50 to 1024 queries with up to 1024 keys before
-// them 166 us; of many short sequences by memory: 128 of 64 tokens 37 us, 4.5 TB/s.
+// Bound by the matrix cores, of which the card's power allows a part: 8192 tokens, 32 / 8 heads of 128, bf16, take 505 us in a
+// long run, 1.09 PFLOP/s at 1.9 GHz (with zeros for inputs 440 us; in the first tenth of a second after idling 550 to 610), 16
+// packed prompts of 50 to 1024 queries with up to 1024 keys before them 168 us (180 to 205); of many short sequences by memory:
+// 128 of 64 tokens 38 us, 4.4 TB/s.
 //
 // A workgroup takes 128 rows, queries of up to four heads that share a key head, and sweeps the keys they may see in tiles
 // of 64: keys and values go straight into LDS, two tiles deep, while the waves, 32 queries of one head each, work on the
@@ -22,7 +23,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kRows = 128, kWaves = 4;  // of a workgroup: queries times heads, waves that they are divided among
 constexpr int kKeys = 64;               // of a tile
-constexpr int kCus = 256;               // compute units
+constexpr int kCus = 256;               // compute units of the card (a call without a handle knows no other number)
 
 template <int QT> struct Half8 { typedef typename Elem<QT>::T V __attribute__((ext_vector_type(8))); };
 template <int QT> using H8 = typename Half8<QT>::V;
@@ -136,8 +137,12 @@ __device__ __forceinline__ Work find_work(const PromptArgs& a, int64_t index, in
 // Scores are computed transposed, S^T = K Q^T (keys x queries): a lane then holds, for one query, the scores of the keys
 // that its operand of O^T = V^T P^T takes, in the order in which that product's other operand, V^T, can be read from
 // row-major LDS by transposing reads; the probabilities never leave their lane, and a row's maximum takes one exchange
-// between two lanes.  P is rounded to DT once: its 2^-9 (bf16) of each term, with independent signs, stays below the
-// rounding of the output.
+// between two lanes.
+//
+// P is rounded to DT once: up to 2^-8 of a term in bf16 (2^-11 in fp16), with independent signs, which stays below the output's
+// own rounding and adds to it: against fp64 2.3e-3 of the root mean square, not 1.7e-3 (16 packed prompts), 2.1e-3, not 1.6e-3
+// (8192 tokens).  P as two numbers leaves the output's rounding alone and takes half as many products again: 168 -> 222 us, 505
+// -> 696.
 //
 // PARTS: as often a workgroup has four waves for its rows, and each four take every PARTS-th tile of keys.
 template <int DT, int COLS, int PARTS>
@@ -203,7 +208,7 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, COLS > 128 ? 1 : 2) void k_pro
   };
 
   // Queries and outputs pass through the second tile's room, so that their rows are read and written whole (not as the
-  // products have them, 16 or 32 bytes of a row at a time: 64 sequences of 128 tokens 49 -> 40 us, 16 of 1000 203 -> 191): a
+  // products have them, 16 or 32 bytes of a row at a time: 128 sequences of 64 tokens 48 -> 37 us, 16 of 1000 203 -> 191): a
   // wave's 32 rows, 16-byte piece lane % kPieces of row lane / kPieces and of every kPer-th after it.
   typedef H8<DT> H8u __attribute__((aligned(sizeof(T))));
   const auto rows_at = [&](uint8_t* base, int row, int piece) { return base + row * L::kRow + L::key(row, piece) * 16; };
@@ -456,7 +461,8 @@ hipError_t launch(const PromptArgs& a, hipStream_t s) {
 // of 8 heads 40.5 -> 32.7, 4096 75 -> 60; 128 of 16 heads 7.6 -> 8.2, 16 of those 10.4 -> 16.0.  And where two would share a
 // unit, one of which sweeps much longer than the other, in long sequences without much of a prefix: 2048 tokens of 32 heads
 // 53.7 -> 47.1, 8192 of 8 180 -> 146; four of 512 of 32 heads 21.6 -> 26.2.  More workgroups than that keep the units busy:
-// 4096 tokens of 32 heads 139 -> 152.
+// 4096 tokens of 32 heads 139 -> 152.  (Lengths by their mean, all that the host knows: a long sequence among many short ones
+// counts as short.)
 template <int DT, int COLS>
 hipError_t prompt(const PromptArgs& a, hipStream_t s) {
   if constexpr (COLS <= 128) {
