@@ -410,9 +410,9 @@ __global__ __launch_bounds__(64 * WAVES, two_a_simd(CT, COLS) ? 2 : 1) void k_at
     const int64_t head = b * a.Hq + h * G + g0 + r;
     if (a.splits == 1) {
       Q* out = static_cast<Q*>(a.out) + head * D + d;
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float inv = 1.0f / sum;  // no sum: zeros, whatever the values are
 #pragma unroll
-      for (int e = 0; e < 4; ++e) out[e] = static_cast<Q>(v[e] * inv);
+      for (int e = 0; e < 4; ++e) out[e] = static_cast<Q>(sum == 0.0f ? 0.0f : v[e] * inv);
     } else {
       *reinterpret_cast<f32x4*>(a.ws + (head * a.splits + split) * D + d) = v;
       if (d == 0) {
@@ -493,10 +493,10 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   if (team == 0 && d < D) {
 #pragma unroll
     for (int i = 1; i < kTeams; ++i) v += part[i][tid];
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = 1.0f / sum;
     Q* out = static_cast<Q*>(a.out) + head * D + d;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) out[e] = static_cast<Q>(v[e] * inv);
+    for (int e = 0; e < 4; ++e) out[e] = static_cast<Q>(sum == 0.0f ? 0.0f : v[e] * inv);
   }
 }
 

@@ -10,7 +10,7 @@ import torch
 import block_quantized_weight_matmul_amd as q
 from block_quantized_weight_matmul_amd import _lib as L
 from tests.test_gpu_attention import CACHES, attend_reference, filled, frequencies, i32, within
-from tests.test_gpu_f8 import dev
+from tests.test_gpu_f8 import DTYPES, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -299,3 +299,28 @@ def test_head_norm_in_place(T, Hq, H, D, R, t, interleaved):
                        qx.data_ptr(), kx.data_ptr(), Hq * D, D, H * D, D, 0, 0, T, Hq, H, D, R, dt, 0, dt, interleaved, 1e-6)
     L.check(L.lib.qmm_head_norm_rope(args, torch.cuda.current_stream().cuda_stream))
     assert torch.equal(qx, want[0]) and torch.equal(kx, want[1])
+
+
+@pytest.mark.parametrize("bad", [0.5, float("inf"), float("nan")])
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_rows_whose_scores_are_all_minus_infinity(kind, bad):
+    """Keys of -inf under a query that is positive there: zeros, whatever the values are; the other queries are not touched."""
+    g = np.random.default_rng(112)
+    t, H, D = DTYPES[kind], 2, 64
+    for n in (40, 100, 500, 4000):
+        qx, k, v = g.standard_normal((n, 4, D)), g.standard_normal((n, H, D)), np.full((n, H, D), 0.5)
+        qx[:, 0, 7] = 1.0                      # head 0, of key head 0
+        qx[:, 1:, 7] = 0.0
+        k[:, 0, 7] = -np.inf
+        v[n // 2, 0, 5] = v[3, 0, 9] = bad
+        qx[:, 1] = 0                           # head 1 meets 0 * -inf
+        qd, kd, vd = (dev(a, t) for a in (qx, k, v))
+        got = q.attend_prompt(qd, kd, vd, i32([0, n]))
+        assert bool((got[:, 0] == 0).all()) and bool(torch.isnan(got[:, 1]).all())
+        assert bool(((got[:, 2:].float() - 0.5).abs() < 1e-2).all())
+        c, table, _, tok = filled(g, [n], 16, H, D, kind)
+        c.write(kd, vd, i32(table[0, tok // 16] * 16 + tok % 16))
+        for m in (None, 0, 5000):
+            got = c.attend(qd[-1:], i32(table.flatten()).view(1, -1), i32([n]), max_length=m)
+            assert bool((got[:, 0] == 0).all()) and bool(torch.isnan(got[:, 1]).all())
+            assert bool(((got[:, 2:].float() - 0.5).abs() < 1e-2).all())
