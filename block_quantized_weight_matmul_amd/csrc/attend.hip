@@ -443,8 +443,9 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   typedef typename Elem<QT>::T Q;
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   const int D = a.cache.D, tid = threadIdx.x, lane = tid & 63;
-  const int64_t head = block_index(), b = head / a.Hq;
-  if (head >= a.B * a.Hq) return;  // the grid may have more workgroups than there are heads
+  const uint32_t index = static_cast<uint32_t>(block_index());  // B * Hq < 2^30
+  if (index >= static_cast<uint32_t>(a.B * a.Hq)) return;       // the grid may have more workgroups than there are heads
+  const int64_t head = index, b = index / static_cast<uint32_t>(a.Hq);
   const int team = tid / L, d = tid % L * 4;
   const float* const o = a.ws + head * a.splits * D + (d < D ? d : 0);
   const f32x2* const ml = reinterpret_cast<const f32x2*>(a.ws + a.B * a.Hq * a.splits * D) + head * a.splits;

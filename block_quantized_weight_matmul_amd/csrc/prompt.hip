@@ -425,7 +425,13 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, COLS > 128 ? 1 : 2) void k_pro
 #pragma unroll
     for (int d = 0; d < kOut * 16; ++d) o[d / 16][d % 16] = o[d / 16][d % 16] * w0 + rest[d * 64] * w1;
   }
-  const float inv = 1.0f / total;  // no sum: zeros, whatever the values are
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  if (__any(total == 0.0f)) {  // no sum: zeros, whatever the values are
+#pragma unroll
+    for (int d = 0; d < kOut; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] = total == 0.0f ? 0.0f : o[d][e];
+  }
   uint8_t* const own = lds + 2 * kBytes + wave * 32 * L::kRow;
   const int lane1 = again(threadIdx.x & 63), col1 = lane1 & 31, half1 = lane1 >> 5;
 #pragma unroll
@@ -435,7 +441,7 @@ __global__ __launch_bounds__(64 * kWaves * PARTS, COLS > 128 ? 1 : 2) void k_pro
       typedef T V4 __attribute__((ext_vector_type(4)));
       V4 v;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) v[x] = static_cast<T>(total == 0.0f ? 0.0f : o[d][4 * e + x] * inv);
+      for (int x = 0; x < 4; ++x) v[x] = static_cast<T>(o[d][4 * e + x] * inv);
       *reinterpret_cast<V4*>(rows_at(own, col1, d * 4 + e) + half1 * 8) = v;
     }
   T* const out = static_cast<T*>(a.out) + (w.q0 * a.Hq + head) * a.D;
